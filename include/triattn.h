@@ -51,7 +51,12 @@ typedef enum {
 } ta_status;
 
 /* Element types.  Precision follows the input dtype (triangle_attention page, Notes 2). */
-typedef enum { TA_F32 = 0, TA_F16 = 1, TA_BF16 = 2 } ta_dtype;
+typedef enum {
+    TA_F32 = 0,
+    TA_F16 = 1,
+    TA_BF16 = 2,
+    TA_E4M3 = 3 /* 8-bit (4 significant bits, |x| <= 448): only as the type of a paged cache, with scales */
+} ta_dtype;
 
 /* Element predicate applied on partial blocks of a BlockMask (tensorplay
  * "BlockMask", Details 2: mask_mod is skipped on full blocks), for query q and
@@ -389,6 +394,38 @@ size_t tri_attn_varlen_bwd_workspace_size(int total_q, int H, int D, int max_seq
  */
 ta_status tri_attn_mask_to_kv_lengths(const uint8_t* mask, int B, int N, int K, int32_t* kv_lengths,
                                       int32_t* nonprefix_count, void* stream);
+
+/*
+ * tri_attn_rotary -- rotary positions of packed queries and keys, or their
+ * inverse (which is the gradient).  Su et al., "RoFormer", section 3.4: pair i of
+ * a head at position p turns by p * theta_i:
+ *     (a, b) -> mscale * (a cos - b sin, a sin + b cos).
+ *   q, q_out      (total, Hq, D) of `dtype`;  k, k_out  (total, Hk, D), or NULL
+ *                 with Hk = 0.  Heads and elements contiguous, rows `*_row_stride`
+ *                 elements apart (0 = contiguous), 16-byte aligned and multiples of
+ *                 16 bytes.  q_out == q (k_out == k) with the same row stride turns in place; any
+ *                 other overlap of an output with an input is not allowed.
+ *   positions     (total) int32, any value (negative ones too).
+ *   turns         (rotary_dim / 2) uint64: theta_i / (2 pi) as a fraction of a turn
+ *                 in units of 2^-64 (far positions lose nothing: the product wraps
+ *                 to the part of a turn that counts).
+ *   rotary_dim    even, 2 <= rotary_dim <= D: the leading elements that turn; the
+ *                 rest of the head is copied.
+ *   interleaved   0: pair i is elements (i, i + rotary_dim / 2); 1: (2i, 2i + 1).
+ *   mscale        factor on cos and sin (1, or the attention factor of a scaled
+ *                 context).
+ *   inverse       0: forward; 1: by the opposite angle, times mscale: the gradient
+ *                 of the forward.
+ * Arithmetic in fp32, one rounding to `dtype`.  Supported: D as in tri_attn_fwd.
+ * Errors: NULL required pointer, misalignment, a row stride below H * D or an odd
+ * rotary_dim -> TA_ERR_INVALID_ARG; D, or a row stride that is no multiple of 16
+ * bytes -> TA_ERR_UNSUPPORTED.  total = 0 does nothing.
+ */
+ta_status tri_attn_rotary(const void* q, const void* k, ta_dtype dtype, const int32_t* positions,
+                          const uint64_t* turns, int rotary_dim, int interleaved, float mscale, int inverse,
+                          int total, int Hq, int Hk, int D, long long q_row_stride, long long k_row_stride,
+                          long long q_out_row_stride, long long k_out_row_stride, void* q_out, void* k_out,
+                          void* stream);
 
 /*
  * tri_attn_get_status -- synchronize `stream`, then read and clear the

@@ -15,14 +15,14 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libtriattn.so")
 
 TA_OK, TA_ERR_INVALID_ARG, TA_ERR_UNSUPPORTED, TA_ERR_CUDA, TA_ERR_TIMEOUT, TA_ERR_DEVICE = range(6)
-TA_F32, TA_F16, TA_BF16 = 0, 1, 2
+TA_F32, TA_F16, TA_BF16, TA_E4M3 = 0, 1, 2, 3
 TA_MASK_NONE, TA_MASK_CAUSAL, TA_MASK_SLIDING_WINDOW, TA_MASK_PREFIX_LM = 0, 1, 2, 3
 
 # Every symbol include/triattn.h declares.
 EXPORTS = ("tri_attn_fwd", "tri_attn_fwd_strided", "tri_attn_varlen_fwd", "tri_attn_varlen_fwd_strided", "tri_attn_varlen_fwd_masked",
            "tri_attn_bwd", "tri_attn_bwd_workspace_size", "tri_attn_bwd_noalloc", "tri_attn_varlen_bwd",
            "tri_attn_varlen_bwd_workspace_size",
-           "tri_attn_mask_to_kv_lengths", "tri_attn_get_status", "tri_attn_error_string", "tri_attn_version")
+           "tri_attn_rotary", "tri_attn_mask_to_kv_lengths", "tri_attn_get_status", "tri_attn_error_string", "tri_attn_version")
 
 _lock = threading.Lock()
 _lib = None
@@ -71,6 +71,8 @@ def load() -> ctypes.CDLL:
         lib.tri_attn_varlen_bwd_workspace_size.restype = Z
         lib.tri_attn_bwd_workspace_size.argtypes = [I, I, I, I, I, I]
         lib.tri_attn_bwd_workspace_size.restype = Z
+        lib.tri_attn_rotary.argtypes = [P, P, I, P, P, I, I, F, I, I, I, I, I, L, L, L, L, P, P, P]
+        lib.tri_attn_rotary.restype = I
         lib.tri_attn_mask_to_kv_lengths.argtypes = [P, I, I, I, P, P, P]
         lib.tri_attn_mask_to_kv_lengths.restype = I
         lib.tri_attn_get_status.argtypes = [P]
@@ -204,6 +206,15 @@ def tri_attn_varlen_fwd_masked(q, k, v, dtype, cu_seqlens_q, cu_seqlens_k, num_s
                                            int(bias_dtype), int(q_row_stride), int(k_row_stride), int(v_row_stride), out,
                                            lse or None, max_ or None, stream or None)
     _check(st, "tri_attn_varlen_fwd_masked")
+
+
+def tri_attn_rotary(q, k, dtype, positions, turns, rotary_dim, interleaved, mscale, inverse, total, Hq, Hk, D,
+                    q_row_stride, k_row_stride, q_out_row_stride, k_out_row_stride, q_out, k_out, stream) -> None:
+    """Rotary positions (inverse: their gradient); k / k_out 0 with Hk = 0."""
+    st = load().tri_attn_rotary(q, k or None, dtype, positions, turns, rotary_dim, 1 if interleaved else 0, mscale,
+                                1 if inverse else 0, total, Hq, Hk, D, q_row_stride, k_row_stride, q_out_row_stride,
+                                k_out_row_stride, q_out, k_out or None, stream or None)
+    _check(st, "tri_attn_rotary")
 
 
 def tri_attn_mask_to_kv_lengths(mask, B, N, K, kv_lengths, nonprefix_count, stream) -> None:

@@ -11,9 +11,7 @@
 
 #include <mutex>
 
-#include "internal.h"
-
-#define TA_EXPORT extern "C" __attribute__((visibility("default")))
+#include "host_checks.h"
 
 namespace triattn {
 
@@ -45,18 +43,11 @@ int* status_word() {
 }  // namespace triattn
 
 using triattn::AttnParams;
+using triattn::aligned;
+using triattn::supported_d;
+using triattn::valid_dtype;
 
 namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool valid_dtype(int d) { return d == TA_F32 || d == TA_F16 || d == TA_BF16; }
-
-// Head-dimension rules: 16-bit inputs D % 8 == 0 and D <= 256; fp32 D % 4 == 0 and D <= 256.
-bool supported_d(int dtype, int D) {
-    if (D > 256) return false;
-    return dtype == TA_F32 ? (D % 4 == 0) : (D % 8 == 0);
-}
 
 // fp32 inputs run on the CUDA-core kernel; 16-bit inputs on the tensor-core kernels:
 // D <= 128 on tc_fwd / tc_split, D in (128, 256] on tc_wide (the triangle form with
@@ -539,4 +530,4 @@ TA_EXPORT const char* tri_attn_error_string(ta_status s) {
     }
 }
 
-TA_EXPORT int tri_attn_version(void) { return (1 << 16) | 3; }
+TA_EXPORT int tri_attn_version(void) { return (1 << 16) | 4; }

@@ -115,6 +115,21 @@ cudaError_t launch_tc_fwd(const AttnParams& p, cudaStream_t stream);
 cudaError_t launch_mask_to_kv_lengths(const uint8_t* mask, long long rows, int K, int32_t* kv_len,
                                       int32_t* nonprefix, cudaStream_t stream);
 
+// Rotary positions of packed q (total, Hq, D) and, optionally, k (total, Hk, D).
+struct RotaryParams {
+    const void* q;
+    const void* k;              // NULL with Hk = 0
+    void* q_out;
+    void* k_out;
+    const int32_t* positions;   // (total)
+    const unsigned long long* turns;  // (dim / 2): turns per position, 2^-64 units
+    int dtype, dim, interleaved, inverse;
+    float mscale;
+    int total, Hq, Hk, D;
+    long long q_rs, k_rs, qo_rs, ko_rs;  // elements between rows
+};
+cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t stream);
+
 // Device address of the status word on the current device (set up once per device).
 int* status_word();
 
