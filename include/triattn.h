@@ -428,6 +428,49 @@ ta_status tri_attn_rotary(const void* q, const void* k, ta_dtype dtype, const in
                           void* stream);
 
 /*
+ * tri_attn_kv_append -- new keys and values of packed sequences into a paged
+ * cache, with the rotation of k and q on the way.
+ *
+ *   The cache: num_pages pages of page_size slots (a power of two, 16 to 1024) for
+ *   each of Hk heads: element (page, head, slot, d) at page * s[0] + head * s[1] +
+ *   slot * s[2] + d with the element strides s = k_strides / v_strides {page, head,
+ *   slot} (host arrays; NULL = contiguous (num_pages, Hk, page_size, D)).  Slot t of sequence i is slot
+ *   t % page_size of page page_table[i][t / page_size].
+ *   q, q_out      (total, Hq, D) of `dtype`, both or neither (neither: Hq = 0); q_out == q in place
+ *                 as in tri_attn_rotary.  Needs a rotation.
+ *   k, v          (total, Hk, D) of `dtype`; row strides as in tri_attn_rotary.
+ *   cu_seqlens    (num_seqs + 1) int32: sequence i's new rows are [cu[i], cu[i + 1])
+ *                 (none is fine; rows past cu[num_seqs] are left alone), at most max_seqlen of them.
+ *                 NULL: one row for each sequence (total = num_seqs, max_seqlen 1).
+ *   kv_lengths    (num_seqs) int32: slots held AFTER this call; the new rows are the
+ *                 last of them.
+ *   page_table    (num_seqs, max_pages) int32.  A page that this call writes belongs
+ *                 to one sequence of the call only.
+ *   turns, rotary_dim, interleaved, mscale   as in tri_attn_rotary; turns NULL (then
+ *                 rotary_dim 0): no rotation.
+ *   positions     (total) int32, or NULL: a row's position is its slot.
+ *   cache_dtype   `dtype`, or TA_E4M3: 8-bit codes (D a multiple of 16) that stand for code * scale with
+ *                 k_scale / v_scale (num_pages, Hk) fp32, 4-byte aligned (NULL otherwise).
+ *                 The scale is the smallest power of two, from 2^-56 to 2^56, with
+ *                 max |x| <= 448 * scale over the rows of the page and head; a row that
+ *                 needs a larger one re-codes the rows before it, and the row in slot 0
+ *                 starts anew.  Values are rounded once to the nearest code (ties to
+ *                 even; beyond 448 * 2^56 to that); infinities and NaN become NaN.
+ * A sequence that breaks the contract (lengths, offsets), or a page out of range, is skipped and
+ * TA_ERR_DEVICE recorded.  Errors as tri_attn_rotary; a page size that is no power
+ * of two in range, or cache strides that are no 16-byte multiples -> TA_ERR_UNSUPPORTED.
+ */
+ta_status tri_attn_kv_append(const void* q, const void* k, const void* v, ta_dtype dtype,
+                             const int32_t* cu_seqlens, const int32_t* kv_lengths, const int32_t* page_table,
+                             int num_seqs, int total, int max_seqlen, int Hq, int Hk, int D,
+                             long long q_row_stride, long long k_row_stride, long long v_row_stride,
+                             long long q_out_row_stride, const int32_t* positions, const uint64_t* turns,
+                             int rotary_dim, int interleaved, float mscale, void* k_cache, void* v_cache,
+                             ta_dtype cache_dtype, float* k_scale, float* v_scale, int num_pages, int page_size,
+                             int max_pages, const long long* k_strides, const long long* v_strides, void* q_out,
+                             void* stream);
+
+/*
  * tri_attn_get_status -- synchronize `stream`, then read and clear the
  * device-side status word of the current device.  Returns TA_OK, or the first
  * TA_ERR_TIMEOUT / TA_ERR_DEVICE recorded by a kernel since the last call, or

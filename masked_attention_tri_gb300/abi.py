@@ -22,7 +22,7 @@ TA_MASK_NONE, TA_MASK_CAUSAL, TA_MASK_SLIDING_WINDOW, TA_MASK_PREFIX_LM = 0, 1, 
 EXPORTS = ("tri_attn_fwd", "tri_attn_fwd_strided", "tri_attn_varlen_fwd", "tri_attn_varlen_fwd_strided", "tri_attn_varlen_fwd_masked",
            "tri_attn_bwd", "tri_attn_bwd_workspace_size", "tri_attn_bwd_noalloc", "tri_attn_varlen_bwd",
            "tri_attn_varlen_bwd_workspace_size",
-           "tri_attn_rotary", "tri_attn_mask_to_kv_lengths", "tri_attn_get_status", "tri_attn_error_string", "tri_attn_version")
+           "tri_attn_rotary", "tri_attn_kv_append", "tri_attn_mask_to_kv_lengths", "tri_attn_get_status", "tri_attn_error_string", "tri_attn_version")
 
 _lock = threading.Lock()
 _lib = None
@@ -73,6 +73,9 @@ def load() -> ctypes.CDLL:
         lib.tri_attn_bwd_workspace_size.restype = Z
         lib.tri_attn_rotary.argtypes = [P, P, I, P, P, I, I, F, I, I, I, I, I, L, L, L, L, P, P, P]
         lib.tri_attn_rotary.restype = I
+        lib.tri_attn_kv_append.argtypes = [P, P, P, I, P, P, P, I, I, I, I, I, I, L, L, L, L, P, P, I, I, F, P, P, I, P,
+                                           P, I, I, I, P, P, P, P]
+        lib.tri_attn_kv_append.restype = I
         lib.tri_attn_mask_to_kv_lengths.argtypes = [P, I, I, I, P, P, P]
         lib.tri_attn_mask_to_kv_lengths.restype = I
         lib.tri_attn_get_status.argtypes = [P]
@@ -215,6 +218,24 @@ def tri_attn_rotary(q, k, dtype, positions, turns, rotary_dim, interleaved, msca
                                 1 if inverse else 0, total, Hq, Hk, D, q_row_stride, k_row_stride, q_out_row_stride,
                                 k_out_row_stride, q_out, k_out or None, stream or None)
     _check(st, "tri_attn_rotary")
+
+
+def strides3(st):
+    """A host array of 3 element strides (page, head, slot) for the C calls on a paged cache."""
+    return (ctypes.c_longlong * 3)(*[int(x) for x in st])
+
+
+def tri_attn_kv_append(q, k, v, dtype, cu_seqlens, kv_lengths, page_table, num_seqs, total, max_seqlen, Hq, Hk, D,
+                       q_row_stride, k_row_stride, v_row_stride, q_out_row_stride, positions, turns, rotary_dim,
+                       interleaved, mscale, k_cache, v_cache, cache_dtype, k_scale, v_scale, num_pages, page_size,
+                       max_pages, k_strides, v_strides, q_out, stream) -> None:
+    """k_strides / v_strides: None (contiguous) or a host array of ``strides3``."""
+    st = load().tri_attn_kv_append(q or None, k, v, dtype, cu_seqlens or None, kv_lengths, page_table, num_seqs, total,
+                                   max_seqlen, Hq, Hk, D, q_row_stride, k_row_stride, v_row_stride, q_out_row_stride,
+                                   positions or None, turns or None, rotary_dim, 1 if interleaved else 0, mscale,
+                                   k_cache, v_cache, cache_dtype, k_scale or None, v_scale or None, num_pages,
+                                   page_size, max_pages, k_strides, v_strides, q_out or None, stream or None)
+    _check(st, "tri_attn_kv_append")
 
 
 def tri_attn_mask_to_kv_lengths(mask, B, N, K, kv_lengths, nonprefix_count, stream) -> None:

@@ -19,6 +19,44 @@ ta_status row_stride(long long& rs, int H, int D, int esz) {
     return TA_OK;
 }
 
+// The element strides {page, head, slot} of a cache whose D elements are contiguous: the given
+// ones (checked), or the contiguous layout.
+ta_status cache_strides(const long long* given, int num_pages, int Hk, int page, int D, int esz, long long (&st)[3]) {
+    if (!given) {
+        st[2] = D;
+        st[1] = (long long)page * D;
+        st[0] = st[1] * Hk;
+    } else {
+        const long long ext[3] = {num_pages, Hk, page};
+        for (int i = 0; i < 3; ++i) {
+            st[i] = given[i];
+            if (st[i] < D) return TA_ERR_INVALID_ARG;  // no two rows overlap
+            if (st[i] > ((1LL << 60) / ext[i])) return TA_ERR_UNSUPPORTED;
+        }
+    }
+    for (int i = 0; i < 3; ++i)  // tensor-map strides: 16-byte multiples below 2^40 bytes
+        if ((st[i] * esz) % 16 != 0 || st[i] * esz >= (1LL << 40)) return TA_ERR_UNSUPPORTED;
+    return TA_OK;
+}
+
+// What the two operators on a paged cache check alike.
+ta_status check_cache(const void* k_cache, const void* v_cache, int dtype, int cache_dtype, const float* k_scale,
+                      const float* v_scale, int num_pages, int page_size, int max_pages, int Hk, int D,
+                      const long long* k_strides, const long long* v_strides, long long (&ks)[3], long long (&vs)[3]) {
+    if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16)) return TA_ERR_INVALID_ARG;
+    if (num_pages <= 0 || page_size <= 0 || max_pages <= 0) return TA_ERR_INVALID_ARG;
+    if (!valid_dtype(cache_dtype) && cache_dtype != TA_E4M3) return TA_ERR_INVALID_ARG;
+    const bool codes = cache_dtype == TA_E4M3;
+    if (codes ? (!k_scale || !v_scale) : (k_scale || v_scale)) return TA_ERR_INVALID_ARG;
+    if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return TA_ERR_INVALID_ARG;
+    if (!codes && cache_dtype != dtype) return TA_ERR_UNSUPPORTED;
+    if (codes && D % 16 != 0) return TA_ERR_UNSUPPORTED;
+    if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return TA_ERR_UNSUPPORTED;
+    const int esz = dtype_bytes(cache_dtype);
+    const ta_status st = cache_strides(k_strides, num_pages, Hk, page_size, D, esz, ks);
+    return st != TA_OK ? st : cache_strides(v_strides, num_pages, Hk, page_size, D, esz, vs);
+}
+
 }  // namespace
 
 TA_EXPORT ta_status tri_attn_rotary(const void* q, const void* k, ta_dtype dtype, const int32_t* positions,
@@ -67,4 +105,76 @@ TA_EXPORT ta_status tri_attn_rotary(const void* q, const void* k, ta_dtype dtype
     p.qo_rs = q_out_row_stride;
     p.ko_rs = k_out_row_stride;
     return launch_rotary(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TA_OK : TA_ERR_CUDA;
+}
+
+TA_EXPORT ta_status tri_attn_kv_append(const void* q, const void* k, const void* v, ta_dtype dtype,
+                                       const int32_t* cu_seqlens, const int32_t* kv_lengths,
+                                       const int32_t* page_table, int num_seqs, int total, int max_seqlen, int Hq,
+                                       int Hk, int D, long long q_row_stride, long long k_row_stride,
+                                       long long v_row_stride, long long q_out_row_stride, const int32_t* positions,
+                                       const uint64_t* turns, int rotary_dim, int interleaved, float mscale,
+                                       void* k_cache, void* v_cache, ta_dtype cache_dtype, float* k_scale,
+                                       float* v_scale, int num_pages, int page_size, int max_pages,
+                                       const long long* k_strides, const long long* v_strides, void* q_out,
+                                       void* stream) {
+    if (!k || !v || !kv_lengths || !page_table) return TA_ERR_INVALID_ARG;
+    if (num_seqs <= 0 || total < 0 || max_seqlen < 0 || Hk <= 0 || D <= 0) return TA_ERR_INVALID_ARG;
+    if (Hq > 0 ? (!q || !q_out || !turns) : (q || q_out || Hq < 0)) return TA_ERR_INVALID_ARG;
+    if (!cu_seqlens && (total != num_seqs || max_seqlen != 1)) return TA_ERR_INVALID_ARG;
+    if (!valid_dtype(dtype)) return TA_ERR_INVALID_ARG;
+    if (turns ? (rotary_dim < 2 || rotary_dim > D || rotary_dim % 2 != 0) : (rotary_dim != 0 || positions))
+        return TA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(cu_seqlens, 4) ||
+        !aligned(kv_lengths, 4) || !aligned(page_table, 4) || !aligned(positions, 4) || !aligned(turns, 8))
+        return TA_ERR_INVALID_ARG;
+    if (!supported_d(dtype, D)) return TA_ERR_UNSUPPORTED;
+    KvAppendParams p{};
+    ta_status st = check_cache(k_cache, v_cache, dtype, cache_dtype, k_scale, v_scale, num_pages, page_size, max_pages,
+                               Hk, D, k_strides, v_strides, p.ks, p.vs);
+    if (st != TA_OK) return st;
+    const int esz = dtype_bytes(dtype);
+    if ((st = row_stride(k_row_stride, Hk, D, esz)) != TA_OK) return st;
+    if ((st = row_stride(v_row_stride, Hk, D, esz)) != TA_OK) return st;
+    if (Hq > 0) {
+        if ((st = row_stride(q_row_stride, Hq, D, esz)) != TA_OK) return st;
+        if ((st = row_stride(q_out_row_stride, Hq, D, esz)) != TA_OK) return st;
+        if (q == q_out && q_row_stride != q_out_row_stride) return TA_ERR_INVALID_ARG;
+    }
+    if ((long long)num_seqs * (max_seqlen / page_size + 2) > 0x7fffffffLL || Hk > 16384 || Hq > 65536)
+        return TA_ERR_UNSUPPORTED;
+    if (total == 0 || max_seqlen == 0) return TA_OK;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_out = q_out;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.cu = cu_seqlens;
+    p.kv_len = kv_lengths;
+    p.table = page_table;
+    p.positions = positions;
+    p.turns = reinterpret_cast<const unsigned long long*>(turns);
+    p.dtype = dtype;
+    p.cache_dtype = cache_dtype;
+    p.dim = rotary_dim;
+    p.interleaved = interleaved != 0;
+    p.mscale = mscale;
+    p.num_seqs = num_seqs;
+    p.total = total;
+    p.max_n = max_seqlen;
+    p.Hq = Hq;
+    p.Hk = Hk;
+    p.D = D;
+    p.num_pages = num_pages;
+    p.page = page_size;
+    p.max_pages = max_pages;
+    p.q_rs = q_row_stride;
+    p.k_rs = k_row_stride;
+    p.v_rs = v_row_stride;
+    p.qo_rs = q_out_row_stride;
+    p.status = status_word();
+    if (!p.status) return TA_ERR_CUDA;
+    return launch_kv_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TA_OK : TA_ERR_CUDA;
 }

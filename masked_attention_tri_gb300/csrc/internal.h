@@ -130,6 +130,30 @@ struct RotaryParams {
 };
 cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t stream);
 
+// New k / v rows (and the rotation of q) into a paged cache.  C of the caches: dtype or e4m3.
+struct KvAppendParams {
+    const void* q;              // (total, Hq, D) or NULL
+    const void* k;              // (total, Hk, D)
+    const void* v;
+    void* q_out;
+    void* k_cache;
+    void* v_cache;
+    float* k_scale;             // (num_pages, Hk), e4m3 only
+    float* v_scale;
+    const int32_t* cu;          // (num_seqs + 1), or NULL: one row a sequence
+    const int32_t* kv_len;      // (num_seqs): rows held after the call
+    const int32_t* table;       // (num_seqs, max_pages)
+    const int32_t* positions;   // (total), or NULL: the row's slot
+    const unsigned long long* turns;
+    int dtype, cache_dtype, dim, interleaved;  // dim 0: no rotation
+    float mscale;
+    int num_seqs, total, max_n, Hq, Hk, D, num_pages, page, max_pages;
+    long long q_rs, k_rs, v_rs, qo_rs;
+    long long ks[3], vs[3];     // element strides {page, head, slot} of the caches
+    int* status;
+};
+cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream);
+
 // Device address of the status word on the current device (set up once per device).
 int* status_word();
 
