@@ -471,6 +471,47 @@ ta_status tri_attn_kv_append(const void* q, const void* k, const void* v, ta_dty
                              void* stream);
 
 /*
+ * tri_attn_paged_fwd -- attention of the newest tokens of each sequence over its
+ * paged cache (the layout of tri_attn_kv_append), with grouped heads:
+ *     O[i, h] = softmax_k(scale q[i, h] . K[k, h / (Hq / Hk)]) V[k, h / (Hq / Hk)].
+ *   q, out        (total_q, Hq, D) of `dtype`, Hq a multiple of Hk; q rows q_row_stride elements
+ *                 apart (0 = contiguous), out contiguous.
+ *   cu_seqlens_q  (num_seqs + 1) int32: sequence i's rows [cu[i], cu[i + 1]), at most
+ *                 max_seqlen_q of them, are its newest tokens: row j has position
+ *                 kv_lengths[i] - n + j and sees the slots up to its own.  Rows past
+ *                 cu[num_seqs] are left alone.  NULL: one row for each sequence
+ *                 (total_q = num_seqs, max_seqlen_q 1).
+ *   kv_lengths    (num_seqs) int32: slots held, the new tokens' among them.
+ *   page_table    (num_seqs, max_pages) int32.  Only pages with a slot that some row
+ *                 sees are read; the other entries may hold anything.
+ *   window        0: every slot up to the token's own.  >= 1: the last `window` of
+ *                 them (slots k > p - window) and the first `sinks` of the sequence
+ *                 (sinks >= 0; ignored without a window).
+ *   k_cache .. v_strides   as in tri_attn_kv_append.  Scales of an 8-bit cache:
+ *                 any positive fp32 values.
+ *   lse           optional (Hq, total_q) fp32.
+ *   workspace     device scratch of tri_attn_paged_workspace_size(...) bytes, 256-byte aligned,
+ *                 owned by the caller; its contents on entry are ignored.  Two
+ *                 calls in flight must not share it.
+ * A row that sees no slot (a sequence that holds nothing) gets O = 0 and lse = -inf.
+ * Slots that no row of the call sees may hold anything, NaN included.  With several
+ * rows of one sequence, a slot that some of them see has to hold finite values of v.
+ * Results do not vary from run to run.  A sequence that breaks the contract
+ * (offsets; a length below 0 or beyond its table, read as 0) or a page out of range (its slots
+ * are not seen) records TA_ERR_DEVICE.  Errors as tri_attn_kv_append.
+ */
+ta_status tri_attn_paged_fwd(const void* q, ta_dtype dtype, const int32_t* cu_seqlens_q, const int32_t* kv_lengths,
+                             const int32_t* page_table, int num_seqs, int total_q, int max_seqlen_q, int Hq, int Hk,
+                             int D, long long q_row_stride, float scale, int window, int sinks, const void* k_cache,
+                             const void* v_cache, ta_dtype cache_dtype, const float* k_scale, const float* v_scale,
+                             int num_pages, int page_size, int max_pages, const long long* k_strides,
+                             const long long* v_strides, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace tri_attn_paged_fwd needs (0 for a non-positive size). */
+size_t tri_attn_paged_workspace_size(ta_dtype dtype, int max_seqlen_q, int Hq, int Hk, int D);
+
+/*
  * tri_attn_get_status -- synchronize `stream`, then read and clear the
  * device-side status word of the current device.  Returns TA_OK, or the first
  * TA_ERR_TIMEOUT / TA_ERR_DEVICE recorded by a kernel since the last call, or

@@ -10,10 +10,10 @@ from . import abi
 from .api import (BlockMask, get_status, mask_to_kv_lengths, triangle_attention, triangle_attention_autograd,
                   triangle_attention_backward, varlen_attention, varlen_attention_backward,
                   varlen_attention_kvpacked, varlen_attention_qkvpacked)
-from .cache import PagedKVCache, kv_cache_append
+from .cache import PagedKVCache, kv_cache_append, paged_attention
 from .positions import Rotary, rotary_embedding, rotary_embedding_autograd, rotary_embedding_backward
 
 __all__ = ["abi", "BlockMask", "get_status", "mask_to_kv_lengths", "triangle_attention", "triangle_attention_autograd",
            "triangle_attention_backward", "varlen_attention", "varlen_attention_backward", "varlen_attention_kvpacked",
-           "varlen_attention_qkvpacked", "PagedKVCache", "Rotary", "kv_cache_append", "rotary_embedding", "rotary_embedding_autograd",
+           "varlen_attention_qkvpacked", "PagedKVCache", "Rotary", "kv_cache_append", "paged_attention", "rotary_embedding", "rotary_embedding_autograd",
            "rotary_embedding_backward"]

@@ -22,7 +22,8 @@ TA_MASK_NONE, TA_MASK_CAUSAL, TA_MASK_SLIDING_WINDOW, TA_MASK_PREFIX_LM = 0, 1, 
 EXPORTS = ("tri_attn_fwd", "tri_attn_fwd_strided", "tri_attn_varlen_fwd", "tri_attn_varlen_fwd_strided", "tri_attn_varlen_fwd_masked",
            "tri_attn_bwd", "tri_attn_bwd_workspace_size", "tri_attn_bwd_noalloc", "tri_attn_varlen_bwd",
            "tri_attn_varlen_bwd_workspace_size",
-           "tri_attn_rotary", "tri_attn_kv_append", "tri_attn_mask_to_kv_lengths", "tri_attn_get_status", "tri_attn_error_string", "tri_attn_version")
+           "tri_attn_rotary", "tri_attn_kv_append", "tri_attn_paged_fwd", "tri_attn_paged_workspace_size",
+           "tri_attn_mask_to_kv_lengths", "tri_attn_get_status", "tri_attn_error_string", "tri_attn_version")
 
 _lock = threading.Lock()
 _lib = None
@@ -76,6 +77,11 @@ def load() -> ctypes.CDLL:
         lib.tri_attn_kv_append.argtypes = [P, P, P, I, P, P, P, I, I, I, I, I, I, L, L, L, L, P, P, I, I, F, P, P, I, P,
                                            P, I, I, I, P, P, P, P]
         lib.tri_attn_kv_append.restype = I
+        lib.tri_attn_paged_fwd.argtypes = [P, I, P, P, P, I, I, I, I, I, I, L, F, I, I, P, P, I, P, P, I, I, I, P, P, P,
+                                           P, P, Z, P]
+        lib.tri_attn_paged_fwd.restype = I
+        lib.tri_attn_paged_workspace_size.argtypes = [I, I, I, I, I]
+        lib.tri_attn_paged_workspace_size.restype = Z
         lib.tri_attn_mask_to_kv_lengths.argtypes = [P, I, I, I, P, P, P]
         lib.tri_attn_mask_to_kv_lengths.restype = I
         lib.tri_attn_get_status.argtypes = [P]
@@ -236,6 +242,22 @@ def tri_attn_kv_append(q, k, v, dtype, cu_seqlens, kv_lengths, page_table, num_s
                                    k_cache, v_cache, cache_dtype, k_scale or None, v_scale or None, num_pages,
                                    page_size, max_pages, k_strides, v_strides, q_out or None, stream or None)
     _check(st, "tri_attn_kv_append")
+
+
+def tri_attn_paged_workspace_size(dtype, max_seqlen_q, Hq, Hk, D) -> int:
+    return int(load().tri_attn_paged_workspace_size(dtype, max_seqlen_q, Hq, Hk, D))
+
+
+def tri_attn_paged_fwd(q, dtype, cu_seqlens_q, kv_lengths, page_table, num_seqs, total_q, max_seqlen_q, Hq, Hk, D,
+                       q_row_stride, scale, window, sinks, k_cache, v_cache, cache_dtype, k_scale, v_scale, num_pages,
+                       page_size, max_pages, k_strides, v_strides, out, lse, workspace, workspace_bytes,
+                       stream) -> None:
+    """k_strides / v_strides: None (contiguous) or a host array of ``strides3``."""
+    st = load().tri_attn_paged_fwd(q, dtype, cu_seqlens_q or None, kv_lengths, page_table, num_seqs, total_q,
+                                   max_seqlen_q, Hq, Hk, D, q_row_stride, scale, window, sinks, k_cache, v_cache,
+                                   cache_dtype, k_scale or None, v_scale or None, num_pages, page_size, max_pages,
+                                   k_strides, v_strides, out, lse or None, workspace, workspace_bytes, stream or None)
+    _check(st, "tri_attn_paged_fwd")
 
 
 def tri_attn_mask_to_kv_lengths(mask, B, N, K, kv_lengths, nonprefix_count, stream) -> None:

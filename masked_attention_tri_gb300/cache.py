@@ -6,12 +6,13 @@ for each (page, head).  The work runs in libtriattn.so's kernels.
 """
 from __future__ import annotations
 
+import math
 from typing import Optional
 
 import torch
 
 from . import abi
-from .api import _DT, _need, _ptr, _row_stride, _stream
+from .api import _DT, _check_out, _need, _ptr, _row_stride, _stream
 from .positions import Rotary, _check_rotary
 
 _CACHE_DT = {**_DT, torch.float8_e4m3fn: abi.TA_E4M3}
@@ -159,3 +160,64 @@ def kv_cache_append(cache: PagedKVCache, k, v, page_table, kv_lengths, cu_seqlen
                                _ptr(cache.k_scale), _ptr(cache.v_scale), cache.num_pages, cache.page_size, MP,
                                cache._strides[0], cache._strides[1], _ptr(out_q), _stream(dev))
     return out_q
+
+
+def paged_attention(q, cache: PagedKVCache, page_table, kv_lengths, cu_seqlens_q=None, max_seqlen_q=1, scale=None, *,
+                    window=None, sinks=0, return_aux=False, out=None):
+    """Attention of each sequence's newest tokens over its pages of the cache.
+
+    q (total_q, Hq, D), Hq a multiple of the cache's heads (consecutive query heads
+    share one).  kv_lengths (S,) int32 counts the slots a sequence holds, its rows of q
+    among them: row j of n sees the slots up to kv_lengths - n + j.
+    cu_seqlens_q (S + 1,) int32 splits the rows (at most max_seqlen_q each; rows past its
+    last entry are left alone); without it there is one row for each sequence.
+    window: only the last ``window`` of those slots, and the first ``sinks`` of the
+    sequence.  scale defaults to 1/sqrt(D).  Returns O, or (O, lse) with return_aux (lse
+    float32 (Hq, total_q)); a row that sees no slot gets O = 0 and lse = -inf.
+    """
+    if not isinstance(cache, PagedKVCache):
+        raise TypeError("cache must be a PagedKVCache")
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dim() != 3:
+        raise ValueError("expected q (total_q, Hq, D)")
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("paged_attention runs on CUDA tensors only")
+    if cache.device != dev:
+        raise ValueError(f"cache is on {cache.device}, expected {dev}")
+    if q.dtype not in _DT:
+        raise TypeError("q must be float32, float16 or bfloat16")
+    total, Hq, D = q.shape
+    Hk = cache.heads
+    if D != cache.head_dim:
+        raise ValueError(f"q must have the cache's head dimension {cache.head_dim}")
+    if Hk == 0 or Hq % Hk:
+        raise ValueError(f"q's heads must be a multiple of the cache's {Hk}")
+    q_rs = _row_stride(q, "q", dev)
+    S, MP = _table(page_table, kv_lengths, cu_seqlens_q, dev)
+    max_seqlen_q = int(max_seqlen_q)
+    if cu_seqlens_q is None and (total != S or max_seqlen_q != 1):
+        raise ValueError("without cu_seqlens_q there is one row for each sequence")
+    if window is not None and int(window) < 1:
+        raise ValueError("window must be at least 1")
+    if int(sinks) < 0:
+        raise ValueError("sinks must not be negative")
+    s = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _check_out(out, q.shape, q.dtype)
+        _need(out, "out", dev)
+    lse = torch.empty(Hq, total, dtype=torch.float32, device=dev) if return_aux else None
+    if total and S:
+        code = _DT[q.dtype]
+        nbytes = abi.tri_attn_paged_workspace_size(code, max_seqlen_q, Hq, Hk, D)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        with torch.cuda.device(dev):
+            abi.tri_attn_paged_fwd(_ptr(q), code, _ptr(cu_seqlens_q), _ptr(kv_lengths), _ptr(page_table), S, total,
+                                   max_seqlen_q, Hq, Hk, D, q_rs, s, 0 if window is None else int(window), int(sinks),
+                                   _ptr(cache.k), _ptr(cache.v), cache._code, _ptr(cache.k_scale), _ptr(cache.v_scale),
+                                   cache.num_pages, cache.page_size, MP, cache._strides[0], cache._strides[1],
+                                   _ptr(out), _ptr(lse), _ptr(ws), nbytes, _stream(dev))
+    return (out, lse) if return_aux else out

@@ -178,3 +178,68 @@ TA_EXPORT ta_status tri_attn_kv_append(const void* q, const void* k, const void*
     if (!p.status) return TA_ERR_CUDA;
     return launch_kv_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TA_OK : TA_ERR_CUDA;
 }
+
+TA_EXPORT size_t tri_attn_paged_workspace_size(ta_dtype dtype, int max_seqlen_q, int Hq, int Hk, int D) {
+    if (max_seqlen_q <= 0 || Hq <= 0 || Hk <= 0 || D <= 0 || Hq % Hk != 0) return 0;
+    return paged_workspace_bytes(paged_rows(dtype, max_seqlen_q, Hq / Hk, D), D);
+}
+
+TA_EXPORT ta_status tri_attn_paged_fwd(const void* q, ta_dtype dtype, const int32_t* cu_seqlens_q,
+                                       const int32_t* kv_lengths, const int32_t* page_table, int num_seqs, int total_q,
+                                       int max_seqlen_q, int Hq, int Hk, int D, long long q_row_stride, float scale,
+                                       int window, int sinks, const void* k_cache, const void* v_cache,
+                                       ta_dtype cache_dtype, const float* k_scale, const float* v_scale,
+                                       int num_pages, int page_size, int max_pages, const long long* k_strides,
+                                       const long long* v_strides, void* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    if (!q || !out || !kv_lengths || !page_table || !workspace) return TA_ERR_INVALID_ARG;
+    if (num_seqs <= 0 || total_q < 0 || max_seqlen_q < 0 || Hq <= 0 || Hk <= 0 || D <= 0 || Hq % Hk != 0)
+        return TA_ERR_INVALID_ARG;
+    if (!cu_seqlens_q && (total_q != num_seqs || max_seqlen_q != 1)) return TA_ERR_INVALID_ARG;
+    if (window < 0 || sinks < 0) return TA_ERR_INVALID_ARG;
+    if (!valid_dtype(dtype)) return TA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(cu_seqlens_q, 4) ||
+        !aligned(kv_lengths, 4) || !aligned(page_table, 4) || !aligned(lse, 4))
+        return TA_ERR_INVALID_ARG;
+    if (!supported_d(dtype, D)) return TA_ERR_UNSUPPORTED;
+    PagedParams p{};
+    ta_status st = check_cache(k_cache, v_cache, dtype, cache_dtype, k_scale, v_scale, num_pages, page_size, max_pages,
+                               Hk, D, k_strides, v_strides, p.ks, p.vs);
+    if (st != TA_OK) return st;
+    if ((st = row_stride(q_row_stride, Hq, D, dtype_bytes(dtype))) != TA_OK) return st;
+    if ((long long)total_q * Hq > 0x7fffffffLL || (long long)max_seqlen_q * Hq > 0x7fffffffLL)
+        return TA_ERR_UNSUPPORTED;
+    if (total_q == 0 || max_seqlen_q == 0) return TA_OK;
+    if (workspace_bytes < tri_attn_paged_workspace_size(dtype, max_seqlen_q, Hq, Hk, D)) return TA_ERR_INVALID_ARG;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.cu = cu_seqlens_q;
+    p.kv_len = kv_lengths;
+    p.table = page_table;
+    p.out = out;
+    p.lse = lse;
+    p.ws = workspace;
+    p.dtype = dtype;
+    p.cache_dtype = cache_dtype;
+    p.num_seqs = num_seqs;
+    p.total_q = total_q;
+    p.max_q = max_seqlen_q;
+    p.Hq = Hq;
+    p.Hk = Hk;
+    p.G = Hq / Hk;
+    p.D = D;
+    p.num_pages = num_pages;
+    p.page = page_size;
+    p.max_pages = max_pages;
+    p.window = window;
+    p.sinks = sinks;
+    p.RT = paged_rows(dtype, max_seqlen_q, p.G, D);
+    p.scale_log2e = scale * 1.4426950408889634f;
+    p.q_rs = q_row_stride;
+    p.status = status_word();
+    if (!p.status) return TA_ERR_CUDA;
+    return launch_paged(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TA_OK : TA_ERR_CUDA;
+}

@@ -154,6 +154,32 @@ struct KvAppendParams {
 };
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream);
 
+// Attention over a paged cache.
+struct PagedParams {
+    const void* q;              // (total_q, Hq, D)
+    const void* k_cache;
+    const void* v_cache;
+    const float* k_scale;       // (num_pages, Hk), e4m3 only
+    const float* v_scale;
+    const int32_t* cu;          // (num_seqs + 1), or NULL: one row a sequence
+    const int32_t* kv_len;      // (num_seqs)
+    const int32_t* table;       // (num_seqs, max_pages)
+    void* out;                  // (total_q, Hq, D)
+    float* lse;                 // (Hq, total_q) or NULL
+    void* ws;
+    int* status;
+    int dtype, cache_dtype;
+    int num_seqs, total_q, max_q, Hq, Hk, G, D, num_pages, page, max_pages;
+    int window, sinks;          // window 0: every earlier slot
+    int RT;                     // rows of a unit
+    float scale_log2e;
+    long long q_rs;
+    long long ks[3], vs[3];     // element strides {page, head, slot} of the caches
+};
+int paged_rows(int dtype, int max_q, int G, int D);  // RT of a problem
+size_t paged_workspace_bytes(int RT, int D);
+cudaError_t launch_paged(const PagedParams& p, cudaStream_t stream);
+
 // Device address of the status word on the current device (set up once per device).
 int* status_word();
 

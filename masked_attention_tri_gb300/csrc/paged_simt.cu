@@ -1,0 +1,298 @@
+// paged_simt.cu -- attention over a paged cache on CUDA cores in exact fp32: fp32
+// queries, with an fp32 or an 8-bit cache; and the kernel that joins split rows.
+//
+// One CTA of eight warps per share of the tile axis (paged.cuh); the warps of a CTA
+// take the tiles of a unit in turn, each with its own running maximum, sum and O,
+// and merge at the unit's end.  A warp reads one slot's row of K (and V) with
+// coalesced vectors, four elements a lane, for eight query rows at once: the 32 dot
+// products of four slots are summed over the lanes by a transposing reduction (31 shuffles),
+// after which each lane holds one (slot, row) logit.  Bound: the FMAs
+// (8 rows x 2 an element) and shuffles, at about half the memory rate for fp32.
+
+#include "paged.cuh"
+
+namespace triattn {
+namespace paged {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 8;
+constexpr int kMinTiles = 8;   // shares are not cut finer than one tile a warp
+
+template <typename C>
+__device__ __forceinline__ float4 load4(const C* p) {
+    float x[4];
+    rot_load<C, 4>(p, x);
+    return make_float4(x[0], x[1], x[2], x[3]);
+}
+template <>
+__device__ __forceinline__ float4 load4<uint8_t>(const uint8_t* p) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3)));
+    const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3)));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// NC: vectors of 4 elements a lane (D up to 128 NC).
+template <typename T, typename C, int NC>
+__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams p) {
+    extern __shared__ float smem[];  // O [kWarps][kRows][D], (m, l) [kWarps][kRows]
+    __shared__ long long scan[kWarps], found[2];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int D = p.D;
+    float* so = smem;
+    float2* sml = reinterpret_cast<float2*>(smem + kWarps * kRows * D);
+    const Workspace ws = workspace(p.ws, p.RT, D);
+    const Share sh = find_share<kThreads>(p, kMinTiles, scan, found);
+    Walk w = walk_begin(p, sh);
+    if (threadIdx.x == 0) ws.join[blockIdx.x].parts = 0;
+    long long at = sh.begin;  // axis position of the unit's first tile in this share
+    Unit u;
+    while (walk_next(p, w, u)) {
+        const long long head0 = (long long)u.h * p.G;
+        // this lane's logits belong to row lane % 8
+        const int myrow = u.rt * kRows + lane % kRows;
+        const int mypos = u.q.len - u.q.n + min(myrow, u.q.n * p.G - 1) / p.G;
+        float4 qf[kRows][NC];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int row = u.rt * kRows + r;
+            const long long tok = u.q.row0 + row / p.G, head = head0 + row % p.G;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int d = (c * 32 + lane) * 4;
+                qf[r][c] = row < u.q.n * p.G && d < D
+                               ? load4<T>(static_cast<const T*>(p.q) + tok * p.q_rs + head * D + d)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+        float4 acc[kRows][NC];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) acc[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float m = -INFINITY, l = 0.f;  // m of row lane % 8; l: this lane's share of the sum
+
+        for (int j = u.j0 + warp; j < u.j1 && j < u.t.nt; j += kWarps) {
+            const int key_t = u.t.tile(j) * kTile;
+            for (int k0 = key_t; k0 < key_t + kTile; k0 += 4) {
+                // (pages hold at least 16 slots: four slots lie in one)
+                if (!unit_sees(p, u.t, k0) && !unit_sees(p, u.t, k0 + 1) && !unit_sees(p, u.t, k0 + 2) &&
+                    !unit_sees(p, u.t, k0 + 3))
+                    continue;
+                const long long page = p.table[(long long)u.seq * p.max_pages + k0 / p.page];
+                if (page < 0 || page >= p.num_pages) {
+                    if (lane == 0) atomicCAS(p.status, 0, kStatusDevice);
+                    continue;
+                }
+                const int slot = k0 % p.page;
+                const C* kp = static_cast<const C*>(p.k_cache) + page * p.ks[0] + u.h * p.ks[1] + slot * p.ks[2];
+                const C* vp = static_cast<const C*>(p.v_cache) + page * p.vs[0] + u.h * p.vs[1] + slot * p.vs[2];
+                float kscale = p.scale_log2e, vs_inv = 1.f, vs_log2 = 0.f;
+                if constexpr (sizeof(C) == 1) {
+                    kscale *= p.k_scale[page * p.Hk + u.h];
+                    const float v = p.v_scale[page * p.Hk + u.h];
+                    vs_inv = 1.f / v;
+                    vs_log2 = log2f(v);
+                }
+                float dot[32];
+                bool on[4];
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    on[kk] = unit_sees(p, u.t, k0 + kk);
+                    float4 kv[NC];
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const int d = (c * 32 + lane) * 4;
+                        kv[c] = on[kk] && d < D ? load4<C>(kp + kk * p.ks[2] + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) {
+                        float s = 0.f;
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) {
+                            s = fmaf(qf[r][c].x, kv[c].x, s);
+                            s = fmaf(qf[r][c].y, kv[c].y, s);
+                            s = fmaf(qf[r][c].z, kv[c].z, s);
+                            s = fmaf(qf[r][c].w, kv[c].w, s);
+                        }
+                        dot[kk * kRows + r] = s;
+                    }
+                }
+                // lane L ends with the sum of dot[L] over the lanes
+#pragma unroll
+                for (int o = 16; o; o >>= 1) {
+                    const bool up = lane & o;
+#pragma unroll
+                    for (int i = 0; i < o; ++i) {
+                        const float keep = up ? dot[i + o] : dot[i], send = up ? dot[i] : dot[i + o];
+                        dot[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                    }
+                }
+                const int mykey = k0 + lane / kRows;
+                const float x = sees(p, mypos, mykey) ? fmaf(dot[0], kscale, vs_log2) : -INFINITY;
+                float mt = x;
+                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+                if (__any_sync(0xffffffffu, mt > m)) {
+                    const float mn = fmaxf(m, mt);
+                    const float alpha = mn == -INFINITY ? 1.f : exp2f(m - mn);
+                    m = mn;
+                    l *= alpha;
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) {
+                        const float al = __shfl_sync(0xffffffffu, alpha, r);
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) {
+                            acc[r][c].x *= al;
+                            acc[r][c].y *= al;
+                            acc[r][c].z *= al;
+                            acc[r][c].w *= al;
+                        }
+                    }
+                }
+                const float pr = x == -INFINITY ? 0.f : exp2f(x - m);
+                l = fmaf(pr, vs_inv, l);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    if (!on[kk]) continue;  // (a slot that no row sees is not read: it may hold anything)
+                    float4 vv[NC];
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const int d = (c * 32 + lane) * 4;
+                        vv[c] = d < D ? load4<C>(vp + kk * p.vs[2] + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) {
+                        const float pk = __shfl_sync(0xffffffffu, pr, kk * kRows + r);
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) {
+                            acc[r][c].x = fmaf(pk, vv[c].x, acc[r][c].x);
+                            acc[r][c].y = fmaf(pk, vv[c].y, acc[r][c].y);
+                            acc[r][c].z = fmaf(pk, vv[c].z, acc[r][c].z);
+                            acc[r][c].w = fmaf(pk, vv[c].w, acc[r][c].w);
+                        }
+                    }
+                }
+            }
+        }
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+
+        // ---- Merge of the warps.
+        __syncthreads();
+        if (lane < kRows) sml[warp * kRows + lane] = make_float2(m, l);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int d = (c * 32 + lane) * 4;
+                if (d < D) *reinterpret_cast<float4*>(so + (warp * kRows + r) * D + d) = acc[r][c];
+            }
+        __syncthreads();
+        const bool whole = u.starts && u.ends;
+        const int slot = u.starts ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
+        for (int e = threadIdx.x; e < u.rows * D; e += kThreads) {
+            const int r = e / D, d = e - r * D;
+            float M = -INFINITY, L = 0.f, o = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sml[i * kRows + r].x);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float2 ml = sml[i * kRows + r];
+                if (no_key(ml.x, ml.y)) continue;
+                const float f = exp2f(ml.x - M);
+                L = fmaf(ml.y, f, L);
+                o = fmaf(so[(i * kRows + r) * D + d], f, o);
+            }
+            if (whole) {
+                const int row = u.rt * kRows + r;
+                const long long tok = u.q.row0 + row / p.G, head = head0 + row % p.G;
+                store_out(p, (tok * p.Hq + head) * D + d, no_key(M, L) ? 0.f : o / L);
+                if (d == 0 && p.lse) p.lse[head * p.total_q + tok] = row_lse(M, L);
+            } else {
+                ws.o[((long long)slot * p.RT + r) * D + d] = o;
+                if (d == 0) ws.ml[slot * p.RT + r] = make_float2(M, L);
+            }
+        }
+        if (u.starts && !u.ends && threadIdx.x == 0) {
+            Join& jn = ws.join[blockIdx.x];
+            jn.seq_row0 = u.q.row0;
+            jn.h = u.h;
+            jn.row0 = u.rt * kRows;
+            jn.rows = u.rows;
+            jn.parts = unit_parts(sh, u, at);
+        }
+        at += u.j1 - u.j0;
+    }
+}
+
+template <typename T, typename C>
+cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
+    const size_t smem = (size_t)kWarps * kRows * (p.D + 2) * 4;
+    auto kern = p.D <= 128 ? paged_simt_kernel<T, C, 1> : paged_simt_kernel<T, C, 2>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kern<<<kGrid, kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Share c's split unit, if one starts there: its parts in the order of the shares.
+__global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
+    const Workspace ws = workspace(p.ws, p.RT, p.D);
+    const Join jn = ws.join[blockIdx.x];
+    if (jn.parts <= 1) return;
+    const int D4 = p.D / 4, c = blockIdx.x;
+    for (int e = threadIdx.x; e < jn.rows * D4; e += blockDim.x) {
+        const int r = e / D4, d = (e - r * D4) * 4;
+        // part 0 in slot 2c + 1, part i in slot 2 (c + i)
+        auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+        float M = -INFINITY, L = 0.f;
+        for (int i = 0; i < jn.parts; ++i) M = fmaxf(M, ws.ml[slot(i) * p.RT + r].x);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < jn.parts; ++i) {
+            const float2 ml = ws.ml[slot(i) * p.RT + r];
+            if (no_key(ml.x, ml.y)) continue;
+            const float f = exp2f(ml.x - M);
+            const float4 x = *reinterpret_cast<const float4*>(ws.o + ((long long)slot(i) * p.RT + r) * p.D + d);
+            L = fmaf(ml.y, f, L);
+            o.x = fmaf(x.x, f, o.x);
+            o.y = fmaf(x.y, f, o.y);
+            o.z = fmaf(x.z, f, o.z);
+            o.w = fmaf(x.w, f, o.w);
+        }
+        const float inv = no_key(M, L) ? 0.f : 1.f / L;
+        const int row = jn.row0 + r;
+        const long long tok = jn.seq_row0 + row / p.G, head = (long long)jn.h * p.G + row % p.G;
+        const long long i0 = (tok * p.Hq + head) * p.D + d;
+        store_out(p, i0, o.x * inv);
+        store_out(p, i0 + 1, o.y * inv);
+        store_out(p, i0 + 2, o.z * inv);
+        store_out(p, i0 + 3, o.w * inv);
+        if (d == 0 && p.lse) p.lse[head * p.total_q + tok] = row_lse(M, L);
+    }
+}
+
+}  // namespace paged
+
+int paged_rows(int, int, int, int) { return paged::kRows; }
+size_t paged_workspace_bytes(int RT, int D) { return paged::workspace_bytes(RT, D); }
+
+cudaError_t launch_paged(const PagedParams& p, cudaStream_t stream) {
+    using namespace paged;
+    const bool codes = p.cache_dtype == TA_E4M3;
+    cudaError_t e;
+    switch (p.dtype) {
+    case TA_F32: e = codes ? launch<float, uint8_t>(p, stream) : launch<float, float>(p, stream); break;
+    case TA_F16: e = codes ? launch<__half, uint8_t>(p, stream) : launch<__half, __half>(p, stream); break;
+    default: e = codes ? launch<__nv_bfloat16, uint8_t>(p, stream) : launch<__nv_bfloat16, __nv_bfloat16>(p, stream);
+    }
+    if (e != cudaSuccess) return e;
+    paged_join_kernel<<<kGrid, 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace triattn
