@@ -64,12 +64,16 @@ typedef enum {
  *   CAUSAL          k <= q
  *   SLIDING_WINDOW  q - window < k <= q  (the query and the window - 1 keys before it)
  *   PREFIX_LM       k <= q  or  k < prefix  (the sequence's prefix is seen by every query)
- * The last two carry a parameter and are taken by tri_attn_varlen_fwd_masked only. */
+ *   SINK_WINDOW     k <= q  and  (k > q - window  or  k < sinks)  (a sliding window and the
+ *                   first `sinks` keys, which stay visible)
+ * All but the first two carry parameters and are taken by tri_attn_varlen_fwd_masked and
+ * tri_attn_varlen_bwd only. */
 typedef enum {
     TA_MASK_NONE = 0,
     TA_MASK_CAUSAL = 1,
     TA_MASK_SLIDING_WINDOW = 2,
-    TA_MASK_PREFIX_LM = 3
+    TA_MASK_PREFIX_LM = 3,
+    TA_MASK_SINK_WINDOW = 6
 } ta_mask_mod;
 
 /*
@@ -298,14 +302,17 @@ ta_status tri_attn_varlen_fwd_strided(const void* q, const void* k, const void* 
  *  Details 2, mask_mod applied on partial blocks only; the sliding-window and
  *  prefix-LM predicates are the two most common mask_mods besides causal.)
  *
- *   mask_mod        TA_MASK_NONE, TA_MASK_CAUSAL, TA_MASK_SLIDING_WINDOW or
- *                   TA_MASK_PREFIX_LM (else TA_ERR_INVALID_ARG)
- *   window          SLIDING_WINDOW: keys q - window < k <= q are kept; must be
- *                   >= 1 (else TA_ERR_INVALID_ARG); ignored otherwise
+ *   mask_mod        TA_MASK_NONE, TA_MASK_CAUSAL, TA_MASK_SLIDING_WINDOW,
+ *                   TA_MASK_PREFIX_LM or TA_MASK_SINK_WINDOW (else TA_ERR_INVALID_ARG)
+ *   window          SLIDING_WINDOW and SINK_WINDOW: keys q - window < k <= q are kept; must be
+ *                   >= 1 (else TA_ERR_INVALID_ARG); ignored otherwise.  SINK_WINDOW without block
+ *                   lists visits only the blocks that hold a kept (query, key); the others
+ *                   count as masked, so every result is as if they were visited.
  *   prefix_lengths  PREFIX_LM: optional (num_seqs) int32 on the device, the
  *                   prefix of each sequence (values <= 0 keep only causal
  *                   keys); when NULL, `prefix_length` (>= 0, else
- *                   TA_ERR_INVALID_ARG) applies to every sequence
+ *                   TA_ERR_INVALID_ARG) applies to every sequence.  SINK_WINDOW: the
+ *                   number of first keys that stay visible, given in the same way
  *   bias            optional post-scale bias (Transformer Engine fused_attn.h,
  *                   NVTE_Bias_Type NVTE_POST_SCALE_BIAS): (H, max_seqlen_q,
  *                   max_seqlen_k) of `bias_dtype` (TA_F32 or `dtype`, else

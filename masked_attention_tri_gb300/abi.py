@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(_PKG, "libtriattn.so")
 
 TA_OK, TA_ERR_INVALID_ARG, TA_ERR_UNSUPPORTED, TA_ERR_CUDA, TA_ERR_TIMEOUT, TA_ERR_DEVICE = range(6)
 TA_F32, TA_F16, TA_BF16, TA_E4M3 = 0, 1, 2, 3
-TA_MASK_NONE, TA_MASK_CAUSAL, TA_MASK_SLIDING_WINDOW, TA_MASK_PREFIX_LM = 0, 1, 2, 3
+TA_MASK_NONE, TA_MASK_CAUSAL, TA_MASK_SLIDING_WINDOW, TA_MASK_PREFIX_LM, TA_MASK_SINK_WINDOW = 0, 1, 2, 3, 6
 
 # Every symbol include/triattn.h declares.
 EXPORTS = ("tri_attn_fwd", "tri_attn_fwd_strided", "tri_attn_varlen_fwd", "tri_attn_varlen_fwd_strided", "tri_attn_varlen_fwd_masked",

@@ -18,7 +18,8 @@ from . import abi
 
 _DT = {torch.float32: abi.TA_F32, torch.float16: abi.TA_F16, torch.bfloat16: abi.TA_BF16}
 _MASK_MODS = {None: abi.TA_MASK_NONE, "none": abi.TA_MASK_NONE, "causal": abi.TA_MASK_CAUSAL,
-              "sliding_window": abi.TA_MASK_SLIDING_WINDOW, "prefix_lm": abi.TA_MASK_PREFIX_LM}
+              "sliding_window": abi.TA_MASK_SLIDING_WINDOW, "prefix_lm": abi.TA_MASK_PREFIX_LM,
+              "sink_window": abi.TA_MASK_SINK_WINDOW}
 
 
 def _ptr(t: Optional[torch.Tensor]) -> int:
@@ -272,9 +273,9 @@ class BlockMask:
     kv_num_blocks (S, Hm, MQ) and kv_indices (S, Hm, MQ, MK): partial blocks
     of each q block, where mask_mod applies; full_kv_* (optional, same shapes):
     blocks where every key is valid.  Indices are sequence-local 128-row
-    blocks.  mask_mod is None, "causal", "sliding_window" or "prefix_lm" (a C
-    ABI cannot take a callable; the last two take their parameter from
-    ``varlen_attention``'s ``window`` / ``prefix_lengths``).
+    blocks.  mask_mod is None, "causal", "sliding_window", "prefix_lm" or
+    "sink_window" (a C ABI cannot take a callable; the last three take their
+    parameters from ``varlen_attention``'s ``window`` / ``prefix_lengths`` / ``sinks``).
     seq_lengths (q_len, kv_len), as on the page's from_kv_blocks, fixes the
     number of kv blocks, i.e. the columns of ``to_dense``; without it the
     columns are the larger of MK and the highest listed block index + 1.
@@ -406,18 +407,29 @@ def _mask_args(block_mask, mask_mod, dev):
     return kn, ki, fn, fi, mask_heads, MQ, MK, bq, bk, mm
 
 
-def _prefix_args(prefix_lengths, S, dev):
-    """(per-sequence tensor or None, one length for all) for the prefix-LM mask_mod."""
+def _prefix_args(prefix_lengths, S, dev, mm=None, sinks=None):
+    """(per-sequence tensor or None, one length for all): the prefix of the prefix-LM mask_mod, or
+    the first keys that stay visible under the sink window."""
+    if sinks is not None:
+        if mm != abi.TA_MASK_SINK_WINDOW:
+            raise ValueError("sinks belong to mask_mod sink_window")
+        if not isinstance(sinks, torch.Tensor) and int(sinks) < 0:
+            raise ValueError("sinks must not be negative")
+    if mm == abi.TA_MASK_SINK_WINDOW:
+        if prefix_lengths is not None:
+            raise ValueError("mask_mod sink_window takes sinks, not prefix_lengths")
+        prefix_lengths = sinks
     if isinstance(prefix_lengths, torch.Tensor):
         _need(prefix_lengths, "prefix_lengths", dev)
         if prefix_lengths.dtype != torch.int32 or prefix_lengths.numel() != S:
-            raise ValueError("prefix_lengths must be int32 with one entry per sequence")
+            raise ValueError("prefix_lengths (sinks) must be int32 with one entry per sequence")
         return prefix_lengths, 0
     return None, (0 if prefix_lengths is None else int(prefix_lengths))
 
 
 def varlen_attention(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, block_mask=None, scale=None,
-                     return_aux=False, *, mask_mod=None, out=None, window=0, prefix_lengths=None, bias=None):
+                     return_aux=False, *, mask_mod=None, out=None, window=0, prefix_lengths=None, bias=None,
+                     sinks=None):
     """Packed-sequence forward with an optional BlockMask.
 
     q (total_q,H,D), k/v (total_k,H,D), cu_seqlens int32 (S+1,).  q, k, v may
@@ -425,9 +437,12 @@ def varlen_attention(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seql
     an interleaved QKV or KV buffer (see ``varlen_attention_qkvpacked`` /
     ``varlen_attention_kvpacked``); ``out`` is contiguous.  Without a
     block_mask every block is visited and ``mask_mod`` applies everywhere.
-    mask_mod: None, "causal" (k <= q), "sliding_window" (q - window < k <= q)
-    or "prefix_lm" (k <= q or k < the sequence's prefix; ``prefix_lengths`` is
-    an int or an int32 CUDA tensor with one length per sequence).  bias: an
+    mask_mod: None, "causal" (k <= q), "sliding_window" (q - window < k <= q),
+    "prefix_lm" (k <= q or k < the sequence's prefix; ``prefix_lengths`` is
+    an int or an int32 CUDA tensor with one length per sequence) or "sink_window" (k <= q and
+    k > q - window or k < ``sinks``, given like prefix_lengths: the window and the first
+    keys, which stay visible; without a block_mask only the blocks that hold a kept
+    pair are visited).  bias: an
     optional post-scale bias (H, max_seqlen_q, max_seqlen_k), float32 or q's
     dtype, indexed by each sequence's local positions.
     Returns O, or (O, lse, max) with lse/max (H, total_q).
@@ -468,7 +483,7 @@ def varlen_attention(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seql
             raise ValueError(f"bias must be (H, max_seqlen_q, max_seqlen_k) = {(H, int(max_seqlen_q), int(max_seqlen_k))}")
         if bias.dtype not in (torch.float32, q.dtype):
             raise TypeError("bias must be float32 or q's dtype")
-    pl, p_all = _prefix_args(prefix_lengths, S, dev)
+    pl, p_all = _prefix_args(prefix_lengths, S, dev, mm, sinks)
     with torch.cuda.device(dev):
         abi.tri_attn_varlen_fwd_masked(_ptr(q), _ptr(k), _ptr(v), _DT[q.dtype], _ptr(cu_seqlens_q),
                                        _ptr(cu_seqlens_k), S, total_q, k.shape[0], int(max_seqlen_q),
@@ -480,31 +495,32 @@ def varlen_attention(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seql
 
 
 def varlen_attention_qkvpacked(qkv, cu_seqlens, max_seqlen, block_mask=None, scale=None, return_aux=False, *,
-                               mask_mod=None, out=None, window=0, prefix_lengths=None):
+                               mask_mod=None, out=None, window=0, prefix_lengths=None, sinks=None):
     """NVTE_QKV_INTERLEAVED (Transformer Engine fused_attn.h): one (total, 3, H, D) buffer, q and k sharing
     cu_seqlens.  The kernels read q, k, v in place through row strides; no copy is made."""
     if qkv.dim() != 4 or qkv.shape[1] != 3:
         raise ValueError("expected qkv (total, 3, H, D)")
     q, k, v = qkv.unbind(1)
     return varlen_attention(q, k, v, cu_seqlens, cu_seqlens, max_seqlen, max_seqlen, block_mask, scale, return_aux,
-                            mask_mod=mask_mod, out=out, window=window, prefix_lengths=prefix_lengths)
+                            mask_mod=mask_mod, out=out, window=window, prefix_lengths=prefix_lengths, sinks=sinks)
 
 
 def varlen_attention_kvpacked(q, kv, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, block_mask=None,
                               scale=None, return_aux=False, *, mask_mod=None, out=None, window=0,
-                              prefix_lengths=None):
+                              prefix_lengths=None, sinks=None):
     """NVTE_KV_INTERLEAVED (Transformer Engine fused_attn.h): q (total_q, H, D) and one (total_k, 2, H, D)
     buffer for k and v, read in place through row strides."""
     if kv.dim() != 4 or kv.shape[1] != 2:
         raise ValueError("expected kv (total_k, 2, H, D)")
     k, v = kv.unbind(1)
     return varlen_attention(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, block_mask, scale,
-                            return_aux, mask_mod=mask_mod, out=out, window=window, prefix_lengths=prefix_lengths)
+                            return_aux, mask_mod=mask_mod, out=out, window=window, prefix_lengths=prefix_lengths,
+                            sinks=sinks)
 
 
 def varlen_attention_backward(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, out, lse, d_out,
                               block_mask=None, scale=None, *, mask_mod=None, window=0, prefix_lengths=None,
-                              bias=None, need_dbias=True):
+                              bias=None, need_dbias=True, sinks=None):
     """Gradients (dq, dk, dv, dbias) of ``varlen_attention`` for dL/dO = d_out.
 
     Arguments as given to the forward (q / k / v contiguous (total, H, D)), plus
@@ -536,7 +552,7 @@ def varlen_attention_backward(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
         raise ValueError("cu_seqlens_q / cu_seqlens_k must both have num_seqs + 1 entries")
     s = 1.0 / math.sqrt(D) if scale is None else float(scale)
     kn, ki, fn, fi, mask_heads, MQ, MK, bq, bk, mm = _mask_args(block_mask, mask_mod, dev)
-    pl, p_all = _prefix_args(prefix_lengths, S, dev)
+    pl, p_all = _prefix_args(prefix_lengths, S, dev, mm, sinks)
     if bias is not None:
         _need(bias, "bias", dev)
         if tuple(bias.shape) != (H, int(max_seqlen_q), int(max_seqlen_k)):

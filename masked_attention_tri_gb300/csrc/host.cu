@@ -49,6 +49,10 @@ using triattn::valid_dtype;
 
 namespace {
 
+bool has_window(int m) { return m == TA_MASK_SLIDING_WINDOW || m == TA_MASK_SINK_WINDOW; }
+bool has_prefix(int m) { return m == TA_MASK_PREFIX_LM || m == TA_MASK_SINK_WINDOW; }
+bool valid_mask_mod(int m) { return (m >= TA_MASK_NONE && m <= TA_MASK_PREFIX_LM) || m == TA_MASK_SINK_WINDOW; }
+
 // fp32 inputs run on the CUDA-core kernel; 16-bit inputs on the tensor-core kernels:
 // D <= 128 on tc_fwd / tc_split, D in (128, 256] on tc_wide (the triangle form with
 // contiguous q / k / v; packed sequences and strided views with D > 128 take the
@@ -205,9 +209,9 @@ TA_EXPORT ta_status tri_attn_varlen_fwd_masked(const void* q, const void* k, con
     if (num_seqs <= 0 || H <= 0 || D <= 0 || max_seqlen_q < 0 || max_seqlen_k < 0) return TA_ERR_INVALID_ARG;
     if (total_q < 0 || total_k < 0) return TA_ERR_INVALID_ARG;
     if (!valid_dtype(dtype)) return TA_ERR_INVALID_ARG;
-    if (mask_mod < TA_MASK_NONE || mask_mod > TA_MASK_PREFIX_LM) return TA_ERR_INVALID_ARG;
-    if (mask_mod == TA_MASK_SLIDING_WINDOW && window <= 0) return TA_ERR_INVALID_ARG;
-    if (mask_mod == TA_MASK_PREFIX_LM && !prefix_lengths && prefix_length < 0) return TA_ERR_INVALID_ARG;
+    if (!valid_mask_mod(mask_mod)) return TA_ERR_INVALID_ARG;
+    if (has_window(mask_mod) && window <= 0) return TA_ERR_INVALID_ARG;
+    if (has_prefix(mask_mod) && !prefix_lengths && prefix_length < 0) return TA_ERR_INVALID_ARG;
     if (prefix_lengths && !aligned(prefix_lengths, 4)) return TA_ERR_INVALID_ARG;
     if (bias) {
         // (H, max_seqlen_q, max_seqlen_k) of bias_dtype, read by the TMA: 16-byte aligned base
@@ -274,9 +278,9 @@ TA_EXPORT ta_status tri_attn_varlen_fwd_masked(const void* q, const void* k, con
     p.MQ = kv_num_blocks ? max_q_blocks : 0;
     p.MK = kv_num_blocks ? max_kv_blocks : 0;
     p.mask_mod = mask_mod;
-    p.window = mask_mod == TA_MASK_SLIDING_WINDOW ? window : 0;
-    p.prefix_len = mask_mod == TA_MASK_PREFIX_LM ? prefix_lengths : nullptr;
-    p.prefix_all = mask_mod == TA_MASK_PREFIX_LM ? prefix_length : 0;
+    p.window = has_window(mask_mod) ? window : 0;
+    p.prefix_len = has_prefix(mask_mod) ? prefix_lengths : nullptr;
+    p.prefix_all = has_prefix(mask_mod) ? prefix_length : 0;
     p.bias = bias;
     p.bias_f32 = bias && bias_dtype == TA_F32;
     p.total_q = total_q;
@@ -388,9 +392,9 @@ TA_EXPORT ta_status tri_attn_varlen_bwd(const void* q, const void* k, const void
     if (num_seqs <= 0 || H <= 0 || D <= 0 || max_seqlen_q < 0 || max_seqlen_k < 0) return TA_ERR_INVALID_ARG;
     if (total_q < 0 || total_k < 0) return TA_ERR_INVALID_ARG;
     if (!valid_dtype(dtype)) return TA_ERR_INVALID_ARG;
-    if (mask_mod < TA_MASK_NONE || mask_mod > TA_MASK_PREFIX_LM) return TA_ERR_INVALID_ARG;
-    if (mask_mod == TA_MASK_SLIDING_WINDOW && window <= 0) return TA_ERR_INVALID_ARG;
-    if (mask_mod == TA_MASK_PREFIX_LM && !prefix_lengths && prefix_length < 0) return TA_ERR_INVALID_ARG;
+    if (!valid_mask_mod(mask_mod)) return TA_ERR_INVALID_ARG;
+    if (has_window(mask_mod) && window <= 0) return TA_ERR_INVALID_ARG;
+    if (has_prefix(mask_mod) && !prefix_lengths && prefix_length < 0) return TA_ERR_INVALID_ARG;
     if (prefix_lengths && !aligned(prefix_lengths, 4)) return TA_ERR_INVALID_ARG;
     if ((kv_num_blocks == nullptr) != (kv_indices == nullptr)) return TA_ERR_INVALID_ARG;
     if ((full_kv_num_blocks == nullptr) != (full_kv_indices == nullptr)) return TA_ERR_INVALID_ARG;
@@ -461,9 +465,9 @@ TA_EXPORT ta_status tri_attn_varlen_bwd(const void* q, const void* k, const void
     p.MQ = kv_num_blocks ? max_q_blocks : 0;
     p.MK = kv_num_blocks ? max_kv_blocks : 0;
     p.mask_mod = mask_mod;
-    p.window = mask_mod == TA_MASK_SLIDING_WINDOW ? window : 0;
-    p.prefix_len = mask_mod == TA_MASK_PREFIX_LM ? prefix_lengths : nullptr;
-    p.prefix_all = mask_mod == TA_MASK_PREFIX_LM ? prefix_length : 0;
+    p.window = has_window(mask_mod) ? window : 0;
+    p.prefix_len = has_prefix(mask_mod) ? prefix_lengths : nullptr;
+    p.prefix_all = has_prefix(mask_mod) ? prefix_length : 0;
     p.status = triattn::status_word();
     if (!p.status) return TA_ERR_CUDA;
     p.tc_main = triattn::tc_bwd_supported(p) ? 1 : 0;  // 16-bit, D <= 128: tensor cores

@@ -118,12 +118,14 @@ __device__ __forceinline__ int block_status(const BwdParams& p, int seq, int h, 
     return 0;
 }
 // mask_mod on a partial block, local indices: causal k <= q; sliding window
-// q - window < k <= q; prefix LM k <= q or k < prefix.
+// q - window < k <= q; prefix LM k <= q or k < prefix; sink window k <= q and (k > q - window
+// or k < prefix).
 __device__ __forceinline__ bool mod_keep(int mod, int q, int k, int window, int prefix) {
     switch (mod) {
     case TA_MASK_CAUSAL: return k <= q;
     case TA_MASK_SLIDING_WINDOW: return k <= q && k > q - window;
     case TA_MASK_PREFIX_LM: return k <= q || k < prefix;
+    case TA_MASK_SINK_WINDOW: return k <= q && (k > q - window || k < prefix);
     default: return true;
     }
 }
@@ -311,7 +313,12 @@ __global__ void __launch_bounds__(kBW * 32) bwd_main_kernel(const BwdParams p) {
         for (int c = 0; c < DPL; ++c) dk[j][c] = dv[j][c] = 0.f;
     const BT* bias = static_cast<const BT*>(p.bias);
 
+    // Sink window without lists: a tile that keeps no (query, key) is skipped, unless a query may
+    // have no valid key at all (then its weights 1 / Lk reach every key).
+    const bool sunk = VARLEN && !p.kv_num && p.mask_mod == TA_MASK_SINK_WINDOW &&
+                      (prefix > 0 || (long long)Lq - Lk < p.window);
     for (int q0 = 0; q0 < Lq; q0 += kT) {
+        if (sunk && !sink_blocks(q0, min(q0 + kT, Lq) - 1, Lk, p.window, prefix).visited(k0 / 128)) continue;
         __syncthreads();  // the previous tile's Qs, dOs, Ps, dSs are no longer read
         load_tile(Qs, static_cast<const T*>(p.q), qbase, q0, Lq, D, rs);
         load_tile(dOs, static_cast<const T*>(p.d_out), qbase, q0, Lq, D, rs);

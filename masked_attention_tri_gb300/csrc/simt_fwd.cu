@@ -123,6 +123,8 @@ __device__ void simt_tile(SimtState<T, BT, DPL>& st, int key0, int mode) {
             if (p.mask_mod == TA_MASK_CAUSAL) valid = valid && key <= qrow;
             else if (p.mask_mod == TA_MASK_SLIDING_WINDOW) valid = valid && key <= qrow && qrow - key < p.window;
             else if (p.mask_mod == TA_MASK_PREFIX_LM) valid = valid && (key <= qrow || key < st.prefix_lm);
+            else if (p.mask_mod == TA_MASK_SINK_WINDOW)
+                valid = valid && key <= qrow && (qrow - key < p.window || key < st.prefix_lm);
         }
         float x;
         if (!exists) {
@@ -273,8 +275,11 @@ __global__ void __launch_bounds__(kWarps * 32) simt_fwd_kernel(const AttnParams 
         const int nbk = (st.Lk + 127) / 128;
         const int qb = st.q0 / 128;
         if (!p.kv_num) {
+            const bool sunk = p.mask_mod == TA_MASK_SINK_WINDOW;
+            SinkBlocks sb{0, 0, -1};
+            if (sunk) sb = sink_blocks(st.q0, min(st.q0 + kQT, Lq) - 1, st.Lk, p.window, st.prefix_lm);
             for (int kb = 0; kb < nbk; ++kb)
-                for (int t = 0; t < 4; ++t)
+                for (int t = 0; t < 4 && (!sunk || sb.visited(kb)); ++t)
                     if (kb * 128 + t * kKT < st.Lk)
                         simt_tile(st, kb * 128 + t * kKT, p.mask_mod != TA_MASK_NONE ? kKeyMod : kKeyAll);
         } else if (qb < p.MQ) {

@@ -139,12 +139,14 @@ constexpr int kProducerWarp = kComputeWarps, kMmaWarp = kComputeWarps + 1;
 constexpr int kBwdThreads = (kComputeWarps + 2) * 32;
 
 // mask_mod on a partial block (indices local to the sequence): causal k <= q; sliding window
-// q - window < k <= q; prefix LM k <= q or k < prefix (tensorplay BlockMask page, Details 2).
+// q - window < k <= q; prefix LM k <= q or k < prefix (tensorplay BlockMask page, Details 2);
+// sink window k <= q and (k > q - window or k < prefix).
 __device__ __forceinline__ bool bwd_mod_keep(int mod, int q, int k, int window, int prefix) {
     switch (mod) {
     case TA_MASK_CAUSAL: return k <= q;
     case TA_MASK_SLIDING_WINDOW: return k <= q && k > q - window;
     case TA_MASK_PREFIX_LM: return k <= q || k < prefix;
+    case TA_MASK_SINK_WINDOW: return k <= q && (k > q - window || k < prefix);
     default: return true;
     }
 }
@@ -258,8 +260,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
             uint32_t* qw = reinterpret_cast<uint32_t*>(gbase + L.qlist);
             const int kb = k0 / kBN, nqb = (Qn + kBM - 1) / kBM;
             int cnt = 0;
+            // Sink window without lists: q blocks without a kept (query, key) are left out.  Their
+            // rows all have a valid key (their own, or a first one) unless there are more
+            // queries than keys and window reach.
+            const bool sunk = !P.kv_num && P.mask_mod == TA_MASK_SINK_WINDOW;
+            const bool all_valid = prefix > 0 || (long long)Qn - Kn < P.window;
             for (int qb = 0; qb < nqb && qb < P.qcap; ++qb) {
                 int st = 1;  // no lists: every block partial
+                if (sunk) {
+                    st = sink_blocks(qb * kBM, min(qb * kBM + kBM, Qn) - 1, Kn, P.window, prefix).visited(kb) ? 1 : 0;
+                    if (st == 0 && all_valid) continue;
+                }
                 if (P.kv_num) {
                     int f = 0;
                     if (qb < P.MQ) {
@@ -708,6 +719,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                         case TA_MASK_CAUSAL: whole = kmax <= qmin; break;
                         case TA_MASK_SLIDING_WINDOW: whole = kmax <= qmin && kmin > qmax - P.window; break;
                         case TA_MASK_PREFIX_LM: whole = kmax <= qmin || kmax < prefix; break;
+                        case TA_MASK_SINK_WINDOW:
+                            whole = kmax <= qmin && (kmin > qmax - P.window || kmax < prefix);
+                            break;
                         default: whole = false;
                         }
                     }

@@ -394,12 +394,14 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 //   causal          k <= q
 //   sliding window  q - window < k <= q
 //   prefix LM       k <= q or k < prefix
+//   sink window     k <= q and (k > q - window or k < prefix)
 __device__ __forceinline__ uint32_t mod_bits(int mod, int q, int kg, int window, int prefix) {
     const uint32_t causal = low_bits(q - kg + 1);
     switch (mod) {
     case TA_MASK_CAUSAL: return causal;
     case TA_MASK_SLIDING_WINDOW: return causal & ~low_bits(q - window + 1 - kg);
     case TA_MASK_PREFIX_LM: return causal | low_bits(prefix - kg);
+    case TA_MASK_SINK_WINDOW: return causal & (~low_bits(q - window + 1 - kg) | low_bits(prefix - kg));
     default: return 0xffffffffu;
     }
 }
@@ -412,6 +414,7 @@ __device__ __forceinline__ bool mod_tile_all(int mod, int q0, int key0, int wind
     case TA_MASK_CAUSAL: return causal;
     case TA_MASK_SLIDING_WINDOW: return causal && (q0 + 127) - key0 < window;
     case TA_MASK_PREFIX_LM: return causal || key0 + 128 <= prefix;
+    case TA_MASK_SINK_WINDOW: return causal && ((q0 + 127) - key0 < window || key0 + 128 <= prefix);
     default: return true;
     }
 }

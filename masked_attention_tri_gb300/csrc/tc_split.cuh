@@ -64,6 +64,8 @@ struct VEntry {
     int seq, h, qb, nkt;       // nkt < 0: no more items
     int q_row0, Lq, k_row0, Lk;
     int nkb, n_part, n_full, lists;
+    SinkBlocks sink;           // no lists, sink window: the visited blocks
+    int sunk;                  // 1: `sink` decides
     const int32_t* part_l;
     const int32_t* full_l;
     unsigned long long part0, full0;
@@ -118,6 +120,8 @@ struct SItem {
     const int32_t* part_l;
     const int32_t* full_l;
     int n_part, n_full;
+    bool sunk;          // packed form, sink window without lists: `sink` says which blocks are visited
+    SinkBlocks sink;
     uint64_t part0, full0;  // packed form: visited blocks of window 0 (blocks 0..63)
 };
 
@@ -137,6 +141,11 @@ __device__ __forceinline__ void split_window(const SItem& it, int w, uint64_t& p
     if (!it.lists) {
         part = range;
         full = 0;
+        if (it.sunk) {
+            // bits below n of the 64 blocks from `lo`
+            auto below = [&](int kb) { return kb <= lo ? 0ull : (kb - lo >= 64 ? ~0ull : (1ull << (kb - lo)) - 1ull); };
+            part &= below(it.sink.nsink) | (below(it.sink.hi + 1) & ~below(it.sink.lo));
+        }
         return;
     }
     const int lane = threadIdx.x % 32;
@@ -223,6 +232,8 @@ __device__ __forceinline__ SItem split_decode(const TcParams& P, const int* sche
     it.part0 = it.full0 = 0;
     it.prefix = 0;
     it.q_row0 = it.k_row0 = 0;
+    it.sunk = false;
+    it.sink = SinkBlocks{0, 0, -1};
     if constexpr (!VARLEN) {
         const Item<1> t = decode<1, false>(P, item, pre_len);
         it.qt = t.qt[0];
@@ -268,6 +279,11 @@ __device__ __forceinline__ SItem split_decode(const TcParams& P, const int* sche
                 it.n_part = min(max(a.kv_num[row], 0), a.MK);
                 if (a.full_num) it.n_full = min(max(a.full_num[row], 0), a.MK);
             }
+        }
+        if (a.kv_num == nullptr && a.mask_mod == TA_MASK_SINK_WINDOW) {
+            it.sunk = true;
+            it.sink = sink_blocks(qb * kBM, min(qb * kBM + kBM, it.Lq) - 1, it.Lk, a.window,
+                                  a.prefix_len ? a.prefix_len[seq] : a.prefix_all);
         }
         split_window(it, 0, it.part0, it.full0, pre_p, pre_f);
         int nkt = __popcll(it.part0 | it.full0);
@@ -383,6 +399,8 @@ struct ItemWalk<true> {
         it.full_l = v->full_l;
         it.n_part = v->n_part;
         it.n_full = v->n_full;
+        it.sunk = v->sunk != 0;
+        it.sink = v->sink;
         it.part0 = v->part0;
         it.full0 = v->full0;
         it.unit = it.bn = 0;
@@ -740,6 +758,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tc_split_kernel(const __grid
                         e->n_part = it.n_part;
                         e->n_full = it.n_full;
                         e->lists = it.lists ? 1 : 0;
+                        e->sunk = it.sunk ? 1 : 0;
+                        e->sink = it.sink;
                         e->part_l = it.part_l;
                         e->full_l = it.full_l;
                         e->part0 = it.part0;
