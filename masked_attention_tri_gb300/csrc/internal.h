@@ -194,6 +194,7 @@ struct PagedParams {
     int num_seqs, total_q, max_q, Hq, Hk, G, D, num_pages, page, max_pages;
     int window, sinks;          // window 0: every earlier slot
     int RT;                     // rows of a unit
+    int tile;                   // slots of a tile (64 or 32)
     float scale_log2e;
     long long q_rs;
     long long ks[3], vs[3];     // element strides {page, head, slot} of the caches

@@ -8,7 +8,7 @@
 // k < sinks.
 //
 // A unit is up to RT rows of one (sequence, kv head): its n tokens x G grouped query
-// heads, row r = token * G + head.  A unit visits the 64-slot tiles that hold a key one of
+// heads, row r = token * G + head.  A unit visits the tiles (of p.tile slots) that hold a key one of
 // its rows sees: all up to the last row's position, or those of the first `sinks` slots
 // and those from the first row's window on.  The units' tiles, in the order
 // (sequence, kv head, row tile), form one axis that is cut into equal shares, one
@@ -31,7 +31,6 @@
 namespace triattn {
 namespace paged {
 
-constexpr int kTile = 64;      // slots of a tile
 constexpr int kGrid = 152;     // shares (one CTA per SM)
 constexpr int kMaxRT = 32;     // rows of a unit, at most
 
@@ -93,11 +92,11 @@ __device__ __forceinline__ Tiles unit_tiles(const PagedParams& p, const Seq& q, 
     t.p0 = q.len - q.n + r0 / p.G;
     t.p1 = q.len - q.n + r1 / p.G;
     t.sink_t = t.lo_t = 0;
-    t.nt = t.p1 < 0 ? 0 : t.p1 / kTile + 1;
+    t.nt = t.p1 < 0 ? 0 : t.p1 / p.tile + 1;
     if (p.window > 0 && t.p1 >= 0) {
         const long long lo = (long long)t.p0 - p.window + 1;
-        const int lo_t = lo > 0 ? (int)(lo / kTile) : 0;
-        const int sink_t = (min(p.sinks, t.p1 + 1) + kTile - 1) / kTile;
+        const int lo_t = lo > 0 ? (int)(lo / p.tile) : 0;
+        const int sink_t = (min(p.sinks, t.p1 + 1) + p.tile - 1) / p.tile;
         if (lo_t > sink_t) {
             t.lo_t = lo_t;
             t.sink_t = sink_t;
@@ -274,7 +273,11 @@ __device__ __forceinline__ float row_lse(float m, float l) {
     return no_key(m, l) ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-__global__ void paged_join_kernel(const PagedParams p);
+// Joins the split units (paged_simt.cu), after the kernel that left their parts.
+cudaError_t launch_join(const PagedParams& p, cudaStream_t stream);
+cudaError_t launch_simt(const PagedParams& p, cudaStream_t stream);
+// 16-bit queries on tensor cores (paged_mma*.cu).
+cudaError_t launch_mma(const PagedParams& p, cudaStream_t stream);
 
 }  // namespace paged
 }  // namespace triattn

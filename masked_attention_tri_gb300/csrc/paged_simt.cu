@@ -35,7 +35,7 @@ __device__ __forceinline__ float4 load4<uint8_t>(const uint8_t* p) {
 }
 
 // NC: vectors of 4 elements a lane (D up to 128 NC).
-template <typename T, typename C, int NC>
+template <typename C, int NC>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams p) {
     extern __shared__ float smem[];  // O [kWarps][kRows][D], (m, l) [kWarps][kRows]
     __shared__ long long scan[kWarps], found[2];
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
             for (int c = 0; c < NC; ++c) {
                 const int d = (c * 32 + lane) * 4;
                 qf[r][c] = row < u.q.n * p.G && d < D
-                               ? load4<T>(static_cast<const T*>(p.q) + tok * p.q_rs + head * D + d)
+                               ? load4<float>(static_cast<const float*>(p.q) + tok * p.q_rs + head * D + d)
                                : make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
         float m = -INFINITY, l = 0.f;  // m of row lane % 8; l: this lane's share of the sum
 
         for (int j = u.j0 + warp; j < u.j1 && j < u.t.nt; j += kWarps) {
-            const int key_t = u.t.tile(j) * kTile;
-            for (int k0 = key_t; k0 < key_t + kTile; k0 += 4) {
+            const int key_t = u.t.tile(j) * p.tile;
+            for (int k0 = key_t; k0 < key_t + p.tile; k0 += 4) {
                 // (pages hold at least 16 slots: four slots lie in one)
                 if (!unit_sees(p, u.t, k0) && !unit_sees(p, u.t, k0 + 1) && !unit_sees(p, u.t, k0 + 2) &&
                     !unit_sees(p, u.t, k0 + 3))
@@ -228,18 +228,6 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
     }
 }
 
-template <typename T, typename C>
-cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
-    const size_t smem = (size_t)kWarps * kRows * (p.D + 2) * 4;
-    auto kern = p.D <= 128 ? paged_simt_kernel<T, C, 1> : paged_simt_kernel<T, C, 2>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    kern<<<kGrid, kThreads, smem, stream>>>(p);
-    return cudaGetLastError();
-}
-
-}  // namespace
-
 // Share c's split unit, if one starts there: its parts in the order of the shares.
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
     const Workspace ws = workspace(p.ws, p.RT, p.D);
@@ -276,23 +264,41 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
     }
 }
 
+template <typename C>
+cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
+    const size_t smem = (size_t)kWarps * kRows * (p.D + 2) * 4;
+    auto kern = p.D <= 128 ? paged_simt_kernel<C, 1> : paged_simt_kernel<C, 2>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kern<<<kGrid, kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_simt(const PagedParams& p, cudaStream_t stream) {
+    return p.cache_dtype == TA_E4M3 ? launch<uint8_t>(p, stream) : launch<float>(p, stream);
+}
+
+cudaError_t launch_join(const PagedParams& p, cudaStream_t stream) {
+    paged_join_kernel<<<kGrid, 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
 }  // namespace paged
 
-int paged_rows(int, int, int, int) { return paged::kRows; }
+// Rows of a unit: eight on CUDA cores; on tensor cores one to four groups of eight (two for D > 128, where
+// four would not leave registers for the accumulators), as few as hold a sequence's rows.
+int paged_rows(int dtype, int max_q, int G, int D) {
+    const long long rows = (long long)max_q * G;
+    if (dtype == TA_F32 || rows <= 8) return 8;
+    return rows <= 16 || D > 128 ? 16 : 32;
+}
 size_t paged_workspace_bytes(int RT, int D) { return paged::workspace_bytes(RT, D); }
 
 cudaError_t launch_paged(const PagedParams& p, cudaStream_t stream) {
-    using namespace paged;
-    const bool codes = p.cache_dtype == TA_E4M3;
-    cudaError_t e;
-    switch (p.dtype) {
-    case TA_F32: e = codes ? launch<float, uint8_t>(p, stream) : launch<float, float>(p, stream); break;
-    case TA_F16: e = codes ? launch<__half, uint8_t>(p, stream) : launch<__half, __half>(p, stream); break;
-    default: e = codes ? launch<__nv_bfloat16, uint8_t>(p, stream) : launch<__nv_bfloat16, __nv_bfloat16>(p, stream);
-    }
-    if (e != cudaSuccess) return e;
-    paged_join_kernel<<<kGrid, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    const cudaError_t e = p.dtype == TA_F32 ? paged::launch_simt(p, stream) : paged::launch_mma(p, stream);
+    return e == cudaSuccess ? paged::launch_join(p, stream) : e;
 }
 
 }  // namespace triattn

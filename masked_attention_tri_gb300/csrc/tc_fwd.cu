@@ -158,6 +158,18 @@ bool encode_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint
                    uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2, CUtensorMapSwizzle sw) {
     return get_encode() && make_map(m, dt, ptr, d0, d1, d2, s1, s2, b0, b1, b2, sw);
 }
+// And with the paged cache (paged_mma.cu): a 4-D map.
+bool encode_map_4d(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, const uint64_t (&dims)[4],
+                   const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle sw) {
+    if (!get_encode()) return false;
+    cuuint64_t d[4], st[3];
+    cuuint32_t b[4];
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) d[i] = dims[i], b[i] = box[i];
+    for (int i = 0; i < 3; ++i) st[i] = strides[i];
+    return g_encode(m, dt, 4, const_cast<void*>(ptr), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 int device_sm_count() { return num_sms(); }
 
 }  // namespace tc

@@ -283,6 +283,15 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* tm,
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int c0, int c1, int c2, int c3,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
 // A triangle-form q / k / v tile: rows [row, row + 128) of slab (b, n, h) from
 // the 3-D (contiguous) or 5-D (strided) map.
 __device__ __forceinline__ void tma_load_tri(const TcParams& P, uint32_t dst, const CUtensorMap* tm, int c0, int row,
