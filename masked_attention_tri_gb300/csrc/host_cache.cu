@@ -237,7 +237,7 @@ TA_EXPORT ta_status tri_attn_paged_fwd(const void* q, ta_dtype dtype, const int3
     p.window = window;
     p.sinks = sinks;
     p.RT = paged_rows(dtype, max_seqlen_q, p.G, D);
-    p.tile = dtype != TA_F32 && cache_dtype != TA_E4M3 && D > 128 ? 32 : 64;
+    p.tile = paged_tile(dtype, cache_dtype, D);
     p.scale_log2e = scale * 1.4426950408889634f;
     p.q_rs = q_row_stride;
     p.status = status_word();

@@ -194,12 +194,13 @@ struct PagedParams {
     int num_seqs, total_q, max_q, Hq, Hk, G, D, num_pages, page, max_pages;
     int window, sinks;          // window 0: every earlier slot
     int RT;                     // rows of a unit
-    int tile;                   // slots of a tile (64 or 32)
+    int tile;                   // slots of a tile
     float scale_log2e;
     long long q_rs;
     long long ks[3], vs[3];     // element strides {page, head, slot} of the caches
 };
 int paged_rows(int dtype, int max_q, int G, int D);  // RT of a problem
+int paged_tile(int dtype, int cache_dtype, int D);   // and its tile
 size_t paged_workspace_bytes(int RT, int D);
 cudaError_t launch_paged(const PagedParams& p, cudaStream_t stream);
 

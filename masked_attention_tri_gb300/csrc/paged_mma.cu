@@ -37,12 +37,11 @@ cudaError_t launch_mma(const PagedParams& p, cudaStream_t stream) {
     P.p = p;
     const bool codes = p.cache_dtype == TA_E4M3;
     const uint64_t esz = codes ? 1 : 2;
-    const CUtensorMapDataType dt = codes                          ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                   : p.cache_dtype == TA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    // (codes move as pairs: only their bytes count)
+    const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_UINT16;
     // (D, slot, head, page); boxes of 128 bytes x the slots of a page that fall in one tile
-    const uint64_t dims[4] = {(uint64_t)p.D, (uint64_t)p.page, (uint64_t)p.Hk, (uint64_t)p.num_pages};
-    const uint32_t box[4] = {(uint32_t)(128 / esz), (uint32_t)(p.page < p.tile ? p.page : p.tile), 1, 1};
+    const uint64_t dims[4] = {(uint64_t)p.D * esz / 2, (uint64_t)p.page, (uint64_t)p.Hk, (uint64_t)p.num_pages};
+    const uint32_t box[4] = {64u, (uint32_t)(p.page < p.tile ? p.page : p.tile), 1, 1};
     const uint64_t ks[3] = {p.ks[2] * esz, p.ks[1] * esz, p.ks[0] * esz};
     const uint64_t vs[3] = {p.vs[2] * esz, p.vs[1] * esz, p.vs[0] * esz};
     if (!tc::encode_map_4d(&P.tm_k, dt, p.k_cache, dims, ks, box, CU_TENSOR_MAP_SWIZZLE_128B) ||

@@ -4,29 +4,35 @@
 //
 // Bound: memory.  Each visible byte of K and V is read once, and a new token brings
 // only its few grouped heads to multiply it with: 4 G FLOPs a byte in 8 bits, 2 G in 16.
-// Eight query rows are one n8 operand, so mma.sync m16n8k16 takes K (16 slots) and V^T
-// (16 columns) as its A operand with no row of padding for G = 8; a tcgen05 tile has 128
-// rows and would carry 8.  The kernel therefore aims to keep loads in flight:
-// one producer warp fills a ring of stages (a tile of K and of V each, up to 190 KB) by TMA,
-// 128-byte swizzled; seven consumer warps take the stages in turn, each with a running
-// maximum, sum and O of its own, and merge once at the unit's end.  No warp waits for
-// another within a unit.
+// Eight query rows are one n8 operand, so mma.sync takes K (16 slots) and V^T (16 columns) as
+// its A operand with no row of padding for G = 8; a tcgen05 tile has 128 rows and would carry
+// 8.  The kernel therefore aims to keep loads in flight: one producer warp fills a ring of
+// stages (a tile of K and of V each, up to 190 KB) by TMA, 128-byte swizzled; the consumer
+// warps take blocks of 16 slots, each with a running maximum, sum and O of its own, and
+// merge once at the unit's end.  No warp waits for another within a unit.  A warp takes a
+// whole stage (four blocks) at a time where there are plenty, or single blocks where the share
+// holds few tiles and the time of one tile on one warp would be what counts.  The loop over
+// blocks is not unrolled: 16 slots' code fits the instruction cache of a cold start.
 //
-//   S^T = K Q^T   A: slots x d from shared memory, B: Q^T, kept in fragment order
+//   S^T = K Q^T      A: slots x d from shared memory, B: Q^T, kept in fragment order
 //   O^T += V^T P^T   A: d x slots; P^T comes from S^T's accumulators by movmatrix
 //
-// Fragments straight from the swizzled rows.  A product's k index may be permuted if both
-// operands agree, and the 16 rows of A may be any slots (or columns of V).  So lane (g, t)
-// = (lane / 4, lane % 4) reads whole 16-byte pieces: row g of K's A operand is slot pi(g),
-// pi(2i) = 2i, pi(2i + 1) = (2i ^ 4) + 1, which makes every shared-memory read below
-// free of bank conflicts: 8 lanes of K's reads meet rows whose bit 2 differs, and
-// V's reads four rows 0, 2, 4, 6 or 5, 7, 1, 3.  8-bit codes go to fp16 by
-// cvt.rn.f16x2.e4m3x2 (exact); pairs of slots of V^T are put together by prmt first.
+// 8-bit codes become fp16 on the way, by cvt.rn.f16x2.e4m3x2 (exact): the ALU's two operations a clock an
+// SM are the kernel's second bound.  (mma.sync takes e4m3 operands itself, but on this GPU each such
+// product is ten instructions more: the conversions again, for every use.)  Queries of an 8-bit
+// cache are fp16 scaled by a power of two, their row's largest magnitude in [1, 2): exact down to 2^-14 of it
+// and off by 2^-25 of it below.
+//
+// Fragments.  K (and 16-bit V, transposed) by ldmatrix, whose four matrices are an A operand's four
+// registers as they stand; of 8-bit K a matrix holds 16 columns, a lane's four codes are two pairs, and
+// k index 2t, 2t + 1, 2t + 8, 2t + 9 of a product stands for columns 4t to 4t + 3.  8-bit V^T: lane (g, t) = (lane / 4, lane % 4) reads eight columns of four slots
+// and pairs the slots' bytes by prmt.  The 16 rows of K's operand may be any slots: row g is slot pi(g)
+// (and row g + 8 slot pi(g) + 8), pi(2i) = 2i, pi(2i + 1) = (2i ^ 4) + 1, so that the lanes' slots of V
+// are 0, 2, 4, 6 and 5, 7, 1, 3 in turn, whose swizzled reads meet no bank twice.
 //
 // Roundings: P to the products' 16-bit type (fp16 for 8-bit caches: 2^-12 of a weight),
-// as everywhere in this library; S, the maxima, sums and O are fp32.  bf16 queries of an
-// 8-bit cache become fp16 scaled by a power of two to [1, 2) at their row's largest magnitude: exact
-// down to 2^-14 of it, off by 2^-25 of it below.
+// as everywhere in this library; S, the maxima, sums and O are fp32.  O is rescaled only
+// when a logit passes the reference by 2^8 (base 2: by 8), which fp16's range allows.
 #pragma once
 
 #include "paged.cuh"
@@ -43,18 +49,23 @@ using tc::pack2;
 using tc::smem_u32;
 using tc::wait_bar;
 
-// Consumers: with the producer eight warps, two on each of the SM's four register files, so that a
-// thread may have 255 registers (a ninth warp would leave it 168: the wider variants would spill).
-constexpr int kMmaWarps = 7;
-constexpr int kMmaThreads = (kMmaWarps + 1) * 32;   // and the producer
-constexpr int kMmaMinTiles = 4;
+struct Yes {
+    static constexpr bool value = true;
+};
+struct No {
+    static constexpr bool value = false;
+};
+
 constexpr uint32_t kMmaSmem = 232448 - 1024 - 256;  // 227 KB less the alignment of the ring and the static part
 
-struct StageMeta {
-    float ks[4], vlog2[4], vinv[4];  // by 16 slots: key scale, log2 and reciprocal of the value scale
+// What the producer tells of a stage; sc[i]: key scale, log2 and reciprocal of the value scale of the i-th
+// page in it (written as one 16-byte store).
+struct alignas(16) StageMeta {
+    float4 sc[8];
     uint32_t valid;                  // bit b: slots [16 b, 16 b + 16) were loaded
     int key0;
-    int pad[2];
+    int use;                         // how often the stage has been given out, less one
+    int pad;
 };
 
 struct MmaParams {
@@ -65,26 +76,28 @@ struct MmaParams {
 // TYPE: 0 fp16 cache, 1 bf16 cache, 2 e4m3 codes.  NDC: 64-column chunks of D.  NT: groups of eight rows.
 template <int TYPE, int NDC, int NT>
 struct MmaConfig {
-    static constexpr int kSlots = TYPE != 2 && NDC == 4 ? 32 : 64;      // slots of a stage
-    static constexpr int kBoxes = TYPE == 2 ? (NDC + 1) / 2 : NDC;      // 128-byte columns of a tile
+    static constexpr bool kCodes = TYPE == 2;
+    static constexpr int kBoxes = kCodes ? (NDC + 1) / 2 : NDC;         // 128-byte columns of a tile
+    static constexpr int kSlots = 128 / kBoxes;                         // slots of a stage: 32 KB, K and V
     static constexpr uint32_t kBoxBytes = kSlots * 128;
     static constexpr uint32_t kStage = 2 * kBoxes * kBoxBytes;          // K boxes, then V boxes
     static constexpr int kRows = NT * 8;
+    // Consumers: with the producer eight warps, so that a thread may have 255 registers (O alone takes 16 NDC
+    // NT).  Measured on 64 sequences of 1k to 16k slots in 8 bits: 7 warps 226 us, 11 warps 257, 15 warps
+    // 275: the more warps work on stages at a time, the fewer stages are left for copies in flight.
+    static constexpr int kWarps = 7;
+    static constexpr int kThreads = (kWarps + 1) * 32;
+    static constexpr int kBufs = 4;                                     // merge buffers (no more than warps)
     static constexpr int kOStride = NDC * 64 + 4;                       // floats of a merged row
-    static constexpr uint32_t kQ = NDC * 4 * NT * 32 * 8;               // Q in fragment order
-    static constexpr uint32_t kO = 4u * kRows * kOStride * 4;           // merge buffers
-    static constexpr uint32_t kFixed = kQ + kO + kMmaWarps * kRows * 8 + kRows * 8 + kRows * 4 + 16 * 16;
+    static constexpr uint32_t kQ = NDC * NT * 1024;  // Q in fragment order
+    static constexpr uint32_t kO = (uint32_t)kBufs * kRows * kOStride * 4;
+    static constexpr uint32_t kFixed = kQ + kO + kWarps * kRows * 8 + kRows * 8 + kRows * 4 + 16 * 16;
     static constexpr int kFit = (int)((kMmaSmem - kFixed) / (kStage + sizeof(StageMeta)));
     static constexpr int kStages = kFit > 12 ? 12 : kFit;
     static constexpr uint32_t kSmem = kStages * (kStage + (uint32_t)sizeof(StageMeta)) + kFixed + 1024;
     static_assert(kStages >= 2, "two stages at least");
 };
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
@@ -92,6 +105,11 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 }
 __device__ __forceinline__ void ldsm_x4_t(uint32_t a, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(a));
 }
@@ -111,6 +129,9 @@ __device__ __forceinline__ uint32_t codes_f16_hi(uint32_t two) {
     asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(y) : "r"(two));
     return y;
 }
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
     if constexpr (BF16)
@@ -129,13 +150,37 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 // Slot (within eight) of row i of an A operand.
 __device__ __forceinline__ int pi8(int i) { return (i & 1) ? ((i - 1) ^ 4) + 1 : i; }
 
-__device__ __forceinline__ void consumers_sync() { tc::named_barrier(1, kMmaWarps * 32); }
+// Waits until use `use` of a stage has arrived.  A parity wait alone can tell only two neighbouring
+// uses apart, and warps run free: one may ask for a use while the one before it is still in
+// flight.  So the producer's count is awaited first: once it says `use`, the use before it has
+// arrived and been read.  Bounded like wait_bar.
+static __device__ __noinline__ bool wait_use_slow(const volatile int* count, int use, volatile int* abort_flag,
+                                                  int* status) {
+    const long long t0 = clock64();
+    for (uint32_t it = 1; *count != use; ++it) {
+        if (*abort_flag) return false;
+        if ((it & 63) == 0 && clock64() - t0 > tc::kTimeoutCycles) {
+            *abort_flag = 1;
+            atomicCAS(status, 0, kStatusTimeout);
+            return false;
+        }
+        __nanosleep(32);
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait_stage(const volatile int* count, int use, uint32_t bar, volatile int* abort_flag,
+                                           int* status) {
+    return (*count == use || wait_use_slow(count, use, abort_flag, status)) &&
+           wait_bar(bar, (uint32_t)use & 1u, abort_flag, status);
+}
 
 template <int TYPE, int NDC, int NT>
-__global__ void __launch_bounds__(kMmaThreads, 1) paged_mma_kernel(const __grid_constant__ MmaParams P) {
+__global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_mma_kernel(const __grid_constant__ MmaParams P) {
     using C = MmaConfig<TYPE, NDC, NT>;
     constexpr bool kBF16 = TYPE == 1;
-    constexpr int kMT = C::kSlots / 16;
+    constexpr bool kCodes = C::kCodes;
+    constexpr int kBlocks = C::kSlots / 16;
+    constexpr int kWarps = C::kWarps;
     const PagedParams& p = P.p;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -145,12 +190,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma_kernel(const __grid_
     const uint32_t ring = base;
     StageMeta* meta = reinterpret_cast<StageMeta*>(g0 + C::kStages * C::kStage);
     float* so = reinterpret_cast<float*>(meta + C::kStages);
-    uint2* sq = reinterpret_cast<uint2*>(so + 4 * C::kRows * C::kOStride);
-    float2* sml = reinterpret_cast<float2*>(sq + NDC * 4 * NT * 32);
-    float2* srow = sml + kMmaWarps * C::kRows;
+    uint8_t* sq = reinterpret_cast<uint8_t*>(so + C::kBufs * C::kRows * C::kOStride);
+    float2* sml = reinterpret_cast<float2*>(sq + C::kQ);
+    float2* srow = sml + kWarps * C::kRows;
     float* sqf = reinterpret_cast<float*>(srow + C::kRows);
     const uint32_t bars = smem_u32(sqf + C::kRows);
-    __shared__ long long scan[kMmaThreads / 32], found[2];
+    __shared__ long long scan[kWarps + 1], found[2];
     __shared__ int abort_word;
     volatile int* abort_flag = &abort_word;
     auto full = [&](int s) { return bars + 16u * (uint32_t)s; };
@@ -161,91 +206,111 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma_kernel(const __grid_
         abort_word = 0;
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
+            mbar_init(empty(s), kBlocks);  // one arrival a block
+            meta[s].use = -1;
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     const Workspace ws = workspace(p.ws, p.RT, p.D);
-    const Share sh = find_share<kMmaThreads>(p, kMmaMinTiles, scan, found);  // (synchronizes the block)
+    const Share sh = find_share<C::kThreads>(p, C::kBoxes, scan, found);  // (not below 128 slots; synchronizes the block)
     if (threadIdx.x == 0) ws.join[blockIdx.x].parts = 0;
     Walk w = walk_begin(p, sh);
     Unit u;
 
-    if (warp == kMmaWarps) {
+    if (warp == kWarps) {
         // ------------------------------------------------------------ producer
         const int span = min(p.page, C::kSlots);      // slots of one load
         const int nb = C::kSlots / span;               // pages of a tile
-        const int per = 32 / nb;                       // tiles whose pages the lanes look up at once
-        const int nbox = TYPE == 2 ? (p.D + 127) / 128 : (p.D + 63) / 64;
+        // Tiles of one batch: each has nb lanes of its own, which look its pages up, wait for its stage and
+        // start its copies, all tiles of a batch at once (a loop over the tiles would cost the
+        // warp some 600 clocks each, about the memory's time for one).  No more than the ring
+        // has stages, so that the tiles of a batch are uses of different stages.
+        const int per = min(32 / nb, C::kStages);
+        constexpr int nbox = C::kBoxes;                // (a box past D is all zeros and reads nothing)
         const int mysub = lane % nb, mytile = lane / nb;
-        uint32_t idx = 0;                              // stages filled so far
+        const int blocks = span / 16;                  // blocks of 16 slots of one load
+        const uint32_t bytes = (uint32_t)(2 * nbox * span * 128);
+        int slot0 = 0, turn0 = 0;                      // the next stage and how often the ring has gone round
         bool ok = true;
         while (walk_next(p, w, u)) {
             const int j_end = min(u.j1, u.t.nt);
             const int32_t* row = p.table + (long long)u.seq * p.max_pages;
-            // the page of this lane's part of tile jb + mytile: -1 not needed, -2 out of range
-            auto look = [&](int jb, int& key) -> int {
-                const int j = jb + mytile;
-                key = 0;
-                if (j >= j_end) return -1;
-                key = u.t.tile(j) * C::kSlots + mysub * span;
-                const bool need = key <= u.t.p1 && (p.window <= 0 || (long long)u.t.p0 - (key + span - 1) < p.window ||
-                                                    key < p.sinks);
-                if (!need) return -1;
-                const int page = row[key / p.page];
-                return page >= 0 && page < p.num_pages ? page : -2;
-            };
-            int key_n, page_n = look(u.j0, key_n);
+            // The table entry of this lane's part of tile jb + mytile (-1: not needed).  Entries and scales are
+            // loaded a batch ahead and not looked at before they are needed.
+            int key_n = 0, page_n = -1;
+            bool need_n = false;
             float ks_n = 1.f, vs_n = 1.f;
-            auto look_scales = [&]() {
-                if (TYPE == 2 && page_n >= 0) {
+            auto look = [&](int jb) {
+                const int j = mytile < per ? jb + mytile : j_end;
+                key_n = j < j_end ? u.t.tile(j) * C::kSlots + mysub * span : 0;
+                need_n = j < j_end && key_n <= u.t.p1 &&
+                         (p.window <= 0 || (long long)u.t.p0 - (key_n + span - 1) < p.window || key_n < p.sinks);
+                page_n = need_n ? row[key_n / p.page] : -1;
+            };
+            auto check_and_scale = [&]() {
+                if (need_n && (page_n < 0 || page_n >= p.num_pages)) {
+                    atomicCAS(p.status, 0, kStatusDevice);
+                    page_n = -1;
+                }
+                if (kCodes && page_n >= 0) {
                     ks_n = p.k_scale[(long long)page_n * p.Hk + u.h];
                     vs_n = p.v_scale[(long long)page_n * p.Hk + u.h];
                 }
             };
-            look_scales();
+            look(u.j0);
+            check_and_scale();
             for (int jb = u.j0; jb < j_end; jb += per) {
+                // What each lane's tile needs, made ready for all of them at once.
                 const int page = page_n, key = key_n;
-                const float ks = ks_n, vs = vs_n;
-                if (page == -2) atomicCAS(p.status, 0, kStatusDevice);
-                page_n = look(jb + per, key_n);
+                const float4 sc = kCodes ? make_float4(ks_n, log2f(vs_n), 1.f / vs_n, 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
+                uint32_t valid = page >= 0 ? ((1u << blocks) - 1u) << (mysub * blocks) : 0u;
+                int loads = page >= 0 ? 1 : 0;
+                for (int o = 1; o < nb; o <<= 1) {  // over the lanes of the tile
+                    valid |= __shfl_xor_sync(0xffffffffu, valid, o);
+                    loads += __shfl_xor_sync(0xffffffffu, loads, o);
+                }
+                const int in_page = key % p.page;
                 const int todo = min(per, j_end - jb);
-                for (int i = 0; i < todo; ++i) {
-                    if (i == todo / 2) look_scales();
-                    const int slot = idx % C::kStages;
-                    const uint32_t turn = idx / C::kStages;
-                    if (turn > 0 && ok)
-                        ok = __all_sync(0xffffffffu, wait_bar(empty(slot), (turn - 1) & 1u, abort_flag, p.status));
-                    const bool load = ok && mytile == i && page >= 0;
-                    const int blocks = span / 16;
-                    const uint32_t bits = load ? ((1u << blocks) - 1u) << (mysub * blocks) : 0u;
-                    const uint32_t valid = __reduce_or_sync(0xffffffffu, bits);
-                    const int loads = __popc(__ballot_sync(0xffffffffu, load));
-                    if (TYPE == 2 && load) {
-                        for (int b = 0; b < blocks; ++b) {
-                            meta[slot].ks[mysub * blocks + b] = ks;
-                            meta[slot].vlog2[mysub * blocks + b] = log2f(vs);
-                            meta[slot].vinv[mysub * blocks + b] = 1.f / vs;
-                        }
-                    }
-                    if (lane == 0) {
-                        meta[slot].valid = valid;
-                        meta[slot].key0 = u.t.tile(jb + i) * C::kSlots;
+                look(jb + per);  // (in flight while the batch is given out)
+                const int slot = slot0 + mytile < C::kStages ? slot0 + mytile : slot0 + mytile - C::kStages;
+                const int turn = slot0 + mytile < C::kStages ? turn0 : turn0 + 1;
+                bool wait = mytile < todo;
+                // (bounded: after a wait that ran out every tile is given out empty and the CTA runs to its end)
+                for (uint32_t spin = 1; __any_sync(0xffffffffu, wait); ++spin) {
+                    // tiles whose stage has been read (the lanes of a tile go by their first)
+                    bool go = wait && (turn == 0 || !ok || tc::mbar_test(empty(slot), (uint32_t)(turn - 1) & 1u));
+                    go = __shfl_sync(0xffffffffu, go, lane - mysub);
+                    StageMeta& mt = meta[slot];
+                    if (go) {
+                        if (kCodes) mt.sc[mysub] = sc;
+                        if (mysub == 0)
+                            tc::st_shared_v4(smem_u32(&mt.valid), ok ? valid : 0u, (uint32_t)key, (uint32_t)turn, 0u);
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(loads * 2 * nbox * span * 128));
+                    if (go && mysub == 0) mbar_expect_tx(full(slot), ok ? (uint32_t)loads * bytes : 0u);
                     __syncwarp();
-                    if (load) {
+                    if (go && page >= 0 && ok) {
                         const uint32_t dst = ring + (uint32_t)slot * C::kStage + (uint32_t)(mysub * span) * 128u;
                         for (int b = 0; b < nbox; ++b) {
-                            const int x = b * (TYPE == 2 ? 128 : 64);
-                            tc::tma_load_4d(dst + b * C::kBoxBytes, &P.tm_k, x, key % p.page, u.h, page, full(slot));
-                            tc::tma_load_4d(dst + (C::kBoxes + b) * C::kBoxBytes, &P.tm_v, x, key % p.page, u.h, page,
-                                            full(slot));
+                            const int x = b * 64;  // (16-bit units)
+                            tc::tma_load_4d(dst + b * C::kBoxBytes, &P.tm_k, x, in_page, u.h, page, full(slot));
+                            tc::tma_load_4d(dst + (C::kBoxes + b) * C::kBoxBytes, &P.tm_v, x, in_page, u.h, page, full(slot));
                         }
                     }
-                    ++idx;
+                    wait = wait && !go;
+                    if (!__any_sync(0xffffffffu, go) && ok) {  // none: sleep until the first of them has been read
+                        const int first = __ffs(__ballot_sync(0xffffffffu, wait)) - 1;
+                        const uint32_t bar = __shfl_sync(0xffffffffu, empty(slot), first);
+                        const int use = __shfl_sync(0xffffffffu, turn, first);
+                        ok = __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(use - 1) & 1u, abort_flag, p.status));
+                    }
+                    if (spin == 1) check_and_scale();  // (the next batch's scales load while this one waits)
+                }
+                slot0 += todo;
+                if (slot0 >= C::kStages) {
+                    slot0 -= C::kStages;
+                    ++turn0;
                 }
             }
         }
@@ -256,21 +321,30 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma_kernel(const __grid_
     }
 
     // ---------------------------------------------------------------- consumers
+    auto consumers_sync = [] { tc::named_barrier(1, kWarps * 32); };
     const int g = lane / 4, t = lane % 4;
-    const int nch = (p.D + 63) / 64;
+    const int sub_shift = p.page >= C::kSlots ? 3 : __ffs(p.page) - 5;  // log2 of a page's blocks (in a stage)
     const uint32_t rg = (uint32_t)pi8(g);                      // slot (of eight) of this lane's rows of K
-    const uint32_t k_row = rg * 128u;
     const uint32_t r0 = 2u * t, r1 = (r0 ^ 4u) + 1u;           // slots (of eight) of this lane's columns of V^T
-    // 16-bit V: this lane's row address of the transposing load
-    const uint32_t vrow = (uint32_t)pi8(lane & 7) + ((lane & 16) ? 8u : 0u);
+    // Byte offsets in a block of 16 swizzled rows: this lane's row address of K's loads (matrices: slots
+    // 0-7, slots 8-15, the same 16 bytes further; the next 32 bytes at ^ 32), 8-bit V's words of
+    // columns g (rows r0, r1; the upper 64 columns at ^ 64), 16-bit V's rows of the transposing load
+    // (16 columns further at ^ 32).
+    const uint32_t k_row = (uint32_t)pi8(lane & 7) + ((lane & 8) ? 8u : 0u);
+    const uint32_t k_off = k_row * 128u + ((((uint32_t)lane >> 4) ^ (k_row & 7u)) << 4);
+    const uint32_t v_off0 = r0 * 128u + (((uint32_t)(g >> 1) ^ r0) << 4) + (g & 1) * 8u;
+    const uint32_t v_off1 = r1 * 128u + (((uint32_t)(g >> 1) ^ r1) << 4) + (g & 1) * 8u;
+    const uint32_t v_row = (uint32_t)pi8(lane & 7) + ((lane & 16) ? 8u : 0u);
+    const uint32_t v_offt = v_row * 128u + ((((uint32_t)lane >> 3 & 1u) ^ (v_row & 7u)) << 4);
+    constexpr float kNone = -1e30f;  // reference of a row that has seen no key
     uint32_t idx = 0;
     bool ok = true;
     long long at = sh.begin;
     while (walk_next(p, w, u)) {
         const long long head0 = (long long)u.h * p.G;
         const int total_rows = u.q.n * p.G, row_first = u.rt * C::kRows;
-        // ---- Q of the unit, in fragment order: warp w takes rows w, w + kMmaWarps, ...
-        for (int r = warp; r < C::kRows; r += kMmaWarps) {
+        // ---- Q of the unit, in fragment order: warp w takes rows w, w + kWarps, ...
+        for (int r = warp; r < C::kRows; r += kWarps) {
             const int row = row_first + r;
             const bool there = row < total_rows;
             const uint16_t* qp = static_cast<const uint16_t*>(p.q);
@@ -283,34 +357,44 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma_kernel(const __grid_
                 const int d = c * 128 + lane * 4;
                 x[c] = there && d < p.D ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0u, 0u);
             }
-            if (TYPE == 2 && p.dtype == TA_BF16) {
+            if constexpr (kCodes) {
+                const bool bf = p.dtype == TA_BF16;
+                float y[(NDC + 1) / 2][4];
                 uint32_t most = 0;
 #pragma unroll
                 for (int c = 0; c < (NDC + 1) / 2; ++c) {
-                    const uint32_t e[4] = {x[c].x & 0x7fffu, (x[c].x >> 16) & 0x7fffu, x[c].y & 0x7fffu,
-                                           (x[c].y >> 16) & 0x7fffu};
+                    const float2 a = bf ? tc::unpack2<true>(x[c].x) : tc::unpack2<false>(x[c].x);
+                    const float2 b = bf ? tc::unpack2<true>(x[c].y) : tc::unpack2<false>(x[c].y);
+                    y[c][0] = a.x, y[c][1] = a.y, y[c][2] = b.x, y[c][3] = b.y;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (e[i] < 0x7f80u) most = max(most, e[i]);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t e = __float_as_uint(y[c][i]) & 0x7fffffffu;
+                        if (e < 0x7f800000u) most = max(most, e);
+                    }
                 }
-                most = __reduce_max_sync(0xffffffffu, most) >> 7;  // the exponent of the largest finite element
-                const uint32_t ex = most < 2 ? 2u : (most > 252 ? 252u : most);
-                const float down = __uint_as_float((254u - ex) << 23);  // 2^(127 - ex)
+                // the exponent of the largest finite element, and the factor that makes it 0
+                uint32_t ex = __reduce_max_sync(0xffffffffu, most) >> 23;
+                ex = ex < 1 ? 1u : (ex > 253 ? 253u : ex);
+                const float up = __uint_as_float((254u - ex) << 23);
                 factor *= __uint_as_float(ex << 23);
 #pragma unroll
                 for (int c = 0; c < (NDC + 1) / 2; ++c) {
-                    const float2 a = tc::unpack2<true>(x[c].x), b = tc::unpack2<true>(x[c].y);
-                    x[c].x = pack2<false>(a.x * down, a.y * down);
-                    x[c].y = pack2<false>(b.x * down, b.y * down);
+                    x[c].x = pack2<false>(y[c][0] * up, y[c][1] * up);
+                    x[c].y = pack2<false>(y[c][2] * up, y[c][3] * up);
                 }
             }
 #pragma unroll
             for (int c = 0; c < (NDC + 1) / 2; ++c) {
                 const int d = c * 128 + lane * 4, ch = d / 64, in = d % 64;
-                // four consecutive elements are one k-step's share of lane (row, t)
-                const int ks = TYPE == 2 ? (in % 16) / 4 : (in / 32) * 2 + (in % 8) / 4;
-                const int tt = TYPE == 2 ? in / 16 : (in % 32) / 8;
-                if (ch < NDC) sq[((ch * 4 + ks) * NT + r / 8) * 32 + (r % 8) * 4 + tt] = x[c];
+                if (ch >= NDC) continue;
+                uint8_t* dst = sq + ((ch * 4 + in / 16) * NT + r / 8) * 256 + (r % 8) * 32;
+                if constexpr (kCodes) {
+                    *reinterpret_cast<uint2*>(dst + (in % 16) / 4 * 8) = x[c];
+                } else {
+                    dst += (in % 8) / 2 * 8 + (in % 16) / 8 * 4;
+                    *reinterpret_cast<uint32_t*>(dst) = x[c].x;
+                    *reinterpret_cast<uint32_t*>(dst + 8) = x[c].y;
+                }
             }
             if (lane == 0) sqf[r] = factor;
         }
@@ -322,13 +406,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma_kernel(const __grid_
             for (int e = 0; e < 2; ++e)
                 pos[nt][e] = u.q.len - u.q.n + min(row_first + nt * 8 + 2 * t + e, total_rows - 1) / p.G;
         consumers_sync();
-        float qf[NT][2], m[NT][2], l[NT][2], o[NDC * 4][NT][4];
+        float qf[NT][2], m[NT][2], l[NT][2], o[NDC * 4][NT][4];  // m: the reference maximum
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 qf[nt][e] = sqf[nt * 8 + 2 * t + e];
-                m[nt][e] = -INFINITY;
+                m[nt][e] = kNone;
                 l[nt][e] = 0.f;
             }
 #pragma unroll
@@ -337,192 +421,189 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma_kernel(const __grid_
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
+        // Q stays in registers where it is small.
+        constexpr int kSteps = NDC * 4;   // k-steps of 16 columns
+        constexpr bool kKeepQ = kSteps * NT <= 8;
+        uint2 qr[kKeepQ ? kSteps * NT : 1];
+        if constexpr (kKeepQ) {
+#pragma unroll
+            for (int i = 0; i < kSteps * NT; ++i) qr[i] = *reinterpret_cast<const uint2*>(sq + i * 256 + lane * 8);
+        }
 
         const int tiles = max(0, min(u.j1, u.t.nt) - u.j0);
-        // stage idx + i goes to warp (idx + i) % kMmaWarps
-        for (int i = (int)((uint32_t)(warp + kMmaWarps - (idx % kMmaWarps)) % kMmaWarps); i < tiles; i += kMmaWarps) {
-            const uint32_t it = idx + (uint32_t)i;
+        // Blocks that a warp takes at once: half a stage's (twelve such pieces in a ring of six), or
+        // one where that leaves warps without work.
+        constexpr int kTake = kBlocks / 2;
+        const int take = tiles * kBlocks >= 2 * kWarps * kTake ? kTake : 1;
+        const int grains = tiles * kBlocks / take;
+        for (int gr = warp; gr < grains; gr += kWarps) {
+            const int b_first = (gr * take) % kBlocks;
+            const uint32_t it = idx + (uint32_t)(gr * take / kBlocks);
             const int slot = (int)(it % C::kStages);
-            if (ok) ok = __all_sync(0xffffffffu, wait_bar(full(slot), (it / C::kStages) & 1u, abort_flag, p.status));
-            const StageMeta& mt_ = meta[slot];
-            const int key0 = mt_.key0;
-            const uint32_t valid = mt_.valid;
-            const uint32_t kb = ring + (uint32_t)slot * C::kStage, vb = kb + C::kBoxes * C::kBoxBytes;
+            if (ok)
+                ok = __all_sync(0xffffffffu, wait_stage(&meta[slot].use, (int)(it / C::kStages), full(slot), abort_flag,
+                                                        p.status));
+            const StageMeta& mt = meta[slot];
+            const uint32_t valid = mt.valid;
+            const int stage_key0 = mt.key0;
+            // every row sees every slot of the stage
+            const bool plain_stage = valid == (1u << kBlocks) - 1u && stage_key0 + C::kSlots - 1 <= u.t.p0 &&
+                                     (p.window <= 0 || u.t.p1 - stage_key0 < p.window || stage_key0 + C::kSlots <= p.sinks);
+            const uint32_t stage = ring + (uint32_t)slot * C::kStage;
+            // One block: S^T, the softmax step, O^T.  PLAIN: every row sees every slot of it.
+            auto block = [&](auto plain_tag, int blk) {
+                constexpr bool PLAIN = decltype(plain_tag)::value;
+                const uint32_t kb = stage + (uint32_t)blk * 2048u, vb = kb + C::kBoxes * C::kBoxBytes;
+                const int key0 = stage_key0 + blk * 16;
+                if constexpr (!PLAIN) {
+                    // Slots that no row sees may hold anything: their V is made 0 in the stage (their weight is 0,
+                    // but 0 times NaN is not).
+                    if (!unit_sees(p, u.t, key0 + lane / 2)) {
+                        for (int b = 0; b < C::kBoxes; ++b)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                tc::st_shared_v4(vb + b * C::kBoxBytes + (uint32_t)(lane / 2) * 128u + (lane & 1) * 64u + i * 16u,
+                                                 0u, 0u, 0u, 0u);
+                    }
+                    tc::fence_async_shared();  // before the stage is filled again
+                    __syncwarp();
+                }
 
-            // ---- S^T
-            float s[kMT][NT][4];
-#pragma unroll
-            for (int i2 = 0; i2 < kMT; ++i2)
+                // ---- S^T
+                float s[NT][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[i2][nt][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+                auto step = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-            for (int c = 0; c < NDC; ++c) {
-                if (c >= nch) break;
-                uint2 b[4][NT];
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint2 b;
+                        if constexpr (kKeepQ) b = qr[i * NT + nt];
+                        else b = *reinterpret_cast<const uint2*>(sq + (i * NT + nt) * 256 + lane * 8);
+                        mma16816<kBF16>(s[nt], a0, a1, a2, a3, b);
+                    }
+                };
+                // (32 bytes of a row at a time: 16 columns, or 32 codes)
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) b[ks][nt] = sq[((c * 4 + ks) * NT + nt) * 32 + lane];
-#pragma unroll
-                for (int i2 = 0; i2 < kMT; ++i2) {
-                    if constexpr (TYPE == 2) {
-                        const uint32_t a = kb + (c / 2) * C::kBoxBytes + i2 * 2048u + k_row +
-                                           (((uint32_t)t + 4u * (c & 1)) ^ rg) * 16u;
-                        const uint4 x = lds128(a), y = lds128(a + 1024u);
-                        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            const uint32_t a0 = codes_f16(xw[ks]), a2 = codes_f16_hi(xw[ks]);
-                            const uint32_t a1 = codes_f16(yw[ks]), a3 = codes_f16_hi(yw[ks]);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[i2][nt], a0, a1, a2, a3, b[ks][nt]);
-                        }
+                for (int i = 0; i < (kCodes ? kSteps / 2 : kSteps); ++i) {
+                    uint32_t a[4];
+                    ldsm_x4(kb + (k_off ^ (32u * (i & 3))) + (i / 4) * C::kBoxBytes, a);
+                    if constexpr (kCodes) {
+                        step(2 * i, codes_f16(a[0]), codes_f16(a[1]), codes_f16_hi(a[0]), codes_f16_hi(a[1]));
+                        step(2 * i + 1, codes_f16(a[2]), codes_f16(a[3]), codes_f16_hi(a[2]), codes_f16_hi(a[3]));
                     } else {
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const uint32_t a = kb + c * C::kBoxBytes + i2 * 2048u + k_row +
-                                               (((uint32_t)t + 4u * hf) ^ rg) * 16u;
-                            const uint4 x = lds128(a), y = lds128(a + 1024u);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                mma16816<kBF16>(s[i2][nt], x.x, y.x, x.y, y.y, b[2 * hf][nt]);
-                                mma16816<kBF16>(s[i2][nt], x.z, y.z, x.w, y.w, b[2 * hf + 1][nt]);
-                            }
-                        }
+                        step(i, a[0], a[1], a[2], a[3]);
                     }
                 }
-            }
-            // ---- Logits in base 2 (with the value scale's log2), masks, the tile's maxima.
-            const bool plain = valid == (1u << kMT) - 1u && key0 + C::kSlots - 1 <= u.t.p0 &&
-                               (p.window <= 0 || u.t.p1 - key0 < p.window || key0 + C::kSlots <= p.sinks);
-            float mx[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
-#pragma unroll
-            for (int i2 = 0; i2 < kMT; ++i2) {
-                const float ks = TYPE == 2 ? mt_.ks[i2] : 1.f, vl = TYPE == 2 ? mt_.vlog2[i2] : 0.f;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = s[i2][nt][e];
-                        if constexpr (TYPE == 2) x = fmaf(x, qf[nt][e & 1] * ks, vl);
-                        else x *= qf[nt][e & 1];
-                        if (!plain) {
-                            const int key = key0 + i2 * 16 + (int)rg + (e & 2) * 4;
-                            if (!((valid >> i2) & 1u) || !sees(p, pos[nt][e & 1], key)) x = -INFINITY;
-                        }
-                        s[i2][nt][e] = x;
-                        mx[nt][e & 1] = fmaxf(mx[nt][e & 1], x);
-                    }
-            }
-            bool grew = false;
-            float mn[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x = mx[nt][e];
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    mn[nt][e] = fmaxf(m[nt][e], x);
-                    grew = grew || mn[nt][e] > m[nt][e];
-                }
-            if (__any_sync(0xffffffffu, grew)) {
+                // ---- Logits in base 2 (with the value scale's log2) less the reference: y = x - m.
+                const float4 sc = kCodes ? mt.sc[blk >> sub_shift] : make_float4(1.f, 0.f, 1.f, 0.f);
+                float y[NT][4], f[NT][2];
+                bool grew = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float al[2];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        al[e] = mn[nt][e] == -INFINITY ? 1.f : ex2(m[nt][e] - mn[nt][e]);
-                        m[nt][e] = mn[nt][e];
-                        l[nt][e] *= al[e];
-                    }
+                    for (int e = 0; e < 2; ++e) f[nt][e] = kCodes ? qf[nt][e] * sc.x : qf[nt][e];
 #pragma unroll
-                    for (int i2 = 0; i2 < NDC * 4; ++i2)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[i2][nt][e] *= al[e & 1];
+                    for (int e = 0; e < 4; ++e) y[nt][e] = fmaf(s[nt][e], f[nt][e & 1], sc.y - m[nt][e & 1]);
                 }
-            }
-            // ---- P^T as the B operand, and O^T += V^T P^T, 16 slots at a time.
+                if constexpr (!PLAIN) {
 #pragma unroll
-            for (int i2 = 0; i2 < kMT; ++i2) {
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!sees(p, pos[nt][e & 1], key0 + (int)rg + (e & 2) * 4)) y[nt][e] = -INFINITY;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) grew = grew || fmaxf(y[nt][e], y[nt][e + 2]) > 8.f;
+                if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float al[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            // (the reference may be far off: x is formed from s again)
+                            const float x0 = y[nt][e] == -INFINITY ? -INFINITY : fmaf(s[nt][e], f[nt][e], sc.y);
+                            const float x1 = y[nt][e + 2] == -INFINITY ? -INFINITY : fmaf(s[nt][e + 2], f[nt][e], sc.y);
+                            float x = fmaxf(x0, x1);
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                            x = fmaxf(m[nt][e], x);
+                            al[e] = ex2(m[nt][e] - x);
+                            m[nt][e] = x;
+                            l[nt][e] *= al[e];
+                            y[nt][e] = x0 - x;
+                            y[nt][e + 2] = x1 - x;
+                        }
+#pragma unroll
+                        for (int i = 0; i < NDC * 4; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[i][nt][e] *= al[e & 1];
+                    }
+                }
+                // ---- P^T as the B operand, and O^T += V^T P^T.
                 uint2 b[NT];
-                // (the scales of slots that were not loaded are whatever an earlier stage left)
-                const float vi = TYPE != 2 ? 1.f : ((valid >> i2) & 1u) ? mt_.vinv[i2] : 0.f;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float pr[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-                        pr[e] = ex2(s[i2][nt][e] - ref);
-                        l[nt][e & 1] = fmaf(pr[e], vi, l[nt][e & 1]);
+                        pr[e] = ex2(y[nt][e]);
+                        if constexpr (kCodes) l[nt][e & 1] = fmaf(pr[e], sc.z, l[nt][e & 1]);
+                        else l[nt][e & 1] += pr[e];
                     }
                     b[nt].x = transpose8(pack2<kBF16>(pr[0], pr[1]));
                     b[nt].y = transpose8(pack2<kBF16>(pr[2], pr[3]));
                 }
-                // Slots that no row sees may hold anything: their V is taken as 0.
-                uint32_t k01 = 0xffffffffu, k23 = 0xffffffffu;  // halves: slots r0, r1; r0 + 8, r1 + 8
-                if (!plain) {
-                    const int k = key0 + i2 * 16;
-                    const bool in = (valid >> i2) & 1u;
-                    k01 = (in && unit_sees(p, u.t, k + (int)r0) ? 0xffffu : 0u) |
-                          (in && unit_sees(p, u.t, k + (int)r1) ? 0xffff0000u : 0u);
-                    k23 = (in && unit_sees(p, u.t, k + (int)r0 + 8) ? 0xffffu : 0u) |
-                          (in && unit_sees(p, u.t, k + (int)r1 + 8) ? 0xffff0000u : 0u);
-                }
 #pragma unroll
                 for (int c = 0; c < NDC; ++c) {
-                    if (c >= nch) break;
-                    if constexpr (TYPE == 2) {
-                        const uint32_t vbox = vb + (c / 2) * C::kBoxBytes + i2 * 2048u + (g & 1) * 8u;
-                        const uint32_t col = (uint32_t)(c & 1) * 4u + (uint32_t)(g >> 1);
-                        const uint32_t a0 = vbox + r0 * 128u + (col ^ r0) * 16u, a1 = vbox + r1 * 128u + (col ^ r1) * 16u;
+                    if constexpr (kCodes) {
+                        const uint32_t a0 = vb + (v_off0 ^ (64u * (c & 1))) + (c / 2) * C::kBoxBytes;
+                        const uint32_t a1 = vb + (v_off1 ^ (64u * (c & 1))) + (c / 2) * C::kBoxBytes;
                         const uint2 w0 = lds64(a0), w1 = lds64(a1), w2 = lds64(a0 + 1024u), w3 = lds64(a1 + 1024u);
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             const uint32_t sel = (h & 1) ? 0x7362u : 0x5140u;
                             const uint32_t x = __byte_perm(h < 2 ? w0.x : w0.y, h < 2 ? w1.x : w1.y, sel);
-                            const uint32_t y = __byte_perm(h < 2 ? w2.x : w2.y, h < 2 ? w3.x : w3.y, sel);
-                            uint32_t f0 = codes_f16(x), f1 = codes_f16_hi(x), f2 = codes_f16(y), f3 = codes_f16_hi(y);
-                            if (!plain) {
-                                f0 &= k01;
-                                f1 &= k01;
-                                f2 &= k23;
-                                f3 &= k23;
-                            }
+                            const uint32_t z = __byte_perm(h < 2 ? w2.x : w2.y, h < 2 ? w3.x : w3.y, sel);
+                            const uint32_t f0 = codes_f16(x), f1 = codes_f16_hi(x), f2 = codes_f16(z), f3 = codes_f16_hi(z);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[c * 4 + h][nt], f0, f1, f2, f3, b[nt]);
                         }
                     } else {
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
-                            uint32_t f[4];
-                            const uint32_t col = 2u * h + ((lane >> 3) & 1);
-                            ldsm_x4_t(vb + c * C::kBoxBytes + i2 * 2048u + vrow * 128u + ((col ^ (vrow & 7u)) * 16u), f);
-                            if (!plain) {
-                                f[0] &= k01;
-                                f[1] &= k01;
-                                f[2] &= k23;
-                                f[3] &= k23;
-                            }
+                            uint32_t a[4];
+                            ldsm_x4_t(vb + (v_offt ^ (32u * h)) + c * C::kBoxBytes, a);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma16816<kBF16>(o[c * 4 + h][nt], f[0], f[1], f[2], f[3], b[nt]);
+                                mma16816<kBF16>(o[c * 4 + h][nt], a[0], a[1], a[2], a[3], b[nt]);
                         }
                     }
                 }
+            };
+            if (plain_stage) {
+#pragma unroll 1
+                for (int blk = b_first; blk < b_first + take; ++blk) block(Yes{}, blk);
+            } else {
+#pragma unroll 1
+                for (int blk = b_first; blk < b_first + take; ++blk) {
+                    const int key0 = stage_key0 + blk * 16;
+                    // (a block that was not loaded, or that no row sees, is passed over)
+                    if (((valid >> blk) & 1u) && key0 <= u.t.p1 &&
+                        (p.window <= 0 || (long long)u.t.p0 - (key0 + 15) < p.window || key0 < p.sinks))
+                        block(No{}, blk);
+                }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty(slot));
+            if (lane == 0) mbar_arrive_n(empty(slot), (uint32_t)take);
         }
         idx += (uint32_t)tiles;
 
-        // ---- Merge: (m, l) of the warps, then their O over four buffers (warps 4.. first, warps 0..3 on top).
+        // ---- Merge: (m, l) of the warps, then their O over the buffers (the last warps first, the others on top).
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -531,7 +612,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma_kernel(const __grid_
                 x += __shfl_xor_sync(0xffffffffu, x, 4);
                 x += __shfl_xor_sync(0xffffffffu, x, 8);
                 x += __shfl_xor_sync(0xffffffffu, x, 16);
-                if (g == 0) sml[warp * C::kRows + nt * 8 + 2 * t + e] = make_float2(m[nt][e], x);
+                if (g == 0)
+                    sml[warp * C::kRows + nt * 8 + 2 * t + e] = make_float2(m[nt][e] == kNone ? -INFINITY : m[nt][e], x);
             }
         consumers_sync();
         float f[NT][2];
@@ -542,7 +624,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma_kernel(const __grid_
                 const int r = nt * 8 + 2 * t + e;
                 float M = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < kMmaWarps; ++i) M = fmaxf(M, sml[i * C::kRows + r].x);
+                for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sml[i * C::kRows + r].x);
                 const float2 mine = sml[warp * C::kRows + r];
                 f[nt][e] = no_key(mine.x, mine.y) ? 0.f : ex2(mine.x - M);
             }
@@ -550,9 +632,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma_kernel(const __grid_
             const int r = threadIdx.x;
             float M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int i = 0; i < kMmaWarps; ++i) M = fmaxf(M, sml[i * C::kRows + r].x);
+            for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sml[i * C::kRows + r].x);
 #pragma unroll
-            for (int i = 0; i < kMmaWarps; ++i) {
+            for (int i = 0; i < kWarps; ++i) {
                 const float2 ml = sml[i * C::kRows + r];
                 if (!no_key(ml.x, ml.y)) L = fmaf(ml.y, ex2(ml.x - M), L);
             }
@@ -561,12 +643,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma_kernel(const __grid_
         // element (d, row) of accumulator i2, nt: 8-bit d = 64 c + 8 g + 2 h (+ 1), 16-bit d = 64 c + 16 h + g (+ 8)
         auto place = [&](int i2, int e) {
             const int c = i2 / 4, h = i2 % 4;
-            return TYPE == 2 ? c * 64 + g * 8 + 2 * h + (e >> 1) : c * 64 + 16 * h + g + 8 * (e >> 1);
+            return kCodes ? c * 64 + g * 8 + 2 * h + (e >> 1) : c * 64 + 16 * h + g + 8 * (e >> 1);
         };
 #pragma unroll 1
-        for (int half = 1; half >= 0; --half) {
-            if (warp / 4 == half) {
-                float* dst = so + (warp % 4) * C::kRows * C::kOStride;
+        for (int turn = (kWarps - 1) / C::kBufs; turn >= 0; --turn) {
+            if (warp / C::kBufs == turn) {
+                float* dst = so + (warp % C::kBufs) * C::kRows * C::kOStride;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -575,7 +657,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma_kernel(const __grid_
                         for (int e = 0; e < 4; ++e) {
                             float* q = dst + (nt * 8 + 2 * t + (e & 1)) * C::kOStride + place(i2, e);
                             const float v = o[i2][nt][e] * f[nt][e & 1];
-                            *q = half || warp + 4 >= kMmaWarps ? v : *q + v;
+                            *q = warp + C::kBufs >= kWarps ? v : *q + v;
                         }
             }
             consumers_sync();
@@ -583,11 +665,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1) paged_mma_kernel(const __grid_
         const bool whole = u.starts && u.ends;
         const int slot = u.starts ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
         const int D4 = p.D / 4;
-        for (int e = threadIdx.x; e < u.rows * D4; e += kMmaWarps * 32) {
+        for (int e = threadIdx.x; e < u.rows * D4; e += kWarps * 32) {
             const int r = e / D4, d = (e - r * D4) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < C::kBufs; ++i) {
                 const float4 y = *reinterpret_cast<const float4*>(so + (i * C::kRows + r) * C::kOStride + d);
                 x.x += y.x;
                 x.y += y.y;
@@ -628,7 +710,7 @@ cudaError_t launch_mma_variant(const MmaParams& P, cudaStream_t stream) {
     auto kern = paged_mma_kernel<TYPE, NDC, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<kGrid, kMmaThreads, C::kSmem, stream>>>(P);
+    kern<<<kGrid, C::kThreads, C::kSmem, stream>>>(P);
     return cudaGetLastError();
 }
 

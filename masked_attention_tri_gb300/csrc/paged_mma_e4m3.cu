@@ -1,4 +1,4 @@
-// paged_mma_e4m3.cu -- instantiates the paged attention kernel's 8 bit-cache variants.
+// paged_mma_e4m3.cu -- instantiates the paged attention kernel's 8-bit cache variants.
 #include "paged_mma.cuh"
 
 namespace triattn {

@@ -294,6 +294,12 @@ int paged_rows(int dtype, int max_q, int G, int D) {
     if (dtype == TA_F32 || rows <= 8) return 8;
     return rows <= 16 || D > 128 ? 16 : 32;
 }
+// Slots of a tile: on tensor cores 32 KB of K and V with columns padded to whole 128 bytes.
+int paged_tile(int dtype, int cache_dtype, int D) {
+    if (dtype == TA_F32) return 64;
+    if (cache_dtype == TA_E4M3) return D <= 128 ? 128 : 64;
+    return D <= 64 ? 128 : (D <= 128 ? 64 : 32);
+}
 size_t paged_workspace_bytes(int RT, int D) { return paged::workspace_bytes(RT, D); }
 
 cudaError_t launch_paged(const PagedParams& p, cudaStream_t stream) {

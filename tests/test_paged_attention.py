@@ -5,8 +5,9 @@ sum behind a logit): a logit is off by at most dx = D 2^-23 E (an fp32 sum of D 
 + 2^-22 |x| (its base-2 form and the exponent's argument); a weight by 2 dx and the exponential's 2^-21; the
 weights are rounded to the products' 16-bit type (the cache's; f16 for codes: eps / 2) and summed in
 fp32 (len 2^-23).  So |O - O64| <= eps_out / 2 |O| + (eps_p / 2 + 2 dx + 2^-21 + len 2^-23) A, and
-|lse - lse64| <= dx + 2^-21 + len 2^-24 + 2^-23 |lse|.  Bare fp16 copies of bf16 queries (8-bit cache) are
-scaled by a power of two to their row's largest magnitude: off by 2^-25 of it at most (D 2^-25 in E's terms).
+|lse - lse64| <= dx + 2^-21 + len 2^-24 + 2^-23 |lse|.  16-bit queries of an 8-bit cache are taken as sums of e4m3 terms
+(16 apart, the row's largest magnitude scaled to [2^7, 2^8)): two for bf16, off by half of e4m3's least step
+2^-9 in the second, 2^-10 2^-4 = 2^-21 2^7, so 2^-21 of that magnitude at most (three for fp16: less); dx grows by scale 2^-21 max|q| max_k sum |k_d|.
 fp16 has a least step of 2^-24: an fp16 output is off by 2^-25 there, and an fp16 weight, which is relative to
 the row's largest weight times value scale W, by 2^-25 W: 2^-25 W sum |code| over the slots it sees.
 """
@@ -167,7 +168,7 @@ class Problem:
                 o, aa = w @ v, w @ v.abs()
                 dx = self.D * 2.0 ** -23 * E + 2.0 ** -22 * big
                 if self.cdtype == F8:
-                    dx = dx + self.D * 2.0 ** -25 * E
+                    dx = dx + 2.0 ** -21 * scale * q.abs().amax(-1) * k.abs().sum(-1).amax(-1, keepdim=True)
                 tol = eps_o / 2 * o.abs() + (eps_p / 2 + 2 * dx + 2.0 ** -21 + h * 2.0 ** -23)[..., None] * aa
                 if self.dtype == torch.float16:
                     tol = tol + 2.0 ** -25
