@@ -385,6 +385,14 @@ ta_status tri_attn_varlen_bwd(const void* q, const void* k, const void* v, ta_dt
                               const void* d_out, void* dq, void* dk, void* dv, void* dbias, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/* Bytes of workspace with which tri_attn_varlen_bwd shares the first key blocks of a SINK_WINDOW
+ * mask (without block lists) out over several CTAs, which long sequences need to be fast (every
+ * query sees those keys): at least tri_attn_varlen_bwd_workspace_size, which is enough
+ * for the call.  sinks: their number, or -1 where it is given for each sequence.  dK and dV of those
+ * keys are then summed with atomic reductions too. */
+size_t tri_attn_varlen_bwd_sink_workspace_size(int num_seqs, int total_q, int H, int D, int max_seqlen_q,
+                                               int max_seqlen_k, int with_bias, int window, int sinks);
+
 /* Bytes of workspace tri_attn_varlen_bwd needs (0 for a negative size). */
 size_t tri_attn_varlen_bwd_workspace_size(int total_q, int H, int D, int max_seqlen_q, int max_seqlen_k,
                                           int with_bias);

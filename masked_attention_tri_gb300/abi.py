@@ -8,6 +8,7 @@ NotImplementedError, anything else as RuntimeError.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -21,7 +22,7 @@ TA_MASK_NONE, TA_MASK_CAUSAL, TA_MASK_SLIDING_WINDOW, TA_MASK_PREFIX_LM, TA_MASK
 # Every symbol include/triattn.h declares.
 EXPORTS = ("tri_attn_fwd", "tri_attn_fwd_strided", "tri_attn_varlen_fwd", "tri_attn_varlen_fwd_strided", "tri_attn_varlen_fwd_masked",
            "tri_attn_bwd", "tri_attn_bwd_workspace_size", "tri_attn_bwd_noalloc", "tri_attn_varlen_bwd",
-           "tri_attn_varlen_bwd_workspace_size",
+           "tri_attn_varlen_bwd_workspace_size", "tri_attn_varlen_bwd_sink_workspace_size",
            "tri_attn_rotary", "tri_attn_kv_append", "tri_attn_paged_fwd", "tri_attn_paged_workspace_size",
            "tri_attn_mask_to_kv_lengths", "tri_attn_get_status", "tri_attn_error_string", "tri_attn_version")
 
@@ -38,6 +39,8 @@ class TriAttnError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load the built library; raise loudly if it is missing (there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -70,6 +73,8 @@ def load() -> ctypes.CDLL:
         lib.tri_attn_varlen_bwd.restype = I
         lib.tri_attn_varlen_bwd_workspace_size.argtypes = [I, I, I, I, I, I]
         lib.tri_attn_varlen_bwd_workspace_size.restype = Z
+        lib.tri_attn_varlen_bwd_sink_workspace_size.argtypes = [I] * 9
+        lib.tri_attn_varlen_bwd_sink_workspace_size.restype = Z
         lib.tri_attn_bwd_workspace_size.argtypes = [I, I, I, I, I, I]
         lib.tri_attn_bwd_workspace_size.restype = Z
         lib.tri_attn_rotary.argtypes = [P, P, I, P, P, I, I, F, I, I, I, I, I, L, L, L, L, P, P, P]
@@ -159,6 +164,13 @@ def tri_attn_varlen_bwd_workspace_size(total_q, H, D, max_seqlen_q, max_seqlen_k
                                                          1 if with_bias else 0))
 
 
+def tri_attn_varlen_bwd_sink_workspace_size(num_seqs, total_q, H, D, max_seqlen_q, max_seqlen_k, with_bias, window,
+                                            sinks) -> int:
+    """sinks: -1 where each sequence has its own number."""
+    return int(load().tri_attn_varlen_bwd_sink_workspace_size(num_seqs, total_q, H, D, max_seqlen_q, max_seqlen_k,
+                                                              1 if with_bias else 0, window, sinks))
+
+
 def tri_attn_bwd_workspace_size(B, N, H, Q, K, D) -> int:
     return int(load().tri_attn_bwd_workspace_size(B, N, H, Q, K, D))
 
@@ -244,6 +256,7 @@ def tri_attn_kv_append(q, k, v, dtype, cu_seqlens, kv_lengths, page_table, num_s
     _check(st, "tri_attn_kv_append")
 
 
+@functools.lru_cache(maxsize=256)
 def tri_attn_paged_workspace_size(dtype, max_seqlen_q, Hq, Hk, D) -> int:
     return int(load().tri_attn_paged_workspace_size(dtype, max_seqlen_q, Hq, Hk, D))
 

@@ -44,8 +44,33 @@ def _check_out(out, shape, dtype) -> None:
         raise ValueError(f"out must be {tuple(shape)} of {dtype}, got {tuple(out.shape)} of {out.dtype}")
 
 
+# (current_stream builds a Stream object, some microseconds; torch's own compiled code asks for the handle)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    if _raw_stream is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
+
+
+class _Here:
+    """Stands in for torch.cuda.device(dev) where dev is the current device already (entering that costs
+    some microseconds of each call, more than the launch)."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on(device: torch.device):
+    """A context in which `device` is current."""
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def triangle_attention(q, k, v, bias, mask=None, scale=None, return_aux=False, *, kv_lengths=None, out=None,
@@ -128,7 +153,7 @@ def triangle_attention(q, k, v, bias, mask=None, scale=None, return_aux=False, *
             mx = torch.empty(B, N, H, Q, 1, device=dev, dtype=torch.float32)
     else:
         lse = mx = None
-    with torch.cuda.device(dev):
+    with _on(dev):
         if strides == [None, None, None]:
             abi.tri_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _DT[q.dtype], _ptr(bias), _DT[bias.dtype], _ptr(m8),
                              _ptr(kl), B, N, H, Q, K, D, s, _ptr(out), _ptr(lse), _ptr(mx), _stream(dev))
@@ -199,7 +224,7 @@ def triangle_attention_backward(q, k, v, bias, lse, d_out, mask=None, scale=None
     dbias = torch.empty_like(bias) if need_dbias else None
     nbytes = abi.tri_attn_bwd_workspace_size(B, N, H, Q, K, D)
     ws = torch.empty(nbytes // 4, dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         abi.tri_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _DT[q.dtype], _ptr(bias), _DT[bias.dtype], _ptr(m8), _ptr(kl),
                          B, N, H, Q, K, D, s, _ptr(lse), _ptr(out), _ptr(d_out), _ptr(dq), _ptr(dk), _ptr(dv),
                          _ptr(dbias),
@@ -262,7 +287,7 @@ def mask_to_kv_lengths(mask: torch.Tensor, return_nonprefix: bool = False):
     _need(mask, "mask", dev)
     kl = torch.empty(B, N, 1, 1, 1, device=dev, dtype=torch.int32)
     cnt = torch.zeros(1, device=dev, dtype=torch.int32) if return_nonprefix else None
-    with torch.cuda.device(dev):
+    with _on(dev):
         abi.tri_attn_mask_to_kv_lengths(_ptr(mask.view(torch.uint8)), B, N, K, _ptr(kl), _ptr(cnt), _stream(dev))
     return (kl, cnt) if return_nonprefix else kl
 
@@ -368,6 +393,8 @@ def _row_stride(t: torch.Tensor, name: str, device: torch.device) -> int:
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     rows, H, D = t.shape
+    if t.is_contiguous():
+        return H * D
     if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
         raise ValueError(f"{name} must have contiguous heads and elements (strides (*, D, 1))")
     if rows <= 1:
@@ -484,7 +511,7 @@ def varlen_attention(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seql
         if bias.dtype not in (torch.float32, q.dtype):
             raise TypeError("bias must be float32 or q's dtype")
     pl, p_all = _prefix_args(prefix_lengths, S, dev, mm, sinks)
-    with torch.cuda.device(dev):
+    with _on(dev):
         abi.tri_attn_varlen_fwd_masked(_ptr(q), _ptr(k), _ptr(v), _DT[q.dtype], _ptr(cu_seqlens_q),
                                        _ptr(cu_seqlens_k), S, total_q, k.shape[0], int(max_seqlen_q),
                                        int(max_seqlen_k), H, D, s, _ptr(kn), _ptr(ki), _ptr(fn), _ptr(fi),
@@ -561,10 +588,14 @@ def varlen_attention_backward(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
             raise TypeError("bias must be float32 or q's dtype")
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     dbias = torch.empty_like(bias) if (bias is not None and need_dbias) else None
-    nbytes = abi.tri_attn_varlen_bwd_workspace_size(total_q, H, D, int(max_seqlen_q), int(max_seqlen_k),
-                                                    dbias is not None)
+    if mm == abi.TA_MASK_SINK_WINDOW and kn is None:
+        nbytes = abi.tri_attn_varlen_bwd_sink_workspace_size(S, total_q, H, D, int(max_seqlen_q), int(max_seqlen_k),
+                                                             dbias is not None, int(window), -1 if pl is not None else p_all)
+    else:
+        nbytes = abi.tri_attn_varlen_bwd_workspace_size(total_q, H, D, int(max_seqlen_q), int(max_seqlen_k),
+                                                        dbias is not None)
     ws = torch.empty(max(nbytes // 4, 1), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         abi.tri_attn_varlen_bwd(_ptr(q), _ptr(k), _ptr(v), _DT[q.dtype], _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), S,
                                 total_q, k.shape[0], int(max_seqlen_q), int(max_seqlen_k), H, D, s, _ptr(kn),
                                 _ptr(ki), _ptr(fn), _ptr(fi), mask_heads, MQ, MK, bq, bk, mm, int(window),

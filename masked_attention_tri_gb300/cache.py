@@ -12,7 +12,7 @@ from typing import Optional
 import torch
 
 from . import abi
-from .api import _DT, _check_out, _need, _ptr, _row_stride, _stream
+from .api import _DT, _check_out, _need, _on, _ptr, _row_stride, _stream
 from .positions import Rotary, _check_rotary
 
 _CACHE_DT = {**_DT, torch.float8_e4m3fn: abi.TA_E4M3}
@@ -135,10 +135,11 @@ def kv_cache_append(cache: PagedKVCache, k, v, page_table, kv_lengths, cu_seqlen
             raise ValueError("q is given only to be turned: pass rotary")
         q_rs, Hq = _rows(q, "q", dev, k.dtype, total, D), q.shape[1]
         if out_q is None:
-            out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        elif out_q.shape != q.shape:
-            raise ValueError("out_q must have q's shape")
-        qo_rs = _rows(out_q, "out_q", dev, k.dtype, total, D)
+            out_q, qo_rs = torch.empty(q.shape, dtype=q.dtype, device=dev), Hq * D
+        else:
+            qo_rs = _rows(out_q, "out_q", dev, k.dtype, total, D)
+            if out_q.shape != q.shape:
+                raise ValueError("out_q must have q's shape")
     elif out_q is not None:
         raise ValueError("out_q needs q")
     if positions is not None:
@@ -153,7 +154,7 @@ def kv_cache_append(cache: PagedKVCache, k, v, page_table, kv_lengths, cu_seqlen
         turns, dim, inter, ms = _ptr(rotary.turns), rotary.dim, rotary.interleaved, rotary.attention_factor
     if total == 0 or S == 0:
         return out_q
-    with torch.cuda.device(dev):
+    with _on(dev):
         abi.tri_attn_kv_append(_ptr(q), _ptr(k), _ptr(v), _DT[k.dtype], _ptr(cu_seqlens), _ptr(kv_lengths),
                                _ptr(page_table), S, total, max_seqlen, Hq, Hk, D, q_rs, k_rs, v_rs, qo_rs,
                                _ptr(positions), turns, dim, inter, ms, _ptr(cache.k), _ptr(cache.v), cache._code,
@@ -214,7 +215,7 @@ def paged_attention(q, cache: PagedKVCache, page_table, kv_lengths, cu_seqlens_q
         code = _DT[q.dtype]
         nbytes = abi.tri_attn_paged_workspace_size(code, max_seqlen_q, Hq, Hk, D)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        with torch.cuda.device(dev):
+        with _on(dev):
             abi.tri_attn_paged_fwd(_ptr(q), code, _ptr(cu_seqlens_q), _ptr(kv_lengths), _ptr(page_table), S, total,
                                    max_seqlen_q, Hq, Hk, D, q_rs, s, 0 if window is None else int(window), int(sinks),
                                    _ptr(cache.k), _ptr(cache.v), cache._code, _ptr(cache.k_scale), _ptr(cache.v_scale),

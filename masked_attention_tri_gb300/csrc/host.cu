@@ -375,6 +375,28 @@ TA_EXPORT size_t tri_attn_varlen_bwd_workspace_size(int total_q, int H, int D, i
     return triattn::bwd_workspace_floats_n(rows * D, nb, rows) * sizeof(float);
 }
 
+TA_EXPORT size_t tri_attn_varlen_bwd_sink_workspace_size(int num_seqs, int total_q, int H, int D, int max_seqlen_q,
+                                                        int max_seqlen_k, int with_bias, int window, int sinks) {
+    const size_t plain = tri_attn_varlen_bwd_workspace_size(total_q, H, D, max_seqlen_q, max_seqlen_k, with_bias);
+    if (num_seqs <= 0 || window <= 0 || total_q < 0 || H <= 0 || D <= 0 || max_seqlen_q < 0 || max_seqlen_k < 0)
+        return plain;
+    triattn::BwdParams p{};
+    static const int32_t given = 0;  // (stands for lengths on the device, which are not read here)
+    p.varlen = 1;
+    p.mask_mod = TA_MASK_SINK_WINDOW;
+    p.num_seqs = num_seqs;
+    p.total_q = total_q;
+    p.H = H;
+    p.D = D;
+    p.max_q = max_seqlen_q;
+    p.max_k = max_seqlen_k;
+    p.window = window;
+    p.prefix_len = sinks < 0 ? &given : nullptr;
+    p.prefix_all = sinks;
+    triattn::bwd_sink_share(p);
+    return plain + (size_t)p.sink.elems * sizeof(float);
+}
+
 TA_EXPORT ta_status tri_attn_varlen_bwd(const void* q, const void* k, const void* v, ta_dtype dtype,
                                         const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int num_seqs,
                                         int total_q, int total_k, int max_seqlen_q, int max_seqlen_k, int H, int D,
@@ -471,6 +493,16 @@ TA_EXPORT ta_status tri_attn_varlen_bwd(const void* q, const void* k, const void
     p.status = triattn::status_word();
     if (!p.status) return TA_ERR_CUDA;
     p.tc_main = triattn::tc_bwd_supported(p) ? 1 : 0;  // 16-bit, D <= 128: tensor cores
+    if (p.tc_main) {  // share the first key blocks of a sink window, given the room for it
+        const size_t plain = tri_attn_varlen_bwd_workspace_size(total_q, H, D, max_seqlen_q, max_seqlen_k, dbias != nullptr);
+        triattn::bwd_sink_share(p);
+        if (workspace_bytes >= plain + (size_t)p.sink.elems * sizeof(float)) {
+            p.sink.acc = ws + plain / sizeof(float);
+        } else {
+            p.sink.nb = 0;
+            p.sink.elems = 0;
+        }
+    }
     const cudaError_t e = triattn::launch_simt_bwd(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? TA_OK : TA_ERR_CUDA;
 }

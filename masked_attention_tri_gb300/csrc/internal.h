@@ -116,7 +116,16 @@ struct BwdParams {
     const int32_t* prefix_len;
     int prefix_all;
     int* status;
+    // Sink window without lists on tensor cores: the first nb key blocks of every sequence are shared by
+    // several CTAs, which sum dK and dV in acc: (num_seqs, H, nb, {dK, dV}, 128, D) fp32.
+    struct {
+        float* acc;
+        int nb, chunk, chunks;  // key blocks; q blocks of a far CTA; far CTAs of a key block (0 nb: off)
+        long long elems;        // of acc
+    } sink;
 };
+// The sharing of a problem (sink.acc left NULL): nb = 0 where it is not worth it.
+void bwd_sink_share(BwdParams& p);
 // Workspace of the backward in floats: dQ, dBias and the per-row sums, each rounded up
 // to a multiple of 64 floats.
 size_t bwd_workspace_floats(int B, int N, int H, int Q, int K, int D);

@@ -35,6 +35,8 @@
 // when a logit passes the reference by 2^8 (base 2: by 8), which fp16's range allows.
 #pragma once
 
+#include <atomic>
+
 #include "paged.cuh"
 #include "tc_kernel.cuh"
 
@@ -201,6 +203,7 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
     auto full = [&](int s) { return bars + 16u * (uint32_t)s; };
     auto empty = [&](int s) { return bars + 16u * (uint32_t)s + 8u; };
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up meanwhile
 
     if (threadIdx.x == 0) {
         abort_word = 0;
@@ -708,8 +711,17 @@ template <int TYPE, int NDC, int NT>
 cudaError_t launch_mma_variant(const MmaParams& P, cudaStream_t stream) {
     using C = MmaConfig<TYPE, NDC, NT>;
     auto kern = paged_mma_kernel<TYPE, NDC, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    // The shared-memory limit is set once per device (an attribute call costs as much as a launch).
+    static std::atomic<unsigned long long> set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev > 63 || !(set.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_release);
+    }
     kern<<<kGrid, C::kThreads, C::kSmem, stream>>>(P);
     return cudaGetLastError();
 }

@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
     __shared__ long long scan[kWarps], found[2];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int D = p.D;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up meanwhile
     float* so = smem;
     float2* sml = reinterpret_cast<float2*>(smem + kWarps * kRows * D);
     const Workspace ws = workspace(p.ws, p.RT, D);
@@ -230,6 +231,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
 
 // Share c's split unit, if one starts there: its parts in the order of the shares.
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
+    // Launched while the first kernel runs (programmatic dependent launch): wait for its end.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const Workspace ws = workspace(p.ws, p.RT, p.D);
     const Join jn = ws.join[blockIdx.x];
     if (jn.parts <= 1) return;
@@ -281,8 +284,16 @@ cudaError_t launch_simt(const PagedParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_join(const PagedParams& p, cudaStream_t stream) {
-    paged_join_kernel<<<kGrid, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kGrid);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel, p);
 }
 
 }  // namespace paged

@@ -227,6 +227,9 @@ __global__ void __launch_bounds__(256) bwd_delta_out_kernel(const BwdParams p) {
              e += (long long)gridDim.x * blockDim.x)
             p.dbias_acc[e] = 0.f;
     }
+    for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < p.sink.elems;
+         e += (long long)gridDim.x * blockDim.x)
+        p.sink.acc[e] = 0.f;
     float acc = 0.f;
     if (row < rows) {
         const T* o = static_cast<const T*>(p.out) + row * p.D;
@@ -453,6 +456,26 @@ __global__ void bwd_finish_kernel(const BwdParams p) {
     const long long tid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     convert_range<T>(p.dq_acc, p.dq, p.dq_elems, tid, stride);
     if (p.dbias) convert_range<BT>(p.dbias_acc, p.dbias, p.dbias_elems, tid, stride);
+    // Shared first key blocks (sink window): dK and dV of their rows, two elements at a time.
+    const long long half = p.sink.elems / 4;  // pairs of dK elements
+    for (long long i = tid; i < half; i += stride) {
+        const int d2 = p.D / 2;
+        const int d = (int)(i % d2) * 2, row = (int)(i / d2 % 128);
+        const long long unit = i / d2 / 128;  // (sequence, head, key block)
+        const int kb = (int)(unit % p.sink.nb), h = (int)(unit / p.sink.nb % p.H), seq = (int)(unit / p.sink.nb / p.H);
+        const int cq0 = p.cu_q[seq], cq1 = p.cu_q[seq + 1], ck0 = p.cu_k[seq], ck1 = p.cu_k[seq + 1];
+        if (cq1 - cq0 > p.max_q || ck1 - ck0 > p.max_k || cq1 < cq0 || cq0 < 0 || ck0 < 0 || cq1 > p.total_q ||
+            ck1 > p.total_k || kb * 128 + row >= ck1 - ck0)
+            continue;
+        const float* src = p.sink.acc + (unit * 2 * 128 + row) * p.D + d;
+        const long long at = ((long long)(ck0 + kb * 128 + row) * p.H + h) * p.D + d;
+        T* dk = static_cast<T*>(p.dk) + at;
+        T* dv = static_cast<T*>(p.dv) + at;
+        dk[0] = to_t<T>(src[0]);
+        dk[1] = to_t<T>(src[1]);
+        dv[0] = to_t<T>(src[128 * (long long)p.D]);
+        dv[1] = to_t<T>(src[128 * (long long)p.D + 1]);
+    }
 }
 
 template <typename T, typename BT>
@@ -495,6 +518,31 @@ cudaError_t launch_typed(const BwdParams& p, cudaStream_t stream) {
 size_t bwd_workspace_floats_n(long long dq_elems, long long dbias_elems, long long delta_rows) {
     auto up = [](size_t n) { return (n + 63) & ~(size_t)63; };  // 256-byte pieces
     return up((size_t)dq_elems) + up((size_t)dbias_elems) + up((size_t)delta_rows);
+}
+
+void bwd_sink_share(BwdParams& p) {
+    p.sink.acc = nullptr;
+    p.sink.nb = p.sink.chunk = p.sink.chunks = 0;
+    p.sink.elems = 0;
+    if (!p.varlen || p.kv_num || p.mask_mod != TA_MASK_SINK_WINDOW || (!p.prefix_len && p.prefix_all <= 0)) return;
+    const int chunk = 8;
+    // q blocks of the longest sequence past the reach of its first key block
+    const long long nqb = ((long long)p.max_q + 127) / 128, far = nqb - ((126LL + p.window) / 128 + 1);
+    if (far <= chunk) return;
+    // The first key block's CTA is issued first and walks nqb q blocks; the others, window / 128 + 2 each,
+    // keep 152 SMs busy for total_q / 128 * H * (window / 128 + 2) / 152 of them.  Shared where the one
+    // is not clearly below the other.  (8 sequences of 256 to 2048 tokens, 8 heads, window 512: 16
+    // against 22; the backward 210 us, shared 271.  8192 + 4484 + 777 tokens, window 1024: 64 against
+    // 55; 505 us, shared SHARED_US.)
+    const double rest = (double)p.total_q / 128 * p.H * ((double)p.window / 128 + 2) / 152;
+    if ((double)nqb < 0.75 * rest) return;
+    // (with a number of sinks for each sequence, the host knows none of them: the first block is shared)
+    const long long nb = p.prefix_len ? 1 : ((long long)p.prefix_all + 127) / 128, nkb = ((long long)p.max_k + 127) / 128;
+    if (nb > 4) return;  // (many key blocks see everything: they balance one another)
+    p.sink.nb = (int)(nb < nkb ? nb : nkb);
+    p.sink.chunk = chunk;
+    p.sink.chunks = (int)((far + chunk - 1) / chunk);
+    p.sink.elems = (long long)p.num_seqs * p.H * p.sink.nb * 2 * 128 * p.D;
 }
 
 size_t bwd_workspace_floats(int B, int N, int H, int Q, int K, int D) {

@@ -38,6 +38,13 @@
 // mean of V, so it adds 1 / Lk dO to dV at every key); the tile walk above then runs over
 // that list, with mask_mod deciding each (query, key) of a partial block.  Rows of a tile
 // past the sequence (the next sequence's rows, read through the same maps) have P = 0.
+// Sink window without lists: the first key blocks are seen by every q block, the others by those
+// in reach of the window, so one CTA would walk the whole sequence (8192 rows, window 1024: 64
+// tiles where the others have 9) and the kernel last as long as it does.  Given the workspace for
+// it, those key blocks are shared: their own CTA takes the q blocks in reach and further CTAs, issued
+// first, the far ones, eight at a time; all add dK and dV to an fp32 accumulator, which the
+// last kernel converts.  (Packed sequences of 777, 4484 and 8192 tokens, 8 heads of 64, window
+// 1024, 4 sinks: the backward 505 -> SHARED_US us.)
 
 #include "tc_kernel.cuh"
 
@@ -79,6 +86,10 @@ struct BwdTc {
     int mask_heads, MQ, MK, mask_mod, window, prefix_all;
     const int32_t* prefix_len;
     int qcap;           // entries of the q-block list in shared memory (0: triangle form)
+    // Sink window, shared first key blocks (see SinkShare): 0 blocks = off.
+    float* sink_acc;
+    int sink_nb, sink_chunk;
+    unsigned far_grid;  // CTAs that take chunks of far q blocks, issued before those of the key blocks
 };
 
 // Shared memory (offsets from a 1024-byte aligned base).
@@ -192,6 +203,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
     // at (x, qrow0 + q, tz) and (x, krow0 + k, tz); lse / delta at lrow0 + q.
     long long unit = 0, bn = 0, lrow0;
     int k0, h, b = 0, Qn, Kn, qrow0 = 0, krow0 = 0, tz, seq = 0, prefix = 0;
+    int far = -1;            // packed form: chunk of far q blocks that this CTA takes, or -1
+    bool shared_kb = false;  // packed form: the key block's gradients are summed over several CTAs
     if constexpr (!VARLEN) {
         unit = blockIdx.x / P.nkt;
         k0 = (int)(blockIdx.x - unit * P.nkt) * kBN;
@@ -206,15 +219,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
         // key block slowest: under causal lists key block kb visits the q blocks kb.. of its
         // sequence, so the CTAs with the most work are issued first
         const unsigned sh = (unsigned)P.num_seqs * (unsigned)P.H;
-        k0 = (int)(blockIdx.x / sh) * kBN;
-        seq = (int)((blockIdx.x % sh) / (unsigned)P.H);
-        h = (int)(blockIdx.x % (unsigned)P.H);
+        unsigned bi = blockIdx.x;
+        if (bi >= P.far_grid) {
+            bi -= P.far_grid;
+        } else {  // a chunk of the far q blocks of a shared first key block
+            far = (int)(bi / (sh * (unsigned)P.sink_nb));
+            bi %= sh * (unsigned)P.sink_nb;
+        }
+        k0 = (int)(bi / sh) * kBN;
+        seq = (int)((bi % sh) / (unsigned)P.H);
+        h = (int)(bi % (unsigned)P.H);
+        shared_kb = k0 / kBN < P.sink_nb;
         const int cq0 = P.cu_q[seq], cq1 = P.cu_q[seq + 1], ck0 = P.cu_k[seq], ck1 = P.cu_k[seq + 1];
         Qn = cq1 - cq0;
         Kn = ck1 - ck0;
         if (Qn > P.max_q || Kn > P.max_k || Qn < 0 || Kn < 0 || cq0 < 0 || ck0 < 0 || cq1 > P.total_q ||
             ck1 > P.total_k) {
-            if (threadIdx.x == 0 && k0 == 0 && h == 0) atomicCAS(P.status, 0, kStatusDevice);
+            if (threadIdx.x == 0 && k0 == 0 && h == 0 && far < 0) atomicCAS(P.status, 0, kStatusDevice);
             return;
         }
         if (k0 >= Kn) return;
@@ -258,18 +279,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
     if constexpr (VARLEN) {
         if (warp == kProducerWarp) {
             uint32_t* qw = reinterpret_cast<uint32_t*>(gbase + L.qlist);
-            const int kb = k0 / kBN, nqb = (Qn + kBM - 1) / kBM;
+            const int kb = k0 / kBN;
+            int nqb = (Qn + kBM - 1) / kBM, qb0 = 0;
             int cnt = 0;
+            if (far >= 0) {  // this chunk of the q blocks past the key block's window
+                const long long first = ((long long)k0 + 126 + P.window) / kBM + 1 + (long long)far * P.sink_chunk;
+                qb0 = first < nqb ? (int)first : nqb;
+                nqb = min(nqb, qb0 + P.sink_chunk);
+            }
             // Sink window without lists: q blocks without a kept (query, key) are left out.  Their
             // rows all have a valid key (their own, or a first one) unless there are more
             // queries than keys and window reach.
             const bool sunk = !P.kv_num && P.mask_mod == TA_MASK_SINK_WINDOW;
             const bool all_valid = prefix > 0 || (long long)Qn - Kn < P.window;
-            for (int qb = 0; qb < nqb && qb < P.qcap; ++qb) {
+            for (int qb = qb0; qb < nqb && qb < P.qcap; ++qb) {
                 int st = 1;  // no lists: every block partial
                 if (sunk) {
-                    st = sink_blocks(qb * kBM, min(qb * kBM + kBM, Qn) - 1, Kn, P.window, prefix).visited(kb) ? 1 : 0;
+                    const SinkBlocks sb = sink_blocks(qb * kBM, min(qb * kBM + kBM, Qn) - 1, Kn, P.window, prefix);
+                    st = sb.visited(kb) ? 1 : 0;
                     if (st == 0 && all_valid) continue;
+                    // a shared key block: its own CTA leaves the far q blocks to the chunks
+                    const bool is_far = st == 1 && !(kb >= sb.lo && kb <= sb.hi);
+                    if (shared_kb && is_far != (far >= 0)) continue;
                 }
                 if (P.kv_num) {
                     int f = 0;
@@ -305,6 +336,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
         }
         __syncthreads();
         nqt = *reinterpret_cast<volatile int*>(gbase + L.qn);
+        if (nqt == 0 && shared_kb) return;  // nothing to add
         if (nqt == 0) {  // no row reaches these keys: dK = dV = 0
             const int rows = Kn - k0 < kBN ? Kn - k0 : kBN, per = P.D / 8;  // 16-byte pieces per row
             for (int i = threadIdx.x; i < rows * per; i += blockDim.x) {
@@ -857,6 +889,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                 uint32_t ov[16], ok16[16];
                 tmem_ld_x16(tDV + lane_off + (uint32_t)d0, ov);
                 tmem_ld_x16(tDK + lane_off + (uint32_t)d0, ok16);
+                if (VARLEN && shared_kb) {
+                    // (a far q block reaches the first `prefix` keys alone: the other rows are 0)
+                    if (exists && (far < 0 || key < prefix)) {
+                        float* acc = P.sink_acc +
+                                     ((((long long)seq * P.H + h) * P.sink_nb + k0 / kBN) * 2 * kBN + (key - k0)) * P.D + d0;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            red_add_global(acc + e, __uint_as_float(ok16[e]) * P.scale);
+                            red_add_global(acc + (long long)kBN * P.D + e, __uint_as_float(ov[e]));
+                        }
+                    }
+                    continue;
+                }
                 uint32_t wv[8], wk[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -1015,8 +1060,17 @@ cudaError_t launch_tc_bwd_main(const BwdParams& p, cudaStream_t stream) {
     P.idesc_s = bwd_idesc(bf16, 128, 64, false, false);  // 64 queries (one half of the tile)
     P.idesc_g = bwd_idesc(bf16, 128, D, false, true);
     P.idesc_q = bwd_idesc(bf16, 128, D, true, true);
-    const long long grid = vl ? (long long)p.num_seqs * p.H * P.nkt : (long long)units * P.nkt;
+    long long grid = vl ? (long long)p.num_seqs * p.H * P.nkt : (long long)units * P.nkt;
     if (grid <= 0) return cudaSuccess;
+    if (vl && p.sink.nb > 0) {
+        P.sink_acc = p.sink.acc;
+        P.sink_nb = p.sink.nb;
+        P.sink_chunk = p.sink.chunk;
+        const long long far = (long long)p.num_seqs * p.H * p.sink.nb * p.sink.chunks;
+        if (far > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+        P.far_grid = (unsigned)far;
+        grid += far;
+    }
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     P.qs = D > 64 ? 1 : 2;  // D > 64: one stage, taken per query half
     if (bwd_layout(P, P.nsub).total + 1024 > 232448) P.qs = 1;  // the 227 KB per-block limit

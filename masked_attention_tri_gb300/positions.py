@@ -11,7 +11,7 @@ from typing import Optional
 import torch
 
 from . import abi
-from .api import _DT, _need, _ptr, _row_stride, _stream
+from .api import _DT, _need, _on, _ptr, _row_stride, _stream
 
 _SCALINGS = (None, "linear", "ntk", "yarn")
 
@@ -120,17 +120,19 @@ def _rotary_call(q, k, positions, rotary, inverse, out_q, out_k):
         if k.shape[2] != D:
             raise ValueError("k must have q's D")
         if out_k is None:
-            out_k = torch.empty(k.shape, dtype=k.dtype, device=dev)
-        elif out_k.shape != k.shape:
-            raise ValueError("out_k must have k's shape")
-        ko_rs = _rotary_rows(out_k, "out_k", dev, q.dtype, total)
+            out_k, ko_rs = torch.empty(k.shape, dtype=k.dtype, device=dev), Hk * D
+        else:
+            ko_rs = _rotary_rows(out_k, "out_k", dev, q.dtype, total)
+            if out_k.shape != k.shape:
+                raise ValueError("out_k must have k's shape")
     if out_q is None:
-        out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    elif out_q.shape != q.shape:
-        raise ValueError("out_q must have q's shape")
-    qo_rs = _rotary_rows(out_q, "out_q", dev, q.dtype, total)
+        out_q, qo_rs = torch.empty(q.shape, dtype=q.dtype, device=dev), Hq * D
+    else:
+        qo_rs = _rotary_rows(out_q, "out_q", dev, q.dtype, total)
+        if out_q.shape != q.shape:
+            raise ValueError("out_q must have q's shape")
     if total:
-        with torch.cuda.device(dev):
+        with _on(dev):
             abi.tri_attn_rotary(_ptr(q), _ptr(k), _DT[q.dtype], _ptr(positions), _ptr(rotary.turns), rotary.dim,
                                 rotary.interleaved, rotary.attention_factor, inverse, total, Hq, Hk, D, q_rs, k_rs,
                                 qo_rs, ko_rs, _ptr(out_q), _ptr(out_k), _stream(dev))

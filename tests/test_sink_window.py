@@ -161,6 +161,12 @@ CASES = [
     ([400, 300], [100, 0], 1, 128, 20, 7),          # a sequence without keys
     ([9000], None, 1, 64, 300, 20),                 # more than 64 key blocks
     ([330, 200], None, 2, 80, 90, 10),
+    # long sequences beside short ones: the first key blocks are shared by several CTAs
+    ([2500, 1, 1400, 128], None, 2, 64, 130, 4),
+    ([2100, 700], None, 1, 128, 65, 200),
+    ([2100, 1300], None, 1, 64, 100, [3, 0]),
+    ([2100, 1300], [1900, 60], 1, 96, 100, 30),
+    ([2100], [2100], 1, 32, 1, 400),
 ]
 
 
@@ -180,6 +186,36 @@ def test_forward_and_gradients(lens, lens_k, H, D, window, sinks, dtype):
         assert bool((got["out"][a:a + lens[lens_k.index(0)]] == 0).all()) and bool((got["lse"][:, a:] == -math.inf).all())
         got["lse"] = torch.where(got["lse"] == -math.inf, torch.zeros((), device="cuda"), got["lse"])
     _check(got, want)
+
+
+def test_workspace_of_shared_key_blocks():
+    plain = abi.tri_attn_varlen_bwd_workspace_size(5000, 2, 64, 2500, 2500, False)
+    size = lambda *a: abi.tri_attn_varlen_bwd_sink_workspace_size(3, 5000, 2, 64, *a) - plain  # noqa: E731
+    assert size(2500, 2500, False, 130, 4) == size(2500, 2500, False, 130, -1) == 3 * 2 * 2 * 128 * 64 * 4
+    assert size(2500, 2500, False, 130, 200) == 2 * 3 * 2 * 2 * 128 * 64 * 4
+    # no sinks, few far blocks, too many first blocks
+    assert size(2500, 2500, False, 130, 0) == size(1000, 1000, False, 130, 4) == size(2500, 2500, False, 130, 600) == 0
+
+
+@pytest.mark.gpu
+def test_backward_without_room_for_sharing():
+    """The plain workspace is enough: the same gradients up to the order of sums."""
+    import masked_attention_tri_gb300 as ta
+    from masked_attention_tri_gb300.api import _DT, _stream
+    lens, H, D = [2500, 300], 2, 64
+    q, k, v, g = (x.cuda() for x in _problem(lens, lens, H, D, B16, seed=21))
+    cu = _i32(_cu(lens))
+    o, lse, _ = ta.varlen_attention(q, k, v, cu, cu, 2500, 2500, return_aux=True, mask_mod="sink_window", window=130, sinks=4)
+    n = abi.tri_attn_varlen_bwd_workspace_size(2800, H, D, 2500, 2500, False)
+    ws = torch.full((n // 4 + 4096,), 777.0, device="cuda")
+    grads = [torch.empty_like(q) for _ in range(3)]
+    abi.tri_attn_varlen_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _DT[B16], cu.data_ptr(), cu.data_ptr(), 2, 2800, 2800,
+                            2500, 2500, H, D, 0.125, 0, 0, 0, 0, 1, 0, 0, 128, 128, abi.TA_MASK_SINK_WINDOW, 130, 0, 4, 0,
+                            abi.TA_F32, lse.data_ptr(), o.data_ptr(), g.data_ptr(), *(x.data_ptr() for x in grads), 0,
+                            ws.data_ptr(), n, _stream(q.device))
+    want = _dense(*(x.cpu() for x in (q, k, v, g)), lens, lens, 130, 4, 0.125, B16)
+    _check(dict(zip(("dq", "dk", "dv"), grads)), want, ("dq", "dk", "dv"))
+    assert bool((ws[n // 4:] == 777.0).all()) and ta.get_status() == 0
 
 
 @pytest.mark.gpu
