@@ -11,28 +11,37 @@
 // page held before.
 //
 // Bound: memory.  One CTA takes one page of one sequence (the rows of this call in
-// it) and one job: some heads of q, or some of k, or some of v.  A thread keeps one
-// unit of one row (rotary.cuh: two vectors, V pairs) with its cos and sin in registers
-// and walks the heads.  For an 8-bit cache it walks them twice: first for the
-// largest |x| of each head, then to write the codes; the second reading comes from
-// L1 / L2.  No two CTAs write the same (page, head), so nothing is ordered by atomics
-// (the largest |x| is a maximum of bit patterns: the same in any order).
+// it) and one job: some heads of q, or some of k, or some of v.  As in rotary.cu a thread
+// keeps one unit (two vectors) of a row, and cos and sin of the rows' pairs lie in a table in
+// shared memory, computed once for the job's heads.  Codes need the largest |x| of a page's rows
+// before the first is written: as many rows as 512 units hold stay in registers between the
+// two (64 rows of D = 128: a page of the usual size is read once); larger pages are read twice.
+// No two CTAs write the same (page, head), so nothing is ordered by atomics (the largest |x| is a maximum
+// of bit patterns: the same in any order).
+//   Eight prompts of 256 to 2048 tokens, 32 + 8 heads of 128, pages of 64 in 8 bits: APPEND_US.
 
 #include <cuda_fp8.h>
 
 #include "internal.h"
 #include "rotary.cuh"
+#include "tc_kernel.cuh"
 
 namespace triattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxJobHeads = 8;  // heads of one CTA
+constexpr int kHold = 2;         // units a thread holds (codes) or has in flight
+constexpr int kMaxHeads = 32;    // heads of one CTA, at most
 
 struct AppendArgs {
     KvAppendParams p;
-    int units, runs;        // units per head; pages a sequence can touch
-    int job_heads, q_jobs, kv_jobs;  // heads per CTA; CTAs per run for q, and for each of k and v
+    int units, lanes;            // units per head; rows (or heads) that the CTA's threads take at once
+    int runs;                    // pages a sequence can touch
+    int table_rows;              // rows of the table of cos and sin
+    int row_part;                // rows of a CTA where no maxima are needed
+    // k, v, q: heads of a CTA (they divide Hk and Hq), parts of a page's rows, CTAs of a page
+    int heads[3], parts[3], jobs[3];
+    tc::FastDiv fd[3];           // heads
 };
 
 __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
@@ -50,10 +59,50 @@ __device__ __forceinline__ int scale_exp(uint32_t most) {
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// A unit as codes: its first vector at p, its second o1 further on.
+template <int V>
+__device__ __forceinline__ void store_codes(uint8_t* p, int o1, const float2 (&f)[V], float inv) {
+    if constexpr (V == 1) {
+        const uint32_t w = to_e4m3x2(f[0].x * inv, f[0].y * inv);
+        p[0] = (uint8_t)w;
+        if (o1 >= 0) p[o1] = (uint8_t)(w >> 8);
+    } else {
+        uint32_t w[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i)
+            w[i] = to_e4m3x2(f[2 * i].x * inv, f[2 * i].y * inv) |
+                   (to_e4m3x2(f[2 * i + 1].x * inv, f[2 * i + 1].y * inv) << 16);
+        if constexpr (V == 8) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+            if (o1 >= 0) *reinterpret_cast<uint2*>(p + o1) = make_uint2(w[2], w[3]);
+        } else {
+            *reinterpret_cast<uint32_t*>(p) = w[0];
+            if (o1 >= 0) *reinterpret_cast<uint32_t*>(p + o1) = w[1];
+        }
+    }
+}
+
+// The bits of the largest finite magnitude of a unit.
+template <int V>
+__device__ __forceinline__ uint32_t largest(const float2 (&f)[V]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t a = __float_as_uint(f[i].x) & 0x7fffffffu, b = __float_as_uint(f[i].y) & 0x7fffffffu;
+        if (a < 0x7f800000u) m = max(m, a);
+        if (b < 0x7f800000u) m = max(m, b);
+    }
+    return m;
+}
+
 // C: the cache's element type (T itself, or uint8_t for e4m3 codes).
 template <typename T, typename C, int V>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const AppendArgs a) {
     constexpr bool kCodes = sizeof(C) == 1;
+    extern __shared__ float4 table4[];
+    float* table = reinterpret_cast<float*>(table4);
+    __shared__ uint32_t most[kMaxHeads];
+    __shared__ float before[kMaxHeads];
     const KvAppendParams& p = a.p;
     const int seq = blockIdx.x / a.runs, run = blockIdx.x % a.runs;
     const int row0 = p.cu ? p.cu[seq] : seq, row1 = p.cu ? p.cu[seq + 1] : seq + 1;
@@ -73,149 +122,198 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
     const int cnt = s1 - s0, off0 = (int)(s0 - slot0);         // rows of this call; first slot in the page
     const long long tok0 = (long long)row0 + (s0 - start);
 
-    // The job: kind 0 q, 1 k, 2 v, and its heads.
+    // The job: kind 0 k, 1 v, 2 q (the longest CTAs, whole pages of codes, are issued first), and its heads.
     int job = blockIdx.y, kind = 0;
-    if (job >= a.q_jobs) {
-        job -= a.q_jobs;
-        kind = 1 + job / a.kv_jobs;
-        job -= (kind - 1) * a.kv_jobs;
-    }
-    const int H = kind == 0 ? p.Hq : p.Hk, h0 = job * a.job_heads, nh = min(a.job_heads, H - h0);
-    const bool turn = kind != 2 && p.dim > 0;
+    while (job >= a.jobs[kind]) job -= a.jobs[kind++];
+    const int part = job % a.parts[kind], nh = a.heads[kind], h0 = job / a.parts[kind] * nh;
     long long page = 0;
-    if (kind != 0) {
+    if (kind != 2) {
         page = p.table[(long long)seq * p.max_pages + lp];
         if (page < 0 || page >= p.num_pages) {
             if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusDevice);
             return;
         }
     }
-    const T* src = static_cast<const T*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v);
-    const long long rs = kind == 0 ? p.q_rs : kind == 1 ? p.k_rs : p.v_rs;
-    const long long* cst = kind == 1 ? p.ks : p.vs;
-    C* cache = static_cast<C*>(kind == 1 ? p.k_cache : p.v_cache) + page * cst[0];
-    float* scale = kind == 1 ? p.k_scale : p.v_scale;
+    const T* src = static_cast<const T*>(kind == 0 ? p.k : kind == 1 ? p.v : p.q);
+    const long long rs = kind == 0 ? p.k_rs : kind == 1 ? p.v_rs : p.q_rs;
+    const long long* cst = kind == 0 ? p.ks : p.vs;
+    C* cache = static_cast<C*>(kind == 0 ? p.k_cache : p.v_cache) + page * cst[0];
 
-    // items = rows x units; threads beyond the items take further heads
-    const int items = cnt * a.units;
-    const int hs = items >= kThreads ? 1 : kThreads / items;
-    const int hsub = items >= kThreads ? 0 : threadIdx.x / items;
-    const int item0 = items >= kThreads ? threadIdx.x : threadIdx.x - hsub * items;
+    // This thread's unit, and the rows' table.
+    const int hl = threadIdx.x / a.units, u = threadIdx.x - hl * a.units;
+    const bool in = hl < a.lanes;
+    const RotUnit r = rot_unit<V>(u, p.D, p.dim, p.interleaved);
+    const int np = p.dim / 2, nr = np / V;
+    const bool turn = kind != 1 && p.dim > 0, turned = turn && r.turned;
+    const int hold = a.lanes * kHold;                          // rows that the CTA's registers hold
+    src += tok0 * rs + (long long)h0 * p.D + r.o0;
+    auto fill = [&](int c0, int rows) {
+        if (!turn) return;
+        __syncthreads();
+        for (int e = threadIdx.x; e < rows * np; e += kThreads) {
+            const int t = e / np, i = e - t * np;
+            const int pos = p.positions ? p.positions[tok0 + c0 + t] : s0 + c0 + t;
+            const float2 cs = rotary_cos_sin(pos, p.turns[i]);
+            rot_table_put<V>(table, t, i, nr, cs.x * p.mscale, cs.y * p.mscale);
+        }
+        __syncthreads();
+    };
+    auto turned_floats = [&](const RotRaw<T, V>& w, int row, float2 (&f)[V]) {
+        rot_floats<T, V>(w, f);
+        if (turned) rot_turn<V>(f, rot_table_at<V>(table, row, u, nr), nr, p.interleaved);
+    };
 
-    __shared__ uint32_t most[kMaxJobHeads];
-    __shared__ float inv[kMaxJobHeads], down[kMaxJobHeads];
+    if (!kCodes || kind == 2) {
+        // ---- q, and caches of the inputs' type: some rows of the page, rows and heads in the order of memory.
+        const int c0 = part * a.row_part;
+        if (c0 < cnt) {
+            const int rows = min(a.row_part, cnt - c0);
+            fill(c0, rows);
+            if (!in) return;
+            for (int n0 = hl; n0 < rows * nh; n0 += hold) {
+                RotRaw<T, V> w[kHold];
+                int row[kHold], head[kHold];
+#pragma unroll
+                for (int j = 0; j < kHold; ++j) {
+                    const int n = n0 + j * a.lanes;
+                    if (n >= rows * nh) break;
+                    row[j] = (int)a.fd[kind].div((uint32_t)n);
+                    head[j] = n - row[j] * nh;
+                    w[j].load(src + (c0 + row[j]) * rs + head[j] * p.D, r.o1);
+                }
+#pragma unroll
+                for (int j = 0; j < kHold; ++j) {
+                    if (n0 + j * a.lanes >= rows * nh) break;
+                    if (turned) {
+                        float2 f[V];
+                        turned_floats(w[j], row[j], f);
+                        w[j] = rot_raw<T, V>(f);
+                    }
+                    if (kind == 2) {
+                        w[j].store(static_cast<T*>(p.q_out) + (tok0 + c0 + row[j]) * p.qo_rs +
+                                       (long long)(h0 + head[j]) * p.D + r.o0, r.o1);
+                    } else if constexpr (!kCodes) {
+                        w[j].store(cache + (h0 + head[j]) * cst[1] + (off0 + c0 + row[j]) * cst[2] + r.o0, r.o1);
+                    }
+                }
+            }
+        }
+        return;
+    }
+
+    // ---- Codes.  The heads go in groups that fit the registers, n = head * cnt + row; a page with more rows than
+    // that goes head by head, twice over its rows.
     if constexpr (kCodes) {
-        if (kind != 0) {
-            if (threadIdx.x < kMaxJobHeads) most[threadIdx.x] = 0;
-            __syncthreads();
+        float* scale = (kind == 0 ? p.k_scale : p.v_scale) + page * p.Hk + h0;
+        if (threadIdx.x < nh) {
+            most[threadIdx.x] = 0;
+            before[threadIdx.x] = off0 > 0 ? scale[threadIdx.x] : 0.f;
         }
-    }
-    // pass 0: the largest finite |x| of each head; pass 1: write
-    for (int pass = (kCodes && kind != 0) ? 0 : 1; pass < 2; ++pass) {
-        if (kCodes && kind != 0 && pass == 1) {
-            __syncthreads();
-            if (threadIdx.x < nh) {
-                float* sp = scale + page * p.Hk + h0 + threadIdx.x;
-                const int e = scale_exp(most[threadIdx.x]);
-                const float need = exp2i(e), before = off0 > 0 ? *sp : 0.f;
-                const bool keep = before >= need;  // the page's scale covers the new rows
-                inv[threadIdx.x] = keep ? 1.f / before : exp2i(-e);
-                down[threadIdx.x] = keep ? 1.f : before * exp2i(-e);
-                if (!keep) *sp = need;
-            }
-            __syncthreads();
-            if (off0 > 0) {  // re-code the rows that were there, where a scale has grown
-                const int words = p.D / 4;
-                for (int i = 0; i < nh; ++i) {
-                    if (down[i] == 1.f) continue;
-                    C* rows = cache + (long long)(h0 + i) * cst[1];
-                    for (int j = threadIdx.x; j < off0 * words; j += kThreads) {
-                        const int r = j / words, d = (j - r * words) * 4;
-                        uint32_t* w = reinterpret_cast<uint32_t*>(rows + (long long)r * cst[2] + d);
-                        const uint32_t x = *w;
-                        const __half2 lo(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3));
-                        const __half2 hi(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x >> 16), __NV_E4M3));
-                        const float2 fl = __half22float2(lo), fh = __half22float2(hi);
-                        *w = to_e4m3x2(fl.x * down[i], fl.y * down[i]) |
-                             (to_e4m3x2(fh.x * down[i], fh.y * down[i]) << 16);
-                    }
-                }
-            }
-        }
-        // (every lane of a warp makes the same number of turns: the maxima are reduced over it)
-        for (int base = 0; base < items; base += kThreads) {
-            const bool on = hsub < hs && base + item0 < items;
-            const int item = on ? base + item0 : 0;
-            const int row = item / a.units, u = item - row * a.units;
-            const RotUnit r = rot_unit<V>(u, p.D, p.dim, p.interleaved);
-            const bool rot = turn && r.pair0 >= 0;
-            float cs[V], sn[V];
-            if (rot) {
-                const int pos = p.positions ? p.positions[tok0 + row] : s0 + row;
+        const bool whole = cnt <= hold;             // the rows stay in registers
+        const bool once = cnt <= a.table_rows;      // the table holds them all
+        if (once) fill(0, cnt);
+        __syncthreads();
+        const int group = whole ? min(nh, hold / cnt) : 1;
+        for (int g0 = 0; g0 < nh; g0 += group) {
+            const int items = min(group, nh - g0) * min(cnt, hold);
+            RotRaw<T, V> w[kHold];
+            auto split = [&](int j, int& head, int& row) -> bool {
+                const int n = hl + j * a.lanes;
+                head = group == 1 ? 0 : n / cnt;
+                row = n - head * cnt;
+                return in && n < items;
+            };
+            auto load = [&](int c0) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float2 t = rotary_cos_sin(pos, p.turns[r.pair0 + i]);
-                    cs[i] = t.x * p.mscale;
-                    sn[i] = t.y * p.mscale;
+                for (int j = 0; j < kHold; ++j) {
+                    int head, row;
+                    if (split(j, head, row) && c0 + row < cnt) w[j].load(src + (c0 + row) * rs + (g0 + head) * p.D, r.o1);
                 }
-            }
-            const T* srow = src + (tok0 + row) * rs + (long long)h0 * p.D;
-            for (int i = hs == 1 ? 0 : hsub; i < nh; i += hs) {
-                if (hs > 1 && !on) break;
-                float x0[V], x1[V];
-                rot_load<T, V>(srow + (long long)i * p.D + r.o0, x0);
-                if (r.o1 >= 0) rot_load<T, V>(srow + (long long)i * p.D + r.o1, x1);
-                if (rot) rot_turn<V>(x0, x1, cs, sn, p.interleaved);
-                if (kind == 0) {
-                    if (!on) continue;
-                    T* dst = static_cast<T*>(p.q_out) + (tok0 + row) * p.qo_rs + (long long)(h0 + i) * p.D;
-                    rot_store<T, V>(dst + r.o0, x0);
-                    if (r.o1 >= 0) rot_store<T, V>(dst + r.o1, x1);
-                    continue;
-                }
-                C* dst = cache + (long long)(h0 + i) * cst[1] + (long long)(off0 + row) * cst[2];
-                if constexpr (!kCodes) {
-                    if (!on) continue;
-                    rot_store<C, V>(dst + r.o0, x0);
-                    if (r.o1 >= 0) rot_store<C, V>(dst + r.o1, x1);
-                } else if (pass == 0) {
+            };
+            auto maxima = [&](int c0) {
+#pragma unroll
+                for (int j = 0; j < kHold; ++j) {
+                    int head, row;
+                    const bool on = split(j, head, row) && c0 + row < cnt;
+                    const int t0 = once ? c0 : 0;
                     uint32_t m = 0;
+                    if (on) {
+                        float2 f[V];
+                        turned_floats(w[j], t0 + row, f);
+                        m = largest<V>(f);
+                    }
+                    if (group == 1) {
+                        m = __reduce_max_sync(0xffffffffu, m);
+                        if (threadIdx.x % 32 == 0) atomicMax(&most[g0], m);
+                    } else if (on) {
+                        atomicMax(&most[g0 + head], m);
+                    }
+                }
+            };
+            // A head's scale: its reciprocal, and the factor on the codes that are there (1: unchanged).
+            auto scales = [&](int head, float& inv, float& down, float& need) {
+                const int e = scale_exp(most[g0 + head]);
+                const float b = before[g0 + head];
+                need = exp2i(e);
+                const bool keep = b >= need;  // the page's scale covers the new rows
+                inv = keep ? 1.f / b : exp2i(-e);
+                down = keep ? 1.f : b * exp2i(-e);
+            };
+            auto write = [&](int c0) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const uint32_t b0 = __float_as_uint(x0[j]) & 0x7fffffffu;
-                        const uint32_t b1 = r.o1 >= 0 ? __float_as_uint(x1[j]) & 0x7fffffffu : 0u;
-                        if (b0 < 0x7f800000u) m = max(m, b0);
-                        if (b1 < 0x7f800000u) m = max(m, b1);
-                    }
-                    if (hs == 1) {  // every lane of the warp is here, with the same head
-                        m = __reduce_max_sync(0xffffffffu, on ? m : 0u);
-                        if ((threadIdx.x & 31) == 0) atomicMax(&most[i], m);
-                    } else {
-                        atomicMax(&most[i], m);
-                    }
-                } else if (on) {
-                    const float iv = inv[i];
-                    RotVec<C, V> c0, c1;
-                    if constexpr (V == 1) {
-                        c0.e[0] = (C)to_e4m3x2(x0[0] * iv, 0.f);
-                        c1.e[0] = (C)to_e4m3x2(x1[0] * iv, 0.f);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < V; j += 2) {
-                            const uint32_t w0 = to_e4m3x2(x0[j] * iv, x0[j + 1] * iv);
-                            c0.e[j] = (C)w0;
-                            c0.e[j + 1] = (C)(w0 >> 8);
-                            const uint32_t w1 = to_e4m3x2(x1[j] * iv, x1[j + 1] * iv);
-                            c1.e[j] = (C)w1;
-                            c1.e[j + 1] = (C)(w1 >> 8);
-                        }
-                    }
-                    *reinterpret_cast<RotVec<C, V>*>(dst + r.o0) = c0;
-                    if (r.o1 >= 0) *reinterpret_cast<RotVec<C, V>*>(dst + r.o1) = c1;
+                for (int j = 0; j < kHold; ++j) {
+                    int head, row;
+                    if (!split(j, head, row) || c0 + row >= cnt) continue;
+                    const int t0 = once ? c0 : 0;
+                    float2 f[V];
+                    turned_floats(w[j], t0 + row, f);
+                    float inv, down, need;
+                    scales(head, inv, down, need);
+                    store_codes<V>(cache + (h0 + g0 + head) * cst[1] + (off0 + c0 + row) * cst[2] + r.o0, r.o1, f, inv);
+                }
+            };
+            for (int c0 = 0; c0 < cnt; c0 += hold) {
+                if (!once) fill(c0, min(hold, cnt - c0));
+                load(c0);
+                maxima(c0);
+            }
+            __syncthreads();
+            // The new scale, and the codes that were there where it has grown.
+            for (int i = 0; i < min(group, nh - g0); ++i) {
+                float inv, down, need;
+                scales(i, inv, down, need);
+                if (down == 1.f) continue;
+                if (threadIdx.x == 0) scale[g0 + i] = need;
+                const int words = p.D / 4;
+                C* rows = cache + (h0 + g0 + i) * cst[1];
+                for (int j = threadIdx.x; j < off0 * words; j += kThreads) {
+                    const int row = j / words, d = (j - row * words) * 4;
+                    uint32_t* at = reinterpret_cast<uint32_t*>(rows + row * cst[2] + d);
+                    const uint32_t x = *at;
+                    const __half2 lo(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3));
+                    const __half2 hi(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x >> 16), __NV_E4M3));
+                    const float2 fl = __half22float2(lo), fh = __half22float2(hi);
+                    *at = to_e4m3x2(fl.x * down, fl.y * down) | (to_e4m3x2(fh.x * down, fh.y * down) << 16);
+                }
+            }
+            if (whole) {
+                write(0);
+            } else {
+                for (int c0 = 0; c0 < cnt; c0 += hold) {
+                    if (!once) fill(c0, min(hold, cnt - c0));
+                    load(c0);
+                    write(c0);
                 }
             }
         }
     }
+}
+
+// The largest divisor of H that is at most `most`.
+int heads_of_job(int H, int most) {
+    for (int h = most < H ? most : H; h > 1; --h)
+        if (H % h == 0) return h;
+    return 1;
 }
 
 template <typename T, typename C, int V>
@@ -223,14 +321,35 @@ cudaError_t launch(const KvAppendParams& p, cudaStream_t stream) {
     AppendArgs a;
     a.p = p;
     a.units = rot_units<V>(p.D, p.dim);
-    a.runs = (p.max_n + p.page - 1) / p.page + 1;
-    if (p.max_n == 1) a.runs = 1;
-    a.job_heads = kMaxJobHeads;
-    a.q_jobs = p.q ? (p.Hq + a.job_heads - 1) / a.job_heads : 0;
-    a.kv_jobs = (p.Hk + a.job_heads - 1) / a.job_heads;
-    const long long gx = (long long)p.num_seqs * a.runs, gy = a.q_jobs + 2LL * a.kv_jobs;
+    a.lanes = kThreads / a.units;  // (a head has at most 128 units)
+    a.runs = p.max_n == 1 ? 1 : (p.max_n + p.page - 1) / p.page + 1;
+    // Heads of a CTA: the table serves them all (16 rows of a page are work enough); but few for codes of
+    // whole pages, which go one after the other.
+    const bool few = p.max_n <= 8;
+    const bool codes = sizeof(C) == 1;
+    a.heads[0] = heads_of_job(p.Hk, codes && !few ? 4 : 16);
+    a.heads[1] = heads_of_job(p.Hk, codes && !few ? 2 : 16);
+    a.heads[2] = p.q ? heads_of_job(p.Hq, 32) : 1;
+    for (int i = 0; i < 3; ++i) a.fd[i] = tc::make_fastdiv((uint32_t)a.heads[i]);
+    // The table: a page's rows of this call, or 64 KB of them (twice what the registers hold, at least).
+    const int row_bytes = (p.dim / 2) * (int)sizeof(float2);
+    int rows = p.page < p.max_n ? p.page : p.max_n;
+    if (row_bytes > 0 && rows > (64 << 10) / row_bytes) rows = (64 << 10) / row_bytes;
+    a.table_rows = rows;
+    a.row_part = rows < 16 ? rows : 16;
+    const int parts = ((p.page < p.max_n ? p.page : p.max_n) + a.row_part - 1) / a.row_part;
+    for (int i = 0; i < 3; ++i) a.parts[i] = i == 2 || !codes ? parts : 1;
+    a.jobs[0] = p.Hk / a.heads[0] * a.parts[0];
+    a.jobs[1] = p.Hk / a.heads[1] * a.parts[1];
+    a.jobs[2] = p.q ? p.Hq / a.heads[2] * a.parts[2] : 0;
+    const long long gx = (long long)p.num_seqs * a.runs, gy = (long long)a.jobs[0] + a.jobs[1] + a.jobs[2];
     if (gx > 0x7fffffffLL || gy > 65535) return cudaErrorInvalidConfiguration;
-    kv_append_kernel<T, C, V><<<dim3((unsigned)gx, (unsigned)gy), kThreads, 0, stream>>>(a);
+    const size_t smem = (size_t)rows * row_bytes;
+    if (smem > (48 << 10)) {
+        const cudaError_t e = cudaFuncSetAttribute(kv_append_kernel<T, C, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10);
+        if (e != cudaSuccess) return e;
+    }
+    kv_append_kernel<T, C, V><<<dim3((unsigned)gx, (unsigned)gy), kThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 

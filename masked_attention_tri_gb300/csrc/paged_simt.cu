@@ -21,10 +21,10 @@ constexpr int kRows = 8;
 constexpr int kMinTiles = 8;   // shares are not cut finer than one tile a warp
 
 template <typename C>
-__device__ __forceinline__ float4 load4(const C* p) {
-    float x[4];
-    rot_load<C, 4>(p, x);
-    return make_float4(x[0], x[1], x[2], x[3]);
+__device__ __forceinline__ float4 load4(const C* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+    return *reinterpret_cast<const float4*>(p);
 }
 template <>
 __device__ __forceinline__ float4 load4<uint8_t>(const uint8_t* p) {
