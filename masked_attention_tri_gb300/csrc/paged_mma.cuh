@@ -9,10 +9,16 @@
 // 8.  The kernel therefore aims to keep loads in flight: one producer warp fills a ring of
 // stages (a tile of K and of V each, up to 190 KB) by TMA, 128-byte swizzled; the consumer
 // warps take blocks of 16 slots, each with a running maximum, sum and O of its own, and
-// merge once at the unit's end.  No warp waits for another within a unit.  A warp takes a
-// whole stage (four blocks) at a time where there are plenty, or single blocks where the share
-// holds few tiles and the time of one tile on one warp would be what counts.  The loop over
-// blocks is not unrolled: 16 slots' code fits the instruction cache of a cold start.
+// merge once at the unit's end.  No warp waits for another within a unit.  A warp takes half
+// a stage at a time where there are plenty, or a block or two where the share holds few tiles
+// and the time of one tile on one warp would be what counts.  The loop over blocks is not
+// unrolled further than two: that code fits the instruction cache of a cold start.  Where a
+// unit ends the producer is already loading the next one's first tiles, and its queries are in registers.
+//
+// Measured from a cold L2, 32 heads over 8 of 128, pages of 64: 64 sequences of 1k to 16k slots in 8 bits
+// 208 us (5.5 TB/s; the copies alone 198, the arithmetic alone 175), in 16 bits 355 us (6.4 TB/s); 256
+// sequences of 256 to 1024 slots in 8 bits 118 us, of which 79 are waits, set-up and merges of the 14 units
+// that a CTA has there.  64 query heads 216 us, 128 276 us: bound by the conversions' and products' rate.
 //
 //   S^T = K Q^T      A: slots x d from shared memory, B: Q^T, kept in fragment order
 //   O^T += V^T P^T   A: d x slots; P^T comes from S^T's accumulators by movmatrix
@@ -25,8 +31,8 @@
 //
 // Fragments.  K (and 16-bit V, transposed) by ldmatrix, whose four matrices are an A operand's four
 // registers as they stand; of 8-bit K a matrix holds 16 columns, a lane's four codes are two pairs, and
-// k index 2t, 2t + 1, 2t + 8, 2t + 9 of a product stands for columns 4t to 4t + 3.  8-bit V^T: lane (g, t) = (lane / 4, lane % 4) reads eight columns of four slots
-// and pairs the slots' bytes by prmt.  The 16 rows of K's operand may be any slots: row g is slot pi(g)
+// k index 2t, 2t + 1, 2t + 8, 2t + 9 of a product stands for columns 4t to 4t + 3.  8-bit V^T: lane
+// (g, t) = (lane / 4, lane % 4) reads eight columns of four slots and pairs the slots' bytes by prmt.  The 16 rows of K's operand may be any slots: row g is slot pi(g)
 // (and row g + 8 slot pi(g) + 8), pi(2i) = 2i, pi(2i + 1) = (2i ^ 4) + 1, so that the lanes' slots of V
 // are 0, 2, 4, 6 and 5, 7, 1, 3 in turn, whose swizzled reads meet no bank twice.
 //
@@ -57,6 +63,10 @@ struct Yes {
 struct No {
     static constexpr bool value = false;
 };
+template <int M>
+struct Blocks {
+    static constexpr int value = M;
+};
 
 constexpr uint32_t kMmaSmem = 232448 - 1024 - 256;  // 227 KB less the alignment of the ring and the static part
 
@@ -85,11 +95,13 @@ struct MmaConfig {
     static constexpr uint32_t kStage = 2 * kBoxes * kBoxBytes;          // K boxes, then V boxes
     static constexpr int kRows = NT * 8;
     // Consumers: with the producer eight warps, so that a thread may have 255 registers (O alone takes 16 NDC
-    // NT).  Measured on 64 sequences of 1k to 16k slots in 8 bits: 7 warps 226 us, 11 warps 257, 15 warps
-    // 275: the more warps work on stages at a time, the fewer stages are left for copies in flight.
+    // NT).  Measured on 64 sequences of 1k to 16k slots in 8 bits (before the warps took two blocks at once):
+    // 7 warps 226 us, 11 warps 257, 15 warps 275: the more warps work on stages at a time, the fewer stages
+    // are left for copies in flight.
     static constexpr int kWarps = 7;
     static constexpr int kThreads = (kWarps + 1) * 32;
-    static constexpr int kBufs = 4;                                     // merge buffers (no more than warps)
+    // Merge buffers: one for each warp where the ring keeps its six stages, else four taken in two turns.
+    static constexpr int kBufs = NT * NDC <= 2 ? kWarps : 4;
     static constexpr int kOStride = NDC * 64 + 4;                       // floats of a merged row
     static constexpr uint32_t kQ = NDC * NT * 1024;  // Q in fragment order
     static constexpr uint32_t kO = (uint32_t)kBufs * kRows * kOStride * 4;
@@ -236,85 +248,95 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
         const uint32_t bytes = (uint32_t)(2 * nbox * span * 128);
         int slot0 = 0, turn0 = 0;                      // the next stage and how often the ring has gone round
         bool ok = true;
-        while (walk_next(p, w, u)) {
-            const int j_end = min(u.j1, u.t.nt);
-            const int32_t* row = p.table + (long long)u.seq * p.max_pages;
-            // The table entry of this lane's part of tile jb + mytile (-1: not needed).  Entries and scales are
-            // loaded a batch ahead and not looked at before they are needed.
-            int key_n = 0, page_n = -1;
-            bool need_n = false;
-            float ks_n = 1.f, vs_n = 1.f;
-            auto look = [&](int jb) {
-                const int j = mytile < per ? jb + mytile : j_end;
-                key_n = j < j_end ? u.t.tile(j) * C::kSlots + mysub * span : 0;
-                need_n = j < j_end && key_n <= u.t.p1 &&
-                         (p.window <= 0 || (long long)u.t.p0 - (key_n + span - 1) < p.window || key_n < p.sinks);
-                page_n = need_n ? row[key_n / p.page] : -1;
-            };
-            auto check_and_scale = [&]() {
-                if (need_n && (page_n < 0 || page_n >= p.num_pages)) {
-                    atomicCAS(p.status, 0, kStatusDevice);
-                    page_n = -1;
+        // The next batch: unit u, tiles from jb.  Its table entries and scales are loaded while the batch before it
+        // is given out (the last of one unit while the first of the next is looked up), and not
+        // looked at before they are needed.
+        int jb = 0, j_end = 0, key_n = 0, page_n = -1;
+        bool need_n = false;
+        float ks_n = 1.f, vs_n = 1.f;
+        auto next_batch = [&]() -> bool {
+            jb += per;
+            while (jb >= j_end) {
+                if (!walk_next(p, w, u)) return false;
+                jb = u.j0;
+                j_end = min(u.j1, u.t.nt);
+            }
+            // the entry of this lane's part of tile jb + mytile (-1: not needed)
+            const int j = mytile < per ? jb + mytile : j_end;
+            key_n = j < j_end ? u.t.tile(j) * C::kSlots + mysub * span : 0;
+            need_n = j < j_end && key_n <= u.t.p1 &&
+                     (p.window <= 0 || (long long)u.t.p0 - (key_n + span - 1) < p.window || key_n < p.sinks);
+            page_n = need_n ? p.table[(long long)u.seq * p.max_pages + key_n / p.page] : -1;
+            return true;
+        };
+        auto check_and_scale = [&]() {
+            if (need_n && (page_n < 0 || page_n >= p.num_pages)) {
+                atomicCAS(p.status, 0, kStatusDevice);
+                page_n = -1;
+            }
+            if (kCodes && page_n >= 0) {
+                ks_n = p.k_scale[(long long)page_n * p.Hk + u.h];
+                vs_n = p.v_scale[(long long)page_n * p.Hk + u.h];
+            }
+        };
+        bool have = next_batch();
+        if (have) check_and_scale();
+        while (have) {
+            // What each lane's tile needs, made ready for all of them at once.
+            const int page = page_n, key = key_n, h = u.h;
+            const float4 sc = kCodes ? make_float4(ks_n, log2f(vs_n), 1.f / vs_n, 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
+            uint32_t valid = page >= 0 ? ((1u << blocks) - 1u) << (mysub * blocks) : 0u;
+            int loads = page >= 0 ? 1 : 0;
+            for (int o = 1; o < nb; o <<= 1) {  // over the lanes of the tile
+                valid |= __shfl_xor_sync(0xffffffffu, valid, o);
+                loads += __shfl_xor_sync(0xffffffffu, loads, o);
+            }
+            const int in_page = key % p.page;
+            const int todo = min(per, j_end - jb);
+            const int slot = slot0 + mytile < C::kStages ? slot0 + mytile : slot0 + mytile - C::kStages;
+            const int turn = slot0 + mytile < C::kStages ? turn0 : turn0 + 1;
+            bool wait = mytile < todo, looked = false, checked = false;
+            // (bounded: after a wait that ran out every tile is given out empty and the CTA runs to its end)
+            while (__any_sync(0xffffffffu, wait)) {
+                // tiles whose stage has been read (the lanes of a tile go by their first)
+                bool go = wait && (turn == 0 || !ok || tc::mbar_test(empty(slot), (uint32_t)(turn - 1) & 1u));
+                go = __shfl_sync(0xffffffffu, go, lane - mysub);
+                StageMeta& mt = meta[slot];
+                if (go) {
+                    if (kCodes) mt.sc[mysub] = sc;
+                    if (mysub == 0)
+                        tc::st_shared_v4(smem_u32(&mt.valid), ok ? valid : 0u, (uint32_t)key, (uint32_t)turn, 0u);
                 }
-                if (kCodes && page_n >= 0) {
-                    ks_n = p.k_scale[(long long)page_n * p.Hk + u.h];
-                    vs_n = p.v_scale[(long long)page_n * p.Hk + u.h];
-                }
-            };
-            look(u.j0);
-            check_and_scale();
-            for (int jb = u.j0; jb < j_end; jb += per) {
-                // What each lane's tile needs, made ready for all of them at once.
-                const int page = page_n, key = key_n;
-                const float4 sc = kCodes ? make_float4(ks_n, log2f(vs_n), 1.f / vs_n, 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
-                uint32_t valid = page >= 0 ? ((1u << blocks) - 1u) << (mysub * blocks) : 0u;
-                int loads = page >= 0 ? 1 : 0;
-                for (int o = 1; o < nb; o <<= 1) {  // over the lanes of the tile
-                    valid |= __shfl_xor_sync(0xffffffffu, valid, o);
-                    loads += __shfl_xor_sync(0xffffffffu, loads, o);
-                }
-                const int in_page = key % p.page;
-                const int todo = min(per, j_end - jb);
-                look(jb + per);  // (in flight while the batch is given out)
-                const int slot = slot0 + mytile < C::kStages ? slot0 + mytile : slot0 + mytile - C::kStages;
-                const int turn = slot0 + mytile < C::kStages ? turn0 : turn0 + 1;
-                bool wait = mytile < todo;
-                // (bounded: after a wait that ran out every tile is given out empty and the CTA runs to its end)
-                for (uint32_t spin = 1; __any_sync(0xffffffffu, wait); ++spin) {
-                    // tiles whose stage has been read (the lanes of a tile go by their first)
-                    bool go = wait && (turn == 0 || !ok || tc::mbar_test(empty(slot), (uint32_t)(turn - 1) & 1u));
-                    go = __shfl_sync(0xffffffffu, go, lane - mysub);
-                    StageMeta& mt = meta[slot];
-                    if (go) {
-                        if (kCodes) mt.sc[mysub] = sc;
-                        if (mysub == 0)
-                            tc::st_shared_v4(smem_u32(&mt.valid), ok ? valid : 0u, (uint32_t)key, (uint32_t)turn, 0u);
+                __syncwarp();
+                if (go && mysub == 0) mbar_expect_tx(full(slot), ok ? (uint32_t)loads * bytes : 0u);
+                __syncwarp();
+                if (go && page >= 0 && ok) {
+                    const uint32_t dst = ring + (uint32_t)slot * C::kStage + (uint32_t)(mysub * span) * 128u;
+                    for (int b = 0; b < nbox; ++b) {
+                        const int x = b * 64;  // (16-bit units)
+                        tc::tma_load_4d(dst + b * C::kBoxBytes, &P.tm_k, x, in_page, h, page, full(slot));
+                        tc::tma_load_4d(dst + (C::kBoxes + b) * C::kBoxBytes, &P.tm_v, x, in_page, h, page, full(slot));
                     }
-                    __syncwarp();
-                    if (go && mysub == 0) mbar_expect_tx(full(slot), ok ? (uint32_t)loads * bytes : 0u);
-                    __syncwarp();
-                    if (go && page >= 0 && ok) {
-                        const uint32_t dst = ring + (uint32_t)slot * C::kStage + (uint32_t)(mysub * span) * 128u;
-                        for (int b = 0; b < nbox; ++b) {
-                            const int x = b * 64;  // (16-bit units)
-                            tc::tma_load_4d(dst + b * C::kBoxBytes, &P.tm_k, x, in_page, u.h, page, full(slot));
-                            tc::tma_load_4d(dst + (C::kBoxes + b) * C::kBoxBytes, &P.tm_v, x, in_page, u.h, page, full(slot));
-                        }
-                    }
-                    wait = wait && !go;
-                    if (!__any_sync(0xffffffffu, go) && ok) {  // none: sleep until the first of them has been read
-                        const int first = __ffs(__ballot_sync(0xffffffffu, wait)) - 1;
-                        const uint32_t bar = __shfl_sync(0xffffffffu, empty(slot), first);
-                        const int use = __shfl_sync(0xffffffffu, turn, first);
-                        ok = __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(use - 1) & 1u, abort_flag, p.status));
-                    }
-                    if (spin == 1) check_and_scale();  // (the next batch's scales load while this one waits)
                 }
-                slot0 += todo;
-                if (slot0 >= C::kStages) {
-                    slot0 -= C::kStages;
-                    ++turn0;
+                wait = wait && !go;
+                if (!looked) {
+                    looked = true;
+                    have = next_batch();
+                } else if (!checked) {
+                    checked = true;
+                    if (have) check_and_scale();
+                } else if (!__any_sync(0xffffffffu, go) && ok) {  // none: sleep until the first of them has been read
+                    const int first = __ffs(__ballot_sync(0xffffffffu, wait)) - 1;
+                    const uint32_t bar = __shfl_sync(0xffffffffu, empty(slot), first);
+                    const int use = __shfl_sync(0xffffffffu, turn, first);
+                    ok = __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(use - 1) & 1u, abort_flag, p.status));
                 }
+            }
+            if (!checked && have) check_and_scale();
+            slot0 += todo;
+            if (slot0 >= C::kStages) {
+                slot0 -= C::kStages;
+                ++turn0;
             }
         }
         if (*abort_flag && lane == 0) {  // copies in flight end before the CTA does
@@ -343,35 +365,44 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
     uint32_t idx = 0;
     bool ok = true;
     long long at = sh.begin;
-    while (walk_next(p, w, u)) {
-        const long long head0 = (long long)u.h * p.G;
-        const int total_rows = u.q.n * p.G, row_first = u.rt * C::kRows;
-        // ---- Q of the unit, in fragment order: warp w takes rows w, w + kWarps, ...
-        for (int r = warp; r < C::kRows; r += kWarps) {
-            const int row = row_first + r;
-            const bool there = row < total_rows;
-            const uint16_t* qp = static_cast<const uint16_t*>(p.q);
-            if (there) qp += (long long)(u.q.row0 + row / p.G) * p.q_rs + (head0 + row % p.G) * p.D;
-            float factor = p.scale_log2e;
-            // lane l holds elements [4 l, 4 l + 4) and, for D > 128, 128 further on
-            uint2 x[(NDC + 1) / 2];
+    // Q of a unit: warp w takes rows w, w + kWarps, ...  Loaded a unit ahead, so that its latency passes
+    // behind the tiles; lane l holds elements [4 l, 4 l + 4) and, for D > 128, 128 further on.
+    constexpr int kQRows = (C::kRows + kWarps - 1) / kWarps, kQPieces = (NDC + 1) / 2;
+    uint2 xq[kQRows][kQPieces];
+    auto fetch_q = [&](const Unit& v) {
 #pragma unroll
-            for (int c = 0; c < (NDC + 1) / 2; ++c) {
+        for (int i = 0; i < kQRows; ++i) {
+            const int r = warp + i * kWarps, row = v.rt * C::kRows + r;
+            const bool there = r < C::kRows && row < v.q.n * p.G;
+            const uint16_t* qp = static_cast<const uint16_t*>(p.q);
+            if (there) qp += (long long)(v.q.row0 + row / p.G) * p.q_rs + ((long long)v.h * p.G + row % p.G) * p.D;
+#pragma unroll
+            for (int c = 0; c < kQPieces; ++c) {
                 const int d = c * 128 + lane * 4;
-                x[c] = there && d < p.D ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0u, 0u);
+                xq[i][c] = there && d < p.D ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0u, 0u);
             }
+        }
+    };
+    // ... and into shared memory in fragment order.
+    auto put_q = [&]() {
+#pragma unroll
+        for (int i = 0; i < kQRows; ++i) {
+            const int r = warp + i * kWarps;
+            if (r >= C::kRows) break;
+            float factor = p.scale_log2e;
+            uint2 (&x)[kQPieces] = xq[i];
             if constexpr (kCodes) {
                 const bool bf = p.dtype == TA_BF16;
-                float y[(NDC + 1) / 2][4];
+                float y[kQPieces][4];
                 uint32_t most = 0;
 #pragma unroll
-                for (int c = 0; c < (NDC + 1) / 2; ++c) {
+                for (int c = 0; c < kQPieces; ++c) {
                     const float2 a = bf ? tc::unpack2<true>(x[c].x) : tc::unpack2<false>(x[c].x);
                     const float2 b = bf ? tc::unpack2<true>(x[c].y) : tc::unpack2<false>(x[c].y);
                     y[c][0] = a.x, y[c][1] = a.y, y[c][2] = b.x, y[c][3] = b.y;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t e = __float_as_uint(y[c][i]) & 0x7fffffffu;
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t e = __float_as_uint(y[c][k]) & 0x7fffffffu;
                         if (e < 0x7f800000u) most = max(most, e);
                     }
                 }
@@ -381,13 +412,13 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                 const float up = __uint_as_float((254u - ex) << 23);
                 factor *= __uint_as_float(ex << 23);
 #pragma unroll
-                for (int c = 0; c < (NDC + 1) / 2; ++c) {
+                for (int c = 0; c < kQPieces; ++c) {
                     x[c].x = pack2<false>(y[c][0] * up, y[c][1] * up);
                     x[c].y = pack2<false>(y[c][2] * up, y[c][3] * up);
                 }
             }
 #pragma unroll
-            for (int c = 0; c < (NDC + 1) / 2; ++c) {
+            for (int c = 0; c < kQPieces; ++c) {
                 const int d = c * 128 + lane * 4, ch = d / 64, in = d % 64;
                 if (ch >= NDC) continue;
                 uint8_t* dst = sq + ((ch * 4 + in / 16) * NT + r / 8) * 256 + (r % 8) * 32;
@@ -401,6 +432,15 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
             }
             if (lane == 0) sqf[r] = factor;
         }
+    };
+    Unit un;
+    bool have = walk_next(p, w, un);
+    if (have) fetch_q(un);
+    while (have) {
+        u = un;
+        const long long head0 = (long long)u.h * p.G;
+        const int total_rows = u.q.n * p.G, row_first = u.rt * C::kRows;
+        put_q();
         // ---- This lane's columns of S^T and O^T: rows nt * 8 + 2 t and the next.
         int pos[NT][2];
 #pragma unroll
@@ -433,11 +473,15 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
             for (int i = 0; i < kSteps * NT; ++i) qr[i] = *reinterpret_cast<const uint2*>(sq + i * 256 + lane * 8);
         }
 
+        have = walk_next(p, w, un);
+        if (have) fetch_q(un);
+
         const int tiles = max(0, min(u.j1, u.t.nt) - u.j0);
-        // Blocks that a warp takes at once: half a stage's (twelve such pieces in a ring of six), or
-        // one where that leaves warps without work.
+        // Blocks that a warp takes at a time: half a stage's (twelve such pieces in a ring of six), or
+        // fewer where that leaves warps without work: two (whose products overlap), or one.
         constexpr int kTake = kBlocks / 2;
-        const int take = tiles * kBlocks >= 2 * kWarps * kTake ? kTake : 1;
+        const int blocks = tiles * kBlocks;
+        const int take = blocks >= 2 * kWarps * kTake ? kTake : (kTake >= 2 && blocks >= 2 * kWarps ? 2 : 1);
         const int grains = tiles * kBlocks / take;
         for (int gr = warp; gr < grains; gr += kWarps) {
             const int b_first = (gr * take) % kBlocks;
@@ -453,9 +497,10 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
             const bool plain_stage = valid == (1u << kBlocks) - 1u && stage_key0 + C::kSlots - 1 <= u.t.p0 &&
                                      (p.window <= 0 || u.t.p1 - stage_key0 < p.window || stage_key0 + C::kSlots <= p.sinks);
             const uint32_t stage = ring + (uint32_t)slot * C::kStage;
-            // One block: S^T, the softmax step, O^T.  PLAIN: every row sees every slot of it.
-            auto block = [&](auto plain_tag, int blk) {
+            // M blocks at once: S^T, the softmax step, O^T.  PLAIN: every row sees every slot of them.
+            auto block = [&](auto plain_tag, auto m_tag, int blk) {
                 constexpr bool PLAIN = decltype(plain_tag)::value;
+                constexpr int M = decltype(m_tag)::value;
                 const uint32_t kb = stage + (uint32_t)blk * 2048u, vb = kb + C::kBoxes * C::kBoxBytes;
                 const int key0 = stage_key0 + blk * 16;
                 if constexpr (!PLAIN) {
@@ -473,54 +518,71 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                 }
 
                 // ---- S^T
-                float s[NT][4];
+                float s[M][NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int mb = 0; mb < M; ++mb)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-                auto step = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[mb][nt][e] = 0.f;
+                auto step = [&](int mb, int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         uint2 b;
                         if constexpr (kKeepQ) b = qr[i * NT + nt];
                         else b = *reinterpret_cast<const uint2*>(sq + (i * NT + nt) * 256 + lane * 8);
-                        mma16816<kBF16>(s[nt], a0, a1, a2, a3, b);
+                        mma16816<kBF16>(s[mb][nt], a0, a1, a2, a3, b);
                     }
                 };
                 // (32 bytes of a row at a time: 16 columns, or 32 codes)
 #pragma unroll
                 for (int i = 0; i < (kCodes ? kSteps / 2 : kSteps); ++i) {
-                    uint32_t a[4];
-                    ldsm_x4(kb + (k_off ^ (32u * (i & 3))) + (i / 4) * C::kBoxBytes, a);
-                    if constexpr (kCodes) {
-                        step(2 * i, codes_f16(a[0]), codes_f16(a[1]), codes_f16_hi(a[0]), codes_f16_hi(a[1]));
-                        step(2 * i + 1, codes_f16(a[2]), codes_f16(a[3]), codes_f16_hi(a[2]), codes_f16_hi(a[3]));
-                    } else {
-                        step(i, a[0], a[1], a[2], a[3]);
+#pragma unroll
+                    for (int mb = 0; mb < M; ++mb) {
+                        uint32_t a[4];
+                        ldsm_x4(kb + mb * 2048u + (k_off ^ (32u * (i & 3))) + (i / 4) * C::kBoxBytes, a);
+                        if constexpr (kCodes) {
+                            step(mb, 2 * i, codes_f16(a[0]), codes_f16(a[1]), codes_f16_hi(a[0]), codes_f16_hi(a[1]));
+                            step(mb, 2 * i + 1, codes_f16(a[2]), codes_f16(a[3]), codes_f16_hi(a[2]), codes_f16_hi(a[3]));
+                        } else {
+                            step(mb, i, a[0], a[1], a[2], a[3]);
+                        }
                     }
                 }
                 // ---- Logits in base 2 (with the value scale's log2) less the reference: y = x - m.
-                const float4 sc = kCodes ? mt.sc[blk >> sub_shift] : make_float4(1.f, 0.f, 1.f, 0.f);
-                float y[NT][4], f[NT][2];
+                float4 sc[M];
+#pragma unroll
+                for (int mb = 0; mb < M; ++mb)
+                    sc[mb] = kCodes ? mt.sc[(blk + mb) >> sub_shift] : make_float4(1.f, 0.f, 1.f, 0.f);
+                float y[M][NT][4];
+                auto factor = [&](int mb, int nt, int e) { return kCodes ? qf[nt][e] * sc[mb].x : qf[nt][e]; };
                 bool grew = false;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) f[nt][e] = kCodes ? qf[nt][e] * sc.x : qf[nt][e];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[nt][e] = fmaf(s[nt][e], f[nt][e & 1], sc.y - m[nt][e & 1]);
-                }
-                if constexpr (!PLAIN) {
+                for (int mb = 0; mb < M; ++mb)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!sees(p, pos[nt][e & 1], key0 + (int)rg + (e & 2) * 4)) y[nt][e] = -INFINITY;
+                        for (int e = 0; e < 2; ++e) {
+                            const float f = factor(mb, nt, e), d = sc[mb].y - m[nt][e];
+                            y[mb][nt][e] = fmaf(s[mb][nt][e], f, d);
+                            y[mb][nt][e + 2] = fmaf(s[mb][nt][e + 2], f, d);
+                        }
+                if constexpr (!PLAIN) {
+#pragma unroll
+                    for (int mb = 0; mb < M; ++mb)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (!sees(p, pos[nt][e & 1], key0 + mb * 16 + (int)rg + (e & 2) * 4))
+                                    y[mb][nt][e] = -INFINITY;
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int mb = 0; mb < M; ++mb)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) grew = grew || fmaxf(y[nt][e], y[nt][e + 2]) > 8.f;
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) grew = grew || fmaxf(y[mb][nt][e], y[mb][nt][e + 2]) > 8.f;
                 if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -528,9 +590,14 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             // (the reference may be far off: x is formed from s again)
-                            const float x0 = y[nt][e] == -INFINITY ? -INFINITY : fmaf(s[nt][e], f[nt][e], sc.y);
-                            const float x1 = y[nt][e + 2] == -INFINITY ? -INFINITY : fmaf(s[nt][e + 2], f[nt][e], sc.y);
-                            float x = fmaxf(x0, x1);
+                            float x = -INFINITY;
+#pragma unroll
+                            for (int mb = 0; mb < M; ++mb)
+#pragma unroll
+                                for (int k = e; k < 4; k += 2) {
+                                    if (y[mb][nt][k] != -INFINITY) y[mb][nt][k] = fmaf(s[mb][nt][k], factor(mb, nt, e), sc[mb].y);
+                                    x = fmaxf(x, y[mb][nt][k]);
+                                }
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -538,8 +605,11 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                             al[e] = ex2(m[nt][e] - x);
                             m[nt][e] = x;
                             l[nt][e] *= al[e];
-                            y[nt][e] = x0 - x;
-                            y[nt][e + 2] = x1 - x;
+#pragma unroll
+                            for (int mb = 0; mb < M; ++mb) {
+                                y[mb][nt][e] -= x;
+                                y[mb][nt][e + 2] -= x;
+                            }
                         }
 #pragma unroll
                         for (int i = 0; i < NDC * 4; ++i)
@@ -548,49 +618,63 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                     }
                 }
                 // ---- P^T as the B operand, and O^T += V^T P^T.
-                uint2 b[NT];
+                uint2 b[M][NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float pr[4];
+                for (int mb = 0; mb < M; ++mb)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        pr[e] = ex2(y[nt][e]);
-                        if constexpr (kCodes) l[nt][e & 1] = fmaf(pr[e], sc.z, l[nt][e & 1]);
-                        else l[nt][e & 1] += pr[e];
-                    }
-                    b[nt].x = transpose8(pack2<kBF16>(pr[0], pr[1]));
-                    b[nt].y = transpose8(pack2<kBF16>(pr[2], pr[3]));
-                }
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float pr[4];
 #pragma unroll
-                for (int c = 0; c < NDC; ++c) {
-                    if constexpr (kCodes) {
-                        const uint32_t a0 = vb + (v_off0 ^ (64u * (c & 1))) + (c / 2) * C::kBoxBytes;
-                        const uint32_t a1 = vb + (v_off1 ^ (64u * (c & 1))) + (c / 2) * C::kBoxBytes;
-                        const uint2 w0 = lds64(a0), w1 = lds64(a1), w2 = lds64(a0 + 1024u), w3 = lds64(a1 + 1024u);
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            const uint32_t sel = (h & 1) ? 0x7362u : 0x5140u;
-                            const uint32_t x = __byte_perm(h < 2 ? w0.x : w0.y, h < 2 ? w1.x : w1.y, sel);
-                            const uint32_t z = __byte_perm(h < 2 ? w2.x : w2.y, h < 2 ? w3.x : w3.y, sel);
-                            const uint32_t f0 = codes_f16(x), f1 = codes_f16_hi(x), f2 = codes_f16(z), f3 = codes_f16_hi(z);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[c * 4 + h][nt], f0, f1, f2, f3, b[nt]);
+                        for (int e = 0; e < 4; ++e) {
+                            pr[e] = ex2(y[mb][nt][e]);
+                            if constexpr (kCodes) l[nt][e & 1] = fmaf(pr[e], sc[mb].z, l[nt][e & 1]);
+                            else l[nt][e & 1] += pr[e];
                         }
-                    } else {
+                        b[mb][nt].x = transpose8(pack2<kBF16>(pr[0], pr[1]));
+                        b[mb][nt].y = transpose8(pack2<kBF16>(pr[2], pr[3]));
+                    }
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            uint32_t a[4];
-                            ldsm_x4_t(vb + (v_offt ^ (32u * h)) + c * C::kBoxBytes, a);
+                for (int mb = 0; mb < M; ++mb)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma16816<kBF16>(o[c * 4 + h][nt], a[0], a[1], a[2], a[3], b[nt]);
+                    for (int c = 0; c < NDC; ++c) {
+                        const uint32_t vc = vb + mb * 2048u;
+                        if constexpr (kCodes) {
+                            const uint32_t a0 = vc + (v_off0 ^ (64u * (c & 1))) + (c / 2) * C::kBoxBytes;
+                            const uint32_t a1 = vc + (v_off1 ^ (64u * (c & 1))) + (c / 2) * C::kBoxBytes;
+                            const uint2 w0 = lds64(a0), w1 = lds64(a1), w2 = lds64(a0 + 1024u), w3 = lds64(a1 + 1024u);
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                const uint32_t sel = (h & 1) ? 0x7362u : 0x5140u;
+                                const uint32_t x = __byte_perm(h < 2 ? w0.x : w0.y, h < 2 ? w1.x : w1.y, sel);
+                                const uint32_t z = __byte_perm(h < 2 ? w2.x : w2.y, h < 2 ? w3.x : w3.y, sel);
+                                const uint32_t f0 = codes_f16(x), f1 = codes_f16_hi(x), f2 = codes_f16(z),
+                                               f3 = codes_f16_hi(z);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma16816<false>(o[c * 4 + h][nt], f0, f1, f2, f3, b[mb][nt]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                uint32_t a[4];
+                                ldsm_x4_t(vc + (v_offt ^ (32u * h)) + c * C::kBoxBytes, a);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma16816<kBF16>(o[c * 4 + h][nt], a[0], a[1], a[2], a[3], b[mb][nt]);
+                            }
                         }
                     }
-                }
             };
             if (plain_stage) {
+                // (two at a time where a warp has several: the one's products fill the other's waits)
+                constexpr int M = kTake >= 2 && NT <= 2 ? 2 : 1;
+                if (M == 1 || take == 1) {
 #pragma unroll 1
-                for (int blk = b_first; blk < b_first + take; ++blk) block(Yes{}, blk);
+                    for (int blk = b_first; blk < b_first + take; ++blk) block(Yes{}, Blocks<1>{}, blk);
+                } else {
+#pragma unroll 1
+                    for (int blk = b_first; blk < b_first + take; blk += M) block(Yes{}, Blocks<M>{}, blk);
+                }
             } else {
 #pragma unroll 1
                 for (int blk = b_first; blk < b_first + take; ++blk) {
@@ -598,7 +682,7 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                     // (a block that was not loaded, or that no row sees, is passed over)
                     if (((valid >> blk) & 1u) && key0 <= u.t.p1 &&
                         (p.window <= 0 || (long long)u.t.p0 - (key0 + 15) < p.window || key0 < p.sinks))
-                        block(No{}, blk);
+                        block(No{}, Blocks<1>{}, blk);
                 }
             }
             __syncwarp();
@@ -643,25 +727,42 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
             }
             srow[r] = make_float2(M, L);
         }
-        // element (d, row) of accumulator i2, nt: 8-bit d = 64 c + 8 g + 2 h (+ 1), 16-bit d = 64 c + 16 h + g (+ 8)
-        auto place = [&](int i2, int e) {
-            const int c = i2 / 4, h = i2 % 4;
-            return kCodes ? c * 64 + g * 8 + 2 * h + (e >> 1) : c * 64 + 16 * h + g + 8 * (e >> 1);
-        };
+        // element e of accumulator i2, nt: row nt * 8 + 2 t + (e & 1), column 64 c + 8 g + 2 h + (e >> 1) of 8-bit V,
+        // 64 c + 16 h + g + 8 (e >> 1) of 16-bit V (c = i2 / 4, h = i2 % 4)
 #pragma unroll 1
         for (int turn = (kWarps - 1) / C::kBufs; turn >= 0; --turn) {
             if (warp / C::kBufs == turn) {
                 float* dst = so + (warp % C::kBufs) * C::kRows * C::kOStride;
+                const bool first = warp + C::kBufs >= kWarps;  // of the warps that share the buffer
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i2 = 0; i2 < NDC * 4; ++i2)
+                    for (int e = 0; e < 2; ++e) {
+                        float* row = dst + (nt * 8 + 2 * t + e) * C::kOStride;
+                        const float ff = f[nt][e];
+                        if constexpr (kCodes) {  // eight neighbouring columns a chunk
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float* q = dst + (nt * 8 + 2 * t + (e & 1)) * C::kOStride + place(i2, e);
-                            const float v = o[i2][nt][e] * f[nt][e & 1];
-                            *q = warp + C::kBufs >= kWarps ? v : *q + v;
+                            for (int i2 = 0; i2 < NDC * 4; i2 += 2) {
+                                float4* q = reinterpret_cast<float4*>(row + (i2 / 4) * 64 + g * 8 + (i2 % 4) * 2);
+                                float4 v = make_float4(o[i2][nt][e] * ff, o[i2][nt][e + 2] * ff, o[i2 + 1][nt][e] * ff,
+                                                       o[i2 + 1][nt][e + 2] * ff);
+                                if (!first) {
+                                    const float4 x = *q;
+                                    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+                                }
+                                *q = v;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i2 = 0; i2 < NDC * 4; ++i2)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    float* q = row + (i2 / 4) * 64 + 16 * (i2 % 4) + g + 8 * k;
+                                    const float v = o[i2][nt][e + 2 * k] * ff;
+                                    *q = first ? v : *q + v;
+                                }
                         }
+                    }
             }
             consumers_sync();
         }

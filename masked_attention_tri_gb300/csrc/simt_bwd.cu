@@ -533,7 +533,7 @@ void bwd_sink_share(BwdParams& p) {
     // keep 152 SMs busy for total_q / 128 * H * (window / 128 + 2) / 152 of them.  Shared where the one
     // is not clearly below the other.  (8 sequences of 256 to 2048 tokens, 8 heads, window 512: 16
     // against 22; the backward 210 us, shared 271.  8192 + 4484 + 777 tokens, window 1024: 64 against
-    // 55; 505 us, shared SHARED_US.)
+    // 55; 505 us, shared 321.)
     const double rest = (double)p.total_q / 128 * p.H * ((double)p.window / 128 + 2) / 152;
     if ((double)nqb < 0.75 * rest) return;
     // (with a number of sinks for each sequence, the host knows none of them: the first block is shared)
