@@ -287,21 +287,47 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                 qb0 = first < nqb ? (int)first : nqb;
                 nqb = min(nqb, qb0 + P.sink_chunk);
             }
+            nqb = min(nqb, P.qcap);
+            // Rows of q block qb without any valid key (the forward gave them the mean of V).
+            auto unreached = [&](int qb) -> bool {
+                bool fm = false;
+#pragma unroll
+                for (int t = 0; t < kBM / 32; ++t) {
+                    const int q = qb * kBM + lane + 32 * t;
+                    if (q < Qn && P.lse[lrow0 + q] <= kMasked + 64.f) fm = true;
+                }
+                return __any_sync(0xffffffffu, fm) != 0;
+            };
             // Sink window without lists: q blocks without a kept (query, key) are left out.  Their
             // rows all have a valid key (their own, or a first one) unless there are more
-            // queries than keys and window reach.
+            // queries than keys and window reach.  A q block a lane: one at a time, 64 blocks took the
+            // warp some 15 us, more than the tiles of a short window.
             const bool sunk = !P.kv_num && P.mask_mod == TA_MASK_SINK_WINDOW;
-            const bool all_valid = prefix > 0 || (long long)Qn - Kn < P.window;
-            for (int qb = qb0; qb < nqb && qb < P.qcap; ++qb) {
-                int st = 1;  // no lists: every block partial
-                if (sunk) {
-                    const SinkBlocks sb = sink_blocks(qb * kBM, min(qb * kBM + kBM, Qn) - 1, Kn, P.window, prefix);
-                    st = sb.visited(kb) ? 1 : 0;
-                    if (st == 0 && all_valid) continue;
-                    // a shared key block: its own CTA leaves the far q blocks to the chunks
-                    const bool is_far = st == 1 && !(kb >= sb.lo && kb <= sb.hi);
-                    if (shared_kb && is_far != (far >= 0)) continue;
+            if (sunk) {
+                const bool all_valid = prefix > 0 || (long long)Qn - Kn < P.window;
+                if (all_valid) qb0 = max(qb0, kb * kBN / kBM);  // (earlier q blocks see no key of this block)
+                for (int q32 = qb0; q32 < nqb; q32 += 32) {
+                    const int qb = q32 + lane;
+                    int st = -1;  // not visited
+                    if (qb < nqb) {
+                        const SinkBlocks sb = sink_blocks(qb * kBM, min(qb * kBM + kBM, Qn) - 1, Kn, P.window, prefix);
+                        st = sb.visited(kb) ? 1 : 0;
+                        // a shared key block: its own CTA leaves the far q blocks to the chunks
+                        const bool is_far = st == 1 && !(kb >= sb.lo && kb <= sb.hi);
+                        if ((st == 0 && all_valid) || (shared_kb && is_far != (far >= 0))) st = -1;
+                    }
+                    for (uint32_t look = __ballot_sync(0xffffffffu, st == 0); look; look &= look - 1) {
+                        const int i = __ffs(look) - 1;
+                        const bool fm = unreached(q32 + i);
+                        if (lane == i) st = fm ? 3 : -1;
+                    }
+                    const uint32_t in = __ballot_sync(0xffffffffu, st > 0);
+                    if (st > 0) qw[cnt + __popc(in & ((1u << lane) - 1u))] = (uint32_t)qb | ((uint32_t)st << 24);
+                    cnt += __popc(in);
                 }
+            }
+            for (int qb = qb0; qb < nqb && !sunk; ++qb) {
+                int st = 1;  // no lists: every block partial
                 if (P.kv_num) {
                     int f = 0;
                     if (qb < P.MQ) {
@@ -318,15 +344,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                     }
                     st = (int)__reduce_max_sync(0xffffffffu, (unsigned)f);  // full before partial
                 }
-                if (st == 0) {  // not listed: visited only for rows with no valid key
-                    bool fm = false;
-#pragma unroll
-                    for (int t = 0; t < kBM / 32; ++t) {
-                        const int q = qb * kBM + lane + 32 * t;
-                        if (q < Qn && P.lse[lrow0 + q] <= kMasked + 64.f) fm = true;
-                    }
-                    if (__any_sync(0xffffffffu, fm)) st = 3;
-                }
+                if (st == 0 && unreached(qb)) st = 3;  // not listed: visited only for rows with no valid key
                 if (st != 0) {
                     if (lane == 0) qw[cnt] = (uint32_t)qb | ((uint32_t)st << 24);
                     ++cnt;
