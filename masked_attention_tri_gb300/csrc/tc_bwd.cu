@@ -142,6 +142,13 @@ __device__ __forceinline__ float bwd_weight(float x, float lse, float inv_k) {
     return lse <= kMasked + 64.f ? inv_k : __expf(x - lse);
 }
 
+struct BwdYes {
+    static constexpr bool value = true;
+};
+struct BwdNo {
+    static constexpr bool value = false;
+};
+
 // Warps 0-15 compute (four per TMEM lane quarter), warp 16 loads, warp 17 issues the MMAs.
 constexpr int kComputeWarps = 16;
 constexpr int kQuarterWarps = kComputeWarps / 4;  // compute warps per TMEM lane quarter
@@ -160,6 +167,14 @@ __device__ __forceinline__ bool bwd_mod_keep(int mod, int q, int k, int window, 
     case TA_MASK_SINK_WINDOW: return k <= q && (k > q - window || k < prefix);
     default: return true;
     }
+}
+
+// Sink window: which of the queries q, q + 1, ..., q + 15 keep key k, as bits.
+__device__ __forceinline__ uint32_t bwd_sink_bits(int q, int k, int window, int prefix) {
+    const int from = min(max(k - q, 0), 16);  // the first query at or past k
+    const long long reach = k < prefix ? 16LL : (long long)k - q + window;
+    const int to = (int)min(max(reach, 0LL), 16LL);
+    return (0xffffu << from) & ((1u << to) - 1u);
 }
 
 // WIDE: D in (64, 128] (two 64-column boxes per tile, one S^T / dP^T buffer that the query
@@ -775,9 +790,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                         default: whole = false;
                         }
                     }
-                    if (__all_sync(0xffffffffu, valid) && nq >= CW && whole) {
-                        // Every key of the warp valid and every query of the chunk present: each row
-                        // has a valid key, so its lse is a plain log-sum-exp and P = 2^(x log2e - lse log2e).
+                    // Each row has a valid key, so its lse is a plain log-sum-exp and P = 2^(x log2e - lse log2e);
+                    // MASKED: P and dS are 0 where the query's bit is not set.
+                    auto plain = [&](auto masked_tag, uint32_t bits) {
+                        constexpr bool MASKED = decltype(masked_tag)::value;
                         const float2 sl2 = make_float2(P.scale * kLog2e, P.scale * kLog2e);
                         const float2 l2e2 = make_float2(kLog2e, kLog2e);
                         float* dbp = dbias_row ? dbias_row + (long long)(q0 + ql) * bst : nullptr;
@@ -799,17 +815,37 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                             const float2 nl = __fmul2_rn(make_float2(ls[i], ls[i + 1]), make_float2(-kLog2e, -kLog2e));
                             const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])),
                                                         sl2, __ffma2_rn(bv, l2e2, nl));
-                            const float2 pr = make_float2(ex2(y.x), ex2(y.y));
-                            const float2 ds = __fmul2_rn(
+                            float2 pr = make_float2(ex2(y.x), ex2(y.y));
+                            float2 ds = __fmul2_rn(
                                 pr, __fadd2_rn(make_float2(__uint_as_float(dr[i]), __uint_as_float(dr[i + 1])),
                                                make_float2(-dl[i], -dl[i + 1])));
+                            if constexpr (MASKED) {
+                                const bool u0 = (bits >> i) & 1u, u1 = (bits >> (i + 1)) & 1u;
+                                pr = make_float2(u0 ? pr.x : 0.f, u1 ? pr.y : 0.f);
+                                ds = make_float2(u0 ? ds.x : 0.f, u1 ? ds.y : 0.f);
+                            }
                             pp[i / 2] = pack2<BF16>(pr.x, pr.y);
                             dd[i / 2] = pack2<BF16>(ds.x, ds.y);
                             if (dbp) {
-                                red_add_global(dbp + (long long)i * bst, ds.x);
-                                red_add_global(dbp + (long long)(i + 1) * bst, ds.y);
+                                if (!MASKED || ((bits >> i) & 1u)) red_add_global(dbp + (long long)i * bst, ds.x);
+                                if (!MASKED || ((bits >> (i + 1)) & 1u)) red_add_global(dbp + (long long)(i + 1) * bst, ds.y);
                             }
                         }
+                    };
+                    // Sink window, a block on an edge of the mask: the same, with the bits of the kept queries.
+                    // (The branch below takes 12k cycles a tile, this 4k.  The other masks keep their
+                    // arithmetic to the bit.)
+                    bool edge = false;
+                    if (VARLEN && tst == 1 && P.mask_mod == TA_MASK_SINK_WINDOW) {
+                        edge = true;
+#pragma unroll
+                        for (int i = 0; i < CW; ++i) edge = edge && ls[i] > kMasked + 64.f;
+                    }
+                    if (__all_sync(0xffffffffu, valid) && nq >= CW && whole) {
+                        plain(BwdNo{}, 0u);
+                    } else if (edge) {
+                        const uint32_t there = nq >= CW ? 0xffffu : (nq > 0 ? (1u << nq) - 1u : 0u);
+                        plain(BwdYes{}, valid ? bwd_sink_bits(q0 + ql, key, P.window, prefix) & there : 0u);
                     } else {
                         // Logits first (every read of the bias tile before any reduction into dBias).
                         // Packed form: bit ii of vm = query ql + ii and this key valid (the block's
