@@ -822,8 +822,10 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tc_split_kernel(const __grid
         qc.walk.begin(P, ring);
         qc.qi = 0;
         bool has_q = split_seek<VARLEN>(P, ring, qc);
-        pc = qc;
-        bool has_p = has_q;
+        // (sought like qc, not copied: each cursor hands every ring entry back)
+        pc.walk.begin(P, ring);
+        pc.qi = 0;
+        bool has_p = split_seek<VARLEN>(P, ring, pc);
         uint32_t np = 0;                                    // PV issued so far
         StageRing qr = {0, 0u, false};                      // Q buffer of qc's item
         StageRing kq = {0, 0u, false}, sq = {0, 0u, false};  // K stage / S buffer of the next QK^T

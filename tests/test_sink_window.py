@@ -259,6 +259,20 @@ def test_many_sequences():
 
 
 @pytest.mark.gpu
+def test_many_items_of_a_cta():
+    """6400 (sequence, head, q block) items, some forty for each CTA: the ring of items goes round several times."""
+    import masked_attention_tri_gb300 as ta
+    lens, H = [1 + (i * 7) % 40 for i in range(100)], 64
+    q, k, v, g = _problem(lens, lens, H, 32, B16, seed=2)
+    _check(_run(q, k, v, g, lens, lens, 8, 2, 0.2), _dense(q, k, v, g, lens, lens, 8, 2, 0.2, B16))
+    cu = _i32(_cu(lens))
+    o, lse, _ = ta.varlen_attention(q.cuda(), k.cuda(), v.cuda(), cu, cu, 40, 40, scale=0.2, mask_mod="causal", return_aux=True)
+    torch.cuda.synchronize()
+    assert ta.get_status() == 0
+    _check({"out": o, "lse": lse}, _dense(q, k, v, g, lens, lens, 1000, 0, 0.2, B16), ("out", "lse"))
+
+
+@pytest.mark.gpu
 def test_bias_and_strided_rows():
     import masked_attention_tri_gb300 as ta
     lens = [300, 129]
