@@ -531,11 +531,12 @@ void bwd_sink_share(BwdParams& p) {
     if (far <= chunk) return;
     // The first key block's CTA is issued first and walks nqb q blocks; the others, window / 128 + 2 each,
     // keep 152 SMs busy for total_q / 128 * H * (window / 128 + 2) / 152 of them.  Shared where the one
-    // is not clearly below the other.  (8 sequences of 256 to 2048 tokens, 8 heads, window 512: 16
-    // against 22; the backward 210 us, shared 271.  8192 + 4484 + 777 tokens, window 1024: 64 against
-    // 55; 505 us, shared 321.)
+    // is longer than the other.  (8 heads of 64; q blocks of the longest against that number, the backward
+    // unshared and shared: 8 sequences of 256 to 2048 tokens, window 512: 16 to 22, 95 and 104 us; 4 of 4096,
+    // window 512: 32 to 40, 173 and 179; 8192 + 4484 + 777, window 1024: 64 to 55, 216 and 204; 2 of 8192,
+    // window 256: 64 to 27, 220 and 154.)
     const double rest = (double)p.total_q / 128 * p.H * ((double)p.window / 128 + 2) / 152;
-    if ((double)nqb < 0.75 * rest) return;
+    if ((double)nqb < rest) return;
     // (with a number of sinks for each sequence, the host knows none of them: the first block is shared)
     const long long nb = p.prefix_len ? 1 : ((long long)p.prefix_all + 127) / 128, nkb = ((long long)p.max_k + 127) / 128;
     if (nb > 4) return;  // (many key blocks see everything: they balance one another)

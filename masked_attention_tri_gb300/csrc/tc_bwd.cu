@@ -44,7 +44,7 @@
 // it, those key blocks are shared: their own CTA takes the q blocks in reach and further CTAs, issued
 // first, the far ones, eight at a time; all add dK and dV to an fp32 accumulator, which the
 // last kernel converts.  (Packed sequences of 777, 4484 and 8192 tokens, 8 heads of 64, window
-// 1024, 4 sinks: the backward 505 -> 321 us.)
+// 1024, 4 sinks: the backward 216 us unshared, 204 shared; two of 8192, window 256: 220 and 154.)
 
 #include "tc_kernel.cuh"
 
@@ -93,7 +93,8 @@ struct BwdTc {
 };
 
 // Shared memory (offsets from a 1024-byte aligned base).
-// Stage s of the query-tile ring: Q at q + s * 2 tile, dO after it; lse / delta at lse + s * 1024
+// Stage s of the query-tile ring: Q at q + s * 2 tile, dO after it; the rows' -lse log2e, -delta and lse
+// (128 floats each) at lse + s * bwd_row_bytes
 // (tile = nsub boxes of 128 rows x 128 bytes).
 struct BwdLayout {
     uint32_t k, v, q, ds, bias, dqst, lse, qlist, bars, tmem_slot, abort_flag, qn, total;
@@ -101,6 +102,8 @@ struct BwdLayout {
 // kv_full, q_full[2], q_empty[2], lse_full[2], bias_full[2], bias_empty[2], s_full[2], p_full[2],
 // dq_full, dq_empty, ds_free, fin, drain
 constexpr int kBwdBars = 20;
+// An fp32 bias with D > 64 leaves no room for the lse row: it is read from global memory where it is needed.
+__host__ __device__ inline uint32_t bwd_row_bytes(bool alias) { return (alias ? 2u : 3u) * kBM * 4; }
 // nsub: the kernel passes its compile-time box count, so that the offsets fold into constants.
 __host__ __device__ inline BwdLayout bwd_layout(const BwdTc& P, int nsub) {
     BwdLayout L;
@@ -112,7 +115,7 @@ __host__ __device__ inline BwdLayout bwd_layout(const BwdTc& P, int nsub) {
     L.bias = L.ds + 2 * kBox;
     L.dqst = L.bias + (P.bias_alias ? P.bias_bytes / 2u : P.bias_bytes);  // dQ staging: 16 warps x 32 rows x 16 fp32
     L.lse = L.dqst + 16u * 2048u;
-    L.qlist = L.lse + (uint32_t)P.qs * 1024u;  // packed form: the q blocks the key tile visits
+    L.qlist = L.lse + (uint32_t)P.qs * bwd_row_bytes(P.bias_alias != 0);  // packed form: the q blocks the key tile visits
     L.bars = L.qlist + (((uint32_t)P.qcap * 4u + 15u) & ~15u);
     L.tmem_slot = L.bars + 8 * kBwdBars;
     L.abort_flag = L.tmem_slot + 4;
@@ -140,6 +143,20 @@ __device__ __forceinline__ float bwd_weight(float x, float lse, float inv_k) {
     // A row with every key masked has lse -1e9 in fp32 (its -1e9 + ln K rounds
     // there); its weights are 1 / K.  Any row with a valid key has lse above -1e9 + 100.
     return lse <= kMasked + 64.f ? inv_k : __expf(x - lse);
+}
+
+// Sixteen columns of each of two TMEM addresses, one wait for both.
+__device__ __forceinline__ void tmem_ld_2x16(uint32_t ta, uint32_t tb, uint32_t (&a)[16], uint32_t (&b)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]),
+          "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(b[0]),
+          "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]),
+          "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
+        : "r"(ta), "r"(tb)
+        : "memory");
 }
 
 struct BwdYes {
@@ -380,6 +397,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
             return;
         }
     }
+    // the stage of tile j and how often the ring has gone round (one or two stages)
+    auto stage_of = [&](int j) -> int { return j & (P.qs - 1); };
+    auto use_of = [&](int j) -> int { return j >> (P.qs - 1); };
     // the first query row (within the unit) and the status of entry j of the tile walk
     auto tile_q0 = [&](int j) -> int {
         if constexpr (VARLEN) return (int)(qlist[j] & 0xffffffu) * kBM;
@@ -442,7 +462,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
             }
         }
         for (int j = 0; j < nqt && ok; ++j) {
-            const int q0 = tile_q0(j), st = j % P.qs, use = j / P.qs;
+            const int q0 = tile_q0(j), st = stage_of(j), use = use_of(j);
             // This tile's Q / dO, bias half 0 (as soon as the compute warps have read half 0 of
             // tile j - 1), the rows' lse / delta, then bias half 1.  One shared slot (kAlias):
             // half 0 once half 1 of tile j - 1 is read, half 1 once half 0 of this tile is.
@@ -520,12 +540,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                     dv[t] = q < Qn ? P.delta[lrow0 + q] : 0.f;
                 }
             }
-            float* lse_s = reinterpret_cast<float*>(gbase + L.lse + (uint32_t)st * 1024u);
-            float* del_s = lse_s + 128;
+            // (the factor and the signs here, once a row, and not once an element)
+            float* nl_s = reinterpret_cast<float*>(gbase + L.lse + (uint32_t)st * bwd_row_bytes(kAlias));
 #pragma unroll
             for (int t = 0; t < kBM / 32; ++t) {
-                lse_s[lane + 32 * t] = lv[t];
-                del_s[lane + 32 * t] = dv[t];
+                nl_s[lane + 32 * t] = lv[t] * -kLog2e;
+                nl_s[kBM + lane + 32 * t] = -dv[t];
+                if constexpr (!kAlias) nl_s[2 * kBM + lane + 32 * t] = lv[t];
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(lse_full(st));  // release: the rows are written
@@ -545,10 +566,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
         const uint64_t kK = sw128_desc(base + L.k, 16, 1024), vK = sw128_desc(base + L.v, 16, 1024);
         const uint64_t kM = sw128_desc(base + L.k, kBox, 1024), dsM = sw128_desc(base + L.ds, kBox, 1024);
         auto mma1 = [&](int j, int hh) -> bool {
-            const int st = j % P.qs;
+            const int st = stage_of(j);
             if (WIDE || hh == 0) {  // WIDE: each half's rows have their own barrier
                 const uint32_t qb = WIDE ? q_full(hh) : q_full(st);
-                if (!__all_sync(0xffffffffu, wait_bar(qb, (uint32_t)(j / P.qs) & 1u, abort_flag, P.status)))
+                if (!__all_sync(0xffffffffu, wait_bar(qb, (uint32_t)use_of(j) & 1u, abort_flag, P.status)))
                     return false;
                 tc_fence_after();
             }
@@ -587,7 +608,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
         };
         if (ok && nqt > 0) ok = WIDE ? mma1(0, 0) : (mma1(0, 0) && mma1(0, 1));
         for (int j = 0; j < nqt && ok; ++j) {
-            const int st = j % P.qs;
+            const int st = stage_of(j);
             const uint64_t qM = sw128_desc(q_smem(st), kBox, 1024), doM = sw128_desc(do_smem(st), kBox, 1024);
             for (int hh = 0; hh < 2 && ok; ++hh) {
                 const uint32_t b = (uint32_t)buf(hh);
@@ -736,10 +757,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
         bool ok = true;
         for (int j = 0; j < nqt && ok; ++j) {
             const uint32_t ph = (uint32_t)j & 1u;
-            const int q0 = tile_q0(j), st = j % P.qs, tst = tile_st(j);
-            const float* lse_s = reinterpret_cast<const float*>(gbase + L.lse + (uint32_t)st * 1024u);
-            const float* del_s = lse_s + 128;
-            ok = __all_sync(0xffffffffu, wait_bar(lse_full(st), (uint32_t)(j / P.qs) & 1u, abort_flag, P.status));
+            const int q0 = tile_q0(j), st = stage_of(j), tst = tile_st(j);
+            const float* nl_s = reinterpret_cast<const float*>(gbase + L.lse + (uint32_t)st * bwd_row_bytes(kAlias));
+            const float* nd_s = nl_s + kBM;
+            const float* lse_s = nl_s + 2 * kBM;
+            ok = __all_sync(0xffffffffu, wait_bar(lse_full(st), (uint32_t)use_of(j) & 1u, abort_flag, P.status));
             if (!ok) break;
             for (int hh = 0; hh < 2 && ok; ++hh) {
                 if (hasb) {
@@ -759,17 +781,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                     const int ql = 64 * hh + kWarpQ * hq + CW * c;
                     const uint32_t col = (uint32_t)(kWarpQ * hq + CW * c);
                     uint32_t sr[CW], dr[CW];
-                    tmem_ld_x16(tSh + lane_off + col, sr);
-                    tmem_ld_x16(tDPh + lane_off + col, dr);
-                    // The chunk's lse and delta (shared-memory broadcasts, four at a time) and this
+                    tmem_ld_2x16(tSh + lane_off + col, tDPh + lane_off + col, sr, dr);
+                    // The chunk's -lse log2e and -delta (shared-memory broadcasts, four at a time) and this
                     // key's bias column: query row ql + i lives at bcb + 128 i + xo[i % 8].
-                    float ls[CW], dl[CW];
+                    float2 nl[CW / 2], nd[CW / 2];
 #pragma unroll
                     for (int i = 0; i < CW; i += 4) {
-                        const float4 l4 = *reinterpret_cast<const float4*>(lse_s + ql + i);
-                        const float4 d4 = *reinterpret_cast<const float4*>(del_s + ql + i);
-                        ls[i] = l4.x, ls[i + 1] = l4.y, ls[i + 2] = l4.z, ls[i + 3] = l4.w;
-                        dl[i] = d4.x, dl[i + 1] = d4.y, dl[i + 2] = d4.z, dl[i + 3] = d4.w;
+                        const float4 l4 = *reinterpret_cast<const float4*>(nl_s + ql + i);
+                        const float4 d4 = *reinterpret_cast<const float4*>(nd_s + ql + i);
+                        nl[i / 2] = make_float2(l4.x, l4.y), nl[i / 2 + 1] = make_float2(l4.z, l4.w);
+                        nd[i / 2] = make_float2(d4.x, d4.y), nd[i / 2 + 1] = make_float2(d4.z, d4.w);
                     }
                     const uint8_t* bcb = gbase + (bias_half(hh) - base) + bbox_off + (uint32_t)(ql - 64 * hh) * 128u;
                     const int nq = Qn - (q0 + ql);  // queries of the chunk that exist
@@ -812,13 +833,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                                 bv = unpack2<BF16>(b0 | (b1 << 16));
                             }
                             // y = s S log2e + b log2e - lse log2e
-                            const float2 nl = __fmul2_rn(make_float2(ls[i], ls[i + 1]), make_float2(-kLog2e, -kLog2e));
                             const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])),
-                                                        sl2, __ffma2_rn(bv, l2e2, nl));
+                                                        sl2, hasb ? __ffma2_rn(bv, l2e2, nl[i / 2]) : nl[i / 2]);
                             float2 pr = make_float2(ex2(y.x), ex2(y.y));
                             float2 ds = __fmul2_rn(
-                                pr, __fadd2_rn(make_float2(__uint_as_float(dr[i]), __uint_as_float(dr[i + 1])),
-                                               make_float2(-dl[i], -dl[i + 1])));
+                                pr, __fadd2_rn(make_float2(__uint_as_float(dr[i]), __uint_as_float(dr[i + 1])), nd[i / 2]));
                             if constexpr (MASKED) {
                                 const bool u0 = (bits >> i) & 1u, u1 = (bits >> (i + 1)) & 1u;
                                 pr = make_float2(u0 ? pr.x : 0.f, u1 ? pr.y : 0.f);
@@ -835,13 +854,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                     // Sink window, a block on an edge of the mask: the same, with the bits of the kept queries.
                     // (The branch below takes 12k cycles a tile, this 4k.  The other masks keep their
                     // arithmetic to the bit.)
+                    const bool all = __all_sync(0xffffffffu, valid) && nq >= CW && whole;
                     bool edge = false;
-                    if (VARLEN && tst == 1 && P.mask_mod == TA_MASK_SINK_WINDOW) {
-                        edge = true;
+                    if (VARLEN && !all && tst == 1 && P.mask_mod == TA_MASK_SINK_WINDOW) {
+                        float most = nl[0].x;
 #pragma unroll
-                        for (int i = 0; i < CW; ++i) edge = edge && ls[i] > kMasked + 64.f;
+                        for (int i = 0; i < CW / 2; ++i) most = fmaxf(most, fmaxf(nl[i].x, nl[i].y));
+                        edge = most < (kMasked + 64.f) * -kLog2e;  // every row has a valid key
                     }
-                    if (__all_sync(0xffffffffu, valid) && nq >= CW && whole) {
+                    if (all) {
                         plain(BwdNo{}, 0u);
                     } else if (edge) {
                         const uint32_t there = nq >= CW ? 0xffffu : (nq > 0 ? (1u << nq) - 1u : 0u);
@@ -885,8 +906,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                                 const int ii = i + u;
                                 const bool live = exists && ii < nq;
                                 const bool ve = VARLEN ? ((vm >> ii) & 1u) != 0u : valid;
-                                const float p = live ? bwd_weight(__uint_as_float(sr[ii]), ls[ii], inv_k) : 0.f;
-                                const float ds = (live && ve) ? p * (__uint_as_float(dr[ii]) - dl[ii]) : 0.f;
+                                float row_lse = 0.f;
+                                if constexpr (!kAlias) row_lse = lse_s[ql + ii];
+                                else if (live) row_lse = P.lse[lrow0 + q0 + ql + ii];
+                                const float p = live ? bwd_weight(__uint_as_float(sr[ii]), row_lse, inv_k) : 0.f;
+                                const float ds = (live && ve) ? p * (__uint_as_float(dr[ii]) + (u ? nd[i / 2].y : nd[i / 2].x)) : 0.f;
                                 pv[u] = p;
                                 sv[u] = ds;
                                 dr[ii] = __float_as_uint(ds);
@@ -1042,7 +1066,7 @@ cudaError_t launch_tc_bwd_main(const BwdParams& p, cudaStream_t stream) {
     P.bias_box_cols = p.bias_f32 ? 32 : 64;
     P.bias_boxes = kBN / P.bias_box_cols;
     P.bias_bytes = (uint32_t)P.bias_boxes * kBox;
-    P.bias_alias = D > 64 && p.bias_f32 ? 1 : 0;
+    P.bias_alias = D > 64 && p.bias && p.bias_f32 ? 1 : 0;
     const uint64_t eb = p.bias_f32 ? 4 : 2;
     const int qbox = D > 64 ? kBM / 2 : kBM;  // D > 64: Q / dO rows loaded per query half
     const bool vl = p.varlen != 0;
