@@ -434,6 +434,11 @@ def _mask_args(block_mask, mask_mod, dev):
     return kn, ki, fn, fi, mask_heads, MQ, MK, bq, bk, mm
 
 
+def _int32(n):
+    """A count as the C ABI takes it: one beyond int32 means all there is."""
+    return max(-2 ** 31, min(int(n), 2 ** 31 - 1))
+
+
 def _prefix_args(prefix_lengths, S, dev, mm=None, sinks=None):
     """(per-sequence tensor or None, one length for all): the prefix of the prefix-LM mask_mod, or
     the first keys that stay visible under the sink window."""
@@ -451,7 +456,7 @@ def _prefix_args(prefix_lengths, S, dev, mm=None, sinks=None):
         if prefix_lengths.dtype != torch.int32 or prefix_lengths.numel() != S:
             raise ValueError("prefix_lengths (sinks) must be int32 with one entry per sequence")
         return prefix_lengths, 0
-    return None, (0 if prefix_lengths is None else int(prefix_lengths))
+    return None, (0 if prefix_lengths is None else _int32(prefix_lengths))
 
 
 def varlen_attention(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, block_mask=None, scale=None,
@@ -511,11 +516,12 @@ def varlen_attention(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seql
         if bias.dtype not in (torch.float32, q.dtype):
             raise TypeError("bias must be float32 or q's dtype")
     pl, p_all = _prefix_args(prefix_lengths, S, dev, mm, sinks)
+    window = _int32(window)
     with _on(dev):
         abi.tri_attn_varlen_fwd_masked(_ptr(q), _ptr(k), _ptr(v), _DT[q.dtype], _ptr(cu_seqlens_q),
                                        _ptr(cu_seqlens_k), S, total_q, k.shape[0], int(max_seqlen_q),
                                        int(max_seqlen_k), H, D, s, _ptr(kn), _ptr(ki), _ptr(fn), _ptr(fi),
-                                       mask_heads, MQ, MK, bq, bk, mm, int(window), _ptr(pl), p_all, _ptr(bias),
+                                       mask_heads, MQ, MK, bq, bk, mm, window, _ptr(pl), p_all, _ptr(bias),
                                        _DT[bias.dtype] if bias is not None else abi.TA_F32, q_rs, k_rs, v_rs,
                                        _ptr(out), _ptr(lse), _ptr(mx), _stream(dev))
     return (out, lse, mx) if return_aux else out
@@ -580,6 +586,7 @@ def varlen_attention_backward(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
     s = 1.0 / math.sqrt(D) if scale is None else float(scale)
     kn, ki, fn, fi, mask_heads, MQ, MK, bq, bk, mm = _mask_args(block_mask, mask_mod, dev)
     pl, p_all = _prefix_args(prefix_lengths, S, dev, mm, sinks)
+    window = _int32(window)
     if bias is not None:
         _need(bias, "bias", dev)
         if tuple(bias.shape) != (H, int(max_seqlen_q), int(max_seqlen_k)):
@@ -590,7 +597,7 @@ def varlen_attention_backward(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
     dbias = torch.empty_like(bias) if (bias is not None and need_dbias) else None
     if mm == abi.TA_MASK_SINK_WINDOW and kn is None:
         nbytes = abi.tri_attn_varlen_bwd_sink_workspace_size(S, total_q, H, D, int(max_seqlen_q), int(max_seqlen_k),
-                                                             dbias is not None, int(window), -1 if pl is not None else p_all)
+                                                             dbias is not None, window, -1 if pl is not None else p_all)
     else:
         nbytes = abi.tri_attn_varlen_bwd_workspace_size(total_q, H, D, int(max_seqlen_q), int(max_seqlen_k),
                                                         dbias is not None)
@@ -598,7 +605,7 @@ def varlen_attention_backward(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
     with _on(dev):
         abi.tri_attn_varlen_bwd(_ptr(q), _ptr(k), _ptr(v), _DT[q.dtype], _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), S,
                                 total_q, k.shape[0], int(max_seqlen_q), int(max_seqlen_k), H, D, s, _ptr(kn),
-                                _ptr(ki), _ptr(fn), _ptr(fi), mask_heads, MQ, MK, bq, bk, mm, int(window),
+                                _ptr(ki), _ptr(fn), _ptr(fi), mask_heads, MQ, MK, bq, bk, mm, window,
                                 _ptr(pl), p_all, _ptr(bias), _DT[bias.dtype] if bias is not None else abi.TA_F32,
                                 _ptr(lse), _ptr(out), _ptr(d_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbias),
                                 _ptr(ws), nbytes, _stream(dev))

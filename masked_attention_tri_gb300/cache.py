@@ -12,7 +12,7 @@ from typing import Optional
 import torch
 
 from . import abi
-from .api import _DT, _check_out, _need, _on, _ptr, _row_stride, _stream
+from .api import _DT, _check_out, _int32, _need, _on, _ptr, _row_stride, _stream
 from .positions import Rotary, _check_rotary
 
 _CACHE_DT = {**_DT, torch.float8_e4m3fn: abi.TA_E4M3}
@@ -101,8 +101,8 @@ def kv_cache_append(cache: PagedKVCache, k, v, page_table, kv_lengths, cu_seqlen
     max_seqlen each; none is fine; rows past its last entry are left alone); without it
     row i belongs to sequence i.  kv_lengths (S,) int32 counts the slots that a
     sequence holds after this call: the new rows are the last of them.
-    page_table (S, max_pages) int32; a page that is written belongs to one sequence
-    of the call.  rotary turns k, and q (total, Hq, D) if given, by each row's slot or
+    page_table (S, max_pages) int32; a page that is written has one place in the
+    tables of the call.  rotary turns k, and q (total, Hq, D) if given, by each row's slot or
     by positions (total,) int32.  Returns the turned q (out_q, which may be q), or None.
 
     An 8-bit cache takes a power-of-two scale for each (page, head): rows that need
@@ -217,7 +217,7 @@ def paged_attention(q, cache: PagedKVCache, page_table, kv_lengths, cu_seqlens_q
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         with _on(dev):
             abi.tri_attn_paged_fwd(_ptr(q), code, _ptr(cu_seqlens_q), _ptr(kv_lengths), _ptr(page_table), S, total,
-                                   max_seqlen_q, Hq, Hk, D, q_rs, s, 0 if window is None else int(window), int(sinks),
+                                   max_seqlen_q, Hq, Hk, D, q_rs, s, 0 if window is None else _int32(window), _int32(sinks),
                                    _ptr(cache.k), _ptr(cache.v), cache._code, _ptr(cache.k_scale), _ptr(cache.v_scale),
                                    cache.num_pages, cache.page_size, MP, cache._strides[0], cache._strides[1],
                                    _ptr(out), _ptr(lse), _ptr(ws), nbytes, _stream(dev))

@@ -39,6 +39,11 @@ ta_status cache_strides(const long long* given, int num_pages, int Hk, int page,
     return TA_OK;
 }
 
+// A launch whose grid would pass the hardware's limits (odd head counts in the ten thousands) is refused.
+ta_status launched(cudaError_t e) {
+    return e == cudaSuccess ? TA_OK : e == cudaErrorInvalidConfiguration ? TA_ERR_UNSUPPORTED : TA_ERR_CUDA;
+}
+
 // What the two operators on a paged cache check alike.
 ta_status check_cache(const void* k_cache, const void* v_cache, int dtype, int cache_dtype, const float* k_scale,
                       const float* v_scale, int num_pages, int page_size, int max_pages, int Hk, int D,
@@ -104,7 +109,7 @@ TA_EXPORT ta_status tri_attn_rotary(const void* q, const void* k, ta_dtype dtype
     p.k_rs = k_row_stride;
     p.qo_rs = q_out_row_stride;
     p.ko_rs = k_out_row_stride;
-    return launch_rotary(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TA_OK : TA_ERR_CUDA;
+    return launched(launch_rotary(p, static_cast<cudaStream_t>(stream)));
 }
 
 TA_EXPORT ta_status tri_attn_kv_append(const void* q, const void* k, const void* v, ta_dtype dtype,
@@ -176,7 +181,7 @@ TA_EXPORT ta_status tri_attn_kv_append(const void* q, const void* k, const void*
     p.qo_rs = q_out_row_stride;
     p.status = status_word();
     if (!p.status) return TA_ERR_CUDA;
-    return launch_kv_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TA_OK : TA_ERR_CUDA;
+    return launched(launch_kv_append(p, static_cast<cudaStream_t>(stream)));
 }
 
 TA_EXPORT size_t tri_attn_paged_workspace_size(ta_dtype dtype, int max_seqlen_q, int Hq, int Hk, int D) {

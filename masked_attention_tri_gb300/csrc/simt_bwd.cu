@@ -540,6 +540,8 @@ void bwd_sink_share(BwdParams& p) {
     // (with a number of sinks for each sequence, the host knows none of them: the first block is shared)
     const long long nb = p.prefix_len ? 1 : ((long long)p.prefix_all + 127) / 128, nkb = ((long long)p.max_k + 127) / 128;
     if (nb > 4) return;  // (many key blocks see everything: they balance one another)
+    // (many short sequences beside a long one: an accumulator larger than dQ's would cost more than it saves)
+    if (p.num_seqs * nb * 2 * 128 > (long long)p.total_q) return;
     p.sink.nb = (int)(nb < nkb ? nb : nkb);
     p.sink.chunk = chunk;
     p.sink.chunks = (int)((far + chunk - 1) / chunk);

@@ -274,6 +274,21 @@ def test_broken_contracts_are_skipped():
 
 
 @pytest.mark.gpu
+def test_more_jobs_than_a_grid_has():
+    """16381 heads (a prime) of whole pages of 1024 rows: refused, nothing written; of single rows: written."""
+    import masked_attention_tri_gb300 as ta
+    Hk = 16381
+    cache = ta.PagedKVCache(*(torch.zeros(1, Hk, 1024, 8, dtype=torch.float16, device="cuda") for _ in range(2)))
+    k = torch.ones(1, Hk, 8, dtype=torch.float16, device="cuda")
+    with pytest.raises(NotImplementedError):
+        ta.kv_cache_append(cache, k, k, _i32([[0]]), _i32([1]), _i32([0, 1]), 1024)
+    assert not bool(cache.k.any())
+    ta.kv_cache_append(cache, k, k, _i32([[0]]), _i32([1]))
+    assert bool((cache.k[0, :, 0] == 1).all()) and not bool(cache.v[0, :, 1:].any())
+    assert ta.get_status() == 0
+
+
+@pytest.mark.gpu
 def test_offsets_beyond_32_bits():
     """The last page of a cache of more than 2^31 elements."""
     import masked_attention_tri_gb300 as ta

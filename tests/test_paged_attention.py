@@ -359,6 +359,19 @@ def test_offsets_beyond_32_bits():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("cdtype", [F8, B16])
+def test_windows_beyond_int32(cdtype):
+    """A window past int32 is every slot, as are sinks past it."""
+    import masked_attention_tri_gb300 as ta
+    pr = Problem([1, 1], [300, 77], 4, 2, 64, 16, B16, cdtype, seed=4, poison=False)
+    want, cache = pr.run(), pr.cache()
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 32 + 5, 0), (5, 2 ** 32 + 3), (2 ** 40, 2 ** 40)):
+        got = ta.paged_attention(pr.q.cuda(), cache, _i32(pr.table), _i32(pr.helds), window=window, sinks=sinks,
+                                 return_aux=True)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cdtype", [F8, B16])
 def test_serving_run(cdtype):
     """A prompt, a chunk and single tokens through append and attention, as a server runs them, against
     fp64 attention over the rows that the cache holds."""

@@ -193,6 +193,9 @@ def test_workspace_of_shared_key_blocks():
     size = lambda *a: abi.tri_attn_varlen_bwd_sink_workspace_size(3, 5000, 2, 64, *a) - plain  # noqa: E731
     assert size(2500, 2500, False, 130, 4) == size(2500, 2500, False, 130, -1) == 3 * 2 * 2 * 128 * 64 * 4
     assert size(2500, 2500, False, 130, 200) == 2 * 3 * 2 * 2 * 128 * 64 * 4
+    # many short sequences beside a long one: no accumulator larger than dQ's
+    many = lambda S: abi.tri_attn_varlen_bwd_sink_workspace_size(S, 5000, 2, 64, 2500, 2500, False, 130, 4) - plain  # noqa: E731
+    assert many(19) == 19 * 2 * 2 * 128 * 64 * 4 and many(20) == 0
     # no sinks, few far blocks, too many first blocks
     assert size(2500, 2500, False, 130, 0) == size(1000, 1000, False, 130, 4) == size(2500, 2500, False, 130, 600) == 0
 
@@ -295,6 +298,55 @@ def test_bias_and_strided_rows():
         tol = 2.0 ** -8 * (w @ V).abs() + (2.0 ** -8 + 2.0 ** -12) * (w @ V.abs())
         assert bool(((o[t:t + n].transpose(0, 1) - w @ V).abs() <= tol).all())
         t += n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,bias_dtype", [(64, B16), (64, F32), (128, B16), (128, F32), (40, F32)])
+def test_gradients_with_a_bias(D, bias_dtype):
+    """dBias is the sum over the sequences; tolerances by the forms at the top, the bias being one more exact logit
+    term: per row m = P (|dP| + |delta|) and its errors, summed over queries, keys or sequences.  Here with one factor
+    for all: every P, dS and result is off by at most u relative to its magnitudes, delta by u sum |dO O|, and
+    fp32's own errors (64 logits' units of 2^-23 D) are below u / 8."""
+    import masked_attention_tri_gb300 as ta
+    lens, H, w, sinks, u = [300, 129, 200], 2, 70, 3, 2.0 ** -8
+    q, k, v, g = _problem(lens, lens, H, D, B16, seed=9 + D)
+    bias = torch.randn(H, 300, 304, generator=torch.Generator().manual_seed(2)).to(bias_dtype)
+    cu, s = _i32(_cu(lens)), 1 / math.sqrt(D)
+    dev = [x.cuda() for x in (q, k, v)]
+    mask = dict(mask_mod="sink_window", window=w, sinks=sinks, bias=bias.cuda())
+    o, lse, _ = ta.varlen_attention(*dev, cu, cu, 300, 304, return_aux=True, **mask)
+    got = ta.varlen_attention_backward(*dev, cu, cu, 300, 304, o, lse, g.cuda(), **mask)
+    assert ta.get_status() == 0
+    dbias, tbias, t = torch.zeros(H, 300, 304).double(), torch.zeros(H, 300, 304).double(), 0
+    for n in lens:
+        Q, K, V, G = (x[t:t + n].double().transpose(0, 1) for x in (q, k, v, g))
+        i, j = torch.arange(n)[:, None], torch.arange(n)
+        keep = (j <= i) & ((j > i - w) | (j < sinks))
+        P = (s * Q @ K.transpose(1, 2) + bias[:, :n, :n].double()).masked_fill(~keep, -math.inf).softmax(-1)
+        O, dP = P @ V, G @ V.transpose(1, 2)
+        delta = (G * O).sum(-1, keepdim=True)
+        dS = P * (dP - delta)
+        tO = 2 * u * (P @ V.abs())
+        m = P * ((u + u / 8) * (dP.abs() + delta.abs()) + (G.abs() * tO).sum(-1, keepdim=True))
+        want = (s * dS @ K, s * dS.transpose(1, 2) @ Q, P.transpose(1, 2) @ G)
+        tols = (s * m @ K.abs(), s * m.transpose(1, 2) @ Q.abs(), (u + u / 8) * P.transpose(1, 2) @ G.abs())
+        for name, x, y, tol in zip(("dq", "dk", "dv"), got, want, tols):
+            err = (x[t:t + n].double().cpu().transpose(0, 1) - y).abs()
+            assert bool((err <= tol + u * y.abs()).all()), (name, n, float((err - tol).max()))
+        dbias[:, :n, :n] += dS
+        tbias[:, :n, :n] += m
+        t += n
+    err = (got[3].double().cpu() - dbias).abs()
+    assert bool((err <= tbias + u * dbias.abs()).all()), float((err - tbias).max())
+
+
+@pytest.mark.gpu
+def test_counts_beyond_int32():
+    lens = [300, 140]
+    q, k, v, g = _problem(lens, lens, 2, 64, B16, seed=13)
+    want = _dense(q, k, v, g, lens, lens, 1000, 0, 0.125, B16)
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 32 + 5, 4), (5, 2 ** 33)):
+        _check(_run(q, k, v, g, lens, lens, window, sinks, 0.125), want)
 
 
 @pytest.mark.gpu
