@@ -72,6 +72,7 @@ struct BwdTc {
     uint32_t bias_bytes;
     int bias_boxes, bias_box_cols;
     int bias_alias;     // 1: the two bias halves share one slot (an fp32 bias with D > 64)
+    int lo;             // 1: dS in two 16-bit pieces, the second at 2 boxes past the first
     int qs;             // stages of (Q, dO, lse, delta): 2 when shared memory allows, else 1
     // Packed sequences (VARLEN): q / k / v / dO (total, H, D) and the fp32 dQ accumulator read
     // through (D, total, H) maps, lse / delta (H, total_q), the BlockMask lists, an optional
@@ -112,7 +113,7 @@ __host__ __device__ inline BwdLayout bwd_layout(const BwdTc& P, int nsub) {
     L.v = L.k + tile;
     L.q = L.v + tile;
     L.ds = L.q + (uint32_t)P.qs * 2 * tile;  // dS as [key][query]: two 64-query boxes
-    L.bias = L.ds + 2 * kBox;
+    L.bias = L.ds + (P.lo ? 4 : 2) * kBox;
     L.dqst = L.bias + (P.bias_alias ? P.bias_bytes / 2u : P.bias_bytes);  // dQ staging: 16 warps x 32 rows x 16 fp32
     L.lse = L.dqst + 16u * 2048u;
     L.qlist = L.lse + (uint32_t)P.qs * bwd_row_bytes(P.bias_alias != 0);  // packed form: the q blocks the key tile visits
@@ -200,7 +201,8 @@ __device__ __forceinline__ uint32_t bwd_sink_bits(int q, int k, int window, int 
 // whose lists hold the key block (full: every key valid; partial: mask_mod decides) and the
 // q blocks with a row that has no valid key (its weights are 1 / Lk at every key).
 // HASB: a bias (always in the triangle form; optional with packed sequences).
-template <bool BF16, bool BIAS_F32, bool WIDE, bool VARLEN, bool HASB>
+// LO: dS in two 16-bit pieces (packed sequences without a bias).
+template <bool BF16, bool BIAS_F32, bool WIDE, bool VARLEN, bool HASB, bool LO>
 __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_constant__ BwdTc P) {
     constexpr int kNsub = WIDE ? 2 : 1;   // 64-column boxes per 128-row tile
     constexpr int kCpw = WIDE ? 32 : 16;  // dQ / dK / dV columns per compute warp
@@ -615,16 +617,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                 ok = __all_sync(0xffffffffu, wait_bar(p_full((int)b), sphase(j, hh), abort_flag, P.status));
                 if (!ok) break;
                 tc_fence_after();
-                if (leader) {
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {  // 16 queries per k step; P^T / dS^T at 16 kk
-                        const uint32_t acc = (j > 0 || hh > 0 || kk > 0) ? 1u : 0u;
-                        const uint32_t qs16 = (uint32_t)(4 * hh + kk);  // 16-query step within the tile
-                        mma_ts(tDV, tS + 64u * b + 16u * (uint32_t)kk, doM + 128u * qs16, P.idesc_g, acc);
-                        mma_ts(tDK, tDP + 64u * b + 16u * (uint32_t)kk, qM + 128u * qs16, P.idesc_g, acc);
-                    }
-                    if constexpr (WIDE) mma_commit(q_empty(hh));  // the rows of half hh are read
-                }
+                // dQ first: the compute warps wait for its read of dS before they write the next tile's.
                 if (hh == 1) {
                     if (j > 0) {  // the compute warps have read dQ of the previous tile
                         ok = __all_sync(0xffffffffu, wait_bar(dq_empty, (uint32_t)(j - 1) & 1u, abort_flag, P.status));
@@ -636,10 +629,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                         for (int kk = 0; kk < kBN / 16; ++kk)  // dQ_j = dS K, 16 keys per k step
                             mma_ss(tDQ, dsM + 128u * (uint32_t)kk, kM + 128u * (uint32_t)kk, P.idesc_q,
                                    kk > 0 ? 1u : 0u);
+                        if constexpr (LO) {
+                            const uint64_t loM = sw128_desc(base + L.ds + 2 * kBox, kBox, 1024);
+#pragma unroll 1
+                            for (int kk = 0; kk < kBN / 16; ++kk)
+                                mma_ss(tDQ, loM + 128u * (uint32_t)kk, kM + 128u * (uint32_t)kk, P.idesc_q, 1u);
+                        }
                         mma_commit(dq_full);
                         mma_commit(ds_free);
-                        if constexpr (!WIDE) mma_commit(q_empty(st));
                     }
+                }
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {  // 16 queries per k step; P^T / dS^T at 16 kk
+                        const uint32_t acc = (j > 0 || hh > 0 || kk > 0) ? 1u : 0u;
+                        const uint32_t qs16 = (uint32_t)(4 * hh + kk);  // 16-query step within the tile
+                        mma_ts(tDV, tS + 64u * b + 16u * (uint32_t)kk, doM + 128u * qs16, P.idesc_g, acc);
+                        mma_ts(tDK, tDP + 64u * b + 16u * (uint32_t)kk, qM + 128u * qs16, P.idesc_g, acc);
+                        if constexpr (LO)
+                            mma_ts(tDK, tDP + 64u * b + 16u * (uint32_t)kk + 8u, qM + 128u * qs16, P.idesc_g, 1u);
+                    }
+                    if constexpr (WIDE) mma_commit(q_empty(hh));  // the rows of half hh are read
+                    else if (hh == 1) mma_commit(q_empty(st));
                 }
                 if constexpr (WIDE) {  // the single buffer: the other half next (the tensor core runs them in order)
                     if (hh == 0) ok = mma1(j, 1);
@@ -794,7 +805,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                     }
                     const uint8_t* bcb = gbase + (bias_half(hh) - base) + bbox_off + (uint32_t)(ql - 64 * hh) * 128u;
                     const int nq = Qn - (q0 + ql);  // queries of the chunk that exist
-                    uint32_t pp[CW / 2], dd[CW / 2];
+                    uint32_t pp[CW / 2], dd[CW / 2], dlo[LO ? CW / 2 : 1] = {};
+                    // What the rounding of a pair of dS leaves, as another pair.
+                    auto low = [&](int i, uint32_t rounded, float x, float y) {
+                        if constexpr (LO) {
+                                const float2 hi = unpack2<BF16>(rounded);
+                                dlo[i / 2] = pack2<BF16>(x - hi.x, y - hi.y);
+                        }
+                    };
                     // Packed form, partial block: the chunk is wholly kept when mask_mod keeps every
                     // (query, key) of it (warp-uniform: this warp's 32 keys x the chunk's 16 queries).
                     bool whole = tst == 2;
@@ -845,6 +863,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                             }
                             pp[i / 2] = pack2<BF16>(pr.x, pr.y);
                             dd[i / 2] = pack2<BF16>(ds.x, ds.y);
+                            low(i, dd[i / 2], ds.x, ds.y);
                             if (dbp) {
                                 if (!MASKED || ((bits >> i) & 1u)) red_add_global(dbp + (long long)i * bst, ds.x);
                                 if (!MASKED || ((bits >> (i + 1)) & 1u)) red_add_global(dbp + (long long)(i + 1) * bst, ds.y);
@@ -917,6 +936,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                             }
                             pp[i / 2] = pack2<BF16>(pv[0], pv[1]);
                             dd[i / 2] = pack2<BF16>(sv[0], sv[1]);
+                            low(i, dd[i / 2], sv[0], sv[1]);
                         }
                         if (dbias_row) {
 #pragma unroll
@@ -927,6 +947,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                     }
                     tmem_st_x8(tSh + lane_off + col, pp);
                     tmem_st_x8(tDPh + lane_off + col, dd);
+                    if constexpr (LO) tmem_st_x8(tDPh + lane_off + col + 8u, dlo);  // (the chunk's other eight columns)
                     // dS as [key][query] in shared memory (box ql / 64, 16-byte chunks of 8 queries),
                     // once dQ of the previous tile has read it.
                     if (j > 0 && hh == 0 && c == 0) {
@@ -938,6 +959,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                     for (int g = 0; g < CW / 8; ++g) {
                         const uint32_t ch = (uint32_t)((ql % 64) / 8 + g);
                         st_shared_v4(drow + ((ch ^ rsw) << 4), dd[4 * g], dd[4 * g + 1], dd[4 * g + 2], dd[4 * g + 3]);
+                        if constexpr (LO)
+                                st_shared_v4(drow + 2 * kBox + ((ch ^ rsw) << 4), dlo[4 * g], dlo[4 * g + 1], dlo[4 * g + 2],
+                                             dlo[4 * g + 3]);
                     }
                 }
                 if (!ok) break;
@@ -1152,23 +1176,36 @@ cudaError_t launch_tc_bwd_main(const BwdParams& p, cudaStream_t stream) {
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     P.qs = D > 64 ? 1 : 2;  // D > 64: one stage, taken per query half
     if (bwd_layout(P, P.nsub).total + 1024 > 232448) P.qs = 1;  // the 227 KB per-block limit
+    // Roundings.  P and dS enter their products in the inputs' type, like P in the forward: half a step each, so
+    // dK, dQ and dV are off by about sqrt(2) times their own rounding.  dS also holds delta's error (the sums come
+    // from the rounded O), and a short window averages neither out; so under a sink window dS is two
+    // pieces of that type where they fit beside the tiles (D <= 64, or 80 q blocks): of dQ's and dK's norm
+    // 0.0018 in place of 0.0025 in bf16, for 214 us in place of 204 on packed 777 + 4484 + 8192 tokens, 8 heads
+    // of 64, window 1024 (heads of 128: 390 and 351).  (The other masks keep their results to the bit.)
+    if (vl && !p.bias && p.mask_mod == TA_MASK_SINK_WINDOW) {
+        P.lo = 1;
+        if (bwd_layout(P, P.nsub).total + 1024 > 232448) P.lo = 0;
+    }
     const size_t smem = bwd_layout(P, P.nsub).total + 1024;
-    // <BF16, BIAS_F32, WIDE, VARLEN, HASB>; the triangle form always has a bias
+    // <BF16, BIAS_F32, WIDE, VARLEN, HASB, LO>; the triangle form always has a bias
     const bool fb = p.bias_f32 != 0;
-    decltype(&tc_bwd_kernel<true, false, false, false, true>) kern;
+    decltype(&tc_bwd_kernel<true, false, false, false, true, false>) kern;
     if (!vl)
-        kern = D > 64 ? (bf16 ? (fb ? tc_bwd_kernel<true, true, true, false, true> : tc_bwd_kernel<true, false, true, false, true>)
-                              : (fb ? tc_bwd_kernel<false, true, true, false, true> : tc_bwd_kernel<false, false, true, false, true>))
-             : bf16   ? (fb ? tc_bwd_kernel<true, true, false, false, true> : tc_bwd_kernel<true, false, false, false, true>)
-                      : (fb ? tc_bwd_kernel<false, true, false, false, true> : tc_bwd_kernel<false, false, false, false, true>);
+        kern = D > 64 ? (bf16 ? (fb ? tc_bwd_kernel<true, true, true, false, true, false> : tc_bwd_kernel<true, false, true, false, true, false>)
+                              : (fb ? tc_bwd_kernel<false, true, true, false, true, false> : tc_bwd_kernel<false, false, true, false, true, false>))
+             : bf16   ? (fb ? tc_bwd_kernel<true, true, false, false, true, false> : tc_bwd_kernel<true, false, false, false, true, false>)
+                      : (fb ? tc_bwd_kernel<false, true, false, false, true, false> : tc_bwd_kernel<false, false, false, false, true, false>);
+    else if (P.lo)
+        kern = D > 64 ? (bf16 ? tc_bwd_kernel<true, false, true, true, false, true> : tc_bwd_kernel<false, false, true, true, false, true>)
+                      : (bf16 ? tc_bwd_kernel<true, false, false, true, false, true> : tc_bwd_kernel<false, false, false, true, false, true>);
     else if (!p.bias)
-        kern = D > 64 ? (bf16 ? tc_bwd_kernel<true, false, true, true, false> : tc_bwd_kernel<false, false, true, true, false>)
-                      : (bf16 ? tc_bwd_kernel<true, false, false, true, false> : tc_bwd_kernel<false, false, false, true, false>);
+        kern = D > 64 ? (bf16 ? tc_bwd_kernel<true, false, true, true, false, false> : tc_bwd_kernel<false, false, true, true, false, false>)
+                      : (bf16 ? tc_bwd_kernel<true, false, false, true, false, false> : tc_bwd_kernel<false, false, false, true, false, false>);
     else
-        kern = D > 64 ? (bf16 ? (fb ? tc_bwd_kernel<true, true, true, true, true> : tc_bwd_kernel<true, false, true, true, true>)
-                              : (fb ? tc_bwd_kernel<false, true, true, true, true> : tc_bwd_kernel<false, false, true, true, true>))
-             : bf16   ? (fb ? tc_bwd_kernel<true, true, false, true, true> : tc_bwd_kernel<true, false, false, true, true>)
-                      : (fb ? tc_bwd_kernel<false, true, false, true, true> : tc_bwd_kernel<false, false, false, true, true>);
+        kern = D > 64 ? (bf16 ? (fb ? tc_bwd_kernel<true, true, true, true, true, false> : tc_bwd_kernel<true, false, true, true, true, false>)
+                              : (fb ? tc_bwd_kernel<false, true, true, true, true, false> : tc_bwd_kernel<false, false, true, true, true, false>))
+             : bf16   ? (fb ? tc_bwd_kernel<true, true, false, true, true, false> : tc_bwd_kernel<true, false, false, true, true, false>)
+                      : (fb ? tc_bwd_kernel<false, true, false, true, true, false> : tc_bwd_kernel<false, false, false, true, true, false>);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)grid, kBwdThreads, smem, stream>>>(P);
