@@ -1,7 +1,8 @@
 /*
- * triattn.h -- C ABI of the GB300 (sm_103a) triangle-attention forward.
+ * triattn.h -- C ABI of the GB300 (sm_103a) attention library: triangle and packed attention,
+ * forward and backward, rotary positions, and attention over a paged cache.
  *
- * Operation (cuEquivariance "triangle_attention" API page, formula):
+ * Operation of the triangle form (cuEquivariance "triangle_attention" API page, formula):
  *
  *   O[b,n,h,q,:] = sum_k softmax_k(x) V[b,n,h,k,:]
  *   x_k = s * (Q[b,n,h,q,:] . K[b,n,h,k,:]) + bias[b,0,h,q,k]   if key k is valid

@@ -195,6 +195,11 @@ __device__ __forceinline__ uint32_t bwd_sink_bits(int q, int k, int window, int 
     return (0xffffu << from) & ((1u << to) - 1u);
 }
 
+// First q block of chunk `far` of those past the window of the key block at k0.
+__device__ __forceinline__ long long far_first(const BwdTc& P, int k0, int far) {
+    return ((long long)k0 + 126 + P.window) / kBM + 1 + (long long)far * P.sink_chunk;
+}
+
 // WIDE: D in (64, 128] (two 64-column boxes per tile, one S^T / dP^T buffer that the query
 // halves take in turn, 32 columns of dQ / dK / dV per compute warp); otherwise D <= 64.
 // VARLEN: packed sequences, one CTA per (sequence, head, 128-key block), visiting the q blocks
@@ -273,6 +278,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
             return;
         }
         if (k0 >= Kn) return;
+        if (far >= 0 && far_first(P, k0, far) >= (Qn + kBM - 1) / kBM) return;  // no q block in this chunk
         qrow0 = cq0;
         krow0 = ck0;
         tz = h;
@@ -306,6 +312,41 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
         }
     }
 
+    // The barriers, and K and V on their way, while tensor memory is taken and the list below is made.
+    if (warp == kProducerWarp) {
+        if (lane == 0) {
+            *abort_flag = 0;
+            mbar_init(kv_full, 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(q_full(i), 1);      // the expect_tx arrival of Q and dO
+                mbar_init(q_empty(i), 1);
+                mbar_init(lse_full(i), 1);    // the lse / delta rows written
+                mbar_init(bias_full(i), 1);
+                mbar_init(bias_empty(i), kComputeWarps);  // every compute warp has read the bias half
+                mbar_init(s_full(i), 1);
+                mbar_init(p_full(i), kComputeWarps);
+            }
+            mbar_init(dq_full, 1);
+            mbar_init(dq_empty, 4 * ((P.D + kCpw - 1) / kCpw));  // the warps that read dQ_j (kCpw columns each)
+            mbar_init(ds_free, 1);
+            mbar_init(fin, 1);
+            mbar_init(drain, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_expect_tx(kv_full, 2u * tileb);
+            for (int bx = 0; bx < kNsub; ++bx) {
+                tma_load_3d(base + L.k + (uint32_t)bx * kBox, &P.tm_k, 64 * bx, krow0 + k0, tz, kv_full);
+                tma_load_3d(base + L.v + (uint32_t)bx * kBox, &P.tm_v, 64 * bx, krow0 + k0, tz, kv_full);
+            }
+        }
+        __syncwarp();
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+
     // Packed form: the q blocks this key tile visits, as (q block | status << 24) in shared
     // memory (status 1 partial, 2 full, 3 every key masked), built by one warp.
     int nqt = P.nqt;
@@ -317,7 +358,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
             int nqb = (Qn + kBM - 1) / kBM, qb0 = 0;
             int cnt = 0;
             if (far >= 0) {  // this chunk of the q blocks past the key block's window
-                const long long first = ((long long)k0 + 126 + P.window) / kBM + 1 + (long long)far * P.sink_chunk;
+                const long long first = far_first(P, k0, far);
                 qb0 = first < nqb ? (int)first : nqb;
                 nqb = min(nqb, qb0 + P.sink_chunk);
             }
@@ -386,8 +427,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
             }
             if (lane == 0) *reinterpret_cast<volatile int*>(gbase + L.qn) = cnt;
         }
-        __syncthreads();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if constexpr (VARLEN) {
         nqt = *reinterpret_cast<volatile int*>(gbase + L.qn);
+        if (nqt == 0) {  // (K and V land before the CTA ends)
+            if (warp == kProducerWarp) wait_bar_drain(kv_full, 0);
+            if (warp == kMmaWarp)
+                asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        }
         if (nqt == 0 && shared_kb) return;  // nothing to add
         if (nqt == 0) {  // no row reaches these keys: dK = dV = 0
             const int rows = Kn - k0 < kBN ? Kn - k0 : kBN, per = P.D / 8;  // 16-byte pieces per row
@@ -412,35 +463,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
         else return 2;
     };
 
-    if (threadIdx.x == 0) {
-        *abort_flag = 0;
-        mbar_init(kv_full, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full(i), 1);      // the expect_tx arrival of Q and dO
-            mbar_init(q_empty(i), 1);
-            mbar_init(lse_full(i), 1);    // the lse / delta rows written
-            mbar_init(bias_full(i), 1);
-            mbar_init(bias_empty(i), kComputeWarps);  // every compute warp has read the bias half
-            mbar_init(s_full(i), 1);
-            mbar_init(p_full(i), kComputeWarps);
-        }
-        mbar_init(dq_full, 1);
-        mbar_init(dq_empty, 4 * ((P.D + kCpw - 1) / kCpw));  // the warps that read dQ_j (kCpw columns each)
-        mbar_init(ds_free, 1);
-        mbar_init(fin, 1);
-        mbar_init(drain, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
-    if (warp == kMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     const uint32_t D = (uint32_t)P.D;
     // S^T of query half hh at tS + 64 hh, dP^T at tDP + 64 hh (P^T and dS^T written over them in
     // place), then dV, dK and dQ_j.
@@ -456,13 +478,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
     if (warp == kProducerWarp) {
         // ------------------------------------------------------------ producer
         bool ok = true;
-        if (lane == 0) {
-            mbar_expect_tx(kv_full, 2u * tileb);
-            for (int bx = 0; bx < kNsub; ++bx) {
-                tma_load_3d(base + L.k + (uint32_t)bx * kBox, &P.tm_k, 64 * bx, krow0 + k0, tz, kv_full);
-                tma_load_3d(base + L.v + (uint32_t)bx * kBox, &P.tm_v, 64 * bx, krow0 + k0, tz, kv_full);
-            }
-        }
         for (int j = 0; j < nqt && ok; ++j) {
             const int q0 = tile_q0(j), st = stage_of(j), use = use_of(j);
             // This tile's Q / dO, bias half 0 (as soon as the compute warps have read half 0 of
