@@ -24,9 +24,7 @@ cudaError_t launch_type(const MmaParams& P, cudaStream_t stream) {
                : nt == 2 ? launch_mma_variant<TYPE, 1, 2>(P, stream)
                          : launch_mma_variant<TYPE, 1, 4>(P, stream);
     if (P.p.D <= 128)
-        return nt == 1   ? launch_mma_variant<TYPE, 2, 1>(P, stream)
-               : nt == 2 ? launch_mma_variant<TYPE, 2, 2>(P, stream)
-                         : launch_mma_variant<TYPE, 2, 4>(P, stream);
+        return nt == 1 ? launch_mma_variant<TYPE, 2, 1>(P, stream) : launch_mma_variant<TYPE, 2, 2>(P, stream);
     return nt == 1 ? launch_mma_variant<TYPE, 4, 1>(P, stream) : launch_mma_variant<TYPE, 4, 2>(P, stream);
 }
 

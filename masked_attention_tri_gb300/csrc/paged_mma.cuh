@@ -18,7 +18,7 @@
 // Measured from a cold L2, 32 heads over 8 of 128, pages of 64: 64 sequences of 1k to 16k slots in 8 bits
 // 208 us (5.5 TB/s; the copies alone 198, the arithmetic alone 175), in 16 bits 355 us (6.4 TB/s); 256
 // sequences of 256 to 1024 slots in 8 bits 118 us, of which 79 are waits, set-up and merges of the 14 units
-// that a CTA has there.  64 query heads 216 us, 128 276 us: bound by the conversions' and products' rate.
+// that a CTA has there.  64 query heads 216 us.
 //
 //   S^T = K Q^T      A: slots x d from shared memory, B: Q^T, kept in fragment order
 //   O^T += V^T P^T   A: d x slots; P^T comes from S^T's accumulators by movmatrix
@@ -827,7 +827,7 @@ cudaError_t launch_mma_variant(const MmaParams& P, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-#define TRIATTN_PAGED_VARIANTS(X, T) X(T, 1, 1) X(T, 1, 2) X(T, 1, 4) X(T, 2, 1) X(T, 2, 2) X(T, 2, 4) X(T, 4, 1) X(T, 4, 2)
+#define TRIATTN_PAGED_VARIANTS(X, T) X(T, 1, 1) X(T, 1, 2) X(T, 1, 4) X(T, 2, 1) X(T, 2, 2) X(T, 4, 1) X(T, 4, 2)
 #define TRIATTN_PAGED_EXTERN(t, d, n) \
     extern template cudaError_t launch_mma_variant<t, d, n>(const MmaParams&, cudaStream_t);
 #define TRIATTN_PAGED_INSTANTIATE(t, d, n) \
