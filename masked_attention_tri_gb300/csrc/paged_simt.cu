@@ -236,20 +236,44 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
     const Workspace ws = workspace(p.ws, p.RT, p.D);
     const Join jn = ws.join[blockIdx.x];
     if (jn.parts <= 1) return;
-    const int D4 = p.D / 4, c = blockIdx.x;
-    for (int e = threadIdx.x; e < jn.rows * D4; e += blockDim.x) {
-        const int r = e / D4, d = (e - r * D4) * 4;
-        // part 0 in slot 2c + 1, part i in slot 2 (c + i)
-        auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+    // (m, l) of all parts at once, then each row's maximum and sum over the lanes of a warp: a loop over the
+    // parts from memory would cost a latency for each (a long sequence alone has up to 152 of them).
+    __shared__ float2 sml[kGrid * kMaxRT];  // part i, row r at i * rows + r; then the part's weight (-1: no key) in x
+    __shared__ float2 srow[kMaxRT];
+    const int D4 = p.D / 4, c = blockIdx.x, rows = jn.rows;
+    // part 0 in slot 2c + 1, part i in slot 2 (c + i)
+    auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+    for (int e = threadIdx.x; e < jn.parts * rows; e += blockDim.x) {
+        const int i = e / rows;
+        sml[e] = ws.ml[slot(i) * p.RT + (e - i * rows)];
+    }
+    __syncthreads();
+    for (int r = threadIdx.x / 32; r < rows; r += blockDim.x / 32) {
+        const int lane = threadIdx.x % 32;
         float M = -INFINITY, L = 0.f;
-        for (int i = 0; i < jn.parts; ++i) M = fmaxf(M, ws.ml[slot(i) * p.RT + r].x);
+        for (int i = lane; i < jn.parts; i += 32) M = fmaxf(M, sml[i * rows + r].x);
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int i = lane; i < jn.parts; i += 32) {
+            const float2 ml = sml[i * rows + r];
+            const bool none = no_key(ml.x, ml.y);
+            const float f = none ? -1.f : exp2f(ml.x - M);
+            if (!none) L = fmaf(ml.y, f, L);
+            sml[i * rows + r].x = f;
+        }
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (lane == 0) srow[r] = make_float2(M, L);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < rows * D4; e += blockDim.x) {
+        const int r = e / D4, d = (e - r * D4) * 4;
+        const float M = srow[r].x, L = srow[r].y;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
         for (int i = 0; i < jn.parts; ++i) {
-            const float2 ml = ws.ml[slot(i) * p.RT + r];
-            if (no_key(ml.x, ml.y)) continue;
-            const float f = exp2f(ml.x - M);
-            const float4 x = *reinterpret_cast<const float4*>(ws.o + ((long long)slot(i) * p.RT + r) * p.D + d);
-            L = fmaf(ml.y, f, L);
+            float f = sml[i * rows + r].x;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (f < 0.f) f = 0.f;
+            else x = *reinterpret_cast<const float4*>(ws.o + ((long long)slot(i) * p.RT + r) * p.D + d);
             o.x = fmaf(x.x, f, o.x);
             o.y = fmaf(x.y, f, o.y);
             o.z = fmaf(x.z, f, o.z);
