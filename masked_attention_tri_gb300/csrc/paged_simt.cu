@@ -268,16 +268,17 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
         const int r = e / D4, d = (e - r * D4) * 4;
         const float M = srow[r].x, L = srow[r].y;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+        const float* at = ws.o + (long long)r * p.D + d;
+#pragma unroll 8
         for (int i = 0; i < jn.parts; ++i) {
-            float f = sml[i * rows + r].x;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (f < 0.f) f = 0.f;
-            else x = *reinterpret_cast<const float4*>(ws.o + ((long long)slot(i) * p.RT + r) * p.D + d);
-            o.x = fmaf(x.x, f, o.x);
-            o.y = fmaf(x.y, f, o.y);
-            o.z = fmaf(x.z, f, o.z);
-            o.w = fmaf(x.w, f, o.w);
+            const float f = sml[i * rows + r].x;
+            const float4 x = *reinterpret_cast<const float4*>(at + (long long)slot(i) * p.RT * p.D);
+            if (!(f < 0.f)) {  // (after the load, so that eight are in flight)
+                o.x = fmaf(x.x, f, o.x);
+                o.y = fmaf(x.y, f, o.y);
+                o.z = fmaf(x.z, f, o.z);
+                o.w = fmaf(x.w, f, o.w);
+            }
         }
         const float inv = no_key(M, L) ? 0.f : 1.f / L;
         const int row = jn.row0 + r;
