@@ -341,6 +341,39 @@ def test_gradients_with_a_bias(D, bias_dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("L,D", [(11000, 128), (70000, 64)])
+def test_long_sequences(L, D):
+    """Hundreds of q blocks, against fp64 over each run of queries and the keys that it sees; tolerances as in
+    test_gradients_with_a_bias."""
+    w, sinks, u, s = 200, 5, 2.0 ** -8, 1 / math.sqrt(D)
+    q, k, v, g = (x.cuda() for x in _problem([L], [L], 1, D, B16, seed=D))
+    got = {n: x.double() for n, x in _run(q, k, v, g, [L], [L], w, sinks, s).items()}
+    Q, K, V, G = (x[:, 0].double() for x in (q, k, v, g))
+    ref = {n: torch.zeros(L, D, dtype=torch.float64, device="cuda") for n in ("out", "dq", "dk", "dv")}
+    tol = {n: x.clone() for n, x in ref.items()}
+    for a in range(0, L, 1000):
+        b = min(L, a + 1000)
+        i = torch.arange(a, b, device="cuda")[:, None]
+        j = torch.cat((torch.arange(min(sinks, b)), torch.arange(max(sinks, a - w + 1), b))).cuda()
+        keep = (j <= i) & ((j > i - w) | (j < sinks))
+        P = (s * Q[a:b] @ K[j].t()).masked_fill(~keep, -math.inf).softmax(-1)
+        O, dP = P @ V[j], G[a:b] @ V[j].t()
+        delta = (G[a:b] * O).sum(-1, keepdim=True)
+        dS = P * (dP - delta)
+        tO = 2 * u * (P @ V[j].abs())
+        m = P * ((u + u / 8) * (dP.abs() + delta.abs()) + (G[a:b].abs() * tO).sum(-1, keepdim=True))
+        ref["out"][a:b], tol["out"][a:b] = O, tO + u * O.abs()
+        ref["dq"][a:b], tol["dq"][a:b] = s * dS @ K[j], s * m @ K[j].abs()
+        for n, x, y in (("dk", s * dS.t() @ Q[a:b], s * m.t() @ Q[a:b].abs()),
+                        ("dv", P.t() @ G[a:b], (u + u / 8) * P.t() @ G[a:b].abs())):
+            ref[n].index_add_(0, j, x)
+            tol[n].index_add_(0, j, y)
+    for n in ref:
+        err = (got[n][:, 0] - ref[n]).abs()
+        assert bool((err <= tol[n] + u * ref[n].abs()).all()), (n, float((err - tol[n]).max()))
+
+
+@pytest.mark.gpu
 def test_counts_beyond_int32():
     lens = [300, 140]
     q, k, v, g = _problem(lens, lens, 2, 64, B16, seed=13)
