@@ -460,8 +460,8 @@ ta_status tri_attn_rotary(const void* q, const void* k, ta_dtype dtype, const in
  *                 NULL: one row for each sequence (total = num_seqs, max_seqlen 1).
  *   kv_lengths    (num_seqs) int32: slots held AFTER this call; the new rows are the
  *                 last of them.
- *   page_table    (num_seqs, max_pages) int32.  A page that this call writes belongs
- *                 to one sequence of the call only.
+ *   page_table    (num_seqs, max_pages) int32.  A page that this call writes has one place in
+ *                 the tables of the call.
  *   turns, rotary_dim, interleaved, mscale   as in tri_attn_rotary; turns NULL (then
  *                 rotary_dim 0): no rotation.
  *   positions     (total) int32, or NULL: a row's position is its slot.
@@ -474,7 +474,8 @@ ta_status tri_attn_rotary(const void* q, const void* k, ta_dtype dtype, const in
  *                 even; beyond 448 * 2^56 to that); infinities and NaN become NaN.
  * A sequence that breaks the contract (lengths, offsets), or a page out of range, is skipped and
  * TA_ERR_DEVICE recorded.  Errors as tri_attn_rotary; a page size that is no power
- * of two in range, or cache strides that are no 16-byte multiples -> TA_ERR_UNSUPPORTED.
+ * of two in range, cache strides that are no 16-byte multiples, or more work for a page than a
+ * launch can hold (some ten thousand heads without common divisors) -> TA_ERR_UNSUPPORTED.
  */
 ta_status tri_attn_kv_append(const void* q, const void* k, const void* v, ta_dtype dtype,
                              const int32_t* cu_seqlens, const int32_t* kv_lengths, const int32_t* page_table,
