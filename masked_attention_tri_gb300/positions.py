@@ -172,5 +172,10 @@ class _RotaryFn(torch.autograd.Function):
 
 
 def rotary_embedding_autograd(q, k: Optional[torch.Tensor], positions, rotary: Rotary):
-    """``rotary_embedding`` with gradients for q and k."""
+    """``rotary_embedding`` with gradients for q and k.
+
+    Its backward may be captured into a graph, as any autograd function's, only while no
+    graph of the same leaves made outside the capture lives (PyTorch ties the leaves'
+    accumulation to the stream of the first).
+    """
     return _RotaryFn.apply(q, k, positions, rotary)

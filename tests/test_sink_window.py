@@ -383,6 +383,45 @@ def test_counts_beyond_int32():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_captured_steps_in_two_streams(D):
+    """Forward and backward captured once for each of two streams (the first key blocks shared out), replayed at the
+    same time with new inputs."""
+    import masked_attention_tri_gb300 as ta
+    lens, H, w, sinks, s = [2500, 300], 2, 130, 4, 0.1
+    mask = dict(mask_mod="sink_window", window=w, sinks=sinks, scale=s)
+    cu, steps = _i32(_cu(lens)), []
+    for i in range(2):
+        x = [t.cuda() for t in _problem(lens, lens, H, D, B16, seed=30 + i)]
+
+        def step():
+            o, lse, _ = ta.varlen_attention(*x[:3], cu, cu, 2500, 2500, return_aux=True, **mask)
+            return (o, lse) + ta.varlen_attention_backward(*x[:3], cu, cu, 2500, 2500, o, lse, x[3], **mask)[:3]
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            step()
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            out = step()
+        steps.append((x, stream, graph, out))
+    new = [_problem(lens, lens, H, D, B16, seed=40 + i) for i in range(2)]
+    for (x, *_), y in zip(steps, new):
+        for t, n in zip(x, y):
+            t.copy_(n)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x, stream, graph, out in steps:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert ta.get_status() == 0
+    for (x, stream, graph, out), y in zip(steps, new):
+        _check(dict(zip(("out", "lse", "dq", "dk", "dv"), out)), _dense(*y, lens, lens, w, sinks, s, B16))
+
+
+@pytest.mark.gpu
 def test_gradient_against_differences():
     """fp32: a central difference of step 2^-6 in fp64 of the formula's loss, and the kernel's gradients."""
     lens = [70, 33]
