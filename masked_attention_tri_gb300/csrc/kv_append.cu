@@ -345,7 +345,7 @@ cudaError_t launch(const KvAppendParams& p, cudaStream_t stream) {
     const long long gx = (long long)p.num_seqs * a.runs, gy = (long long)a.jobs[0] + a.jobs[1] + a.jobs[2];
     if (gx > 0x7fffffffLL || gy > 65535) return cudaErrorInvalidConfiguration;
     const size_t smem = (size_t)rows * row_bytes;
-    if (smem > (48 << 10)) {
+    if (smem > (47 << 10)) {  // (48 KB without the attribute, the maxima and scales of the heads among them)
         const cudaError_t e = cudaFuncSetAttribute(kv_append_kernel<T, C, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10);
         if (e != cudaSuccess) return e;
     }

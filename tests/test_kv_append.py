@@ -138,6 +138,9 @@ CASES = [
     (torch.float16, torch.float8_e4m3fn, 2, 1, 96, 32, True, 32, "heads last"),
     (torch.float32, torch.float8_e4m3fn, 3, 1, 48, 36, False, 16, ""),     # one pair at a time
     (torch.float16, torch.float8_e4m3fn, 1, 1, 256, 256, True, 128, ""),
+    (torch.float16, torch.float8_e4m3fn, 3, 2, 192, 192, True, 64, ""),    # 64 rows' table: just 48 KB
+    (torch.bfloat16, torch.bfloat16, 2, 1, 192, 192, False, 64, ""),
+    (torch.bfloat16, torch.float8_e4m3fn, 2, 1, 200 + 8, 96, False, 1024, ""),
     (torch.bfloat16, torch.bfloat16, 8, 2, 72, 40, False, 16, "heads last"),
     (torch.float16, torch.float16, 5, 5, 64, 64, True, 32, "one buffer"),
     (torch.float32, torch.float32, 2, 2, 20, 20, False, 16, ""),
