@@ -6,34 +6,13 @@
 #include <stdint.h>
 
 #include "../../include/triattn.h"
+#include "sink_window.h"
 
 namespace triattn {
 
 // Device-side status codes (match ta_status).  A kernel that gives up writes
 // one with atomicCAS(status, 0, code) so the first fault is kept.
 enum : int { kStatusOk = 0, kStatusTimeout = TA_ERR_TIMEOUT, kStatusDevice = TA_ERR_DEVICE };
-
-// TA_MASK_SINK_WINDOW without block lists: the 128-key blocks that hold a kept key for some
-// query of [q0, q1], of a sequence with Lk keys: [0, nsink) and [lo, hi].  (A key k is kept for a
-// query of the range when k < sinks and k <= q1, or when q0 - window < k <= q1.)
-struct SinkBlocks {
-    int nsink, lo, hi;
-#ifdef __CUDACC__
-    __device__ __forceinline__ bool visited(int kb) const { return kb < nsink || (kb >= lo && kb <= hi); }
-#endif
-};
-#ifdef __CUDACC__
-__device__ __forceinline__ SinkBlocks sink_blocks(int q0, int q1, int Lk, int window, int sinks) {
-    SinkBlocks b;
-    const int last = q1 < Lk - 1 ? q1 : Lk - 1;  // last key that any query reaches
-    const int first = q0 - window + 1 > 0 ? q0 - window + 1 : 0;
-    const int ns = sinks < last + 1 ? sinks : last + 1;
-    b.nsink = ns > 0 ? (ns + 127) / 128 : 0;
-    b.lo = first / 128;
-    b.hi = first <= last ? last / 128 : -1;
-    return b;
-}
-#endif
 
 // One attention problem as the kernels see it.  Triangle form: units are
 // (b, n, h) slabs with Q query rows and K keys.  Varlen form: units are

@@ -525,26 +525,10 @@ void bwd_sink_share(BwdParams& p) {
     p.sink.nb = p.sink.chunk = p.sink.chunks = 0;
     p.sink.elems = 0;
     if (!p.varlen || p.kv_num || p.mask_mod != TA_MASK_SINK_WINDOW || (!p.prefix_len && p.prefix_all <= 0)) return;
-    const int chunk = 8;
-    // q blocks of the longest sequence past the reach of its first key block
-    const long long nqb = ((long long)p.max_q + 127) / 128, far = nqb - ((126LL + p.window) / 128 + 1);
-    if (far <= chunk) return;
-    // The first key block's CTA is issued first and walks nqb q blocks; the others, window / 128 + 2 each,
-    // keep 152 SMs busy for total_q / 128 * H * (window / 128 + 2) / 152 of them.  Shared where the one
-    // is longer than the other.  (8 heads of 64; q blocks of the longest against that number, the backward
-    // unshared and shared: 8 sequences of 256 to 2048 tokens, window 512: 16 to 22, 95 and 104 us; 4 of 4096,
-    // window 512: 32 to 40, 173 and 179; 8192 + 4484 + 777, window 1024: 64 to 55, 216 and 204; 2 of 8192,
-    // window 256: 64 to 27, 220 and 154.)
-    const double rest = (double)p.total_q / 128 * p.H * ((double)p.window / 128 + 2) / 152;
-    if ((double)nqb < rest) return;
-    // (with a number of sinks for each sequence, the host knows none of them: the first block is shared)
-    const long long nb = p.prefix_len ? 1 : ((long long)p.prefix_all + 127) / 128, nkb = ((long long)p.max_k + 127) / 128;
-    if (nb > 4) return;  // (many key blocks see everything: they balance one another)
-    // (many short sequences beside a long one: an accumulator larger than dQ's would cost more than it saves)
-    if (p.num_seqs * nb * 2 * 128 > (long long)p.total_q) return;
-    p.sink.nb = (int)(nb < nkb ? nb : nkb);
-    p.sink.chunk = chunk;
-    p.sink.chunks = (int)((far + chunk - 1) / chunk);
+    const SinkSharing s = sink_sharing(p.num_seqs, p.total_q, p.H, p.max_q, p.max_k, p.window, p.prefix_len ? -1 : p.prefix_all);
+    p.sink.nb = s.nb;
+    p.sink.chunk = s.chunk;
+    p.sink.chunks = s.chunks;
     p.sink.elems = (long long)p.num_seqs * p.H * p.sink.nb * 2 * 128 * p.D;
 }
 

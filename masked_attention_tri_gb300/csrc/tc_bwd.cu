@@ -87,7 +87,7 @@ struct BwdTc {
     int mask_heads, MQ, MK, mask_mod, window, prefix_all;
     const int32_t* prefix_len;
     int qcap;           // entries of the q-block list in shared memory (0: triangle form)
-    // Sink window, shared first key blocks (see SinkShare): 0 blocks = off.
+    // Sink window, shared first key blocks (see sink_window.h): 0 blocks = off.
     float* sink_acc;
     int sink_nb, sink_chunk;
     unsigned far_grid;  // CTAs that take chunks of far q blocks, issued before those of the key blocks
@@ -195,11 +195,6 @@ __device__ __forceinline__ uint32_t bwd_sink_bits(int q, int k, int window, int 
     return (0xffffu << from) & ((1u << to) - 1u);
 }
 
-// First q block of chunk `far` of those past the window of the key block at k0.
-__device__ __forceinline__ long long far_first(const BwdTc& P, int k0, int far) {
-    return ((long long)k0 + 126 + P.window) / kBM + 1 + (long long)far * P.sink_chunk;
-}
-
 // WIDE: D in (64, 128] (two 64-column boxes per tile, one S^T / dP^T buffer that the query
 // halves take in turn, 32 columns of dQ / dK / dV per compute warp); otherwise D <= 64.
 // VARLEN: packed sequences, one CTA per (sequence, head, 128-key block), visiting the q blocks
@@ -278,7 +273,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
             return;
         }
         if (k0 >= Kn) return;
-        if (far >= 0 && far_first(P, k0, far) >= (Qn + kBM - 1) / kBM) return;  // no q block in this chunk
+        if (far >= 0 && sink_far_first(k0 / kBN, P.window, P.sink_chunk, far) >= (Qn + kBM - 1) / kBM) return;  // none in this chunk
         qrow0 = cq0;
         krow0 = ck0;
         tz = h;
@@ -355,14 +350,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
         if (warp == kProducerWarp) {
             uint32_t* qw = reinterpret_cast<uint32_t*>(gbase + L.qlist);
             const int kb = k0 / kBN;
-            int nqb = (Qn + kBM - 1) / kBM, qb0 = 0;
             int cnt = 0;
-            if (far >= 0) {  // this chunk of the q blocks past the key block's window
-                const long long first = far_first(P, k0, far);
-                qb0 = first < nqb ? (int)first : nqb;
-                nqb = min(nqb, qb0 + P.sink_chunk);
-            }
-            nqb = min(nqb, P.qcap);
             // Rows of q block qb without any valid key (the forward gave them the mean of V).
             auto unreached = [&](int qb) -> bool {
                 bool fm = false;
@@ -379,18 +367,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
             // warp some 15 us, more than the tiles of a short window.
             const bool sunk = !P.kv_num && P.mask_mod == TA_MASK_SINK_WINDOW;
             if (sunk) {
-                const bool all_valid = prefix > 0 || (long long)Qn - Kn < P.window;
-                if (all_valid) qb0 = max(qb0, kb * kBN / kBM);  // (earlier q blocks see no key of this block)
-                for (int q32 = qb0; q32 < nqb; q32 += 32) {
+                const QBlocks qbs = sink_q_blocks(kb, Qn, Kn, P.window, prefix, P.sink_chunk, far);
+                const int qb1 = min(qbs.qb1, P.qcap);
+                for (int q32 = qbs.qb0; q32 < qb1; q32 += 32) {
                     const int qb = q32 + lane;
                     int st = -1;  // not visited
-                    if (qb < nqb) {
-                        const SinkBlocks sb = sink_blocks(qb * kBM, min(qb * kBM + kBM, Qn) - 1, Kn, P.window, prefix);
-                        st = sb.visited(kb) ? 1 : 0;
-                        // a shared key block: its own CTA leaves the far q blocks to the chunks
-                        const bool is_far = st == 1 && !(kb >= sb.lo && kb <= sb.hi);
-                        if ((st == 0 && all_valid) || (shared_kb && is_far != (far >= 0))) st = -1;
-                    }
+                    if (qb < qb1)
+                        st = sink_q_state(qb, kb, Qn, Kn, P.window, prefix, qbs.all_valid, shared_kb, far);
                     for (uint32_t look = __ballot_sync(0xffffffffu, st == 0); look; look &= look - 1) {
                         const int i = __ffs(look) - 1;
                         const bool fm = unreached(q32 + i);
@@ -401,7 +384,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                     cnt += __popc(in);
                 }
             }
-            for (int qb = qb0; qb < nqb && !sunk; ++qb) {
+            const int nqb = sunk ? 0 : min((Qn + kBM - 1) / kBM, P.qcap);
+            for (int qb = 0; qb < nqb; ++qb) {
                 int st = 1;  // no lists: every block partial
                 if (P.kv_num) {
                     int f = 0;
