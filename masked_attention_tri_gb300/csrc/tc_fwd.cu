@@ -17,8 +17,10 @@ namespace tc {
 
 TRIATTN_TC_VARIANTS(TRIATTN_TC_EXTERN)
 TRIATTN_SPLIT_TRI_VARIANTS(TRIATTN_SPLIT_EXTERN)
-TRIATTN_SPLIT_VARLEN_VARIANTS(TRIATTN_SPLIT_EXTERN)
-TRIATTN_SPLIT_VARLEN_BIAS_VARIANTS(TRIATTN_SPLIT_EXTERN)
+TRIATTN_SPLIT_VARLEN_VARIANTS(TRIATTN_SPLIT_EXTERN, false)
+TRIATTN_SPLIT_VARLEN_VARIANTS(TRIATTN_SPLIT_EXTERN, true)
+TRIATTN_SPLIT_VARLEN_BIAS_VARIANTS(TRIATTN_SPLIT_EXTERN, false)
+TRIATTN_SPLIT_VARLEN_BIAS_VARIANTS(TRIATTN_SPLIT_EXTERN, true)
 
 namespace {
 
@@ -143,11 +145,20 @@ bool choose_split_geometry(TcParams& P, bool varlen) {
 template <bool VARLEN, bool BF16, bool BIAS_F32, bool FOLD>
 cudaError_t launch_nq(int NQ, const TcParams& P, int grid, cudaStream_t stream) {
     if constexpr (VARLEN) {
-        return NQ == 2 ? launch_kernel<2, true, BF16, false, FOLD>(P, grid, stream) : cudaErrorInvalidConfiguration;
+        if (NQ != 2) return cudaErrorInvalidConfiguration;
+        return P.a.mask_mod == TA_MASK_SINK_WINDOW ? launch_kernel<2, true, BF16, false, FOLD, true>(P, grid, stream)
+                                                   : launch_kernel<2, true, BF16, false, FOLD, false>(P, grid, stream);
     } else {
-        return NQ == 2 ? launch_kernel<2, false, BF16, BIAS_F32, FOLD>(P, grid, stream)
-                       : launch_kernel<1, false, BF16, BIAS_F32, FOLD>(P, grid, stream);
+        return NQ == 2 ? launch_kernel<2, false, BF16, BIAS_F32, FOLD, false>(P, grid, stream)
+                       : launch_kernel<1, false, BF16, BIAS_F32, FOLD, false>(P, grid, stream);
     }
+}
+
+// The key-split kernel's packed form: under a sink window, or another mask.
+template <bool BF16, bool BIAS_F32, bool FOLD, bool BIAS>
+cudaError_t launch_split_varlen(const TcParams& P, int grid, cudaStream_t stream) {
+    return P.a.mask_mod == TA_MASK_SINK_WINDOW ? launch_split<BF16, BIAS_F32, true, FOLD, BIAS, true>(P, grid, stream)
+                                               : launch_split<BF16, BIAS_F32, true, FOLD, BIAS, false>(P, grid, stream);
 }
 
 }  // namespace
@@ -271,16 +282,16 @@ cudaError_t launch_tc_fwd(const AttnParams& a, cudaStream_t stream) {
     P.fd_2g = make_fastdiv(2u * (uint32_t)grid);
 
     if (a.varlen && split && a.bias) {
-        if (bf16) return a.bias_f32 ? launch_split<true, true, true, false, true>(P, grid, stream)
-                                    : launch_split<true, false, true, false, true>(P, grid, stream);
-        return a.bias_f32 ? launch_split<false, true, true, false, true>(P, grid, stream)
-                          : launch_split<false, false, true, false, true>(P, grid, stream);
+        if (bf16) return a.bias_f32 ? launch_split_varlen<true, true, false, true>(P, grid, stream)
+                                    : launch_split_varlen<true, false, false, true>(P, grid, stream);
+        return a.bias_f32 ? launch_split_varlen<false, true, false, true>(P, grid, stream)
+                          : launch_split_varlen<false, false, false, true>(P, grid, stream);
     }
     if (a.varlen && split) {
-        if (bf16) return fold ? launch_split<true, false, true, true, false>(P, grid, stream)
-                              : launch_split<true, false, true, false, false>(P, grid, stream);
-        return fold ? launch_split<false, false, true, true, false>(P, grid, stream)
-                    : launch_split<false, false, true, false, false>(P, grid, stream);
+        if (bf16) return fold ? launch_split_varlen<true, false, true, false>(P, grid, stream)
+                              : launch_split_varlen<true, false, false, false>(P, grid, stream);
+        return fold ? launch_split_varlen<false, false, true, false>(P, grid, stream)
+                    : launch_split_varlen<false, false, false, false>(P, grid, stream);
     }
     if (a.varlen) {
         if (bf16) return fold ? launch_nq<true, true, false, true>(NQ, P, grid, stream)
@@ -290,10 +301,10 @@ cudaError_t launch_tc_fwd(const AttnParams& a, cudaStream_t stream) {
     }
     (void)fold;
     if (split) {
-        if (bf16) return a.bias_f32 ? launch_split<true, true, false, false, true>(P, grid, stream)
-                                    : launch_split<true, false, false, false, true>(P, grid, stream);
-        return a.bias_f32 ? launch_split<false, true, false, false, true>(P, grid, stream)
-                          : launch_split<false, false, false, false, true>(P, grid, stream);
+        if (bf16) return a.bias_f32 ? launch_split<true, true, false, false, true, false>(P, grid, stream)
+                                    : launch_split<true, false, false, false, true, false>(P, grid, stream);
+        return a.bias_f32 ? launch_split<false, true, false, false, true, false>(P, grid, stream)
+                          : launch_split<false, false, false, false, true, false>(P, grid, stream);
     }
     if (bf16) return a.bias_f32 ? launch_nq<false, true, true, false>(NQ, P, grid, stream)
                                 : launch_nq<false, true, false, false>(NQ, P, grid, stream);

@@ -5,10 +5,10 @@
 namespace triattn {
 namespace tc {
 
-TRIATTN_TC_INSTANTIATE(1, false, true, false, false)
-TRIATTN_TC_INSTANTIATE(1, false, true, true, false)
-TRIATTN_TC_INSTANTIATE(2, false, true, false, false)
-TRIATTN_TC_INSTANTIATE(2, false, true, true, false)
+TRIATTN_TC_INSTANTIATE(1, false, true, false, false, false)
+TRIATTN_TC_INSTANTIATE(1, false, true, true, false, false)
+TRIATTN_TC_INSTANTIATE(2, false, true, false, false, false)
+TRIATTN_TC_INSTANTIATE(2, false, true, true, false, false)
 
 }  // namespace tc
 }  // namespace triattn

@@ -5,10 +5,10 @@
 namespace triattn {
 namespace tc {
 
-TRIATTN_TC_INSTANTIATE(1, false, false, false, false)
-TRIATTN_TC_INSTANTIATE(1, false, false, true, false)
-TRIATTN_TC_INSTANTIATE(2, false, false, false, false)
-TRIATTN_TC_INSTANTIATE(2, false, false, true, false)
+TRIATTN_TC_INSTANTIATE(1, false, false, false, false, false)
+TRIATTN_TC_INSTANTIATE(1, false, false, true, false, false)
+TRIATTN_TC_INSTANTIATE(2, false, false, false, false, false)
+TRIATTN_TC_INSTANTIATE(2, false, false, true, false, false)
 
 }  // namespace tc
 }  // namespace triattn

@@ -5,7 +5,7 @@
 namespace triattn {
 namespace tc {
 
-TRIATTN_SPLIT_VARLEN_BIAS_VARIANTS(TRIATTN_SPLIT_INSTANTIATE)
+TRIATTN_SPLIT_VARLEN_BIAS_VARIANTS(TRIATTN_SPLIT_INSTANTIATE, false)
 
 }  // namespace tc
 }  // namespace triattn

@@ -5,10 +5,10 @@
 namespace triattn {
 namespace tc {
 
-TRIATTN_TC_INSTANTIATE(2, true, true, false, false)
-TRIATTN_TC_INSTANTIATE(2, true, true, false, true)
-TRIATTN_TC_INSTANTIATE(2, true, false, false, false)
-TRIATTN_TC_INSTANTIATE(2, true, false, false, true)
+TRIATTN_TC_INSTANTIATE(2, true, true, false, false, false)
+TRIATTN_TC_INSTANTIATE(2, true, true, false, true, false)
+TRIATTN_TC_INSTANTIATE(2, true, false, false, false, false)
+TRIATTN_TC_INSTANTIATE(2, true, false, false, true, false)
 
 }  // namespace tc
 }  // namespace triattn

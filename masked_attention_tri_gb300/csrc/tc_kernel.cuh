@@ -404,26 +404,30 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 //   sliding window  q - window < k <= q
 //   prefix LM       k <= q or k < prefix
 //   sink window     k <= q and (k > q - window or k < prefix)
+// SINK: the sink window, known when the kernel is compiled; else one of the others.  (One switch for all of them cost the
+// packed kernels' other masks 3 registers and 4 to 5% of their time.)
+template <bool SINK>
 __device__ __forceinline__ uint32_t mod_bits(int mod, int q, int kg, int window, int prefix) {
     const uint32_t causal = low_bits(q - kg + 1);
+    if constexpr (SINK) return causal & (~low_bits(q - window + 1 - kg) | low_bits(prefix - kg));
     switch (mod) {
     case TA_MASK_CAUSAL: return causal;
     case TA_MASK_SLIDING_WINDOW: return causal & ~low_bits(q - window + 1 - kg);
     case TA_MASK_PREFIX_LM: return causal | low_bits(prefix - kg);
-    case TA_MASK_SINK_WINDOW: return causal & (~low_bits(q - window + 1 - kg) | low_bits(prefix - kg));
     default: return 0xffffffffu;
     }
 }
 
 // True when mask_mod keeps every key of [key0, key0 + 128) for every query of
 // [q0, q0 + 128).
+template <bool SINK>
 __device__ __forceinline__ bool mod_tile_all(int mod, int q0, int key0, int window, int prefix) {
     const bool causal = key0 + 127 <= q0;
+    if constexpr (SINK) return causal && ((q0 + 127) - key0 < window || key0 + 128 <= prefix);
     switch (mod) {
     case TA_MASK_CAUSAL: return causal;
     case TA_MASK_SLIDING_WINDOW: return causal && (q0 + 127) - key0 < window;
     case TA_MASK_PREFIX_LM: return causal || key0 + 128 <= prefix;
-    case TA_MASK_SINK_WINDOW: return causal && ((q0 + 127) - key0 < window || key0 + 128 <= prefix);
     default: return true;
     }
 }
@@ -635,7 +639,7 @@ __device__ __forceinline__ void for_each_tile(const Item<NQ>& it, F&& f) {
 template <int NQ>
 constexpr int kThreads = NQ * 128 + 96;
 
-template <int NQ, bool VARLEN, bool BF16, bool BIAS_F32, bool FOLD>
+template <int NQ, bool VARLEN, bool BF16, bool BIAS_F32, bool FOLD, bool SINK>
 __global__ void __launch_bounds__(kThreads<NQ>, 1) tc_fwd_kernel(const __grid_constant__ TcParams P) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -966,7 +970,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, 1) tc_fwd_kernel(const __grid_co
                     modded = !full && a.mask_mod != TA_MASK_NONE;
                 }
                 const bool all_valid = (VARLEN || P.mask_kind != 2) && key0 + kBN <= vlim &&
-                                       (!modded || mod_tile_all(a.mask_mod, qt_s * kBM, key0, a.window, prefix_lm));
+                                       (!modded || mod_tile_all<SINK>(a.mask_mod, qt_s * kBM, key0, a.window, prefix_lm));
                 const int nexist = (VARLEN ? it.Lk : a.K) - key0;
 
                 uint32_t boff = 0, mwoff = 0;  // this row's bias / the mask words, from the aligned base
@@ -1057,7 +1061,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, 1) tc_fwd_kernel(const __grid_co
                                 if (P.mask_kind == 2)
                                     vm &= *reinterpret_cast<const uint32_t*>(gbase + mwoff + 4u * (uint32_t)(2 * c + h));
                             } else {
-                                if (modded) vm &= mod_bits(a.mask_mod, qrow, key0 + k0, a.window, prefix_lm);
+                                if (modded) vm &= mod_bits<SINK>(a.mask_mod, qrow, key0 + k0, a.window, prefix_lm);
                             }
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
@@ -1258,11 +1262,11 @@ __global__ void __launch_bounds__(kThreads<NQ>, 1) tc_fwd_kernel(const __grid_co
 
 
 
-template <int NQ, bool VARLEN, bool BF16, bool BIAS_F32, bool FOLD>
+template <int NQ, bool VARLEN, bool BF16, bool BIAS_F32, bool FOLD, bool SINK>
 cudaError_t launch_kernel(const TcParams& P, int grid, cudaStream_t stream) {
     const Layout L = make_layout(NQ, P);
     const size_t smem = L.total + 1024;
-    auto kern = tc_fwd_kernel<NQ, VARLEN, BF16, BIAS_F32, FOLD>;
+    auto kern = tc_fwd_kernel<NQ, VARLEN, BF16, BIAS_F32, FOLD, SINK>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kern<<<grid, kThreads<NQ>, smem, stream>>>(P);
@@ -1272,23 +1276,27 @@ cudaError_t launch_kernel(const TcParams& P, int grid, cudaStream_t stream) {
 // The kernel variants the host launches (each instantiated in one tc_inst_*.cu
 // file).  The folded softmax is used by the packed form only.
 #define TRIATTN_TC_VARIANTS(X)                  \
-    X(1, false, true, false, false)             \
-    X(1, false, true, true, false)              \
-    X(2, false, true, false, false)             \
-    X(2, false, true, true, false)              \
-    X(1, false, false, false, false)            \
-    X(1, false, false, true, false)             \
-    X(2, false, false, false, false)            \
-    X(2, false, false, true, false)             \
-    X(2, true, true, false, false)              \
-    X(2, true, true, false, true)               \
-    X(2, true, false, false, false)             \
-    X(2, true, false, false, true)
+    X(1, false, true, false, false, false)      \
+    X(1, false, true, true, false, false)       \
+    X(2, false, true, false, false, false)      \
+    X(2, false, true, true, false, false)       \
+    X(1, false, false, false, false, false)     \
+    X(1, false, false, true, false, false)      \
+    X(2, false, false, false, false, false)     \
+    X(2, false, false, true, false, false)      \
+    X(2, true, true, false, false, false)       \
+    X(2, true, true, false, true, false)        \
+    X(2, true, false, false, false, false)      \
+    X(2, true, false, false, true, false)       \
+    X(2, true, true, false, false, true)        \
+    X(2, true, true, false, true, true)         \
+    X(2, true, false, false, false, true)       \
+    X(2, true, false, false, true, true)
 
-#define TRIATTN_TC_EXTERN(nq, v, b, f, fo) \
-    extern template cudaError_t launch_kernel<nq, v, b, f, fo>(const TcParams&, int, cudaStream_t);
-#define TRIATTN_TC_INSTANTIATE(nq, v, b, f, fo) \
-    template cudaError_t launch_kernel<nq, v, b, f, fo>(const TcParams&, int, cudaStream_t);
+#define TRIATTN_TC_EXTERN(nq, v, b, f, fo, sk) \
+    extern template cudaError_t launch_kernel<nq, v, b, f, fo, sk>(const TcParams&, int, cudaStream_t);
+#define TRIATTN_TC_INSTANTIATE(nq, v, b, f, fo, sk) \
+    template cudaError_t launch_kernel<nq, v, b, f, fo, sk>(const TcParams&, int, cudaStream_t);
 
 }  // namespace tc
 }  // namespace triattn

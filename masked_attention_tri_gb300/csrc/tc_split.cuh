@@ -64,8 +64,6 @@ struct VEntry {
     int seq, h, qb, nkt;       // nkt < 0: no more items
     int q_row0, Lq, k_row0, Lk;
     int nkb, n_part, n_full, lists;
-    SinkBlocks sink;           // no lists, sink window: the visited blocks
-    int sunk;                  // 1: `sink` decides
     const int32_t* part_l;
     const int32_t* full_l;
     unsigned long long part0, full0;
@@ -120,8 +118,6 @@ struct SItem {
     const int32_t* part_l;
     const int32_t* full_l;
     int n_part, n_full;
-    bool sunk;          // packed form, sink window without lists: `sink` says which blocks are visited
-    SinkBlocks sink;
     uint64_t part0, full0;  // packed form: visited blocks of window 0 (blocks 0..63)
 };
 
@@ -129,8 +125,9 @@ struct SItem {
 // and `full` (mask_mod skipped).  Warp-cooperative (every lane of the warp
 // calls it and gets the same masks): lane t reads list entries t, t + 32, ...
 // pre_p / pre_f: entries `lane` of the two lists when the caller has loaded them already (else < 0).
-__device__ __forceinline__ void split_window(const SItem& it, int w, uint64_t& part, uint64_t& full, int pre_p = -1,
-                                             int pre_f = -1) {
+template <bool SINK>
+__device__ __forceinline__ void split_window(const AttnParams& a, const SItem& it, int w, uint64_t& part, uint64_t& full,
+                                             int pre_p = -1, int pre_f = -1) {
     const int lo = 64 * w;
     const int n = min(64, it.nkb - lo);
     if (n <= 0) {
@@ -141,10 +138,12 @@ __device__ __forceinline__ void split_window(const SItem& it, int w, uint64_t& p
     if (!it.lists) {
         part = range;
         full = 0;
-        if (it.sunk) {
+        if constexpr (SINK) {  // (formed again for each 64 blocks: carried with the item it would cost every role registers)
+            const SinkBlocks sb = sink_blocks(it.qt * kBM, min(it.qt * kBM + kBM, it.Lq) - 1, it.Lk, a.window,
+                                              a.prefix_len ? a.prefix_len[it.seq] : a.prefix_all);
             // bits below n of the 64 blocks from `lo`
             auto below = [&](int kb) { return kb <= lo ? 0ull : (kb - lo >= 64 ? ~0ull : (1ull << (kb - lo)) - 1ull); };
-            part &= below(it.sink.nsink) | (below(it.sink.hi + 1) & ~below(it.sink.lo));
+            part &= below(sb.nsink) | (below(sb.hi + 1) & ~below(sb.lo));
         }
         return;
     }
@@ -221,7 +220,7 @@ __device__ __forceinline__ bool vcursor_next(const TcParams& P, const int* snb, 
 
 // Triangle item from its index (kv_lengths resolved), or packed item from
 // (sequence, head, q block) with its visited-tile count (warp-cooperative).
-template <bool VARLEN>
+template <bool VARLEN, bool SINK = false>
 __device__ __forceinline__ SItem split_decode(const TcParams& P, const int* sched, int item, int seq, int h, int qb,
                                               int pre_len = kNoLen) {
     SItem it;
@@ -232,8 +231,6 @@ __device__ __forceinline__ SItem split_decode(const TcParams& P, const int* sche
     it.part0 = it.full0 = 0;
     it.prefix = 0;
     it.q_row0 = it.k_row0 = 0;
-    it.sunk = false;
-    it.sink = SinkBlocks{0, 0, -1};
     if constexpr (!VARLEN) {
         const Item<1> t = decode<1, false>(P, item, pre_len);
         it.qt = t.qt[0];
@@ -280,16 +277,11 @@ __device__ __forceinline__ SItem split_decode(const TcParams& P, const int* sche
                 if (a.full_num) it.n_full = min(max(a.full_num[row], 0), a.MK);
             }
         }
-        if (a.kv_num == nullptr && a.mask_mod == TA_MASK_SINK_WINDOW) {
-            it.sunk = true;
-            it.sink = sink_blocks(qb * kBM, min(qb * kBM + kBM, it.Lq) - 1, it.Lk, a.window,
-                                  a.prefix_len ? a.prefix_len[seq] : a.prefix_all);
-        }
-        split_window(it, 0, it.part0, it.full0, pre_p, pre_f);
+        split_window<SINK>(a, it, 0, it.part0, it.full0, pre_p, pre_f);
         int nkt = __popcll(it.part0 | it.full0);
         for (int w = 1; 64 * w < it.nkb; ++w) {
             uint64_t pm, fm;
-            split_window(it, w, pm, fm);
+            split_window<SINK>(a, it, w, pm, fm);
             nkt += __popcll(pm | fm);
         }
         it.nkt = nkt;
@@ -314,8 +306,8 @@ __device__ __forceinline__ TileWalk tiles_begin(const SItem& it) {
     return tw;
 }
 
-template <bool VARLEN>
-__device__ __forceinline__ bool tiles_next(const SItem& it, TileWalk& tw, int& kb, bool& is_full) {
+template <bool VARLEN, bool SINK>
+__device__ __forceinline__ bool tiles_next(const AttnParams& a, const SItem& it, TileWalk& tw, int& kb, bool& is_full) {
     if constexpr (!VARLEN) {
         if (tw.t >= it.nkt) return false;
         kb = tw.t++;
@@ -326,7 +318,7 @@ __device__ __forceinline__ bool tiles_next(const SItem& it, TileWalk& tw, int& k
             ++tw.w;
             if (64 * tw.w >= it.nkb) return false;
             uint64_t pm, fm;
-            split_window(it, tw.w, pm, fm);
+            split_window<SINK>(a, it, tw.w, pm, fm);
             tw.rem = pm | fm;
             tw.full = fm;
         }
@@ -399,8 +391,6 @@ struct ItemWalk<true> {
         it.full_l = v->full_l;
         it.n_part = v->n_part;
         it.n_full = v->n_full;
-        it.sunk = v->sunk != 0;
-        it.sink = v->sink;
         it.part0 = v->part0;
         it.full0 = v->full0;
         it.unit = it.bn = 0;
@@ -500,7 +490,7 @@ __device__ __forceinline__ void issue_pv_split(uint32_t d0, uint32_t d1, uint32_
     }
 }
 
-template <bool BF16, bool BIAS_F32, bool VARLEN, bool FOLD, bool BIAS>
+template <bool BF16, bool BIAS_F32, bool VARLEN, bool FOLD, bool BIAS, bool SINK>
 __global__ void __launch_bounds__(kSplitThreads, 1) tc_split_kernel(const __grid_constant__ TcParams P) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -649,7 +639,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tc_split_kernel(const __grid
             TileWalk tw = tiles_begin<VARLEN>(it);
             int kb;
             bool fb;
-            while (ok && tiles_next<VARLEN>(it, tw, kb, fb)) {
+            while (ok && tiles_next<VARLEN, SINK>(a, it, tw, kb, fb)) {
                 const int st = kr.idx;
                 if (lane == 0 && kr.wrapped) ok = wait_bar(k_empty(st), kr.ph ^ 1u, abort_flag, a.status);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -682,7 +672,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tc_split_kernel(const __grid
             TileWalk tw = tiles_begin<VARLEN>(it);
             int kb;
             bool fb;
-            while (ok && tiles_next<VARLEN>(it, tw, kb, fb)) {
+            while (ok && tiles_next<VARLEN, SINK>(a, it, tw, kb, fb)) {
                 if constexpr (VARLEN && BIAS) {
                     const int bs = br.idx;
                     if (lane == 0 && br.wrapped) ok = wait_bar(bias_empty(bs), br.ph ^ 1u, abort_flag, a.status);
@@ -742,7 +732,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tc_split_kernel(const __grid
                     if (!ok) break;
                 }
                 SItem it;
-                if (more) it = split_decode<true>(P, sched, 0, seq, hh, qb);
+                if (more) it = split_decode<true, SINK>(P, sched, 0, seq, hh, qb);
                 if (lane == 0) {
                     VEntry* e = ents + slot;
                     e->nkt = more ? it.nkt : -1;
@@ -758,8 +748,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tc_split_kernel(const __grid
                         e->n_part = it.n_part;
                         e->n_full = it.n_full;
                         e->lists = it.lists ? 1 : 0;
-                        e->sunk = it.sunk ? 1 : 0;
-                        e->sink = it.sink;
                         e->part_l = it.part_l;
                         e->full_l = it.full_l;
                         e->part0 = it.part0;
@@ -1224,7 +1212,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tc_split_kernel(const __grid
             TileWalk tw = tiles_begin<VARLEN>(it);
             int kb;
             bool is_full;
-            while (ok && tiles_next<VARLEN>(it, tw, kb, is_full)) {
+            while (ok && tiles_next<VARLEN, SINK>(a, it, tw, kb, is_full)) {
                 const int key0 = kb * kBN;
                 int vlim;
                 bool modded = false;  // mask_mod applies (a partial block)
@@ -1235,7 +1223,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tc_split_kernel(const __grid
                     modded = !is_full && a.mask_mod != TA_MASK_NONE;
                 }
                 const bool all_valid = (VARLEN || P.mask_kind != 2) && key0 + kBN <= vlim &&
-                                       (!modded || mod_tile_all(a.mask_mod, it.qt * kBM, key0, a.window, prefix_lm));
+                                       (!modded || mod_tile_all<SINK>(a.mask_mod, it.qt * kBM, key0, a.window, prefix_lm));
                 const int nexist = (VARLEN ? it.Lk : a.K) - key0;
                 int bs = 0;
                 uint32_t boff = 0, mwoff = 0;
@@ -1320,7 +1308,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tc_split_kernel(const __grid
                             if (P.mask_kind == 2)
                                 vm &= *reinterpret_cast<const uint32_t*>(gbase + mwoff + 4u * (uint32_t)(2 * h + hh));
                         } else {
-                            if (modded) vm &= mod_bits(a.mask_mod, qrow, key0 + k0, a.window, prefix_lm);
+                            if (modded) vm &= mod_bits<SINK>(a.mask_mod, qrow, key0 + k0, a.window, prefix_lm);
                         }
                         // (em and vm are uniform across the warp: the branches do not diverge)
                         if (em == 0xffffffffu) {  // every key exists: valid, or masked to -1e9
@@ -1477,30 +1465,29 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tc_split_kernel(const __grid
     }
 }
 
-template <bool BF16, bool BIAS_F32, bool VARLEN, bool FOLD, bool BIAS>
+template <bool BF16, bool BIAS_F32, bool VARLEN, bool FOLD, bool BIAS, bool SINK>
 cudaError_t launch_split(const TcParams& P, int grid, cudaStream_t stream) {
     const SplitLayout L = make_split_layout(P);
     const size_t smem = L.total + 1024;
-    auto kern = tc_split_kernel<BF16, BIAS_F32, VARLEN, FOLD, BIAS>;
+    auto kern = tc_split_kernel<BF16, BIAS_F32, VARLEN, FOLD, BIAS, SINK>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kern<<<grid, kSplitThreads, smem, stream>>>(P);
     return cudaGetLastError();
 }
 
-// Triangle form (bias dtype) and packed form (folded scale or not).
 // Triangle form (bias dtype); packed form without a bias (folded scale or not) and
-// with a post-scale bias (bias dtype).
-#define TRIATTN_SPLIT_TRI_VARIANTS(X) X(true, false, false, false, true) X(true, true, false, false, true) \
-    X(false, false, false, false, true) X(false, true, false, false, true)
-#define TRIATTN_SPLIT_VARLEN_VARIANTS(X) X(true, false, true, true, false) X(true, false, true, false, false) \
-    X(false, false, true, true, false) X(false, false, true, false, false)
-#define TRIATTN_SPLIT_VARLEN_BIAS_VARIANTS(X) X(true, false, true, false, true) X(true, true, true, false, true) \
-    X(false, false, true, false, true) X(false, true, true, false, true)
-#define TRIATTN_SPLIT_EXTERN(b, f, v, fo, bi) \
-    extern template cudaError_t launch_split<b, f, v, fo, bi>(const TcParams&, int, cudaStream_t);
-#define TRIATTN_SPLIT_INSTANTIATE(b, f, v, fo, bi) \
-    template cudaError_t launch_split<b, f, v, fo, bi>(const TcParams&, int, cudaStream_t);
+// with a post-scale bias (bias dtype), under a sink window or another mask.
+#define TRIATTN_SPLIT_TRI_VARIANTS(X) X(true, false, false, false, true, false) X(true, true, false, false, true, false) \
+    X(false, false, false, false, true, false) X(false, true, false, false, true, false)
+#define TRIATTN_SPLIT_VARLEN_VARIANTS(X, SK) X(true, false, true, true, false, SK) X(true, false, true, false, false, SK) \
+    X(false, false, true, true, false, SK) X(false, false, true, false, false, SK)
+#define TRIATTN_SPLIT_VARLEN_BIAS_VARIANTS(X, SK) X(true, false, true, false, true, SK) X(true, true, true, false, true, SK) \
+    X(false, false, true, false, true, SK) X(false, true, true, false, true, SK)
+#define TRIATTN_SPLIT_EXTERN(b, f, v, fo, bi, sk) \
+    extern template cudaError_t launch_split<b, f, v, fo, bi, sk>(const TcParams&, int, cudaStream_t);
+#define TRIATTN_SPLIT_INSTANTIATE(b, f, v, fo, bi, sk) \
+    template cudaError_t launch_split<b, f, v, fo, bi, sk>(const TcParams&, int, cudaStream_t);
 
 }  // namespace tc
 }  // namespace triattn
