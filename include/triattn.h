@@ -367,7 +367,8 @@ ta_status tri_attn_varlen_fwd_masked(const void* q, const void* k, const void* v
  *                 with_bias = dbias != NULL) bytes, 256-byte aligned, owned by
  *                 the caller.
  * Arithmetic: fp16 / bf16 inputs with D a multiple of 16 up to 128 (no bias, or
- * a bias whose max_seqlen_k rows are 16-byte multiples) run on tensor cores (one CTA per sequence, head and 128-key block, over the q
+ * a bias whose max_seqlen_k rows are 16-byte multiples; max_seqlen_q up to 27136 with a bias and D > 64, and to
+ * a million otherwise) run on tensor cores (one CTA per sequence, head and 128-key block, over the q
  * blocks whose lists hold that block and those with a row that has no valid
  * key; P and dS rounded to the input type as the MMAs' operands, fp32
  * accumulation); every other case exact fp32 on CUDA cores (one CTA per

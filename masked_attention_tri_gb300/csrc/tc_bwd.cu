@@ -46,6 +46,7 @@
 // last kernel converts.  (Packed sequences of 777, 4484 and 8192 tokens, 8 heads of 64, window
 // 1024, 4 sinks: the backward 216 us unshared, 204 shared; two of 8192, window 256: 220 and 154.)
 
+#include "bwd_layout.h"
 #include "tc_kernel.cuh"
 
 namespace triattn {
@@ -69,11 +70,8 @@ struct BwdTc {
     uint32_t idesc_s;   // M 128, N 64: K-major A and B
     uint32_t idesc_g;   // M 128, N D: A from TMEM, B MN-major
     uint32_t idesc_q;   // M 128, N D: A and B MN-major in shared memory
-    uint32_t bias_bytes;
+    BwdShape sm;        // of the shared memory
     int bias_boxes, bias_box_cols;
-    int bias_alias;     // 1: the two bias halves share one slot (an fp32 bias with D > 64)
-    int lo;             // 1: dS in two 16-bit pieces, the second at 2 boxes past the first
-    int qs;             // stages of (Q, dO, lse, delta): 2 when shared memory allows, else 1
     // Packed sequences (VARLEN): q / k / v / dO (total, H, D) and the fp32 dQ accumulator read
     // through (D, total, H) maps, lse / delta (H, total_q), the BlockMask lists, an optional
     // bias (H, max_q, max_k) at local indices (dBias summed over the sequences).
@@ -86,44 +84,11 @@ struct BwdTc {
     const int32_t* full_idx;
     int mask_heads, MQ, MK, mask_mod, window, prefix_all;
     const int32_t* prefix_len;
-    int qcap;           // entries of the q-block list in shared memory (0: triangle form)
     // Sink window, shared first key blocks (see sink_window.h): 0 blocks = off.
     float* sink_acc;
     int sink_nb, sink_chunk;
     unsigned far_grid;  // CTAs that take chunks of far q blocks, issued before those of the key blocks
 };
-
-// Shared memory (offsets from a 1024-byte aligned base).
-// Stage s of the query-tile ring: Q at q + s * 2 tile, dO after it; the rows' -lse log2e, -delta and lse
-// (128 floats each) at lse + s * bwd_row_bytes
-// (tile = nsub boxes of 128 rows x 128 bytes).
-struct BwdLayout {
-    uint32_t k, v, q, ds, bias, dqst, lse, qlist, bars, tmem_slot, abort_flag, qn, total;
-};
-// kv_full, q_full[2], q_empty[2], lse_full[2], bias_full[2], bias_empty[2], s_full[2], p_full[2],
-// dq_full, dq_empty, ds_free, fin, drain
-constexpr int kBwdBars = 20;
-// An fp32 bias with D > 64 leaves no room for the lse row: it is read from global memory where it is needed.
-__host__ __device__ inline uint32_t bwd_row_bytes(bool alias) { return (alias ? 2u : 3u) * kBM * 4; }
-// nsub: the kernel passes its compile-time box count, so that the offsets fold into constants.
-__host__ __device__ inline BwdLayout bwd_layout(const BwdTc& P, int nsub) {
-    BwdLayout L;
-    const uint32_t tile = (uint32_t)nsub * kBox;  // one 128-row tile of D columns
-    L.k = 0;
-    L.v = L.k + tile;
-    L.q = L.v + tile;
-    L.ds = L.q + (uint32_t)P.qs * 2 * tile;  // dS as [key][query]: two 64-query boxes
-    L.bias = L.ds + (P.lo ? 4 : 2) * kBox;
-    L.dqst = L.bias + (P.bias_alias ? P.bias_bytes / 2u : P.bias_bytes);  // dQ staging: 16 warps x 32 rows x 16 fp32
-    L.lse = L.dqst + 16u * 2048u;
-    L.qlist = L.lse + (uint32_t)P.qs * bwd_row_bytes(P.bias_alias != 0);  // packed form: the q blocks the key tile visits
-    L.bars = L.qlist + (((uint32_t)P.qcap * 4u + 15u) & ~15u);
-    L.tmem_slot = L.bars + 8 * kBwdBars;
-    L.abort_flag = L.tmem_slot + 4;
-    L.qn = L.abort_flag + 4;                   // packed form: entries of the q-block list
-    L.total = L.qn + 4;
-    return L;
-}
 
 // TMA reduce-add (fp32 add into global) of a shared-memory box.
 __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* tm, uint32_t src, int c0, int c1, int c2) {
@@ -210,7 +175,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw);
-    const BwdLayout L = bwd_layout(P, kNsub);
+    const BwdLayout L = bwd_layout(P.sm, kNsub);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L.abort_flag);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L.tmem_slot);
@@ -230,7 +195,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
     // bias rows [64 hh, 64 hh + 64) of the tile: boxes of bias_box_cols keys x 64 rows (8 KB each)
     // An fp32 bias with D > 64: both halves in one slot, used in the order (j, 0), (j, 1), (j + 1, 0).
     constexpr bool kAlias = WIDE && BIAS_F32;
-    auto bias_half = [&](int hh) { return base + L.bias + (kAlias ? 0u : (uint32_t)hh * (P.bias_bytes / 2u)); };
+    // (known when the kernel is compiled but for packed sequences, whose q-block list may take its place)
+    const bool lse_row = !kAlias && (!VARLEN || P.sm.lse_row != 0);
+    auto bias_half = [&](int hh) { return base + L.bias + (kAlias ? 0u : (uint32_t)hh * (P.sm.bias_bytes / 2u)); };
 
     // The key tile's unit.  Triangle form: slab unit = (b*N + n)*H + h, Qn x Kn = Q x K.
     // Packed form: sequence seq and head h, Qn x Kn = its lengths.  Rows go through the maps
@@ -368,7 +335,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
             const bool sunk = !P.kv_num && P.mask_mod == TA_MASK_SINK_WINDOW;
             if (sunk) {
                 const QBlocks qbs = sink_q_blocks(kb, Qn, Kn, P.window, prefix, P.sink_chunk, far);
-                const int qb1 = min(qbs.qb1, P.qcap);
+                const int qb1 = min(qbs.qb1, P.sm.qcap);
                 for (int q32 = qbs.qb0; q32 < qb1; q32 += 32) {
                     const int qb = q32 + lane;
                     int st = -1;  // not visited
@@ -384,7 +351,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                     cnt += __popc(in);
                 }
             }
-            const int nqb = sunk ? 0 : min((Qn + kBM - 1) / kBM, P.qcap);
+            const int nqb = sunk ? 0 : min((Qn + kBM - 1) / kBM, P.sm.qcap);
             for (int qb = 0; qb < nqb; ++qb) {
                 int st = 1;  // no lists: every block partial
                 if (P.kv_num) {
@@ -435,8 +402,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
         }
     }
     // the stage of tile j and how often the ring has gone round (one or two stages)
-    auto stage_of = [&](int j) -> int { return j & (P.qs - 1); };
-    auto use_of = [&](int j) -> int { return j >> (P.qs - 1); };
+    auto stage_of = [&](int j) -> int { return j & (P.sm.qs - 1); };
+    auto use_of = [&](int j) -> int { return j >> (P.sm.qs - 1); };
     // the first query row (within the unit) and the status of entry j of the tile walk
     auto tile_q0 = [&](int j) -> int {
         if constexpr (VARLEN) return (int)(qlist[j] & 0xffffffu) * kBM;
@@ -481,7 +448,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                     return false;
                 }
                 if (lane == 0) {
-                    mbar_expect_tx(bias_full(hh), P.bias_bytes / 2u);
+                    mbar_expect_tx(bias_full(hh), P.sm.bias_bytes / 2u);
                     for (int bx = 0; bx < P.bias_boxes; ++bx)
                         tma_load_3d(bias_half(hh) + (uint32_t)bx * 8192u, &P.tm_bias, k0 + bx * P.bias_box_cols,
                                     q0 + 64 * hh, bz, bias_full(hh));
@@ -519,7 +486,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                 }
                 if (!ok) break;
             } else {
-                if (j >= P.qs) {  // stage st held tile j - qs: its MMAs and its compute are done
+                if (j >= P.sm.qs) {  // stage st held tile j - qs: its MMAs and its compute are done
                     ok = __all_sync(0xffffffffu,
                                     wait_bar(q_empty(st), (uint32_t)(use - 1) & 1u, abort_flag, P.status));
                     if (!ok) break;
@@ -542,12 +509,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                 }
             }
             // (the factor and the signs here, once a row, and not once an element)
-            float* nl_s = reinterpret_cast<float*>(gbase + L.lse + (uint32_t)st * bwd_row_bytes(kAlias));
+            float* nl_s = reinterpret_cast<float*>(gbase + L.lse + (uint32_t)st * bwd_row_bytes(lse_row));
 #pragma unroll
             for (int t = 0; t < kBM / 32; ++t) {
                 nl_s[lane + 32 * t] = lv[t] * -kLog2e;
                 nl_s[kBM + lane + 32 * t] = -dv[t];
-                if constexpr (!kAlias) nl_s[2 * kBM + lane + 32 * t] = lv[t];
+                if (lse_row) nl_s[2 * kBM + lane + 32 * t] = lv[t];
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(lse_full(st));  // release: the rows are written
@@ -655,7 +622,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                     if (hh == 0) ok = mma1(j, 1);
                     else if (j + 1 < nqt) ok = mma1(j + 1, 0);
                 } else if (j + 1 < nqt) {
-                    if (P.qs > 1) ok = mma1(j + 1, hh);
+                    if (P.sm.qs > 1) ok = mma1(j + 1, hh);
                     else if (hh == 1) ok = mma1(j + 1, 0) && mma1(j + 1, 1);
                 }
             }
@@ -768,7 +735,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
         for (int j = 0; j < nqt && ok; ++j) {
             const uint32_t ph = (uint32_t)j & 1u;
             const int q0 = tile_q0(j), st = stage_of(j), tst = tile_st(j);
-            const float* nl_s = reinterpret_cast<const float*>(gbase + L.lse + (uint32_t)st * bwd_row_bytes(kAlias));
+            const float* nl_s = reinterpret_cast<const float*>(gbase + L.lse + (uint32_t)st * bwd_row_bytes(lse_row));
             const float* nd_s = nl_s + kBM;
             const float* lse_s = nl_s + 2 * kBM;
             ok = __all_sync(0xffffffffu, wait_bar(lse_full(st), (uint32_t)use_of(j) & 1u, abort_flag, P.status));
@@ -925,7 +892,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) tc_bwd_kernel(const __grid_con
                                 const bool live = exists && ii < nq;
                                 const bool ve = VARLEN ? ((vm >> ii) & 1u) != 0u : valid;
                                 float row_lse = 0.f;
-                                if constexpr (!kAlias) row_lse = lse_s[ql + ii];
+                                if (lse_row) row_lse = lse_s[ql + ii];
                                 else if (live) row_lse = P.lse[lrow0 + q0 + ql + ii];
                                 const float p = live ? bwd_weight(__uint_as_float(sr[ii]), row_lse, inv_k) : 0.f;
                                 const float ds = (live && ve) ? p * (__uint_as_float(dr[ii]) + (u ? nd[i / 2].y : nd[i / 2].x)) : 0.f;
@@ -1043,6 +1010,12 @@ uint32_t bwd_idesc(bool bf16, int M, int N, bool a_mn, bool b_mn) {
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// Packed sequences: the q-block list of the longest must fit beside the tiles.  The triangle form has a bias always.
+bool shape_of(const BwdParams& p, BwdShape& s) {
+    const int bias = p.bias ? (p.bias_f32 ? 4 : 2) : 0;
+    return bwd_shape(s, p.D, bias, p.varlen ? p.max_q : -1, p.varlen && !p.bias && p.mask_mod == TA_MASK_SINK_WINDOW);
+}
+
 }  // namespace
 }  // namespace tc
 
@@ -1050,29 +1023,14 @@ bool tc_bwd_supported(const BwdParams& p) {
     if (p.dtype == TA_F32) return false;
     const bool d_ok = p.D == 16 || p.D == 32 || p.D == 64 || (p.D % 16 == 0 && p.D > 64 && p.D <= 128);
     if (!d_ok) return false;
-    tc::BwdTc t;
-    memset(&t, 0, sizeof(t));
-    t.nsub = (p.D + 63) / 64;
-    t.qs = 1;
-    t.D = p.D;
     if (p.varlen) {
-        // Packed sequences; the q-block list of the longest sequence must fit beside the tiles.
         // A bias (H, max_q, max_k) is read through a tensor map: its rows must be 16-byte multiples.
-        t.qcap = (p.max_q + tc::kBM - 1) / tc::kBM;
-        if (p.bias) {
-            if (p.max_q <= 0 || p.max_k <= 0 || ((long long)p.max_k * (p.bias_f32 ? 4 : 2)) % 16 != 0) return false;
-            t.bias_bytes = (uint32_t)(tc::kBN / (p.bias_f32 ? 32 : 64)) * tc::kBox;
-            t.bias_alias = p.D > 64 && p.bias_f32 ? 1 : 0;
-        }
-        return tc::bwd_layout(t, t.nsub).total + 1024 <= 232448;
+        if (p.bias && (p.max_q <= 0 || p.max_k <= 0 || ((long long)p.max_k * (p.bias_f32 ? 4 : 2)) % 16 != 0)) return false;
+    } else if (p.K % 8 != 0) {
+        return false;
     }
-    if (p.K % 8 != 0) return false;
-    if (p.D <= 64) return true;
-    // D in (64, 128]: two-box tiles, one Q / dO stage; an fp32 bias tile fits beside them as
-    // one half at a time.
-    t.bias_bytes = (uint32_t)(tc::kBN / (p.bias_f32 ? 32 : 64)) * tc::kBox;
-    t.bias_alias = p.bias_f32 ? 1 : 0;
-    return tc::bwd_layout(t, t.nsub).total + 1024 <= 232448;
+    tc::BwdShape t;
+    return tc::shape_of(p, t);
 }
 
 cudaError_t launch_tc_bwd_main(const BwdParams& p, cudaStream_t stream) {
@@ -1088,8 +1046,6 @@ cudaError_t launch_tc_bwd_main(const BwdParams& p, cudaStream_t stream) {
     const auto sw128 = CU_TENSOR_MAP_SWIZZLE_128B;
     P.bias_box_cols = p.bias_f32 ? 32 : 64;
     P.bias_boxes = kBN / P.bias_box_cols;
-    P.bias_bytes = (uint32_t)P.bias_boxes * kBox;
-    P.bias_alias = D > 64 && p.bias && p.bias_f32 ? 1 : 0;
     const uint64_t eb = p.bias_f32 ? 4 : 2;
     const int qbox = D > 64 ? kBM / 2 : kBM;  // D > 64: Q / dO rows loaded per query half
     const bool vl = p.varlen != 0;
@@ -1134,7 +1090,6 @@ cudaError_t launch_tc_bwd_main(const BwdParams& p, cudaStream_t stream) {
     P.nkt = vl ? (p.max_k + kBN - 1) / kBN : (p.K + kBN - 1) / kBN;
     P.nqt = vl ? 0 : (p.Q + kBM - 1) / kBM;  // packed form: per key tile, from its q-block list
     if (vl) {
-        P.bias_bytes = p.bias ? (uint32_t)P.bias_boxes * kBox : 0;  // 0: no bias
         P.dbias_acc = p.bias ? p.dbias_acc : nullptr;
         P.cu_q = p.cu_q;
         P.cu_k = p.cu_k;
@@ -1154,7 +1109,6 @@ cudaError_t launch_tc_bwd_main(const BwdParams& p, cudaStream_t stream) {
         P.window = p.window;
         P.prefix_len = p.prefix_len;
         P.prefix_all = p.prefix_all;
-        P.qcap = (p.max_q + kBM - 1) / kBM;
     }
     P.ksteps = D / 16;
     P.nsub = (D + 63) / 64;
@@ -1173,19 +1127,14 @@ cudaError_t launch_tc_bwd_main(const BwdParams& p, cudaStream_t stream) {
         grid += far;
     }
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    P.qs = D > 64 ? 1 : 2;  // D > 64: one stage, taken per query half
-    if (bwd_layout(P, P.nsub).total + 1024 > 232448) P.qs = 1;  // the 227 KB per-block limit
     // Roundings.  P and dS enter their products in the inputs' type, like P in the forward: half a step each, so
     // dK, dQ and dV are off by about sqrt(2) times their own rounding.  dS also holds delta's error (the sums come
     // from the rounded O), and a short window averages neither out; so under a sink window dS is two
-    // pieces of that type where they fit beside the tiles (D <= 64, or 80 q blocks): of dQ's and dK's norm
+    // pieces of that type where they fit beside the tiles (D <= 64, or 84 q blocks): of dQ's and dK's norm
     // 0.0018 in place of 0.0025 in bf16, for 214 us in place of 204 on packed 777 + 4484 + 8192 tokens, 8 heads
     // of 64, window 1024 (heads of 128: 390 and 351).  (The other masks keep their results to the bit.)
-    if (vl && !p.bias && p.mask_mod == TA_MASK_SINK_WINDOW) {
-        P.lo = 1;
-        if (bwd_layout(P, P.nsub).total + 1024 > 232448) P.lo = 0;
-    }
-    const size_t smem = bwd_layout(P, P.nsub).total + 1024;
+    if (!shape_of(p, P.sm)) return cudaErrorInvalidValue;
+    const size_t smem = bwd_layout(P.sm, P.nsub).total + kBwdAlign;
     // <BF16, BIAS_F32, WIDE, VARLEN, HASB, LO>; the triangle form always has a bias
     const bool fb = p.bias_f32 != 0;
     decltype(&tc_bwd_kernel<true, false, false, false, true, false>) kern;
@@ -1194,7 +1143,7 @@ cudaError_t launch_tc_bwd_main(const BwdParams& p, cudaStream_t stream) {
                               : (fb ? tc_bwd_kernel<false, true, true, false, true, false> : tc_bwd_kernel<false, false, true, false, true, false>))
              : bf16   ? (fb ? tc_bwd_kernel<true, true, false, false, true, false> : tc_bwd_kernel<true, false, false, false, true, false>)
                       : (fb ? tc_bwd_kernel<false, true, false, false, true, false> : tc_bwd_kernel<false, false, false, false, true, false>);
-    else if (P.lo)
+    else if (P.sm.lo)
         kern = D > 64 ? (bf16 ? tc_bwd_kernel<true, false, true, true, false, true> : tc_bwd_kernel<false, false, true, true, false, true>)
                       : (bf16 ? tc_bwd_kernel<true, false, false, true, false, true> : tc_bwd_kernel<false, false, false, true, false, true>);
     else if (!p.bias)
