@@ -510,7 +510,7 @@ ta_status tri_attn_kv_append(const void* q, const void* k, const void* v, ta_dty
  *   lse           optional (Hq, total_q) fp32.
  *   workspace     device scratch of tri_attn_paged_workspace_size(...) bytes, 256-byte aligned,
  *                 owned by the caller; its contents on entry are ignored.  Two
- *                 calls in flight must not share it.
+ *                 calls in flight must not share it.  (NULL where it needs none.)
  * A row that sees no slot (a sequence that holds nothing) gets O = 0 and lse = -inf.
  * Slots that no row of the call sees may hold anything, NaN included.  With several
  * rows of one sequence, a slot that some of them see has to hold finite values of v.

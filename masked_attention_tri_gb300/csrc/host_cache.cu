@@ -197,7 +197,7 @@ TA_EXPORT ta_status tri_attn_paged_fwd(const void* q, ta_dtype dtype, const int3
                                        int num_pages, int page_size, int max_pages, const long long* k_strides,
                                        const long long* v_strides, void* out, float* lse, void* workspace,
                                        size_t workspace_bytes, void* stream) {
-    if (!q || !out || !kv_lengths || !page_table || !workspace) return TA_ERR_INVALID_ARG;
+    if (!q || !out || !kv_lengths || !page_table) return TA_ERR_INVALID_ARG;
     if (num_seqs <= 0 || total_q < 0 || max_seqlen_q < 0 || Hq <= 0 || Hk <= 0 || D <= 0 || Hq % Hk != 0)
         return TA_ERR_INVALID_ARG;
     if (!cu_seqlens_q && (total_q != num_seqs || max_seqlen_q != 1)) return TA_ERR_INVALID_ARG;
@@ -215,7 +215,8 @@ TA_EXPORT ta_status tri_attn_paged_fwd(const void* q, ta_dtype dtype, const int3
     if ((long long)total_q * Hq > 0x7fffffffLL || (long long)max_seqlen_q * Hq > 0x7fffffffLL)
         return TA_ERR_UNSUPPORTED;
     if (total_q == 0 || max_seqlen_q == 0) return TA_OK;
-    if (workspace_bytes < tri_attn_paged_workspace_size(dtype, max_seqlen_q, Hq, Hk, D)) return TA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < tri_attn_paged_workspace_size(dtype, max_seqlen_q, Hq, Hk, D))
+        return TA_ERR_INVALID_ARG;
     p.q = q;
     p.k_cache = k_cache;
     p.v_cache = v_cache;
