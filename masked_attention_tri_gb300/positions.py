@@ -157,25 +157,26 @@ def rotary_embedding_backward(d_q, d_k, positions, rotary: Rotary, *, out_q=None
 
 class _RotaryFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, positions, rotary):
+    def forward(ctx, q, k, positions, rotary, inverse):
         ctx.save_for_backward(positions)
-        ctx.rotary = rotary
-        return rotary_embedding(q, k, positions, rotary)
+        ctx.rotary, ctx.inverse = rotary, inverse
+        return _rotary_call(q, k, positions, rotary, inverse, None, None)
 
     @staticmethod
     def backward(ctx, d_q, d_k=None):
+        # (the turn is linear: its gradient is the opposite turn, itself differentiable, for second derivatives)
         (positions,) = ctx.saved_tensors
         if d_k is None:
-            return rotary_embedding_backward(d_q.contiguous(), None, positions, ctx.rotary), None, None, None
-        d_q, d_k = rotary_embedding_backward(d_q.contiguous(), d_k.contiguous(), positions, ctx.rotary)
-        return d_q, d_k, None, None
+            return _RotaryFn.apply(d_q.contiguous(), None, positions, ctx.rotary, not ctx.inverse), None, None, None, None
+        d_q, d_k = _RotaryFn.apply(d_q.contiguous(), d_k.contiguous(), positions, ctx.rotary, not ctx.inverse)
+        return d_q, d_k, None, None, None
 
 
 def rotary_embedding_autograd(q, k: Optional[torch.Tensor], positions, rotary: Rotary):
-    """``rotary_embedding`` with gradients for q and k.
+    """``rotary_embedding`` with gradients for q and k, of any order.
 
     Its backward may be captured into a graph, as any autograd function's, only while no
     graph of the same leaves made outside the capture lives (PyTorch ties the leaves'
     accumulation to the stream of the first).
     """
-    return _RotaryFn.apply(q, k, positions, rotary)
+    return _RotaryFn.apply(q, k, positions, rotary, False)
