@@ -361,7 +361,9 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
     const uint32_t v_off1 = r1 * 128u + (((uint32_t)(g >> 1) ^ r1) << 4) + (g & 1) * 8u;
     const uint32_t v_row = (uint32_t)pi8(lane & 7) + ((lane & 16) ? 8u : 0u);
     const uint32_t v_offt = v_row * 128u + ((((uint32_t)lane >> 3 & 1u) ^ (v_row & 7u)) << 4);
-    constexpr float kNone = -1e30f;  // reference of a row that has seen no key
+    // Reference of a row that has seen no key: below the logits of any finite bf16 rows whose sums fp32 holds (far above
+    // it a difference from it overflows to an infinity, which is a new maximum like any other).
+    constexpr float kNone = -3e38f;
     uint32_t idx = 0;
     bool ok = true;
     long long at = sh.begin;

@@ -36,3 +36,31 @@ def test_no_sequence_has_a_new_token(dtype):
     r, lse = ta.paged_attention(q, cache, _i32([[0], [1]]), _i32([3, 0]), _i32([0, 0, 0]), 0, out=out, return_aux=True)
     torch.cuda.synchronize()
     assert r is out and bool((out == 7.0).all()) and lse.shape == (2, 3) and ta.get_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,cdtype", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32),
+                                          (torch.bfloat16, torch.float8_e4m3fn), (torch.float32, torch.float8_e4m3fn)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_logits_far_below_zero(dtype, cdtype, D):
+    """Every logit of a row far below zero, and of another far above; the largest alone counts.  The sums behind them,
+    2 D mag at most, stay below fp32's 2^128."""
+    import masked_attention_tri_gb300 as ta
+    n, P = 40, 16
+    e4 = cdtype == torch.float8_e4m3fn
+    k = torch.full((3, 1, P, D), -1.0)
+    k[0, 0, 3] = -0.5                        # slot 3 has the largest logit of a positive row
+    k[1, 0, 5] = -2.0                        # slot 21 that of a negative one
+    v = torch.arange(3 * P).view(3, 1, P, 1).expand(3, 1, P, D) / 4.0
+    for mag in (2.0 ** 110, 2.0 ** 118):
+        ks = 2.0 ** 20 if e4 else 1.0
+        cache = ta.PagedKVCache(*(x.contiguous().to(cdtype).cuda() for x in (k, v)),
+                                *((torch.full((3, 1), ks, device="cuda"), torch.ones(3, 1, device="cuda")) if e4 else ()))
+        q = torch.stack([torch.full((2, D), mag / ks), torch.full((2, D), -mag / ks)]).to(dtype).cuda()
+        o, lse = ta.paged_attention(q, cache, _i32([[0, 1, 2], [0, 1, 2]]), _i32([n, n]), return_aux=True)
+        torch.cuda.synchronize()
+        assert ta.get_status() == 0
+        for i, (slot, x) in enumerate(((3, -0.5), (21, 2.0))):
+            assert bool((o[i].float() == v[slot // P, 0, slot % P].to(cdtype).to(dtype).float().cuda()).all()), (mag, i, o[i, 0, 0])
+            want = x * mag * D ** 0.5
+            assert bool(((lse[:, i].double() - want).abs() <= 2.0 ** -20 * abs(want)).all())
