@@ -505,8 +505,9 @@ ta_status tri_attn_kv_append(const void* q, const void* k, const void* v, ta_dty
  *   window        0: every slot up to the token's own.  >= 1: the last `window` of
  *                 them (slots k > p - window) and the first `sinks` of the sequence
  *                 (sinks >= 0; ignored without a window).
- *   k_cache .. v_strides   as in tri_attn_kv_append.  Scales of an 8-bit cache:
- *                 any positive fp32 values.
+ *   k_cache .. v_strides   as in tri_attn_kv_append.  Scales of an 8-bit cache: any finite
+ *                 k_scale; v_scale from 2^-56 to 2^56, the range that tri_attn_kv_append writes.  (Where
+ *                 a row sees pages whose v_scale differ by a factor r, weights below r 2^-126 of its largest may be lost.)
  *   lse           optional (Hq, total_q) fp32.
  *   workspace     device scratch of tri_attn_paged_workspace_size(...) bytes, 256-byte aligned,
  *                 owned by the caller; its contents on entry are ignored.  Two
@@ -515,7 +516,7 @@ ta_status tri_attn_kv_append(const void* q, const void* k, const void* v, ta_dty
  * Slots that no row of the call sees may hold anything, NaN included.  With several
  * rows of one sequence, a slot that some of them see has to hold finite values of v.
  * Results do not vary from run to run.  A sequence that breaks the contract
- * (offsets; a length below 0 or beyond its table, read as 0) or a page out of range (its slots
+ * (offsets; a length below 0 or beyond its table, read as 0), a page out of range or a v_scale out of range (its slots
  * are not seen) records TA_ERR_DEVICE.  Errors as tri_attn_kv_append.
  */
 ta_status tri_attn_paged_fwd(const void* q, ta_dtype dtype, const int32_t* cu_seqlens_q, const int32_t* kv_lengths,

@@ -20,7 +20,9 @@
 //
 // Scales of 8-bit pages.  Keys: a factor on the logit.  Values: 2^log2(vs) joins the
 // exponent, x' = x + log2 vs, so the weights 2^(x' - m') multiply the bare codes and
-// their maximum m' is the largest weighted page's; the sum takes 2^(x' - m') / vs.
+// their maximum m' is the largest weighted page's; the sum takes 2^(x' - m') / vs.  That wants vs in the range that
+// kv_append.cu writes, 2^-56 to 2^56: then no sum passes fp32, and what a weight loses below 2^-126 is less than
+// 2^-126 of the ratio of the row's largest and smallest vs (2^-14 of the largest weight at worst).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -121,6 +123,9 @@ __device__ __forceinline__ bool sees(const PagedParams& p, int pos, int key) {
 __device__ __forceinline__ bool unit_sees(const PagedParams& p, const Tiles& t, int key) {
     return key <= t.p1 && (p.window <= 0 || (long long)t.p0 - key < p.window || key < p.sinks);
 }
+
+// A value scale that the kernels take (a NaN is none).
+__device__ __forceinline__ bool v_scale_ok(float vs) { return vs >= 0x1p-56f && vs <= 0x1p56f; }
 
 // The CTA's share: tiles [begin, end) of the axis and the unit that begin falls in.  Every
 // thread of the block calls it; scan is shared scratch of one long long a warp.

@@ -283,7 +283,9 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
         if (have) check_and_scale();
         while (have) {
             // What each lane's tile needs, made ready for all of them at once.
-            const int page = page_n, key = key_n, h = u.h;
+            const bool v_ok = !kCodes || page_n < 0 || v_scale_ok(vs_n);  // (else its slots are not seen)
+            if (!v_ok) atomicCAS(p.status, 0, kStatusDevice);
+            const int page = v_ok ? page_n : -1, key = key_n, h = u.h;
             const float4 sc = kCodes ? make_float4(ks_n, log2f(vs_n), 1.f / vs_n, 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
             uint32_t valid = page >= 0 ? ((1u << blocks) - 1u) << (mysub * blocks) : 0u;
             int loads = page >= 0 ? 1 : 0;

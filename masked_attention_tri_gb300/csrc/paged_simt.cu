@@ -94,6 +94,10 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
                 if constexpr (sizeof(C) == 1) {
                     kscale *= p.k_scale[page * p.Hk + u.h];
                     const float v = p.v_scale[page * p.Hk + u.h];
+                    if (!v_scale_ok(v)) {
+                        if (lane == 0) atomicCAS(p.status, 0, kStatusDevice);
+                        continue;
+                    }
                     vs_inv = 1.f / v;
                     vs_log2 = log2f(v);
                 }

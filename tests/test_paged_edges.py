@@ -64,3 +64,35 @@ def test_logits_far_below_zero(dtype, cdtype, D):
             assert bool((o[i].float() == v[slot // P, 0, slot % P].to(cdtype).to(dtype).float().cuda()).all()), (mag, i, o[i, 0, 0])
             want = x * mag * D ** 0.5
             assert bool(((lse[:, i].double() - want).abs() <= 2.0 ** -20 * abs(want)).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_value_scales_at_and_past_their_range(dtype):
+    """2^-56 and 2^56 beside 1: every weight counts (32 equal logits, so each weight is 2^-5 and O the mean over pages);
+    past them, zero, NaN and infinity: the page's slots are not seen, and the status says so."""
+    import math
+
+    import masked_attention_tri_gb300 as ta
+    F8, D = torch.float8_e4m3fn, 64
+    k = torch.zeros(3, 1, 16, D, device="cuda").to(F8)
+    v = torch.ones(3, 1, 16, D, device="cuda").to(F8)
+    ks = torch.ones(3, 1, device="cuda")
+    q = torch.ones(1, 2, D, device="cuda").to(dtype)
+    call = lambda vs, pages, n: ta.paged_attention(q, ta.PagedKVCache(k, v, ks, vs), _i32([pages]), _i32([n]), return_aux=True)  # noqa: E731
+    for scale in (2.0 ** -56, 1.0, 2.0 ** 56):
+        vs = torch.tensor([[1.0], [scale], [1.0]], device="cuda")
+        o, lse = call(vs, [0, 1], 32)
+        assert ta.get_status() == 0
+        want = torch.tensor((1 + scale) / 2).to(dtype).float()       # (2^55 is an infinity in fp16)
+        assert bool((o.float().cpu() == want).all()) or abs(float(o[0, 0, 0]) / float(want) - 1) <= 2.0 ** -11
+        assert float((lse.double().cpu() - math.log(32)).abs().max()) <= 2.0 ** -19
+    for bad in (2.0 ** -57, 2.0 ** 57, 1e-40, 0.0, -1.0, math.nan, math.inf):
+        vs = torch.tensor([[1.0], [bad], [1.0]], device="cuda")
+        o, lse = call(vs, [0, 1, 2], 48)
+        assert ta.get_status() == abi.TA_ERR_DEVICE
+        assert bool((o == 1).all()) and float((lse.double().cpu() - math.log(32)).abs().max()) <= 2.0 ** -19
+        o, lse = call(vs, [1], 7)
+        assert ta.get_status() == abi.TA_ERR_DEVICE and bool((o == 0).all()) and bool((lse == -math.inf).all())
+        call(vs, [0, 2, 1], 32)                                      # a page that no row sees may have any
+        assert ta.get_status() == 0
