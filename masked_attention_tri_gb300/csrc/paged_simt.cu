@@ -300,7 +300,9 @@ template <typename C>
 cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
     const size_t smem = (size_t)kWarps * kRows * (p.D + 2) * 4;
     auto kern = p.D <= 128 ? paged_simt_kernel<C, 1> : paged_simt_kernel<C, 2>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the limit of the kernel's widest heads, whatever this call's: two threads' calls may come between one another)
+    const int most = kWarps * kRows * ((p.D <= 128 ? 128 : 256) + 2) * 4;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     kern<<<kGrid, kThreads, smem, stream>>>(p);
     return cudaGetLastError();
