@@ -49,6 +49,15 @@ int num_sms() {
     return g_num_sms[dev];
 }
 
+// Encodes a tensor map.  The driver wants the device's context bound to the calling thread, which only the
+// runtime's own calls do: where the first thing a host thread does is a call of this library, the first attempt fails.
+template <typename... A>
+bool encode(A... args) {
+    if (g_encode(args...) == CUDA_SUCCESS) return true;
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && g_encode(args...) == CUDA_SUCCESS;
+}
+
 // 3-D tiled map: dims {d0, d1, d2} (d0 innermost), byte strides of d1 and d2,
 // box {b0, b1, b2}; 128-byte swizzle unless given, out-of-range elements read
 // as zero (and are not written by a store).
@@ -59,9 +68,8 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t 
     cuuint64_t strides[2] = {s1, s2};
     cuuint32_t box[3] = {b0, b1, b2};
     cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = g_encode(m, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    return encode(m, dt, 3u, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // 5-D tiled map of a triangle-form q / k / v: dims {D, rows, H, N, B} with the
@@ -72,10 +80,8 @@ bool make_map5(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t
     cuuint64_t strides[4] = {(cuuint64_t)st[3] * 2, (cuuint64_t)st[2] * 2, (cuuint64_t)st[1] * 2, (cuuint64_t)st[0] * 2};
     cuuint32_t box[5] = {64, 128, 1, 1, 1};
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-    CUresult r = g_encode(m, dt, 5, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    return encode(m, dt, 5u, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // Instruction descriptor of kind::f16: D fp32 at [4,6), A/B type at [7,10) /
@@ -178,8 +184,8 @@ bool encode_map_4d(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, cons
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     for (int i = 0; i < 4; ++i) d[i] = dims[i], b[i] = box[i];
     for (int i = 0; i < 3; ++i) st[i] = strides[i];
-    return g_encode(m, dt, 4, const_cast<void*>(ptr), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(m, dt, 4u, const_cast<void*>(ptr), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 int device_sm_count() { return num_sms(); }
 
