@@ -11,7 +11,7 @@ namespace triattn {
 namespace tc {
 
 constexpr uint32_t kBwdBox = 128 * 128;        // one [128 rows][128 B] box
-constexpr uint32_t kBwdMaxSmem = 232448;       // 227 KB, what a block may have
+constexpr uint32_t kBwdMaxSmem = 232448;       // 227 KB, what a block may have (kMaxDynamicSmem)
 constexpr uint32_t kBwdAlign = 1024;           // of the first box
 
 // What the layout depends on.

@@ -14,6 +14,11 @@ namespace triattn {
 // one with atomicCAS(status, 0, code) so the first fault is kept.
 enum : int { kStatusOk = 0, kStatusTimeout = TA_ERR_TIMEOUT, kStatusDevice = TA_ERR_DEVICE };
 
+// Dynamic shared memory that a block may have (227 KB).  A kernel without static shared memory raises its limit to
+// this and not to a call's size: two host threads' calls may come between one another, and a smaller call's limit would
+// make the larger one's launch fail.
+constexpr int kMaxDynamicSmem = 232448;
+
 // One attention problem as the kernels see it.  Triangle form: units are
 // (b, n, h) slabs with Q query rows and K keys.  Varlen form: units are
 // (sequence, h) with lengths read from cu_seqlens.

@@ -488,8 +488,8 @@ cudaError_t launch_typed(const BwdParams& p, cudaStream_t stream) {
     auto k2 = p.varlen ? (D <= 128 ? bwd_main_kernel<T, BT, 4, true> : bwd_main_kernel<T, BT, 8, true>)
                        : (D <= 128 ? bwd_main_kernel<T, BT, 4, false> : bwd_main_kernel<T, BT, 8, false>);
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm1)) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm2)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem)) != cudaSuccess) return e;
     const long long g1 = units * ((p.Q + kT - 1) / kT);
     const long long g2 = p.varlen ? (long long)p.num_seqs * p.H * ((p.max_k + kT - 1) / kT)
                                   : units * ((p.K + kT - 1) / kT);

@@ -368,7 +368,7 @@ cudaError_t launch_typed(const AttnParams& p, cudaStream_t stream) {
     size_t smem = sizeof(float) * ((size_t)kQT * (D + 1) + (size_t)kKT * (D + 1) + (size_t)kKT * D +
                                    (size_t)kWarps * kRows * kKT);
     auto kern = D <= 128 ? simt_fwd_kernel<T, BT, 4> : simt_fwd_kernel<T, BT, 8>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
     if (e != cudaSuccess) return e;
     long long grid;
     if (!p.varlen) grid = (long long)p.B * p.N * p.H * ((p.Q + kQT - 1) / kQT);

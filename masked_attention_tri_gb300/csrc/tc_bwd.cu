@@ -1154,8 +1154,8 @@ cudaError_t launch_tc_bwd_main(const BwdParams& p, cudaStream_t stream) {
                               : (fb ? tc_bwd_kernel<false, true, true, true, true, false> : tc_bwd_kernel<false, false, true, true, true, false>))
              : bf16   ? (fb ? tc_bwd_kernel<true, true, false, true, true, false> : tc_bwd_kernel<true, false, false, true, true, false>)
                       : (fb ? tc_bwd_kernel<false, true, false, true, true, false> : tc_bwd_kernel<false, false, false, true, true, false>);
-    // (the limit, not this call's size: two threads' calls may come between one another)
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBwdMaxSmem);
+    static_assert(kBwdMaxSmem == kMaxDynamicSmem, "one limit");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)grid, kBwdThreads, smem, stream>>>(P);
     return cudaGetLastError();

@@ -1267,7 +1267,7 @@ cudaError_t launch_kernel(const TcParams& P, int grid, cudaStream_t stream) {
     const Layout L = make_layout(NQ, P);
     const size_t smem = L.total + 1024;
     auto kern = tc_fwd_kernel<NQ, VARLEN, BF16, BIAS_F32, FOLD, SINK>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
     if (e != cudaSuccess) return e;
     kern<<<grid, kThreads<NQ>, smem, stream>>>(P);
     return cudaGetLastError();

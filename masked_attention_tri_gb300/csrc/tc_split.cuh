@@ -1470,7 +1470,7 @@ cudaError_t launch_split(const TcParams& P, int grid, cudaStream_t stream) {
     const SplitLayout L = make_split_layout(P);
     const size_t smem = L.total + 1024;
     auto kern = tc_split_kernel<BF16, BIAS_F32, VARLEN, FOLD, BIAS, SINK>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
     if (e != cudaSuccess) return e;
     kern<<<grid, kSplitThreads, smem, stream>>>(P);
     return cudaGetLastError();

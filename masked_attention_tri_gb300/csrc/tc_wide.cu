@@ -546,7 +546,7 @@ cudaError_t launch_tc_wide(const AttnParams& a, cudaStream_t stream) {
     const size_t smem = wide_layout(P).total + 1024;
     auto kern = bf16 ? (a.bias_f32 ? tc_wide_kernel<true, true> : tc_wide_kernel<true, false>)
                      : (a.bias_f32 ? tc_wide_kernel<false, true> : tc_wide_kernel<false, false>);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
     if (e != cudaSuccess) return e;
     kern<<<grid, kWThreads, smem, stream>>>(P);
     return cudaGetLastError();
