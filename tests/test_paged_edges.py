@@ -96,3 +96,34 @@ def test_value_scales_at_and_past_their_range(dtype):
         assert ta.get_status() == abi.TA_ERR_DEVICE and bool((o == 0).all()) and bool((lse == -math.inf).all())
         call(vs, [0, 2, 1], 32)                                      # a page that no row sees may have any
         assert ta.get_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_small_elements_of_a_query_over_8_bit_keys(dtype, D):
+    """A query row whose elements span 2^-24 to 1, against keys whose codes grow as its elements shrink.  16-bit queries are
+    scaled by a power of two, their largest magnitude into [1, 2), and held in fp16, whose least step there is 2^-24:
+    an element is off by at most 2^-25 of the largest, a logit by scale 2^-25 max|q| sum|k|; fp32 queries by nothing.  The
+    rest as in test_paged_attention.py: the products' sum D 2^-23 E, 2^-22 |x|, the logarithm's 2^-20."""
+    import masked_attention_tri_gb300 as ta
+    F8 = torch.float8_e4m3fn
+    g = torch.Generator().manual_seed(D)
+    i = torch.arange(D)
+    size = torch.exp2(-24.0 * i / (D - 1))
+    q = (size * torch.randn(1, 4, D, generator=g).sign() * (1 + torch.rand(1, 4, D, generator=g))).to(dtype)
+    big = torch.exp2((i * 8 // D).float())                     # up to 2^7 where the query is smallest
+    k = ((torch.rand(2, 1, 16, D, generator=g) + 0.5) * big * torch.randn(2, 1, 16, D, generator=g).sign()).to(F8)
+    v = torch.ones(2, 1, 16, D).to(F8)
+    cache = ta.PagedKVCache(k.cuda(), v.cuda(), torch.ones(2, 1, device="cuda"), torch.ones(2, 1, device="cuda"))
+    _, lse = ta.paged_attention(q.cuda(), cache, _i32([[0, 1]]), _i32([32]), scale=1.0, return_aux=True)
+    torch.cuda.synchronize()
+    assert ta.get_status() == 0
+    kk, qq = k.double().reshape(32, D), q.double()[0]
+    x = qq @ kk.t()
+    E = (qq.abs() @ kk.abs().t()).amax(-1)
+    tol = D * 2.0 ** -23 * E + 2.0 ** -22 * x.abs().amax(-1) + 2.0 ** -20
+    if dtype != torch.float32:
+        tol = tol + 2.0 ** -25 * qq.abs().amax(-1) * kk.abs().sum(-1).amax()
+    err = (lse[:, 0].double().cpu() - torch.logsumexp(x, -1)).abs()
+    assert bool((err <= tol).all()), (err, tol)
