@@ -119,13 +119,14 @@ __device__ __forceinline__ int block_status(const BwdParams& p, int seq, int h, 
 }
 // mask_mod on a partial block, local indices: causal k <= q; sliding window
 // q - window < k <= q; prefix LM k <= q or k < prefix; sink window k <= q and (k > q - window
-// or k < prefix).
+// or k < prefix), known when the kernel is compiled (in the switch it cost the other masks 1% of the kernel).
+template <bool SINK>
 __device__ __forceinline__ bool mod_keep(int mod, int q, int k, int window, int prefix) {
+    if constexpr (SINK) return k <= q && (k > q - window || k < prefix);
     switch (mod) {
     case TA_MASK_CAUSAL: return k <= q;
     case TA_MASK_SLIDING_WINDOW: return k <= q && k > q - window;
     case TA_MASK_PREFIX_LM: return k <= q || k < prefix;
-    case TA_MASK_SINK_WINDOW: return k <= q && (k > q - window || k < prefix);
     default: return true;
     }
 }
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(256) bwd_delta_out_kernel(const BwdParams p) {
     if (g == 0 && row < rows) p.delta[p.varlen ? (row % p.H) * p.total_q + row / p.H : row] = acc;
 }
 
-template <typename T, typename BT, int DPL, bool VARLEN>
+template <typename T, typename BT, int DPL, bool VARLEN, bool SINK>
 __global__ void __launch_bounds__(kBW * 32) bwd_main_kernel(const BwdParams p) {
     extern __shared__ float sm[];
     const int D = p.D, Dp1 = D + 1;
@@ -318,8 +319,7 @@ __global__ void __launch_bounds__(kBW * 32) bwd_main_kernel(const BwdParams p) {
 
     // Sink window without lists: a tile that keeps no (query, key) is skipped, unless a query may
     // have no valid key at all (then its weights 1 / Lk reach every key).
-    const bool sunk = VARLEN && !p.kv_num && p.mask_mod == TA_MASK_SINK_WINDOW &&
-                      (prefix > 0 || (long long)Lq - Lk < p.window);
+    const bool sunk = SINK && !p.kv_num && (prefix > 0 || (long long)Lq - Lk < p.window);
     for (int q0 = 0; q0 < Lq; q0 += kT) {
         if (sunk && !sink_blocks(q0, min(q0 + kT, Lq) - 1, Lk, p.window, prefix).visited(k0 / 128)) continue;
         __syncthreads();  // the previous tile's Qs, dOs, Ps, dSs are no longer read
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kBW * 32) bwd_main_kernel(const BwdParams p) {
                 const long long row = lrow0 + q;
                 bool valid = key_ok;
                 if constexpr (VARLEN)
-                    valid = bstat == 2 || (bstat == 1 && mod_keep(p.mask_mod, q, key, p.window, prefix));
+                    valid = bstat == 2 || (bstat == 1 && mod_keep<SINK>(p.mask_mod, q, key, p.window, prefix));
                 const long long bi = brow0 + (long long)q * bstride + key;
                 const float bv = bias ? ld_f(bias, bi) : 0.f;
                 const float x = valid ? fmaf(p.scale, qk[i], bv) : kMaskedLogit;
@@ -485,8 +485,10 @@ cudaError_t launch_typed(const BwdParams& p, cudaStream_t stream) {
     const size_t sm1 = sizeof(float) * 4 * kT * (size_t)(D + 1);
     const size_t sm2 = sm1 + sizeof(float) * 2 * kT * (kT + 1);
     auto k1 = bwd_delta_kernel<T, BT>;
-    auto k2 = p.varlen ? (D <= 128 ? bwd_main_kernel<T, BT, 4, true> : bwd_main_kernel<T, BT, 8, true>)
-                       : (D <= 128 ? bwd_main_kernel<T, BT, 4, false> : bwd_main_kernel<T, BT, 8, false>);
+    auto k2 = !p.varlen ? (D <= 128 ? bwd_main_kernel<T, BT, 4, false, false> : bwd_main_kernel<T, BT, 8, false, false>)
+              : p.mask_mod == TA_MASK_SINK_WINDOW
+                  ? (D <= 128 ? bwd_main_kernel<T, BT, 4, true, true> : bwd_main_kernel<T, BT, 8, true, true>)
+                  : (D <= 128 ? bwd_main_kernel<T, BT, 4, true, false> : bwd_main_kernel<T, BT, 8, true, false>);
     cudaError_t e;
     if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem)) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem)) != cudaSuccess) return e;
