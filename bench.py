@@ -48,13 +48,13 @@ ESIZE = {"f32": 4, "f16": 2, "bf16": 2}
 
 def kernel_source_hash() -> str:
     """SHA-256 over the sources of the tensor-core forward kernels (path + content): tc_*.cu,
-    tc_*.cuh, tmem_io.h and internal.h.  The CUDA-core kernels, the backward and the host entry
+    tc_*.cuh, tmem_io.h, internal.h and sink_window.h.  The CUDA-core kernels, the backward and the host entry
     points do not change what the measured kernels do, so they are left out."""
     import glob
     import hashlib
     cs = os.path.join(ROOT, "masked_attention_tri_gb300", "csrc")
     files = sorted(glob.glob(os.path.join(cs, "tc_*.cu")) + glob.glob(os.path.join(cs, "tc_*.cuh")) +
-                   [os.path.join(cs, "tmem_io.h"), os.path.join(cs, "internal.h")])
+                   [os.path.join(cs, n) for n in ("tmem_io.h", "internal.h", "sink_window.h")])
     files = [f for f in files if os.path.basename(f) not in ("tc_bwd.cu", "tc_wide.cu")]
     h = hashlib.sha256()
     for f in files:

@@ -371,7 +371,8 @@ ta_status tri_attn_varlen_fwd_masked(const void* q, const void* k, const void* v
  * a million otherwise) run on tensor cores (one CTA per sequence, head and 128-key block, over the q
  * blocks whose lists hold that block and those with a row that has no valid
  * key; P and dS rounded to the input type as the MMAs' operands, fp32
- * accumulation); every other case exact fp32 on CUDA cores (one CTA per
+ * accumulation; under a SINK_WINDOW without a bias dS keeps a second piece of that type, with D > 64 for
+ * max_seqlen_q up to 10752); every other case exact fp32 on CUDA cores (one CTA per
  * sequence, head and 32 keys).  dQ and dBias are added in fp32 with atomic
  * reductions, so their summation order varies from run to run.  Errors as tri_attn_bwd; a sequence that
  * breaks the max_seqlen / total contract is skipped and TA_ERR_DEVICE recorded.
@@ -469,9 +470,9 @@ ta_status tri_attn_rotary(const void* q, const void* k, ta_dtype dtype, const in
  *   cache_dtype   `dtype`, or TA_E4M3: 8-bit codes (D a multiple of 16) that stand for code * scale with
  *                 k_scale / v_scale (num_pages, Hk) fp32, 4-byte aligned (NULL otherwise).
  *                 The scale is the smallest power of two, from 2^-56 to 2^56, with
- *                 max |x| <= 448 * scale over the rows of the page and head; a row that
- *                 needs a larger one re-codes the rows before it, and the row in slot 0
- *                 starts anew.  Values are rounded once to the nearest code (ties to
+ *                 max |x| <= 448 * scale over the rows written to the page and head since its slot 0
+ *                 was; a row that needs a larger one re-codes the rows before it, and the row in slot 0
+ *                 starts anew.  It does not shrink when rows are written over (tokens taken back).  Values are rounded once to the nearest code (ties to
  *                 even; beyond 448 * 2^56 to that); infinities and NaN become NaN.
  * A sequence that breaks the contract (lengths, offsets), or a page out of range, is skipped and
  * TA_ERR_DEVICE recorded.  Errors as tri_attn_rotary; a page size that is no power
@@ -515,6 +516,8 @@ ta_status tri_attn_kv_append(const void* q, const void* k, const void* v, ta_dty
  * A row that sees no slot (a sequence that holds nothing) gets O = 0 and lse = -inf.
  * Slots that no row of the call sees may hold anything, NaN included.  With several
  * rows of one sequence, a slot that some of them see has to hold finite values of v.
+ * Made for few new tokens a sequence: each 16 rows (tokens x Hq / Hk; 32 with D <= 64, 8 in fp32) read K and V
+ * again.  A prompt without a cached prefix runs faster through tri_attn_varlen_fwd_masked (equal numbers of heads).
  * Results do not vary from run to run.  A sequence that breaks the contract
  * (offsets; a length below 0 or beyond its table, read as 0), a page out of range or a v_scale out of range (its slots
  * are not seen) records TA_ERR_DEVICE.  Errors as tri_attn_kv_append.

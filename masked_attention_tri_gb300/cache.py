@@ -20,7 +20,8 @@ _CACHE_DT = {**_DT, torch.float8_e4m3fn: abi.TA_E4M3}
 
 class PagedKVCache:
     """The pages of a cache: k and v (num_pages, Hk, page_size, D), with k_scale and v_scale
-    (num_pages, Hk) float32 where they hold float8_e4m3fn codes (an element stands for code * scale).
+    (num_pages, Hk) float32 where they hold float8_e4m3fn codes (an element stands for code * scale;
+    v_scale from 2^-56 to 2^56).
 
     The tensors are used in place.  k and v may be strided views whose last
     dimension is contiguous, such as the halves of one (num_pages, 2, Hk,
@@ -106,7 +107,8 @@ def kv_cache_append(cache: PagedKVCache, k, v, page_table, kv_lengths, cu_seqlen
     by positions (total,) int32.  Returns the turned q (out_q, which may be q), or None.
 
     An 8-bit cache takes a power-of-two scale for each (page, head): rows that need
-    a larger one re-code the rows before them.  Infinities and NaN become NaN.
+    a larger one re-code the rows before them.  It starts anew with the row in slot 0 of the page and does not
+    shrink when rows are written over.  Infinities and NaN become NaN.
     """
     if not isinstance(cache, PagedKVCache):
         raise TypeError("cache must be a PagedKVCache")
@@ -175,6 +177,10 @@ def paged_attention(q, cache: PagedKVCache, page_table, kv_lengths, cu_seqlens_q
     window: only the last ``window`` of those slots, and the first ``sinks`` of the
     sequence.  scale defaults to 1/sqrt(D).  Returns O, or (O, lse) with return_aux (lse
     float32 (Hq, total_q)); a row that sees no slot gets O = 0 and lse = -inf.
+
+    Made for few new tokens a sequence: K and V are read again for each 16 rows (tokens x query heads
+    of a key head).  A whole prompt without a cached prefix runs faster through ``varlen_attention``
+    (which takes as many heads of k and v as of q).
     """
     if not isinstance(cache, PagedKVCache):
         raise TypeError("cache must be a PagedKVCache")

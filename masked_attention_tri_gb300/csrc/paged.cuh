@@ -108,6 +108,8 @@ __device__ __forceinline__ Tiles unit_tiles(const PagedParams& p, const Seq& q, 
     return t;
 }
 __device__ __forceinline__ int row_tiles(const PagedParams& p, const Seq& q) { return (q.n * p.G + p.RT - 1) / p.RT; }
+// (These walk the row tiles one by one: made for sequences with few new rows.  8192 new tokens in one call are 2048 row
+// tiles of 16 rows, 4 heads a group, and every CTA walks them before its first load.)
 // Tiles of one kv head of a sequence (a unit without keys counts one: its rows are written too).
 __device__ __forceinline__ long long head_tiles(const PagedParams& p, const Seq& q) {
     long long t = 0;

@@ -43,7 +43,10 @@
 // serpentine (CTA c takes positions c, 2G - 1 - c, 2G + c, ... of G CTAs),
 // which balances the CTAs' key-tile counts much like a longest-first
 // schedule.  Every CTA reads the sequence offsets into shared memory once and
-// walks this order itself; every role walks it the same way.
+// walks this order itself; every role walks it the same way.  Under a sink window
+// without lists (SINK) a q block visits the blocks that hold a kept pair (sink_window.h).
+// It is a variant of its own: with its blocks carried in every item and its case in the mask's
+// switch the other masks took 4 to 7% longer (bf16_varlen causal without lists 77.9 us, now 73.4).
 
 #pragma once
 
