@@ -1,6 +1,6 @@
 /*
  * triattn.h -- C ABI of the GB300 (sm_103a) attention library: triangle and packed attention,
- * forward and backward, rotary positions, and attention over a paged cache.
+ * forward and backward, rotary positions, attention over a paged cache (of up to 4 bits) and of prompts.
  *
  * Operation of the triangle form (cuEquivariance "triangle_attention" API page, formula):
  *
@@ -56,7 +56,8 @@ typedef enum {
     TA_F32 = 0,
     TA_F16 = 1,
     TA_BF16 = 2,
-    TA_E4M3 = 3 /* 8-bit (4 significant bits, |x| <= 448): only as the type of a paged cache, with scales */
+    TA_E4M3 = 3, /* 8-bit (4 significant bits, |x| <= 448): only as the type of a paged cache, with scales */
+    TA_INT4 = 4  /* 4-bit whole numbers, a scale for 16 of them: only as the type of a paged cache (ta_cache4) */
 } ta_dtype;
 
 /* Element predicate applied on partial blocks of a BlockMask (tensorplay
@@ -76,6 +77,30 @@ typedef enum {
     TA_MASK_PREFIX_LM = 3,
     TA_MASK_SINK_WINDOW = 6
 } ta_mask_mod;
+
+/*
+ * A 4-bit paged cache: whole numbers n from -7 to 7 held as n + 8, two a byte (the even element in the low half), 16
+ * neighbouring elements of a row to an e4m3 scale.  An element of head h stands for n * scale * factor[h].
+ *   k, v              (num_pages, Hk, page_size, D / 2) bytes
+ *   k_scale, v_scale  (num_pages, Hk, page_size, D / 16) e4m3 numbers
+ *   k_factor, v_factor  (Hk) fp32, positive and finite, fixed for the cache's life; powers of two cost no precision.
+ *                     NULL: 1.  The scale covers magnitudes up to 3136 factors, and 7 * 2^-9 factors is the least
+ *                     largest magnitude of 16 elements that uses all of the codes.
+ *   strides           bytes between pages and between heads: {k, v, k_scale, v_scale} x {page, head}; a head's slots
+ *                     lie one after the other.  Multiples of 16; all 0: contiguous as above.
+ * D a multiple of 32, up to 256; page_size a power of two from 16 to 1024.  Pointers 16-byte aligned (factors 4).
+ */
+typedef struct {
+    void* k;
+    void* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    const float* k_factor;
+    const float* v_factor;
+    int num_pages;
+    int page_size;
+    long long strides[8];
+} ta_cache4;
 
 /*
  * tri_attn_fwd -- triangle-attention forward.
@@ -446,6 +471,20 @@ ta_status tri_attn_rotary(const void* q, const void* k, ta_dtype dtype, const in
                           void* stream);
 
 /*
+ * tri_attn_rotary_axes -- tri_attn_rotary with several axes (time, height and width of an image's or video's tokens):
+ * pair i of a head turns by positions[pair_axes[i]][row] * theta_i.
+ *   positions     (num_axes, total) int32.
+ *   pair_axes     (rotary_dim / 2) int32, each from 0 to num_axes - 1 (another value reads axis 0).
+ * Every other argument, the arithmetic and the errors as in tri_attn_rotary; num_axes < 1 or pair_axes NULL or not 4-byte
+ * aligned -> TA_ERR_INVALID_ARG.
+ */
+ta_status tri_attn_rotary_axes(const void* q, const void* k, ta_dtype dtype, const int32_t* positions, int num_axes,
+                               const int32_t* pair_axes, const uint64_t* turns, int rotary_dim, int interleaved,
+                               float mscale, int inverse, int total, int Hq, int Hk, int D, long long q_row_stride,
+                               long long k_row_stride, long long q_out_row_stride, long long k_out_row_stride,
+                               void* q_out, void* k_out, void* stream);
+
+/*
  * tri_attn_kv_append -- new keys and values of packed sequences into a paged
  * cache, with the rotation of k and q on the way.
  *
@@ -490,6 +529,63 @@ ta_status tri_attn_kv_append(const void* q, const void* k, const void* v, ta_dty
                              void* stream);
 
 /*
+ * tri_attn_kv_append_axes -- tri_attn_kv_append with several axes: positions (num_axes, total), or NULL (every axis the
+ * row's slot), and pair_axes as in tri_attn_rotary_axes (needs a rotation).
+ */
+ta_status tri_attn_kv_append_axes(const void* q, const void* k, const void* v, ta_dtype dtype,
+                                  const int32_t* cu_seqlens, const int32_t* kv_lengths, const int32_t* page_table,
+                                  int num_seqs, int total, int max_seqlen, int Hq, int Hk, int D,
+                                  long long q_row_stride, long long k_row_stride, long long v_row_stride,
+                                  long long q_out_row_stride, const int32_t* positions, int num_axes,
+                                  const int32_t* pair_axes, const uint64_t* turns, int rotary_dim, int interleaved,
+                                  float mscale, void* k_cache, void* v_cache, ta_dtype cache_dtype, float* k_scale,
+                                  float* v_scale, int num_pages, int page_size, int max_pages,
+                                  const long long* k_strides, const long long* v_strides, void* q_out, void* stream);
+
+/*
+ * tri_attn_kv_append4 -- tri_attn_kv_append into a 4-bit cache.
+ *   positions, num_axes, pair_axes   one axis: positions (total) or NULL, num_axes 1, pair_axes NULL; several: as in
+ *                 tri_attn_kv_append_axes.
+ *   rotary_dim    a multiple of 32 (or 0: no rotation); others -> TA_ERR_UNSUPPORTED (turn the rows first).
+ *   cache         the 4-bit cache (the struct is read before the call returns).
+ * With a the largest |x| / factor of 16 elements, scale = e4m3(a / 7), not below 2^-9 and not above 448, and
+ * n = x / (factor scale) rounded to the nearest whole number (ties to even) and to 7 at most; fp32 arithmetic.  Rows that
+ * are there keep their codes and scales.  An infinity or NaN makes its 16 elements NaN.  Every other argument and error as
+ * in tri_attn_kv_append.
+ */
+ta_status tri_attn_kv_append4(const void* q, const void* k, const void* v, ta_dtype dtype, const int32_t* cu_seqlens,
+                              const int32_t* kv_lengths, const int32_t* page_table, int num_seqs, int total,
+                              int max_seqlen, int Hq, int Hk, int D, long long q_row_stride, long long k_row_stride,
+                              long long v_row_stride, long long q_out_row_stride, const int32_t* positions,
+                              int num_axes, const int32_t* pair_axes, const uint64_t* turns, int rotary_dim,
+                              int interleaved, float mscale, const ta_cache4* cache, int max_pages, void* q_out,
+                              void* stream);
+
+/*
+ * tri_attn_kv_read -- rows of a paged cache (the layout of tri_attn_kv_append) back into packed k and v.
+ *   cu_seqlens, kv_lengths, page_table, num_seqs, total, max_seqlen   as in tri_attn_kv_append: sequence i's rows
+ *                 [cu[i], cu[i + 1]) become the last ones of its kv_lengths[i] slots (any count that the sequence holds: a
+ *                 prefix, or with cu[i + 1] - cu[i] = kv_lengths[i] all of it).  Rows past cu[num_seqs] are left alone.
+ *   k_cache .. v_strides   as in tri_attn_kv_append, num_pages, page_size and max_pages among them.
+ *   k_out, v_out  (total, Hk, D) of `dtype` (that of the cache, or any where the cache holds codes: code * scale, rounded
+ *                 once); rows `*_row_stride` elements apart (0 = contiguous).
+ * A sequence that breaks the contract, or a page out of range, is skipped and TA_ERR_DEVICE recorded.  Errors as
+ * tri_attn_kv_append.
+ */
+ta_status tri_attn_kv_read(const int32_t* cu_seqlens, const int32_t* kv_lengths, const int32_t* page_table, int num_seqs,
+                           int total, int max_seqlen, int Hk, int D, const void* k_cache, const void* v_cache,
+                           ta_dtype cache_dtype, const float* k_scale, const float* v_scale, int num_pages,
+                           int page_size, int max_pages, const long long* k_strides, const long long* v_strides,
+                           void* k_out, void* v_out, ta_dtype dtype, long long k_row_stride, long long v_row_stride,
+                           void* stream);
+
+/* tri_attn_kv_read4 -- tri_attn_kv_read from a 4-bit cache: n * scale * factor, rounded once to `dtype`. */
+ta_status tri_attn_kv_read4(const int32_t* cu_seqlens, const int32_t* kv_lengths, const int32_t* page_table,
+                            int num_seqs, int total, int max_seqlen, int Hk, int D, const ta_cache4* cache,
+                            int max_pages, void* k_out, void* v_out, ta_dtype dtype, long long k_row_stride,
+                            long long v_row_stride, void* stream);
+
+/*
  * tri_attn_paged_fwd -- attention of the newest tokens of each sequence over its
  * paged cache (the layout of tri_attn_kv_append), with grouped heads:
  *     O[i, h] = softmax_k(scale q[i, h] . K[k, h / (Hq / Hk)]) V[k, h / (Hq / Hk)].
@@ -517,7 +613,7 @@ ta_status tri_attn_kv_append(const void* q, const void* k, const void* v, ta_dty
  * Slots that no row of the call sees may hold anything, NaN included.  With several
  * rows of one sequence, a slot that some of them see has to hold finite values of v.
  * Made for few new tokens a sequence: each 16 rows (tokens x Hq / Hk; 32 with D <= 64, 8 in fp32) read K and V
- * again.  A prompt without a cached prefix runs faster through tri_attn_varlen_fwd_masked (equal numbers of heads).
+ * again.  A prompt runs faster through tri_attn_prompt_fwd (its prefix read back by tri_attn_kv_read).
  * Results do not vary from run to run.  A sequence that breaks the contract
  * (offsets; a length below 0 or beyond its table, read as 0), a page out of range or a v_scale out of range (its slots
  * are not seen) records TA_ERR_DEVICE.  Errors as tri_attn_kv_append.
@@ -532,6 +628,65 @@ ta_status tri_attn_paged_fwd(const void* q, ta_dtype dtype, const int32_t* cu_se
 
 /* Bytes of workspace tri_attn_paged_fwd needs (0 for a non-positive size). */
 size_t tri_attn_paged_workspace_size(ta_dtype dtype, int max_seqlen_q, int Hq, int Hk, int D);
+
+/*
+ * tri_attn_paged4_fwd -- tri_attn_paged_fwd over a 4-bit cache.  Arguments, results, workspace and errors as there, the
+ * cache as in tri_attn_kv_append4.  16-bit queries: products in fp16 with fp32 sums (codes times scales are exact in
+ * fp16); fp32 queries: exact fp32.
+ */
+ta_status tri_attn_paged4_fwd(const void* q, ta_dtype dtype, const int32_t* cu_seqlens_q, const int32_t* kv_lengths,
+                              const int32_t* page_table, int num_seqs, int total_q, int max_seqlen_q, int Hq, int Hk,
+                              int D, long long q_row_stride, float scale, int window, int sinks,
+                              const ta_cache4* cache, int max_pages, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * tri_attn_prompt_fwd -- causal attention of whole prompts, or of the chunks of prompts whose prefix's keys and values are
+ * at hand, with grouped heads:
+ *     O[i, h] = softmax_k(scale q[i, h] . K[k, h / (Hq / Hk)]) V[k, h / (Hq / Hk)].
+ *   q, out        (total_q, Hq, D) of `dtype`, Hq a multiple of Hk; k, v (total_k, Hk, D).  Rows of q, k, v
+ *                 `*_row_stride` elements apart (0 = contiguous); out contiguous.
+ *   cu_seqlens_q  (num_seqs + 1) int32: sequence i's queries are rows [cu_q[i], cu_q[i + 1]), at most max_seqlen_q of them;
+ *   cu_seqlens_k  (num_seqs + 1) int32: its keys, at most max_seqlen_k.  The queries are its newest tokens: of Lq queries
+ *                 and Lk keys, query j sees the keys k <= Lk - Lq + j (the last one all of them).  Either may have none.
+ *                 Rows of out and lse past cu_q[num_seqs] are left alone.
+ *   lse           optional (Hq, total_q) fp32.
+ * A query that sees no key (Lk < Lq) gets O = 0 and lse = -inf.  A key row that no query of its sequence sees takes no
+ * part (finite values of v are wanted all the same in rows that share a tile with seen ones: a NaN there may spread).
+ * Arithmetic: 16-bit inputs with D <= 128 on tensor cores (P rounded to the inputs' type as an operand, fp32
+ * accumulation); fp32 inputs and D > 128 exact fp32 on CUDA cores.  Results do not vary from run to run.
+ * Supported: D as in tri_attn_fwd, up to 65535 key heads or sequences.  A sequence that breaks the contract (offsets,
+ * lengths) is skipped and TA_ERR_DEVICE recorded.  Errors: NULL required pointer, misalignment (16 bytes for tensors, 4 for
+ * the rest), sizes or a row stride below H * D -> TA_ERR_INVALID_ARG; D, or strides that are no 16-byte multiples ->
+ * TA_ERR_UNSUPPORTED.
+ */
+ta_status tri_attn_prompt_fwd(const void* q, const void* k, const void* v, ta_dtype dtype, const int32_t* cu_seqlens_q,
+                              const int32_t* cu_seqlens_k, int num_seqs, int total_q, int total_k, int max_seqlen_q,
+                              int max_seqlen_k, int Hq, int Hk, int D, float scale, long long q_row_stride,
+                              long long k_row_stride, long long v_row_stride, void* out, float* lse, void* stream);
+
+/*
+ * tri_attn_prompt_bwd -- gradients of tri_attn_prompt_fwd: with P = exp(x - lse) and dx = P (dO . V - dO . O) at the
+ * keys a query sees,
+ *     dQ = scale dx K,   dK = scale sum dx Q,   dV = sum P dO,
+ * the sums over the queries and over the query heads that share a key head.
+ *   q .. v_row_stride   as given to tri_attn_prompt_fwd;  lse, out  its results (required).
+ *   d_out         (total_q, Hq, D) contiguous;  dq, dk, dv  outputs like q, k, v, contiguous.  Rows past cu_q[num_seqs] /
+ *                 cu_k[num_seqs] are left alone; a key that no query sees gets 0.
+ *   workspace     device scratch of tri_attn_prompt_bwd_workspace_size(...) bytes, 256-byte aligned, owned by the caller;
+ *                 two calls in flight must not share it.
+ * Arithmetic as in the forward (dx rounded to the inputs' type as an operand on tensor cores).  There dQ is summed with
+ * fp32 atomic reductions over the keys: its order varies from run to run.  Errors as tri_attn_prompt_fwd.
+ */
+ta_status tri_attn_prompt_bwd(const void* q, const void* k, const void* v, ta_dtype dtype, const int32_t* cu_seqlens_q,
+                              const int32_t* cu_seqlens_k, int num_seqs, int total_q, int total_k, int max_seqlen_q,
+                              int max_seqlen_k, int Hq, int Hk, int D, float scale, long long q_row_stride,
+                              long long k_row_stride, long long v_row_stride, const float* lse, const void* out,
+                              const void* d_out, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Bytes of workspace tri_attn_prompt_bwd needs (0 for a non-positive size). */
+size_t tri_attn_prompt_bwd_workspace_size(ta_dtype dtype, int total_q, int Hq, int D);
 
 /*
  * tri_attn_get_status -- synchronize `stream`, then read and clear the

@@ -16,7 +16,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libtriattn.so")
 
 TA_OK, TA_ERR_INVALID_ARG, TA_ERR_UNSUPPORTED, TA_ERR_CUDA, TA_ERR_TIMEOUT, TA_ERR_DEVICE = range(6)
-TA_F32, TA_F16, TA_BF16, TA_E4M3 = 0, 1, 2, 3
+TA_F32, TA_F16, TA_BF16, TA_E4M3, TA_INT4 = 0, 1, 2, 3, 4
 TA_MASK_NONE, TA_MASK_CAUSAL, TA_MASK_SLIDING_WINDOW, TA_MASK_PREFIX_LM, TA_MASK_SINK_WINDOW = 0, 1, 2, 3, 6
 
 # Every symbol include/triattn.h declares.
@@ -24,7 +24,17 @@ EXPORTS = ("tri_attn_fwd", "tri_attn_fwd_strided", "tri_attn_varlen_fwd", "tri_a
            "tri_attn_bwd", "tri_attn_bwd_workspace_size", "tri_attn_bwd_noalloc", "tri_attn_varlen_bwd",
            "tri_attn_varlen_bwd_workspace_size", "tri_attn_varlen_bwd_sink_workspace_size",
            "tri_attn_rotary", "tri_attn_kv_append", "tri_attn_paged_fwd", "tri_attn_paged_workspace_size",
+           "tri_attn_rotary_axes", "tri_attn_kv_append_axes", "tri_attn_kv_append4", "tri_attn_kv_read", "tri_attn_kv_read4",
+           "tri_attn_paged4_fwd", "tri_attn_prompt_fwd", "tri_attn_prompt_bwd", "tri_attn_prompt_bwd_workspace_size",
            "tri_attn_mask_to_kv_lengths", "tri_attn_get_status", "tri_attn_error_string", "tri_attn_version")
+
+
+class Cache4(ctypes.Structure):
+    """ta_cache4: the parts of a 4-bit paged cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_factor", ctypes.c_void_p), ("v_factor", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("strides", ctypes.c_longlong * 8)]
+
 
 _lock = threading.Lock()
 _lib = None
@@ -87,6 +97,27 @@ def load() -> ctypes.CDLL:
         lib.tri_attn_paged_fwd.restype = I
         lib.tri_attn_paged_workspace_size.argtypes = [I, I, I, I, I]
         lib.tri_attn_paged_workspace_size.restype = Z
+        C4 = ctypes.POINTER(Cache4)
+        lib.tri_attn_rotary_axes.argtypes = [P, P, I, P, I, P, P, I, I, F, I, I, I, I, I, L, L, L, L, P, P, P]
+        lib.tri_attn_rotary_axes.restype = I
+        lib.tri_attn_kv_append_axes.argtypes = [P, P, P, I, P, P, P, I, I, I, I, I, I, L, L, L, L, P, I, P, P, I, I, F, P,
+                                                P, I, P, P, I, I, I, P, P, P, P]
+        lib.tri_attn_kv_append_axes.restype = I
+        lib.tri_attn_kv_append4.argtypes = [P, P, P, I, P, P, P, I, I, I, I, I, I, L, L, L, L, P, I, P, P, I, I, F, C4, I,
+                                            P, P]
+        lib.tri_attn_kv_append4.restype = I
+        lib.tri_attn_kv_read.argtypes = [P, P, P, I, I, I, I, I, P, P, I, P, P, I, I, I, P, P, P, P, I, L, L, P]
+        lib.tri_attn_kv_read.restype = I
+        lib.tri_attn_kv_read4.argtypes = [P, P, P, I, I, I, I, I, C4, I, P, P, I, L, L, P]
+        lib.tri_attn_kv_read4.restype = I
+        lib.tri_attn_paged4_fwd.argtypes = [P, I, P, P, P, I, I, I, I, I, I, L, F, I, I, C4, I, P, P, P, Z, P]
+        lib.tri_attn_paged4_fwd.restype = I
+        lib.tri_attn_prompt_fwd.argtypes = [P, P, P, I, P, P, I, I, I, I, I, I, I, I, F, L, L, L, P, P, P]
+        lib.tri_attn_prompt_fwd.restype = I
+        lib.tri_attn_prompt_bwd.argtypes = [P, P, P, I, P, P, I, I, I, I, I, I, I, I, F, L, L, L, P, P, P, P, P, P, P, Z, P]
+        lib.tri_attn_prompt_bwd.restype = I
+        lib.tri_attn_prompt_bwd_workspace_size.argtypes = [I, I, I, I]
+        lib.tri_attn_prompt_bwd_workspace_size.restype = Z
         lib.tri_attn_mask_to_kv_lengths.argtypes = [P, I, I, I, P, P, P]
         lib.tri_attn_mask_to_kv_lengths.restype = I
         lib.tri_attn_get_status.argtypes = [P]
@@ -271,6 +302,93 @@ def tri_attn_paged_fwd(q, dtype, cu_seqlens_q, kv_lengths, page_table, num_seqs,
                                    cache_dtype, k_scale or None, v_scale or None, num_pages, page_size, max_pages,
                                    k_strides, v_strides, out, lse or None, workspace, workspace_bytes, stream or None)
     _check(st, "tri_attn_paged_fwd")
+
+
+def tri_attn_rotary_axes(q, k, dtype, positions, num_axes, pair_axes, turns, rotary_dim, interleaved, mscale, inverse,
+                         total, Hq, Hk, D, q_row_stride, k_row_stride, q_out_row_stride, k_out_row_stride, q_out, k_out,
+                         stream) -> None:
+    """tri_attn_rotary with positions (num_axes, total) and an axis for each pair."""
+    st = load().tri_attn_rotary_axes(q, k or None, dtype, positions, num_axes, pair_axes, turns, rotary_dim,
+                                     1 if interleaved else 0, mscale, 1 if inverse else 0, total, Hq, Hk, D,
+                                     q_row_stride, k_row_stride, q_out_row_stride, k_out_row_stride, q_out,
+                                     k_out or None, stream or None)
+    _check(st, "tri_attn_rotary_axes")
+
+
+def tri_attn_kv_append_axes(q, k, v, dtype, cu_seqlens, kv_lengths, page_table, num_seqs, total, max_seqlen, Hq, Hk, D,
+                            q_row_stride, k_row_stride, v_row_stride, q_out_row_stride, positions, num_axes, pair_axes,
+                            turns, rotary_dim, interleaved, mscale, k_cache, v_cache, cache_dtype, k_scale, v_scale,
+                            num_pages, page_size, max_pages, k_strides, v_strides, q_out, stream) -> None:
+    """tri_attn_kv_append with positions (num_axes, total), or none, and an axis for each pair."""
+    st = load().tri_attn_kv_append_axes(q or None, k, v, dtype, cu_seqlens or None, kv_lengths, page_table, num_seqs,
+                                        total, max_seqlen, Hq, Hk, D, q_row_stride, k_row_stride, v_row_stride,
+                                        q_out_row_stride, positions or None, num_axes, pair_axes or None, turns or None,
+                                        rotary_dim, 1 if interleaved else 0, mscale, k_cache, v_cache, cache_dtype,
+                                        k_scale or None, v_scale or None, num_pages, page_size, max_pages, k_strides,
+                                        v_strides, q_out or None, stream or None)
+    _check(st, "tri_attn_kv_append_axes")
+
+
+def tri_attn_kv_append4(q, k, v, dtype, cu_seqlens, kv_lengths, page_table, num_seqs, total, max_seqlen, Hq, Hk, D,
+                        q_row_stride, k_row_stride, v_row_stride, q_out_row_stride, positions, num_axes, pair_axes, turns,
+                        rotary_dim, interleaved, mscale, cache, max_pages, q_out, stream) -> None:
+    """cache: a ``Cache4`` or None."""
+    st = load().tri_attn_kv_append4(q or None, k, v, dtype, cu_seqlens or None, kv_lengths, page_table, num_seqs, total,
+                                    max_seqlen, Hq, Hk, D, q_row_stride, k_row_stride, v_row_stride, q_out_row_stride,
+                                    positions or None, num_axes, pair_axes or None, turns or None, rotary_dim,
+                                    1 if interleaved else 0, mscale, cache, max_pages, q_out or None, stream or None)
+    _check(st, "tri_attn_kv_append4")
+
+
+def tri_attn_kv_read(cu_seqlens, kv_lengths, page_table, num_seqs, total, max_seqlen, Hk, D, k_cache, v_cache, cache_dtype,
+                     k_scale, v_scale, num_pages, page_size, max_pages, k_strides, v_strides, k_out, v_out, dtype,
+                     k_row_stride, v_row_stride, stream) -> None:
+    """k_strides / v_strides: None (contiguous) or a host array of ``strides3``."""
+    st = load().tri_attn_kv_read(cu_seqlens or None, kv_lengths, page_table, num_seqs, total, max_seqlen, Hk, D, k_cache,
+                                 v_cache, cache_dtype, k_scale or None, v_scale or None, num_pages, page_size, max_pages,
+                                 k_strides, v_strides, k_out, v_out, dtype, k_row_stride, v_row_stride, stream or None)
+    _check(st, "tri_attn_kv_read")
+
+
+def tri_attn_kv_read4(cu_seqlens, kv_lengths, page_table, num_seqs, total, max_seqlen, Hk, D, cache, max_pages, k_out,
+                      v_out, dtype, k_row_stride, v_row_stride, stream) -> None:
+    """cache: a ``Cache4`` or None."""
+    st = load().tri_attn_kv_read4(cu_seqlens or None, kv_lengths, page_table, num_seqs, total, max_seqlen, Hk, D, cache,
+                                  max_pages, k_out, v_out, dtype, k_row_stride, v_row_stride, stream or None)
+    _check(st, "tri_attn_kv_read4")
+
+
+def tri_attn_paged4_fwd(q, dtype, cu_seqlens_q, kv_lengths, page_table, num_seqs, total_q, max_seqlen_q, Hq, Hk, D,
+                        q_row_stride, scale, window, sinks, cache, max_pages, out, lse, workspace, workspace_bytes,
+                        stream) -> None:
+    """cache: a ``Cache4`` or None."""
+    st = load().tri_attn_paged4_fwd(q, dtype, cu_seqlens_q or None, kv_lengths, page_table, num_seqs, total_q,
+                                    max_seqlen_q, Hq, Hk, D, q_row_stride, scale, window, sinks, cache, max_pages, out,
+                                    lse or None, workspace, workspace_bytes, stream or None)
+    _check(st, "tri_attn_paged4_fwd")
+
+
+def tri_attn_prompt_fwd(q, k, v, dtype, cu_seqlens_q, cu_seqlens_k, num_seqs, total_q, total_k, max_seqlen_q,
+                        max_seqlen_k, Hq, Hk, D, scale, q_row_stride, k_row_stride, v_row_stride, out, lse,
+                        stream) -> None:
+    st = load().tri_attn_prompt_fwd(q, k, v, dtype, cu_seqlens_q, cu_seqlens_k, num_seqs, total_q, total_k, max_seqlen_q,
+                                    max_seqlen_k, Hq, Hk, D, scale, q_row_stride, k_row_stride, v_row_stride, out,
+                                    lse or None, stream or None)
+    _check(st, "tri_attn_prompt_fwd")
+
+
+def tri_attn_prompt_bwd(q, k, v, dtype, cu_seqlens_q, cu_seqlens_k, num_seqs, total_q, total_k, max_seqlen_q,
+                        max_seqlen_k, Hq, Hk, D, scale, q_row_stride, k_row_stride, v_row_stride, lse, out, d_out, dq, dk,
+                        dv, workspace, workspace_bytes, stream) -> None:
+    st = load().tri_attn_prompt_bwd(q, k, v, dtype, cu_seqlens_q, cu_seqlens_k, num_seqs, total_q, total_k, max_seqlen_q,
+                                    max_seqlen_k, Hq, Hk, D, scale, q_row_stride, k_row_stride, v_row_stride, lse, out,
+                                    d_out, dq, dk, dv, workspace or None, workspace_bytes, stream or None)
+    _check(st, "tri_attn_prompt_bwd")
+
+
+@functools.lru_cache(maxsize=256)
+def tri_attn_prompt_bwd_workspace_size(dtype, total_q, Hq, D) -> int:
+    return int(load().tri_attn_prompt_bwd_workspace_size(dtype, total_q, Hq, D))
 
 
 def tri_attn_mask_to_kv_lengths(mask, B, N, K, kv_lengths, nonprefix_count, stream) -> None:

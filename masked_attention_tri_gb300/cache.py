@@ -1,19 +1,20 @@
 """A paged cache of keys and values, and the operators that fill and read it.
 
 Pages are shared by all sequences; a page table gives each sequence its pages in
-order.  The cache holds the inputs' type, or 8-bit e4m3 codes with one fp32 scale
-for each (page, head).  The work runs in libtriattn.so's kernels.
+order.  The cache holds the inputs' type, 8-bit e4m3 codes with one fp32 scale
+for each (page, head), or 4-bit whole numbers with an e4m3 scale for 16 neighbours.  The work runs in libtriattn.so's kernels.
 """
 from __future__ import annotations
 
+import ctypes
 import math
-from typing import Optional
+from typing import Optional, Union
 
 import torch
 
 from . import abi
 from .api import _DT, _check_out, _int32, _need, _on, _ptr, _row_stride, _stream
-from .positions import Rotary, _check_rotary
+from .positions import Rotary, _check_positions, _check_rotary
 
 _CACHE_DT = {**_DT, torch.float8_e4m3fn: abi.TA_E4M3}
 
@@ -66,6 +67,71 @@ class PagedKVCache:
         return cls(k, v, ks, vs)
 
 
+class PagedKVCache4:
+    """The pages of a 4-bit cache: an element of head h stands for n * scale * factor[h], n a whole number from -7 to 7.
+
+    k, v: uint8 (num_pages, Hk, page_size, D / 2), two codes n + 8 a byte (the even element in the low half);
+    k_scale, v_scale: float8_e4m3fn (num_pages, Hk, page_size, D / 16), one for 16 neighbouring elements of a row;
+    k_factor, v_factor: float32 (Hk,) or None (1), positive, fixed for the cache's life (powers of two cost no
+    precision; a factor around the 100th part of a head's usual magnitudes keeps its scales in e4m3's middle).
+
+    The tensors are used in place.  Pages and heads may be strided (a head's page is contiguous), such as the halves
+    of one (num_pages, 2, Hk, page_size, D / 2) buffer.  page_size is a power of two from 16 to 1024, D a multiple
+    of 32.
+    """
+
+    def __init__(self, k, v, k_scale, v_scale, k_factor=None, v_factor=None):
+        for t, nm in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{nm} must be a torch.Tensor")
+            if t.dim() != 4:
+                raise ValueError(f"{nm} must have four dimensions (num_pages, Hk, page_size, ...)")
+            want = torch.uint8 if nm in "kv" else torch.float8_e4m3fn
+            if t.dtype != want:
+                raise TypeError(f"{nm} must be {want}")
+            if t.device != k.device:
+                raise ValueError(f"{nm} is on {t.device}, expected {k.device}")
+            if t.stride(3) != 1 or (t.shape[2] > 1 and t.stride(2) != t.shape[3]):
+                raise ValueError(f"{nm}: a head's page (the last two dimensions) must be contiguous")
+        self.num_pages, self.heads, self.page_size, half = k.shape
+        self.head_dim, self.dtype, self.device = 2 * half, torch.uint8, k.device
+        if self.head_dim % 32:
+            raise ValueError("the head dimension must be a multiple of 32")
+        if v.shape != k.shape:
+            raise ValueError("k and v must share their shape")
+        for t, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if tuple(t.shape) != (self.num_pages, self.heads, self.page_size, self.head_dim // 16):
+                raise ValueError(f"{nm} must be {(self.num_pages, self.heads, self.page_size, self.head_dim // 16)}")
+        for t, nm in ((k_factor, "k_factor"), (v_factor, "v_factor")):
+            if t is None:
+                continue
+            _need(t, nm, k.device)
+            if t.dtype != torch.float32 or tuple(t.shape) != (self.heads,):
+                raise ValueError(f"{nm} must be float32 {(self.heads,)}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.k_factor, self.v_factor = k_factor, v_factor
+        strides = (ctypes.c_longlong * 8)()
+        parts = (k, v, k_scale, v_scale)
+        if not all(t.is_contiguous() for t in parts):
+            for i, t in enumerate(parts):
+                head = t.stride(1) if t.shape[1] > 1 else t.shape[2] * t.shape[3]
+                strides[2 * i] = t.stride(0) if t.shape[0] > 1 else max(head * t.shape[1], t.shape[2] * t.shape[3])
+                strides[2 * i + 1] = head
+        self._c = abi.Cache4(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(k_factor) or None,
+                             _ptr(v_factor) or None, self.num_pages, self.page_size, strides)
+
+    @classmethod
+    def empty(cls, num_pages, heads, page_size, head_dim, k_factor=None, v_factor=None, device="cuda"):
+        """A new cache; its memory is not initialised (rows are written before they are read)."""
+        k, v = (torch.empty(num_pages, heads, page_size, head_dim // 2, dtype=torch.uint8, device=device) for _ in range(2))
+        ks, vs = (torch.empty(num_pages, heads, page_size, head_dim // 16, dtype=torch.uint8,
+                              device=device).view(torch.float8_e4m3fn) for _ in range(2))
+        return cls(k, v, ks, vs, k_factor, v_factor)
+
+
+_CACHES = (PagedKVCache, PagedKVCache4)
+
+
 def _table(page_table, kv_lengths, cu_seqlens, dev):
     """(number of sequences, pages a sequence) of the three int32 tensors that describe the sequences."""
     for t, nm in ((page_table, "page_table"), (kv_lengths, "kv_lengths")):
@@ -94,7 +160,7 @@ def _rows(t, name, dev, dtype, total, D):
     return _row_stride(t, name, dev)
 
 
-def kv_cache_append(cache: PagedKVCache, k, v, page_table, kv_lengths, cu_seqlens=None, max_seqlen=1, *,
+def kv_cache_append(cache: Union[PagedKVCache, PagedKVCache4], k, v, page_table, kv_lengths, cu_seqlens=None, max_seqlen=1, *,
                     rotary: Optional[Rotary] = None, positions=None, q=None, out_q=None):
     """Writes the new rows k, v (total, Hk, D) of each sequence into the cache, in place.
 
@@ -104,14 +170,17 @@ def kv_cache_append(cache: PagedKVCache, k, v, page_table, kv_lengths, cu_seqlen
     sequence holds after this call: the new rows are the last of them.
     page_table (S, max_pages) int32; a page that is written has one place in the
     tables of the call.  rotary turns k, and q (total, Hq, D) if given, by each row's slot or
-    by positions (total,) int32.  Returns the turned q (out_q, which may be q), or None.
+    by positions (total,) int32 ((axes, total) where rotary has sections; without positions every axis
+    is the slot).  Returns the turned q (out_q, which may be q), or None.
 
     An 8-bit cache takes a power-of-two scale for each (page, head): rows that need
     a larger one re-code the rows before them.  It starts anew with the row in slot 0 of the page and does not
     shrink when rows are written over.  Infinities and NaN become NaN.
+    A 4-bit cache takes an e4m3 scale for 16 elements of a row, and rows keep their codes (rotary.dim a multiple of
+    32); an infinity or NaN makes its 16 elements NaN.
     """
-    if not isinstance(cache, PagedKVCache):
-        raise TypeError("cache must be a PagedKVCache")
+    if not isinstance(cache, _CACHES):
+        raise TypeError("cache must be a PagedKVCache or a PagedKVCache4")
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("expected k (total, Hk, D)")
     dev = k.device
@@ -147,25 +216,89 @@ def kv_cache_append(cache: PagedKVCache, k, v, page_table, kv_lengths, cu_seqlen
     if positions is not None:
         if rotary is None:
             raise ValueError("positions need rotary")
-        _need(positions, "positions", dev)
-        if positions.dtype != torch.int32 or positions.numel() != total:
-            raise ValueError("positions must be int32 with one entry per row")
-    turns, dim, inter, ms = 0, 0, False, 1.0
+        _check_rotary(rotary, dev)
+        _check_positions(positions, rotary, dev, total)
+    turns, dim, inter, ms, axes, pair_axes = 0, 0, False, 1.0, 1, None
     if rotary is not None:
         _check_rotary(rotary, dev)
         turns, dim, inter, ms = _ptr(rotary.turns), rotary.dim, rotary.interleaved, rotary.attention_factor
+        axes, pair_axes = rotary.num_axes, rotary.pair_axes
     if total == 0 or S == 0:
         return out_q
+    rows = (_ptr(q), _ptr(k), _ptr(v), _DT[k.dtype], _ptr(cu_seqlens), _ptr(kv_lengths), _ptr(page_table), S, total,
+            max_seqlen, Hq, Hk, D, q_rs, k_rs, v_rs, qo_rs, _ptr(positions))
     with _on(dev):
-        abi.tri_attn_kv_append(_ptr(q), _ptr(k), _ptr(v), _DT[k.dtype], _ptr(cu_seqlens), _ptr(kv_lengths),
-                               _ptr(page_table), S, total, max_seqlen, Hq, Hk, D, q_rs, k_rs, v_rs, qo_rs,
-                               _ptr(positions), turns, dim, inter, ms, _ptr(cache.k), _ptr(cache.v), cache._code,
-                               _ptr(cache.k_scale), _ptr(cache.v_scale), cache.num_pages, cache.page_size, MP,
-                               cache._strides[0], cache._strides[1], _ptr(out_q), _stream(dev))
+        if isinstance(cache, PagedKVCache4):
+            abi.tri_attn_kv_append4(*rows, axes, _ptr(pair_axes), turns, dim, inter, ms, cache._c, MP, _ptr(out_q),
+                                    _stream(dev))
+            return out_q
+        rest = (turns, dim, inter, ms, _ptr(cache.k), _ptr(cache.v), cache._code, _ptr(cache.k_scale),
+                _ptr(cache.v_scale), cache.num_pages, cache.page_size, MP, cache._strides[0], cache._strides[1],
+                _ptr(out_q), _stream(dev))
+        if pair_axes is None:
+            abi.tri_attn_kv_append(*rows, *rest)
+        else:
+            abi.tri_attn_kv_append_axes(*rows, axes, _ptr(pair_axes), *rest)
     return out_q
 
 
-def paged_attention(q, cache: PagedKVCache, page_table, kv_lengths, cu_seqlens_q=None, max_seqlen_q=1, scale=None, *,
+def kv_cache_read(cache: Union[PagedKVCache, PagedKVCache4], page_table, kv_lengths, cu_seqlens=None, max_seqlen=1,
+                  total=None, *, dtype=None, out_k=None, out_v=None):
+    """Rows of the cache back as packed (k, v), each (total, Hk, D).
+
+    cu_seqlens (S + 1,) int32 splits the rows over the sequences (at most max_seqlen each; none is fine); without it
+    there is one row for each sequence.  A sequence's rows are the last of its kv_lengths (S,) int32 slots, which may
+    count fewer than it holds: a prefix for ``prompt_attention``, say.  total: rows of the outputs (at least the last
+    entry of cu_seqlens; rows past that are left alone).  dtype: of the outputs where the cache holds codes (bfloat16
+    by default), each rounded once.  out_k, out_v: outputs given, row-strided views among them.
+    """
+    if not isinstance(cache, _CACHES):
+        raise TypeError("cache must be a PagedKVCache or a PagedKVCache4")
+    dev, Hk, D = cache.device, cache.heads, cache.head_dim
+    if dev.type != "cuda":
+        raise ValueError("kv_cache_read runs on CUDA tensors only")
+    S, MP = _table(page_table, kv_lengths, cu_seqlens, dev)
+    max_seqlen = int(max_seqlen)
+    if total is None:
+        if cu_seqlens is not None and out_k is None:
+            raise ValueError("with cu_seqlens the rows of the outputs are counted by total, or by out_k")
+        total = S if cu_seqlens is None else out_k.shape[0]
+    total = int(total)
+    if total < 0:
+        raise ValueError("total must not be negative")
+    if cu_seqlens is None and (total != S or max_seqlen != 1):
+        raise ValueError("without cu_seqlens there is one row for each sequence")
+    if (out_k is None) != (out_v is None):
+        raise ValueError("out_k and out_v are given together")
+    codes = isinstance(cache, PagedKVCache4) or cache.dtype == torch.float8_e4m3fn
+    if dtype is None:
+        dtype = out_k.dtype if out_k is not None else torch.bfloat16 if codes else cache.dtype
+    if dtype not in _DT:
+        raise TypeError("dtype must be float32, float16 or bfloat16")
+    if not codes and dtype != cache.dtype:
+        raise TypeError(f"the cache holds {cache.dtype}, and its rows come back as that")
+    if out_k is None:
+        out_k, out_v = (torch.empty(total, Hk, D, dtype=dtype, device=dev) for _ in range(2))
+        k_rs = v_rs = 0
+    else:
+        k_rs, v_rs = _rows(out_k, "out_k", dev, dtype, total, D), _rows(out_v, "out_v", dev, dtype, total, D)
+        if out_k.shape[1] != Hk or out_v.shape[1] != Hk:
+            raise ValueError(f"out_k and out_v must have the cache's {Hk} heads")
+    if total == 0 or S == 0:
+        return out_k, out_v
+    seqs = (_ptr(cu_seqlens), _ptr(kv_lengths), _ptr(page_table), S, total, max_seqlen, Hk, D)
+    outs = (_ptr(out_k), _ptr(out_v), _DT[dtype], k_rs, v_rs, _stream(dev))
+    with _on(dev):
+        if isinstance(cache, PagedKVCache4):
+            abi.tri_attn_kv_read4(*seqs, cache._c, MP, *outs)
+        else:
+            abi.tri_attn_kv_read(*seqs, _ptr(cache.k), _ptr(cache.v), cache._code, _ptr(cache.k_scale),
+                                 _ptr(cache.v_scale), cache.num_pages, cache.page_size, MP, cache._strides[0],
+                                 cache._strides[1], *outs)
+    return out_k, out_v
+
+
+def paged_attention(q, cache: Union[PagedKVCache, PagedKVCache4], page_table, kv_lengths, cu_seqlens_q=None, max_seqlen_q=1, scale=None, *,
                     window=None, sinks=0, return_aux=False, out=None):
     """Attention of each sequence's newest tokens over its pages of the cache.
 
@@ -179,11 +312,11 @@ def paged_attention(q, cache: PagedKVCache, page_table, kv_lengths, cu_seqlens_q
     float32 (Hq, total_q)); a row that sees no slot gets O = 0 and lse = -inf.
 
     Made for few new tokens a sequence: K and V are read again for each 16 rows (tokens x query heads
-    of a key head).  A whole prompt without a cached prefix runs faster through ``varlen_attention``
-    (which takes as many heads of k and v as of q).
+    of a key head).  A whole prompt, or a chunk of one with its prefix read back by ``kv_cache_read``, runs
+    faster through ``prompt_attention``.
     """
-    if not isinstance(cache, PagedKVCache):
-        raise TypeError("cache must be a PagedKVCache")
+    if not isinstance(cache, _CACHES):
+        raise TypeError("cache must be a PagedKVCache or a PagedKVCache4")
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     if q.dim() != 3:
@@ -221,10 +354,14 @@ def paged_attention(q, cache: PagedKVCache, page_table, kv_lengths, cu_seqlens_q
         code = _DT[q.dtype]
         nbytes = abi.tri_attn_paged_workspace_size(code, max_seqlen_q, Hq, Hk, D)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        rows = (_ptr(q), code, _ptr(cu_seqlens_q), _ptr(kv_lengths), _ptr(page_table), S, total, max_seqlen_q, Hq, Hk, D,
+                q_rs, s, 0 if window is None else _int32(window), _int32(sinks))
+        outs = (_ptr(out), _ptr(lse), _ptr(ws), nbytes, _stream(dev))
         with _on(dev):
-            abi.tri_attn_paged_fwd(_ptr(q), code, _ptr(cu_seqlens_q), _ptr(kv_lengths), _ptr(page_table), S, total,
-                                   max_seqlen_q, Hq, Hk, D, q_rs, s, 0 if window is None else _int32(window), _int32(sinks),
-                                   _ptr(cache.k), _ptr(cache.v), cache._code, _ptr(cache.k_scale), _ptr(cache.v_scale),
-                                   cache.num_pages, cache.page_size, MP, cache._strides[0], cache._strides[1],
-                                   _ptr(out), _ptr(lse), _ptr(ws), nbytes, _stream(dev))
+            if isinstance(cache, PagedKVCache4):
+                abi.tri_attn_paged4_fwd(*rows, cache._c, MP, *outs)
+            else:
+                abi.tri_attn_paged_fwd(*rows, _ptr(cache.k), _ptr(cache.v), cache._code, _ptr(cache.k_scale),
+                                       _ptr(cache.v_scale), cache.num_pages, cache.page_size, MP, cache._strides[0],
+                                       cache._strides[1], *outs)
     return (out, lse) if return_aux else out

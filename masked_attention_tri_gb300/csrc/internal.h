@@ -136,16 +136,26 @@ struct RotaryParams {
     const void* k;              // NULL with Hk = 0
     void* q_out;
     void* k_out;
-    const int32_t* positions;   // (total)
+    const int32_t* positions;   // (total), or with axes (num_axes, total)
+    const int32_t* axes;        // (dim / 2): the axis of each pair, or NULL (one axis)
     const unsigned long long* turns;  // (dim / 2): turns per position, 2^-64 units
-    int dtype, dim, interleaved, inverse;
+    int dtype, dim, interleaved, inverse, num_axes;
     float mscale;
     int total, Hq, Hk, D;
     long long q_rs, k_rs, qo_rs, ko_rs;  // elements between rows
 };
 cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t stream);
 
-// New k / v rows (and the rotation of q) into a paged cache.  C of the caches: dtype or e4m3.
+// The parts of a 4-bit cache: codes two a byte (the even element in the low half), 16 of them to an e4m3 scale, a
+// factor a head; byte strides {page, head} (a head's slots lie one after the other).
+struct Cache4 {
+    uint8_t* codes[2];          // k, v: (num_pages, Hk, page, D / 2)
+    uint8_t* scale[2];          // (num_pages, Hk, page, D / 16)
+    const float* factor[2];     // (Hk) or NULL: 1
+    long long cs[2][2], ss[2][2];
+};
+
+// New k / v rows (and the rotation of q) into a paged cache.  C of the caches: dtype, e4m3 or 4-bit codes.
 struct KvAppendParams {
     const void* q;              // (total, Hq, D) or NULL
     const void* k;              // (total, Hk, D)
@@ -158,13 +168,15 @@ struct KvAppendParams {
     const int32_t* cu;          // (num_seqs + 1), or NULL: one row a sequence
     const int32_t* kv_len;      // (num_seqs): rows held after the call
     const int32_t* table;       // (num_seqs, max_pages)
-    const int32_t* positions;   // (total), or NULL: the row's slot
+    const int32_t* positions;   // (total), or with axes (num_axes, total), or NULL: the row's slot
+    const int32_t* axes;        // (dim / 2): the axis of each pair, or NULL
     const unsigned long long* turns;
-    int dtype, cache_dtype, dim, interleaved;  // dim 0: no rotation
+    int dtype, cache_dtype, dim, interleaved, num_axes;  // dim 0: no rotation
     float mscale;
     int num_seqs, total, max_n, Hq, Hk, D, num_pages, page, max_pages;
     long long q_rs, k_rs, v_rs, qo_rs;
     long long ks[3], vs[3];     // element strides {page, head, slot} of the caches
+    Cache4 c4;                  // 4-bit caches
     int* status;
 };
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream);
@@ -191,11 +203,57 @@ struct PagedParams {
     float scale_log2e;
     long long q_rs;
     long long ks[3], vs[3];     // element strides {page, head, slot} of the caches
+    Cache4 c4;                  // 4-bit caches
 };
 int paged_rows(int dtype, int max_q, int G, int D);  // RT of a problem
 int paged_tile(int dtype, int cache_dtype, int D);   // and its tile
 size_t paged_workspace_bytes(int RT, int D);
 cudaError_t launch_paged(const PagedParams& p, cudaStream_t stream);
+
+// Rows of a paged cache into packed k / v rows.
+struct KvReadParams {
+    const void* cache[2];       // k, v: as in KvAppendParams, or c4
+    const float* scale[2];      // (num_pages, Hk), e4m3 only
+    void* out[2];               // (total, Hk, D) of dtype
+    const int32_t* cu;          // (num_seqs + 1), or NULL: one row a sequence
+    const int32_t* kv_len;      // (num_seqs): the rows read are the last of these slots
+    const int32_t* table;
+    int dtype, cache_dtype;
+    int num_seqs, total, max_n, Hk, D, num_pages, page, max_pages;
+    long long rs[2];            // elements between rows of out
+    long long st[2][3];         // element strides {page, head, slot} of the caches
+    Cache4 c4;
+    int* status;
+};
+cudaError_t launch_kv_read(const KvReadParams& p, cudaStream_t stream);
+
+// Causal attention of packed prompts with grouped heads, and its gradients.
+struct PromptParams {
+    const void* q;              // (total_q, Hq, D)
+    const void* k;              // (total_k, Hk, D)
+    const void* v;
+    const int32_t* cu_q;        // (num_seqs + 1)
+    const int32_t* cu_k;
+    void* out;                  // (total_q, Hq, D): written by the forward, read by the backward
+    float* lse;                 // (Hq, total_q), or NULL in the forward
+    int* status;
+    int dtype, num_seqs, total_q, total_k, max_q, max_k, Hq, Hk, G, D;
+    float scale;
+    long long q_rs, k_rs, v_rs; // elements between rows
+    // backward
+    const void* d_out;          // (total_q, Hq, D)
+    void* dq;
+    void* dk;
+    void* dv;
+    float* dq_acc;              // workspace: fp32 dQ (total_q, Hq, D), tensor cores only
+    float* delta;               // workspace: dO . O (Hq, total_q)
+};
+// 16-bit inputs with D <= 128 run on tensor cores.
+inline bool prompt_on_tc(int dtype, int D) { return dtype != TA_F32 && D <= 128; }
+cudaError_t launch_prompt_simt_fwd(const PromptParams& p, cudaStream_t stream);
+cudaError_t launch_prompt_simt_bwd(const PromptParams& p, cudaStream_t stream);
+cudaError_t launch_prompt_tc_fwd(const PromptParams& p, cudaStream_t stream);
+cudaError_t launch_prompt_tc_bwd(const PromptParams& p, cudaStream_t stream);
 
 // Device address of the status word on the current device (set up once per device).
 int* status_word();

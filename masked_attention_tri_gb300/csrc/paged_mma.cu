@@ -13,6 +13,7 @@ namespace paged {
 TRIATTN_PAGED_VARIANTS(TRIATTN_PAGED_EXTERN, 0)
 TRIATTN_PAGED_VARIANTS(TRIATTN_PAGED_EXTERN, 1)
 TRIATTN_PAGED_VARIANTS(TRIATTN_PAGED_EXTERN, 2)
+TRIATTN_PAGED_VARIANTS(TRIATTN_PAGED_EXTERN, 3)
 
 namespace {
 
@@ -33,6 +34,21 @@ cudaError_t launch_type(const MmaParams& P, cudaStream_t stream) {
 cudaError_t launch_mma(const PagedParams& p, cudaStream_t stream) {
     MmaParams P;
     P.p = p;
+    if (p.cache_dtype == TA_INT4) {
+        // (D / 2 bytes, slot, head, page); boxes of 32 bytes for each 64 columns (zeros past D), swizzled by that width
+        const int ndc = p.D <= 64 ? 1 : p.D <= 128 ? 2 : 4;
+        const uint64_t dims[4] = {(uint64_t)p.D / 2, (uint64_t)p.page, (uint64_t)p.Hk, (uint64_t)p.num_pages};
+        const uint32_t box[4] = {32u * (uint32_t)ndc, (uint32_t)(p.page < p.tile ? p.page : p.tile), 1, 1};
+        const CUtensorMapSwizzle sw = ndc == 1   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                      : ndc == 2 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                 : CU_TENSOR_MAP_SWIZZLE_128B;
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t st[3] = {(uint64_t)p.D / 2, (uint64_t)p.c4.cs[i][1], (uint64_t)p.c4.cs[i][0]};
+            if (!tc::encode_map_4d(i ? &P.tm_v : &P.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.c4.codes[i], dims, st, box, sw))
+                return cudaErrorInvalidValue;
+        }
+        return launch_type<3>(P, stream);
+    }
     const bool codes = p.cache_dtype == TA_E4M3;
     const uint64_t esz = codes ? 1 : 2;
     // (codes move as pairs: only their bytes count)

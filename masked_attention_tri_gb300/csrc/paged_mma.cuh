@@ -36,7 +36,13 @@
 // (and row g + 8 slot pi(g) + 8), pi(2i) = 2i, pi(2i + 1) = (2i ^ 4) + 1, so that the lanes' slots of V
 // are 0, 2, 4, 6 and 5, 7, 1, 3 in turn, whose swizzled reads meet no bank twice.
 //
-// Roundings: P to the products' 16-bit type (fp16 for 8-bit caches: 2^-12 of a weight),
+// Four-bit codes (cache4.cuh) become fp16 times their scales on the way, both exact: a word's codes by one logical
+// operation each that puts them into the low bits of 1024, then a fused multiplication or two on the FMA pipe (e4m3's
+// conversion instructions run at a quarter of that rate).  k index 2t, 2t + 1, 2t + 8, 2t + 9 of K's products stands for
+// elements e, e + 4, e + 1, e + 5 of lane t's word; of V a lane reads 8 NDC columns of four slots, whose
+// 16-bit halves side by side hold four columns' pairs.  The scales come into the stage by untiled copies beside the tiles.
+//
+// Roundings: P to the products' 16-bit type (fp16 for 8-bit and 4-bit caches: 2^-12 of a weight),
 // as everywhere in this library; S, the maxima, sums and O are fp32.  O is rescaled only
 // when a logit passes the reference by 2^8 (base 2: by 8), which fp16's range allows.
 #pragma once
@@ -85,14 +91,18 @@ struct MmaParams {
     PagedParams p;
 };
 
-// TYPE: 0 fp16 cache, 1 bf16 cache, 2 e4m3 codes.  NDC: 64-column chunks of D.  NT: groups of eight rows.
+// TYPE: 0 fp16 cache, 1 bf16 cache, 2 e4m3 codes, 3 four-bit codes.  NDC: 64-column chunks of D.  NT: groups of eight rows.
 template <int TYPE, int NDC, int NT>
 struct MmaConfig {
-    static constexpr bool kCodes = TYPE == 2;
-    static constexpr int kBoxes = kCodes ? (NDC + 1) / 2 : NDC;         // 128-byte columns of a tile
-    static constexpr int kSlots = 128 / kBoxes;                         // slots of a stage: 32 KB, K and V
-    static constexpr uint32_t kBoxBytes = kSlots * 128;
-    static constexpr uint32_t kStage = 2 * kBoxes * kBoxBytes;          // K boxes, then V boxes
+    static constexpr bool kCodes = TYPE == 2, kFour = TYPE == 3;
+    static constexpr int kBoxes = kFour ? 1 : kCodes ? (NDC + 1) / 2 : NDC;  // columns of a tile's rows, kRowB bytes each
+    static constexpr uint32_t kRowB = kFour ? NDC * 32 : 128;
+    // slots of a stage: 32 KB, K and V (four-bit codes: 16 KB where D <= 128)
+    static constexpr int kSlots = kFour ? (NDC == 1 ? 256 : 128) : 128 / kBoxes;
+    static constexpr uint32_t kBoxBytes = kSlots * kRowB;
+    static constexpr uint32_t kBlockB = 16 * kRowB;                     // 16 slots of a box
+    static constexpr uint32_t kScales = kFour ? kSlots * NDC * 4 : 0;   // of K's slots, and of V's
+    static constexpr uint32_t kStage = 2 * kBoxes * kBoxBytes + 2 * kScales;  // K boxes, V boxes, K scales, V scales
     static constexpr int kRows = NT * 8;
     // Consumers: with the producer eight warps, so that a thread may have 255 registers (O alone takes 16 NDC
     // NT).  Measured on 64 sequences of 1k to 16k slots in 8 bits (before the warps took two blocks at once):
@@ -146,6 +156,46 @@ __device__ __forceinline__ uint32_t codes_f16_hi(uint32_t two) {
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+// Four-bit codes u = n + 8 as fp16 numbers n, exactly: the code put into the low bits of 1024 makes 1024 + u (the low
+// code of a byte) or 1024 + 16 u (the high one).
+__device__ __forceinline__ uint32_t four_or(uint32_t w, uint32_t mask) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(y) : "r"(w), "r"(mask));
+    return y;
+}
+__device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+// The low and the high code of byte 0 of both halves of w, times s (pairs: one number of each half).
+__device__ __forceinline__ uint32_t four_lo(uint32_t w, __half2 s) {
+    return as_u32(__hmul2(__hsub2(as_h2(four_or(w, 0x000f000fu)), as_h2(0x64086408u)), s));  // - 1032
+}
+__device__ __forceinline__ uint32_t four_hi(uint32_t w, __half2 s) {
+    return as_u32(__hmul2(__hfma2(as_h2(four_or(w, 0x00f000f0u)), as_h2(0x2c002c00u), as_h2(0xd480d480u)), s));  // / 16 - 72
+}
+// ... with s / 16 and -72 s at hand (exact: s has four significant bits).
+__device__ __forceinline__ uint32_t four_hi(uint32_t w, __half2 s16, __half2 s72) {
+    return as_u32(__hfma2(as_h2(four_or(w, 0x00f000f0u)), s16, s72));
+}
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
     if constexpr (BF16)
@@ -161,8 +211,18 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
 }
-// Slot (within eight) of row i of an A operand.
-__device__ __forceinline__ int pi8(int i) { return (i & 1) ? ((i - 1) ^ 4) + 1 : i; }
+// Slot (within eight) of row i of an A operand.  (Four-bit codes: the orders in which a lane's reads of V, 4 NDC bytes of
+// slots pi(2t) and of slots pi(2t + 1), meet no bank twice.)
+template <int TYPE, int NDC>
+__device__ __forceinline__ int pi8(int i) {
+    if (TYPE != 3) return (i & 1) ? ((i - 1) ^ 4) + 1 : i;
+    return NDC == 1 ? (i >> 1) | ((i & 1) << 2) : NDC == 2 ? ((i << 1) & 7) | (i >> 2) : i;
+}
+// What the swizzle of rows of 32 NDC bytes adds to a slot's 16-byte pieces (exclusive or).
+template <int NDC>
+__device__ __forceinline__ uint32_t four_swizzle(uint32_t slot) {
+    return NDC == 1 ? (slot >> 2) & 1u : NDC == 2 ? (slot >> 1) & 3u : slot & 7u;
+}
 
 // Waits until use `use` of a stage has arrived.  A parity wait alone can tell only two neighbouring
 // uses apart, and warps run free: one may ask for a use while the one before it is still in
@@ -192,7 +252,7 @@ template <int TYPE, int NDC, int NT>
 __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_mma_kernel(const __grid_constant__ MmaParams P) {
     using C = MmaConfig<TYPE, NDC, NT>;
     constexpr bool kBF16 = TYPE == 1;
-    constexpr bool kCodes = C::kCodes;
+    constexpr bool kCodes = C::kCodes, kFour = C::kFour;
     constexpr int kBlocks = C::kSlots / 16;
     constexpr int kWarps = C::kWarps;
     const PagedParams& p = P.p;
@@ -245,7 +305,7 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
         constexpr int nbox = C::kBoxes;                // (a box past D is all zeros and reads nothing)
         const int mysub = lane % nb, mytile = lane / nb;
         const int blocks = span / 16;                  // blocks of 16 slots of one load
-        const uint32_t bytes = (uint32_t)(2 * nbox * span * 128);
+        const uint32_t bytes = 2u * (uint32_t)span * (nbox * C::kRowB + (kFour ? (uint32_t)p.D / 16u : 0u));
         int slot0 = 0, turn0 = 0;                      // the next stage and how often the ring has gone round
         bool ok = true;
         // The next batch: unit u, tiles from jb.  Its table entries and scales are loaded while the batch before it
@@ -313,11 +373,19 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                 if (go && mysub == 0) mbar_expect_tx(full(slot), ok ? (uint32_t)loads * bytes : 0u);
                 __syncwarp();
                 if (go && page >= 0 && ok) {
-                    const uint32_t dst = ring + (uint32_t)slot * C::kStage + (uint32_t)(mysub * span) * 128u;
+                    const uint32_t dst = ring + (uint32_t)slot * C::kStage + (uint32_t)(mysub * span) * C::kRowB;
                     for (int b = 0; b < nbox; ++b) {
                         const int x = b * 64;  // (16-bit units)
                         tc::tma_load_4d(dst + b * C::kBoxBytes, &P.tm_k, x, in_page, h, page, full(slot));
                         tc::tma_load_4d(dst + (C::kBoxes + b) * C::kBoxBytes, &P.tm_v, x, in_page, h, page, full(slot));
+                    }
+                    if constexpr (kFour) {  // (spans are multiples of 16 slots: 16-byte multiples)
+                        const uint32_t sb = (uint32_t)p.D / 16u;
+                        const uint32_t to = ring + (uint32_t)slot * C::kStage + 2u * C::kBoxBytes + (uint32_t)(mysub * span) * sb;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            bulk_load(to + i * C::kScales, p.c4.scale[i] + page * p.c4.ss[i][0] + h * p.c4.ss[i][1] + in_page * (int)sb,
+                                      (uint32_t)span * sb, full(slot));
                     }
                 }
                 wait = wait && !go;
@@ -351,17 +419,26 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
     auto consumers_sync = [] { tc::named_barrier(1, kWarps * 32); };
     const int g = lane / 4, t = lane % 4;
     const int sub_shift = p.page >= C::kSlots ? 3 : __ffs(p.page) - 5;  // log2 of a page's blocks (in a stage)
-    const uint32_t rg = (uint32_t)pi8(g);                      // slot (of eight) of this lane's rows of K
-    const uint32_t r0 = 2u * t, r1 = (r0 ^ 4u) + 1u;           // slots (of eight) of this lane's columns of V^T
+    const uint32_t rg = (uint32_t)pi8<TYPE, NDC>(g);           // slot (of eight) of this lane's rows of K
+    // slots (of eight) of this lane's columns of V^T
+    const uint32_t r0 = kFour ? (uint32_t)pi8<TYPE, NDC>(2 * t) : 2u * t;
+    const uint32_t r1 = kFour ? (uint32_t)pi8<TYPE, NDC>(2 * t + 1) : (r0 ^ 4u) + 1u;
     // Byte offsets in a block of 16 swizzled rows: this lane's row address of K's loads (matrices: slots
     // 0-7, slots 8-15, the same 16 bytes further; the next 32 bytes at ^ 32), 8-bit V's words of
     // columns g (rows r0, r1; the upper 64 columns at ^ 64), 16-bit V's rows of the transposing load
     // (16 columns further at ^ 32).
-    const uint32_t k_row = (uint32_t)pi8(lane & 7) + ((lane & 8) ? 8u : 0u);
-    const uint32_t k_off = k_row * 128u + ((((uint32_t)lane >> 4) ^ (k_row & 7u)) << 4);
-    const uint32_t v_off0 = r0 * 128u + (((uint32_t)(g >> 1) ^ r0) << 4) + (g & 1) * 8u;
-    const uint32_t v_off1 = r1 * 128u + (((uint32_t)(g >> 1) ^ r1) << 4) + (g & 1) * 8u;
-    const uint32_t v_row = (uint32_t)pi8(lane & 7) + ((lane & 16) ? 8u : 0u);
+    // Four-bit: the same load of K (16 columns are now 32 codes); V's words of columns 8 NDC g.
+    const uint32_t k_row = (uint32_t)pi8<TYPE, NDC>(lane & 7) + ((lane & 8) ? 8u : 0u);
+    const uint32_t k_off =
+        kFour ? k_row * C::kRowB + ((((uint32_t)lane >> 4) ^ four_swizzle<NDC>(k_row)) << 4)
+              : k_row * 128u + ((((uint32_t)lane >> 4) ^ (k_row & 7u)) << 4);
+    auto v_off4 = [&](uint32_t r) {
+        const uint32_t byte = (uint32_t)g * NDC * 4u;
+        return r * C::kRowB + (((byte >> 4) ^ four_swizzle<NDC>(r)) << 4) + (byte & 15u);
+    };
+    const uint32_t v_off0 = kFour ? v_off4(r0) : r0 * 128u + (((uint32_t)(g >> 1) ^ r0) << 4) + (g & 1) * 8u;
+    const uint32_t v_off1 = kFour ? v_off4(r1) : r1 * 128u + (((uint32_t)(g >> 1) ^ r1) << 4) + (g & 1) * 8u;
+    const uint32_t v_row = (uint32_t)pi8<TYPE, NDC>(lane & 7) + ((lane & 16) ? 8u : 0u);
     const uint32_t v_offt = v_row * 128u + ((((uint32_t)lane >> 3 & 1u) ^ (v_row & 7u)) << 4);
     // Reference of a row that has seen no key: below the logits of any finite bf16 rows whose sums fp32 holds (far above
     // it a difference from it overflows to an infinity, which is a new maximum like any other).
@@ -395,7 +472,10 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
             if (r >= C::kRows) break;
             float factor = p.scale_log2e;
             uint2 (&x)[kQPieces] = xq[i];
-            if constexpr (kCodes) {
+            if constexpr (kFour) {
+                if (p.c4.factor[0]) factor *= p.c4.factor[0][u.h];
+            }
+            if constexpr (kCodes || kFour) {
                 const bool bf = p.dtype == TA_BF16;
                 float y[kQPieces][4];
                 uint32_t most = 0;
@@ -425,6 +505,16 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
             for (int c = 0; c < kQPieces; ++c) {
                 const int d = c * 128 + lane * 4, ch = d / 64, in = d % 64;
                 if (ch >= NDC) continue;
+                if constexpr (kFour) {
+                    // Element e of eight neighbours (four-bit codes of a word): a pair is (e, e + 4), e / 2 of four the
+                    // product, e % 2 the operand's register; lane t of 32 columns has the word of columns 8 t.
+                    uint8_t* to = sq + ((d / 32 * 2) * NT + r / 8) * 256 + (r % 8) * 32 + (d % 32) / 8 * 8 + (d % 8) / 4 * 2;
+                    const uint32_t w[2] = {x[c].x, x[c].y};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint16_t*>(to + (e / 2) * NT * 256 + (e % 2) * 4) = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+                    continue;
+                }
                 uint8_t* dst = sq + ((ch * 4 + in / 16) * NT + r / 8) * 256 + (r % 8) * 32;
                 if constexpr (kCodes) {
                     *reinterpret_cast<uint2*>(dst + (in % 16) / 4 * 8) = x[c];
@@ -505,13 +595,20 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
             auto block = [&](auto plain_tag, auto m_tag, int blk) {
                 constexpr bool PLAIN = decltype(plain_tag)::value;
                 constexpr int M = decltype(m_tag)::value;
-                const uint32_t kb = stage + (uint32_t)blk * 2048u, vb = kb + C::kBoxes * C::kBoxBytes;
+                const uint32_t kb = stage + (uint32_t)blk * C::kBlockB, vb = kb + C::kBoxes * C::kBoxBytes;
+                // (four-bit: the scales of the block's first slot, sb bytes a slot)
+                const uint32_t sb = (uint32_t)p.D / 16u;
+                [[maybe_unused]] const uint32_t ksb = stage + 2u * C::kBoxBytes + (uint32_t)blk * 16u * sb, vsb = ksb + C::kScales;
                 const int key0 = stage_key0 + blk * 16;
                 if constexpr (!PLAIN) {
                     // Slots that no row sees may hold anything: their V is made 0 in the stage (their weight is 0,
                     // but 0 times NaN is not).
+                    // (Four-bit: their scales.)
                     if (!unit_sees(p, u.t, key0 + lane / 2)) {
-                        for (int b = 0; b < C::kBoxes; ++b)
+                        if constexpr (kFour) {
+                            for (uint32_t i = lane & 1; i < sb; i += 2)
+                                asm volatile("st.shared.u8 [%0], %1;" ::"r"(vsb + (uint32_t)(lane / 2) * sb + i), "r"(0u) : "memory");
+                        } else for (int b = 0; b < C::kBoxes; ++b)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 tc::st_shared_v4(vb + b * C::kBoxBytes + (uint32_t)(lane / 2) * 128u + (lane & 1) * 64u + i * 16u,
@@ -538,6 +635,27 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                         mma16816<kBF16>(s[mb][nt], a0, a1, a2, a3, b);
                     }
                 };
+                if constexpr (kFour) {
+                    // 32 bytes of a row at a time are 64 columns, half of which share a lane's scale: two products each
+#pragma unroll
+                    for (int c = 0; c < NDC; ++c)
+#pragma unroll
+                        for (int mb = 0; mb < M; ++mb) {
+                            uint32_t a[4];
+                            ldsm_x4(kb + mb * C::kBlockB + (k_off ^ (32u * c)), a);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (c * 64 + h * 32 >= p.D) continue;  // (there are no scales)
+                                const uint32_t at = ksb + (mb * 16u + rg) * sb + c * 4u + h * 2u + (t >> 1);
+                                const uint32_t s2 = codes_f16(lds8(at) | (lds8(at + 8u * sb) << 8));
+                                const __half2 s0 = __low2half2(as_h2(s2)), s1 = __high2half2(as_h2(s2));
+                                const uint32_t w0 = a[2 * h], w1 = a[2 * h + 1];
+                                step(mb, c * 4 + h * 2, four_lo(w0, s0), four_lo(w1, s1), four_hi(w0, s0), four_hi(w1, s1));
+                                step(mb, c * 4 + h * 2 + 1, four_lo(w0 >> 8, s0), four_lo(w1 >> 8, s1), four_hi(w0 >> 8, s0),
+                                     four_hi(w1 >> 8, s1));
+                            }
+                        }
+                } else {
                 // (32 bytes of a row at a time: 16 columns, or 32 codes)
 #pragma unroll
                 for (int i = 0; i < (kCodes ? kSteps / 2 : kSteps); ++i) {
@@ -552,6 +670,7 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                             step(mb, i, a[0], a[1], a[2], a[3]);
                         }
                     }
+                }
                 }
                 // ---- Logits in base 2 (with the value scale's log2) less the reference: y = x - m.
                 float4 sc[M];
@@ -637,6 +756,56 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                         b[mb][nt].x = transpose8(pack2<kBF16>(pr[0], pr[1]));
                         b[mb][nt].y = transpose8(pack2<kBF16>(pr[2], pr[3]));
                     }
+                if constexpr (kFour) {
+#pragma unroll
+                    for (int mb = 0; mb < M; ++mb) {
+                        // words j of slots r0, r1, r0 + 8, r1 + 8: columns 8 (NDC g + j) and on
+                        uint32_t w[4][NDC];
+                        const uint32_t at[4] = {v_off0, v_off1, v_off0 + 8u * C::kRowB, v_off1 + 8u * C::kRowB};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t from = vb + mb * C::kBlockB + at[i];
+                            if constexpr (NDC == 1) {
+                                w[i][0] = lds32(from);
+                            } else if constexpr (NDC == 2) {
+                                const uint2 x = lds64(from);
+                                w[i][0] = x.x, w[i][1] = x.y;
+                            } else {
+                                const uint4 x = lds128(from);
+                                w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < (NDC + 1) / 2; ++q) {  // the lane's groups of 16 columns
+                            const uint32_t sg = vsb + (mb * 16u) * sb + (NDC == 1 ? (uint32_t)g >> 1 : (uint32_t)(g * (NDC / 2) + q));
+                            __half2 s[2], s16[2], s72[2];  // of slots r0, r1, and of r0 + 8, r1 + 8
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t f = sg + i * 8u * sb;
+                                s[i] = as_h2(codes_f16(lds8(f + r0 * sb) | (lds8(f + r1 * sb) << 8)));
+                                s16[i] = __hmul2(s[i], as_h2(0x2c002c00u));
+                                s72[i] = __hmul2(s[i], as_h2(0xd480d480u));
+                            }
+#pragma unroll
+                            for (int j = 2 * q; j < (NDC == 1 ? 1 : 2 * q + 2); ++j)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {  // four columns: the slots' halves side by side
+                                    const uint32_t sel = h ? 0x7632u : 0x5410u;
+                                    uint32_t x = __byte_perm(w[0][j], w[1][j], sel), z = __byte_perm(w[2][j], w[3][j], sel);
+#pragma unroll
+                                    for (int m2 = 0; m2 < 2; ++m2) {
+                                        const uint32_t f0 = four_lo(x, s[0]), f1 = four_hi(x, s16[0], s72[0]);
+                                        const uint32_t f2 = four_lo(z, s[1]), f3 = four_hi(z, s16[1], s72[1]);
+#pragma unroll
+                                        for (int nt = 0; nt < NT; ++nt)
+                                            mma16816<false>(o[j * 4 + h * 2 + m2][nt], f0, f1, f2, f3, b[mb][nt]);
+                                        x >>= 8;
+                                        z >>= 8;
+                                    }
+                                }
+                        }
+                    }
+                } else {
 #pragma unroll
                 for (int mb = 0; mb < M; ++mb)
 #pragma unroll
@@ -668,6 +837,7 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                             }
                         }
                     }
+                }
             };
             if (plain_stage) {
                 // (two at a time where a warp has several: the one's products fill the other's waits)
@@ -732,7 +902,7 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
             srow[r] = make_float2(M, L);
         }
         // element e of accumulator i2, nt: row nt * 8 + 2 t + (e & 1), column 64 c + 8 g + 2 h + (e >> 1) of 8-bit V,
-        // 64 c + 16 h + g + 8 (e >> 1) of 16-bit V (c = i2 / 4, h = i2 % 4)
+        // 64 c + 16 h + g + 8 (e >> 1) of 16-bit V (c = i2 / 4, h = i2 % 4), 8 NDC g + 2 i2 + (e >> 1) of four-bit V
 #pragma unroll 1
         for (int turn = (kWarps - 1) / C::kBufs; turn >= 0; --turn) {
             if (warp / C::kBufs == turn) {
@@ -744,10 +914,11 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                     for (int e = 0; e < 2; ++e) {
                         float* row = dst + (nt * 8 + 2 * t + e) * C::kOStride;
                         const float ff = f[nt][e];
-                        if constexpr (kCodes) {  // eight neighbouring columns a chunk
+                        if constexpr (kCodes || kFour) {  // eight neighbouring columns a chunk, or 8 NDC
 #pragma unroll
                             for (int i2 = 0; i2 < NDC * 4; i2 += 2) {
-                                float4* q = reinterpret_cast<float4*>(row + (i2 / 4) * 64 + g * 8 + (i2 % 4) * 2);
+                                float4* q = reinterpret_cast<float4*>(
+                                    kFour ? row + g * (8 * NDC) + i2 * 2 : row + (i2 / 4) * 64 + g * 8 + (i2 % 4) * 2);
                                 float4 v = make_float4(o[i2][nt][e] * ff, o[i2][nt][e + 2] * ff, o[i2 + 1][nt][e] * ff,
                                                        o[i2 + 1][nt][e + 2] * ff);
                                 if (!first) {
@@ -773,6 +944,7 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
         const bool whole = u.starts && u.ends;
         const int slot = u.starts ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
         const int D4 = p.D / 4;
+        const float v_factor = kFour && p.c4.factor[1] ? p.c4.factor[1][u.h] : 1.f;
         for (int e = threadIdx.x; e < u.rows * D4; e += kWarps * 32) {
             const int r = e / D4, d = (e - r * D4) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -784,6 +956,7 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                 x.z += y.z;
                 x.w += y.w;
             }
+            if constexpr (kFour) x.x *= v_factor, x.y *= v_factor, x.z *= v_factor, x.w *= v_factor;
             const float2 ML = srow[r];
             if (whole) {
                 const int row = row_first + r;

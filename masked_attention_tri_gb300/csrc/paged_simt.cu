@@ -1,5 +1,5 @@
 // paged_simt.cu -- attention over a paged cache on CUDA cores in exact fp32: fp32
-// queries, with an fp32 or an 8-bit cache; and the kernel that joins split rows.
+// queries, with an fp32, an 8-bit or a 4-bit cache; and the kernel that joins split rows.
 //
 // One CTA of eight warps per share of the tile axis (paged.cuh); the warps of a CTA
 // take the tiles of a unit in turn, each with its own running maximum, sum and O,
@@ -9,6 +9,9 @@
 // after which each lane holds one (slot, row) logit.  Bound: the FMAs
 // (8 rows x 2 an element) and shuffles, at about half the memory rate for fp32.
 
+#include <type_traits>
+
+#include "cache4.cuh"
 #include "paged.cuh"
 
 namespace triattn {
@@ -34,9 +37,18 @@ __device__ __forceinline__ float4 load4<uint8_t>(const uint8_t* p) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// NC: vectors of 4 elements a lane (D up to 128 NC).
+// One slot's row of a 4-bit cache, elements [d, d + 4).
+__device__ __forceinline__ float4 load4_codes(const uint8_t* codes, const uint8_t* scale, int d) {
+    const uint32_t w = *reinterpret_cast<const uint16_t*>(codes + d / 2);
+    const float s = cache4::scale_value(scale[d / 16]);
+    auto value = [&](int i) { return (float)((int)((w >> (4 * i)) & 15u) - 8) * s; };
+    return make_float4(value(0), value(1), value(2), value(3));
+}
+
+// C: the cache's elements: fp32, uint8_t (e4m3) or cache4::Code.  NC: vectors of 4 elements a lane (D up to 128 NC).
 template <typename C, int NC>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams p) {
+    constexpr bool kFour = std::is_same<C, cache4::Code>::value, kCodes = std::is_same<C, uint8_t>::value;
     extern __shared__ float smem[];  // O [kWarps][kRows][D], (m, l) [kWarps][kRows]
     __shared__ long long scan[kWarps], found[2];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -88,10 +100,23 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
                     continue;
                 }
                 const int slot = k0 % p.page;
-                const C* kp = static_cast<const C*>(p.k_cache) + page * p.ks[0] + u.h * p.ks[1] + slot * p.ks[2];
-                const C* vp = static_cast<const C*>(p.v_cache) + page * p.vs[0] + u.h * p.vs[1] + slot * p.vs[2];
+                // row kk of four slots, elements [d, d + 4)
+                auto row = [&](int kind, int kk, int d) {
+                    if constexpr (kFour) {
+                        const Cache4& c = p.c4;
+                        return load4_codes(c.codes[kind] + page * c.cs[kind][0] + u.h * c.cs[kind][1] + (long long)(slot + kk) * (D / 2),
+                                           c.scale[kind] + page * c.ss[kind][0] + u.h * c.ss[kind][1] + (long long)(slot + kk) * (D / 16), d);
+                    } else {
+                        const long long* st = kind == 0 ? p.ks : p.vs;
+                        return load4<C>(static_cast<const C*>(kind == 0 ? p.k_cache : p.v_cache) + page * st[0] + u.h * st[1] +
+                                        (slot + kk) * st[2] + d);
+                    }
+                };
                 float kscale = p.scale_log2e, vs_inv = 1.f, vs_log2 = 0.f;
-                if constexpr (sizeof(C) == 1) {
+                if constexpr (kFour) {
+                    if (p.c4.factor[0]) kscale *= p.c4.factor[0][u.h];
+                }
+                if constexpr (kCodes) {
                     kscale *= p.k_scale[page * p.Hk + u.h];
                     const float v = p.v_scale[page * p.Hk + u.h];
                     if (!v_scale_ok(v)) {
@@ -110,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         const int d = (c * 32 + lane) * 4;
-                        kv[c] = on[kk] && d < D ? load4<C>(kp + kk * p.ks[2] + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        kv[c] = on[kk] && d < D ? row(0, kk, d) : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
 #pragma unroll
                     for (int r = 0; r < kRows; ++r) {
@@ -166,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         const int d = (c * 32 + lane) * 4;
-                        vv[c] = d < D ? load4<C>(vp + kk * p.vs[2] + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        vv[c] = d < D ? row(1, kk, d) : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
 #pragma unroll
                     for (int r = 0; r < kRows; ++r) {
@@ -198,6 +223,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
         __syncthreads();
         const bool whole = u.starts && u.ends;
         const int slot = u.starts ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
+        const float v_factor = kFour && p.c4.factor[1] ? p.c4.factor[1][u.h] : 1.f;
         for (int e = threadIdx.x; e < u.rows * D; e += kThreads) {
             const int r = e / D, d = e - r * D;
             float M = -INFINITY, L = 0.f, o = 0.f;
@@ -211,6 +237,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
                 L = fmaf(ml.y, f, L);
                 o = fmaf(so[(i * kRows + r) * D + d], f, o);
             }
+            if constexpr (kFour) o *= v_factor;
             if (whole) {
                 const int row = u.rt * kRows + r;
                 const long long tok = u.q.row0 + row / p.G, head = head0 + row % p.G;
@@ -311,6 +338,7 @@ cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_simt(const PagedParams& p, cudaStream_t stream) {
+    if (p.cache_dtype == TA_INT4) return launch<cache4::Code>(p, stream);
     return p.cache_dtype == TA_E4M3 ? launch<uint8_t>(p, stream) : launch<float>(p, stream);
 }
 
@@ -342,6 +370,7 @@ int paged_rows(int dtype, int max_q, int G, int D) {
 // Slots of a tile: on tensor cores 32 KB of K and V with columns padded to whole 128 bytes.
 int paged_tile(int dtype, int cache_dtype, int D) {
     if (dtype == TA_F32) return 64;
+    if (cache_dtype == TA_INT4) return D <= 64 ? 256 : 128;  // (16 KB with up to 128 columns, 32 KB above)
     if (cache_dtype == TA_E4M3) return D <= 128 ? 128 : 64;
     return D <= 64 ? 128 : (D <= 128 ? 64 : 32);
 }

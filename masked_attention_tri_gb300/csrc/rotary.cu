@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
     const int np = p.dim / 2, nr = np / V, H = p.Hq + p.Hk;
     for (int e = threadIdx.x; e < nt * np; e += kThreads) {
         const int t = e / np, i = e - t * np;
-        const float2 cs = rotary_cos_sin(p.positions[tok0 + t], p.turns[i]);
+        const float2 cs = rotary_cos_sin(rotary_position(p.positions, p.axes, p.num_axes, i, p.total, tok0 + t), p.turns[i]);
         rot_table_put<V>(table, t, i, nr, cs.x * p.mscale, (p.inverse ? -cs.y : cs.y) * p.mscale);
     }
     __syncthreads();

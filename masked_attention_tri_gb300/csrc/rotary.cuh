@@ -8,7 +8,8 @@
 // opposite angle.  Only the angle's part of a whole turn matters, so f_i is held
 // as a 64-bit fixed-point fraction of a turn and the product p * f_i wraps to it
 // exactly (two's complement: negative positions too).  A position of 2^31 is thus
-// as exact as position 1, where p * theta_i in fp32 is off by a radian at p = 2^24.
+// as exact as position 1, where p * theta_i in fp32 is off by a radian at p = 2^24.  Several axes change only which
+// position a pair is multiplied with.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -29,6 +30,15 @@ __device__ __forceinline__ float2 rotary_cos_sin(int pos, unsigned long long tur
     sincospif((float)r * 4.656612873077393e-10f /* 2^-31: half-turns */, &s, &c);
     const float cq = (quad & 1u) ? s : c, sq = (quad & 1u) ? c : s;
     return make_float2((quad + 1u) & 2u ? -cq : cq, quad & 2u ? -sq : sq);
+}
+
+// The position by which pair i of row `row` turns: with several axes (time, height, width: positions (num_axes, total))
+// each pair has an axis of its own.  (A number that names no axis is read as axis 0.)
+__device__ __forceinline__ int rotary_position(const int32_t* positions, const int32_t* axes, int num_axes, int i,
+                                               int total, long long row) {
+    if (!axes) return positions[row];
+    const uint32_t a = (uint32_t)axes[i];
+    return positions[(a < (uint32_t)num_axes ? (long long)a * total : 0LL) + row];
 }
 
 // One value of T to and from fp32.

@@ -16,6 +16,24 @@ from .api import _DT, _need, _on, _ptr, _row_stride, _stream
 _SCALINGS = (None, "linear", "ntk", "yarn")
 
 
+def _pair_axes(sections, pairs, layout):
+    """The axis of each pair."""
+    want = [int(n) for n in sections]
+    if not want or min(want) < 1 or sum(want) != pairs:
+        raise ValueError(f"sections must be positive and add up to dim / 2 = {pairs}")
+    if layout == "blocks":
+        return [a for a, n in enumerate(want) for _ in range(n)]
+    if layout != "interleaved":
+        raise ValueError("section_layout must be 'blocks' or 'interleaved'")
+    axes = []
+    while len(axes) < pairs:
+        for a in range(len(want)):
+            if want[a]:
+                want[a] -= 1
+                axes.append(a)
+    return axes
+
+
 class Rotary:
     """The frequencies of rotary positions, kept on one device for any number of calls.
 
@@ -33,10 +51,18 @@ class Rotary:
       r_i between; cos and sin are multiplied by 0.1 ln(factor) + 1.
 
     attention_factor replaces that multiplier (1 without "yarn").
+
+    sections: pairs of each axis where a token has a position on several (time, height, width;
+    their sum is dim / 2).  Calls then take positions (axes, total), and pair i turns by
+    its axis' position.  section_layout "blocks": the first sections[0] pairs are axis 0's, the
+    next axis 1's, and so on; "interleaved": the pairs go round the axes that still want
+    some (0, 1, 2, 0, 1, 2, ...).  section_frequencies "shared": theta_i as above, over all pairs;
+    "own": over the axis' own pairs (theta = base^(-j / sections[a]) for its j-th; without scaling).
     """
 
     def __init__(self, dim, base=10000.0, *, interleaved=False, scaling=None, factor=1.0, original_length=0,
-                 beta_fast=32.0, beta_slow=1.0, attention_factor=None, device=None):
+                 beta_fast=32.0, beta_slow=1.0, attention_factor=None, sections=None, section_layout="blocks",
+                 section_frequencies="shared", device=None):
         dim, factor = int(dim), float(factor)
         if dim < 2 or dim % 2:
             raise ValueError("dim must be even and at least 2")
@@ -50,7 +76,15 @@ class Rotary:
             if dim < 4:
                 raise ValueError("ntk scaling needs dim >= 4")
             base = base * factor ** (dim / (dim - 2))
+        axes = None if sections is None else _pair_axes(sections, dim // 2, section_layout)
+        if section_frequencies not in ("shared", "own"):
+            raise ValueError("section_frequencies must be 'shared' or 'own'")
         theta = [base ** (-2.0 * i / dim) for i in range(dim // 2)]
+        if section_frequencies == "own":
+            if sections is None or scaling is not None:
+                raise ValueError("frequencies of each section's own need sections and no scaling")
+            place = [axes[:i].count(a) for i, a in enumerate(axes)]
+            theta = [base ** (-float(j) / int(sections[a])) for a, j in zip(axes, place)]
         if scaling == "linear":
             theta = [t / factor for t in theta]
         if scaling == "yarn":
@@ -72,6 +106,12 @@ class Rotary:
         turns = [int(round(t / (2 * math.pi) * 2.0 ** 64)) & (2 ** 64 - 1) for t in theta]
         turns = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
         self.turns = torch.tensor(turns, dtype=torch.int64, device=device)
+        self.num_axes = 1 if axes is None else len(sections)
+        self.pair_axes = None if axes is None else torch.tensor(axes, dtype=torch.int32, device=self.turns.device)
+
+    def positions_shape(self, total):
+        """The shape of a call's positions."""
+        return (total,) if self.pair_axes is None else (self.num_axes, total)
 
     @property
     def device(self) -> torch.device:
@@ -95,6 +135,15 @@ def _check_rotary(rotary, dev):
         raise ValueError(f"rotary is on {rotary.turns.device}, expected {dev}")
 
 
+def _check_positions(positions, rotary, dev, total):
+    _need(positions, "positions", dev)
+    if rotary.pair_axes is None:
+        if positions.dtype != torch.int32 or positions.numel() != total:
+            raise ValueError("positions must be int32 with one entry per row")
+    elif positions.dtype != torch.int32 or tuple(positions.shape) != (rotary.num_axes, total):
+        raise ValueError(f"positions must be int32 (axes, rows) = {(rotary.num_axes, total)}")
+
+
 def _rotary_call(q, k, positions, rotary, inverse, out_q, out_k):
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
@@ -108,9 +157,7 @@ def _rotary_call(q, k, positions, rotary, inverse, out_q, out_k):
     total, Hq, D = q.shape
     q_rs = _rotary_rows(q, "q", dev, q.dtype, total)
     _check_rotary(rotary, dev)
-    _need(positions, "positions", dev)
-    if positions.dtype != torch.int32 or positions.numel() != total:
-        raise ValueError("positions must be int32 with one entry per row")
+    _check_positions(positions, rotary, dev, total)
     Hk, k_rs, ko_rs = 0, 0, 0
     if k is None and out_k is not None:
         raise ValueError("out_k needs k")
@@ -132,17 +179,21 @@ def _rotary_call(q, k, positions, rotary, inverse, out_q, out_k):
         if out_q.shape != q.shape:
             raise ValueError("out_q must have q's shape")
     if total:
+        args = (_ptr(rotary.turns), rotary.dim, rotary.interleaved, rotary.attention_factor, inverse, total, Hq, Hk, D,
+                q_rs, k_rs, qo_rs, ko_rs, _ptr(out_q), _ptr(out_k), _stream(dev))
         with _on(dev):
-            abi.tri_attn_rotary(_ptr(q), _ptr(k), _DT[q.dtype], _ptr(positions), _ptr(rotary.turns), rotary.dim,
-                                rotary.interleaved, rotary.attention_factor, inverse, total, Hq, Hk, D, q_rs, k_rs,
-                                qo_rs, ko_rs, _ptr(out_q), _ptr(out_k), _stream(dev))
+            if rotary.pair_axes is None:
+                abi.tri_attn_rotary(_ptr(q), _ptr(k), _DT[q.dtype], _ptr(positions), *args)
+            else:
+                abi.tri_attn_rotary_axes(_ptr(q), _ptr(k), _DT[q.dtype], _ptr(positions), rotary.num_axes,
+                                         _ptr(rotary.pair_axes), *args)
     return out_q if k is None else (out_q, out_k)
 
 
 def rotary_embedding(q, k, positions, rotary: Rotary, *, out_q=None, out_k=None):
     """q (total, Hq, D) and k (total, Hk, D) turned by their rows' positions.
 
-    positions: int32 (total,), any values.  k may be None (then q alone is
+    positions: int32 (total,), any values; (axes, total) where rotary has sections.  k may be None (then q alone is
     returned, else (q, k)).  q, k and the outputs may be row-strided views (heads
     and elements contiguous), such as the slices of an interleaved QKV buffer;
     out_q=q / out_k=k turn in place.  fp32 arithmetic, one rounding.
