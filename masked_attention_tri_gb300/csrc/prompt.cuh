@@ -38,7 +38,7 @@ __device__ __forceinline__ Seq load_seq(const PromptParams& p, int s, bool tell)
     return q;
 }
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kToLog2 = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // delta[h, t] = dO[t, h] . O[t, h], which is sum_k P dP (prompt_simt.cu).
 cudaError_t launch_delta(const PromptParams& p, cudaStream_t stream);

@@ -1,0 +1,730 @@
+// prompt_fwd.cu -- causal attention of packed prompts with grouped heads on tcgen05 tensor cores: 16-bit inputs, D <= 128.
+//
+// The mathematics is prompt.cuh's: the heads of a group are rows.  A tile is up to 128 rows, tq tokens x hp heads of a group
+// (hp a divisor of the group, the whole group where it fits), loaded by one TMA box of a (D, head, token) map, so that
+// short sequences fill tiles by their heads and the keys past the causal border are few.  A work item is two neighbouring
+// tiles of one (sequence, key head), which share every K and V tile (128 keys) that is loaded.
+//
+// One CTA a SM, 16 warps:
+//   0-3, 4-7   softmax of tile 0 / 1: thread = row = tensor-memory lane, the row's 128 logits in registers
+//   8-11       epilogue: O / l to memory while the next item has begun
+//   12         tcgen05.mma: S_i = Q_i K^T (shared x shared), O_i += P_i V (P from tensor memory, over S_i)
+//   13         TMA of Q_0, Q_1 and the ring of K and V tiles
+//   14         the items, handed to the others through a ring
+// Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (64 or 128 each): all 512 columns at D = 128.  The tensor core works on
+// one tile while the other's softmax runs.
+//
+// Softmax: one pass with a reference maximum that is raised only when a row's maximum passes it by 2^8 (fp16's range allows
+// that), which scales O by its own threads and is rare; sums, maxima, O in fp32, P rounded to the inputs' type.  P is handed
+// over in two halves.  V's rows past the sequence's end are other sequences' (or NaN that nobody wrote): their weights are 0,
+// and the products stop at the sixteen keys that hold the last one, the rest of which is zeroed in shared memory.
+//
+// Items go by falling cost (the number of key tiles), one at a time to the CTA that has finished its own: the grid has a
+// block for every item, and a running CTA takes the next block's place by clusterlaunchcontrol.try_cancel, so no
+// counter in memory has to be zeroed and the tail is as short as one item.
+#include "prompt.cuh"
+#include "tc_kernel.cuh"
+
+namespace triattn {
+namespace prompt {
+namespace {
+
+using namespace tc;
+
+struct FwdParams {
+    CUtensorMap tm_q, tm_k, tm_v;
+    PromptParams p;
+    int hp, tq, ng;            // heads and tokens of a tile; tiles of the same tokens (G / hp)
+    FastDiv fd_hp, fd_hk;
+    uint32_t idesc_qk, idesc_pv;
+    int ksteps;                // D / 16, rounded up
+    float scale_log2e;         // |scale| log2 e
+    int negative;              // scale < 0: the logits change their sign
+};
+
+// wait_bar inline: a call keeps the compiler from giving the softmax warps the registers that setmaxnreg gives them.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    if (mbar_test(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63) == 0) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > kTimeoutCycles) {
+                *abort_flag = 1;
+                atomicCAS(status, 0, kStatusTimeout);
+                return false;
+            }
+        }
+    }
+}
+
+constexpr int kRing = 2;       // items known ahead
+constexpr int kWarps = 16;
+constexpr int kConsumers = 14; // warps that read an item: 8 softmax, 4 epilogue, MMA, TMA
+
+struct alignas(16) Item {
+    int on;                    // 0: the end
+    int q0, k0, lq, shift;     // the sequence: first packed rows, queries, and how many more keys than queries it has
+    int h;                     // key head
+    int tok[2], head[2];       // of each tile: first token (of the sequence), first query head
+    int keys[2];               // keys that some row of the tile sees
+    int rows[2];               // rows that exist (0: no tile)
+};
+
+template <int NB>
+struct Smem {
+    static constexpr uint32_t kTile = NB * kBox;                       // 128 rows
+    static constexpr int kStages = NB == 1 ? 8 : 4;
+    static constexpr uint32_t kQ = 0, kKV = 2 * kTile, kMl = kKV + kStages * kTile;  // (m, l) of the rows
+    static constexpr uint32_t kItems = kMl + 2 * 128 * 8, kClc = kItems + kRing * sizeof(Item);
+    static constexpr uint32_t kBars = kClc + 16;
+    static constexpr int kNumBars = 2 * 2 + 2 * kStages + 5 * 2 + 2 * 2 + 2 * kRing + 2;
+    static constexpr uint32_t kSlot = kBars + 8 * kNumBars, kAbort = kSlot + 4, kTotal = kAbort + 4 + 1024;
+};
+
+// 128 columns by two loads and one wait.
+__device__ __forceinline__ void tmem_ld_2x64(uint32_t ta, uint32_t (&r)[128]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%128];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%129];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
+          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
+          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
+          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
+          "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
+          "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+          "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+        : "r"(ta), "r"(ta + 64u));
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// The next block's place in the grid, or -1 (none is left): asks (one thread), and reads the answer.
+__device__ __forceinline__ void clc_ask(uint32_t to, uint32_t bar) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    mbar_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to),
+                 "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ int clc_answer(uint32_t at) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 r, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "mov.b32 %0, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, r;\n\t}"
+        : "=r"(x)
+        : "r"(at)
+        : "memory");
+    return x;
+}
+
+// The order of the items (one warp): by the key tiles of their second tile, most first; of those with as many by
+// sequence, then tile pair, then head.
+struct Order {
+    int level;                 // key tiles
+    long long base;            // items of the levels before
+    long long here;            // items of this level
+};
+// Pairs of a sequence that end within n key tiles.
+__device__ __forceinline__ int pairs_upto(const FwdParams& P, const Seq& q, int n) {
+    const int tiles = (q.lq + P.tq - 1) / P.tq * P.ng, pairs = (tiles + 1) / 2;
+    if (n < 0) return 0;
+    if (q.lk <= 128LL * n) return pairs;
+    const int x = 128 * n - q.shift;                   // tokens (of the sequence) whose last key lies there
+    return x <= 0 ? 0 : (int)((long long)(x / P.tq) * P.ng / 2);
+}
+__device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
+__device__ __forceinline__ long long level_items(const FwdParams& P, int n) {
+    const int lane = threadIdx.x % 32;
+    long long sum = 0;
+    for (int s0 = 0; s0 < P.p.num_seqs; s0 += 32) {
+        int c = 0;
+        if (s0 + lane < P.p.num_seqs) {
+            const Seq q = load_seq(P.p, s0 + lane, false);
+            c = pairs_upto(P, q, n) - pairs_upto(P, q, n - 1);
+        }
+        sum += warp_sum(c);
+    }
+    return sum * P.p.Hk;
+}
+__device__ __forceinline__ Order order_begin(const FwdParams& P) {
+    int most = 0;
+    for (int s = threadIdx.x % 32; s < P.p.num_seqs; s += 32) {
+        const Seq q = load_seq(P.p, s, blockIdx.x == 0);
+        if (q.lq > 0) most = max(most, (q.lk + 127) / 128);
+    }
+    Order o;
+    o.level = __reduce_max_sync(0xffffffffu, most);
+    o.base = 0;
+    o.here = level_items(P, o.level);
+    return o;
+}
+// Item `at` (never an earlier one than before): false past the last.
+__device__ __forceinline__ bool order_item(const FwdParams& P, Order& o, long long at, Item& it) {
+    while (at >= o.base + o.here) {
+        o.base += o.here;
+        if (--o.level < 0) return false;
+        o.here = level_items(P, o.level);
+    }
+    const int lane = threadIdx.x % 32;
+    const int rank = (int)(at - o.base);
+    int pair = (int)P.fd_hk.div((uint32_t)rank);
+    it.h = rank - pair * P.p.Hk;
+    for (int s0 = 0; s0 < P.p.num_seqs; s0 += 32) {
+        Seq q{};
+        int c = 0, first = 0;
+        if (s0 + lane < P.p.num_seqs) {
+            q = load_seq(P.p, s0 + lane, false);
+            first = pairs_upto(P, q, o.level - 1);
+            c = pairs_upto(P, q, o.level) - first;
+        }
+        int upto = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += x;
+        }
+        const uint32_t has = __ballot_sync(0xffffffffu, pair < upto);
+        if (!has) {
+            pair -= __shfl_sync(0xffffffffu, upto, 31);
+            continue;
+        }
+        const int l = __ffs((int)has) - 1;
+        auto get = [&](int x) { return __shfl_sync(0xffffffffu, x, l); };
+        const int t0 = 2 * get(first + pair - (upto - c));
+        it.on = 1;
+        it.q0 = get(q.q0);
+        it.k0 = get(q.k0);
+        it.lq = get(q.lq);
+        it.shift = get(q.shift);
+        const int blocks = (it.lq + P.tq - 1) / P.tq;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + i, b = t / P.ng;
+            const bool there = b < blocks;
+            it.tok[i] = b * P.tq;
+            it.head[i] = it.h * P.p.G + (t - b * P.ng) * P.hp;
+            const int tokens = there ? min(P.tq, it.lq - it.tok[i]) : 0;
+            it.rows[i] = tokens * P.hp;
+            it.keys[i] = there ? max(0, it.tok[i] + tokens + it.shift) : 0;
+        }
+        return true;
+    }
+    return false;
+}
+
+template <bool BF16, int NB>
+__global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid_constant__ FwdParams P) {
+    using M = Smem<NB>;
+    constexpr int S = M::kStages;
+    constexpr uint32_t kTile = M::kTile, kOCols = NB * 64;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t* g0 = smem_raw + (base - raw);
+    const PromptParams& p = P.p;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(g0 + M::kAbort);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(g0 + M::kSlot);
+    Item* items = reinterpret_cast<Item*>(g0 + M::kItems);
+    float2* ml = reinterpret_cast<float2*>(g0 + M::kMl);
+    auto bar = [&](int i) { return base + M::kBars + 8u * (uint32_t)i; };
+    auto q_full = [&](int i) { return bar(i); };
+    auto q_empty = [&](int i) { return bar(2 + i); };
+    auto kv_full = [&](int s) { return bar(4 + s); };
+    auto kv_empty = [&](int s) { return bar(4 + S + s); };
+    constexpr int b0 = 4 + 2 * S;
+    auto s_full = [&](int i) { return bar(b0 + i); };
+    auto p_half = [&](int i, int h) { return bar(b0 + 2 + 2 * i + h); };
+    auto o_full = [&](int i) { return bar(b0 + 6 + i); };
+    auto o_empty = [&](int i) { return bar(b0 + 8 + i); };
+    auto ml_full = [&](int i) { return bar(b0 + 10 + i); };
+    auto ml_empty = [&](int i) { return bar(b0 + 12 + i); };
+    auto it_full = [&](int r) { return bar(b0 + 14 + r); };
+    auto it_empty = [&](int r) { return bar(b0 + 14 + kRing + r); };
+    const uint32_t clc = bar(b0 + 14 + 2 * kRing), drain = bar(b0 + 15 + 2 * kRing);
+    static_assert(4 + 2 * S + 16 + 2 * kRing <= M::kNumBars + 0, "barriers");
+    auto q_smem = [&](int i) { return base + M::kQ + (uint32_t)i * kTile; };
+    auto kv_smem = [&](int s) { return base + M::kKV + (uint32_t)s * kTile; };
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full(i), 1);
+            mbar_init(q_empty(i), 1);
+            mbar_init(s_full(i), 1);
+            mbar_init(p_half(i, 0), 4);
+            mbar_init(p_half(i, 1), 4);
+            mbar_init(o_full(i), 1);
+            mbar_init(o_empty(i), 4);
+            mbar_init(ml_full(i), 4);
+            mbar_init(ml_empty(i), 4);
+        }
+#pragma unroll 1
+        for (int s = 0; s < S; ++s) {
+            mbar_init(kv_full(s), 1);
+            mbar_init(kv_empty(s), 1);
+        }
+        for (int r = 0; r < kRing; ++r) {
+            mbar_init(it_full(r), 1);
+            mbar_init(it_empty(r), kConsumers);
+        }
+        mbar_init(clc, 1);
+        mbar_init(drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // Rows of Q that no box fills (tq hp < 128) stay zeros.
+    for (int e = threadIdx.x; e < 2 * NB * (128 - P.tq * P.hp) * 8; e += kWarps * 32) {
+        const int c = e % 8, r = e / 8 % (128 - P.tq * P.hp) + P.tq * P.hp, b = e / 8 / (128 - P.tq * P.hp);
+        st_shared_v4(base + M::kQ + (uint32_t)b * kBox + (uint32_t)r * 128u + c * 16u, 0u, 0u, 0u, 0u);
+    }
+    fence_async_shared();
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+    int item_n = 0;            // items so far
+    // The next item, for the warps that consume them: false at the end.
+    auto next_item = [&](Item& it) -> bool {
+        const int r = item_n % kRing;
+        ok = __all_sync(0xffffffffu, wait(it_full(r), (uint32_t)(item_n / kRing) & 1u, abort_flag, p.status));
+        if (!ok) return false;
+        it = items[r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(it_empty(r));
+        ++item_n;
+        return it.on != 0;
+    };
+
+    // (the block has 128 registers a thread: 2 x 192 + 72 + 56 = 4 x 128)
+    if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 14) {
+            // ------------------------------------------------------------ the items
+            Order o = order_begin(P);
+            int at = (int)blockIdx.x;
+            uint32_t asked = 0;
+            for (;;) {
+                Item it{};
+                if (at < 0 || !order_item(P, o, at, it)) it.on = 0;
+                const int r = item_n % kRing;
+                if (item_n >= kRing)
+                    ok = __all_sync(0xffffffffu, wait(it_empty(r), (uint32_t)(item_n / kRing - 1) & 1u, abort_flag, p.status));
+                if (!ok) break;
+                if (lane == 0) {
+                    items[r] = it;
+                    mbar_arrive(it_full(r));
+                }
+                ++item_n;
+                if (!it.on) break;
+                if (lane == 0) clc_ask(base + M::kClc, clc);
+                // (awaited whatever happens: the answer is written into this block's memory)
+                ok = __all_sync(0xffffffffu, wait_bar_drain(clc, asked & 1u));
+                if (!ok) break;
+                ++asked;
+                at = clc_answer(base + M::kClc);
+                __syncwarp();
+            }
+            if (!ok) *abort_flag = 1;
+        } else if (warp == 13) {
+            // ------------------------------------------------------------ TMA
+            StageRing kr = {0, 0u, false};
+            Item it;
+            uint32_t q_use[2] = {0u, 0u};
+            const uint32_t q_bytes = (uint32_t)(P.tq * P.hp) * 128u * NB;
+            while (ok && next_item(it)) {
+                const int n = (max(it.keys[0], it.keys[1]) + 127) / 128;
+                auto load_q = [&](int i) {
+                    if (it.keys[i] <= 0 || !ok) return;
+                    if (q_use[i] > 0) ok = __all_sync(0xffffffffu, wait(q_empty(i), (q_use[i] - 1u) & 1u, abort_flag, p.status));
+                    ++q_use[i];
+                    if (ok && lane == 0) {
+                        mbar_expect_tx(q_full(i), q_bytes);
+                        for (int b = 0; b < NB; ++b)
+                            tma_load_3d(q_smem(i) + b * kBox, &P.tm_q, 64 * b, it.head[i], it.q0 + it.tok[i], q_full(i));
+                    }
+                };
+                auto load_kv = [&](const CUtensorMap* tm, int j) {
+                    if (!ok) return;
+                    if (kr.wrapped) ok = __all_sync(0xffffffffu, wait(kv_empty(kr.idx), kr.ph ^ 1u, abort_flag, p.status));
+                    if (ok && lane == 0) {
+                        mbar_expect_tx(kv_full(kr.idx), kTile);
+                        for (int b = 0; b < NB; ++b)
+                            tma_load_3d(kv_smem(kr.idx) + b * kBox, tm, 64 * b, it.h, it.k0 + 128 * j, kv_full(kr.idx));
+                    }
+                    kr.next(S);
+                };
+                if (n > 0) load_kv(&P.tm_k, 0);
+                load_q(0);
+                load_q(1);
+                for (int j = 0; j < n && ok; ++j) {
+                    load_kv(&P.tm_v, j);
+                    if (j + 1 < n) load_kv(&P.tm_k, j + 1);
+                }
+            }
+            if (!ok) *abort_flag = 1;
+        } else if (warp == 12) {
+            // ------------------------------------------------------------ MMA
+            const bool leader = elect_one();
+            StageRing kr = {0, 0u, false};
+            Item it;
+            uint32_t q_use[2] = {0u, 0u}, p_use[2] = {0u, 0u}, o_use[2] = {0u, 0u};
+            while (ok && next_item(it)) {
+                const int n0 = (it.keys[0] + 127) / 128, n1 = (it.keys[1] + 127) / 128, n = max(n0, n1);
+                const int lk = it.lq + it.shift;
+                auto wait_kv = [&](const StageRing& r) {
+                    if (ok) ok = __all_sync(0xffffffffu, wait(kv_full(r.idx), r.ph, abort_flag, p.status));
+                    tc_fence_after();
+                };
+                // S_i of key tile j, K in stage st
+                auto qk = [&](int i, int j, int st) {
+                    const int cols = min(128, (it.keys[i] - 128 * j + 15) & ~15);
+                    const uint32_t idesc = P.idesc_qk | ((uint32_t)(cols >> 3) << 17);
+                    const uint64_t a = sw128_desc(q_smem(i), 16, 1024), b = sw128_desc(kv_smem(st), 16, 1024);
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < 4 * NB; ++kk) {
+                            const uint64_t s = (uint64_t)(((kk >> 2) * kBox + (kk & 3) * 32) >> 4);
+                            if (kk < P.ksteps) mma_ss(tmem + i * 128, a + s, b + s, idesc, kk > 0 ? 1u : 0u);
+                        }
+                        mma_commit(s_full(i));
+                    }
+                };
+                // O_i += P_i V of key tile j, V in stage st
+                auto pv = [&](int i, int j, int st) {
+                    if (j == 0) {  // the epilogue has read the last item's O
+                        if (o_use[i] > 0)
+                            ok = ok && __all_sync(0xffffffffu, wait(o_empty(i), (o_use[i] - 1u) & 1u, abort_flag, p.status));
+                        ++o_use[i];
+                    }
+                    const int steps = min(8, (it.keys[i] - 128 * j + 15) / 16);
+                    const uint64_t b = sw128_desc(kv_smem(st), kBox, 1024);
+                    const uint32_t d = tmem + 256u + (uint32_t)i * kOCols, a = tmem + i * 128;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (ok) ok = __all_sync(0xffffffffu, wait(p_half(i, h), p_use[i] & 1u, abort_flag, p.status));
+                        if (!ok) return;
+                        tc_fence_after();
+                        if (leader) {
+#pragma unroll
+                            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                                if (kk < steps) mma_ts(d, a + kk * 8, b + (uint64_t)kk * 128, P.idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+                        }
+                    }
+                    ++p_use[i];
+                };
+                for (int i = 0; i < 2; ++i) {
+                    if (it.keys[i] <= 0) continue;
+                    if (ok) ok = __all_sync(0xffffffffu, wait(q_full(i), q_use[i] & 1u, abort_flag, p.status));
+                    ++q_use[i];
+                }
+                StageRing kst = kr, vst = kr;
+                if (n > 0) {
+                    wait_kv(kst);
+                    if (!ok) break;
+                    if (n0 > 0) qk(0, 0, kst.idx);
+                    if (n1 > 0) qk(1, 0, kst.idx);
+                    if (leader) {
+                        mma_commit(kv_empty(kst.idx));
+                        if (n0 == 1) mma_commit(q_empty(0));
+                        if (n1 == 1) mma_commit(q_empty(1));
+                    }
+                    kr.next(S);
+                }
+                // step j: PV of key tile j - 1 and QK of key tile j, tile 0 then tile 1
+                for (int j = 1; j <= n && ok; ++j) {
+                    vst = kr;
+                    kr.next(S);
+                    const bool more = j < n;
+                    if (more) {
+                        kst = kr;
+                        kr.next(S);
+                    }
+                    wait_kv(vst);
+                    if (!ok) break;
+                    const int valid = lk - 128 * (j - 1);  // rows of V that are the sequence's
+                    if (valid < 128 && (valid & 15)) {
+                        const int zeros = 16 - (valid & 15);
+                        for (int e = lane; e < zeros * 8 * NB; e += 32)
+                            st_shared_v4(kv_smem(vst.idx) + (uint32_t)(e / 8 / zeros) * kBox +
+                                             (uint32_t)(valid + e / 8 % zeros) * 128u + (e % 8) * 16u, 0u, 0u, 0u, 0u);
+                        fence_async_shared();
+                        __syncwarp();
+                    }
+                    bool k_here = false;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int ni = i == 0 ? n0 : n1;
+                        if (j - 1 < ni) pv(i, j - 1, vst.idx);
+                        if (!ok) break;
+                        if (leader && j == ni) mma_commit(o_full(i));
+                        if (i == 1 && leader) mma_commit(kv_empty(vst.idx));
+                        if (j < ni) {
+                            if (!k_here) wait_kv(kst);
+                            k_here = true;
+                            if (!ok) break;
+                            qk(i, j, kst.idx);
+                            if (leader && j == ni - 1) mma_commit(q_empty(i));
+                        }
+                    }
+                    if (more && ok && leader) mma_commit(kv_empty(kst.idx));
+                }
+            }
+            if (!ok && leader) *abort_flag = 1;
+            if (leader) mma_commit(drain);
+            wait_bar_drain(drain, 0);
+            __syncwarp();
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        const int i = warp / 4, r = warp % 4 * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(warp % 4 * 32) << 16;
+        const uint32_t st = tmem + lane_off + i * 128, ot = tmem + lane_off + 256u + (uint32_t)i * kOCols;
+        const int tok_r = (int)P.fd_hp.div((uint32_t)r);
+        const float f = P.scale_log2e, step = kRescaleLog2 / f;
+        Item it;
+        uint32_t s_use = 0, ml_use = 0;
+        while (ok && next_item(it)) {
+            const int keys = i == 0 ? it.keys[0] : it.keys[1], tok = (i == 0 ? it.tok[0] : it.tok[1]) + tok_r;
+            const int n = (keys + 127) / 128;
+            const int limit = tok + it.shift;                            // the last key that this row sees
+            const int first = (i == 0 ? it.tok[0] : it.tok[1]) + it.shift;  // ... and the tile's first row
+            float m = -INFINITY, l = 0.f;                                // the reference maximum (of S), the sum
+            for (int j = 0; j < n && ok; ++j) {
+                ok = __all_sync(0xffffffffu, wait(s_full(i), s_use & 1u, abort_flag, p.status));
+                if (!ok) break;
+                ++s_use;
+                tc_fence_after();
+                uint32_t sr[128];
+                tmem_ld_2x64(st, sr);
+                float x[128];
+#pragma unroll
+                for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(sr[c]);
+                if (P.negative) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) x[c] = -x[c];
+                }
+                if (128 * j + 127 > first) {  // some row does not see every key
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const uint32_t vm = low_bits(limit - 128 * j - 32 * h + 1);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) x[32 * h + c] = (vm >> c) & 1u ? x[32 * h + c] : -INFINITY;
+                    }
+                }
+                float a0 = x[0], a1 = x[1], a2 = x[2], a3 = x[3];
+#pragma unroll
+                for (int c = 4; c < 124; c += 8) {
+                    a0 = max3(a0, x[c], x[c + 1]);
+                    a1 = max3(a1, x[c + 2], x[c + 3]);
+                    a2 = max3(a2, x[c + 4], x[c + 5]);
+                    a3 = max3(a3, x[c + 6], x[c + 7]);
+                }
+                a0 = max3(a0, x[124], x[125]);
+                a1 = max3(a1, x[126], x[127]);
+                const float tm = fmaxf(max3(a0, a1, a2), a3);
+                // (from -inf: inf, a new reference)
+                if (__any_sync(0xffffffffu, tm - m > step)) {
+                    const float mn = fmaxf(m, tm);
+                    const float alpha = mn == -INFINITY ? 1.f : ex2((m - mn) * f);
+                    m = mn;
+                    l *= alpha;
+                    if (j > 0) {  // (PV of the last key tile is done: S was asked for behind it)
+#pragma unroll 1
+                        for (uint32_t c = 0; c < kOCols; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld_x16(ot + c, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st_x16(ot + c, o);
+                        }
+                    }
+                }
+                const float nb = m == -INFINITY ? 0.f : -m * f;
+                const float2 f2 = make_float2(f, f), nb2 = make_float2(nb, nb);
+                float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float2 y = __ffma2_rn(make_float2(x[32 * h + 2 * c], x[32 * h + 2 * c + 1]), f2, nb2);
+                        const float2 w = make_float2(ex2(y.x), ex2(y.y));
+                        if (c & 1) s1 = __fadd2_rn(s1, w);
+                        else s0 = __fadd2_rn(s0, w);
+                        pk[c] = pack2<BF16>(w.x, w.y);
+                    }
+                    tmem_st_x16(st + 16 * h, pk);
+                    if (h & 1) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_half(i, h / 2));
+                    }
+                }
+                l += (s0.x + s0.y) + (s1.x + s1.y);
+            }
+            if (!ok) break;
+            if (ml_use > 0) ok = __all_sync(0xffffffffu, wait(ml_empty(i), (ml_use - 1u) & 1u, abort_flag, p.status));
+            if (!ok) break;
+            ++ml_use;
+            ml[i * 128 + r] = make_float2(m, l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ml_full(i));
+        }
+        if (!ok) *abort_flag = 1;
+    } else {
+        // ------------------------------------------------------------ epilogue
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        const int wq = warp % 4, r = wq * 32 + lane;
+        const int tok_r = (int)P.fd_hp.div((uint32_t)r), head_r = r - tok_r * P.hp;
+        const bool wide = p.D % 16 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;  // rows in 32-byte pieces
+        Item it;
+        uint32_t ml_use = 0, o_use[2] = {0u, 0u};
+        while (ok && next_item(it)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                ok = ok && __all_sync(0xffffffffu, wait(ml_full(i), ml_use & 1u, abort_flag, p.status));
+                if (!ok) break;
+                const float2 x = ml[i * 128 + r];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ml_empty(i));
+                const bool none = x.x == -INFINITY && x.y == 0.f;
+                const float inv = none ? 0.f : __fdividef(1.f, x.y);
+                const bool row = r < it.rows[i];
+                const long long tok = it.q0 + it.tok[i] + tok_r, head = it.head[i] + head_r;
+                uint16_t* out = static_cast<uint16_t*>(p.out) + (tok * p.Hq + head) * p.D;
+                if (row && p.lse) p.lse[head * p.total_q + tok] = none ? -INFINITY : (x.x * P.scale_log2e + log2f(x.y)) * kLn2;
+                const bool any = it.keys[i] > 0;
+                if (any) {
+                    ok = __all_sync(0xffffffffu, wait(o_full(i), o_use[i] & 1u, abort_flag, p.status));
+                    if (!ok) break;
+                    ++o_use[i];
+                    tc_fence_after();
+                }
+                const uint32_t ot = tmem + ((uint32_t)(wq * 32) << 16) + 256u + (uint32_t)i * kOCols;
+#pragma unroll 1
+                for (int c = 0; c < (int)kOCols; c += 32) {
+                    uint32_t o[32];
+                    if (any) tmem_ld_x32(ot + c, o);
+                    if (any && c + 32 >= (int)kOCols) {  // the last columns are in registers
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(o_empty(i));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            // (a row that sees no key: its columns may hold anything)
+                            const float a = none ? 0.f : __uint_as_float(o[e + 2 * k]) * inv;
+                            const float b = none ? 0.f : __uint_as_float(o[e + 2 * k + 1]) * inv;
+                            w[k] = pack2<BF16>(a, b);
+                        }
+                        if (row && c + e + 16 <= p.D) {
+                            if (wide) {
+                                store32(out + c + e, w);
+                            } else {
+                                *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                                *reinterpret_cast<uint4*>(out + c + e + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                            }
+                        } else if (row && c + e + 8 <= p.D) {
+                            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+            }
+            ++ml_use;
+        }
+        if (!ok) *abort_flag = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
+}
+
+template <bool BF16, int NB>
+cudaError_t start(const FwdParams& P, unsigned grid, cudaStream_t stream) {
+    auto kern = prompt_fwd_kernel<BF16, NB>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<NB>::kTotal);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kWarps * 32, Smem<NB>::kTotal, stream>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Heads of a tile: the divisor of the group that fills most of 128 rows, the largest of those (fewer keys past the
+// causal border).
+void tile_shape(int G, int& hp, int& tq) {
+    hp = 1;
+    for (int d = 1; d <= G && d <= 128; ++d)
+        if (G % d == 0 && 128 / d * d >= 128 / hp * hp) hp = d;
+    tq = 128 / hp;
+}
+
+}  // namespace prompt
+
+cudaError_t launch_prompt_tc_fwd(const PromptParams& p, cudaStream_t stream) {
+    using namespace prompt;
+    FwdParams P;
+    P.p = p;
+    tile_shape(p.G, P.hp, P.tq);
+    P.ng = p.G / P.hp;
+    P.fd_hp = tc::make_fastdiv((uint32_t)P.hp);
+    P.fd_hk = tc::make_fastdiv((uint32_t)p.Hk);
+    const bool bf16 = p.dtype == TA_BF16;
+    const uint32_t ab = bf16 ? 1u : 0u, npv = (uint32_t)(p.D + 15) / 16 * 16;
+    P.idesc_qk = (1u << 4) | (ab << 7) | (ab << 10) | (8u << 24);  // (N is set for each product)
+    P.idesc_pv = (1u << 4) | (ab << 7) | (ab << 10) | (1u << 16) | ((npv >> 3) << 17) | (8u << 24);
+    P.ksteps = (p.D + 15) / 16;
+    // (a scale of 0 makes every logit 0: so does one far below the least that counts, and a hidden key's -inf stays)
+    P.scale_log2e = fmaxf(fabsf(p.scale) * kToLog2, 1e-30f);
+    P.negative = p.scale < 0.f;
+    const CUtensorMapDataType dt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const uint64_t D = (uint64_t)p.D;
+    if (!tc::encode_map_3d(&P.tm_q, dt, p.q, D, p.Hq, p.total_q, D * 2, p.q_rs * 2, 64, P.hp, P.tq, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !tc::encode_map_3d(&P.tm_k, dt, p.k, D, p.Hk, p.total_k, D * 2, p.k_rs * 2, 64, 1, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !tc::encode_map_3d(&P.tm_v, dt, p.v, D, p.Hk, p.total_k, D * 2, p.v_rs * 2, 64, 1, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    // A block for each item that there can be: a sequence has ceil(ceil(lq / tq) ng / 2) pairs of tiles, at most
+    // lq ng / (2 tq) + ng / 2 + 1, and no more than the longest has.
+    const long long longest = (((long long)p.max_q + P.tq - 1) / P.tq * P.ng + 1) / 2;
+    const long long sum = (long long)p.total_q * P.ng / (2 * P.tq) + (long long)p.num_seqs * (P.ng / 2 + 1) + 1;
+    const long long items = (longest * p.num_seqs < sum ? longest * p.num_seqs : sum) * p.Hk;
+    if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const unsigned grid = (unsigned)items;
+    if (p.D <= 64) return bf16 ? start<true, 1>(P, grid, stream) : start<false, 1>(P, grid, stream);
+    return bf16 ? start<true, 2>(P, grid, stream) : start<false, 2>(P, grid, stream);
+}
+
+}  // namespace triattn

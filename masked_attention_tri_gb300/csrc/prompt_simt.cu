@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) prompt_fwd_simt(const PromptParams p
         for (int c = 0; c < NC; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     const int last = min(r0 + BM, rows) - 1, keys = last / p.G + q.shift + 1;  // keys that some row sees
-    const float f = p.scale * kLog2e;
+    const float f = p.scale * kToLog2;
     for (int k0 = 0; k0 < keys; k0 += kKeys) {
         __syncthreads();
         load_tile<T, kKeys, LD>(sk, p.D, [&](int k) { return k0 + k < keys ? key_at<T>(p, q, x.h, k0 + k, p.k, p.k_rs) : nullptr; });
@@ -254,13 +254,13 @@ __device__ __forceinline__ void weights(const PromptParams& p, const Seq& q, int
     float s[RM][4], g[RM][4];
     products<RM, LD>(sq, sk, p.D, s);
     products<RM, LD>(sg, sv, p.D, g);
-    const float f = p.scale * kLog2e;
+    const float f = p.scale * kToLog2;
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
         const int r = r0 + ty * RM + i;
         const long long at = (long long)(h * p.G + r % p.G) * p.total_q + q.q0 + r / p.G;
         const int limit = r < rows ? r / p.G + q.shift : -1;
-        const float lse = r < rows ? p.lse[at] * kLog2e : 0.f, delta = r < rows ? p.delta[at] : 0.f;
+        const float lse = r < rows ? p.lse[at] * kToLog2 : 0.f, delta = r < rows ? p.delta[at] : 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const bool sees = k0 + tx + 16 * j <= limit;
@@ -441,7 +441,6 @@ cudaError_t launch_prompt_simt_fwd(const PromptParams& p, cudaStream_t stream) {
 cudaError_t launch_prompt_simt_bwd(const PromptParams& p, cudaStream_t stream) { return prompt::launch_any(p, true, stream); }
 
 // (first form: tensor cores come after)
-cudaError_t launch_prompt_tc_fwd(const PromptParams& p, cudaStream_t stream) { return prompt::launch_any(p, false, stream); }
 cudaError_t launch_prompt_tc_bwd(const PromptParams& p, cudaStream_t stream) { return prompt::launch_any(p, true, stream); }
 
 }  // namespace triattn
