@@ -116,7 +116,7 @@ def load() -> ctypes.CDLL:
         lib.tri_attn_prompt_fwd.restype = I
         lib.tri_attn_prompt_bwd.argtypes = [P, P, P, I, P, P, I, I, I, I, I, I, I, I, F, L, L, L, P, P, P, P, P, P, P, Z, P]
         lib.tri_attn_prompt_bwd.restype = I
-        lib.tri_attn_prompt_bwd_workspace_size.argtypes = [I, I, I, I]
+        lib.tri_attn_prompt_bwd_workspace_size.argtypes = [I] * 9
         lib.tri_attn_prompt_bwd_workspace_size.restype = Z
         lib.tri_attn_mask_to_kv_lengths.argtypes = [P, I, I, I, P, P, P]
         lib.tri_attn_mask_to_kv_lengths.restype = I
@@ -387,8 +387,9 @@ def tri_attn_prompt_bwd(q, k, v, dtype, cu_seqlens_q, cu_seqlens_k, num_seqs, to
 
 
 @functools.lru_cache(maxsize=256)
-def tri_attn_prompt_bwd_workspace_size(dtype, total_q, Hq, D) -> int:
-    return int(load().tri_attn_prompt_bwd_workspace_size(dtype, total_q, Hq, D))
+def tri_attn_prompt_bwd_workspace_size(dtype, num_seqs, total_q, total_k, max_seqlen_q, max_seqlen_k, Hq, Hk, D) -> int:
+    return int(load().tri_attn_prompt_bwd_workspace_size(dtype, num_seqs, total_q, total_k, max_seqlen_q, max_seqlen_k, Hq, Hk,
+                                                         D))
 
 
 def tri_attn_mask_to_kv_lengths(mask, B, N, K, kv_lengths, nonprefix_count, stream) -> None:

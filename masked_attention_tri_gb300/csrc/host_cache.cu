@@ -388,15 +388,25 @@ ta_status prompt_params(const void* q, const void* k, const void* v, ta_dtype dt
     return TA_OK;
 }
 
-// The backward's workspace: fp32 dQ (tensor cores) and dO . O; its size, and with p its parts.
-size_t prompt_workspace(int dtype, int total_q, int Hq, int D, char* ws, PromptParams* p) {
-    const size_t rows = ((size_t)total_q * Hq + 63) / 64 * 64;
-    const size_t acc = prompt_on_tc(dtype, D) ? rows * D * sizeof(float) : 0;
+// The backward's workspace: fp32 sums of dQ, and of dK and dV where several CTAs share them (tensor cores), and dO . O; its
+// size, and with p its parts.
+size_t prompt_workspace(int dtype, int num_seqs, int total_q, int total_k, int max_q, int max_k, int Hq, int Hk, int D,
+                        char* ws, PromptParams* p) {
+    const bool tc = prompt_on_tc(dtype, D);
+    if (max_q > total_q) max_q = total_q;
+    if (max_k > total_k) max_k = total_k;
+    const size_t rows = ((size_t)total_q * Hq + 63) / 64 * 64, keys = ((size_t)total_k * Hk + 63) / 64 * 64;
+    const size_t acc = tc ? rows * D * sizeof(float) : 0;
+    const bool shared = tc && prompt_bwd_splits(num_seqs, total_k, max_q, max_k, Hk, Hq / Hk) > 1;
     if (p) {
-        p->dq_acc = reinterpret_cast<float*>(ws);
+        p->dq_acc = tc ? reinterpret_cast<float*>(ws) : nullptr;
         p->delta = reinterpret_cast<float*>(ws + acc);
+        if (shared) {
+            p->dk_acc = p->delta + rows;
+            p->dv_acc = p->dk_acc + (size_t)total_k * Hk * D;
+        }
     }
-    return acc + rows * sizeof(float);
+    return acc + rows * sizeof(float) + (shared ? 2 * keys * D * sizeof(float) : 0);
 }
 
 }  // namespace
@@ -544,9 +554,12 @@ TA_EXPORT ta_status tri_attn_prompt_fwd(const void* q, const void* k, const void
     return launched(prompt_on_tc(dtype, D) ? launch_prompt_tc_fwd(p, s) : launch_prompt_simt_fwd(p, s));
 }
 
-TA_EXPORT size_t tri_attn_prompt_bwd_workspace_size(ta_dtype dtype, int total_q, int Hq, int D) {
-    if (total_q <= 0 || Hq <= 0 || D <= 0) return 0;
-    return prompt_workspace(dtype, total_q, Hq, D, nullptr, nullptr);
+TA_EXPORT size_t tri_attn_prompt_bwd_workspace_size(ta_dtype dtype, int num_seqs, int total_q, int total_k,
+                                                    int max_seqlen_q, int max_seqlen_k, int Hq, int Hk, int D) {
+    if (num_seqs <= 0 || total_q <= 0 || total_k < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || Hq <= 0 || Hk <= 0 ||
+        D <= 0 || Hq % Hk != 0)
+        return 0;
+    return prompt_workspace(dtype, num_seqs, total_q, total_k, max_seqlen_q, max_seqlen_k, Hq, Hk, D, nullptr, nullptr);
 }
 
 TA_EXPORT ta_status tri_attn_prompt_bwd(const void* q, const void* k, const void* v, ta_dtype dtype,
@@ -565,13 +578,16 @@ TA_EXPORT ta_status tri_attn_prompt_bwd(const void* q, const void* k, const void
                                        v_row_stride, const_cast<void*>(out), const_cast<float*>(lse), p);
     if (st != TA_OK) return st;
     if ((total_q == 0 || max_seqlen_q == 0) && (total_k == 0 || max_seqlen_k == 0)) return TA_OK;
-    const size_t need = total_q > 0 ? prompt_workspace(dtype, total_q, Hq, D, nullptr, nullptr) : 0;
+    const size_t need = tri_attn_prompt_bwd_workspace_size(dtype, num_seqs, total_q, total_k, max_seqlen_q, max_seqlen_k, Hq,
+                                                           Hk, D);
     if (need && (!workspace || workspace_bytes < need)) return TA_ERR_INVALID_ARG;
     p.d_out = d_out;
     p.dq = dq;
     p.dk = dk;
     p.dv = dv;
-    prompt_workspace(dtype, total_q, Hq, D, static_cast<char*>(workspace), &p);
+    if (total_q > 0)
+        prompt_workspace(dtype, num_seqs, total_q, total_k, max_seqlen_q, max_seqlen_k, Hq, Hk, D,
+                         static_cast<char*>(workspace), &p);
     p.status = status_word();
     if (!p.status) return TA_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -247,6 +247,8 @@ struct PromptParams {
     void* dv;
     float* dq_acc;              // workspace: fp32 dQ (total_q, Hq, D), tensor cores only
     float* delta;               // workspace: dO . O (Hq, total_q)
+    float* dk_acc;              // workspace: fp32 dK and dV (total_k, Hk, D) where several CTAs sum them, else NULL
+    float* dv_acc;
 };
 // 16-bit inputs with D <= 128 run on tensor cores.
 inline bool prompt_on_tc(int dtype, int D) { return dtype != TA_F32 && D <= 128; }
@@ -254,6 +256,7 @@ cudaError_t launch_prompt_simt_fwd(const PromptParams& p, cudaStream_t stream);
 cudaError_t launch_prompt_simt_bwd(const PromptParams& p, cudaStream_t stream);
 cudaError_t launch_prompt_tc_fwd(const PromptParams& p, cudaStream_t stream);
 cudaError_t launch_prompt_tc_bwd(const PromptParams& p, cudaStream_t stream);
+int prompt_bwd_splits(int num_seqs, int total_k, int max_q, int max_k, int Hk, int G);  // CTAs of a key tile there
 
 // Device address of the status word on the current device (set up once per device).
 int* status_word();

@@ -40,7 +40,7 @@ __device__ __forceinline__ Seq load_seq(const PromptParams& p, int s, bool tell)
 
 constexpr float kToLog2 = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// delta[h, t] = dO[t, h] . O[t, h], which is sum_k P dP (prompt_simt.cu).
+// delta[h, t] = dO[t, h] . O[t, h], which is sum_k P dP; and zeros into the fp32 sums that there are (prompt_simt.cu).
 cudaError_t launch_delta(const PromptParams& p, cudaStream_t stream);
 
 }  // namespace prompt

@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_simt(const PromptParams p,
     }
 }
 
-// Sixteen lanes a row of (t, h).
+// Sixteen lanes a row of (t, h).  The tensor-core form's fp32 sums begin with zeros.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) prompt_delta_kernel(const PromptParams p) {
     constexpr int kV = Vec<T>::n;
@@ -370,6 +370,14 @@ __global__ void __launch_bounds__(kThreads) prompt_delta_kernel(const PromptPara
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (in && lane == 0) p.delta[(r % p.Hq) * p.total_q + r / p.Hq] = sum;
+    if (p.dq_acc) {
+        for (int d = lane * 4; in && d < p.D; d += 64) *reinterpret_cast<float4*>(p.dq_acc + r * p.D + d) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (p.dk_acc) {  // (both sums, one after the other)
+        const long long n = 2LL * p.total_k * p.Hk * p.D / 4, all = (long long)gridDim.x * kThreads;
+        for (long long e = (long long)blockIdx.x * kThreads + threadIdx.x; e < n; e += all)
+            reinterpret_cast<float4*>(p.dk_acc)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
 }
 
 cudaError_t grid_of(const PromptParams& p, long long tiles, unsigned& grid) {
@@ -439,8 +447,5 @@ cudaError_t launch_delta(const PromptParams& p, cudaStream_t stream) {
 
 cudaError_t launch_prompt_simt_fwd(const PromptParams& p, cudaStream_t stream) { return prompt::launch_any(p, false, stream); }
 cudaError_t launch_prompt_simt_bwd(const PromptParams& p, cudaStream_t stream) { return prompt::launch_any(p, true, stream); }
-
-// (first form: tensor cores come after)
-cudaError_t launch_prompt_tc_bwd(const PromptParams& p, cudaStream_t stream) { return prompt::launch_any(p, true, stream); }
 
 }  // namespace triattn

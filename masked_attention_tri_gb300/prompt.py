@@ -95,7 +95,7 @@ def prompt_attention_backward(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
     if total_q == 0:  # (keys that no query sees)
         return dq, dk.zero_(), dv.zero_()
     if S:
-        nbytes = abi.tri_attn_prompt_bwd_workspace_size(_DT[q.dtype], total_q, Hq, D)
+        nbytes = abi.tri_attn_prompt_bwd_workspace_size(*args[3:4], *args[6:14])
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         gk, gv = (dk, dv) if k.shape[0] else hold
         with _on(dev):

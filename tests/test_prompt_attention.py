@@ -140,10 +140,12 @@ def test_nothing_to_do_and_workspace():
     _fwd(total_q=0)
     _fwd(max_seqlen_q=0)
     _bwd(total_q=0, total_k=0, workspace=0, workspace_bytes=0)
-    assert abi.tri_attn_prompt_bwd_workspace_size(abi.TA_BF16, 0, 4, 64) == 0
-    # fp32 inputs and wide heads keep no sums of dQ
-    assert abi.tri_attn_prompt_bwd_workspace_size(abi.TA_F32, 100, 4, 64) == 448 * 4
-    assert abi.tri_attn_prompt_bwd_workspace_size(abi.TA_BF16, 100, 4, 64) == 448 * 4 * 65
+    size = abi.tri_attn_prompt_bwd_workspace_size
+    assert size(abi.TA_BF16, 1, 0, 100, 0, 100, 4, 2, 64) == 0 and size(abi.TA_BF16, 1, 100, 100, 100, 100, 4, 3, 64) == 0
+    # fp32 inputs and wide heads keep no sums of dQ; few key tiles, and the sums of dK and dV are there, too
+    assert size(abi.TA_F32, 1, 100, 100, 100, 100, 4, 2, 64) == size(abi.TA_BF16, 1, 100, 100, 100, 100, 4, 2, 256) == 448 * 4
+    assert size(abi.TA_BF16, 1, 100, 100, 100, 100, 4, 2, 64) == 448 * 4 * 65
+    assert size(abi.TA_BF16, 1, 1000, 1000, 1000, 1000, 4, 2, 64) == (4032 * 65 + 2 * 2048 * 64) * 4
 
 
 def test_python_refusals():
@@ -305,7 +307,7 @@ def test_written_rows_only(dtype, D):
     o, lse = ta.prompt_attention(q, k, v, cu, cu, 70, 70, return_aux=True)
     dq, dk, dv = (torch.full_like(t, 5.0) for t in (q, k, v))
     code = {BF: abi.TA_BF16, F32: abi.TA_F32}[dtype]
-    nb = abi.tri_attn_prompt_bwd_workspace_size(code, q.shape[0], Hq, D)
+    nb = abi.tri_attn_prompt_bwd_workspace_size(code, 1, q.shape[0], k.shape[0], 70, 70, Hq, Hk, D)
     ws = torch.full((nb,), 255, dtype=torch.uint8, device="cuda")
     p = lambda t: t.data_ptr()  # noqa: E731
     abi.tri_attn_prompt_bwd(p(q), p(k), p(v), code, p(cu), p(cu), 1, q.shape[0], k.shape[0], 70, 70, Hq, Hk, D, D ** -0.5, 0, 0,
