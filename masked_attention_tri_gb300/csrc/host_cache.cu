@@ -388,25 +388,19 @@ ta_status prompt_params(const void* q, const void* k, const void* v, ta_dtype dt
     return TA_OK;
 }
 
-// The backward's workspace: fp32 sums of dQ, and of dK and dV where several CTAs share them (tensor cores), and dO . O; its
-// size, and with p its parts.
+// The backward's workspace: dO . O, and fp32 parts of dK and dV where several CTAs share them (tensor cores); its size, and
+// with p its parts.
 size_t prompt_workspace(int dtype, int num_seqs, int total_q, int total_k, int max_q, int max_k, int Hq, int Hk, int D,
                         char* ws, PromptParams* p) {
-    const bool tc = prompt_on_tc(dtype, D);
     if (max_q > total_q) max_q = total_q;
     if (max_k > total_k) max_k = total_k;
-    const size_t rows = ((size_t)total_q * Hq + 63) / 64 * 64, keys = ((size_t)total_k * Hk + 63) / 64 * 64;
-    const size_t acc = tc ? rows * D * sizeof(float) : 0;
-    const bool shared = tc && prompt_bwd_splits(num_seqs, total_k, max_q, max_k, Hk, Hq / Hk) > 1;
+    const size_t rows = ((size_t)total_q * Hq + 63) / 64 * 64 * sizeof(float);
+    const int splits = prompt_on_tc(dtype, D) ? prompt_bwd_splits(num_seqs, total_k, max_q, max_k, Hk, Hq / Hk) : 1;
     if (p) {
-        p->dq_acc = tc ? reinterpret_cast<float*>(ws) : nullptr;
-        p->delta = reinterpret_cast<float*>(ws + acc);
-        if (shared) {
-            p->dk_acc = p->delta + rows;
-            p->dv_acc = p->dk_acc + (size_t)total_k * Hk * D;
-        }
+        p->delta = reinterpret_cast<float*>(ws);
+        p->parts = splits > 1 ? reinterpret_cast<float*>(ws + rows) : nullptr;
     }
-    return acc + rows * sizeof(float) + (shared ? 2 * keys * D * sizeof(float) : 0);
+    return rows + (splits > 1 ? (size_t)splits * 2 * total_k * Hk * D * sizeof(float) : 0);
 }
 
 }  // namespace

@@ -245,10 +245,8 @@ struct PromptParams {
     void* dq;
     void* dk;
     void* dv;
-    float* dq_acc;              // workspace: fp32 dQ (total_q, Hq, D), tensor cores only
     float* delta;               // workspace: dO . O (Hq, total_q)
-    float* dk_acc;              // workspace: fp32 dK and dV (total_k, Hk, D) where several CTAs sum them, else NULL
-    float* dv_acc;
+    float* parts;               // workspace: fp32 parts of dK and dV (splits, 2, total_k, Hk, D) where several CTAs share them, else NULL
 };
 // 16-bit inputs with D <= 128 run on tensor cores.
 inline bool prompt_on_tc(int dtype, int D) { return dtype != TA_F32 && D <= 128; }

@@ -1,5 +1,5 @@
-// prompt.cuh -- causal attention of packed prompts with grouped heads: what its kernels (prompt_simt.cu,
-// prompt_fwd.cu, prompt_bwd.cu) share.
+// prompt.cuh -- causal attention of packed prompts with grouped heads: what its kernels (prompt_simt.cu, prompt_fwd.cu,
+// prompt_dq.cu, prompt_dkv.cu) share.
 //
 //     O[i, h] = softmax_k(scale q_i . K[k]) V,  the keys k <= Lk - Lq + j seen by query j of a sequence's Lq,
 // query head h on key head h / G.  The G heads of a group read the same keys, so their queries are rows of one matrix:
@@ -39,9 +39,6 @@ __device__ __forceinline__ Seq load_seq(const PromptParams& p, int s, bool tell)
 }
 
 constexpr float kToLog2 = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-// delta[h, t] = dO[t, h] . O[t, h], which is sum_k P dP; and zeros into the fp32 sums that there are (prompt_simt.cu).
-cudaError_t launch_delta(const PromptParams& p, cudaStream_t stream);
 
 }  // namespace prompt
 }  // namespace triattn

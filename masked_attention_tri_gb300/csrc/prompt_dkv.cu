@@ -1,0 +1,474 @@
+// prompt_dkv.cu -- the gradients of keys and values in the causal attention of packed prompts with grouped heads on tcgen05
+// tensor cores: 16-bit inputs, D <= 128.  (dQ and delta = dO . O: prompt_dq.cu, before it.)
+//
+// Rows are tokens x heads of a group (prompt.cuh), in tiles as in the forward.  With P = 2^(s - lse) recomputed, one CTA for each
+// (sequence, key head, 128 keys) walks the row tiles that see a key of its own:
+//     S^T = K Q^T, dP^T = V dO^T         keys on the tensor-memory lanes, rows of the tile in the columns
+//     dV += P^T dO                       P^T as 16-bit pairs over S^T
+//     dS = P (dP - delta),  dK += dS^T Q dS^T as 16-bit pairs over dP^T
+// Tensor memory: S^T, dP^T, dV, dK: 4 x 128 columns at D = 128.  The sums over the group's heads are sums over rows.
+//
+// 12 warps: 0-7 softmax and dS (key = lane, 64 rows each half), 8 MMA, 9 TMA, 10 the rows' lse and delta.  The tensor core's order is
+// dV(i), S(i+1), dK(i), dP(i+1): while dS(i) is formed it has dV(i) and S(i+1) to do, and dK(i) and dP(i+1) while P(i+1) is.
+//
+// Bound: the tensor core, 2048 clocks a tile at D = 128, and shared memory with nearly as much (its operands and the loads).  Where there are too few
+// (sequence, head, key tile) for the GPU, the row tiles of one are dealt to several CTAs, whose fp32 parts are added in their order.
+#include "prompt_tc.cuh"
+
+namespace triattn {
+namespace prompt {
+
+namespace {
+
+struct DkvParams {
+    CUtensorMap tm_q, tm_k, tm_v, tm_do;
+    PromptParams p;
+    Tiles t;
+    int splits;                // CTAs of a key tile
+    uint32_t idesc_s, idesc_g;
+    int ksteps;                // D / 16, rounded up
+    float scale_log2e;
+};
+
+constexpr int kWarps = 12;
+
+template <int NB>
+struct Smem {
+    static constexpr uint32_t kTile = NB * kBox;
+    static constexpr uint32_t kK = 0, kV = kTile, kQ = 2 * kTile, kDO = kQ + 2 * kTile;
+    static constexpr uint32_t kRows = kDO + 2 * kTile;                 // [2 stages][-lse log2 e, delta][128]
+    static constexpr uint32_t kBars = kRows + 2 * 2 * 128 * 4;
+    static constexpr int kNumBars = 1 + 2 * 2 + 2 * 2 + 2 * 2 + 5;
+    static constexpr uint32_t kSlot = kBars + 8 * kNumBars, kAbort = kSlot + 4, kTotal = kAbort + 4;
+};
+static_assert(Smem<2>::kTotal <= kMaxDynamicSmem, "shared memory");
+
+// Where a CTA's part of dK (0) or dV (1) begins: keys from row `key` on of split `split`.
+__device__ __forceinline__ float* part(const PromptParams& p, int split, int which, long long key, int h) {
+    return p.parts + (((long long)split * 2 + which) * p.total_k + key) * p.Hk * p.D + (long long)h * p.D;
+}
+
+template <bool BF16, int NB>
+__global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid_constant__ DkvParams P) {
+    using M = Smem<NB>;
+    constexpr uint32_t kTile = M::kTile;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* g0 = smem_raw;
+    const uint32_t base = smem_u32(smem_raw);
+    const PromptParams& p = P.p;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    // ---- The CTA's work: key tile slowest, as the first of a sequence is seen by most rows.
+    const unsigned per = (unsigned)p.num_seqs * (unsigned)p.Hk * (unsigned)P.splits;
+    const int kt = (int)(blockIdx.x / per);
+    unsigned rest = blockIdx.x % per;
+    const int split = (int)(rest % (unsigned)P.splits);
+    rest /= (unsigned)P.splits;
+    const int h = (int)(rest % (unsigned)p.Hk), seq = (int)(rest / (unsigned)p.Hk);
+    const Seq q = load_seq(p, seq, threadIdx.x == 0 && kt == 0 && h == 0 && split == 0);
+    const int k0 = 128 * kt;
+    if (k0 >= q.lk) return;
+    const int keys = min(128, q.lk - k0);                               // that exist
+    const int blocks = (q.lq + P.t.tq - 1) / P.t.tq;
+    const int first = max(0, k0 - q.shift) / P.t.tq * P.t.ng + split;       // the first tile with a row that sees the key k0
+    const int n = first < blocks * P.t.ng ? (blocks * P.t.ng - first + P.splits - 1) / P.splits : 0;
+    uint16_t* dk = static_cast<uint16_t*>(p.dk) + ((long long)(q.k0 + k0) * p.Hk + h) * p.D;
+    uint16_t* dv = static_cast<uint16_t*>(p.dv) + ((long long)(q.k0 + k0) * p.Hk + h) * p.D;
+    if (n == 0) {  // no row for this CTA: zeros
+        const int pieces = p.D / 8;
+        for (int e = threadIdx.x; e < keys * pieces; e += kWarps * 32) {
+            const int k = e / pieces, d = (e % pieces) * 8;
+            if (P.splits == 1) {
+                *reinterpret_cast<uint4*>(dk + (long long)k * p.Hk * p.D + d) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(dv + (long long)k * p.Hk * p.D + d) = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+                for (int w = 0; w < 2; ++w) {
+                    float4* to = reinterpret_cast<float4*>(part(p, split, w, q.k0 + k0 + k, h) + d);
+                    to[0] = to[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
+        }
+        return;
+    }
+    // Tile j of the walk: its first token, first query head and rows.
+    auto tile = [&](int j, int& tok, int& head, int& rows) {
+        const int t = first + j * P.splits, b = t / P.t.ng;
+        tok = b * P.t.tq;
+        head = h * p.G + (t - b * P.t.ng) * P.t.hp;
+        rows = min(P.t.tq, q.lq - tok) * P.t.hp;
+    };
+
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(g0 + M::kAbort);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(g0 + M::kSlot);
+    float* row_s = reinterpret_cast<float*>(g0 + M::kRows);
+    auto bar = [&](int i) { return base + M::kBars + 8u * (uint32_t)i; };
+    const uint32_t kv_full = bar(0);
+    auto q_full = [&](int s) { return bar(1 + s); };
+    auto q_empty = [&](int s) { return bar(3 + s); };
+    auto do_full = [&](int s) { return bar(5 + s); };
+    auto do_empty = [&](int s) { return bar(7 + s); };
+    auto row_full = [&](int s) { return bar(9 + s); };
+    auto row_empty = [&](int s) { return bar(11 + s); };
+    const uint32_t s_full = bar(13), p_full = bar(14), dp_full = bar(15), ds_full = bar(16), fin = bar(17);
+    auto q_smem = [&](int s) { return base + M::kQ + (uint32_t)s * kTile; };
+    auto do_smem = [&](int s) { return base + M::kDO + (uint32_t)s * kTile; };
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        mbar_init(kv_full, 1);
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(q_full(s), 1);
+            mbar_init(q_empty(s), 1);
+            mbar_init(do_full(s), 1);
+            mbar_init(do_empty(s), 1);
+            mbar_init(row_full(s), 1);
+            mbar_init(row_empty(s), 8);
+        }
+        mbar_init(s_full, 1);
+        mbar_init(p_full, 8);
+        mbar_init(dp_full, 1);
+        mbar_init(ds_full, 8);
+        mbar_init(fin, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // Rows of Q and dO that no box fills (tq hp < 128) stay zeros.
+    const int full_rows = P.t.tq * P.t.hp;
+    for (int e = threadIdx.x; e < 4 * NB * (128 - full_rows) * 8; e += kWarps * 32) {
+        const int c = e % 8, r = e / 8 % (128 - full_rows) + full_rows, b = e / 8 / (128 - full_rows);
+        st_shared_v4(base + M::kQ + (uint32_t)b * kBox + (uint32_t)r * 128u + c * 16u, 0u, 0u, 0u, 0u);
+    }
+    fence_async_shared();
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tS = tmem, tDP = tmem + 128, tDV = tmem + 256, tDK = tmem + 256 + NB * 64;
+    bool ok = true;
+
+    if (warp == 9) {
+        // -------------------------------------------------------- TMA
+        if (lane == 0) {
+            mbar_expect_tx(kv_full, 2 * kTile);
+            for (int b = 0; b < NB; ++b) {
+                tma_load_3d(base + M::kK + b * kBox, &P.tm_k, 64 * b, h, q.k0 + k0, kv_full);
+                tma_load_3d(base + M::kV + b * kBox, &P.tm_v, 64 * b, h, q.k0 + k0, kv_full);
+            }
+        }
+        const uint32_t bytes = (uint32_t)full_rows * 128u * NB;
+        for (int j = 0; j < n && ok; ++j) {
+            int tok, head, rows;
+            tile(j, tok, head, rows);
+            const int s = j & 1;
+            const uint32_t before = (uint32_t)(j / 2 - 1) & 1u;
+            if (j >= 2) ok = __all_sync(0xffffffffu, wait(q_empty(s), before, abort_flag, p.status));
+            if (ok && lane == 0) {
+                mbar_expect_tx(q_full(s), bytes);
+                for (int b = 0; b < NB; ++b) tma_load_3d(q_smem(s) + b * kBox, &P.tm_q, 64 * b, head, q.q0 + tok, q_full(s));
+            }
+            if (j >= 2 && ok) ok = __all_sync(0xffffffffu, wait(do_empty(s), before, abort_flag, p.status));
+            if (ok && lane == 0) {
+                mbar_expect_tx(do_full(s), bytes);
+                for (int b = 0; b < NB; ++b) tma_load_3d(do_smem(s) + b * kBox, &P.tm_do, 64 * b, head, q.q0 + tok, do_full(s));
+            }
+        }
+        if (!ok) *abort_flag = 1;
+    } else if (warp == 10) {
+        // -------------------------------------------------------- the rows' factors
+        for (int j = 0; j < n && ok; ++j) {
+            int tok, head, rows;
+            tile(j, tok, head, rows);
+            const int s = j & 1;
+            float a[4], b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 32 * i + lane, t = (int)P.t.fd_hp.div((uint32_t)r);
+                const long long at = (long long)(head + r - t * P.t.hp) * p.total_q + q.q0 + tok + t;
+                a[i] = r < rows ? p.lse[at] : 0.f;
+                b[i] = r < rows ? p.delta[at] : 0.f;
+            }
+            if (j >= 2) ok = __all_sync(0xffffffffu, wait(row_empty(s), (uint32_t)(j / 2 - 1) & 1u, abort_flag, p.status));
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                row_s[s * 256 + 32 * i + lane] = -a[i] * tc::kLog2e;
+                row_s[s * 256 + 128 + 32 * i + lane] = -b[i];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(row_full(s));
+        }
+        if (!ok) *abort_flag = 1;
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ MMA
+        const bool leader = elect_one();
+        auto wait_all = [&](uint32_t b, uint32_t parity) {
+            if (ok) ok = __all_sync(0xffffffffu, wait(b, parity, abort_flag, p.status));
+            tc_fence_after();
+            return ok;
+        };
+        auto kstep = [](int kk) { return (uint64_t)(((kk >> 2) * kBox + (kk & 3) * 32) >> 4); };
+        const uint64_t kK = sw128_desc(base + M::kK, 16, 1024), vK = sw128_desc(base + M::kV, 16, 1024);
+        int tok, head, rows;
+        // S^T or dP^T of tile j.  (Rows of a tile past its own are another sequence's, or nobody's: zeroed up to the next 16,
+        // which dV and dK multiply with zeros.)
+        auto first_mma = [&](int j, bool dp) {
+            const int s = j & 1;
+            if (!wait_all(dp ? do_full(s) : q_full(s), (uint32_t)(j / 2) & 1u)) return;
+            const uint32_t at = dp ? do_smem(s) : q_smem(s);
+            tile(j, tok, head, rows);
+            if (rows < full_rows) clear_rows<NB>(at, rows, (rows + 15) & ~15);
+            if (leader) {
+                const uint64_t a = dp ? vK : kK, b = sw128_desc(at, 16, 1024);
+                const uint32_t d = dp ? tDP : tS;
+#pragma unroll
+                for (int kk = 0; kk < 4 * NB; ++kk)
+                    if (kk < P.ksteps) mma_ss(d, a + kstep(kk), b + kstep(kk), P.idesc_s, kk > 0 ? 1u : 0u);
+                mma_commit(dp ? dp_full : s_full);
+            }
+        };
+        // dV += P^T dO or dK += dS^T Q of tile j: 16 rows a step, those of the second half 64 columns on
+        auto second_mma = [&](int j, bool dk_) {
+            if (!wait_all(dk_ ? ds_full : p_full, (uint32_t)j & 1u)) return;
+            tile(j, tok, head, rows);
+            if (leader) {
+                const int steps = (rows + 15) / 16;
+                const uint64_t b = sw128_desc(dk_ ? q_smem(j & 1) : do_smem(j & 1), kBox, 1024);
+                const uint32_t a = dk_ ? tDP : tS, d = dk_ ? tDK : tDV;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    if (kk < steps)
+                        mma_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b + (uint64_t)kk * 128, P.idesc_g, (j > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(dk_ ? q_empty(j & 1) : do_empty(j & 1));
+            }
+        };
+        if (wait_all(kv_full, 0)) {
+            first_mma(0, false);
+            if (ok) first_mma(0, true);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+            second_mma(j, false);
+            if (ok && j + 1 < n) first_mma(j + 1, false);
+            if (ok) second_mma(j, true);
+            if (ok && j + 1 < n) first_mma(j + 1, true);
+        }
+        if (!ok && leader) *abort_flag = 1;
+        if (leader) mma_commit(fin);
+        wait_bar_drain(fin, 0);
+        __syncwarp();
+    } else if (warp < 8) {
+        // ------------------------------------------------------------ P and dS
+        const int half = warp / 4, kr = warp % 4 * 32 + lane;          // rows [64 half, + 64) of a tile; key
+        const uint32_t lane_off = (uint32_t)(warp % 4 * 32) << 16;
+        const uint32_t sA = tS + lane_off + 64u * half, dpA = tDP + lane_off + 64u * half;
+        const float f = P.scale_log2e;
+        for (int j = 0; j < n && ok; ++j) {
+            const uint32_t ph = (uint32_t)j & 1u;
+            const int s = j & 1;
+            int tok, head, rows;
+            tile(j, tok, head, rows);
+            // the rows that see this key: from `from` on, of those that exist
+            const long long from = (long long)(k0 + kr - q.shift - tok) * P.t.hp;
+            const bool edge = rows < 128 || keys < 128 || k0 + 127 > tok + q.shift;
+            uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int c0 = 64 * half + 32 * i;
+                    const int lo = from <= c0 ? 0 : from >= c0 + 32 ? 32 : (int)from - c0;
+                    see[i] = kr < keys ? low_bits(rows - c0) & ~low_bits(lo) : 0u;
+                }
+            }
+            const float4* nl = reinterpret_cast<const float4*>(row_s + s * 256 + 64 * half);
+            const float4* nd = nl + 32;
+            ok = __all_sync(0xffffffffu, wait(row_full(s), (uint32_t)(j / 2) & 1u, abort_flag, p.status)) &&
+                 __all_sync(0xffffffffu, wait(s_full, ph, abort_flag, p.status));
+            if (!ok) break;
+            tc_fence_after();
+            float pr[64];
+            {
+                uint32_t sr[64];
+                tmem_ld_x64(sA, sr);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const float4 l = nl[c];
+                    const float2 a = __ffma2_rn(make_float2(__uint_as_float(sr[4 * c]), __uint_as_float(sr[4 * c + 1])),
+                                                make_float2(f, f), make_float2(l.x, l.y));
+                    const float2 b = __ffma2_rn(make_float2(__uint_as_float(sr[4 * c + 2]), __uint_as_float(sr[4 * c + 3])),
+                                                make_float2(f, f), make_float2(l.z, l.w));
+                    pr[4 * c] = ex2(a.x);
+                    pr[4 * c + 1] = ex2(a.y);
+                    pr[4 * c + 2] = ex2(b.x);
+                    pr[4 * c + 3] = ex2(b.y);
+                }
+            }
+            if (edge) {
+#pragma unroll
+                for (int c = 0; c < 64; ++c) pr[c] = (see[c / 32] >> (c % 32)) & 1u ? pr[c] : 0.f;
+            }
+            {
+                uint32_t pk[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) pk[c] = pack2<BF16>(pr[2 * c], pr[2 * c + 1]);
+                tmem_st_x32(sA, pk);
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full);
+            ok = __all_sync(0xffffffffu, wait(dp_full, ph, abort_flag, p.status));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t dr[32];
+                tmem_ld_x32(dpA + 32 * i, dr);
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) {
+                    const float4 d = nd[8 * i + c / 4];
+                    const int pa = 32 * i + c;
+                    float2 u = __fadd2_rn(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), make_float2(d.x, d.y));
+                    float2 v = __fadd2_rn(make_float2(__uint_as_float(dr[c + 2]), __uint_as_float(dr[c + 3])), make_float2(d.z, d.w));
+                    u = __fmul2_rn(u, make_float2(pr[pa], pr[pa + 1]));
+                    v = __fmul2_rn(v, make_float2(pr[pa + 2], pr[pa + 3]));
+                    if (edge) {  // (dP and delta of a row that is not there may be anything)
+                        u.x = (see[i] >> c) & 1u ? u.x : 0.f;
+                        u.y = (see[i] >> (c + 1)) & 1u ? u.y : 0.f;
+                        v.x = (see[i] >> (c + 2)) & 1u ? v.x : 0.f;
+                        v.y = (see[i] >> (c + 3)) & 1u ? v.y : 0.f;
+                    }
+                    pk[pa / 2] = pack2<BF16>(u.x, u.y);
+                    pk[pa / 2 + 1] = pack2<BF16>(v.x, v.y);
+                }
+            }
+            tmem_st_x32(dpA, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(ds_full);
+                mbar_arrive(row_empty(s));
+            }
+        }
+        // ---- dV (warps 0-3) and dK (4-7), when every product is done.
+        if (ok) ok = __all_sync(0xffffffffu, wait(fin, 0, abort_flag, p.status));
+        if (ok && !*abort_flag) {
+            tc_fence_after();
+            const uint32_t from = (half ? tDK : tDV) + lane_off;
+            const float by = half ? p.scale : 1.f;
+            uint16_t* to = (half ? dk : dv) + (long long)kr * p.Hk * p.D;
+            float* acc = P.splits > 1 ? part(p, split, half ? 0 : 1, q.k0 + k0 + kr, h) : nullptr;
+#pragma unroll 1
+            for (int c = 0; c < p.D; c += 16) {
+                uint32_t o[16];
+                tmem_ld_x16(from + c, o);
+                if (kr >= keys) continue;
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                    if (c + e >= p.D) break;
+                    float x[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[e + k]) * by;
+                    if (acc) {
+                        *reinterpret_cast<float4*>(acc + c + e) = make_float4(x[0], x[1], x[2], x[3]);
+                        *reinterpret_cast<float4*>(acc + c + e + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                    } else {
+                        *reinterpret_cast<uint4*>(to + c + e) = make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]),
+                                                                           pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
+                    }
+                }
+            }
+        }
+        if (!ok) *abort_flag = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
+}
+
+// The CTAs' parts of a (sequence, key head, 128 keys), added in their order.
+template <bool BF16>
+__global__ void __launch_bounds__(256) prompt_dkv_join(const PromptParams p, int splits) {
+    const unsigned per = (unsigned)p.num_seqs * (unsigned)p.Hk;
+    const int k0 = 128 * (int)(blockIdx.x / per), h = (int)(blockIdx.x % per % (unsigned)p.Hk);
+    const Seq q = load_seq(p, (int)(blockIdx.x % per / (unsigned)p.Hk), false);
+    const int keys = min(128, q.lk - k0), pieces = p.D / 8;
+    for (int e = threadIdx.x; e < 2 * keys * pieces; e += 256) {
+        const int which = e >= keys * pieces, x = which ? e - keys * pieces : e, k = x / pieces, d = (x - k * pieces) * 8;
+        const long long key = q.k0 + k0 + k;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll 4
+        for (int i = 0; i < splits; ++i) {
+            const float4* from = reinterpret_cast<const float4*>(part(p, i, which, key, h) + d);
+            const float4 u = from[0], v = from[1];
+            a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
+            b.x += v.x, b.y += v.y, b.z += v.z, b.w += v.w;
+        }
+        uint16_t* to = static_cast<uint16_t*>(which ? p.dv : p.dk) + (key * p.Hk + h) * p.D + d;
+        *reinterpret_cast<uint4*>(to) =
+            make_uint4(pack2<BF16>(a.x, a.y), pack2<BF16>(a.z, a.w), pack2<BF16>(b.x, b.y), pack2<BF16>(b.z, b.w));
+    }
+}
+
+template <bool BF16, int NB>
+cudaError_t start(const DkvParams& P, unsigned grid, cudaStream_t stream) {
+    auto kern = prompt_dkv_kernel<BF16, NB>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<NB>::kTotal);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kWarps * 32, Smem<NB>::kTotal, stream>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_dq(const PromptParams& p, cudaStream_t stream);  // prompt_dq.cu
+
+}  // namespace prompt
+
+// CTAs of a key tile: one, or as many as give the GPU's 152 SMs two each where there are few (sequence, head, key tile), but
+// four row tiles for each at least.
+int prompt_bwd_splits(int num_seqs, int total_k, int max_q, int max_k, int Hk, int G) {
+    const long long a = (long long)num_seqs * ((max_k + 127) / 128), b = (long long)total_k / 128 + num_seqs;
+    const long long ctas = (a < b ? a : b) * Hk, tiles = ((long long)max_q * G + 127) / 128;
+    if (ctas <= 0 || ctas >= 304) return 1;
+    long long s = (304 + ctas - 1) / ctas;
+    if (s > tiles / 4) s = tiles / 4;
+    return s < 1 ? 1 : (int)(s > 32 ? 32 : s);
+}
+
+cudaError_t launch_prompt_tc_bwd(const PromptParams& p, cudaStream_t stream) {
+    using namespace prompt;
+    cudaError_t e = p.total_q > 0 && p.max_q > 0 ? launch_dq(p, stream) : cudaSuccess;
+    if (e != cudaSuccess || p.max_k <= 0) return e;
+    DkvParams P;
+    P.p = p;
+    P.t = make_tiles(p);
+    P.splits = p.parts ? prompt_bwd_splits(p.num_seqs, p.total_k, p.max_q, p.max_k, p.Hk, p.G) : 1;
+    const bool bf16 = p.dtype == TA_BF16;
+    P.idesc_s = make_idesc(bf16, 128, 0, 0);
+    P.idesc_g = make_idesc(bf16, (uint32_t)(p.D + 15) / 16 * 16, 0, 1);
+    P.ksteps = (p.D + 15) / 16;
+    P.scale_log2e = p.scale * kToLog2;
+    const long long tiles = (long long)p.num_seqs * p.Hk * ((p.max_k + 127) / 128), grid = tiles * P.splits;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (!make_rows_map(&P.tm_q, bf16, p.q, p.D, p.Hq, p.total_q, p.q_rs, P.t.hp, P.t.tq) ||
+        !make_rows_map(&P.tm_do, bf16, p.d_out, p.D, p.Hq, p.total_q, (long long)p.Hq * p.D, P.t.hp, P.t.tq) ||
+        !make_rows_map(&P.tm_k, bf16, p.k, p.D, p.Hk, p.total_k, p.k_rs, 1, 128) ||
+        !make_rows_map(&P.tm_v, bf16, p.v, p.D, p.Hk, p.total_k, p.v_rs, 1, 128))
+        return cudaErrorInvalidValue;
+    if (p.D <= 64) e = bf16 ? start<true, 1>(P, (unsigned)grid, stream) : start<false, 1>(P, (unsigned)grid, stream);
+    else e = bf16 ? start<true, 2>(P, (unsigned)grid, stream) : start<false, 2>(P, (unsigned)grid, stream);
+    if (e != cudaSuccess || P.splits == 1) return e;
+    if (bf16) prompt_dkv_join<true><<<(unsigned)tiles, 256, 0, stream>>>(p, P.splits);
+    else prompt_dkv_join<false><<<(unsigned)tiles, 256, 0, stream>>>(p, P.splits);
+    return cudaGetLastError();
+}
+
+}  // namespace triattn

@@ -1,0 +1,407 @@
+// prompt_dq.cu -- the gradient of the queries in the causal attention of packed prompts with grouped heads on tcgen05 tensor
+// cores (16-bit inputs, D <= 128), and the rows' delta = dO . O, which prompt_dkv.cu reads after it.
+//
+// A tile of rows (prompt_tc.cuh) walks the key tiles that it sees, as in the forward, with P = 2^(s - lse) recomputed:
+//     S = Q K^T, dP = dO V^T             rows on the tensor-memory lanes
+//     dS = P (dP - delta)                as 16-bit pairs over S
+//     dQ += dS K                         dS from tensor memory
+// lse and delta are one number a thread, dQ stays in tensor memory, and is rounded once: no sum in memory, no order that varies.
+// (One kernel for dQ, dK and dV computes S and dP once, five products a tile where the two kernels have seven; but its dQ has to be added
+// up in memory over the key tiles and stands between the tiles' products, and four 128 x 128 x D products a tile from shared memory are more
+// than that gives: four sequences of 8192 tokens, 16 heads over 4 of 128, 3.86 ms, of which 0.5 ms were the reductions.)
+//
+// One CTA a SM, 12 warps: 0-7 softmax and dS (a row's two halves of 64 keys each), 8 MMA, 9 TMA, 10 the items.  Tensor memory: S twice, dP,
+// dQ: 4 x 128 columns at D = 128.  S of the next tile is there while dS is formed, dP follows as soon as the last one is read.
+#include "prompt_tc.cuh"
+
+namespace triattn {
+namespace prompt {
+namespace {
+
+struct DqParams {
+    CUtensorMap tm_q, tm_k, tm_v, tm_do;
+    PromptParams p;
+    Tiles t;
+    uint32_t idesc_s, idesc_q;
+    int ksteps;                // D / 16, rounded up
+    float scale_log2e;
+};
+
+constexpr int kRing = 2, kWarps = 12, kConsumers = 10;
+constexpr int kKStages = 3, kVStages = 2;
+
+template <int NB>
+struct Smem {
+    static constexpr uint32_t kTile = NB * kBox;
+    static constexpr uint32_t kQ = 0, kDO = kTile, kK = 2 * kTile, kV = kK + kKStages * kTile;
+    static constexpr uint32_t kItems = kV + kVStages * kTile, kClc = kItems + kRing * sizeof(Item<1>), kBars = kClc + 16;
+    static constexpr int kNumBars = 2 + 2 * kKStages + 2 * kVStages + 6 + 2 * kRing + 2;
+    static constexpr uint32_t kSlot = kBars + 8 * kNumBars, kAbort = kSlot + 4, kTotal = kAbort + 4;
+};
+static_assert(Smem<2>::kTotal <= kMaxDynamicSmem, "shared memory");
+
+template <bool BF16, int NB>
+__global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_constant__ DqParams P) {
+    using M = Smem<NB>;
+    constexpr uint32_t kTile = M::kTile;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* g0 = smem_raw;
+    const uint32_t base = smem_u32(smem_raw);
+    const PromptParams& p = P.p;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(g0 + M::kAbort);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(g0 + M::kSlot);
+    Item<1>* items = reinterpret_cast<Item<1>*>(g0 + M::kItems);
+    auto bar = [&](int i) { return base + M::kBars + 8u * (uint32_t)i; };
+    const uint32_t q_full = bar(0), q_empty = bar(1);
+    auto k_full = [&](int s) { return bar(2 + s); };
+    auto k_empty = [&](int s) { return bar(2 + kKStages + s); };
+    constexpr int b0 = 2 + 2 * kKStages;
+    auto v_full = [&](int s) { return bar(b0 + s); };
+    auto v_empty = [&](int s) { return bar(b0 + kVStages + s); };
+    constexpr int b1 = b0 + 2 * kVStages;
+    auto s_full = [&](int b) { return bar(b1 + b); };
+    const uint32_t dp_full = bar(b1 + 2), ds_full = bar(b1 + 3), dq_full = bar(b1 + 4), dq_empty = bar(b1 + 5);
+    auto it_full = [&](int r) { return bar(b1 + 6 + r); };
+    auto it_empty = [&](int r) { return bar(b1 + 6 + kRing + r); };
+    const uint32_t clc = bar(b1 + 6 + 2 * kRing), drain = bar(b1 + 7 + 2 * kRing);
+    static_assert(b1 + 8 + 2 * kRing == M::kNumBars, "barriers");
+    auto k_smem = [&](int s) { return base + M::kK + (uint32_t)s * kTile; };
+    auto v_smem = [&](int s) { return base + M::kV + (uint32_t)s * kTile; };
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+#pragma unroll 1
+        for (int s = 0; s < kKStages; ++s) {
+            mbar_init(k_full(s), 1);
+            mbar_init(k_empty(s), 1);
+        }
+#pragma unroll 1
+        for (int s = 0; s < kVStages; ++s) {
+            mbar_init(v_full(s), 1);
+            mbar_init(v_empty(s), 1);
+        }
+        mbar_init(s_full(0), 1);
+        mbar_init(s_full(1), 1);
+        mbar_init(dp_full, 1);
+        mbar_init(ds_full, 8);
+        mbar_init(dq_full, 1);
+        mbar_init(dq_empty, 8);
+        for (int r = 0; r < kRing; ++r) {
+            mbar_init(it_full(r), 1);
+            mbar_init(it_empty(r), kConsumers);
+        }
+        mbar_init(clc, 1);
+        mbar_init(drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // Rows of Q and dO that no box fills (tq hp < 128) stay zeros.
+    const int full_rows = P.t.tq * P.t.hp;
+    for (int e = threadIdx.x; e < 2 * NB * (128 - full_rows) * 8; e += kWarps * 32) {
+        const int c = e % 8, r = e / 8 % (128 - full_rows) + full_rows, b = e / 8 / (128 - full_rows);
+        st_shared_v4(base + M::kQ + (uint32_t)b * kBox + (uint32_t)r * 128u + c * 16u, 0u, 0u, 0u, 0u);
+    }
+    fence_async_shared();
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot, tDP = tmem + 256, tDQ = tmem + 384;
+    bool ok = true;
+    int item_n = 0;
+    auto next_item = [&](Item<1>& it) -> bool {
+        const int r = item_n % kRing;
+        ok = __all_sync(0xffffffffu, wait(it_full(r), (uint32_t)(item_n / kRing) & 1u, abort_flag, p.status));
+        if (!ok) return false;
+        it = items[r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(it_empty(r));
+        ++item_n;
+        return it.on != 0;
+    };
+
+    if (warp == 10) {
+        // ------------------------------------------------------------ the items
+        ok = hand_out<1, kRing>(p, P.t, items, it_full, it_empty, base + M::kClc, clc, abort_flag);
+        if (!ok) *abort_flag = 1;
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ TMA
+        StageRing kr = {0, 0u, false}, vr = {0, 0u, false};
+        Item<1> it;
+        uint32_t q_use = 0;
+        const uint32_t q_bytes = (uint32_t)full_rows * 128u * NB;
+        while (ok && next_item(it)) {
+            const int n = (it.keys[0] + 127) / 128;
+            if (n == 0) continue;
+            if (q_use > 0) ok = __all_sync(0xffffffffu, wait(q_empty, (q_use - 1u) & 1u, abort_flag, p.status));
+            ++q_use;
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_expect_tx(q_full, 2 * q_bytes);
+                for (int b = 0; b < NB; ++b) {
+                    tma_load_3d(base + M::kQ + b * kBox, &P.tm_q, 64 * b, it.head[0], it.q0 + it.tok[0], q_full);
+                    tma_load_3d(base + M::kDO + b * kBox, &P.tm_do, 64 * b, it.head[0], it.q0 + it.tok[0], q_full);
+                }
+            }
+            auto load = [&](StageRing& r, int stages, bool v, int j) {
+                const uint32_t full = v ? v_full(r.idx) : k_full(r.idx);
+                if (ok && r.wrapped)
+                    ok = __all_sync(0xffffffffu, wait(v ? v_empty(r.idx) : k_empty(r.idx), r.ph ^ 1u, abort_flag, p.status));
+                if (ok && lane == 0) {
+                    mbar_expect_tx(full, kTile);
+                    for (int b = 0; b < NB; ++b)
+                        tma_load_3d((v ? v_smem(r.idx) : k_smem(r.idx)) + b * kBox, v ? &P.tm_v : &P.tm_k, 64 * b, it.h,
+                                    it.k0 + 128 * j, full);
+                }
+                r.next(stages);
+            };
+            for (int j = 0; j < n && ok; ++j) {
+                load(kr, kKStages, false, j);
+                load(vr, kVStages, true, j);
+            }
+        }
+        if (!ok) *abort_flag = 1;
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ MMA
+        const bool leader = elect_one();
+        StageRing ks = {0, 0u, false}, kq = {0, 0u, false}, vr = {0, 0u, false};  // K for S, K for dQ, V
+        Item<1> it;
+        uint32_t q_use = 0, ds_use = 0;
+        auto wait_all = [&](uint32_t b, uint32_t parity) {
+            if (ok) ok = __all_sync(0xffffffffu, wait(b, parity, abort_flag, p.status));
+            tc_fence_after();
+            return ok;
+        };
+        auto kstep = [](int kk) { return (uint64_t)(((kk >> 2) * kBox + (kk & 3) * 32) >> 4); };
+        const uint64_t qd = sw128_desc(base + M::kQ, 16, 1024), dod = sw128_desc(base + M::kDO, 16, 1024);
+        while (ok && next_item(it)) {
+            const int keys = it.keys[0], n = (keys + 127) / 128, lk = it.lq + it.shift;
+            if (n == 0) continue;
+            auto s_mma = [&](int j) {
+                if (!wait_all(k_full(ks.idx), ks.ph)) return;
+                // (rows of K that are not the sequence's: dQ multiplies their zeros with them, sixteen keys at a time)
+                if (lk - 128 * j < 128) clear_rows<NB>(k_smem(ks.idx), lk - 128 * j, (lk - 128 * j + 15) & ~15);
+                const uint32_t idesc = P.idesc_s | ((uint32_t)(min(128, (keys - 128 * j + 15) & ~15) >> 3) << 17);
+                if (leader) {
+                    const uint64_t b = sw128_desc(k_smem(ks.idx), 16, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < 4 * NB; ++kk)
+                        if (kk < P.ksteps) mma_ss(tmem + (j & 1) * 128, qd + kstep(kk), b + kstep(kk), idesc, kk > 0 ? 1u : 0u);
+                    mma_commit(s_full(j & 1));
+                }
+                ks.next(kKStages);
+            };
+            auto dp_mma = [&](int j) {
+                if (!wait_all(v_full(vr.idx), vr.ph)) return;
+                const uint32_t idesc = P.idesc_s | ((uint32_t)(min(128, (keys - 128 * j + 15) & ~15) >> 3) << 17);
+                if (leader) {
+                    const uint64_t b = sw128_desc(v_smem(vr.idx), 16, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < 4 * NB; ++kk)
+                        if (kk < P.ksteps) mma_ss(tDP, dod + kstep(kk), b + kstep(kk), idesc, kk > 0 ? 1u : 0u);
+                    mma_commit(dp_full);
+                    mma_commit(v_empty(vr.idx));
+                }
+                vr.next(kVStages);
+            };
+            if (!wait_all(q_full, q_use & 1u)) break;
+            s_mma(0);
+            if (ok) dp_mma(0);
+            if (ok && n > 1) s_mma(1);
+            for (int j = 0; j < n && ok; ++j) {
+                if (!wait_all(ds_full, ds_use & 1u)) break;
+                ++ds_use;
+                if (j + 1 < n) dp_mma(j + 1);
+                if (!ok) break;
+                if (j == 0 && q_use > 0 && !wait_all(dq_empty, (q_use - 1u) & 1u)) break;  // the last item's dQ is read
+                if (leader) {
+                    const int steps = min(8, (keys - 128 * j + 15) / 16);
+                    const uint64_t b = sw128_desc(k_smem(kq.idx), kBox, 1024);
+                    const uint32_t a = tmem + (j & 1) * 128;  // dS: 64 keys a half, the second 64 columns on
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        if (kk < steps)
+                            mma_ts(tDQ, a + (kk >> 2) * 64 + (kk & 3) * 8, b + (uint64_t)kk * 128, P.idesc_q, (j > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(k_empty(kq.idx));
+                    if (j == n - 1) {
+                        mma_commit(dq_full);
+                        mma_commit(q_empty);
+                    }
+                }
+                kq.next(kKStages);
+                if (j + 2 < n) s_mma(j + 2);
+            }
+            ++q_use;
+        }
+        if (!ok && leader) *abort_flag = 1;
+        if (leader) mma_commit(drain);
+        wait_bar_drain(drain, 0);
+        __syncwarp();
+    } else if (warp < 8) {
+        // ------------------------------------------------------------ dS, and dQ to memory
+        const int half = warp / 4, r = warp % 4 * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(warp % 4 * 32) << 16;
+        const int tok_r = (int)P.t.fd_hp.div((uint32_t)r), head_r = r - tok_r * P.t.hp;
+        const bool wide = p.D % 16 == 0 && (reinterpret_cast<uintptr_t>(p.dq) & 31) == 0;
+        const float f = P.scale_log2e;
+        Item<1> it;
+        uint32_t s_use[2] = {0u, 0u}, dp_use = 0, dq_use = 0;
+        while (ok && next_item(it)) {
+            const int keys = it.keys[0], n = (keys + 127) / 128;
+            const bool row = r < it.rows[0];
+            const long long tok = it.q0 + it.tok[0] + tok_r, head = it.head[0] + head_r;
+            const long long at = head * p.total_q + tok, row0 = (tok * p.Hq + head) * p.D;
+            const int limit = it.tok[0] + tok_r + it.shift, first = it.tok[0] + it.shift;
+            float nl = 0.f, delta = 0.f;
+            if (row) {
+                nl = -p.lse[at] * tc::kLog2e;
+                const uint4* a = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.out) + row0);
+                const uint4* b = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.d_out) + row0);
+                float2 s = make_float2(0.f, 0.f);
+#pragma unroll 4
+                for (int c = 0; c < p.D / 8; ++c) {
+                    const uint4 x = a[c], y = b[c];
+                    s = __ffma2_rn(unpack2<BF16>(x.x), unpack2<BF16>(y.x), s);
+                    s = __ffma2_rn(unpack2<BF16>(x.y), unpack2<BF16>(y.y), s);
+                    s = __ffma2_rn(unpack2<BF16>(x.z), unpack2<BF16>(y.z), s);
+                    s = __ffma2_rn(unpack2<BF16>(x.w), unpack2<BF16>(y.w), s);
+                }
+                delta = s.x + s.y;
+                if (half == 0) p.delta[at] = delta;
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                const int b = j & 1;
+                const uint32_t sA = tmem + lane_off + 128u * b + 64u * half, dpA = tDP + lane_off + 64u * half;
+                const bool edge = 128 * j + 127 > first;  // some row does not see every key
+                uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) see[i] = low_bits(limit - 128 * j - 64 * half - 32 * i + 1);
+                }
+                const uint32_t use = b ? s_use[1]++ : s_use[0]++;
+                ok = __all_sync(0xffffffffu, wait(s_full(b), use & 1u, abort_flag, p.status));
+                if (!ok) break;
+                tc_fence_after();
+                float pr[64];
+                {
+                    uint32_t sr[64];
+                    tmem_ld_x64(sA, sr);
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) {
+                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), make_float2(f, f),
+                                                    make_float2(nl, nl));
+                        pr[c] = ex2(y.x);
+                        pr[c + 1] = ex2(y.y);
+                    }
+                }
+                ok = __all_sync(0xffffffffu, wait(dp_full, dp_use & 1u, abort_flag, p.status));
+                if (!ok) break;
+                ++dp_use;
+                tc_fence_after();
+                uint32_t pk[32];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t dr[32];
+                    tmem_ld_x32(dpA + 32 * i, dr);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        float2 x = __fadd2_rn(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), make_float2(-delta, -delta));
+                        x = __fmul2_rn(x, make_float2(pr[32 * i + c], pr[32 * i + c + 1]));
+                        if (edge) {
+                            x.x = (see[i] >> c) & 1u ? x.x : 0.f;
+                            x.y = (see[i] >> (c + 1)) & 1u ? x.y : 0.f;
+                        }
+                        pk[16 * i + c / 2] = pack2<BF16>(x.x, x.y);
+                    }
+                }
+                tmem_st_x32(sA, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ds_full);
+            }
+            if (!ok) break;
+            if (n > 0) {
+                ok = __all_sync(0xffffffffu, wait(dq_full, dq_use & 1u, abort_flag, p.status));
+                if (!ok) break;
+                ++dq_use;
+                tc_fence_after();
+            }
+            uint16_t* to = static_cast<uint16_t*>(p.dq) + row0;
+#pragma unroll 1
+            for (int c = half * 32 * NB; c < (half + 1) * 32 * NB; c += 32) {
+                uint32_t o[32];
+                if (n > 0) tmem_ld_x32(tDQ + lane_off + c, o);
+                if (n > 0 && c + 32 >= (half + 1) * 32 * NB) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(dq_empty);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 16) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        w[k] = n > 0 ? pack2<BF16>(__uint_as_float(o[e + 2 * k]) * p.scale, __uint_as_float(o[e + 2 * k + 1]) * p.scale) : 0u;
+                    if (row && c + e + 16 <= p.D) {
+                        if (wide) {
+                            store32(to + c + e, w);
+                        } else {
+                            *reinterpret_cast<uint4*>(to + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4*>(to + c + e + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
+                    } else if (row && c + e + 8 <= p.D) {
+                        *reinterpret_cast<uint4*>(to + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+        if (!ok) *abort_flag = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
+}
+
+template <bool BF16, int NB>
+cudaError_t start(const DqParams& P, unsigned grid, cudaStream_t stream) {
+    auto kern = prompt_dq_kernel<BF16, NB>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<NB>::kTotal);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kWarps * 32, Smem<NB>::kTotal, stream>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_dq(const PromptParams& p, cudaStream_t stream) {
+    DqParams P;
+    P.p = p;
+    P.t = make_tiles(p);
+    const bool bf16 = p.dtype == TA_BF16;
+    P.idesc_s = make_idesc(bf16, 0, 0, 0);  // (N is set for each product)
+    P.idesc_q = make_idesc(bf16, (uint32_t)(p.D + 15) / 16 * 16, 0, 1);
+    P.ksteps = (p.D + 15) / 16;
+    P.scale_log2e = p.scale * kToLog2;
+    if (!make_rows_map(&P.tm_q, bf16, p.q, p.D, p.Hq, p.total_q, p.q_rs, P.t.hp, P.t.tq) ||
+        !make_rows_map(&P.tm_do, bf16, p.d_out, p.D, p.Hq, p.total_q, (long long)p.Hq * p.D, P.t.hp, P.t.tq) ||
+        !make_rows_map(&P.tm_k, bf16, p.k, p.D, p.Hk, p.total_k, p.k_rs, 1, 128) ||
+        !make_rows_map(&P.tm_v, bf16, p.v, p.D, p.Hk, p.total_k, p.v_rs, 1, 128))
+        return cudaErrorInvalidValue;
+    const long long items = most_items(p, P.t, 1);
+    if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (p.D <= 64) return bf16 ? start<true, 1>(P, (unsigned)items, stream) : start<false, 1>(P, (unsigned)items, stream);
+    return bf16 ? start<true, 2>(P, (unsigned)items, stream) : start<false, 2>(P, (unsigned)items, stream);
+}
+
+}  // namespace prompt
+}  // namespace triattn

@@ -22,62 +22,32 @@
 // Items go by falling cost (the number of key tiles), one at a time to the CTA that has finished its own: the grid has a
 // block for every item, and a running CTA takes the next block's place by clusterlaunchcontrol.try_cancel, so no
 // counter in memory has to be zeroed and the tail is as short as one item.
-#include "prompt.cuh"
-#include "tc_kernel.cuh"
+#include "prompt_tc.cuh"
 
 namespace triattn {
 namespace prompt {
 namespace {
 
-using namespace tc;
-
 struct FwdParams {
     CUtensorMap tm_q, tm_k, tm_v;
     PromptParams p;
-    int hp, tq, ng;            // heads and tokens of a tile; tiles of the same tokens (G / hp)
-    FastDiv fd_hp, fd_hk;
+    Tiles t;
     uint32_t idesc_qk, idesc_pv;
     int ksteps;                // D / 16, rounded up
     float scale_log2e;         // |scale| log2 e
     int negative;              // scale < 0: the logits change their sign
 };
 
-// wait_bar inline: a call keeps the compiler from giving the softmax warps the registers that setmaxnreg gives them.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-    if (mbar_test(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 63) == 0) {
-            if (*abort_flag) return false;
-            if (clock64() - t0 > kTimeoutCycles) {
-                *abort_flag = 1;
-                atomicCAS(status, 0, kStatusTimeout);
-                return false;
-            }
-        }
-    }
-}
-
 constexpr int kRing = 2;       // items known ahead
 constexpr int kWarps = 16;
 constexpr int kConsumers = 14; // warps that read an item: 8 softmax, 4 epilogue, MMA, TMA
-
-struct alignas(16) Item {
-    int on;                    // 0: the end
-    int q0, k0, lq, shift;     // the sequence: first packed rows, queries, and how many more keys than queries it has
-    int h;                     // key head
-    int tok[2], head[2];       // of each tile: first token (of the sequence), first query head
-    int keys[2];               // keys that some row of the tile sees
-    int rows[2];               // rows that exist (0: no tile)
-};
 
 template <int NB>
 struct Smem {
     static constexpr uint32_t kTile = NB * kBox;                       // 128 rows
     static constexpr int kStages = NB == 1 ? 8 : 4;
     static constexpr uint32_t kQ = 0, kKV = 2 * kTile, kMl = kKV + kStages * kTile;  // (m, l) of the rows
-    static constexpr uint32_t kItems = kMl + 2 * 128 * 8, kClc = kItems + kRing * sizeof(Item);
+    static constexpr uint32_t kItems = kMl + 2 * 128 * 8, kClc = kItems + kRing * sizeof(Item<2>);
     static constexpr uint32_t kBars = kClc + 16;
     static constexpr int kNumBars = 2 * 2 + 2 * kStages + 5 * 2 + 2 * 2 + 2 * kRing + 2;
     static constexpr uint32_t kSlot = kBars + 8 * kNumBars, kAbort = kSlot + 4, kTotal = kAbort + 4 + 1024;
@@ -108,129 +78,6 @@ __device__ __forceinline__ void tmem_ld_2x64(uint32_t ta, uint32_t (&r)[128]) {
         : "r"(ta), "r"(ta + 64u));
 }
 
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-
-// The next block's place in the grid, or -1 (none is left): asks (one thread), and reads the answer.
-__device__ __forceinline__ void clc_ask(uint32_t to, uint32_t bar) {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    mbar_expect_tx(bar, 16);
-    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to),
-                 "r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ int clc_answer(uint32_t at) {
-    int x;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\t"
-        "ld.shared.b128 r, [%1];\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
-        "mov.b32 %0, -1;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, r;\n\t}"
-        : "=r"(x)
-        : "r"(at)
-        : "memory");
-    return x;
-}
-
-// The order of the items (one warp): by the key tiles of their second tile, most first; of those with as many by
-// sequence, then tile pair, then head.
-struct Order {
-    int level;                 // key tiles
-    long long base;            // items of the levels before
-    long long here;            // items of this level
-};
-// Pairs of a sequence that end within n key tiles.
-__device__ __forceinline__ int pairs_upto(const FwdParams& P, const Seq& q, int n) {
-    const int tiles = (q.lq + P.tq - 1) / P.tq * P.ng, pairs = (tiles + 1) / 2;
-    if (n < 0) return 0;
-    if (q.lk <= 128LL * n) return pairs;
-    const int x = 128 * n - q.shift;                   // tokens (of the sequence) whose last key lies there
-    return x <= 0 ? 0 : (int)((long long)(x / P.tq) * P.ng / 2);
-}
-__device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
-__device__ __forceinline__ long long level_items(const FwdParams& P, int n) {
-    const int lane = threadIdx.x % 32;
-    long long sum = 0;
-    for (int s0 = 0; s0 < P.p.num_seqs; s0 += 32) {
-        int c = 0;
-        if (s0 + lane < P.p.num_seqs) {
-            const Seq q = load_seq(P.p, s0 + lane, false);
-            c = pairs_upto(P, q, n) - pairs_upto(P, q, n - 1);
-        }
-        sum += warp_sum(c);
-    }
-    return sum * P.p.Hk;
-}
-__device__ __forceinline__ Order order_begin(const FwdParams& P) {
-    int most = 0;
-    for (int s = threadIdx.x % 32; s < P.p.num_seqs; s += 32) {
-        const Seq q = load_seq(P.p, s, blockIdx.x == 0);
-        if (q.lq > 0) most = max(most, (q.lk + 127) / 128);
-    }
-    Order o;
-    o.level = __reduce_max_sync(0xffffffffu, most);
-    o.base = 0;
-    o.here = level_items(P, o.level);
-    return o;
-}
-// Item `at` (never an earlier one than before): false past the last.
-__device__ __forceinline__ bool order_item(const FwdParams& P, Order& o, long long at, Item& it) {
-    while (at >= o.base + o.here) {
-        o.base += o.here;
-        if (--o.level < 0) return false;
-        o.here = level_items(P, o.level);
-    }
-    const int lane = threadIdx.x % 32;
-    const int rank = (int)(at - o.base);
-    int pair = (int)P.fd_hk.div((uint32_t)rank);
-    it.h = rank - pair * P.p.Hk;
-    for (int s0 = 0; s0 < P.p.num_seqs; s0 += 32) {
-        Seq q{};
-        int c = 0, first = 0;
-        if (s0 + lane < P.p.num_seqs) {
-            q = load_seq(P.p, s0 + lane, false);
-            first = pairs_upto(P, q, o.level - 1);
-            c = pairs_upto(P, q, o.level) - first;
-        }
-        int upto = c;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += x;
-        }
-        const uint32_t has = __ballot_sync(0xffffffffu, pair < upto);
-        if (!has) {
-            pair -= __shfl_sync(0xffffffffu, upto, 31);
-            continue;
-        }
-        const int l = __ffs((int)has) - 1;
-        auto get = [&](int x) { return __shfl_sync(0xffffffffu, x, l); };
-        const int t0 = 2 * get(first + pair - (upto - c));
-        it.on = 1;
-        it.q0 = get(q.q0);
-        it.k0 = get(q.k0);
-        it.lq = get(q.lq);
-        it.shift = get(q.shift);
-        const int blocks = (it.lq + P.tq - 1) / P.tq;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = t0 + i, b = t / P.ng;
-            const bool there = b < blocks;
-            it.tok[i] = b * P.tq;
-            it.head[i] = it.h * P.p.G + (t - b * P.ng) * P.hp;
-            const int tokens = there ? min(P.tq, it.lq - it.tok[i]) : 0;
-            it.rows[i] = tokens * P.hp;
-            it.keys[i] = there ? max(0, it.tok[i] + tokens + it.shift) : 0;
-        }
-        return true;
-    }
-    return false;
-}
-
 template <bool BF16, int NB>
 __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid_constant__ FwdParams P) {
     using M = Smem<NB>;
@@ -243,7 +90,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(g0 + M::kAbort);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(g0 + M::kSlot);
-    Item* items = reinterpret_cast<Item*>(g0 + M::kItems);
+    Item<2>* items = reinterpret_cast<Item<2>*>(g0 + M::kItems);
     float2* ml = reinterpret_cast<float2*>(g0 + M::kMl);
     auto bar = [&](int i) { return base + M::kBars + 8u * (uint32_t)i; };
     auto q_full = [&](int i) { return bar(i); };
@@ -292,8 +139,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // Rows of Q that no box fills (tq hp < 128) stay zeros.
-    for (int e = threadIdx.x; e < 2 * NB * (128 - P.tq * P.hp) * 8; e += kWarps * 32) {
-        const int c = e % 8, r = e / 8 % (128 - P.tq * P.hp) + P.tq * P.hp, b = e / 8 / (128 - P.tq * P.hp);
+    for (int e = threadIdx.x; e < 2 * NB * (128 - P.t.tq * P.t.hp) * 8; e += kWarps * 32) {
+        const int c = e % 8, r = e / 8 % (128 - P.t.tq * P.t.hp) + P.t.tq * P.t.hp, b = e / 8 / (128 - P.t.tq * P.t.hp);
         st_shared_v4(base + M::kQ + (uint32_t)b * kBox + (uint32_t)r * 128u + c * 16u, 0u, 0u, 0u, 0u);
     }
     fence_async_shared();
@@ -309,7 +156,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
     bool ok = true;
     int item_n = 0;            // items so far
     // The next item, for the warps that consume them: false at the end.
-    auto next_item = [&](Item& it) -> bool {
+    auto next_item = [&](Item<2>& it) -> bool {
         const int r = item_n % kRing;
         ok = __all_sync(0xffffffffu, wait(it_full(r), (uint32_t)(item_n / kRing) & 1u, abort_flag, p.status));
         if (!ok) return false;
@@ -325,37 +172,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 14) {
             // ------------------------------------------------------------ the items
-            Order o = order_begin(P);
-            int at = (int)blockIdx.x;
-            uint32_t asked = 0;
-            for (;;) {
-                Item it{};
-                if (at < 0 || !order_item(P, o, at, it)) it.on = 0;
-                const int r = item_n % kRing;
-                if (item_n >= kRing)
-                    ok = __all_sync(0xffffffffu, wait(it_empty(r), (uint32_t)(item_n / kRing - 1) & 1u, abort_flag, p.status));
-                if (!ok) break;
-                if (lane == 0) {
-                    items[r] = it;
-                    mbar_arrive(it_full(r));
-                }
-                ++item_n;
-                if (!it.on) break;
-                if (lane == 0) clc_ask(base + M::kClc, clc);
-                // (awaited whatever happens: the answer is written into this block's memory)
-                ok = __all_sync(0xffffffffu, wait_bar_drain(clc, asked & 1u));
-                if (!ok) break;
-                ++asked;
-                at = clc_answer(base + M::kClc);
-                __syncwarp();
-            }
+            ok = hand_out<2, kRing>(p, P.t, items, it_full, it_empty, base + M::kClc, clc, abort_flag);
             if (!ok) *abort_flag = 1;
         } else if (warp == 13) {
             // ------------------------------------------------------------ TMA
             StageRing kr = {0, 0u, false};
-            Item it;
+            Item<2> it;
             uint32_t q_use[2] = {0u, 0u};
-            const uint32_t q_bytes = (uint32_t)(P.tq * P.hp) * 128u * NB;
+            const uint32_t q_bytes = (uint32_t)(P.t.tq * P.t.hp) * 128u * NB;
             while (ok && next_item(it)) {
                 const int n = (max(it.keys[0], it.keys[1]) + 127) / 128;
                 auto load_q = [&](int i) {
@@ -391,7 +215,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
             // ------------------------------------------------------------ MMA
             const bool leader = elect_one();
             StageRing kr = {0, 0u, false};
-            Item it;
+            Item<2> it;
             uint32_t q_use[2] = {0u, 0u}, p_use[2] = {0u, 0u}, o_use[2] = {0u, 0u};
             while (ok && next_item(it)) {
                 const int n0 = (it.keys[0] + 127) / 128, n1 = (it.keys[1] + 127) / 128, n = max(n0, n1);
@@ -467,14 +291,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
                     wait_kv(vst);
                     if (!ok) break;
                     const int valid = lk - 128 * (j - 1);  // rows of V that are the sequence's
-                    if (valid < 128 && (valid & 15)) {
-                        const int zeros = 16 - (valid & 15);
-                        for (int e = lane; e < zeros * 8 * NB; e += 32)
-                            st_shared_v4(kv_smem(vst.idx) + (uint32_t)(e / 8 / zeros) * kBox +
-                                             (uint32_t)(valid + e / 8 % zeros) * 128u + (e % 8) * 16u, 0u, 0u, 0u, 0u);
-                        fence_async_shared();
-                        __syncwarp();
-                    }
+                    if (valid < 128) clear_rows<NB>(kv_smem(vst.idx), valid, (valid + 15) & ~15);
                     bool k_here = false;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -505,9 +322,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
         const int i = warp / 4, r = warp % 4 * 32 + lane;
         const uint32_t lane_off = (uint32_t)(warp % 4 * 32) << 16;
         const uint32_t st = tmem + lane_off + i * 128, ot = tmem + lane_off + 256u + (uint32_t)i * kOCols;
-        const int tok_r = (int)P.fd_hp.div((uint32_t)r);
+        const int tok_r = (int)P.t.fd_hp.div((uint32_t)r);
         const float f = P.scale_log2e, step = kRescaleLog2 / f;
-        Item it;
+        Item<2> it;
         uint32_t s_use = 0, ml_use = 0;
         while (ok && next_item(it)) {
             const int keys = i == 0 ? it.keys[0] : it.keys[1], tok = (i == 0 ? it.tok[0] : it.tok[1]) + tok_r;
@@ -602,9 +419,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
         // ------------------------------------------------------------ epilogue
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int wq = warp % 4, r = wq * 32 + lane;
-        const int tok_r = (int)P.fd_hp.div((uint32_t)r), head_r = r - tok_r * P.hp;
+        const int tok_r = (int)P.t.fd_hp.div((uint32_t)r), head_r = r - tok_r * P.t.hp;
         const bool wide = p.D % 16 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;  // rows in 32-byte pieces
-        Item it;
+        Item<2> it;
         uint32_t ml_use = 0, o_use[2] = {0u, 0u};
         while (ok && next_item(it)) {
 #pragma unroll
@@ -685,11 +502,16 @@ cudaError_t start(const FwdParams& P, unsigned grid, cudaStream_t stream) {
 
 // Heads of a tile: the divisor of the group that fills most of 128 rows, the largest of those (fewer keys past the
 // causal border).
-void tile_shape(int G, int& hp, int& tq) {
-    hp = 1;
-    for (int d = 1; d <= G && d <= 128; ++d)
-        if (G % d == 0 && 128 / d * d >= 128 / hp * hp) hp = d;
-    tq = 128 / hp;
+Tiles make_tiles(const PromptParams& p) {
+    Tiles t;
+    t.hp = 1;
+    for (int d = 1; d <= p.G && d <= 128; ++d)
+        if (p.G % d == 0 && 128 / d * d >= 128 / t.hp * t.hp) t.hp = d;
+    t.tq = 128 / t.hp;
+    t.ng = p.G / t.hp;
+    t.fd_hp = make_fastdiv((uint32_t)t.hp);
+    t.fd_hk = make_fastdiv((uint32_t)p.Hk);
+    return t;
 }
 
 }  // namespace prompt
@@ -698,29 +520,19 @@ cudaError_t launch_prompt_tc_fwd(const PromptParams& p, cudaStream_t stream) {
     using namespace prompt;
     FwdParams P;
     P.p = p;
-    tile_shape(p.G, P.hp, P.tq);
-    P.ng = p.G / P.hp;
-    P.fd_hp = tc::make_fastdiv((uint32_t)P.hp);
-    P.fd_hk = tc::make_fastdiv((uint32_t)p.Hk);
+    P.t = make_tiles(p);
     const bool bf16 = p.dtype == TA_BF16;
-    const uint32_t ab = bf16 ? 1u : 0u, npv = (uint32_t)(p.D + 15) / 16 * 16;
-    P.idesc_qk = (1u << 4) | (ab << 7) | (ab << 10) | (8u << 24);  // (N is set for each product)
-    P.idesc_pv = (1u << 4) | (ab << 7) | (ab << 10) | (1u << 16) | ((npv >> 3) << 17) | (8u << 24);
+    P.idesc_qk = make_idesc(bf16, 0, 0, 0);  // (N is set for each product)
+    P.idesc_pv = make_idesc(bf16, (uint32_t)(p.D + 15) / 16 * 16, 0, 1);
     P.ksteps = (p.D + 15) / 16;
     // (a scale of 0 makes every logit 0: so does one far below the least that counts, and a hidden key's -inf stays)
     P.scale_log2e = fmaxf(fabsf(p.scale) * kToLog2, 1e-30f);
     P.negative = p.scale < 0.f;
-    const CUtensorMapDataType dt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    const uint64_t D = (uint64_t)p.D;
-    if (!tc::encode_map_3d(&P.tm_q, dt, p.q, D, p.Hq, p.total_q, D * 2, p.q_rs * 2, 64, P.hp, P.tq, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !tc::encode_map_3d(&P.tm_k, dt, p.k, D, p.Hk, p.total_k, D * 2, p.k_rs * 2, 64, 1, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !tc::encode_map_3d(&P.tm_v, dt, p.v, D, p.Hk, p.total_k, D * 2, p.v_rs * 2, 64, 1, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!make_rows_map(&P.tm_q, bf16, p.q, p.D, p.Hq, p.total_q, p.q_rs, P.t.hp, P.t.tq) ||
+        !make_rows_map(&P.tm_k, bf16, p.k, p.D, p.Hk, p.total_k, p.k_rs, 1, 128) ||
+        !make_rows_map(&P.tm_v, bf16, p.v, p.D, p.Hk, p.total_k, p.v_rs, 1, 128))
         return cudaErrorInvalidValue;
-    // A block for each item that there can be: a sequence has ceil(ceil(lq / tq) ng / 2) pairs of tiles, at most
-    // lq ng / (2 tq) + ng / 2 + 1, and no more than the longest has.
-    const long long longest = (((long long)p.max_q + P.tq - 1) / P.tq * P.ng + 1) / 2;
-    const long long sum = (long long)p.total_q * P.ng / (2 * P.tq) + (long long)p.num_seqs * (P.ng / 2 + 1) + 1;
-    const long long items = (longest * p.num_seqs < sum ? longest * p.num_seqs : sum) * p.Hk;
+    const long long items = most_items(p, P.t, 2);
     if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const unsigned grid = (unsigned)items;
     if (p.D <= 64) return bf16 ? start<true, 1>(P, grid, stream) : start<false, 1>(P, grid, stream);

@@ -1,5 +1,5 @@
 // prompt_simt.cu -- causal attention of packed prompts with grouped heads, forward and backward, on CUDA cores in exact
-// fp32: fp32 inputs, and 16-bit ones with D > 128; and the per-row sums dO . O of both backward forms.
+// fp32: fp32 inputs, and 16-bit ones with D > 128.
 //
 // Tiles of BM rows (tokens x grouped heads, prompt.cuh) and 64 keys in shared memory as fp32, 256 threads.  A thread forms
 // a BM / 16 x 4 piece of the logits from vectors of four columns (16 FMAs for two shared loads) and holds as many rows of
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_simt(const PromptParams p,
     }
 }
 
-// Sixteen lanes a row of (t, h).  The tensor-core form's fp32 sums begin with zeros.
+// Sixteen lanes a row of (t, h).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) prompt_delta_kernel(const PromptParams p) {
     constexpr int kV = Vec<T>::n;
@@ -370,14 +370,6 @@ __global__ void __launch_bounds__(kThreads) prompt_delta_kernel(const PromptPara
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (in && lane == 0) p.delta[(r % p.Hq) * p.total_q + r / p.Hq] = sum;
-    if (p.dq_acc) {
-        for (int d = lane * 4; in && d < p.D; d += 64) *reinterpret_cast<float4*>(p.dq_acc + r * p.D + d) = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    if (p.dk_acc) {  // (both sums, one after the other)
-        const long long n = 2LL * p.total_k * p.Hk * p.D / 4, all = (long long)gridDim.x * kThreads;
-        for (long long e = (long long)blockIdx.x * kThreads + threadIdx.x; e < n; e += all)
-            reinterpret_cast<float4*>(p.dk_acc)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
 }
 
 cudaError_t grid_of(const PromptParams& p, long long tiles, unsigned& grid) {
@@ -402,6 +394,17 @@ template <typename T, int NC>
 cudaError_t forward(const PromptParams& p, cudaStream_t stream) {
     const long long tiles = ((long long)p.max_q * p.G + 63) / 64;
     return start(prompt_fwd_simt<T, NC>, p, tiles, (size_t)3 * 64 * (64 * NC + 4), stream);
+}
+
+cudaError_t launch_delta(const PromptParams& p, cudaStream_t stream) {
+    const long long n = ((long long)p.total_q * p.Hq + 15) / 16;
+    if (n > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    switch (p.dtype) {
+    case TA_F32: prompt_delta_kernel<float><<<(unsigned)n, kThreads, 0, stream>>>(p); break;
+    case TA_F16: prompt_delta_kernel<__half><<<(unsigned)n, kThreads, 0, stream>>>(p); break;
+    default: prompt_delta_kernel<__nv_bfloat16><<<(unsigned)n, kThreads, 0, stream>>>(p); break;
+    }
+    return cudaGetLastError();
 }
 
 template <typename T, int NC>
@@ -431,18 +434,6 @@ cudaError_t launch_any(const PromptParams& p, bool back, cudaStream_t stream) {
 }
 
 }  // namespace
-
-cudaError_t launch_delta(const PromptParams& p, cudaStream_t stream) {
-    const long long n = ((long long)p.total_q * p.Hq + 15) / 16;
-    if (n > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    switch (p.dtype) {
-    case TA_F32: prompt_delta_kernel<float><<<(unsigned)n, kThreads, 0, stream>>>(p); break;
-    case TA_F16: prompt_delta_kernel<__half><<<(unsigned)n, kThreads, 0, stream>>>(p); break;
-    default: prompt_delta_kernel<__nv_bfloat16><<<(unsigned)n, kThreads, 0, stream>>>(p); break;
-    }
-    return cudaGetLastError();
-}
-
 }  // namespace prompt
 
 cudaError_t launch_prompt_simt_fwd(const PromptParams& p, cudaStream_t stream) { return prompt::launch_any(p, false, stream); }

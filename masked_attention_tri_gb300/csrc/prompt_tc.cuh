@@ -1,0 +1,231 @@
+// prompt_tc.cuh -- what the tensor-core kernels of prompt attention share: tiles of rows, the order in which CTAs take them,
+// bounded waits.
+#pragma once
+
+#include "prompt.cuh"
+#include "tc_kernel.cuh"
+
+namespace triattn {
+namespace prompt {
+
+using namespace tc;
+
+// Tiles of rows: tq tokens x hp heads of a group, ng tiles of the same tokens (G / hp).
+struct Tiles {
+    int hp, tq, ng;
+    FastDiv fd_hp, fd_hk;
+};
+Tiles make_tiles(const PromptParams& p);
+
+// wait_bar inline: a call keeps the compiler from giving a kernel's warps the registers that setmaxnreg gives them.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    if (mbar_test(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63) == 0) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > kTimeoutCycles) {
+                *abort_flag = 1;
+                atomicCAS(status, 0, kStatusTimeout);
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// An item: PER tiles of one (sequence, key head).
+template <int PER>
+struct alignas(16) Item {
+    int on;                    // 0: the end
+    int q0, k0, lq, shift;     // the sequence: first packed rows, queries, and how many more keys than queries it has
+    int h;                     // key head
+    int tok[PER], head[PER];     // of each tile: first token (of the sequence), first query head
+    int keys[PER];             // keys that some row of the tile sees
+    int rows[PER];             // rows that exist (0: no tile)
+};
+
+// The next block's place in the grid, or -1 (none is left): asks (one thread), and reads the answer.
+__device__ __forceinline__ void clc_ask(uint32_t to, uint32_t bar) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    mbar_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to),
+                 "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ int clc_answer(uint32_t at) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 r, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "mov.b32 %0, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, r;\n\t}"
+        : "=r"(x)
+        : "r"(at)
+        : "memory");
+    return x;
+}
+
+// The order of the items of PER tiles each (one warp): by the key tiles of their last tile, most first; of those with as many
+// by sequence, then place, then head.
+struct Order {
+    int level;                 // key tiles
+    long long base;            // items of the levels before
+    long long here;            // items of this level
+};
+// Items of a sequence that end within n key tiles.
+template <int PER>
+__device__ __forceinline__ int items_upto(const Tiles& T, const Seq& q, int n) {
+    const int tiles = (q.lq + T.tq - 1) / T.tq * T.ng;
+    if (n < 0) return 0;
+    if (q.lk <= 128LL * n) return (tiles + PER - 1) / PER;
+    const int x = 128 * n - q.shift;                   // tokens (of the sequence) whose last key lies there
+    return x <= 0 ? 0 : (int)((long long)(x / T.tq) * T.ng / PER);
+}
+template <int PER>
+__device__ __forceinline__ long long level_items(const PromptParams& p, const Tiles& T, int n) {
+    const int lane = threadIdx.x % 32;
+    long long sum = 0;
+    for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+        int c = 0;
+        if (s0 + lane < p.num_seqs) {
+            const Seq q = load_seq(p, s0 + lane, false);
+            c = items_upto<PER>(T, q, n) - items_upto<PER>(T, q, n - 1);
+        }
+        sum += __reduce_add_sync(0xffffffffu, c);
+    }
+    return sum * p.Hk;
+}
+template <int PER>
+__device__ __forceinline__ Order order_begin(const PromptParams& p, const Tiles& T) {
+    int most = 0;
+    for (int s = threadIdx.x % 32; s < p.num_seqs; s += 32) {
+        const Seq q = load_seq(p, s, blockIdx.x == 0);
+        if (q.lq > 0) most = max(most, (q.lk + 127) / 128);
+    }
+    Order o;
+    o.level = __reduce_max_sync(0xffffffffu, most);
+    o.base = 0;
+    o.here = level_items<PER>(p, T, o.level);
+    return o;
+}
+// Item `at` (never an earlier one than before): false past the last.
+template <int PER>
+__device__ __forceinline__ bool order_item(const PromptParams& p, const Tiles& T, Order& o, long long at, Item<PER>& it) {
+    while (at >= o.base + o.here) {
+        o.base += o.here;
+        if (--o.level < 0) return false;
+        o.here = level_items<PER>(p, T, o.level);
+    }
+    const int lane = threadIdx.x % 32;
+    const int rank = (int)(at - o.base);
+    int place = (int)T.fd_hk.div((uint32_t)rank);
+    it.h = rank - place * p.Hk;
+    for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+        Seq q{};
+        int c = 0, first = 0;
+        if (s0 + lane < p.num_seqs) {
+            q = load_seq(p, s0 + lane, false);
+            first = items_upto<PER>(T, q, o.level - 1);
+            c = items_upto<PER>(T, q, o.level) - first;
+        }
+        int upto = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += x;
+        }
+        const uint32_t has = __ballot_sync(0xffffffffu, place < upto);
+        if (!has) {
+            place -= __shfl_sync(0xffffffffu, upto, 31);
+            continue;
+        }
+        const int l = __ffs((int)has) - 1;
+        auto get = [&](int x) { return __shfl_sync(0xffffffffu, x, l); };
+        const int t0 = PER * get(first + place - (upto - c));
+        it.on = 1;
+        it.q0 = get(q.q0);
+        it.k0 = get(q.k0);
+        it.lq = get(q.lq);
+        it.shift = get(q.shift);
+        const int blocks = (it.lq + T.tq - 1) / T.tq;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int t = t0 + i, b = t / T.ng;
+            const bool there = b < blocks;
+            it.tok[i] = b * T.tq;
+            it.head[i] = it.h * p.G + (t - b * T.ng) * T.hp;
+            const int tokens = there ? min(T.tq, it.lq - it.tok[i]) : 0;
+            it.rows[i] = tokens * T.hp;
+            it.keys[i] = there ? max(0, it.tok[i] + tokens + it.shift) : 0;
+        }
+        return true;
+    }
+    return false;
+}
+// The warp that hands the items to `consumers` warps through a ring of R: items in shared memory, barriers full(r) (1) and
+// empty(r) (consumers), the answer's place and barrier.  False after a wait that ran out.
+template <int PER, int R, typename Full, typename Empty>
+__device__ __forceinline__ bool hand_out(const PromptParams& p, const Tiles& T, Item<PER>* items, Full full, Empty empty,
+                                         uint32_t clc_at, uint32_t clc_bar, volatile int* abort_flag) {
+    const int lane = threadIdx.x % 32;
+    Order o = order_begin<PER>(p, T);
+    int at = (int)blockIdx.x;
+    for (int n = 0;; ++n) {
+        Item<PER> it{};
+        if (at < 0 || !order_item<PER>(p, T, o, at, it)) it.on = 0;
+        const int r = n % R;
+        if (n >= R && !__all_sync(0xffffffffu, wait(empty(r), (uint32_t)(n / R - 1) & 1u, abort_flag, p.status))) return false;
+        if (lane == 0) {
+            items[r] = it;
+            mbar_arrive(full(r));
+        }
+        if (!it.on) return true;
+        if (lane == 0) clc_ask(clc_at, clc_bar);
+        // (awaited whatever happens: the answer is written into this block's memory)
+        if (!__all_sync(0xffffffffu, wait_bar_drain(clc_bar, (uint32_t)n & 1u))) return false;
+        at = clc_answer(clc_at);
+        __syncwarp();
+    }
+}
+// Blocks of the grid: one for each item that there can be.  A sequence has ceil(ceil(lq / tq) ng / PER) items, at most
+// lq ng / (PER tq) + (ng + PER - 1) / PER, and no more than the longest has.
+inline long long most_items(const PromptParams& p, const Tiles& T, int PER) {
+    const long long longest = (((long long)p.max_q + T.tq - 1) / T.tq * T.ng + PER - 1) / PER;
+    const long long sum = (long long)p.total_q * T.ng / (PER * T.tq) + (long long)p.num_seqs * ((T.ng + PER - 1) / PER) + 1;
+    return (longest * p.num_seqs < sum ? longest * p.num_seqs : sum) * p.Hk;
+}
+
+// Zeros into rows [from, to) of a tile of NB boxes (a warp), for the async proxy to read.
+template <int NB>
+__device__ __forceinline__ void clear_rows(uint32_t tile, int from, int to) {
+    const int n = to - from;
+    if (n <= 0) return;
+    for (int e = threadIdx.x % 32; e < n * 8 * NB; e += 32)
+        st_shared_v4(tile + (uint32_t)(e / 8 / n) * kBox + (uint32_t)(from + e / 8 % n) * 128u + (e % 8) * 16u, 0u, 0u, 0u, 0u);
+    fence_async_shared();
+    __syncwarp();
+}
+
+// Instruction descriptors (tc_bwd.cu has the fields); N may be left out and added later.
+inline uint32_t make_idesc(bool bf16, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
+    const uint32_t ab = bf16 ? 1u : 0u;
+    return (1u << 4) | (ab << 7) | (ab << 10) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | (8u << 24);
+}
+// A map of packed rows (total, heads, D): boxes of 64 columns x heads x tokens.
+inline bool make_rows_map(CUtensorMap* m, bool bf16, const void* ptr, int D, int heads, int total, long long rs, int box_heads,
+                          int box_rows) {
+    return encode_map_3d(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ptr, (uint64_t)D,
+                         (uint64_t)heads, (uint64_t)(total > 0 ? total : 1), (uint64_t)D * 2, (uint64_t)rs * 2, 64,
+                         (uint32_t)box_heads, (uint32_t)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace prompt
+}  // namespace triattn

@@ -142,10 +142,10 @@ def test_nothing_to_do_and_workspace():
     _bwd(total_q=0, total_k=0, workspace=0, workspace_bytes=0)
     size = abi.tri_attn_prompt_bwd_workspace_size
     assert size(abi.TA_BF16, 1, 0, 100, 0, 100, 4, 2, 64) == 0 and size(abi.TA_BF16, 1, 100, 100, 100, 100, 4, 3, 64) == 0
-    # fp32 inputs and wide heads keep no sums of dQ; few key tiles, and the sums of dK and dV are there, too
-    assert size(abi.TA_F32, 1, 100, 100, 100, 100, 4, 2, 64) == size(abi.TA_BF16, 1, 100, 100, 100, 100, 4, 2, 256) == 448 * 4
-    assert size(abi.TA_BF16, 1, 100, 100, 100, 100, 4, 2, 64) == 448 * 4 * 65
-    assert size(abi.TA_BF16, 1, 1000, 1000, 1000, 1000, 4, 2, 64) == (4032 * 65 + 2 * 2048 * 64) * 4
+    # the rows' dO . O; few key tiles, and the parts of dK and dV are there, too (four row tiles for each CTA of a key tile)
+    for dt, D in ((abi.TA_F32, 64), (abi.TA_BF16, 256), (abi.TA_BF16, 64)):
+        assert size(dt, 1, 100, 100, 100, 100, 4, 2, D) == 448 * 4
+    assert size(abi.TA_BF16, 1, 1000, 1000, 1000, 1000, 4, 2, 64) == (4032 + 4 * 2 * 1000 * 2 * 64) * 4
 
 
 def test_python_refusals():
@@ -343,9 +343,7 @@ def test_the_same_twice_and_autograd():
     o.backward(g)
     o, lse = ta.prompt_attention(q, k, v, *a, return_aux=True)
     dq, dk, dv = ta.prompt_attention_backward(q, k, v, *a, o, lse, g)
-    assert bool((ka.grad == dk).all()) and bool((va.grad == dv).all())
-    # (dq's sums are reductions in any order: fp32, rounded to bf16 at the end)
-    assert float((qa.grad.double() - dq.double()).norm() / dq.double().norm()) < 2.0 ** -9
+    assert bool((qa.grad == dq).all()) and bool((ka.grad == dk).all()) and bool((va.grad == dv).all())
 
 
 @pytest.mark.gpu
