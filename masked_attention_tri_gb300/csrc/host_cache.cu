@@ -285,6 +285,7 @@ ta_status paged_fwd(const void* q, ta_dtype dtype, const int32_t* cu_seqlens_q, 
     p.sinks = sinks;
     p.RT = paged_rows(dtype, max_seqlen_q, p.G, D);
     p.tile = paged_tile(dtype, cache_dtype, D);
+    p.unit_tiles = paged_unit_tiles(dtype, cache_dtype);
     p.scale_log2e = scale * 1.4426950408889634f;
     p.q_rs = q_row_stride;
     p.status = status_word();

@@ -200,6 +200,7 @@ struct PagedParams {
     int window, sinks;          // window 0: every earlier slot
     int RT;                     // rows of a unit
     int tile;                   // slots of a tile
+    int unit_tiles;             // what a unit's set-up and merge weigh, in tiles
     float scale_log2e;
     long long q_rs;
     long long ks[3], vs[3];     // element strides {page, head, slot} of the caches
@@ -207,6 +208,7 @@ struct PagedParams {
 };
 int paged_rows(int dtype, int max_q, int G, int D);  // RT of a problem
 int paged_tile(int dtype, int cache_dtype, int D);   // and its tile
+int paged_unit_tiles(int dtype, int cache_dtype);    // and what a unit weighs beside its tiles
 size_t paged_workspace_bytes(int RT, int D);
 cudaError_t launch_paged(const PagedParams& p, cudaStream_t stream);
 

@@ -110,10 +110,12 @@ __device__ __forceinline__ Tiles unit_tiles(const PagedParams& p, const Seq& q, 
 __device__ __forceinline__ int row_tiles(const PagedParams& p, const Seq& q) { return (q.n * p.G + p.RT - 1) / p.RT; }
 // (These walk the row tiles one by one: made for sequences with few new rows.  8192 new tokens in one call are 2048 row
 // tiles of 16 rows, 4 heads a group, and every CTA walks them before its first load.)
-// Tiles of one kv head of a sequence (a unit without keys counts one: its rows are written too).
+// What a unit weighs on the axis: its tiles (one without keys counts one: its rows are written too), and p.unit_tiles for its
+// set-up and merge, which lie after its tiles.
+__device__ __forceinline__ int unit_weight(const PagedParams& p, const Tiles& t) { return max(1, t.nt) + p.unit_tiles; }
 __device__ __forceinline__ long long head_tiles(const PagedParams& p, const Seq& q) {
     long long t = 0;
-    for (int rt = 0; rt < row_tiles(p, q); ++rt) t += max(1, unit_tiles(p, q, rt).nt);
+    for (int rt = 0; rt < row_tiles(p, q); ++rt) t += unit_weight(p, unit_tiles(p, q, rt));
     return t;
 }
 
@@ -237,7 +239,7 @@ __device__ __forceinline__ bool walk_next(const PagedParams& p, Walk& w, Unit& u
             }
         }
         u.t = unit_tiles(p, w.q, w.rt);
-        const int nt = max(1, u.t.nt);
+        const int nt = unit_weight(p, u.t);
         if (w.skip >= nt) {
             w.skip -= nt;
             ++w.rt;
@@ -260,8 +262,8 @@ __device__ __forceinline__ bool walk_next(const PagedParams& p, Walk& w, Unit& u
 }
 
 // The shares that unit u reaches over, from the one that it starts in (this one).
-__device__ __forceinline__ int unit_parts(const Share& sh, const Unit& u, long long u_begin) {
-    const long long last = u_begin + max(1, u.t.nt) - 1;
+__device__ __forceinline__ int unit_parts(const PagedParams& p, const Share& sh, const Unit& u, long long u_begin) {
+    const long long last = u_begin + unit_weight(p, u.t) - 1;
     return (int)(last / sh.per - blockIdx.x) + 1;
 }
 

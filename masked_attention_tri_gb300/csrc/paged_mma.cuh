@@ -39,7 +39,7 @@
 // Four-bit codes (cache4.cuh) become fp16 times their scales on the way, both exact: a word's codes by one logical
 // operation each that puts them into the low bits of 1024, then a fused multiplication or two on the FMA pipe (e4m3's
 // conversion instructions run at a quarter of that rate).  k index 2t, 2t + 1, 2t + 8, 2t + 9 of K's products stands for
-// elements e, e + 4, e + 1, e + 5 of lane t's word; of V a lane reads 8 NDC columns of four slots, whose
+// elements e, e + 4, e + 1, e + 5 of lane t's word (it has whole groups of 16); of V a lane reads 8 NDC columns of four slots, whose
 // 16-bit halves side by side hold four columns' pairs.  The scales come into the stage by untiled copies beside the tiles.
 //
 // Roundings: P to the products' 16-bit type (fp16 for 8-bit and 4-bit caches: 2^-12 of a weight),
@@ -74,6 +74,15 @@ struct Blocks {
     static constexpr int value = M;
 };
 
+#ifndef TRIATTN_FOUR_WARPS
+#define TRIATTN_FOUR_WARPS 11
+#endif
+#ifndef TRIATTN_FOUR_WARPS2
+#define TRIATTN_FOUR_WARPS2 7
+#endif
+#ifndef TRIATTN_FOUR_BUFS
+#define TRIATTN_FOUR_BUFS 11
+#endif
 constexpr uint32_t kMmaSmem = 232448 - 1024 - 256;  // 227 KB less the alignment of the ring and the static part
 
 // What the producer tells of a stage; sc[i]: key scale, log2 and reciprocal of the value scale of the i-th
@@ -108,10 +117,11 @@ struct MmaConfig {
     // NT).  Measured on 64 sequences of 1k to 16k slots in 8 bits (before the warps took two blocks at once):
     // 7 warps 226 us, 11 warps 257, 15 warps 275: the more warps work on stages at a time, the fewer stages
     // are left for copies in flight.
-    static constexpr int kWarps = 7;
+    // Four-bit codes are bound by their arithmetic's latencies, and their stages are small: more warps.
+    static constexpr int kWarps = kFour && NDC * NT <= 2 ? TRIATTN_FOUR_WARPS : kFour && NDC * NT <= 4 ? TRIATTN_FOUR_WARPS2 : 7;
     static constexpr int kThreads = (kWarps + 1) * 32;
     // Merge buffers: one for each warp where the ring keeps its six stages, else four taken in two turns.
-    static constexpr int kBufs = NT * NDC <= 2 ? kWarps : 4;
+    static constexpr int kBufs = kFour ? (NT * NDC <= 2 ? TRIATTN_FOUR_BUFS : 4) : NT * NDC <= 2 ? kWarps : 4;
     static constexpr int kOStride = NDC * 64 + 4;                       // floats of a merged row
     static constexpr uint32_t kQ = NDC * NT * 1024;  // Q in fragment order
     static constexpr uint32_t kO = (uint32_t)kBufs * kRows * kOStride * 4;
@@ -166,6 +176,11 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint32_t v;
+    asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(a));
+    return v;
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -176,26 +191,35 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
-// Four-bit codes u = n + 8 as fp16 numbers n, exactly: the code put into the low bits of 1024 makes 1024 + u (the low
-// code of a byte) or 1024 + 16 u (the high one).
-__device__ __forceinline__ uint32_t four_or(uint32_t w, uint32_t mask) {
-    uint32_t y;
-    asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(y) : "r"(w), "r"(mask));
-    return y;
-}
 __device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
-// The low and the high code of byte 0 of both halves of w, times s (pairs: one number of each half).
-__device__ __forceinline__ uint32_t four_lo(uint32_t w, __half2 s) {
-    return as_u32(__hmul2(__hsub2(as_h2(four_or(w, 0x000f000fu)), as_h2(0x64086408u)), s));  // - 1032
-}
-__device__ __forceinline__ uint32_t four_hi(uint32_t w, __half2 s) {
-    return as_u32(__hmul2(__hfma2(as_h2(four_or(w, 0x00f000f0u)), as_h2(0x2c002c00u), as_h2(0xd480d480u)), s));  // / 16 - 72
-}
-// ... with s / 16 and -72 s at hand (exact: s has four significant bits).
-__device__ __forceinline__ uint32_t four_hi(uint32_t w, __half2 s16, __half2 s72) {
-    return as_u32(__hfma2(as_h2(four_or(w, 0x00f000f0u)), s16, s72));
-}
+// Four-bit codes u = n + 8 as fp16 numbers n s 2^-8, exactly.  A code put into the low bits of 1024 makes 1024 + u (the low code
+// of a byte) or 1024 + 16 u (the high one), and one fused multiplication is left: t s' - 1032 s' or t s' / 16 - 72 s' with
+// s' = s 2^-8.  s has four significant bits, so 1032 s' = 129 * 8 s' has eleven and 72 s' has seven: both are fp16 numbers, as s' and n s'
+// are (s' is 2^-17 at least, and 1032 s' 1806 at most).
+struct Four {
+    __half2 s, s16, c_lo, c_hi;
+    __device__ __forceinline__ explicit Four(uint32_t two) {  // of two e4m3 scales
+        s = __hmul2(as_h2(codes_f16(two)), as_h2(0x1c001c00u));  // 2^-8
+        s16 = __hmul2(s, as_h2(0x2c002c00u));
+        c_lo = __hmul2(s, as_h2(0xe408e408u));                   // -1032
+        c_hi = __hmul2(s, as_h2(0xd480d480u));                   // -72
+    }
+    __device__ __forceinline__ Four(const Four& f, bool high) {  // one of the two for both halves
+        s = high ? __high2half2(f.s) : __low2half2(f.s);
+        s16 = high ? __high2half2(f.s16) : __low2half2(f.s16);
+        c_lo = high ? __high2half2(f.c_lo) : __low2half2(f.c_lo);
+        c_hi = high ? __high2half2(f.c_hi) : __low2half2(f.c_hi);
+    }
+    static __device__ __forceinline__ __half2 put(uint32_t w, uint32_t mask) {
+        uint32_t y;
+        asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(y) : "r"(w), "r"(mask));
+        return as_h2(y);
+    }
+    // The low and the high code of byte 0 of both halves of w.
+    __device__ __forceinline__ uint32_t lo(uint32_t w) const { return as_u32(__hfma2(put(w, 0x000f000fu), s, c_lo)); }
+    __device__ __forceinline__ uint32_t hi(uint32_t w) const { return as_u32(__hfma2(put(w, 0x00f000f0u), s16, c_hi)); }
+};
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
     if constexpr (BF16)
@@ -211,12 +235,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
 }
-// Slot (within eight) of row i of an A operand.  (Four-bit codes: the orders in which a lane's reads of V, 4 NDC bytes of
-// slots pi(2t) and of slots pi(2t + 1), meet no bank twice.)
+// Slot (within eight) of row i of an A operand.  (Four-bit codes: orders in which neither a lane's reads of K, 8 NDC bytes of
+// slot pi(g), nor those of V, 4 NDC bytes of slots pi(2t) and of slots pi(2t + 1), meet a bank twice.)
 template <int TYPE, int NDC>
 __device__ __forceinline__ int pi8(int i) {
     if (TYPE != 3) return (i & 1) ? ((i - 1) ^ 4) + 1 : i;
-    return NDC == 1 ? (i >> 1) | ((i & 1) << 2) : NDC == 2 ? ((i << 1) & 7) | (i >> 2) : i;
+    return NDC == 1 ? i ^ (i >> 2) : NDC == 2 ? (((i & 2) << 1) | ((i >> 2) * 3)) ^ (i & 1) : i;
 }
 // What the swizzle of rows of 32 NDC bytes adds to a slot's 16-byte pieces (exclusive or).
 template <int NDC>
@@ -427,17 +451,15 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
     // 0-7, slots 8-15, the same 16 bytes further; the next 32 bytes at ^ 32), 8-bit V's words of
     // columns g (rows r0, r1; the upper 64 columns at ^ 64), 16-bit V's rows of the transposing load
     // (16 columns further at ^ 32).
-    // Four-bit: the same load of K (16 columns are now 32 codes); V's words of columns 8 NDC g.
+    // Four-bit: K's words of columns 16 NDC t, V's of columns 8 NDC g.
     const uint32_t k_row = (uint32_t)pi8<TYPE, NDC>(lane & 7) + ((lane & 8) ? 8u : 0u);
-    const uint32_t k_off =
-        kFour ? k_row * C::kRowB + ((((uint32_t)lane >> 4) ^ four_swizzle<NDC>(k_row)) << 4)
-              : k_row * 128u + ((((uint32_t)lane >> 4) ^ (k_row & 7u)) << 4);
-    auto v_off4 = [&](uint32_t r) {
-        const uint32_t byte = (uint32_t)g * NDC * 4u;
+    const uint32_t k_off = k_row * 128u + ((((uint32_t)lane >> 4) ^ (k_row & 7u)) << 4);
+    auto off4 = [&](uint32_t r, uint32_t byte) {
         return r * C::kRowB + (((byte >> 4) ^ four_swizzle<NDC>(r)) << 4) + (byte & 15u);
     };
-    const uint32_t v_off0 = kFour ? v_off4(r0) : r0 * 128u + (((uint32_t)(g >> 1) ^ r0) << 4) + (g & 1) * 8u;
-    const uint32_t v_off1 = kFour ? v_off4(r1) : r1 * 128u + (((uint32_t)(g >> 1) ^ r1) << 4) + (g & 1) * 8u;
+    const uint32_t k_off4 = off4(rg, (uint32_t)t * NDC * 8u);
+    const uint32_t v_off0 = kFour ? off4(r0, (uint32_t)g * NDC * 4u) : r0 * 128u + (((uint32_t)(g >> 1) ^ r0) << 4) + (g & 1) * 8u;
+    const uint32_t v_off1 = kFour ? off4(r1, (uint32_t)g * NDC * 4u) : r1 * 128u + (((uint32_t)(g >> 1) ^ r1) << 4) + (g & 1) * 8u;
     const uint32_t v_row = (uint32_t)pi8<TYPE, NDC>(lane & 7) + ((lane & 16) ? 8u : 0u);
     const uint32_t v_offt = v_row * 128u + ((((uint32_t)lane >> 3 & 1u) ^ (v_row & 7u)) << 4);
     // Reference of a row that has seen no key: below the logits of any finite bf16 rows whose sums fp32 holds (far above
@@ -450,7 +472,12 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
     // behind the tiles; lane l holds elements [4 l, 4 l + 4) and, for D > 128, 128 further on.
     constexpr int kQRows = (C::kRows + kWarps - 1) / kWarps, kQPieces = (NDC + 1) / 2;
     uint2 xq[kQRows][kQPieces];
+    float kf_n = 1.f, vf_n = 1.f;  // four-bit: the key head's factors
     auto fetch_q = [&](const Unit& v) {
+        if constexpr (kFour) {
+            if (p.c4.factor[0]) kf_n = p.c4.factor[0][v.h];
+            if (p.c4.factor[1]) vf_n = p.c4.factor[1][v.h];
+        }
 #pragma unroll
         for (int i = 0; i < kQRows; ++i) {
             const int r = warp + i * kWarps, row = v.rt * C::kRows + r;
@@ -473,7 +500,7 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
             float factor = p.scale_log2e;
             uint2 (&x)[kQPieces] = xq[i];
             if constexpr (kFour) {
-                if (p.c4.factor[0]) factor *= p.c4.factor[0][u.h];
+                factor *= kf_n * 256.f;  // (the products' numbers are 2^-8 of K's)
             }
             if constexpr (kCodes || kFour) {
                 const bool bf = p.dtype == TA_BF16;
@@ -507,12 +534,13 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                 if (ch >= NDC) continue;
                 if constexpr (kFour) {
                     // Element e of eight neighbours (four-bit codes of a word): a pair is (e, e + 4), e / 2 of four the
-                    // product, e % 2 the operand's register; lane t of 32 columns has the word of columns 8 t.
-                    uint8_t* to = sq + ((d / 32 * 2) * NT + r / 8) * 256 + (r % 8) * 32 + (d % 32) / 8 * 8 + (d % 8) / 4 * 2;
+                    // product, e % 2 the operand's register; lane t has the words of columns 16 NDC t on.
+                    const int tq = d / (16 * NDC), word = d % (16 * NDC) / 8;
+                    uint8_t* to = sq + (word * 2 * NT + r / 8) * 256 + (r % 8) * 32 + tq * 8 + (d % 8) / 4 * 2;
                     const uint32_t w[2] = {x[c].x, x[c].y};
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<uint16_t*>(to + (e / 2) * NT * 256 + (e % 2) * 4) = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+                        if (tq < 4) *reinterpret_cast<uint16_t*>(to + (e / 2) * NT * 256 + (e % 2) * 4) = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
                     continue;
                 }
                 uint8_t* dst = sq + ((ch * 4 + in / 16) * NT + r / 8) * 256 + (r % 8) * 32;
@@ -535,6 +563,7 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
         const long long head0 = (long long)u.h * p.G;
         const int total_rows = u.q.n * p.G, row_first = u.rt * C::kRows;
         put_q();
+        [[maybe_unused]] const float v_factor = vf_n * 256.f;
         // ---- This lane's columns of S^T and O^T: rows nt * 8 + 2 t and the next.
         int pos[NT][2];
 #pragma unroll
@@ -636,23 +665,37 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                     }
                 };
                 if constexpr (kFour) {
-                    // 32 bytes of a row at a time are 64 columns, half of which share a lane's scale: two products each
+                    // A lane reads 16 NDC columns of slots pi(g) and pi(g) + 8: whole groups, with scales of their own
 #pragma unroll
-                    for (int c = 0; c < NDC; ++c)
+                    for (int mb = 0; mb < M; ++mb)
 #pragma unroll
-                        for (int mb = 0; mb < M; ++mb) {
-                            uint32_t a[4];
-                            ldsm_x4(kb + mb * C::kBlockB + (k_off ^ (32u * c)), a);
+                        for (int q = 0; q < (NDC + 1) / 2; ++q) {  // 32 columns (NDC 1: 16)
+                            uint32_t w[2][4];
+                            Four f[2] = {Four(0u), Four(0u)};
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if (c * 64 + h * 32 >= p.D) continue;  // (there are no scales)
-                                const uint32_t at = ksb + (mb * 16u + rg) * sb + c * 4u + h * 2u + (t >> 1);
-                                const uint32_t s2 = codes_f16(lds8(at) | (lds8(at + 8u * sb) << 8));
-                                const __half2 s0 = __low2half2(as_h2(s2)), s1 = __high2half2(as_h2(s2));
-                                const uint32_t w0 = a[2 * h], w1 = a[2 * h + 1];
-                                step(mb, c * 4 + h * 2, four_lo(w0, s0), four_lo(w1, s1), four_hi(w0, s0), four_hi(w1, s1));
-                                step(mb, c * 4 + h * 2 + 1, four_lo(w0 >> 8, s0), four_lo(w1 >> 8, s1), four_hi(w0 >> 8, s0),
-                                     four_hi(w1 >> 8, s1));
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t from = kb + mb * C::kBlockB + (k_off4 ^ (16u * q)) + i * 8u * C::kRowB;
+                                if constexpr (NDC == 1) {
+                                    const uint2 x = lds64(from);
+                                    w[i][0] = x.x, w[i][1] = x.y;
+                                } else {
+                                    const uint4 x = lds128(from);
+                                    w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+                                }
+                                // (past D there are no scales: zeros)
+                                const uint32_t at = ksb + (mb * 16u + rg + 8u * i) * sb + t * NDC + 2u * q;
+                                const bool there = (uint32_t)(t * NDC + 2 * q) < sb;
+                                f[i] = Four(there ? (NDC == 1 ? lds8(at) : lds16(at)) : 0u);
+                            }
+#pragma unroll
+                            for (int h = 0; h < (NDC == 1 ? 1 : 2); ++h) {  // a group
+                                const Four f0(f[0], h), f1(f[1], h);
+#pragma unroll
+                                for (int k = 2 * h; k < 2 * h + 2; ++k) {  // a word: two products
+                                    const uint32_t w0 = w[0][k], w1 = w[1][k];
+                                    step(mb, q * 8 + k * 2, f0.lo(w0), f1.lo(w1), f0.hi(w0), f1.hi(w1));
+                                    step(mb, q * 8 + k * 2 + 1, f0.lo(w0 >> 8), f1.lo(w1 >> 8), f0.hi(w0 >> 8), f1.hi(w1 >> 8));
+                                }
                             }
                         }
                 } else {
@@ -778,14 +821,9 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
 #pragma unroll
                         for (int q = 0; q < (NDC + 1) / 2; ++q) {  // the lane's groups of 16 columns
                             const uint32_t sg = vsb + (mb * 16u) * sb + (NDC == 1 ? (uint32_t)g >> 1 : (uint32_t)(g * (NDC / 2) + q));
-                            __half2 s[2], s16[2], s72[2];  // of slots r0, r1, and of r0 + 8, r1 + 8
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint32_t f = sg + i * 8u * sb;
-                                s[i] = as_h2(codes_f16(lds8(f + r0 * sb) | (lds8(f + r1 * sb) << 8)));
-                                s16[i] = __hmul2(s[i], as_h2(0x2c002c00u));
-                                s72[i] = __hmul2(s[i], as_h2(0xd480d480u));
-                            }
+                            // of slots r0, r1, and of r0 + 8, r1 + 8
+                            const Four fa(lds8(sg + r0 * sb) | (lds8(sg + r1 * sb) << 8));
+                            const Four fb(lds8(sg + (r0 + 8u) * sb) | (lds8(sg + (r1 + 8u) * sb) << 8));
 #pragma unroll
                             for (int j = 2 * q; j < (NDC == 1 ? 1 : 2 * q + 2); ++j)
 #pragma unroll
@@ -794,8 +832,7 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
                                     uint32_t x = __byte_perm(w[0][j], w[1][j], sel), z = __byte_perm(w[2][j], w[3][j], sel);
 #pragma unroll
                                     for (int m2 = 0; m2 < 2; ++m2) {
-                                        const uint32_t f0 = four_lo(x, s[0]), f1 = four_hi(x, s16[0], s72[0]);
-                                        const uint32_t f2 = four_lo(z, s[1]), f3 = four_hi(z, s16[1], s72[1]);
+                                        const uint32_t f0 = fa.lo(x), f1 = fa.hi(x), f2 = fb.lo(z), f3 = fb.hi(z);
 #pragma unroll
                                         for (int nt = 0; nt < NT; ++nt)
                                             mma16816<false>(o[j * 4 + h * 2 + m2][nt], f0, f1, f2, f3, b[mb][nt]);
@@ -841,7 +878,7 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
             };
             if (plain_stage) {
                 // (two at a time where a warp has several: the one's products fill the other's waits)
-                constexpr int M = kTake >= 2 && NT <= 2 ? 2 : 1;
+                constexpr int M = kTake >= 2 && NT <= 2 && kWarps < 11 ? 2 : 1;
                 if (M == 1 || take == 1) {
 #pragma unroll 1
                     for (int blk = b_first; blk < b_first + take; ++blk) block(Yes{}, Blocks<1>{}, blk);
@@ -944,7 +981,6 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
         const bool whole = u.starts && u.ends;
         const int slot = u.starts ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
         const int D4 = p.D / 4;
-        const float v_factor = kFour && p.c4.factor[1] ? p.c4.factor[1][u.h] : 1.f;
         for (int e = threadIdx.x; e < u.rows * D4; e += kWarps * 32) {
             const int r = e / D4, d = (e - r * D4) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -979,7 +1015,7 @@ __global__ void __launch_bounds__(MmaConfig<TYPE, NDC, NT>::kThreads, 1) paged_m
             jn.h = u.h;
             jn.row0 = row_first;
             jn.rows = u.rows;
-            jn.parts = unit_parts(sh, u, at);
+            jn.parts = unit_parts(p, sh, u, at);
         }
         at += u.j1 - u.j0;
     }
