@@ -32,10 +32,29 @@ __device__ __forceinline__ uint32_t scale_code(uint32_t most, float inv_factor) 
 __device__ __forceinline__ float scale_value(uint32_t code) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
 }
-// n + 8 of y = x / f_h.  (A NaN gives 8: its scale says what it is.)
-__device__ __forceinline__ uint32_t nibble(float y, float s) {
-    const int n = __float2int_rn(__fdiv_rn(y, s));
-    return (uint32_t)(min(7, max(-7, n)) + 8);
+// A scale s with what the codes of its elements take.
+struct Scale {
+    float s, inv, half, most;
+    __device__ __forceinline__ explicit Scale(float v) : s(v), inv(1.f / v), half(0.5f * v), most(7.f * v) {}
+};
+// n + 8 in the low four bits (the others are not zero) of y = x / f_h: y / s to the nearest whole number, ties to even, 7 at most.
+// y times 1 / s may fall on the wrong side of a border, so the remainder y - n s decides (fp32 holds it exactly: n s has eight significant
+// bits, and y is at most 7 s and n s not far from it).  (A NaN's scale says what it is.)
+__device__ __forceinline__ uint32_t code(float y, const Scale& c) {
+    y = fminf(fmaxf(y, -c.most), c.most);
+    const float t = fmaf(y, c.inv, 12582920.f);  // 1.5 * 2^23 + 8: whole numbers, n + 8 in the low bits
+    const float d = fmaf(12582920.f - t, c.s, y), a = fabsf(d);
+    const uint32_t n = __float_as_uint(t);
+    const bool off = a > c.half || (a == c.half && (n & 1u));
+    return off ? (d > 0.f ? n + 1u : n - 1u) : n;
+}
+
+// The same of a y that has eleven significant bits, by two roundings: to 2^-16 first, which takes the product's error off a border.  (With m of
+// s = m 2^k from 8 to 15, y / s is a / (m 2^j), a < 2^11 and 2^j < 2^12: if it is no border, at least 2^-13 from one.)
+__device__ __forceinline__ uint32_t code16(float y, const Scale& c) {
+    y = fminf(fmaxf(y, -c.most), c.most);
+    const float t = fmaf(y, c.inv, 192.f);        // 1.5 * 2^7: multiples of 2^-16
+    return __float_as_uint(t + 12582728.f);       // 12582920 - 192
 }
 
 // Eight codes of a word as eight numbers times s.

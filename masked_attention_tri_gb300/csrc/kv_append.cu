@@ -100,22 +100,26 @@ __device__ __forceinline__ uint32_t largest(const float2 (&f)[V]) {
 }
 
 // A run of N elements to 4-bit codes, which shares its scale with the runs of the lanes of `lanes`
-// (a mask; they follow one another, N times their number is 16); `first`: this lane writes the scale.
-template <int N>
+// (a mask; they follow one another, N times their number is 16); `first`: this lane writes the scale.  SHORT: elements of 16 bits.
+template <int N, bool SHORT>
 __device__ __forceinline__ void store_four(uint8_t* codes, uint8_t* scale, const float2* f, float inv_factor,
                                            uint32_t lanes, bool first) {
-    uint32_t m = 0;
+    float most = 0.f;  // (a NaN stays)
 #pragma unroll
     for (int i = 0; i < N / 2; ++i)
-        m = max(m, max(__float_as_uint(f[i].x) & 0x7fffffffu, __float_as_uint(f[i].y) & 0x7fffffffu));
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(most) : "f"(most), "f"(fabsf(f[i].x)), "f"(fabsf(f[i].y)));
+    uint32_t m = __float_as_uint(most);
 #pragma unroll
     for (int o = 1; o < 16 / N; o <<= 1) m = max(m, __shfl_xor_sync(lanes, m, o));
     const uint32_t code = cache4::scale_code(m, inv_factor);
-    const float s = cache4::scale_value(code);
+    const cache4::Scale s(cache4::scale_value(code));
     uint32_t w[N / 8 > 0 ? N / 8 : 1] = {};
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i)
-        w[i / 4] |= (cache4::nibble(f[i].x * inv_factor, s) | (cache4::nibble(f[i].y * inv_factor, s) << 4)) << (8 * (i % 4));
+    for (int i = N / 2 - 1; i >= 0; --i) {
+        const float x = f[i].x * inv_factor, y = f[i].y * inv_factor;
+        w[i / 4] = (w[i / 4] << 4) | ((SHORT ? cache4::code16(y, s) : cache4::code(y, s)) & 15u);
+        w[i / 4] = (w[i / 4] << 4) | ((SHORT ? cache4::code16(x, s) : cache4::code(x, s)) & 15u);
+    }
     if constexpr (N == 16) *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
     else if constexpr (N == 8) *reinterpret_cast<uint32_t*>(codes) = w[0];
     else *reinterpret_cast<uint16_t*>(codes) = (uint16_t)w[0];
@@ -124,7 +128,7 @@ __device__ __forceinline__ void store_four(uint8_t* codes, uint8_t* scale, const
 
 // C: the cache's element type (T itself, uint8_t for e4m3 codes, cache4::Code for 4 bits).
 template <typename T, typename C, int V>
-__global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, std::is_same<C, cache4::Code>::value ? 3 : 4) kv_append_kernel(const AppendArgs a) {
     constexpr bool kCodes = std::is_same<C, uint8_t>::value;
     constexpr bool kFour = std::is_same<C, cache4::Code>::value;
     extern __shared__ float4 table4[];
@@ -227,16 +231,23 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const AppendArgs
                             // (head and rotary dimensions are multiples of 32, so that a group's lanes are neighbours
                             // in one head of one row)
                             const int lane = threadIdx.x % 32;
-                            if (r.turned && !p.interleaved) {  // two runs of V elements
-                                constexpr int kL = 16 / V;
-                                const uint32_t lanes = ((1u << kL) - 1u) << (lane & ~(kL - 1));
-                                store_four<V>(codes, scale, f, inv, lanes, u % kL == 0);
-                                store_four<V>(codes + r.o1 / 2, scale + r.o1 / 16, f + V / 2, inv, lanes, u % kL == 0);
-                            } else {                           // one of 2 V
-                                constexpr int kL = 8 / V;
-                                const uint32_t lanes = ((1u << kL) - 1u) << (lane & ~(kL - 1));
-                                store_four<2 * V>(codes, scale, f, inv, lanes, u % kL == 0);
-                            }
+                            // (a factor that is no power of two leaves more bits)
+                            const bool brief = sizeof(T) == 2 && !turned && (__float_as_uint(inv) & 0x7fffffu) == 0;
+                            auto store = [&](auto tag) {
+                                constexpr bool kShort = decltype(tag)::value;
+                                if (r.turned && !p.interleaved) {  // two runs of V elements
+                                    constexpr int kL = 16 / V;
+                                    const uint32_t lanes = ((1u << kL) - 1u) << (lane & ~(kL - 1));
+                                    store_four<V, kShort>(codes, scale, f, inv, lanes, u % kL == 0);
+                                    store_four<V, kShort>(codes + r.o1 / 2, scale + r.o1 / 16, f + V / 2, inv, lanes, u % kL == 0);
+                                } else {                           // one of 2 V
+                                    constexpr int kL = 8 / V;
+                                    const uint32_t lanes = ((1u << kL) - 1u) << (lane & ~(kL - 1));
+                                    store_four<2 * V, kShort>(codes, scale, f, inv, lanes, u % kL == 0);
+                                }
+                            };
+                            if (brief) store(std::true_type{});
+                            else store(std::false_type{});
                             continue;
                         }
                     }

@@ -28,6 +28,45 @@ struct ReadArgs {
 
 struct Raw {};                   // a cache of the output's own type
 
+// Sixteen 4-bit codes as n * x in 16 bits, for a scale times a factor x (four significant bits) within `reads_fast`: a code put
+// into the low bits of a power of two makes 128 + u (bf16) or 16 + u (fp16), u = n + 8, and one fused multiplication and a sum give
+// (128 + u) x - 136 x or (16 + u) x - 24 x exactly: 136 x = 17 * 8 x has eight significant bits at most, 24 x six.
+__device__ __forceinline__ void fast_values(__nv_bfloat16, uint32_t w, float x, uint32_t (&y)[4]) {
+    const __nv_bfloat162 s = __float2bfloat162_rn(x), c = __float2bfloat162_rn(-136.f * x);
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // codes i and i + 4
+        uint32_t t;
+        asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xEA;" : "=r"(t) : "r"(w >> (4 * i)));
+        const __nv_bfloat162 z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&t), s, c);
+        v[i] = *reinterpret_cast<const uint32_t*>(&z);
+    }
+    y[0] = __byte_perm(v[0], v[1], 0x5410), y[1] = __byte_perm(v[2], v[3], 0x5410);
+    y[2] = __byte_perm(v[0], v[1], 0x7632), y[3] = __byte_perm(v[2], v[3], 0x7632);
+}
+__device__ __forceinline__ void fast_values(__half, uint32_t w, float x, uint32_t (&y)[4]) {
+    const __half2 s = __float2half2_rn(x), c = __float2half2_rn(-24.f * x);
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t t;
+        asm("lop3.b32 %0, %1, 0x03c003c0, 0x4c004c00, 0xEA;" : "=r"(t) : "r"(i < 2 ? w << (6 - 4 * i) : w >> (4 * i - 6)));
+        const __half2 z = __hfma2(*reinterpret_cast<const __half2*>(&t), s, c);
+        v[i] = *reinterpret_cast<const uint32_t*>(&z);
+    }
+    y[0] = __byte_perm(v[0], v[1], 0x5410), y[1] = __byte_perm(v[2], v[3], 0x5410);
+    y[2] = __byte_perm(v[0], v[1], 0x7632), y[3] = __byte_perm(v[2], v[3], 0x7632);
+}
+// A factor that is a power of two, and far enough from what the type holds (scales are 2^-9 to 448).
+__device__ __forceinline__ bool reads_fast(__nv_bfloat16, float f) {
+    return (__float_as_uint(f) & 0x007fffffu) == 0 && f >= 0x1p-100f && f <= 0x1p100f;
+}
+__device__ __forceinline__ bool reads_fast(__half, float f) {
+    return (__float_as_uint(f) & 0x007fffffu) == 0 && f >= 0x1p-15f && f <= 4.f;
+}
+__device__ __forceinline__ bool reads_fast(float, float) { return false; }
+__device__ __forceinline__ void fast_values(float, uint32_t, float, uint32_t (&)[4]) {}
+
 // The numbers of N floats as T, 16 bytes at a time.
 template <typename T, int N>
 __device__ __forceinline__ void store_row(T* p, const float (&f)[N]) {
@@ -73,27 +112,30 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadArgs a) {
     const long long tok0 = (long long)row0 + (s0 - start);
     const int h0 = blockIdx.y * a.heads, nh = min(a.heads, p.Hk - h0);
 
-    // Piece e: of the k rows of the heads, one after the other, then of the v rows.
-    const int row_units = cnt * a.units, items = 2 * nh * row_units;
+    // (16-bit outputs whose rows are 32-byte multiples: a piece is one store)
+    const bool wide = sizeof(T) == 2 && ((reinterpret_cast<uintptr_t>(p.out[0]) | reinterpret_cast<uintptr_t>(p.out[1])) & 31) == 0 &&
+                      p.rs[0] % 16 == 0 && p.rs[1] % 16 == 0;
+    // A warp takes the rows of a head's k or v (or, where there are fewer of those than warps, every `share`th piece of them).
     struct Piece {
         int kind, h, row, u;
     };
-    auto piece = [&](int e) {
-        Piece x;
-        const int r = (int)a.fu.div((uint32_t)e);
-        x.u = e - r * a.units;
-        const int hh = r / cnt;
-        x.row = r - hh * cnt;
-        x.kind = hh >= nh;
-        x.h = h0 + (x.kind ? hh - nh : hh);
-        return x;
-    };
-    for (int e0 = threadIdx.x; e0 < items; e0 += kAhead * kThreads) {
+    constexpr int kWarps = kThreads / 32;
+    const int share = 2 * nh < kWarps ? kWarps / (2 * nh) : 1, warp = threadIdx.x / 32, items = cnt * a.units;
+    for (int hh = warp / share; hh < 2 * nh; hh += kWarps)
+    for (int e0 = warp % share * 32 + threadIdx.x % 32; e0 < items; e0 += kAhead * 32 * share) {
+        auto piece = [&](int e) {
+            Piece x;
+            x.row = (int)a.fu.div((uint32_t)e);
+            x.u = e - x.row * a.units;
+            x.kind = hh >= nh;
+            x.h = h0 + (x.kind ? hh - nh : hh);
+            return x;
+        };
         uint4 w[kAhead];
         uint32_t sc[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            const int e = e0 + j * kThreads;
+            const int e = e0 + j * 32 * share;
             if (e >= items) break;
             const Piece x = piece(e);
             const int slot = off0 + x.row;
@@ -112,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            const int e = e0 + j * kThreads;
+            const int e = e0 + j * 32 * share;
             if (e >= items) break;
             const Piece x = piece(e);
             T* out = static_cast<T*>(p.out[x.kind]) + (tok0 + x.row) * p.rs[x.kind] + (long long)x.h * p.D;
@@ -124,6 +166,21 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadArgs a) {
                 if constexpr (kFour) {
                     const float s = cache4::scale_value(sc[j]);
                     const float fac = p.c4.factor[x.kind] ? p.c4.factor[x.kind][x.h] : 1.f;
+                    if (reads_fast(T(), fac)) {
+                        uint32_t y[2][4];
+                        fast_values(T(), ws[0], s * fac, y[0]);
+                        fast_values(T(), ws[1], s * fac, y[1]);
+                        T* at = out + x.u * 16;
+                        if (wide) {
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(y[0][0]), "r"(y[0][1]),
+                                         "r"(y[0][2]), "r"(y[0][3]), "r"(y[1][0]), "r"(y[1][1]), "r"(y[1][2]), "r"(y[1][3])
+                                         : "memory");
+                        } else {
+                            reinterpret_cast<uint4*>(at)[0] = make_uint4(y[0][0], y[0][1], y[0][2], y[0][3]);
+                            reinterpret_cast<uint4*>(at)[1] = make_uint4(y[1][0], y[1][1], y[1][2], y[1][3]);
+                        }
+                        continue;
+                    }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float v[8];
