@@ -1,4 +1,4 @@
-// cache4.cuh -- the 4-bit codes of a paged cache, shared by the kernels that write them (kv_append.cu), read them back
+// cache4.cuh -- the 4-bit codes of a paged cache, shared by the kernels that write them (kv_append4.cu), read them back
 // (kv_read.cu) and attend to them (paged_simt.cu, paged_mma.cuh).
 //
 // 16 neighbouring elements of a row share a scale.  An element of head h stands for n * s * f_h: n a whole number from
@@ -32,10 +32,16 @@ __device__ __forceinline__ uint32_t scale_code(uint32_t most, float inv_factor) 
 __device__ __forceinline__ float scale_value(uint32_t code) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
 }
+// 1 / x to within 2^-23 of it.
+__device__ __forceinline__ float about_inverse(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // A scale s with what the codes of its elements take.
 struct Scale {
     float s, inv, half, most;
-    __device__ __forceinline__ explicit Scale(float v) : s(v), inv(1.f / v), half(0.5f * v), most(7.f * v) {}
+    __device__ __forceinline__ explicit Scale(float v) : s(v), inv(about_inverse(v)), half(0.5f * v), most(7.f * v) {}
 };
 // n + 8 in the low four bits (the others are not zero) of y = x / f_h: y / s to the nearest whole number, ties to even, 7 at most.
 // y times 1 / s may fall on the wrong side of a border, so the remainder y - n s decides (fp32 holds it exactly: n s has eight significant
@@ -49,12 +55,31 @@ __device__ __forceinline__ uint32_t code(float y, const Scale& c) {
     return off ? (d > 0.f ? n + 1u : n - 1u) : n;
 }
 
-// The same of a y that has eleven significant bits, by two roundings: to 2^-16 first, which takes the product's error off a border.  (With m of
-// s = m 2^k from 8 to 15, y / s is a / (m 2^j), a < 2^11 and 2^j < 2^12: if it is no border, at least 2^-13 from one.)
-__device__ __forceinline__ uint32_t code16(float y, const Scale& c) {
-    y = fminf(fmaxf(y, -c.most), c.most);
-    const float t = fmaf(y, c.inv, 192.f);        // 1.5 * 2^7: multiples of 2^-16
-    return __float_as_uint(t + 12582728.f);       // 12582920 - 192
+// Eight codes (n + 8 from 0 to 15, whole bytes zero above) of the low bytes of u as a word.
+__device__ __forceinline__ uint32_t pack8(const uint32_t (&u)[8]) {
+    uint32_t x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t y = __byte_perm(__byte_perm(u[4 * i], u[4 * i + 1], 0x0040), __byte_perm(u[4 * i + 2], u[4 * i + 3], 0x0040), 0x5410);
+        x[i] = y | (y >> 4);
+    }
+    return __byte_perm(x[0], x[1], 0x6420);
+}
+// Sixteen elements x of 16 bits as codes, two words.  x / (f_h s) is rounded to 2^-16 first, which takes the product's error off a border,
+// and then to whole numbers.  This is the nearest for elements of at most eleven significant bits and a factor that is a power of two: with m
+// of s = m 2^k from 8 to 15, x / (f_h s) is a / (m 2^j), a < 2^11 and 2^j < 2^12; if it is no border, it is at least 2^-13 from one.  (Turned
+// elements and other factors: within 2^-16 of a border a code may fall on either side.)
+__device__ __forceinline__ uint2 codes16(const float (&x)[16], float inv, const Scale& c, bool clamp) {
+    const float r = c.inv * inv;
+    uint32_t u[2][8];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) u[i / 8][i % 8] = __float_as_uint(fmaf(x[i], r, 192.f) + 12582728.f);  // 1.5 * 2^7; 1.5 * 2^23 + 8 - 192
+    if (clamp) {  // a scale at an end of e4m3's range: some element is more than 7 of it
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            u[i / 8][i % 8] = __float_as_uint(fmaf(fminf(fmaxf(x[i] * inv, -c.most), c.most), c.inv, 192.f) + 12582728.f);
+    }
+    return make_uint2(pack8(u[0]), pack8(u[1]));
 }
 
 // Eight codes of a word as eight numbers times s.

@@ -16,16 +16,12 @@
 // shared memory, computed once for the job's heads.  Codes need the largest |x| of a page's rows
 // before the first is written: as many rows as 512 units hold stay in registers between the
 // two (64 rows of D = 128: a page of the usual size is read once); larger pages are read twice.
-// 4-bit pages need only 16 elements at a time, which one thread or a few neighbouring lanes hold: cache4.cuh.
 // No two CTAs write the same (page, head), so nothing is ordered by atomics (the largest |x| is a maximum
 // of bit patterns: the same in any order).
 //   Eight prompts of 256 to 2048 tokens, 32 + 8 heads of 128, pages of 64 in 8 bits: 54 us.
 
 #include <cuda_fp8.h>
 
-#include <type_traits>
-
-#include "cache4.cuh"
 #include "internal.h"
 #include "rotary.cuh"
 #include "tc_kernel.cuh"
@@ -99,38 +95,10 @@ __device__ __forceinline__ uint32_t largest(const float2 (&f)[V]) {
     return m;
 }
 
-// A run of N elements to 4-bit codes, which shares its scale with the runs of the lanes of `lanes`
-// (a mask; they follow one another, N times their number is 16); `first`: this lane writes the scale.  SHORT: elements of 16 bits.
-template <int N, bool SHORT>
-__device__ __forceinline__ void store_four(uint8_t* codes, uint8_t* scale, const float2* f, float inv_factor,
-                                           uint32_t lanes, bool first) {
-    float most = 0.f;  // (a NaN stays)
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i)
-        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(most) : "f"(most), "f"(fabsf(f[i].x)), "f"(fabsf(f[i].y)));
-    uint32_t m = __float_as_uint(most);
-#pragma unroll
-    for (int o = 1; o < 16 / N; o <<= 1) m = max(m, __shfl_xor_sync(lanes, m, o));
-    const uint32_t code = cache4::scale_code(m, inv_factor);
-    const cache4::Scale s(cache4::scale_value(code));
-    uint32_t w[N / 8 > 0 ? N / 8 : 1] = {};
-#pragma unroll
-    for (int i = N / 2 - 1; i >= 0; --i) {
-        const float x = f[i].x * inv_factor, y = f[i].y * inv_factor;
-        w[i / 4] = (w[i / 4] << 4) | ((SHORT ? cache4::code16(y, s) : cache4::code(y, s)) & 15u);
-        w[i / 4] = (w[i / 4] << 4) | ((SHORT ? cache4::code16(x, s) : cache4::code(x, s)) & 15u);
-    }
-    if constexpr (N == 16) *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
-    else if constexpr (N == 8) *reinterpret_cast<uint32_t*>(codes) = w[0];
-    else *reinterpret_cast<uint16_t*>(codes) = (uint16_t)w[0];
-    if (first) *scale = (uint8_t)code;
-}
-
-// C: the cache's element type (T itself, uint8_t for e4m3 codes, cache4::Code for 4 bits).
+// C: the cache's element type (T itself, or uint8_t for e4m3 codes).
 template <typename T, typename C, int V>
-__global__ void __launch_bounds__(kThreads, std::is_same<C, cache4::Code>::value ? 3 : 4) kv_append_kernel(const AppendArgs a) {
-    constexpr bool kCodes = std::is_same<C, uint8_t>::value;
-    constexpr bool kFour = std::is_same<C, cache4::Code>::value;
+__global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const AppendArgs a) {
+    constexpr bool kCodes = sizeof(C) == 1;
     extern __shared__ float4 table4[];
     float* table = reinterpret_cast<float*>(table4);
     __shared__ uint32_t most[kMaxHeads];
@@ -217,40 +185,6 @@ __global__ void __launch_bounds__(kThreads, std::is_same<C, cache4::Code>::value
 #pragma unroll
                 for (int j = 0; j < kHold; ++j) {
                     if (n0 + j * a.lanes >= rows * nh) break;
-                    if constexpr (kFour) {
-                        if (kind != 2) {
-                            float2 f[V];
-                            turned_floats(w[j], row[j], f);
-                            const int h = h0 + head[j], slot = off0 + c0 + row[j];
-                            const Cache4& c4 = p.c4;
-                            uint8_t* codes = c4.codes[kind] + page * c4.cs[kind][0] + h * c4.cs[kind][1] +
-                                             (long long)slot * (p.D / 2) + r.o0 / 2;
-                            uint8_t* scale = c4.scale[kind] + page * c4.ss[kind][0] + h * c4.ss[kind][1] +
-                                             (long long)slot * (p.D / 16) + r.o0 / 16;
-                            const float inv = c4.factor[kind] ? 1.f / c4.factor[kind][h] : 1.f;
-                            // (head and rotary dimensions are multiples of 32, so that a group's lanes are neighbours
-                            // in one head of one row)
-                            const int lane = threadIdx.x % 32;
-                            // (a factor that is no power of two leaves more bits)
-                            const bool brief = sizeof(T) == 2 && !turned && (__float_as_uint(inv) & 0x7fffffu) == 0;
-                            auto store = [&](auto tag) {
-                                constexpr bool kShort = decltype(tag)::value;
-                                if (r.turned && !p.interleaved) {  // two runs of V elements
-                                    constexpr int kL = 16 / V;
-                                    const uint32_t lanes = ((1u << kL) - 1u) << (lane & ~(kL - 1));
-                                    store_four<V, kShort>(codes, scale, f, inv, lanes, u % kL == 0);
-                                    store_four<V, kShort>(codes + r.o1 / 2, scale + r.o1 / 16, f + V / 2, inv, lanes, u % kL == 0);
-                                } else {                           // one of 2 V
-                                    constexpr int kL = 8 / V;
-                                    const uint32_t lanes = ((1u << kL) - 1u) << (lane & ~(kL - 1));
-                                    store_four<2 * V, kShort>(codes, scale, f, inv, lanes, u % kL == 0);
-                                }
-                            };
-                            if (brief) store(std::true_type{});
-                            else store(std::false_type{});
-                            continue;
-                        }
-                    }
                     if (turned) {
                         float2 f[V];
                         turned_floats(w[j], row[j], f);
@@ -259,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, std::is_same<C, cache4::Code>::value
                     if (kind == 2) {
                         w[j].store(static_cast<T*>(p.q_out) + (tok0 + c0 + row[j]) * p.qo_rs +
                                        (long long)(h0 + head[j]) * p.D + r.o0, r.o1);
-                    } else if constexpr (!kCodes && !kFour) {
+                    } else if constexpr (!kCodes) {
                         w[j].store(cache + (h0 + head[j]) * cst[1] + (off0 + c0 + row[j]) * cst[2] + r.o0, r.o1);
                     }
                 }
@@ -393,7 +327,7 @@ cudaError_t launch(const KvAppendParams& p, cudaStream_t stream) {
     // Heads of a CTA: the table serves them all (16 rows of a page are work enough); but few for codes of
     // whole pages, which go one after the other.
     const bool few = p.max_n <= 8;
-    const bool codes = std::is_same<C, uint8_t>::value;
+    const bool codes = sizeof(C) == 1;
     a.heads[0] = heads_of_job(p.Hk, codes && !few ? 4 : 16);
     a.heads[1] = heads_of_job(p.Hk, codes && !few ? 2 : 16);
     a.heads[2] = p.q ? heads_of_job(p.Hq, 32) : 1;
@@ -422,7 +356,6 @@ cudaError_t launch(const KvAppendParams& p, cudaStream_t stream) {
 
 template <typename T, int V>
 cudaError_t launch_t(const KvAppendParams& p, cudaStream_t stream) {
-    if (p.cache_dtype == TA_INT4) return launch<T, cache4::Code, V>(p, stream);
     const bool codes = p.cache_dtype == TA_E4M3;
     if (p.dim % (2 * V) == 0) return codes ? launch<T, uint8_t, V>(p, stream) : launch<T, T, V>(p, stream);
     return codes ? launch<T, uint8_t, 1>(p, stream) : launch<T, T, 1>(p, stream);
@@ -430,7 +363,10 @@ cudaError_t launch_t(const KvAppendParams& p, cudaStream_t stream) {
 
 }  // namespace
 
+cudaError_t launch_kv_append4(const KvAppendParams& p, cudaStream_t stream);  // kv_append4.cu
+
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream) {
+    if (p.cache_dtype == TA_INT4) return launch_kv_append4(p, stream);
     switch (p.dtype) {
     case TA_F32: return launch_t<float, 4>(p, stream);
     case TA_F16: return launch_t<__half, 8>(p, stream);
