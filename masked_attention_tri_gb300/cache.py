@@ -13,7 +13,7 @@ from typing import Optional, Union
 import torch
 
 from . import abi
-from .api import _DT, _check_out, _int32, _need, _on, _ptr, _row_stride, _stream
+from .api import _DT, _check_out, _int32, _need, _new, _on, _ptr, _row_stride, _stream
 from .positions import Rotary, _check_positions, _check_rotary
 
 _CACHE_DT = {**_DT, torch.float8_e4m3fn: abi.TA_E4M3}
@@ -184,7 +184,7 @@ def kv_cache_append(cache: Union[PagedKVCache, PagedKVCache4], k, v, page_table,
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("expected k (total, Hk, D)")
     dev = k.device
-    if dev.type != "cuda":
+    if not k.is_cuda:
         raise ValueError("kv_cache_append runs on CUDA tensors only")
     if cache.device != dev:
         raise ValueError(f"cache is on {cache.device}, expected {dev}")
@@ -206,7 +206,7 @@ def kv_cache_append(cache: Union[PagedKVCache, PagedKVCache4], k, v, page_table,
             raise ValueError("q is given only to be turned: pass rotary")
         q_rs, Hq = _rows(q, "q", dev, k.dtype, total, D), q.shape[1]
         if out_q is None:
-            out_q, qo_rs = torch.empty(q.shape, dtype=q.dtype, device=dev), Hq * D
+            out_q, qo_rs = _new(q), Hq * D
         else:
             qo_rs = _rows(out_q, "out_q", dev, k.dtype, total, D)
             if out_q.shape != q.shape:
@@ -255,7 +255,7 @@ def kv_cache_read(cache: Union[PagedKVCache, PagedKVCache4], page_table, kv_leng
     if not isinstance(cache, _CACHES):
         raise TypeError("cache must be a PagedKVCache or a PagedKVCache4")
     dev, Hk, D = cache.device, cache.heads, cache.head_dim
-    if dev.type != "cuda":
+    if not cache.k.is_cuda:
         raise ValueError("kv_cache_read runs on CUDA tensors only")
     S, MP = _table(page_table, kv_lengths, cu_seqlens, dev)
     max_seqlen = int(max_seqlen)
@@ -278,7 +278,8 @@ def kv_cache_read(cache: Union[PagedKVCache, PagedKVCache4], page_table, kv_leng
     if not codes and dtype != cache.dtype:
         raise TypeError(f"the cache holds {cache.dtype}, and its rows come back as that")
     if out_k is None:
-        out_k, out_v = (torch.empty(total, Hk, D, dtype=dtype, device=dev) for _ in range(2))
+        out_k = torch.empty(total, Hk, D, dtype=dtype, device=dev)
+        out_v = torch.empty_like(out_k)
         k_rs = v_rs = 0
     else:
         k_rs, v_rs = _rows(out_k, "out_k", dev, dtype, total, D), _rows(out_v, "out_v", dev, dtype, total, D)
@@ -322,7 +323,7 @@ def paged_attention(q, cache: Union[PagedKVCache, PagedKVCache4], page_table, kv
     if q.dim() != 3:
         raise ValueError("expected q (total_q, Hq, D)")
     dev = q.device
-    if dev.type != "cuda":
+    if not q.is_cuda:
         raise ValueError("paged_attention runs on CUDA tensors only")
     if cache.device != dev:
         raise ValueError(f"cache is on {cache.device}, expected {dev}")
@@ -345,7 +346,7 @@ def paged_attention(q, cache: Union[PagedKVCache, PagedKVCache4], page_table, kv
         raise ValueError("sinks must not be negative")
     s = 1.0 / math.sqrt(D) if scale is None else float(scale)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = _new(q)
     else:
         _check_out(out, q.shape, q.dtype)
         _need(out, "out", dev)

@@ -41,6 +41,8 @@
 // conversion instructions run at a quarter of that rate).  k index 2t, 2t + 1, 2t + 8, 2t + 9 of K's products stands for
 // elements e, e + 4, e + 1, e + 5 of lane t's word (it has whole groups of 16); of V a lane reads 8 NDC columns of four slots, whose
 // 16-bit halves side by side hold four columns' pairs.  The scales come into the stage by untiled copies beside the tiles.
+// The 64 sequences above in four bits: 163 us (644 MB, 3.9 TB/s; the copies alone 117, the arithmetic alone 155: 320
+// instructions a block of 16 slots, 128 of them the conversions).  Pages of 16, whose scales are copies of 128 bytes, 330 us.
 //
 // Roundings: P to the products' 16-bit type (fp16 for 8-bit and 4-bit caches: 2^-12 of a weight),
 // as everywhere in this library; S, the maxima, sums and O are fp32.  O is rescaled only
@@ -74,15 +76,6 @@ struct Blocks {
     static constexpr int value = M;
 };
 
-#ifndef TRIATTN_FOUR_WARPS
-#define TRIATTN_FOUR_WARPS 11
-#endif
-#ifndef TRIATTN_FOUR_WARPS2
-#define TRIATTN_FOUR_WARPS2 7
-#endif
-#ifndef TRIATTN_FOUR_BUFS
-#define TRIATTN_FOUR_BUFS 11
-#endif
 constexpr uint32_t kMmaSmem = 232448 - 1024 - 256;  // 227 KB less the alignment of the ring and the static part
 
 // What the producer tells of a stage; sc[i]: key scale, log2 and reciprocal of the value scale of the i-th
@@ -117,11 +110,12 @@ struct MmaConfig {
     // NT).  Measured on 64 sequences of 1k to 16k slots in 8 bits (before the warps took two blocks at once):
     // 7 warps 226 us, 11 warps 257, 15 warps 275: the more warps work on stages at a time, the fewer stages
     // are left for copies in flight.
-    // Four-bit codes are bound by their arithmetic's latencies, and their stages are small: more warps.
-    static constexpr int kWarps = kFour && NDC * NT <= 2 ? TRIATTN_FOUR_WARPS : kFour && NDC * NT <= 4 ? TRIATTN_FOUR_WARPS2 : 7;
+    // Four-bit codes are bound by their arithmetic, and their stages are small: eleven where the registers allow it
+    // (the same sequences, 32 and 64 query heads: 7 warps 164 and 168 us, 9 176 and 178, 11 163 and 166, 13 264 and 268).
+    static constexpr int kWarps = kFour && NDC * NT <= 2 ? 11 : 7;
     static constexpr int kThreads = (kWarps + 1) * 32;
     // Merge buffers: one for each warp where the ring keeps its six stages, else four taken in two turns.
-    static constexpr int kBufs = kFour ? (NT * NDC <= 2 ? TRIATTN_FOUR_BUFS : 4) : NT * NDC <= 2 ? kWarps : 4;
+    static constexpr int kBufs = NT * NDC <= 2 ? kWarps : 4;
     static constexpr int kOStride = NDC * 64 + 4;                       // floats of a merged row
     static constexpr uint32_t kQ = NDC * NT * 1024;  // Q in fragment order
     static constexpr uint32_t kO = (uint32_t)kBufs * kRows * kOStride * 4;

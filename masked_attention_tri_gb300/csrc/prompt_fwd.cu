@@ -491,10 +491,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
 
 template <bool BF16, int NB>
 cudaError_t start(const FwdParams& P, unsigned grid, cudaStream_t stream) {
-    auto kern = prompt_fwd_kernel<BF16, NB>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<NB>::kTotal);
+    const cudaError_t e = allow_smem<prompt_fwd_kernel<BF16, NB>>(Smem<NB>::kTotal);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kWarps * 32, Smem<NB>::kTotal, stream>>>(P);
+    prompt_fwd_kernel<BF16, NB><<<grid, kWarps * 32, Smem<NB>::kTotal, stream>>>(P);
     return cudaGetLastError();
 }
 

@@ -2,6 +2,8 @@
 // bounded waits.
 #pragma once
 
+#include <atomic>
+
 #include "prompt.cuh"
 #include "tc_kernel.cuh"
 
@@ -16,6 +18,20 @@ struct Tiles {
     FastDiv fd_hp, fd_hk;
 };
 Tiles make_tiles(const PromptParams& p);
+
+// A kernel's shared-memory limit, set once per device (an attribute call costs a part of a launch).
+template <auto Kernel>
+cudaError_t allow_smem(size_t bytes) {
+    static std::atomic<unsigned long long> set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev <= 63 && (set.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) set.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // wait_bar inline: a call keeps the compiler from giving a kernel's warps the registers that setmaxnreg gives them.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {

@@ -11,7 +11,7 @@ from typing import Optional
 import torch
 
 from . import abi
-from .api import _DT, _need, _on, _ptr, _row_stride, _stream
+from .api import _DT, _need, _new, _on, _ptr, _row_stride, _stream
 
 _SCALINGS = (None, "linear", "ntk", "yarn")
 
@@ -150,7 +150,7 @@ def _rotary_call(q, k, positions, rotary, inverse, out_q, out_k):
     if q.dim() != 3:
         raise ValueError("expected q (total, Hq, D)")
     dev = q.device
-    if dev.type != "cuda":
+    if not q.is_cuda:
         raise ValueError("rotary_embedding runs on CUDA tensors only")
     if q.dtype not in _DT:
         raise TypeError("q must be float32, float16 or bfloat16")
@@ -167,13 +167,13 @@ def _rotary_call(q, k, positions, rotary, inverse, out_q, out_k):
         if k.shape[2] != D:
             raise ValueError("k must have q's D")
         if out_k is None:
-            out_k, ko_rs = torch.empty(k.shape, dtype=k.dtype, device=dev), Hk * D
+            out_k, ko_rs = _new(k), Hk * D
         else:
             ko_rs = _rotary_rows(out_k, "out_k", dev, q.dtype, total)
             if out_k.shape != k.shape:
                 raise ValueError("out_k must have k's shape")
     if out_q is None:
-        out_q, qo_rs = torch.empty(q.shape, dtype=q.dtype, device=dev), Hq * D
+        out_q, qo_rs = _new(q), Hq * D
     else:
         qo_rs = _rotary_rows(out_q, "out_q", dev, q.dtype, total)
         if out_q.shape != q.shape:

@@ -10,7 +10,7 @@ import math
 import torch
 
 from . import abi
-from .api import _DT, _check_out, _need, _on, _ptr, _row_stride, _stream
+from .api import _DT, _check_out, _need, _new, _on, _ptr, _row_stride, _stream
 
 
 def _prompt_args(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale):
@@ -20,31 +20,32 @@ def _prompt_args(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k
             raise TypeError(f"{nm} must be a torch.Tensor")
         if t.dim() != 3:
             raise ValueError("expected q (total_q, Hq, D) and k, v (total_k, Hk, D)")
-    dev = q.device
-    if dev.type != "cuda":
+    if not q.is_cuda:
         raise ValueError("prompt_attention runs on CUDA tensors only")
-    if q.dtype not in _DT:
+    dev, dtype, kv_shape = q.device, q.dtype, k.shape
+    if dtype not in _DT:
         raise TypeError("q must be float32, float16 or bfloat16")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    if k.dtype != dtype or v.dtype != dtype:
         raise TypeError("q, k and v must share one dtype")
     total_q, Hq, D = q.shape
-    total_k, Hk = k.shape[:2]
-    if k.shape[2] != D or v.shape != k.shape:
+    total_k, Hk, Dk = kv_shape
+    if Dk != D or v.shape != kv_shape:
         raise ValueError("k and v must share their shape and q's D")
     if Hk == 0 or Hq == 0 or Hq % Hk:
         raise ValueError(f"q's heads must be a multiple of k's {Hk}")
     strides = _row_stride(q, "q", dev), _row_stride(k, "k", dev), _row_stride(v, "v", dev)
-    for t, nm in ((cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_k, "cu_seqlens_k")):
-        _need(t, nm, dev)
-        if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != cu_seqlens_q.numel() or t.numel() < 1:
-            raise ValueError("cu_seqlens_q and cu_seqlens_k must be int32 with num_seqs + 1 entries each")
+    _need(cu_seqlens_q, "cu_seqlens_q", dev)
+    _need(cu_seqlens_k, "cu_seqlens_k", dev)
     S = cu_seqlens_q.numel() - 1
+    if (cu_seqlens_q.dtype != torch.int32 or cu_seqlens_k.dtype != torch.int32 or S < 0 or cu_seqlens_q.dim() != 1
+            or cu_seqlens_k.dim() != 1 or cu_seqlens_k.numel() != S + 1):
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must be int32 with num_seqs + 1 entries each")
     if total_k == 0:  # (no key at all: some memory stands for the rows that no sequence has)
-        k = v = torch.empty(1, Hk, D, dtype=q.dtype, device=dev)
+        k = v = torch.empty(1, Hk, D, dtype=dtype, device=dev)
         strides = strides[0], 0, 0
     s = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    args = (_ptr(q), _ptr(k), _ptr(v), _DT[q.dtype], _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), S, total_q,
-            max(total_k, 1), int(max_seqlen_q), int(max_seqlen_k), Hq, Hk, D, s, *strides)
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _DT[dtype], cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), S, total_q,
+            total_k or 1, int(max_seqlen_q), int(max_seqlen_k), Hq, Hk, D, s, *strides)
     return args, S, (k, v)
 
 
@@ -63,7 +64,7 @@ def prompt_attention(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seql
     args, S, hold = _prompt_args(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale)
     dev = q.device
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = _new(q)
     else:
         _check_out(out, q.shape, q.dtype)
         _need(out, "out", dev)
@@ -90,8 +91,7 @@ def prompt_attention_backward(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
     _need(lse, "lse", dev)
     if lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, total_q):
         raise ValueError(f"lse must be float32 {(Hq, total_q)}")
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    dk, dv = (torch.empty(k.shape, dtype=q.dtype, device=dev) for _ in range(2))
+    dq, dk, dv = _new(q), _new(k), _new(k)
     if total_q == 0:  # (keys that no query sees)
         return dq, dk.zero_(), dv.zero_()
     if S:
