@@ -7,8 +7,10 @@
 // threads walk the tokens' units (V pairs, two vectors of 16 bytes each) in the order of memory,
 // so that a warp's loads cover whole kilobytes of one token's row.  The 16-bit values stay packed
 // until they are turned, two at a time: at 48 registers a thread five CTAs share an SM, which
-// does more for the loads in flight than longer queues of a thread (at 120 registers: 187 us).
-// 16384 tokens x 40 heads of 128 in bf16, both ways: 110 us, 6.1 TB/s.
+// does more for the loads in flight than longer queues of a thread (at 120 registers: 187 us).  A thread's first
+// loads are on their way while the table is made (two dependent loads, 64-bit products and a sincos a pair).
+// 16384 tokens x 40 heads of 128 in bf16, both ways: 105 us, 6.4 TB/s (106 with the table first); with three
+// axes, whose pairs look their axis up, 107 us (112).
 
 #include "internal.h"
 #include "rotary.cuh"
@@ -29,23 +31,15 @@ struct RotaryArgs {
     tc::FastDiv fd_heads;        // Hq + Hk
 };
 
-template <typename T, int V, bool INTER>
+template <typename T, int V, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
     extern __shared__ float4 table4[];
     float* table = reinterpret_cast<float*>(table4);
     const RotaryParams& p = a.p;
     const int tok0 = blockIdx.x * a.tokens, nt = min(a.tokens, p.total - tok0);
     const int np = p.dim / 2, nr = np / V, H = p.Hq + p.Hk;
-    for (int e = threadIdx.x; e < nt * np; e += kThreads) {
-        const int t = e / np, i = e - t * np;
-        const float2 cs = rotary_cos_sin(rotary_position(p.positions, p.axes, p.num_axes, i, p.total, tok0 + t), p.turns[i]);
-        rot_table_put<V>(table, t, i, nr, cs.x * p.mscale, (p.inverse ? -cs.y : cs.y) * p.mscale);
-    }
-    __syncthreads();
-
     // This thread's unit; its heads are hl, hl + lanes, ... of the CTA's tokens' in a row.
     const int hl = threadIdx.x / a.units, u = threadIdx.x - hl * a.units;
-    if (hl >= a.lanes) return;
     const RotUnit r = rot_unit<V>(u, p.D, p.dim, INTER);
     auto place = [&](int n, const T*& src, T*& dst) -> int {
         const int t = (int)a.fd_heads.div((uint32_t)n), h = n - t * H;
@@ -59,21 +53,33 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
         }
         return t;
     };
-    for (int n0 = hl; n0 < nt * H; n0 += kAhead * a.lanes) {
-        RotRaw<T, V> w[kAhead];
-        T* dst[kAhead];
-        int tok[kAhead];
+    const int all = hl < a.lanes ? nt * H : 0;
+    RotRaw<T, V> w[kAhead];
+    T* dst[kAhead];
+    int tok[kAhead];
+    auto load = [&](int n0) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int n = n0 + j * a.lanes;
-            if (n >= nt * H) break;
+            if (n >= all) break;
             const T* src;
             tok[j] = place(n, src, dst[j]);
             w[j].load(src, r.o1);
         }
+    };
+    load(hl);  // (on its way while the table is made)
+    for (int e = threadIdx.x; e < nt * np; e += kThreads) {
+        const int t = e / np, i = e - t * np;
+        const int at = rotary_position(p.positions, AXES ? p.axes : nullptr, p.num_axes, i, p.total, tok0 + t);
+        const float2 cs = rotary_cos_sin(at, p.turns[i]);
+        rot_table_put<V>(table, t, i, nr, cs.x * p.mscale, (p.inverse ? -cs.y : cs.y) * p.mscale);
+    }
+    __syncthreads();
+
+    for (int n0 = hl; n0 < all;) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            if (n0 + j * a.lanes >= nt * H) break;
+            if (n0 + j * a.lanes >= all) break;
             if (r.turned) {
                 float2 f[V];
                 rot_floats<T, V>(w[j], f);
@@ -82,7 +88,17 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
             }
             w[j].store(dst[j], r.o1);
         }
+        n0 += kAhead * a.lanes;
+        load(n0);
     }
+}
+
+// (Several axes are a kernel of their own: the choice in it cost one axis' calls 2%, 108.5 us for 106.1, with the table
+// first.)
+template <typename T, int V, bool INTER>
+void start(const RotaryArgs& a, unsigned grid, size_t smem, cudaStream_t stream) {
+    if (a.p.axes) rotary_kernel<T, V, INTER, true><<<grid, kThreads, smem, stream>>>(a);
+    else rotary_kernel<T, V, INTER, false><<<grid, kThreads, smem, stream>>>(a);
 }
 
 template <typename T, int V>
@@ -100,8 +116,8 @@ cudaError_t launch(const RotaryParams& p, cudaStream_t stream) {
     a.fd_heads = tc::make_fastdiv((uint32_t)H);
     const unsigned grid = (unsigned)(((long long)p.total + a.tokens - 1) / a.tokens);
     const size_t smem = (size_t)a.tokens * (p.dim / 2) * sizeof(float2);  // at most 4 KB
-    if (p.interleaved) rotary_kernel<T, V, true><<<grid, kThreads, smem, stream>>>(a);
-    else rotary_kernel<T, V, false><<<grid, kThreads, smem, stream>>>(a);
+    if (p.interleaved) start<T, V, true>(a, grid, smem, stream);
+    else start<T, V, false>(a, grid, smem, stream);
     return cudaGetLastError();
 }
 
