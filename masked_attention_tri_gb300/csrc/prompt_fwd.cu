@@ -213,103 +213,135 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
             if (!ok) *abort_flag = 1;
         } else if (warp == 12) {
             // ------------------------------------------------------------ MMA
+            // One thread runs the loop; the others help where a tile of V ends with rows that are not the sequence's.
             const bool leader = elect_one();
+            const int lead = __ffs((int)__ballot_sync(0xffffffffu, leader)) - 1;
             StageRing kr = {0, 0u, false};
-            Item<2> it;
-            uint32_t q_use[2] = {0u, 0u}, p_use[2] = {0u, 0u}, o_use[2] = {0u, 0u};
-            while (ok && next_item(it)) {
-                const int n0 = (it.keys[0] + 127) / 128, n1 = (it.keys[1] + 127) / 128, n = max(n0, n1);
-                const int lk = it.lq + it.shift;
-                auto wait_kv = [&](const StageRing& r) {
-                    if (ok) ok = __all_sync(0xffffffffu, wait(kv_full(r.idx), r.ph, abort_flag, p.status));
-                    tc_fence_after();
-                };
-                // S_i of key tile j, K in stage st
-                auto qk = [&](int i, int j, int st) {
-                    const int cols = min(128, (it.keys[i] - 128 * j + 15) & ~15);
-                    const uint32_t idesc = P.idesc_qk | ((uint32_t)(cols >> 3) << 17);
-                    const uint64_t a = sw128_desc(q_smem(i), 16, 1024), b = sw128_desc(kv_smem(st), 16, 1024);
-                    if (leader) {
-#pragma unroll
-                        for (int kk = 0; kk < 4 * NB; ++kk) {
-                            const uint64_t s = (uint64_t)(((kk >> 2) * kBox + (kk & 3) * 32) >> 4);
-                            if (kk < P.ksteps) mma_ss(tmem + i * 128, a + s, b + s, idesc, kk > 0 ? 1u : 0u);
-                        }
-                        mma_commit(s_full(i));
-                    }
-                };
-                // O_i += P_i V of key tile j, V in stage st
-                auto pv = [&](int i, int j, int st) {
-                    if (j == 0) {  // the epilogue has read the last item's O
-                        if (o_use[i] > 0)
-                            ok = ok && __all_sync(0xffffffffu, wait(o_empty(i), (o_use[i] - 1u) & 1u, abort_flag, p.status));
-                        ++o_use[i];
-                    }
-                    const int steps = min(8, (it.keys[i] - 128 * j + 15) / 16);
-                    const uint64_t b = sw128_desc(kv_smem(st), kBox, 1024);
-                    const uint32_t d = tmem + 256u + (uint32_t)i * kOCols, a = tmem + i * 128;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (ok) ok = __all_sync(0xffffffffu, wait(p_half(i, h), p_use[i] & 1u, abort_flag, p.status));
-                        if (!ok) return;
-                        tc_fence_after();
-                        if (leader) {
-#pragma unroll
-                            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                                if (kk < steps) mma_ts(d, a + kk * 8, b + (uint64_t)kk * 128, P.idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-                        }
-                    }
-                    ++p_use[i];
-                };
-                for (int i = 0; i < 2; ++i) {
-                    if (it.keys[i] <= 0) continue;
-                    if (ok) ok = __all_sync(0xffffffffu, wait(q_full(i), q_use[i] & 1u, abort_flag, p.status));
-                    ++q_use[i];
+            uint32_t use = 0;  // parities of tile i's barriers: bit i of Q, 2 + i of P, 4 + i of O; 6 + i: O was in use
+            auto await = [&](uint32_t b, uint32_t parity) {
+                if (ok) ok = wait(b, parity, abort_flag, p.status);
+                tc_fence_after();
+            };
+            // The next item that has keys: those of its tiles, and of its sequence.
+            auto fetch = [&](int& k0, int& k1, int& lk) -> bool {
+                for (;;) {
+                    const int r = item_n % kRing;
+                    await(it_full(r), (uint32_t)(item_n / kRing) & 1u);
+                    if (!ok) return false;
+                    const bool on = items[r].on != 0;
+                    k0 = items[r].keys[0];
+                    k1 = items[r].keys[1];
+                    lk = items[r].lq + items[r].shift;
+                    mbar_arrive(it_empty(r));
+                    ++item_n;
+                    if (!on || max(k0, k1) > 0) return on;
                 }
-                StageRing kst = kr, vst = kr;
-                if (n > 0) {
-                    wait_kv(kst);
-                    if (!ok) break;
-                    if (n0 > 0) qk(0, 0, kst.idx);
-                    if (n1 > 0) qk(1, 0, kst.idx);
-                    if (leader) {
-                        mma_commit(kv_empty(kst.idx));
-                        if (n0 == 1) mma_commit(q_empty(0));
-                        if (n1 == 1) mma_commit(q_empty(1));
-                    }
-                    kr.next(S);
+            };
+            // S_i of key tile j of a tile that sees `keys`, K in stage st
+            auto qk = [&](int i, int keys, int j, int st) {
+                if (j == 0) {
+                    await(q_full(i), (use >> i) & 1u);
+                    if (!ok) return;
+                    use ^= 1u << i;
                 }
-                // step j: PV of key tile j - 1 and QK of key tile j, tile 0 then tile 1
-                for (int j = 1; j <= n && ok; ++j) {
-                    vst = kr;
-                    kr.next(S);
-                    const bool more = j < n;
-                    if (more) {
-                        kst = kr;
+                const int cols = min(128, (keys - 128 * j + 15) & ~15);
+                issue_rows<NB>(tmem + i * 128, desc_lo(q_smem(i), 16), desc_lo(kv_smem(st), 16),
+                               P.idesc_qk | ((uint32_t)(cols >> 3) << 17), P.ksteps);
+                mma_commit(s_full(i));
+                if (128 * (j + 1) >= keys) mma_commit(q_empty(i));
+            };
+            // O_i += P_i V of key tile j, V in stage st
+            auto pv = [&](int i, int keys, int j, int st) {
+                if (j == 0) {  // the epilogue has read the last item's O
+                    if ((use >> (6 + i)) & 1u) {
+                        await(o_empty(i), (use >> (4 + i)) & 1u);
+                        use ^= 16u << i;
+                    }
+                    use |= 64u << i;
+                }
+                const int steps = min(8, (keys - 128 * j + 15) / 16);
+                const uint32_t b = desc_lo(kv_smem(st), kBox), d = tmem + 256u + (uint32_t)i * kOCols, a = tmem + i * 128;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    await(p_half(i, h), (use >> (2 + i)) & 1u);
+                    if (!ok) return;
+                    if (steps == 8) {
+#pragma unroll
+                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk) issue_ts(d, a + kk * 8, b + kk * 128u, P.idesc_pv, j > 0 || kk > 0);
+                    } else {
+#pragma unroll 1
+                        for (int kk = 4 * h; kk < min(steps, 4 * h + 4); ++kk)
+                            issue_ts(d, a + kk * 8, b + kk * 128u, P.idesc_pv, j > 0 || kk > 0);
+                    }
+                }
+                use ^= 4u << i;
+                if (128 * (j + 1) >= keys) mma_commit(o_full(i));
+            };
+            // Step j of an item: PV of key tile j - 1, tile 0 then tile 1, behind each QK of key tile j; after the last PV the next
+            // item's first, whose K tile is the next in the ring: its softmax runs while the other tile ends.
+            int k0 = 0, k1 = 0, lk = 0, n = 0, j = 0;
+            bool there = true, clean = false;
+            for (;;) {
+                int tail = 0, tail_st = 0;
+                if (leader) {
+                    if (j == 0) {
+                        there = fetch(k0, k1, lk);
+                        if (there) await(kv_full(kr.idx), kr.ph);
+                        if (there && ok && k0 > 0) qk(0, k0, 0, kr.idx);
+                        if (there && ok && k1 > 0) qk(1, k1, 0, kr.idx);
+                        if (there && ok) mma_commit(kv_empty(kr.idx));
                         kr.next(S);
+                        n = (max(k0, k1) + 127) / 128;
+                        j = 1;
                     }
-                    wait_kv(vst);
-                    if (!ok) break;
-                    const int valid = lk - 128 * (j - 1);  // rows of V that are the sequence's
-                    if (valid < 128) clear_rows<NB>(kv_smem(vst.idx), valid, (valid + 15) & ~15);
-                    bool k_here = false;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int ni = i == 0 ? n0 : n1;
-                        if (j - 1 < ni) pv(i, j - 1, vst.idx);
-                        if (!ok) break;
-                        if (leader && j == ni) mma_commit(o_full(i));
-                        if (i == 1 && leader) mma_commit(kv_empty(vst.idx));
-                        if (j < ni) {
-                            if (!k_here) wait_kv(kst);
-                            k_here = true;
+                    while (ok && there) {
+                        if (!clean) {
+                            await(kv_full(kr.idx), kr.ph);
                             if (!ok) break;
-                            qk(i, j, kst.idx);
-                            if (leader && j == ni - 1) mma_commit(q_empty(i));
+                            const int valid = lk - 128 * (j - 1);  // rows of V that are the sequence's
+                            if (valid < 128 && valid % 16) {
+                                tail = valid;
+                                tail_st = kr.idx;
+                                clean = true;
+                                break;
+                            }
+                        }
+                        clean = false;
+                        const int vst = kr.idx;
+                        kr.next(S);
+                        const bool last = j == n;
+                        int n0 = 0, n1 = 0, nlk = 0;
+                        bool k_here = false;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int keys = i ? k1 : k0;
+                            if (128 * (j - 1) < keys) pv(i, keys, j - 1, vst);
+                            if (!ok) break;
+                            if (i == 1) mma_commit(kv_empty(vst));
+                            if (i == 0 && last) there = fetch(n0, n1, nlk);
+                            const int to = last ? (i ? n1 : n0) : keys, at = last ? 0 : j;
+                            if (!ok || 128 * at >= to) continue;
+                            if (!k_here) await(kv_full(kr.idx), kr.ph);
+                            k_here = true;
+                            if (ok) qk(i, to, at, kr.idx);
+                        }
+                        if (k_here) {
+                            if (ok) mma_commit(kv_empty(kr.idx));
+                            kr.next(S);
+                        }
+                        ++j;
+                        if (last) {
+                            k0 = n0;
+                            k1 = n1;
+                            lk = nlk;
+                            n = (max(k0, k1) + 127) / 128;
+                            j = 1;
                         }
                     }
-                    if (more && ok && leader) mma_commit(kv_empty(kst.idx));
                 }
+                tail = __shfl_sync(0xffffffffu, tail, lead);
+                if (tail == 0) break;
+                clear_rows<NB>(kv_smem(__shfl_sync(0xffffffffu, tail_st, lead)), tail, (tail + 15) & ~15);
             }
             if (!ok && leader) *abort_flag = 1;
             if (leader) mma_commit(drain);

@@ -56,6 +56,47 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
+// Products issued by one thread.  A descriptor is its low word (start and leading offset; the high word is the same for all tiles
+// here: a stride of 1024 bytes, 128-byte swizzle), so that a step to the next 16 of K is one addition, and a thread that runs
+// its loop alone waits for no other lane: the thread that feeds the tensor core has 64 clocks for a product of 128 x 128 x 16.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | (lbo >> 4 << 16); }
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ void issue_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(add ? 1u : 0u), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b), "r"(idesc), "r"(add ? 1u : 0u), "n"(kDescHi)
+        : "memory");
+}
+// D = A B^T, A and B tiles of NB boxes of 64 columns in shared memory; `ksteps` sixteens of columns.
+template <int NB>
+__device__ __forceinline__ void issue_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int ksteps) {
+    if (ksteps == 4 * NB) {
+#pragma unroll
+        for (int kk = 0; kk < 4 * NB; ++kk) {
+            const uint32_t s = ((uint32_t)(kk >> 2) * kBox + (uint32_t)(kk & 3) * 32u) >> 4;
+            issue_ss(d, a + s, b + s, idesc, kk > 0);
+        }
+    } else {
+#pragma unroll 1
+        for (int kk = 0; kk < ksteps; ++kk) {
+            const uint32_t s = ((uint32_t)(kk >> 2) * kBox + (uint32_t)(kk & 3) * 32u) >> 4;
+            issue_ss(d, a + s, b + s, idesc, kk > 0);
+        }
+    }
+}
+
 // An item: PER tiles of one (sequence, key head).
 template <int PER>
 struct alignas(16) Item {
