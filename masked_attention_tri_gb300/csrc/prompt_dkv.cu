@@ -204,56 +204,55 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
         if (!ok) *abort_flag = 1;
     } else if (warp == 8) {
         // ------------------------------------------------------------ MMA
+        // One thread runs the loop; the others help where a tile ends with rows that are not the sequence's: they are another's, or
+        // nobody's, and are zeroed up to the next 16, which dV and dK multiply with zeros.
         const bool leader = elect_one();
-        auto wait_all = [&](uint32_t b, uint32_t parity) {
-            if (ok) ok = __all_sync(0xffffffffu, wait(b, parity, abort_flag, p.status));
+        const int lead = __ffs((int)__ballot_sync(0xffffffffu, leader)) - 1;
+        const int last_from = (blocks - 1) * P.t.ng, last_rows = min(P.t.tq, q.lq - (blocks - 1) * P.t.tq) * P.t.hp;
+        auto rows_of = [&](int j) { return first + j * P.splits < last_from ? full_rows : last_rows; };
+        auto await = [&](uint32_t b, uint32_t parity) {
+            if (ok) ok = wait(b, parity, abort_flag, p.status);
             tc_fence_after();
-            return ok;
         };
-        auto kstep = [](int kk) { return (uint64_t)(((kk >> 2) * kBox + (kk & 3) * 32) >> 4); };
-        const uint64_t kK = sw128_desc(base + M::kK, 16, 1024), vK = sw128_desc(base + M::kV, 16, 1024);
-        int tok, head, rows;
-        // S^T or dP^T of tile j.  (Rows of a tile past its own are another sequence's, or nobody's: zeroed up to the next 16,
-        // which dV and dK multiply with zeros.)
-        auto first_mma = [&](int j, bool dp) {
-            const int s = j & 1;
-            if (!wait_all(dp ? do_full(s) : q_full(s), (uint32_t)(j / 2) & 1u)) return;
-            const uint32_t at = dp ? do_smem(s) : q_smem(s);
-            tile(j, tok, head, rows);
-            if (rows < full_rows) clear_rows<NB>(at, rows, (rows + 15) & ~15);
+        bool clean = false;
+        for (int u = -2;;) {  // S(0), dP(0); then for each j: dV(j), S(j + 1), dK(j), dP(j + 1)
+            int tail = 0;
+            uint32_t tail_at = 0;
             if (leader) {
-                const uint64_t a = dp ? vK : kK, b = sw128_desc(at, 16, 1024);
-                const uint32_t d = dp ? tDP : tS;
-#pragma unroll
-                for (int kk = 0; kk < 4 * NB; ++kk)
-                    if (kk < P.ksteps) mma_ss(d, a + kstep(kk), b + kstep(kk), P.idesc_s, kk > 0 ? 1u : 0u);
-                mma_commit(dp ? dp_full : s_full);
+                if (u == -2 && !clean) await(kv_full, 0);
+                for (; ok && u < 4 * n; ++u) {
+                    const bool odd = u & 1, second = u < 0 ? odd : (u & 2) != 0;   // S or dP; and dP or dK
+                    const int j = u < 0 ? 0 : u / 4 + (odd ? 1 : 0), s = j & 1;
+                    if (u < 0 || odd) {
+                        if (j >= n) continue;
+                        const uint32_t at = second ? do_smem(s) : q_smem(s);
+                        if (!clean) {
+                            await(second ? do_full(s) : q_full(s), (uint32_t)(j / 2) & 1u);
+                            const int rows = rows_of(j);
+                            if (ok && rows < full_rows && rows % 16) {
+                                tail = rows;
+                                tail_at = at;
+                                clean = true;
+                                break;
+                            }
+                        }
+                        clean = false;
+                        if (!ok) break;
+                        issue_rows<NB>(second ? tDP : tS, desc_lo(base + (second ? M::kV : M::kK), 16), desc_lo(at, 16), P.idesc_s, P.ksteps);
+                        mma_commit(second ? dp_full : s_full);
+                    } else {
+                        await(second ? ds_full : p_full, (uint32_t)j & 1u);
+                        if (!ok) break;
+                        // (the rows of the second half: 64 columns on)
+                        issue_cols<64>(second ? tDK : tDV, second ? tDP : tS, desc_lo(second ? q_smem(s) : do_smem(s), kBox), P.idesc_g, 0, 8,
+                                       (rows_of(j) + 15) / 16, j == 0);
+                        mma_commit(second ? q_empty(s) : do_empty(s));
+                    }
+                }
             }
-        };
-        // dV += P^T dO or dK += dS^T Q of tile j: 16 rows a step, those of the second half 64 columns on
-        auto second_mma = [&](int j, bool dk_) {
-            if (!wait_all(dk_ ? ds_full : p_full, (uint32_t)j & 1u)) return;
-            tile(j, tok, head, rows);
-            if (leader) {
-                const int steps = (rows + 15) / 16;
-                const uint64_t b = sw128_desc(dk_ ? q_smem(j & 1) : do_smem(j & 1), kBox, 1024);
-                const uint32_t a = dk_ ? tDP : tS, d = dk_ ? tDK : tDV;
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    if (kk < steps)
-                        mma_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b + (uint64_t)kk * 128, P.idesc_g, (j > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(dk_ ? q_empty(j & 1) : do_empty(j & 1));
-            }
-        };
-        if (wait_all(kv_full, 0)) {
-            first_mma(0, false);
-            if (ok) first_mma(0, true);
-        }
-        for (int j = 0; j < n && ok; ++j) {
-            second_mma(j, false);
-            if (ok && j + 1 < n) first_mma(j + 1, false);
-            if (ok) second_mma(j, true);
-            if (ok && j + 1 < n) first_mma(j + 1, true);
+            tail = __shfl_sync(0xffffffffu, tail, lead);
+            if (tail == 0) break;
+            clear_rows<NB>(__shfl_sync(0xffffffffu, tail_at, lead), tail, (tail + 15) & ~15);
         }
         if (!ok && leader) *abort_flag = 1;
         if (leader) mma_commit(fin);

@@ -35,7 +35,7 @@ struct Smem {
     static constexpr uint32_t kTile = NB * kBox;
     static constexpr uint32_t kQ = 0, kDO = kTile, kK = 2 * kTile, kV = kK + kKStages * kTile;
     static constexpr uint32_t kItems = kV + kVStages * kTile, kClc = kItems + kRing * sizeof(Item<1>), kBars = kClc + 16;
-    static constexpr int kNumBars = 2 + 2 * kKStages + 2 * kVStages + 6 + 2 * kRing + 2;
+    static constexpr int kNumBars = 4 + 2 * kKStages + 2 * kVStages + 6 + 2 * kRing + 2;
     static constexpr uint32_t kSlot = kBars + 8 * kNumBars, kAbort = kSlot + 4, kTotal = kAbort + 4;
 };
 static_assert(Smem<2>::kTotal <= kMaxDynamicSmem, "shared memory");
@@ -53,10 +53,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(g0 + M::kSlot);
     Item<1>* items = reinterpret_cast<Item<1>*>(g0 + M::kItems);
     auto bar = [&](int i) { return base + M::kBars + 8u * (uint32_t)i; };
-    const uint32_t q_full = bar(0), q_empty = bar(1);
-    auto k_full = [&](int s) { return bar(2 + s); };
-    auto k_empty = [&](int s) { return bar(2 + kKStages + s); };
-    constexpr int b0 = 2 + 2 * kKStages;
+    const uint32_t q_full = bar(0), q_empty = bar(1), do_full = bar(2), do_empty = bar(3);
+    auto k_full = [&](int s) { return bar(4 + s); };
+    auto k_empty = [&](int s) { return bar(4 + kKStages + s); };
+    constexpr int b0 = 4 + 2 * kKStages;
     auto v_full = [&](int s) { return bar(b0 + s); };
     auto v_empty = [&](int s) { return bar(b0 + kVStages + s); };
     constexpr int b1 = b0 + 2 * kVStages;
@@ -73,6 +73,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
         *abort_flag = 0;
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
+        mbar_init(do_full, 1);
+        mbar_init(do_empty, 1);
 #pragma unroll 1
         for (int s = 0; s < kKStages; ++s) {
             mbar_init(k_full(s), 1);
@@ -139,16 +141,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
         while (ok && next_item(it)) {
             const int n = (it.keys[0] + 127) / 128;
             if (n == 0) continue;
-            if (q_use > 0) ok = __all_sync(0xffffffffu, wait(q_empty, (q_use - 1u) & 1u, abort_flag, p.status));
-            ++q_use;
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_expect_tx(q_full, 2 * q_bytes);
-                for (int b = 0; b < NB; ++b) {
-                    tma_load_3d(base + M::kQ + b * kBox, &P.tm_q, 64 * b, it.head[0], it.q0 + it.tok[0], q_full);
-                    tma_load_3d(base + M::kDO + b * kBox, &P.tm_do, 64 * b, it.head[0], it.q0 + it.tok[0], q_full);
+            // Q (false) or dO of the item's rows, when the last item's are read
+            auto load_rows = [&](bool d_o) {
+                const uint32_t full = d_o ? do_full : q_full;
+                if (ok && q_use > 0) ok = __all_sync(0xffffffffu, wait(d_o ? do_empty : q_empty, (q_use - 1u) & 1u, abort_flag, p.status));
+                if (ok && lane == 0) {
+                    mbar_expect_tx(full, q_bytes);
+                    for (int b = 0; b < NB; ++b)
+                        tma_load_3d(base + (d_o ? M::kDO : M::kQ) + b * kBox, d_o ? &P.tm_do : &P.tm_q, 64 * b, it.head[0],
+                                    it.q0 + it.tok[0], full);
                 }
-            }
+            };
             auto load = [&](StageRing& r, int stages, bool v, int j) {
                 const uint32_t full = v ? v_full(r.idx) : k_full(r.idx);
                 if (ok && r.wrapped)
@@ -161,83 +164,132 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                 }
                 r.next(stages);
             };
+            load(kr, kKStages, false, 0);
+            load_rows(false);
+            load_rows(true);
+            ++q_use;
             for (int j = 0; j < n && ok; ++j) {
-                load(kr, kKStages, false, j);
+                if (j > 0) load(kr, kKStages, false, j);
                 load(vr, kVStages, true, j);
             }
         }
         if (!ok) *abort_flag = 1;
     } else if (warp == 8) {
         // ------------------------------------------------------------ MMA
+        // One thread runs the loop; the others help where a tile of K ends with rows that are not the sequence's (dQ multiplies
+        // their zeros with them, sixteen keys at a time).
         const bool leader = elect_one();
+        const int lead = __ffs((int)__ballot_sync(0xffffffffu, leader)) - 1;
         StageRing ks = {0, 0u, false}, kq = {0, 0u, false}, vr = {0, 0u, false};  // K for S, K for dQ, V
-        Item<1> it;
-        uint32_t q_use = 0, ds_use = 0;
-        auto wait_all = [&](uint32_t b, uint32_t parity) {
-            if (ok) ok = __all_sync(0xffffffffu, wait(b, parity, abort_flag, p.status));
+        uint32_t ds_use = 0, items_s = 0, items_dp = 0;
+        auto await = [&](uint32_t b, uint32_t parity) {
+            if (ok) ok = wait(b, parity, abort_flag, p.status);
             tc_fence_after();
-            return ok;
         };
-        auto kstep = [](int kk) { return (uint64_t)(((kk >> 2) * kBox + (kk & 3) * 32) >> 4); };
-        const uint64_t qd = sw128_desc(base + M::kQ, 16, 1024), dod = sw128_desc(base + M::kDO, 16, 1024);
-        while (ok && next_item(it)) {
-            const int keys = it.keys[0], n = (keys + 127) / 128, lk = it.lq + it.shift;
-            if (n == 0) continue;
-            auto s_mma = [&](int j) {
-                if (!wait_all(k_full(ks.idx), ks.ph)) return;
-                // (rows of K that are not the sequence's: dQ multiplies their zeros with them, sixteen keys at a time)
-                if (lk - 128 * j < 128) clear_rows<NB>(k_smem(ks.idx), lk - 128 * j, (lk - 128 * j + 15) & ~15);
-                const uint32_t idesc = P.idesc_s | ((uint32_t)(min(128, (keys - 128 * j + 15) & ~15) >> 3) << 17);
-                if (leader) {
-                    const uint64_t b = sw128_desc(k_smem(ks.idx), 16, 1024);
-#pragma unroll
-                    for (int kk = 0; kk < 4 * NB; ++kk)
-                        if (kk < P.ksteps) mma_ss(tmem + (j & 1) * 128, qd + kstep(kk), b + kstep(kk), idesc, kk > 0 ? 1u : 0u);
-                    mma_commit(s_full(j & 1));
-                }
-                ks.next(kKStages);
-            };
-            auto dp_mma = [&](int j) {
-                if (!wait_all(v_full(vr.idx), vr.ph)) return;
-                const uint32_t idesc = P.idesc_s | ((uint32_t)(min(128, (keys - 128 * j + 15) & ~15) >> 3) << 17);
-                if (leader) {
-                    const uint64_t b = sw128_desc(v_smem(vr.idx), 16, 1024);
-#pragma unroll
-                    for (int kk = 0; kk < 4 * NB; ++kk)
-                        if (kk < P.ksteps) mma_ss(tDP, dod + kstep(kk), b + kstep(kk), idesc, kk > 0 ? 1u : 0u);
-                    mma_commit(dp_full);
-                    mma_commit(v_empty(vr.idx));
-                }
-                vr.next(kVStages);
-            };
-            if (!wait_all(q_full, q_use & 1u)) break;
-            s_mma(0);
-            if (ok) dp_mma(0);
-            if (ok && n > 1) s_mma(1);
-            for (int j = 0; j < n && ok; ++j) {
-                if (!wait_all(ds_full, ds_use & 1u)) break;
-                ++ds_use;
-                if (j + 1 < n) dp_mma(j + 1);
-                if (!ok) break;
-                if (j == 0 && q_use > 0 && !wait_all(dq_empty, (q_use - 1u) & 1u)) break;  // the last item's dQ is read
-                if (leader) {
-                    const int steps = min(8, (keys - 128 * j + 15) / 16);
-                    const uint64_t b = sw128_desc(k_smem(kq.idx), kBox, 1024);
-                    const uint32_t a = tmem + (j & 1) * 128;  // dS: 64 keys a half, the second 64 columns on
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        if (kk < steps)
-                            mma_ts(tDQ, a + (kk >> 2) * 64 + (kk & 3) * 8, b + (uint64_t)kk * 128, P.idesc_q, (j > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(k_empty(kq.idx));
-                    if (j == n - 1) {
-                        mma_commit(dq_full);
-                        mma_commit(q_empty);
-                    }
-                }
-                kq.next(kKStages);
-                if (j + 2 < n) s_mma(j + 2);
+        auto fetch = [&](int& keys, int& lk) -> bool {  // the next item that has keys
+            for (;;) {
+                const int r = item_n % kRing;
+                await(it_full(r), (uint32_t)(item_n / kRing) & 1u);
+                if (!ok) return false;
+                const bool on = items[r].on != 0;
+                keys = items[r].keys[0];
+                lk = items[r].lq + items[r].shift;
+                mbar_arrive(it_empty(r));
+                ++item_n;
+                if (!on || keys > 0) return on;
             }
-            ++q_use;
+        };
+        auto idesc_of = [&](int keys, int j) {
+            return P.idesc_s | ((uint32_t)(min(128, (keys - 128 * j + 15) & ~15) >> 3) << 17);
+        };
+        // Step m of an item: dP(m), dQ(m - 1), S(m + 1); in its last but one, S of the next item's first tile.  S and dS of tile m are
+        // in buffer (g + m) % 2, g tiles before the item.
+        int keys = 0, lk = 0, n = 0, m = -1, next_keys = 0, next_lk = 0;
+        uint32_t g = 0;
+        bool s_part = true, asked = false, there = true, clean = false;
+        for (;;) {
+            int tail = 0, tail_st = 0;
+            if (leader) {
+                while (ok) {
+                    if (s_part) {
+                        const bool in = m + 1 < n;
+                        if (!in && !asked) {
+                            asked = true;
+                            there = fetch(next_keys, next_lk);
+                            if (!ok) break;
+                            if (there) {
+                                await(q_full, items_s & 1u);
+                                ++items_s;
+                            }
+                        }
+                        if (in || there) {
+                            const int j = in ? m + 1 : 0, valid = (in ? lk : next_lk) - 128 * j;
+                            if (!clean) {
+                                await(k_full(ks.idx), ks.ph);
+                                if (!ok) break;
+                                if (valid < 128 && valid % 16) {
+                                    tail = valid;
+                                    tail_st = ks.idx;
+                                    clean = true;
+                                    break;
+                                }
+                            }
+                            clean = false;
+                            const uint32_t b = (g + (uint32_t)(m + 1)) & 1u;
+                            const int see = in ? keys : next_keys;
+                            issue_rows<NB>(tmem + b * 128u, desc_lo(base + M::kQ, 16), desc_lo(k_smem(ks.idx), 16), idesc_of(see, j),
+                                           P.ksteps);
+                            mma_commit(s_full((int)b));
+                            if (128 * (j + 1) >= see) mma_commit(q_empty);
+                            ks.next(kKStages);
+                        }
+                        s_part = false;
+                        ++m;
+                    }
+                    if (m > 0) {
+                        await(ds_full, ds_use & 1u);
+                        ++ds_use;
+                        if (!ok) break;
+                    }
+                    if (m < n) {
+                        if (m == 0) await(do_full, items_dp & 1u);
+                        await(v_full(vr.idx), vr.ph);
+                        if (!ok) break;
+                        issue_rows<NB>(tDP, desc_lo(base + M::kDO, 16), desc_lo(v_smem(vr.idx), 16), idesc_of(keys, m), P.ksteps);
+                        mma_commit(dp_full);
+                        mma_commit(v_empty(vr.idx));
+                        if (m == n - 1) mma_commit(do_empty);
+                        vr.next(kVStages);
+                    }
+                    if (m > 0) {
+                        if (m == 1 && items_dp > 0) await(dq_empty, (items_dp - 1u) & 1u);  // the last item's dQ is read
+                        if (!ok) break;
+                        // dS: 64 keys a half, the second 64 columns on
+                        issue_cols<64>(tDQ, tmem + ((g + (uint32_t)(m - 1)) & 1u) * 128u, desc_lo(k_smem(kq.idx), kBox), P.idesc_q, 0, 8,
+                                       min(8, (keys - 128 * (m - 1) + 15) / 16), m == 1);
+                        mma_commit(k_empty(kq.idx));
+                        kq.next(kKStages);
+                    }
+                    if (m < n) {
+                        s_part = true;
+                        continue;
+                    }
+                    if (n > 0) {
+                        mma_commit(dq_full);
+                        ++items_dp;
+                    }
+                    if (!there) break;
+                    g += (uint32_t)n;
+                    keys = next_keys;
+                    lk = next_lk;
+                    n = (keys + 127) / 128;
+                    m = 0;
+                    asked = false;
+                }
+            }
+            tail = __shfl_sync(0xffffffffu, tail, lead);
+            if (tail == 0) break;
+            clear_rows<NB>(k_smem(__shfl_sync(0xffffffffu, tail_st, lead)), tail, (tail + 15) & ~15);
         }
         if (!ok && leader) *abort_flag = 1;
         if (leader) mma_commit(drain);
@@ -251,7 +303,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
         const bool wide = p.D % 16 == 0 && (reinterpret_cast<uintptr_t>(p.dq) & 31) == 0;
         const float f = P.scale_log2e;
         Item<1> it;
-        uint32_t s_use[2] = {0u, 0u}, dp_use = 0, dq_use = 0;
+        uint32_t g = 0, dp_use = 0, dq_use = 0;  // tiles so far
         while (ok && next_item(it)) {
             const int keys = it.keys[0], n = (keys + 127) / 128;
             const bool row = r < it.rows[0];
@@ -275,8 +327,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                 delta = s.x + s.y;
                 if (half == 0) p.delta[at] = delta;
             }
-            for (int j = 0; j < n && ok; ++j) {
-                const int b = j & 1;
+            for (int j = 0; j < n && ok; ++j, ++g) {
+                const uint32_t b = g & 1u;
                 const uint32_t sA = tmem + lane_off + 128u * b + 64u * half, dpA = tDP + lane_off + 64u * half;
                 const bool edge = 128 * j + 127 > first;  // some row does not see every key
                 uint32_t see[2] = {0xffffffffu, 0xffffffffu};
@@ -284,8 +336,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
 #pragma unroll
                     for (int i = 0; i < 2; ++i) see[i] = low_bits(limit - 128 * j - 64 * half - 32 * i + 1);
                 }
-                const uint32_t use = b ? s_use[1]++ : s_use[0]++;
-                ok = __all_sync(0xffffffffu, wait(s_full(b), use & 1u, abort_flag, p.status));
+                ok = __all_sync(0xffffffffu, wait(s_full((int)b), (g >> 1) & 1u, abort_flag, p.status));
                 if (!ok) break;
                 tc_fence_after();
                 float pr[64];

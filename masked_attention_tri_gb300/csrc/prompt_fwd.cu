@@ -265,14 +265,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
                 for (int h = 0; h < 2; ++h) {
                     await(p_half(i, h), (use >> (2 + i)) & 1u);
                     if (!ok) return;
-                    if (steps == 8) {
-#pragma unroll
-                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk) issue_ts(d, a + kk * 8, b + kk * 128u, P.idesc_pv, j > 0 || kk > 0);
-                    } else {
-#pragma unroll 1
-                        for (int kk = 4 * h; kk < min(steps, 4 * h + 4); ++kk)
-                            issue_ts(d, a + kk * 8, b + kk * 128u, P.idesc_pv, j > 0 || kk > 0);
-                    }
+                    issue_cols<32>(d, a, b, P.idesc_pv, 4 * h, 4 * h + 4, steps, j == 0);
                 }
                 use ^= 4u << i;
                 if (128 * (j + 1) >= keys) mma_commit(o_full(i));

@@ -96,6 +96,20 @@ __device__ __forceinline__ void issue_rows(uint32_t d, uint32_t a, uint32_t b, u
         }
     }
 }
+// D += A B, A: rows x up to 128 of K in tensor memory, the second 64 of K `HALF` columns on; B: those rows of a tile in shared memory.
+// Sixteens [from, to) of K, of `steps` that there are.
+template <int HALF>
+__device__ __forceinline__ void issue_cols(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int from, int to, int steps, bool fresh) {
+    if (steps == 8) {
+#pragma unroll
+        for (int kk = from; kk < to; ++kk)
+            issue_ts(d, a + (uint32_t)((kk >> 2) * HALF + (kk & 3) * 8), b + (uint32_t)kk * 128u, idesc, !fresh || kk > 0);
+    } else {
+#pragma unroll 1
+        for (int kk = from; kk < min(to, steps); ++kk)
+            issue_ts(d, a + (uint32_t)((kk >> 2) * HALF + (kk & 3) * 8), b + (uint32_t)kk * 128u, idesc, !fresh || kk > 0);
+    }
+}
 
 // An item: PER tiles of one (sequence, key head).
 template <int PER>
