@@ -31,14 +31,15 @@ struct DkvParams {
 };
 
 constexpr int kWarps = 12;
+constexpr int kQStages = 3;    // (a tile of Q stays until dK: with two stages the next but one came too late)
 
 template <int NB>
 struct Smem {
     static constexpr uint32_t kTile = NB * kBox;
-    static constexpr uint32_t kK = 0, kV = kTile, kQ = 2 * kTile, kDO = kQ + 2 * kTile;
+    static constexpr uint32_t kK = 0, kV = kTile, kQ = 2 * kTile, kDO = kQ + kQStages * kTile;
     static constexpr uint32_t kRows = kDO + 2 * kTile;                 // [2 stages][-lse log2 e, delta][128]
     static constexpr uint32_t kBars = kRows + 2 * 2 * 128 * 4;
-    static constexpr int kNumBars = 1 + 2 * 2 + 2 * 2 + 2 * 2 + 5;
+    static constexpr int kNumBars = 1 + 2 * kQStages + 2 * 2 + 2 * 2 + 5;
     static constexpr uint32_t kSlot = kBars + 8 * kNumBars, kAbort = kSlot + 4, kTotal = kAbort + 4;
 };
 static_assert(Smem<2>::kTotal <= kMaxDynamicSmem, "shared memory");
@@ -104,21 +105,26 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
     auto bar = [&](int i) { return base + M::kBars + 8u * (uint32_t)i; };
     const uint32_t kv_full = bar(0);
     auto q_full = [&](int s) { return bar(1 + s); };
-    auto q_empty = [&](int s) { return bar(3 + s); };
-    auto do_full = [&](int s) { return bar(5 + s); };
-    auto do_empty = [&](int s) { return bar(7 + s); };
-    auto row_full = [&](int s) { return bar(9 + s); };
-    auto row_empty = [&](int s) { return bar(11 + s); };
-    const uint32_t s_full = bar(13), p_full = bar(14), dp_full = bar(15), ds_full = bar(16), fin = bar(17);
+    auto q_empty = [&](int s) { return bar(1 + kQStages + s); };
+    constexpr int b0 = 1 + 2 * kQStages;
+    auto do_full = [&](int s) { return bar(b0 + s); };
+    auto do_empty = [&](int s) { return bar(b0 + 2 + s); };
+    auto row_full = [&](int s) { return bar(b0 + 4 + s); };
+    auto row_empty = [&](int s) { return bar(b0 + 6 + s); };
+    const uint32_t s_full = bar(b0 + 8), p_full = bar(b0 + 9), dp_full = bar(b0 + 10), ds_full = bar(b0 + 11), fin = bar(b0 + 12);
+    static_assert(b0 + 13 == M::kNumBars, "barriers");
     auto q_smem = [&](int s) { return base + M::kQ + (uint32_t)s * kTile; };
     auto do_smem = [&](int s) { return base + M::kDO + (uint32_t)s * kTile; };
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         mbar_init(kv_full, 1);
 #pragma unroll 1
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < kQStages; ++s) {
             mbar_init(q_full(s), 1);
             mbar_init(q_empty(s), 1);
+        }
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
             mbar_init(do_full(s), 1);
             mbar_init(do_empty(s), 1);
             mbar_init(row_full(s), 1);
@@ -133,7 +139,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
     }
     // Rows of Q and dO that no box fills (tq hp < 128) stay zeros.
     const int full_rows = P.t.tq * P.t.hp;
-    for (int e = threadIdx.x; e < 4 * NB * (128 - full_rows) * 8; e += kWarps * 32) {
+    for (int e = threadIdx.x; e < (kQStages + 2) * NB * (128 - full_rows) * 8; e += kWarps * 32) {
         const int c = e % 8, r = e / 8 % (128 - full_rows) + full_rows, b = e / 8 / (128 - full_rows);
         st_shared_v4(base + M::kQ + (uint32_t)b * kBox + (uint32_t)r * 128u + c * 16u, 0u, 0u, 0u, 0u);
     }
@@ -160,16 +166,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
             }
         }
         const uint32_t bytes = (uint32_t)full_rows * 128u * NB;
+        StageRing qr = {0, 0u, false};
         for (int j = 0; j < n && ok; ++j) {
             int tok, head, rows;
             tile(j, tok, head, rows);
             const int s = j & 1;
             const uint32_t before = (uint32_t)(j / 2 - 1) & 1u;
-            if (j >= 2) ok = __all_sync(0xffffffffu, wait(q_empty(s), before, abort_flag, p.status));
+            if (qr.wrapped) ok = __all_sync(0xffffffffu, wait(q_empty(qr.idx), qr.ph ^ 1u, abort_flag, p.status));
             if (ok && lane == 0) {
-                mbar_expect_tx(q_full(s), bytes);
-                for (int b = 0; b < NB; ++b) tma_load_3d(q_smem(s) + b * kBox, &P.tm_q, 64 * b, head, q.q0 + tok, q_full(s));
+                mbar_expect_tx(q_full(qr.idx), bytes);
+                for (int b = 0; b < NB; ++b)
+                    tma_load_3d(q_smem(qr.idx) + b * kBox, &P.tm_q, 64 * b, head, q.q0 + tok, q_full(qr.idx));
             }
+            qr.next(kQStages);
             if (j >= 2 && ok) ok = __all_sync(0xffffffffu, wait(do_empty(s), before, abort_flag, p.status));
             if (ok && lane == 0) {
                 mbar_expect_tx(do_full(s), bytes);
@@ -214,40 +223,72 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
             if (ok) ok = wait(b, parity, abort_flag, p.status);
             tc_fence_after();
         };
+        const int steps = (full_rows + 15) / 16;
+        const int whole = P.ksteps == 4 * NB && steps == 8 ? max(0, (last_from - first + P.splits - 1) / P.splits) : 0;  // tiles before the last block's
+        StageRing qs = {0, 0u, false}, qk = {0, 0u, false};  // Q for S, Q for dK
         bool clean = false;
         for (int u = -2;;) {  // S(0), dP(0); then for each j: dV(j), S(j + 1), dK(j), dP(j + 1)
             int tail = 0;
             uint32_t tail_at = 0;
             if (leader) {
                 if (u == -2 && !clean) await(kv_full, 0);
-                for (; ok && u < 4 * n; ++u) {
+                while (ok && u < 4 * n) {
+                    // Whole tiles, without a question (a few dozen instructions of one thread are a product's time).
+                    for (; u > 0 && (u & 3) == 0 && u / 4 + 1 < whole; u += 4) {
+                        const uint32_t ph = (uint32_t)(u >> 2) & 1u, to = (uint32_t)(u >> 3);  // (tile j = u / 4's parity; dO(j + 1)'s below)
+                        const int s = (int)ph;
+                        await(p_full, ph);
+                        if (!ok) break;
+                        issue_cols<64>(tDV, tS, desc_lo(do_smem(s), kBox), P.idesc_g, 0, 8, 8, false);
+                        mma_commit(do_empty(s));
+                        await(q_full(qs.idx), qs.ph);
+                        if (!ok) break;
+                        issue_rows<NB>(tS, desc_lo(base + M::kK, 16), desc_lo(q_smem(qs.idx), 16), P.idesc_s, 4 * NB);
+                        mma_commit(s_full);
+                        qs.next(kQStages);
+                        await(ds_full, ph);
+                        if (!ok) break;
+                        issue_cols<64>(tDK, tDP, desc_lo(q_smem(qk.idx), kBox), P.idesc_g, 0, 8, 8, false);
+                        mma_commit(q_empty(qk.idx));
+                        qk.next(kQStages);
+                        await(do_full(s ^ 1), (to + ph) & 1u);
+                        if (!ok) break;
+                        issue_rows<NB>(tDP, desc_lo(base + M::kV, 16), desc_lo(do_smem(s ^ 1), 16), P.idesc_s, 4 * NB);
+                        mma_commit(dp_full);
+                    }
+                    if (!ok || u >= 4 * n) break;
                     const bool odd = u & 1, second = u < 0 ? odd : (u & 2) != 0;   // S or dP; and dP or dK
                     const int j = u < 0 ? 0 : u / 4 + (odd ? 1 : 0), s = j & 1;
                     if (u < 0 || odd) {
-                        if (j >= n) continue;
-                        const uint32_t at = second ? do_smem(s) : q_smem(s);
-                        if (!clean) {
-                            await(second ? do_full(s) : q_full(s), (uint32_t)(j / 2) & 1u);
-                            const int rows = rows_of(j);
-                            if (ok && rows < full_rows && rows % 16) {
-                                tail = rows;
-                                tail_at = at;
-                                clean = true;
-                                break;
+                        if (j < n) {
+                            const uint32_t at = second ? do_smem(s) : q_smem(qs.idx);
+                            if (!clean) {
+                                await(second ? do_full(s) : q_full(qs.idx), second ? (uint32_t)(j / 2) & 1u : qs.ph);
+                                const int rows = rows_of(j);
+                                if (ok && rows < full_rows && rows % 16) {
+                                    tail = rows;
+                                    tail_at = at;
+                                    clean = true;
+                                    break;
+                                }
                             }
+                            clean = false;
+                            if (!ok) break;
+                            issue_rows<NB>(second ? tDP : tS, desc_lo(base + (second ? M::kV : M::kK), 16), desc_lo(at, 16), P.idesc_s,
+                                           P.ksteps);
+                            mma_commit(second ? dp_full : s_full);
+                            if (!second) qs.next(kQStages);
                         }
-                        clean = false;
-                        if (!ok) break;
-                        issue_rows<NB>(second ? tDP : tS, desc_lo(base + (second ? M::kV : M::kK), 16), desc_lo(at, 16), P.idesc_s, P.ksteps);
-                        mma_commit(second ? dp_full : s_full);
                     } else {
                         await(second ? ds_full : p_full, (uint32_t)j & 1u);
                         if (!ok) break;
                         // (the rows of the second half: 64 columns on)
-                        issue_cols<64>(second ? tDK : tDV, second ? tDP : tS, desc_lo(second ? q_smem(s) : do_smem(s), kBox), P.idesc_g, 0, 8,
-                                       (rows_of(j) + 15) / 16, j == 0);
-                        mma_commit(second ? q_empty(s) : do_empty(s));
+                        issue_cols<64>(second ? tDK : tDV, second ? tDP : tS, desc_lo(second ? q_smem(qk.idx) : do_smem(s), kBox), P.idesc_g, 0,
+                                       8, (rows_of(j) + 15) / 16, j == 0);
+                        mma_commit(second ? q_empty(qk.idx) : do_empty(s));
+                        if (second) qk.next(kQStages);
                     }
+                    ++u;
                 }
             }
             tail = __shfl_sync(0xffffffffu, tail, lead);

@@ -211,6 +211,28 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
             int tail = 0, tail_st = 0;
             if (leader) {
                 while (ok) {
+                    // Whole key tiles in the middle of an item, without a question.
+                    for (const int whole = P.ksteps == 4 * NB ? keys : 0; s_part && m > 0 && 128 * (m + 2) < whole; ++m) {
+                        const uint32_t b = (g + (uint32_t)m) & 1u, b2 = tmem + (b ^ 1u) * 128u;  // of tile m; tile m + 1's (and m - 1's)
+                        const uint32_t idesc = P.idesc_s | (16u << 17);
+                        await(k_full(ks.idx), ks.ph);
+                        if (!ok) break;
+                        issue_rows<NB>(b2, desc_lo(base + M::kQ, 16), desc_lo(k_smem(ks.idx), 16), idesc, 4 * NB);
+                        mma_commit(s_full((int)(b ^ 1u)));
+                        ks.next(kKStages);
+                        await(ds_full, ds_use & 1u);
+                        ++ds_use;
+                        await(v_full(vr.idx), vr.ph);
+                        if (!ok) break;
+                        issue_rows<NB>(tDP, desc_lo(base + M::kDO, 16), desc_lo(v_smem(vr.idx), 16), idesc, 4 * NB);
+                        mma_commit(dp_full);
+                        mma_commit(v_empty(vr.idx));
+                        vr.next(kVStages);
+                        issue_cols<64>(tDQ, tmem + b * 128u, desc_lo(k_smem(kq.idx), kBox), P.idesc_q, 0, 8, 8, false);
+                        mma_commit(k_empty(kq.idx));
+                        kq.next(kKStages);
+                    }
+                    if (!ok) break;
                     if (s_part) {
                         const bool in = m + 1 < n;
                         if (!in && !asked) {

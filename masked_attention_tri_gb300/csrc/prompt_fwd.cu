@@ -167,9 +167,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
         return it.on != 0;
     };
 
-    // (the block has 128 registers a thread: 2 x 192 + 72 + 56 = 4 x 128)
+    // (the block has 128 registers a thread: 2 x 184 + 80 + 64 = 4 x 128)
     if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 14) {
             // ------------------------------------------------------------ the items
             ok = hand_out<2, kRing>(p, P.t, items, it_full, it_empty, base + M::kClc, clc, abort_flag);
@@ -288,6 +288,42 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
                         j = 1;
                     }
                     while (ok && there) {
+                        // Whole key tiles in the middle of an item, without a question (a few dozen instructions of one thread are a
+                        // product's time).
+                        for (const int whole = P.ksteps == 4 * NB ? min(k0, k1) : 0; j > 1 && 128 * (j + 1) < whole; ++j) {
+                            const int vst = kr.idx;
+                            const uint32_t vph = kr.ph;
+                            kr.next(S);
+                            const uint32_t v = desc_lo(kv_smem(vst), kBox), k = desc_lo(kv_smem(kr.idx), 16);
+                            const uint32_t pp = (use >> 2) & 1u, pq = (use >> 3) & 1u;
+                            ok = wait(kv_full(vst), vph, abort_flag, p.status);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t d = tmem + 256u + (uint32_t)i * kOCols, a = tmem + i * 128;
+                                if (ok) ok = wait(p_half(i, 0), i ? pq : pp, abort_flag, p.status);
+                                tc_fence_after();
+                                if (!ok) break;
+                                issue_cols<32>(d, a, v, P.idesc_pv, 0, 4, 8, false);
+                                ok = wait(p_half(i, 1), i ? pq : pp, abort_flag, p.status);
+                                tc_fence_after();
+                                if (!ok) break;
+                                issue_cols<32>(d, a, v, P.idesc_pv, 4, 8, 8, false);
+                                if (i == 0) {
+                                    ok = wait(kv_full(kr.idx), kr.ph, abort_flag, p.status);
+                                    tc_fence_after();
+                                    if (!ok) break;
+                                } else {
+                                    mma_commit(kv_empty(vst));
+                                }
+                                issue_rows<NB>(a, desc_lo(q_smem(i), 16), k, P.idesc_qk | (16u << 17), 4 * NB);
+                                mma_commit(s_full(i));
+                            }
+                            if (!ok) break;
+                            mma_commit(kv_empty(kr.idx));
+                            kr.next(S);
+                            use ^= 12u;
+                        }
+                        if (!ok) break;
                         if (!clean) {
                             await(kv_full(kr.idx), kr.ph);
                             if (!ok) break;
@@ -343,7 +379,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
         }
     } else if (warp < 8) {
         // ------------------------------------------------------------ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int i = warp / 4, r = warp % 4 * 32 + lane;
         const uint32_t lane_off = (uint32_t)(warp % 4 * 32) << 16;
         const uint32_t st = tmem + lane_off + i * 128, ot = tmem + lane_off + 256u + (uint32_t)i * kOCols;
@@ -442,7 +478,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
         if (!ok) *abort_flag = 1;
     } else {
         // ------------------------------------------------------------ epilogue
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const int wq = warp % 4, r = wq * 32 + lane;
         const int tok_r = (int)P.t.fd_hp.div((uint32_t)r), head_r = r - tok_r * P.t.hp;
         const bool wide = p.D % 16 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;  // rows in 32-byte pieces
