@@ -341,13 +341,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
                         const bool last = j == n;
                         int n0 = 0, n1 = 0, nlk = 0;
                         bool k_here = false;
+                        if (last) there = fetch(n0, n1, nlk);  // (while the last P is made)
+                        if (!ok) break;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const int keys = i ? k1 : k0;
                             if (128 * (j - 1) < keys) pv(i, keys, j - 1, vst);
                             if (!ok) break;
                             if (i == 1) mma_commit(kv_empty(vst));
-                            if (i == 0 && last) there = fetch(n0, n1, nlk);
                             const int to = last ? (i ? n1 : n0) : keys, at = last ? 0 : j;
                             if (!ok || 128 * at >= to) continue;
                             if (!k_here) await(kv_full(kr.idx), kr.ph);
