@@ -3,15 +3,16 @@
 //
 // A tile of rows (prompt_tc.cuh) walks the key tiles that it sees, as in the forward, with P = 2^(s - lse) recomputed:
 //     S = Q K^T, dP = dO V^T             rows on the tensor-memory lanes
-//     dS = P (dP - delta)                as 16-bit pairs over S
+//     dS = P (dP - delta)                as 16-bit pairs over dP
 //     dQ += dS K                         dS from tensor memory
 // lse and delta are one number a thread, dQ stays in tensor memory, and is rounded once: no sum in memory, no order that varies.
 // (One kernel for dQ, dK and dV computes S and dP once, five products a tile where the two kernels have seven; but its dQ has to be added
 // up in memory over the key tiles and stands between the tiles' products, and four 128 x 128 x D products a tile from shared memory are more
 // than that gives: four sequences of 8192 tokens, 16 heads over 4 of 128, 3.86 ms, of which 0.5 ms were the reductions.)
 //
-// One CTA a SM, 12 warps: 0-7 softmax and dS (a row's two halves of 64 keys each), 8 MMA, 9 TMA, 10 the items.  Tensor memory: S twice, dP,
-// dQ: 4 x 128 columns at D = 128.  S of the next tile is there while dS is formed, dP follows as soon as the last one is read.
+// One CTA a SM, 12 warps: 0-7 softmax and dS (a row's two halves of 64 keys each), 8 MMA, 9 TMA, 10 the items.  Tensor memory: S, dP
+// twice (dS over it), dQ: 4 x 128 columns at D = 128.  The tensor core's order is dQ(i - 2), S(i), dP(i): S(i) follows as soon as S(i - 1) is
+// in registers, and both are there when dS(i - 1) is done, across items too.
 #include "prompt_tc.cuh"
 
 namespace triattn {
@@ -35,7 +36,7 @@ struct Smem {
     static constexpr uint32_t kTile = NB * kBox;
     static constexpr uint32_t kQ = 0, kDO = kTile, kK = 2 * kTile, kV = kK + kKStages * kTile;
     static constexpr uint32_t kItems = kV + kVStages * kTile, kClc = kItems + kRing * sizeof(Item<1>), kBars = kClc + 16;
-    static constexpr int kNumBars = 4 + 2 * kKStages + 2 * kVStages + 6 + 2 * kRing + 2;
+    static constexpr int kNumBars = 4 + 2 * kKStages + 2 * kVStages + 8 + 2 * kRing + 2;
     static constexpr uint32_t kSlot = kBars + 8 * kNumBars, kAbort = kSlot + 4, kTotal = kAbort + 4;
 };
 static_assert(Smem<2>::kTotal <= kMaxDynamicSmem, "shared memory");
@@ -60,12 +61,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
     auto v_full = [&](int s) { return bar(b0 + s); };
     auto v_empty = [&](int s) { return bar(b0 + kVStages + s); };
     constexpr int b1 = b0 + 2 * kVStages;
-    auto s_full = [&](int b) { return bar(b1 + b); };
-    const uint32_t dp_full = bar(b1 + 2), ds_full = bar(b1 + 3), dq_full = bar(b1 + 4), dq_empty = bar(b1 + 5);
-    auto it_full = [&](int r) { return bar(b1 + 6 + r); };
-    auto it_empty = [&](int r) { return bar(b1 + 6 + kRing + r); };
-    const uint32_t clc = bar(b1 + 6 + 2 * kRing), drain = bar(b1 + 7 + 2 * kRing);
-    static_assert(b1 + 8 + 2 * kRing == M::kNumBars, "barriers");
+    const uint32_t s_full = bar(b1), s_read = bar(b1 + 1);
+    auto dp_full = [&](uint32_t b) { return bar(b1 + 2 + (int)b); };
+    auto ds_full = [&](uint32_t b) { return bar(b1 + 4 + (int)b); };
+    const uint32_t dq_full = bar(b1 + 6), dq_empty = bar(b1 + 7);
+    auto it_full = [&](int r) { return bar(b1 + 8 + r); };
+    auto it_empty = [&](int r) { return bar(b1 + 8 + kRing + r); };
+    const uint32_t clc = bar(b1 + 8 + 2 * kRing), drain = bar(b1 + 9 + 2 * kRing);
+    static_assert(b1 + 10 + 2 * kRing == M::kNumBars, "barriers");
     auto k_smem = [&](int s) { return base + M::kK + (uint32_t)s * kTile; };
     auto v_smem = [&](int s) { return base + M::kV + (uint32_t)s * kTile; };
 
@@ -85,10 +88,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
             mbar_init(v_full(s), 1);
             mbar_init(v_empty(s), 1);
         }
-        mbar_init(s_full(0), 1);
-        mbar_init(s_full(1), 1);
-        mbar_init(dp_full, 1);
-        mbar_init(ds_full, 8);
+        mbar_init(s_full, 1);
+        mbar_init(s_read, 8);
+#pragma unroll 1
+        for (uint32_t b = 0; b < 2; ++b) {
+            mbar_init(dp_full(b), 1);
+            mbar_init(ds_full(b), 8);
+        }
         mbar_init(dq_full, 1);
         mbar_init(dq_empty, 8);
         for (int r = 0; r < kRing; ++r) {
@@ -114,7 +120,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot, tDP = tmem + 256, tDQ = tmem + 384;
+    const uint32_t tmem = *tmem_slot, tDP = tmem + 128, tDQ = tmem + 384;  // S, dP and dS twice, dQ
     bool ok = true;
     int item_n = 0;
     auto next_item = [&](Item<1>& it) -> bool {
@@ -181,7 +187,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
         const bool leader = elect_one();
         const int lead = __ffs((int)__ballot_sync(0xffffffffu, leader)) - 1;
         StageRing ks = {0, 0u, false}, kq = {0, 0u, false}, vr = {0, 0u, false};  // K for S, K for dQ, V
-        uint32_t ds_use = 0, items_s = 0, items_dp = 0;
         auto await = [&](uint32_t b, uint32_t parity) {
             if (ok) ok = wait(b, parity, abort_flag, p.status);
             tc_fence_after();
@@ -199,114 +204,104 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                 if (!on || keys > 0) return on;
             }
         };
-        auto idesc_of = [&](int keys, int j) {
-            return P.idesc_s | ((uint32_t)(min(128, (keys - 128 * j + 15) & ~15) >> 3) << 17);
+        // dQ of tile u (of all that the CTA walks), whose dS is in buffer u % 2
+        auto dq_mma = [&](uint32_t u, int steps, bool fresh) {
+            issue_cols<64>(tDQ, tDP + (u & 1u) * 128u, desc_lo(k_smem(kq.idx), kBox), P.idesc_q, 0, 8, steps, fresh);
+            mma_commit(k_empty(kq.idx));
+            kq.next(kKStages);
         };
-        // Step m of an item: dP(m), dQ(m - 1), S(m + 1); in its last but one, S of the next item's first tile.  S and dS of tile m are
-        // in buffer (g + m) % 2, g tiles before the item.
-        int keys = 0, lk = 0, n = 0, m = -1, next_keys = 0, next_lk = 0;
-        uint32_t g = 0;
-        bool s_part = true, asked = false, there = true, clean = false;
+        // S of tile u, K there, and dP of it
+        auto s_mma = [&](uint32_t u, uint32_t idesc, int ksteps) {
+            if (u > 0) await(s_read, (u - 1u) & 1u);
+            if (!ok) return;
+            issue_rows<NB>(tmem, desc_lo(base + M::kQ, 16), desc_lo(k_smem(ks.idx), 16), idesc, ksteps);
+            mma_commit(s_full);
+            ks.next(kKStages);
+        };
+        auto dp_mma = [&](uint32_t u, uint32_t idesc, int ksteps) {
+            await(v_full(vr.idx), vr.ph);
+            if (!ok) return;
+            issue_rows<NB>(tDP + (u & 1u) * 128u, desc_lo(base + M::kDO, 16), desc_lo(v_smem(vr.idx), 16), idesc, ksteps);
+            mma_commit(dp_full(u & 1u));
+            mma_commit(v_empty(vr.idx));
+            vr.next(kVStages);
+        };
+        // Step u: dQ of tile u - 2, S and dP of tile u, which is tile j of an item.  Of the two tiles between: sixteens of keys, 16
+        // for an item's first, 32 for its last (0: no tile).
+        int keys = 0, lk = 0, j = 0, one = 0, two = 0;
+        uint32_t u = 0, items_in = 0, items_out = 0;
+        bool there = true, ask = true, clean = false;
         for (;;) {
             int tail = 0, tail_st = 0;
             if (leader) {
                 while (ok) {
-                    // Whole key tiles in the middle of an item, without a question.
-                    for (const int whole = P.ksteps == 4 * NB ? keys : 0; s_part && m > 0 && 128 * (m + 2) < whole; ++m) {
-                        const uint32_t b = (g + (uint32_t)m) & 1u, b2 = tmem + (b ^ 1u) * 128u;  // of tile m; tile m + 1's (and m - 1's)
-                        const uint32_t idesc = P.idesc_s | (16u << 17);
+                    // Whole key tiles in the middle of an item, without a question (a few dozen instructions of one thread are a
+                    // product's time).
+                    for (const int whole = P.ksteps == 4 * NB && there && !ask ? keys : 0; j > 2 && two && 128 * (j + 1) < whole; ++j, ++u) {
+                        await(ds_full(u & 1u), ((u - 2u) >> 1) & 1u);
+                        if (!ok) break;
+                        dq_mma(u, 8, false);
                         await(k_full(ks.idx), ks.ph);
                         if (!ok) break;
-                        issue_rows<NB>(b2, desc_lo(base + M::kQ, 16), desc_lo(k_smem(ks.idx), 16), idesc, 4 * NB);
-                        mma_commit(s_full((int)(b ^ 1u)));
-                        ks.next(kKStages);
-                        await(ds_full, ds_use & 1u);
-                        ++ds_use;
-                        await(v_full(vr.idx), vr.ph);
+                        s_mma(u, P.idesc_s | (16u << 17), 4 * NB);
                         if (!ok) break;
-                        issue_rows<NB>(tDP, desc_lo(base + M::kDO, 16), desc_lo(v_smem(vr.idx), 16), idesc, 4 * NB);
-                        mma_commit(dp_full);
-                        mma_commit(v_empty(vr.idx));
-                        vr.next(kVStages);
-                        issue_cols<64>(tDQ, tmem + b * 128u, desc_lo(k_smem(kq.idx), kBox), P.idesc_q, 0, 8, 8, false);
-                        mma_commit(k_empty(kq.idx));
-                        kq.next(kKStages);
+                        dp_mma(u, P.idesc_s | (16u << 17), 4 * NB);
                     }
                     if (!ok) break;
-                    if (s_part) {
-                        const bool in = m + 1 < n;
-                        if (!in && !asked) {
-                            asked = true;
-                            there = fetch(next_keys, next_lk);
-                            if (!ok) break;
-                            if (there) {
-                                await(q_full, items_s & 1u);
-                                ++items_s;
-                            }
+                    if (two) {
+                        await(ds_full(u & 1u), ((u - 2u) >> 1) & 1u);
+                        if ((two & 16) && items_out > 0) await(dq_empty, (items_out - 1u) & 1u);  // the last item's dQ is read
+                        if (!ok) break;
+                        dq_mma(u, two & 15, two & 16);
+                        if (two & 32) {
+                            mma_commit(dq_full);
+                            ++items_out;
                         }
-                        if (in || there) {
-                            const int j = in ? m + 1 : 0, valid = (in ? lk : next_lk) - 128 * j;
-                            if (!clean) {
-                                await(k_full(ks.idx), ks.ph);
-                                if (!ok) break;
-                                if (valid < 128 && valid % 16) {
-                                    tail = valid;
-                                    tail_st = ks.idx;
-                                    clean = true;
-                                    break;
-                                }
-                            }
-                            clean = false;
-                            const uint32_t b = (g + (uint32_t)(m + 1)) & 1u;
-                            const int see = in ? keys : next_keys;
-                            issue_rows<NB>(tmem + b * 128u, desc_lo(base + M::kQ, 16), desc_lo(k_smem(ks.idx), 16), idesc_of(see, j),
-                                           P.ksteps);
-                            mma_commit(s_full((int)b));
-                            if (128 * (j + 1) >= see) mma_commit(q_empty);
-                            ks.next(kKStages);
+                        two = 0;
+                    }
+                    if (ask) {
+                        there = fetch(keys, lk);
+                        ask = false;
+                        j = 0;
+                        if (there) {
+                            await(q_full, items_in & 1u);
+                            ++items_in;
                         }
-                        s_part = false;
-                        ++m;
-                    }
-                    if (m > 0) {
-                        await(ds_full, ds_use & 1u);
-                        ++ds_use;
                         if (!ok) break;
                     }
-                    if (m < n) {
-                        if (m == 0) await(do_full, items_dp & 1u);
-                        await(v_full(vr.idx), vr.ph);
-                        if (!ok) break;
-                        issue_rows<NB>(tDP, desc_lo(base + M::kDO, 16), desc_lo(v_smem(vr.idx), 16), idesc_of(keys, m), P.ksteps);
-                        mma_commit(dp_full);
-                        mma_commit(v_empty(vr.idx));
-                        if (m == n - 1) mma_commit(do_empty);
-                        vr.next(kVStages);
-                    }
-                    if (m > 0) {
-                        if (m == 1 && items_dp > 0) await(dq_empty, (items_dp - 1u) & 1u);  // the last item's dQ is read
-                        if (!ok) break;
-                        // dS: 64 keys a half, the second 64 columns on
-                        issue_cols<64>(tDQ, tmem + ((g + (uint32_t)(m - 1)) & 1u) * 128u, desc_lo(k_smem(kq.idx), kBox), P.idesc_q, 0, 8,
-                                       min(8, (keys - 128 * (m - 1) + 15) / 16), m == 1);
-                        mma_commit(k_empty(kq.idx));
-                        kq.next(kKStages);
-                    }
-                    if (m < n) {
-                        s_part = true;
+                    if (!there) {
+                        if (!one) break;
+                        two = one;
+                        one = 0;
+                        ++u;
                         continue;
                     }
-                    if (n > 0) {
-                        mma_commit(dq_full);
-                        ++items_dp;
+                    if (!clean) {
+                        await(k_full(ks.idx), ks.ph);
+                        if (!ok) break;
+                        const int valid = lk - 128 * j;
+                        if (valid < 128 && valid % 16) {
+                            tail = valid;
+                            tail_st = ks.idx;
+                            clean = true;
+                            break;
+                        }
                     }
-                    if (!there) break;
-                    g += (uint32_t)n;
-                    keys = next_keys;
-                    lk = next_lk;
-                    n = (keys + 127) / 128;
-                    m = 0;
-                    asked = false;
+                    clean = false;
+                    const int steps = min(8, (keys - 128 * j + 15) / 16);
+                    const bool last = 128 * (j + 1) >= keys;
+                    s_mma(u, P.idesc_s | ((uint32_t)(2 * steps) << 17), P.ksteps);
+                    if (!ok) break;
+                    if (last) mma_commit(q_empty);
+                    if (j == 0) await(do_full, (items_in - 1u) & 1u);
+                    dp_mma(u, P.idesc_s | ((uint32_t)(2 * steps) << 17), P.ksteps);
+                    if (!ok) break;
+                    if (last) mma_commit(do_empty);
+                    two = one;
+                    one = steps | (j == 0 ? 16 : 0) | (last ? 32 : 0);
+                    ++u;
+                    ++j;
+                    ask = last;
                 }
             }
             tail = __shfl_sync(0xffffffffu, tail, lead);
@@ -325,7 +320,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
         const bool wide = p.D % 16 == 0 && (reinterpret_cast<uintptr_t>(p.dq) & 31) == 0;
         const float f = P.scale_log2e;
         Item<1> it;
-        uint32_t g = 0, dp_use = 0, dq_use = 0;  // tiles so far
+        uint32_t g = 0, dq_use = 0;  // tiles so far
         while (ok && next_item(it)) {
             const int keys = it.keys[0], n = (keys + 127) / 128;
             const bool row = r < it.rows[0];
@@ -351,20 +346,23 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
             }
             for (int j = 0; j < n && ok; ++j, ++g) {
                 const uint32_t b = g & 1u;
-                const uint32_t sA = tmem + lane_off + 128u * b + 64u * half, dpA = tDP + lane_off + 64u * half;
+                const uint32_t sA = tmem + lane_off + 64u * half, dpA = tDP + lane_off + 128u * b + 64u * half;
                 const bool edge = 128 * j + 127 > first;  // some row does not see every key
                 uint32_t see[2] = {0xffffffffu, 0xffffffffu};
                 if (edge) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) see[i] = low_bits(limit - 128 * j - 64 * half - 32 * i + 1);
                 }
-                ok = __all_sync(0xffffffffu, wait(s_full((int)b), (g >> 1) & 1u, abort_flag, p.status));
+                ok = __all_sync(0xffffffffu, wait(s_full, g & 1u, abort_flag, p.status));
                 if (!ok) break;
                 tc_fence_after();
                 float pr[64];
                 {
                     uint32_t sr[64];
                     tmem_ld_x64(sA, sr);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_read);
 #pragma unroll
                     for (int c = 0; c < 64; c += 2) {
                         const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), make_float2(f, f),
@@ -373,9 +371,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                         pr[c + 1] = ex2(y.y);
                     }
                 }
-                ok = __all_sync(0xffffffffu, wait(dp_full, dp_use & 1u, abort_flag, p.status));
+                ok = __all_sync(0xffffffffu, wait(dp_full(b), (g >> 1) & 1u, abort_flag, p.status));
                 if (!ok) break;
-                ++dp_use;
                 tc_fence_after();
                 uint32_t pk[32];
 #pragma unroll
@@ -393,11 +390,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                         pk[16 * i + c / 2] = pack2<BF16>(x.x, x.y);
                     }
                 }
-                tmem_st_x32(sA, pk);
+                tmem_st_x32(dpA, pk);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(ds_full);
+                if (lane == 0) mbar_arrive(ds_full(b));
             }
             if (!ok) break;
             if (n > 0) {
