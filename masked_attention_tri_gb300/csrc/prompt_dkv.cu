@@ -1,5 +1,5 @@
 // prompt_dkv.cu -- the gradients of keys and values in the causal attention of packed prompts with grouped heads on tcgen05
-// tensor cores: 16-bit inputs, D <= 128.  (dQ and delta = dO . O: prompt_dq.cu, before it.)
+// tensor cores: 16-bit inputs, D <= 128.  (dQ: prompt_dq.cu; delta = dO . O: prompt_simt.cu, before both.)
 //
 // Rows are tokens x heads of a group (prompt.cuh), in tiles as in the forward.  With P = 2^(s - lse) recomputed, one CTA for each
 // (sequence, key head, 128 keys) walks the row tiles that see a key of its own:
@@ -467,7 +467,8 @@ cudaError_t start(const DkvParams& P, unsigned grid, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_dq(const PromptParams& p, cudaStream_t stream);  // prompt_dq.cu
+cudaError_t launch_dq(const PromptParams& p, cudaStream_t stream);     // prompt_dq.cu
+cudaError_t launch_delta(const PromptParams& p, cudaStream_t stream);  // prompt_simt.cu
 
 }  // namespace prompt
 
@@ -484,7 +485,9 @@ int prompt_bwd_splits(int num_seqs, int total_k, int max_q, int max_k, int Hk, i
 
 cudaError_t launch_prompt_tc_bwd(const PromptParams& p, cudaStream_t stream) {
     using namespace prompt;
-    cudaError_t e = p.total_q > 0 && p.max_q > 0 ? launch_dq(p, stream) : cudaSuccess;
+    const bool rows = p.total_q > 0 && p.max_q > 0;
+    cudaError_t e = rows ? launch_delta(p, stream) : cudaSuccess;
+    if (e == cudaSuccess && rows) e = launch_dq(p, stream);
     if (e != cudaSuccess || p.max_k <= 0) return e;
     DkvParams P;
     P.p = p;

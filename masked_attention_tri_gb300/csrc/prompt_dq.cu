@@ -1,11 +1,12 @@
 // prompt_dq.cu -- the gradient of the queries in the causal attention of packed prompts with grouped heads on tcgen05 tensor
-// cores (16-bit inputs, D <= 128), and the rows' delta = dO . O, which prompt_dkv.cu reads after it.
+// cores: 16-bit inputs, D <= 128.
 //
 // A tile of rows (prompt_tc.cuh) walks the key tiles that it sees, as in the forward, with P = 2^(s - lse) recomputed:
 //     S = Q K^T, dP = dO V^T             rows on the tensor-memory lanes
 //     dS = P (dP - delta)                as 16-bit pairs over dP
 //     dQ += dS K                         dS from tensor memory
-// lse and delta are one number a thread, dQ stays in tensor memory, and is rounded once: no sum in memory, no order that varies.
+// lse and delta = dO . O (one pass of its own before: half a row a thread at the start of an item was 5 us of each) are one number a
+// thread, dQ stays in tensor memory, and is rounded once: no sum in memory, no order that varies.
 // (One kernel for dQ, dK and dV computes S and dP once, five products a tile where the two kernels have seven; but its dQ has to be added
 // up in memory over the key tiles and stands between the tiles' products, and four 128 x 128 x D products a tile from shared memory are more
 // than that gives: four sequences of 8192 tokens, 16 heads over 4 of 128, 3.86 ms, of which 0.5 ms were the reductions.)
@@ -231,6 +232,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
         int keys = 0, lk = 0, j = 0, one = 0, two = 0;
         uint32_t u = 0, items_in = 0, items_out = 0;
         bool there = true, ask = true, clean = false;
+        auto finish = [&](int what, uint32_t v) {  // dQ of tile v
+            await(ds_full(v & 1u), (v >> 1) & 1u);
+            if ((what & 16) && items_out > 0) await(dq_empty, (items_out - 1u) & 1u);  // the last item's dQ is read
+            if (!ok) return;
+            dq_mma(v, what & 15, what & 16);
+            if (what & 32) {
+                mma_commit(dq_full);
+                ++items_out;
+            }
+        };
         for (;;) {
             int tail = 0, tail_st = 0;
             if (leader) {
@@ -249,16 +260,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                     }
                     if (!ok) break;
                     if (two) {
-                        await(ds_full(u & 1u), ((u - 2u) >> 1) & 1u);
-                        if ((two & 16) && items_out > 0) await(dq_empty, (items_out - 1u) & 1u);  // the last item's dQ is read
-                        if (!ok) break;
-                        dq_mma(u, two & 15, two & 16);
-                        if (two & 32) {
-                            mma_commit(dq_full);
-                            ++items_out;
-                        }
+                        finish(two, u - 2u);
                         two = 0;
                     }
+                    if (!ok) break;
                     if (ask) {
                         there = fetch(keys, lk);
                         ask = false;
@@ -293,7 +298,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                     s_mma(u, P.idesc_s | ((uint32_t)(2 * steps) << 17), P.ksteps);
                     if (!ok) break;
                     if (last) mma_commit(q_empty);
-                    if (j == 0) await(do_full, (items_in - 1u) & 1u);
+                    if (j == 0) {
+                        if (one) {  // (the last item's dQ first: this dO may be on its way yet)
+                            finish(one, u - 1u);
+                            one = 0;
+                        }
+                        await(do_full, (items_in - 1u) & 1u);
+                    }
                     dp_mma(u, P.idesc_s | ((uint32_t)(2 * steps) << 17), P.ksteps);
                     if (!ok) break;
                     if (last) mma_commit(do_empty);
@@ -327,23 +338,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
             const long long tok = it.q0 + it.tok[0] + tok_r, head = it.head[0] + head_r;
             const long long at = head * p.total_q + tok, row0 = (tok * p.Hq + head) * p.D;
             const int limit = it.tok[0] + tok_r + it.shift, first = it.tok[0] + it.shift;
-            float nl = 0.f, delta = 0.f;
-            if (row) {
-                nl = -p.lse[at] * tc::kLog2e;
-                const uint4* a = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.out) + row0);
-                const uint4* b = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.d_out) + row0);
-                float2 s = make_float2(0.f, 0.f);
-#pragma unroll 4
-                for (int c = 0; c < p.D / 8; ++c) {
-                    const uint4 x = a[c], y = b[c];
-                    s = __ffma2_rn(unpack2<BF16>(x.x), unpack2<BF16>(y.x), s);
-                    s = __ffma2_rn(unpack2<BF16>(x.y), unpack2<BF16>(y.y), s);
-                    s = __ffma2_rn(unpack2<BF16>(x.z), unpack2<BF16>(y.z), s);
-                    s = __ffma2_rn(unpack2<BF16>(x.w), unpack2<BF16>(y.w), s);
-                }
-                delta = s.x + s.y;
-                if (half == 0) p.delta[at] = delta;
-            }
+            const float nl = row ? -p.lse[at] * tc::kLog2e : 0.f, nd = row ? -p.delta[at] : 0.f;
             for (int j = 0; j < n && ok; ++j, ++g) {
                 const uint32_t b = g & 1u;
                 const uint32_t sA = tmem + lane_off + 64u * half, dpA = tDP + lane_off + 128u * b + 64u * half;
@@ -381,7 +376,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                     tmem_ld_x32(dpA + 32 * i, dr);
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        float2 x = __fadd2_rn(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), make_float2(-delta, -delta));
+                        float2 x = __fadd2_rn(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), make_float2(nd, nd));
                         x = __fmul2_rn(x, make_float2(pr[32 * i + c], pr[32 * i + c + 1]));
                         if (edge) {
                             x.x = (see[i] >> c) & 1u ? x.x : 0.f;

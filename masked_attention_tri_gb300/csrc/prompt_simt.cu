@@ -396,6 +396,8 @@ cudaError_t forward(const PromptParams& p, cudaStream_t stream) {
     return start(prompt_fwd_simt<T, NC>, p, tiles, (size_t)3 * 64 * (64 * NC + 4), stream);
 }
 
+}  // namespace
+
 cudaError_t launch_delta(const PromptParams& p, cudaStream_t stream) {
     const long long n = ((long long)p.total_q * p.Hq + 15) / 16;
     if (n > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -406,6 +408,8 @@ cudaError_t launch_delta(const PromptParams& p, cudaStream_t stream) {
     }
     return cudaGetLastError();
 }
+
+namespace {
 
 template <typename T, int NC>
 cudaError_t backward(const PromptParams& p, cudaStream_t stream) {
