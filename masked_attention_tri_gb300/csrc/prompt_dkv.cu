@@ -433,14 +433,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
     }
 }
 
-// The CTAs' parts of a (sequence, key head, 128 keys), added in their order.
+// The CTAs' parts of a (sequence, key head, 128 keys), added in their order.  (Eight CTAs for each of them, four pieces of 32 bytes and
+// their parts a thread: there are few such where parts are made; 3507 tokens, 8 heads over 2 of 128:
+// 32 us with one CTA for each, 7 so.)
+constexpr int kJoin = 8;
 template <bool BF16>
 __global__ void __launch_bounds__(256) prompt_dkv_join(const PromptParams p, int splits) {
     const unsigned per = (unsigned)p.num_seqs * (unsigned)p.Hk;
     const int k0 = 128 * (int)(blockIdx.x / per), h = (int)(blockIdx.x % per % (unsigned)p.Hk);
     const Seq q = load_seq(p, (int)(blockIdx.x % per / (unsigned)p.Hk), false);
     const int keys = min(128, q.lk - k0), pieces = p.D / 8;
-    for (int e = threadIdx.x; e < 2 * keys * pieces; e += 256) {
+    for (int e = (int)blockIdx.y * 256 + threadIdx.x; e < 2 * keys * pieces; e += 256 * kJoin) {
         const int which = e >= keys * pieces, x = which ? e - keys * pieces : e, k = x / pieces, d = (x - k * pieces) * 8;
         const long long key = q.k0 + k0 + k;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
@@ -508,8 +511,8 @@ cudaError_t launch_prompt_tc_bwd(const PromptParams& p, cudaStream_t stream) {
     if (p.D <= 64) e = bf16 ? start<true, 1>(P, (unsigned)grid, stream) : start<false, 1>(P, (unsigned)grid, stream);
     else e = bf16 ? start<true, 2>(P, (unsigned)grid, stream) : start<false, 2>(P, (unsigned)grid, stream);
     if (e != cudaSuccess || P.splits == 1) return e;
-    if (bf16) prompt_dkv_join<true><<<(unsigned)tiles, 256, 0, stream>>>(p, P.splits);
-    else prompt_dkv_join<false><<<(unsigned)tiles, 256, 0, stream>>>(p, P.splits);
+    if (bf16) prompt_dkv_join<true><<<dim3((unsigned)tiles, kJoin), 256, 0, stream>>>(p, P.splits);
+    else prompt_dkv_join<false><<<dim3((unsigned)tiles, kJoin), 256, 0, stream>>>(p, P.splits);
     return cudaGetLastError();
 }
 

@@ -250,15 +250,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
                 mma_commit(s_full(i));
                 if (128 * (j + 1) >= keys) mma_commit(q_empty(i));
             };
+            // The epilogue has read the last item's O_i.
+            auto o_mine = [&](int i) {
+                if ((use >> (6 + i)) & 1u) {
+                    await(o_empty(i), (use >> (4 + i)) & 1u);
+                    use ^= 16u << i;
+                }
+                use |= 64u << i;
+            };
             // O_i += P_i V of key tile j, V in stage st
             auto pv = [&](int i, int keys, int j, int st) {
-                if (j == 0) {  // the epilogue has read the last item's O
-                    if ((use >> (6 + i)) & 1u) {
-                        await(o_empty(i), (use >> (4 + i)) & 1u);
-                        use ^= 16u << i;
-                    }
-                    use |= 64u << i;
-                }
+                if (j == 0) o_mine(i);
                 const int steps = min(8, (keys - 128 * j + 15) / 16);
                 const uint32_t b = desc_lo(kv_smem(st), kBox), d = tmem + 256u + (uint32_t)i * kOCols, a = tmem + i * 128;
 #pragma unroll
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
                     while (ok && there) {
                         // Whole key tiles in the middle of an item, without a question (a few dozen instructions of one thread are a
                         // product's time).
-                        for (const int whole = P.ksteps == 4 * NB ? min(k0, k1) : 0; j > 1 && 128 * (j + 1) < whole; ++j) {
+                        for (const int whole = P.ksteps == 4 * NB ? min(k0, k1) : 0; 128 * (j + 1) < whole; ++j) {
                             const int vst = kr.idx;
                             const uint32_t vph = kr.ph;
                             kr.next(S);
@@ -300,10 +302,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const uint32_t d = tmem + 256u + (uint32_t)i * kOCols, a = tmem + i * 128;
+                                if (j == 1) o_mine(i);
                                 if (ok) ok = wait(p_half(i, 0), i ? pq : pp, abort_flag, p.status);
                                 tc_fence_after();
                                 if (!ok) break;
-                                issue_cols<32>(d, a, v, P.idesc_pv, 0, 4, 8, false);
+                                issue_cols<32>(d, a, v, P.idesc_pv, 0, 4, 8, j == 1);
                                 ok = wait(p_half(i, 1), i ? pq : pp, abort_flag, p.status);
                                 tc_fence_after();
                                 if (!ok) break;
