@@ -5,7 +5,7 @@
 // (sequence, key head, 128 keys) walks the row tiles that see a key of its own:
 //     S^T = K Q^T, dP^T = V dO^T         keys on the tensor-memory lanes, rows of the tile in the columns
 //     dV += P^T dO                       P^T as 16-bit pairs over S^T
-//     dS = P (dP - delta),  dK += dS^T Q dS^T as 16-bit pairs over dP^T
+//     dS = P (dP - delta),  dK += dS^T Q dS^T as 16-bit pairs over dP^T (as two in rows that see few keys: prompt_dq.cu)
 // Tensor memory: S^T, dP^T, dV, dK: 4 x 128 columns at D = 128.  The sums over the group's heads are sums over rows.
 //
 // 12 warps: 0-7 softmax and dS (key = lane, 64 rows each half), 8 MMA, 9 TMA, 10 the rows' lse and delta.  The tensor core's order is
@@ -91,6 +91,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
         }
         return;
     }
+    // The tiles of the walk whose rows see up to kFineKeys keys.
+    const int fine_blocks = min(blocks, max(0, kFineKeys - q.shift) / P.t.tq) * P.t.ng;
+    const int fine = max(0, (fine_blocks - first + P.splits - 1) / P.splits);
     // Tile j of the walk: its first token, first query head and rows.
     auto tile = [&](int j, int& tok, int& head, int& rows) {
         const int t = first + j * P.splits, b = t / P.t.ng;
@@ -249,6 +252,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
                         await(ds_full, ph);
                         if (!ok) break;
                         issue_cols<64>(tDK, tDP, desc_lo(q_smem(qk.idx), kBox), P.idesc_g, 0, 8, 8, false);
+                        if (u / 4 < fine) issue_cols<64>(tDK, tDP + 32u, desc_lo(q_smem(qk.idx), kBox), P.idesc_g, 0, 8, 8, false);
                         mma_commit(q_empty(qk.idx));
                         qk.next(kQStages);
                         await(do_full(s ^ 1), (to + ph) & 1u);
@@ -283,8 +287,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
                         await(second ? ds_full : p_full, (uint32_t)j & 1u);
                         if (!ok) break;
                         // (the rows of the second half: 64 columns on)
-                        issue_cols<64>(second ? tDK : tDV, second ? tDP : tS, desc_lo(second ? q_smem(qk.idx) : do_smem(s), kBox), P.idesc_g, 0,
-                                       8, (rows_of(j) + 15) / 16, j == 0);
+                        const uint32_t b = desc_lo(second ? q_smem(qk.idx) : do_smem(s), kBox);
+                        const int sixteens = (rows_of(j) + 15) / 16;
+                        issue_cols<64>(second ? tDK : tDV, second ? tDP : tS, b, P.idesc_g, 0, 8, sixteens, j == 0);
+                        if (second && j < fine) issue_cols<64>(tDK, tDP + 32u, b, P.idesc_g, 0, 8, sixteens, false);
                         mma_commit(second ? q_empty(qk.idx) : do_empty(s));
                         if (second) qk.next(kQStages);
                     }
@@ -362,30 +368,40 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
             ok = __all_sync(0xffffffffu, wait(dp_full, ph, abort_flag, p.status));
             if (!ok) break;
             tc_fence_after();
-            uint32_t pk[32];
+            auto form = [&](auto pieces) {
+                constexpr bool kFine = decltype(pieces)::value == 2;
+                uint32_t pk[32], low[kFine ? 32 : 1];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t dr[32];
-                tmem_ld_x32(dpA + 32 * i, dr);
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t dr[32];
+                    tmem_ld_x32(dpA + 32 * i, dr);
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const float4 d = nd[8 * i + c / 4];
-                    const int pa = 32 * i + c;
-                    float2 u = __fadd2_rn(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), make_float2(d.x, d.y));
-                    float2 v = __fadd2_rn(make_float2(__uint_as_float(dr[c + 2]), __uint_as_float(dr[c + 3])), make_float2(d.z, d.w));
-                    u = __fmul2_rn(u, make_float2(pr[pa], pr[pa + 1]));
-                    v = __fmul2_rn(v, make_float2(pr[pa + 2], pr[pa + 3]));
-                    if (edge) {  // (dP and delta of a row that is not there may be anything)
-                        u.x = (see[i] >> c) & 1u ? u.x : 0.f;
-                        u.y = (see[i] >> (c + 1)) & 1u ? u.y : 0.f;
-                        v.x = (see[i] >> (c + 2)) & 1u ? v.x : 0.f;
-                        v.y = (see[i] >> (c + 3)) & 1u ? v.y : 0.f;
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 d = nd[8 * i + c / 4];
+                        const int pa = 32 * i + c;
+                        float2 u = __fadd2_rn(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), make_float2(d.x, d.y));
+                        float2 v = __fadd2_rn(make_float2(__uint_as_float(dr[c + 2]), __uint_as_float(dr[c + 3])), make_float2(d.z, d.w));
+                        u = __fmul2_rn(u, make_float2(pr[pa], pr[pa + 1]));
+                        v = __fmul2_rn(v, make_float2(pr[pa + 2], pr[pa + 3]));
+                        if (edge) {  // (dP and delta of a row that is not there may be anything)
+                            u.x = (see[i] >> c) & 1u ? u.x : 0.f;
+                            u.y = (see[i] >> (c + 1)) & 1u ? u.y : 0.f;
+                            v.x = (see[i] >> (c + 2)) & 1u ? v.x : 0.f;
+                            v.y = (see[i] >> (c + 3)) & 1u ? v.y : 0.f;
+                        }
+                        pk[pa / 2] = pack2<BF16>(u.x, u.y);
+                        pk[pa / 2 + 1] = pack2<BF16>(v.x, v.y);
+                        if constexpr (kFine) {
+                            low[pa / 2] = rest2<BF16>(u, pk[pa / 2]);
+                            low[pa / 2 + 1] = rest2<BF16>(v, pk[pa / 2 + 1]);
+                        }
                     }
-                    pk[pa / 2] = pack2<BF16>(u.x, u.y);
-                    pk[pa / 2 + 1] = pack2<BF16>(v.x, v.y);
                 }
-            }
-            tmem_st_x32(dpA, pk);
+                tmem_st_x32(dpA, pk);
+                if constexpr (kFine) tmem_st_x32(dpA + 32, low);
+            };
+            if (__builtin_expect(j >= fine, 1)) form(Count<1>());
+            else form(Count<2>());
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();

@@ -111,6 +111,18 @@ __device__ __forceinline__ void issue_cols(uint32_t d, uint32_t a, uint32_t b, u
     }
 }
 
+// dS of rows that see up to so many keys is two 16-bit numbers, the second the rest of the first's rounding (prompt_dq.cu).
+constexpr int kFineKeys = 512;
+template <int N>
+struct Count {
+    static constexpr int value = N;
+};
+template <bool BF16>
+__device__ __forceinline__ uint32_t rest2(float2 x, uint32_t rounded) {
+    const float2 y = unpack2<BF16>(rounded);
+    return pack2<BF16>(x.x - y.x, x.y - y.y);
+}
+
 // An item: PER tiles of one (sequence, key head).
 template <int PER>
 struct alignas(16) Item {
