@@ -227,8 +227,36 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
             tc_fence_after();
         };
         const int steps = (full_rows + 15) / 16;
-        const int whole = P.ksteps == 4 * NB && steps == 8 ? max(0, (last_from - first + P.splits - 1) / P.splits) : 0;  // tiles before the last block's
+        const int whole = steps == 8 ? max(0, (last_from - first + P.splits - 1) / P.splits) : 0;  // tiles before the last block's
         StageRing qs = {0, 0u, false}, qk = {0, 0u, false};  // Q for S, Q for dK
+        // Whole tiles, without a question (a few dozen instructions of one thread are a product's time; by all sixteens of columns, or
+        // by as many as there are).
+        auto straight = [&](auto all, int& u) {
+            constexpr bool kAll = decltype(all)::value == 1;
+            for (; u > 0 && (u & 3) == 0 && u / 4 + 1 < whole; u += 4) {
+                const uint32_t ph = (uint32_t)(u >> 2) & 1u, to = (uint32_t)(u >> 3);  // (tile j = u / 4's parity; dO(j + 1)'s below)
+                const int s = (int)ph;
+                await(p_full, ph);
+                if (!ok) break;
+                issue_cols<64>(tDV, tS, desc_lo(do_smem(s), kBox), P.idesc_g, 0, 8, 8, false);
+                mma_commit(do_empty(s));
+                await(q_full(qs.idx), qs.ph);
+                if (!ok) break;
+                issue_rows<NB>(tS, desc_lo(base + M::kK, 16), desc_lo(q_smem(qs.idx), 16), P.idesc_s, kAll ? 4 * NB : P.ksteps);
+                mma_commit(s_full);
+                qs.next(kQStages);
+                await(ds_full, ph);
+                if (!ok) break;
+                issue_cols<64>(tDK, tDP, desc_lo(q_smem(qk.idx), kBox), P.idesc_g, 0, 8, 8, false);
+                if (u / 4 < fine) issue_cols<64>(tDK, tDP + 32u, desc_lo(q_smem(qk.idx), kBox), P.idesc_g, 0, 8, 8, false);
+                mma_commit(q_empty(qk.idx));
+                qk.next(kQStages);
+                await(do_full(s ^ 1), (to + ph) & 1u);
+                if (!ok) break;
+                issue_rows<NB>(tDP, desc_lo(base + M::kV, 16), desc_lo(do_smem(s ^ 1), 16), P.idesc_s, kAll ? 4 * NB : P.ksteps);
+                mma_commit(dp_full);
+            }
+        };
         bool clean = false;
         for (int u = -2;;) {  // S(0), dP(0); then for each j: dV(j), S(j + 1), dK(j), dP(j + 1)
             int tail = 0;
@@ -236,30 +264,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
             if (leader) {
                 if (u == -2 && !clean) await(kv_full, 0);
                 while (ok && u < 4 * n) {
-                    // Whole tiles, without a question (a few dozen instructions of one thread are a product's time).
-                    for (; u > 0 && (u & 3) == 0 && u / 4 + 1 < whole; u += 4) {
-                        const uint32_t ph = (uint32_t)(u >> 2) & 1u, to = (uint32_t)(u >> 3);  // (tile j = u / 4's parity; dO(j + 1)'s below)
-                        const int s = (int)ph;
-                        await(p_full, ph);
-                        if (!ok) break;
-                        issue_cols<64>(tDV, tS, desc_lo(do_smem(s), kBox), P.idesc_g, 0, 8, 8, false);
-                        mma_commit(do_empty(s));
-                        await(q_full(qs.idx), qs.ph);
-                        if (!ok) break;
-                        issue_rows<NB>(tS, desc_lo(base + M::kK, 16), desc_lo(q_smem(qs.idx), 16), P.idesc_s, 4 * NB);
-                        mma_commit(s_full);
-                        qs.next(kQStages);
-                        await(ds_full, ph);
-                        if (!ok) break;
-                        issue_cols<64>(tDK, tDP, desc_lo(q_smem(qk.idx), kBox), P.idesc_g, 0, 8, 8, false);
-                        if (u / 4 < fine) issue_cols<64>(tDK, tDP + 32u, desc_lo(q_smem(qk.idx), kBox), P.idesc_g, 0, 8, 8, false);
-                        mma_commit(q_empty(qk.idx));
-                        qk.next(kQStages);
-                        await(do_full(s ^ 1), (to + ph) & 1u);
-                        if (!ok) break;
-                        issue_rows<NB>(tDP, desc_lo(base + M::kV, 16), desc_lo(do_smem(s ^ 1), 16), P.idesc_s, 4 * NB);
-                        mma_commit(dp_full);
-                    }
+                    if (P.ksteps == 4 * NB) straight(Count<1>(), u);
+                    else straight(Count<0>(), u);
                     if (!ok || u >= 4 * n) break;
                     const bool odd = u & 1, second = u < 0 ? odd : (u & 2) != 0;   // S or dP; and dP or dK
                     const int j = u < 0 ? 0 : u / 4 + (odd ? 1 : 0), s = j & 1;

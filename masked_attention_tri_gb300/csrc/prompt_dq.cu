@@ -248,22 +248,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                 ++items_out;
             }
         };
+        // Whole key tiles in the middle of an item, without a question (a few dozen instructions of one thread are a product's time;
+        // by all sixteens of columns, or by as many as there are).
+        auto straight = [&](auto all) {
+            constexpr bool kAll = decltype(all)::value == 1;
+            for (const int whole = there && !ask ? keys : 0; j > 2 && two && 128 * (j + 1) < whole; ++j, ++u) {
+                await(ds_full(u & 1u), ((u - 2u) >> 1) & 1u);
+                if (!ok) break;
+                dq_mma(u, 8, false, keys <= kFineKeys);
+                await(k_full(ks.idx), ks.ph);
+                if (!ok) break;
+                s_mma(u, P.idesc_s | (16u << 17), kAll ? 4 * NB : P.ksteps);
+                if (!ok) break;
+                dp_mma(u, P.idesc_s | (16u << 17), kAll ? 4 * NB : P.ksteps);
+            }
+        };
         for (;;) {
             int tail = 0, tail_st = 0;
             if (leader) {
                 while (ok) {
-                    // Whole key tiles in the middle of an item, without a question (a few dozen instructions of one thread are a
-                    // product's time).
-                    for (const int whole = P.ksteps == 4 * NB && there && !ask ? keys : 0; j > 2 && two && 128 * (j + 1) < whole; ++j, ++u) {
-                        await(ds_full(u & 1u), ((u - 2u) >> 1) & 1u);
-                        if (!ok) break;
-                        dq_mma(u, 8, false, keys <= kFineKeys);
-                        await(k_full(ks.idx), ks.ph);
-                        if (!ok) break;
-                        s_mma(u, P.idesc_s | (16u << 17), 4 * NB);
-                        if (!ok) break;
-                        dp_mma(u, P.idesc_s | (16u << 17), 4 * NB);
-                    }
+                    if (P.ksteps == 4 * NB) straight(Count<1>());
+                    else straight(Count<0>());
                     if (!ok) break;
                     if (two) {
                         finish(two, u - 2u);

@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
                     while (ok && there) {
                         // Whole key tiles in the middle of an item, without a question (a few dozen instructions of one thread are a
                         // product's time).
-                        for (const int whole = P.ksteps == 4 * NB ? min(k0, k1) : 0; 128 * (j + 1) < whole; ++j) {
+                        for (const int whole = min(k0, k1); 128 * (j + 1) < whole; ++j) {
                             const int vst = kr.idx;
                             const uint32_t vph = kr.ph;
                             kr.next(S);
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
                                 } else {
                                     mma_commit(kv_empty(vst));
                                 }
-                                issue_rows<NB>(a, desc_lo(q_smem(i), 16), k, P.idesc_qk | (16u << 17), 4 * NB);
+                                issue_rows<NB>(a, desc_lo(q_smem(i), 16), k, P.idesc_qk | (16u << 17), P.ksteps);
                                 mma_commit(s_full(i));
                             }
                             if (!ok) break;
