@@ -676,8 +676,8 @@ ta_status tri_attn_prompt_fwd(const void* q, const void* k, const void* v, ta_dt
  *                 cu_k[num_seqs] are left alone; a key that no query sees gets 0.
  *   workspace     device scratch of tri_attn_prompt_bwd_workspace_size(...) bytes, 256-byte aligned, owned by the caller;
  *                 two calls in flight must not share it.
- * Arithmetic as in the forward (dx rounded to the inputs' type as an operand on tensor cores).  Results do not vary from run
- * to run.  Errors as tri_attn_prompt_fwd.
+ * Arithmetic as in the forward (P and dx rounded to the inputs' type as operands on tensor cores; dx as two such numbers
+ * for queries that see up to 512 keys).  Results do not vary from run to run.  Errors as tri_attn_prompt_fwd.
  */
 ta_status tri_attn_prompt_bwd(const void* q, const void* k, const void* v, ta_dtype dtype, const int32_t* cu_seqlens_q,
                               const int32_t* cu_seqlens_k, int num_seqs, int total_q, int total_k, int max_seqlen_q,

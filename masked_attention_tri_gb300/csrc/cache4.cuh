@@ -43,9 +43,9 @@ struct Scale {
     float s, inv, half, most;
     __device__ __forceinline__ explicit Scale(float v) : s(v), inv(about_inverse(v)), half(0.5f * v), most(7.f * v) {}
 };
-// n + 8 in the low four bits (the others are not zero) of y = x / f_h: y / s to the nearest whole number, ties to even, 7 at most.
-// y times 1 / s may fall on the wrong side of a border, so the remainder y - n s decides (fp32 holds it exactly: n s has eight significant
-// bits, and y is at most 7 s and n s not far from it).  (A NaN's scale says what it is.)
+// n + 8 in the low four bits (the others are not zero) of y = x / f_h: y / s to the nearest whole number, ties to even, 7 at
+// most. y times 1 / s may fall on the wrong side of a border, so the remainder y - n s decides (fp32 holds it exactly: n s has
+// eight significant bits, and y is at most 7 s and n s not far from it).  (A NaN's scale says what it is.)
 __device__ __forceinline__ uint32_t code(float y, const Scale& c) {
     y = fminf(fmaxf(y, -c.most), c.most);
     const float t = fmaf(y, c.inv, 12582920.f);  // 1.5 * 2^23 + 8: whole numbers, n + 8 in the low bits
@@ -65,10 +65,11 @@ __device__ __forceinline__ uint32_t pack8(const uint32_t (&u)[8]) {
     }
     return __byte_perm(x[0], x[1], 0x6420);
 }
-// Sixteen elements x of 16 bits as codes, two words.  x / (f_h s) is rounded to 2^-16 first, which takes the product's error off a border,
-// and then to whole numbers.  This is the nearest for elements of at most eleven significant bits and a factor that is a power of two: with m
-// of s = m 2^k from 8 to 15, x / (f_h s) is a / (m 2^j), a < 2^11 and 2^j < 2^12; if it is no border, it is at least 2^-13 from one.  (Turned
-// elements and other factors: within 2^-16 of a border a code may fall on either side.)
+// Sixteen elements x of 16 bits as codes, two words.  x / (f_h s) is rounded to 2^-16 first, which takes the product's error
+// off a border, and then to whole numbers.  This is the nearest for elements of at most eleven significant bits and a factor
+// that is a power of two: with m of s = m 2^k from 8 to 15, x / (f_h s) is a / (m 2^j), a < 2^11 and 2^j < 2^12; if it is no
+// border, it is at least 2^-13 from one.  (Turned elements and other factors: within 2^-16 of a border a code may fall on
+// either side.)
 __device__ __forceinline__ uint2 codes16(const float (&x)[16], float inv, const Scale& c, bool clamp) {
     const float r = c.inv * inv;
     uint32_t u[2][8];

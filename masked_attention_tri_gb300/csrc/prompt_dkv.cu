@@ -1,18 +1,21 @@
 // prompt_dkv.cu -- the gradients of keys and values in the causal attention of packed prompts with grouped heads on tcgen05
 // tensor cores: 16-bit inputs, D <= 128.  (dQ: prompt_dq.cu; delta = dO . O: prompt_simt.cu, before both.)
 //
-// Rows are tokens x heads of a group (prompt.cuh), in tiles as in the forward.  With P = 2^(s - lse) recomputed, one CTA for each
-// (sequence, key head, 128 keys) walks the row tiles that see a key of its own:
+// Rows are tokens x heads of a group (prompt.cuh), in tiles as in the forward.  With P = 2^(s - lse) recomputed, one CTA for
+// each (sequence, key head, 128 keys) walks the row tiles that see a key of its own:
 //     S^T = K Q^T, dP^T = V dO^T         keys on the tensor-memory lanes, rows of the tile in the columns
 //     dV += P^T dO                       P^T as 16-bit pairs over S^T
 //     dS = P (dP - delta),  dK += dS^T Q dS^T as 16-bit pairs over dP^T (as two in rows that see few keys: prompt_dq.cu)
 // Tensor memory: S^T, dP^T, dV, dK: 4 x 128 columns at D = 128.  The sums over the group's heads are sums over rows.
 //
-// 12 warps: 0-7 softmax and dS (key = lane, 64 rows each half), 8 MMA, 9 TMA, 10 the rows' lse and delta.  The tensor core's order is
-// dV(i), S(i+1), dK(i), dP(i+1): while dS(i) is formed it has dV(i) and S(i+1) to do, and dK(i) and dP(i+1) while P(i+1) is.
+// 12 warps: 0-7 softmax and dS (key = lane, 64 rows each half), 8 MMA, 9 TMA, 10 the rows' lse and delta.  The tensor core's
+// order is dV(i), S(i+1), dK(i), dP(i+1): while dS(i) is formed it has dV(i) and S(i+1) to do, and dK(i) and dP(i+1) while
+// P(i+1) is.
 //
-// Bound: the tensor core, 2048 clocks a tile at D = 128, and shared memory with nearly as much (its operands and the loads).  Where there are too few
-// (sequence, head, key tile) for the GPU, the row tiles of one are dealt to several CTAs, whose fp32 parts are added in their order.
+// Bound: the tensor core, 2048 clocks a tile at D = 128 (75% of the time in long sequences), then the softmax warps, two
+// phases of some thousand clocks a tile, which is what counts at D = 64.  bf16, four sequences of 8192 tokens, 16 heads over 4
+// of 128: 1.26 ms of the backward's 2.45.  Where there are too few (sequence, head, key tile) for the GPU, the row tiles of
+// one are dealt to several CTAs, whose fp32 parts are added in their order.
 #include "prompt_tc.cuh"
 
 namespace triattn {
@@ -216,8 +219,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
         if (!ok) *abort_flag = 1;
     } else if (warp == 8) {
         // ------------------------------------------------------------ MMA
-        // One thread runs the loop; the others help where a tile ends with rows that are not the sequence's: they are another's, or
-        // nobody's, and are zeroed up to the next 16, which dV and dK multiply with zeros.
+        // One thread runs the loop; the others help where a tile ends with rows that are not the sequence's: they are
+        // another's, or nobody's, and are zeroed up to the next 16, which dV and dK multiply with zeros.
         const bool leader = elect_one();
         const int lead = __ffs((int)__ballot_sync(0xffffffffu, leader)) - 1;
         const int last_from = (blocks - 1) * P.t.ng, last_rows = min(P.t.tq, q.lq - (blocks - 1) * P.t.tq) * P.t.hp;
@@ -229,8 +232,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
         const int steps = (full_rows + 15) / 16;
         const int whole = steps == 8 ? max(0, (last_from - first + P.splits - 1) / P.splits) : 0;  // tiles before the last block's
         StageRing qs = {0, 0u, false}, qk = {0, 0u, false};  // Q for S, Q for dK
-        // Whole tiles, without a question (a few dozen instructions of one thread are a product's time; by all sixteens of columns, or
-        // by as many as there are).
+        // Whole tiles, without a question (a few dozen instructions of one thread are a product's time; by all sixteens of
+        // columns, or by as many as there are).
         auto straight = [&](auto all, int& u) {
             constexpr bool kAll = decltype(all)::value == 1;
             for (; u > 0 && (u & 3) == 0 && u / 4 + 1 < whole; u += 4) {
@@ -455,8 +458,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
     }
 }
 
-// The CTAs' parts of a (sequence, key head, 128 keys), added in their order.  (Eight CTAs for each of them, four pieces of 32 bytes and
-// their parts a thread: there are few such where parts are made; 3507 tokens, 8 heads over 2 of 128:
+// The CTAs' parts of a (sequence, key head, 128 keys), added in their order.  (Eight CTAs for each of them, four pieces of 32
+// bytes and their parts a thread: there are few such where parts are made; 3507 tokens, 8 heads over 2 of 128:
 // 32 us with one CTA for each, 7 so.)
 constexpr int kJoin = 8;
 template <bool BF16>

@@ -5,19 +5,20 @@
 //     S = Q K^T, dP = dO V^T             rows on the tensor-memory lanes
 //     dS = P (dP - delta)                as 16-bit pairs over dP
 //     dQ += dS K                         dS from tensor memory
-// lse and delta = dO . O (one pass of its own before: half a row a thread at the start of an item was 5 us of each) are one number a
-// thread, dQ stays in tensor memory, and is rounded once: no sum in memory, no order that varies.
-// dS goes to the products as one 16-bit number, which adds as much to the gradient's error as its own rounding does, but as two (the
-// rounding's rest is the second, and one product more) in rows that see up to kFineKeys keys: P spreads over the keys, so those rows
-// carry most of the gradients' norms.  bf16, prompts of 777 to 8192 tokens: off by 0.0018 of dQ's norm with two everywhere, 0.0022 so,
-// 0.0025 with one, 0.0017 by the rounding alone; the backward takes 864, 801 and 775 us.
-// (One kernel for dQ, dK and dV computes S and dP once, five products a tile where the two kernels have seven; but its dQ has to be added
-// up in memory over the key tiles and stands between the tiles' products, and four 128 x 128 x D products a tile from shared memory are more
-// than that gives: four sequences of 8192 tokens, 16 heads over 4 of 128, 3.86 ms, of which 0.5 ms were the reductions.)
+// lse and delta = dO . O (one pass of its own before: half a row a thread at the start of an item was 5 us of each) are one
+// number a thread, dQ stays in tensor memory, and is rounded once: no sum in memory, no order that varies.
+// dS goes to the products as one 16-bit number, which adds as much to the gradient's error as its own rounding does, but as
+// two (the rounding's rest is the second, and one product more) in rows that see up to kFineKeys keys: P spreads over the
+// keys, so those rows carry most of the gradients' norms.  bf16, prompts of 777 to 8192 tokens: off by 0.0018 of dQ's norm
+// with two everywhere, 0.0022 so, 0.0025 with one, 0.0017 by the rounding alone; the backward takes 864, 801 and 775 us.
+// (One kernel for dQ, dK and dV computes S and dP once, five products a tile where the two kernels have seven; but its dQ has
+// to be added up in memory over the key tiles and stands between the tiles' products, and four 128 x 128 x D products a tile
+// from shared memory are more than that gives: four sequences of 8192 tokens, 16 heads over 4 of 128, 3.86 ms, of which 0.5 ms
+// were the reductions.)
 //
-// One CTA a SM, 12 warps: 0-7 softmax and dS (a row's two halves of 64 keys each), 8 MMA, 9 TMA, 10 the items.  Tensor memory: S, dP
-// twice (dS over it), dQ: 4 x 128 columns at D = 128.  The tensor core's order is dQ(i - 2), S(i), dP(i): S(i) follows as soon as S(i - 1) is
-// in registers, and both are there when dS(i - 1) is done, across items too.
+// One CTA a SM, 12 warps: 0-7 softmax and dS (a row's two halves of 64 keys each), 8 MMA, 9 TMA, 10 the items.  Tensor
+// memory: S, dP twice (dS over it), dQ: 4 x 128 columns at D = 128.  The tensor core's order is dQ(i - 2), S(i), dP(i): S(i)
+// follows as soon as S(i - 1) is in registers, and both are there when dS(i - 1) is done, across items too.
 #include "prompt_tc.cuh"
 
 namespace triattn {
@@ -233,8 +234,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
             mma_commit(v_empty(vr.idx));
             vr.next(kVStages);
         };
-        // Step u: dQ of tile u - 2, S and dP of tile u, which is tile j of an item.  Of the two tiles between: sixteens of keys, 16
-        // for an item's first, 32 for its last, 64 for two pieces of dS (0: no tile).
+        // Step u: dQ of tile u - 2, S and dP of tile u, which is tile j of an item.  Of the two tiles between: sixteens of
+        // keys, 16 for an item's first, 32 for its last, 64 for two pieces of dS (0: no tile).
         int keys = 0, lk = 0, j = 0, one = 0, two = 0;
         uint32_t u = 0, items_in = 0, items_out = 0;
         bool there = true, ask = true, clean = false;
@@ -248,8 +249,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                 ++items_out;
             }
         };
-        // Whole key tiles in the middle of an item, without a question (a few dozen instructions of one thread are a product's time;
-        // by all sixteens of columns, or by as many as there are).
+        // Whole key tiles in the middle of an item, without a question (a few dozen instructions of one thread are a
+        // product's time; by all sixteens of columns, or by as many as there are).
         auto straight = [&](auto all) {
             constexpr bool kAll = decltype(all)::value == 1;
             for (const int whole = there && !ask ? keys : 0; j > 2 && two && 128 * (j + 1) < whole; ++j, ++u) {

@@ -8,7 +8,7 @@
 // One CTA a SM, 16 warps:
 //   0-3, 4-7   softmax of tile 0 / 1: thread = row = tensor-memory lane, the row's 128 logits in registers
 //   8-11       epilogue: O / l to memory while the next item has begun
-//   12         tcgen05.mma: S_i = Q_i K^T (shared x shared), O_i += P_i V (P from tensor memory, over S_i)
+//   12         tcgen05.mma, by one thread: S_i = Q_i K^T (shared x shared), O_i += P_i V (P from tensor memory, over S_i)
 //   13         TMA of Q_0, Q_1 and the ring of K and V tiles
 //   14         the items, handed to the others through a ring
 // Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (64 or 128 each): all 512 columns at D = 128.  The tensor core works on
@@ -22,6 +22,13 @@
 // Items go by falling cost (the number of key tiles), one at a time to the CTA that has finished its own: the grid has a
 // block for every item, and a running CTA takes the next block's place by clusterlaunchcontrol.try_cancel, so no
 // counter in memory has to be zeroed and the tail is as short as one item.
+//
+// Bound: the tensor core, 2048 clocks a pair of tiles and 128 keys at D = 128, as long as its products are asked for in time.
+// So one thread issues them, without votes or other lanes to wait for, straight on over whole key tiles and from one item into the
+// next (bf16, 32 heads over 8 of 128; a warp whose waits were votes, before: one chunk of 1216 tokens on a prefix of 30000 425
+// us, 1434 TFLOP/s; so 333 us, 1830; eight prompts of 512 to 4096 tokens 360 and 295, 1480 TFLOP/s, where an item is 9 steps
+// and its first and last are slower).  Heads of 64 are bound by the softmax (two sequences of 16384, 16 heads over 4: 1.01 ms,
+// 1090 TFLOP/s). Code is time as well: a second form of the softmax for the causal border, with fewer columns, cost 3%.
 #include "prompt_tc.cuh"
 
 namespace triattn {
@@ -272,8 +279,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
                 use ^= 4u << i;
                 if (128 * (j + 1) >= keys) mma_commit(o_full(i));
             };
-            // Step j of an item: PV of key tile j - 1, tile 0 then tile 1, behind each QK of key tile j; after the last PV the next
-            // item's first, whose K tile is the next in the ring: its softmax runs while the other tile ends.
+            // Step j of an item: PV of key tile j - 1, tile 0 then tile 1, behind each QK of key tile j; after the last PV
+            // the next item's first, whose K tile is the next in the ring: its softmax runs while the other tile ends.
             int k0 = 0, k1 = 0, lk = 0, n = 0, j = 0;
             bool there = true, clean = false;
             for (;;) {
@@ -290,8 +297,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
                         j = 1;
                     }
                     while (ok && there) {
-                        // Whole key tiles in the middle of an item, without a question (a few dozen instructions of one thread are a
-                        // product's time).
+                        // Whole key tiles in the middle of an item, without a question (a few dozen instructions of one
+                        // thread are a product's time).
                         for (const int whole = min(k0, k1); 128 * (j + 1) < whole; ++j) {
                             const int vst = kr.idx;
                             const uint32_t vph = kr.ph;

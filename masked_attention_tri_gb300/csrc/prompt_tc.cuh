@@ -56,9 +56,10 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
-// Products issued by one thread.  A descriptor is its low word (start and leading offset; the high word is the same for all tiles
-// here: a stride of 1024 bytes, 128-byte swizzle), so that a step to the next 16 of K is one addition, and a thread that runs
-// its loop alone waits for no other lane: the thread that feeds the tensor core has 64 clocks for a product of 128 x 128 x 16.
+// Products issued by one thread.  A descriptor is its low word (start and leading offset; the high word is the same for all
+// tiles here: a stride of 1024 bytes, 128-byte swizzle), so that a step to the next 16 of K is one addition, and a thread that
+// runs its loop alone waits for no other lane: the thread that feeds the tensor core has 64 clocks for a product of 128 x 128
+// x 16.
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | (lbo >> 4 << 16); }
 constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ void issue_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
@@ -96,8 +97,8 @@ __device__ __forceinline__ void issue_rows(uint32_t d, uint32_t a, uint32_t b, u
         }
     }
 }
-// D += A B, A: rows x up to 128 of K in tensor memory, the second 64 of K `HALF` columns on; B: those rows of a tile in shared memory.
-// Sixteens [from, to) of K, of `steps` that there are.
+// D += A B, A: rows x up to 128 of K in tensor memory, the second 64 of K `HALF` columns on; B: those rows of a tile in
+// shared memory. Sixteens [from, to) of K, of `steps` that there are.
 template <int HALF>
 __device__ __forceinline__ void issue_cols(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int from, int to, int steps, bool fresh) {
     if (steps == 8) {
