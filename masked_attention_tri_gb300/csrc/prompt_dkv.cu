@@ -12,10 +12,12 @@
 // order is dV(i), S(i+1), dK(i), dP(i+1): while dS(i) is formed it has dV(i) and S(i+1) to do, and dK(i) and dP(i+1) while
 // P(i+1) is.
 //
-// Bound: the tensor core, 2048 clocks a tile at D = 128 (75% of the time in long sequences), then the softmax warps, two
-// phases of some thousand clocks a tile, which is what counts at D = 64.  bf16, four sequences of 8192 tokens, 16 heads over 4
-// of 128: 1.26 ms of the backward's 2.45.  Where there are too few (sequence, head, key tile) for the GPU, the row tiles of
-// one are dealt to several CTAs, whose fp32 parts are added in their order.
+// Bound: the tensor core and shared memory alike, 2048 clocks a tile at D = 128 (192 KB of operands and 64 KB of loads at 128
+// bytes a clock; a tile takes some 2650), then the softmax warps, two phases of about a thousand clocks a tile, which is what
+// counts at D = 64.  bf16, four sequences of 8192 tokens, 16 heads over 4 of 128: 1.26 ms of the backward's 2.45.  (16 softmax
+// warps of 32 rows: a twentieth less at D = 64, the same at 128, and short sequences pay for the threads.)
+// Where there are too few (sequence, head, key tile) for the GPU, the row tiles of one are dealt to several CTAs, whose fp32
+// parts are added in their order.
 #include "prompt_tc.cuh"
 
 namespace triattn {
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
     const int fine = max(0, (fine_blocks - first + P.splits - 1) / P.splits);
     // Tile j of the walk: its first token, first query head and rows.
     auto tile = [&](int j, int& tok, int& head, int& rows) {
-        const int t = first + j * P.splits, b = t / P.t.ng;
+        const int t = first + j * P.splits, b = P.t.ng == 1 ? t : t / P.t.ng;
         tok = b * P.t.tq;
         head = h * p.G + (t - b * P.t.ng) * P.t.hp;
         rows = min(P.t.tq, q.lq - tok) * P.t.hp;
@@ -325,11 +327,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
             const int s = j & 1;
             int tok, head, rows;
             tile(j, tok, head, rows);
-            // the rows that see this key: from `from` on, of those that exist
-            const long long from = (long long)(k0 + kr - q.shift - tok) * P.t.hp;
             const bool edge = rows < 128 || keys < 128 || k0 + 127 > tok + q.shift;
             uint32_t see[2] = {0xffffffffu, 0xffffffffu};
             if (edge) {
+                // the rows that see this key: from `from` on, of those that exist
+                const long long from = (long long)(k0 + kr - q.shift - tok) * P.t.hp;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int c0 = 64 * half + 32 * i;
@@ -339,8 +341,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
             }
             const float4* nl = reinterpret_cast<const float4*>(row_s + s * 256 + 64 * half);
             const float4* nd = nl + 32;
-            ok = __all_sync(0xffffffffu, wait(row_full(s), (uint32_t)(j / 2) & 1u, abort_flag, p.status)) &&
-                 __all_sync(0xffffffffu, wait(s_full, ph, abort_flag, p.status));
+            ok = __all_sync(0xffffffffu, wait(row_full(s), (uint32_t)(j / 2) & 1u, abort_flag, p.status) &&
+                                             wait(s_full, ph, abort_flag, p.status));
             if (!ok) break;
             tc_fence_after();
             float pr[64];

@@ -19,6 +19,9 @@
 // One CTA a SM, 12 warps: 0-7 softmax and dS (a row's two halves of 64 keys each), 8 MMA, 9 TMA, 10 the items.  Tensor
 // memory: S, dP twice (dS over it), dQ: 4 x 128 columns at D = 128.  The tensor core's order is dQ(i - 2), S(i), dP(i): S(i)
 // follows as soon as S(i - 1) is in registers, and both are there when dS(i - 1) is done, across items too.
+//
+// Bound: shared memory, 1792 clocks a tile at D = 128 (160 KB of operands, 64 KB of loads), the tensor core 1536, the softmax
+// warps' two phases 1500 and more; a tile takes some 1900.  Four sequences of 8192 tokens, 16 heads over 4 of 128: 0.94 ms.
 #include "prompt_tc.cuh"
 
 namespace triattn {
