@@ -287,7 +287,7 @@ def kv_cache_read(cache: Union[PagedKVCache, PagedKVCache4], page_table, kv_leng
             raise ValueError(f"out_k and out_v must have the cache's {Hk} heads")
     if total == 0 or S == 0:
         return out_k, out_v
-    seqs = (_ptr(cu_seqlens), _ptr(kv_lengths), _ptr(page_table), S, total, max_seqlen, Hk, D)
+    seqs = (_ptr(cu_seqlens), _ptr(kv_lengths), _ptr(page_table), S, total, min(max_seqlen, total), Hk, D)
     outs = (_ptr(out_k), _ptr(out_v), _DT[dtype], k_rs, v_rs, _stream(dev))
     with _on(dev):
         if isinstance(cache, PagedKVCache4):

@@ -45,7 +45,7 @@ def _prompt_args(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k
         strides = strides[0], 0, 0
     s = 1.0 / math.sqrt(D) if scale is None else float(scale)
     args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _DT[dtype], cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), S, total_q,
-            total_k or 1, int(max_seqlen_q), int(max_seqlen_k), Hq, Hk, D, s, *strides)
+            total_k or 1, min(int(max_seqlen_q), total_q), min(int(max_seqlen_k), total_k), Hq, Hk, D, s, *strides)
     return args, S, (k, v)
 
 

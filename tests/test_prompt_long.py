@@ -147,3 +147,47 @@ def test_fresh_threads():
         _in_thread(lambda c=c, got=got: got.extend(c()))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_any_upper_bound_of_the_lengths():
+    """max_seqlen is an upper bound: one beyond the rows there are, or beyond int32, is as good as the longest length."""
+    import masked_attention_tri_gb300 as ta
+    lq = [70, 130]
+    q, k, v, g = _inputs(lq, lq, 4, 2, 64, BF)
+    cu, most = _i32(_cu(lq)), 2 ** 32 + 5
+    o, lse = ta.prompt_attention(q, k, v, cu, cu, 130, 130, return_aux=True)
+    o2, lse2 = ta.prompt_attention(q, k, v, cu, cu, most, most, return_aux=True)
+    d = ta.prompt_attention_backward(q, k, v, cu, cu, 130, 130, o, lse, g)
+    d2 = ta.prompt_attention_backward(q, k, v, cu, cu, most, most, o, lse, g)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and all(torch.equal(a, b) for a, b in zip(d, d2))
+    cache = ta.PagedKVCache4.empty(4, 2, 64, 64)
+    table, held = _i32([[0, 1, 0], [1, 2, 3]]), _i32([70, 130])
+    ta.kv_cache_append(cache, k[70:], v[70:], table[1:], held[1:], _i32([0, 130]), 130)
+    a = ta.kv_cache_read(cache, table[1:], held[1:], _i32([0, 130]), 130, 130)
+    b = ta.kv_cache_read(cache, table[1:], held[1:], _i32([0, 130]), most, 130)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    # pages may be read by several sequences, and twice by one
+    twice = ta.kv_cache_read(cache, _i32([[1, 1], [1, 2]]), _i32([128, 128]), _i32([0, 128, 256]), 128, 256)
+    for x, y in zip(twice, a):
+        assert torch.equal(x[:64], y[:64]) and torch.equal(x[64:128], y[:64]) and torch.equal(x[128:], y[:128])
+    assert ta.get_status() == 0
+
+
+def test_one_leaf_alone_and_through_rotation():
+    """Gradients where one input asks for them, and along the chain rotation -> attention."""
+    import masked_attention_tri_gb300 as ta
+    lq = [200, 31]
+    q, k, v, g = _inputs(lq, lq, 4, 2, 64, BF)
+    cu = _i32(_cu(lq))
+    rotary = ta.Rotary(64, sections=(16, 8, 8), device="cuda")
+    positions = torch.randint(0, 5000, (3, 231), dtype=torch.int32, device="cuda")
+    qr, kr = ta.rotary_embedding(q, k, positions, rotary)
+    o, lse = ta.prompt_attention(qr, kr, v, cu, cu, 200, 200, return_aux=True)
+    dq, dk, dv = ta.prompt_attention_backward(qr, kr, v, cu, cu, 200, 200, o, lse, g)
+    dq, dk = ta.rotary_embedding_backward(dq, dk, positions, rotary)
+    for ask in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 1)):
+        leaves = [t.clone().requires_grad_(bool(a)) for t, a in zip((q, k, v), ask)]
+        turned = ta.rotary_embedding_autograd(leaves[0], leaves[1], positions, rotary)
+        ta.prompt_attention_autograd(*turned, leaves[2], cu, cu, 200, 200).backward(g)
+        for leaf, a, want in zip(leaves, ask, (dq, dk, dv)):
+            assert torch.equal(leaf.grad, want) if a else leaf.grad is None
