@@ -424,8 +424,10 @@ cudaError_t backward(const PromptParams& p, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t launch(const PromptParams& p, bool back, cudaStream_t stream) {
-    if (p.D <= 64) return back ? backward<T, 1>(p, stream) : forward<T, 1>(p, stream);
-    if (p.D <= 128) return back ? backward<T, 2>(p, stream) : forward<T, 2>(p, stream);
+    if constexpr (sizeof(T) == 4) {  // (16-bit rows of these widths run on tensor cores)
+        if (p.D <= 64) return back ? backward<T, 1>(p, stream) : forward<T, 1>(p, stream);
+        if (p.D <= 128) return back ? backward<T, 2>(p, stream) : forward<T, 2>(p, stream);
+    }
     return back ? backward<T, 4>(p, stream) : forward<T, 4>(p, stream);
 }
 
