@@ -1,7 +1,7 @@
 // kv_append4.cu -- new keys and values of packed sequences into the pages of a 4-bit cache (cache4.cuh), with the rotation of k
 // and of q on the way.
 //
-// Bound: memory, with the arithmetic of the codes close behind: eight prompts of 256 to 2048 tokens, 8 heads of 128, 18 us (2.6
+// Bound: memory, with the arithmetic of the codes close behind: eight prompts of 256 to 2048 tokens, 8 heads of 128, 16.6 us (2.9
 // TB/s; 27 by kv_append.cu's threads of half groups with two divisions an element).  One CTA takes some rows of one page of one
 // sequence and one job: some heads of k, of v or of q.  A thread takes a group of 16 elements, or, where the halves of a head
 // turn together, a group and its partner half a turn away; so no lane waits for another, a row is read and written once, and
@@ -16,7 +16,7 @@
 namespace triattn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;    // of a CTA, at most
 constexpr int kRows = 16;        // rows of a CTA, at most
 constexpr int kMaxHeads = 32;    // heads of a CTA, at most
 
@@ -88,8 +88,8 @@ __device__ __forceinline__ void store_codes(uint8_t* codes, uint8_t* scale, cons
 }
 
 // BOTH: units of two groups (the halves of a head turn together); else each is one.
-template <typename T, bool BOTH>
-__global__ void __launch_bounds__(kThreads) kv_append4_kernel(const Append4Args a) {
+template <typename T, bool BOTH, int THREADS>
+__global__ void __launch_bounds__(THREADS) kv_append4_kernel(const Append4Args a) {
     constexpr int kAhead = (BOTH ? 4 : 8) / (int)sizeof(T);    // units in flight a thread
     extern __shared__ float2 table[];          // cos and sin of (row, pair)
     __shared__ float inv_s[kMaxHeads];         // reciprocals of the heads' factors
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) kv_append4_kernel(const Append4Args 
     const bool turn = kind != 1 && p.dim > 0;
     const int np = p.dim / 2;
     if (turn) {
-        for (int e = threadIdx.x; e < cnt * np; e += kThreads) {
+        for (int e = threadIdx.x; e < cnt * np; e += THREADS) {
             const int t = e / np, i = e - t * np;
             const int pos = p.positions ? rotary_position(p.positions, p.axes, p.num_axes, i, p.total, tok0 + t) : s0 + t;
             const float2 cs = rotary_cos_sin(pos, p.turns[i]);
@@ -155,20 +155,20 @@ __global__ void __launch_bounds__(kThreads) kv_append4_kernel(const Append4Args 
         x.at = !BOTH || x.two ? 16 * u : 16 * (u + a.both);
         return x;
     };
-    for (int e0 = threadIdx.x; e0 < items; e0 += kAhead * kThreads) {
+    for (int e0 = threadIdx.x; e0 < items; e0 += kAhead * THREADS) {
         Group<T> x[kAhead], y[BOTH ? kAhead : 1];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            if (e0 + j * kThreads >= items) break;
-            const Place b = place(e0 + j * kThreads);
+            if (e0 + j * THREADS >= items) break;
+            const Place b = place(e0 + j * THREADS);
             const T* from = src + (tok0 + b.row) * rs + (long long)b.head * p.D + b.at;
             x[j].load(from);
             if (BOTH && b.two) y[BOTH ? j : 0].load(from + np);
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            if (e0 + j * kThreads >= items) break;
-            const Place b = place(e0 + j * kThreads);
+            if (e0 + j * THREADS >= items) break;
+            const Place b = place(e0 + j * THREADS);
             float f[16], g[16];
             x[j].floats(f);
             if (BOTH && b.two) y[BOTH ? j : 0].floats(g);
@@ -234,8 +234,11 @@ cudaError_t launch(const KvAppendParams& p, cudaStream_t stream) {
     if (gx > 0x7fffffffLL || gy > 65535) return cudaErrorInvalidConfiguration;
     const size_t smem = (size_t)rows * (p.dim / 2) * sizeof(float2);  // at most 16 KB
     const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)parts);
-    if (a.both > 0) kv_append4_kernel<T, true><<<grid, kThreads, smem, stream>>>(a);
-    else kv_append4_kernel<T, false><<<grid, kThreads, smem, stream>>>(a);
+    // Half as many threads where nothing turns and no table is shared (the prompts above: 16.6 us for 18.6; with k and 32
+    // heads of q turned 62 for 61).
+    if (a.both > 0) kv_append4_kernel<T, true, kThreads><<<grid, kThreads, smem, stream>>>(a);
+    else if (p.dim > 0) kv_append4_kernel<T, false, kThreads><<<grid, kThreads, smem, stream>>>(a);
+    else kv_append4_kernel<T, false, kThreads / 2><<<grid, kThreads / 2, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
