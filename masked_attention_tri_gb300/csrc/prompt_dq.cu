@@ -200,18 +200,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
             if (ok) ok = wait(b, parity, abort_flag, p.status);
             tc_fence_after();
         };
-        auto fetch = [&](int& keys, int& lk) -> bool {  // the next item that has keys
-            for (;;) {
-                const int r = item_n % kRing;
-                await(it_full(r), (uint32_t)(item_n / kRing) & 1u);
-                if (!ok) return false;
-                const bool on = items[r].on != 0;
-                keys = items[r].keys[0];
-                lk = items[r].lq + items[r].shift;
-                mbar_arrive(it_empty(r));
-                ++item_n;
-                if (!on || keys > 0) return on;
-            }
+        auto fetch = [&](int& keys, int& lk) -> bool {  // the next item
+            const int r = item_n % kRing;
+            await(it_full(r), (uint32_t)(item_n / kRing) & 1u);
+            if (!ok) return false;
+            const bool on = items[r].on != 0;
+            keys = items[r].keys[0];
+            lk = items[r].lq + items[r].shift;
+            mbar_arrive(it_empty(r));
+            ++item_n;
+            return on;
         };
         // dQ of tile u (of all that the CTA walks), whose dS is in buffer u % 2
         auto dq_mma = [&](uint32_t u, int steps, bool fresh, bool fine) {
@@ -280,7 +278,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                     }
                     if (!ok) break;
                     if (ask) {
-                        there = fetch(keys, lk);
+                        // The first item that has keys.  Past one without, the last dQ of the item before may wait no longer:
+                        // the ring's third item from there waits for the warps that wait for it.
+                        while ((there = fetch(keys, lk)) && keys <= 0) {
+                            if (one) finish(one, u - 1u);
+                            one = 0;
+                            if (!ok) break;
+                        }
+                        if (!ok) break;
                         ask = false;
                         j = 0;
                         if (there) {

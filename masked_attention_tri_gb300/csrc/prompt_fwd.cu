@@ -229,20 +229,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
                 if (ok) ok = wait(b, parity, abort_flag, p.status);
                 tc_fence_after();
             };
-            // The next item that has keys: those of its tiles, and of its sequence.
+            // The next item: the keys of its tiles, and of its sequence.  One at a time while a product of the item before is
+            // pending: the ring's third item from there waits for the epilogue, and the epilogue for that product.
             auto fetch = [&](int& k0, int& k1, int& lk) -> bool {
-                for (;;) {
-                    const int r = item_n % kRing;
-                    await(it_full(r), (uint32_t)(item_n / kRing) & 1u);
-                    if (!ok) return false;
-                    const bool on = items[r].on != 0;
-                    k0 = items[r].keys[0];
-                    k1 = items[r].keys[1];
-                    lk = items[r].lq + items[r].shift;
-                    mbar_arrive(it_empty(r));
-                    ++item_n;
-                    if (!on || max(k0, k1) > 0) return on;
-                }
+                const int r = item_n % kRing;
+                await(it_full(r), (uint32_t)(item_n / kRing) & 1u);
+                if (!ok) return false;
+                const bool on = items[r].on != 0;
+                k0 = items[r].keys[0];
+                k1 = items[r].keys[1];
+                lk = items[r].lq + items[r].shift;
+                mbar_arrive(it_empty(r));
+                ++item_n;
+                return on;
             };
             // S_i of key tile j of a tile that sees `keys`, K in stage st
             auto qk = [&](int i, int keys, int j, int st) {
@@ -286,17 +285,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
             for (;;) {
                 int tail = 0, tail_st = 0;
                 if (leader) {
-                    if (j == 0) {
-                        there = fetch(k0, k1, lk);
-                        if (there) await(kv_full(kr.idx), kr.ph);
-                        if (there && ok && k0 > 0) qk(0, k0, 0, kr.idx);
-                        if (there && ok && k1 > 0) qk(1, k1, 0, kr.idx);
-                        if (there && ok) mma_commit(kv_empty(kr.idx));
-                        kr.next(S);
-                        n = (max(k0, k1) + 127) / 128;
-                        j = 1;
-                    }
                     while (ok && there) {
+                        if (j == 0) {  // (nothing is pending)
+                            do there = fetch(k0, k1, lk);
+                            while (there && max(k0, k1) <= 0);
+                            if (there) await(kv_full(kr.idx), kr.ph);
+                            if (!there || !ok) break;
+                            if (k0 > 0) qk(0, k0, 0, kr.idx);
+                            if (ok && k1 > 0) qk(1, k1, 0, kr.idx);
+                            if (!ok) break;
+                            mma_commit(kv_empty(kr.idx));
+                            kr.next(S);
+                            n = (max(k0, k1) + 127) / 128;
+                            j = 1;
+                        }
                         // Whole key tiles in the middle of an item, without a question (a few dozen instructions of one
                         // thread are a product's time).
                         for (const int whole = min(k0, k1); 128 * (j + 1) < whole; ++j) {
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
                             k1 = n1;
                             lk = nlk;
                             n = (max(k0, k1) + 127) / 128;
-                            j = 1;
+                            j = n > 0 ? 1 : 0;  // (an item without keys: its rows are the epilogue's)
                         }
                     }
                 }
