@@ -691,6 +691,15 @@ size_t tri_attn_prompt_bwd_workspace_size(ta_dtype dtype, int num_seqs, int tota
                                           int max_seqlen_k, int Hq, int Hk, int D);
 
 /*
+ * tri_attn_zero_rest -- zeros into the rows of a packed buffer that no sequence has.
+ *   x             (total, H, D) of `dtype`, contiguous, 16-byte aligned; D as in tri_attn_fwd.
+ *   cu_seqlens    (num_seqs + 1) int32: the rows before cu[0] and from cu[num_seqs] on become 0, the others stay.
+ * For what the packed operators leave alone: the rows of gradients, say, that are summed over all rows afterwards.
+ */
+ta_status tri_attn_zero_rest(void* x, ta_dtype dtype, const int32_t* cu_seqlens, int num_seqs, int total, int H, int D,
+                             void* stream);
+
+/*
  * tri_attn_get_status -- synchronize `stream`, then read and clear the
  * device-side status word of the current device.  Returns TA_OK, or the first
  * TA_ERR_TIMEOUT / TA_ERR_DEVICE recorded by a kernel since the last call, or

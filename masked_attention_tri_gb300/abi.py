@@ -26,6 +26,7 @@ EXPORTS = ("tri_attn_fwd", "tri_attn_fwd_strided", "tri_attn_varlen_fwd", "tri_a
            "tri_attn_rotary", "tri_attn_kv_append", "tri_attn_paged_fwd", "tri_attn_paged_workspace_size",
            "tri_attn_rotary_axes", "tri_attn_kv_append_axes", "tri_attn_kv_append4", "tri_attn_kv_read", "tri_attn_kv_read4",
            "tri_attn_paged4_fwd", "tri_attn_prompt_fwd", "tri_attn_prompt_bwd", "tri_attn_prompt_bwd_workspace_size",
+           "tri_attn_zero_rest",
            "tri_attn_mask_to_kv_lengths", "tri_attn_get_status", "tri_attn_error_string", "tri_attn_version")
 
 
@@ -118,6 +119,8 @@ def load() -> ctypes.CDLL:
         lib.tri_attn_prompt_bwd.restype = I
         lib.tri_attn_prompt_bwd_workspace_size.argtypes = [I] * 9
         lib.tri_attn_prompt_bwd_workspace_size.restype = Z
+        lib.tri_attn_zero_rest.argtypes = [P, I, P, I, I, I, I, P]
+        lib.tri_attn_zero_rest.restype = I
         lib.tri_attn_mask_to_kv_lengths.argtypes = [P, I, I, I, P, P, P]
         lib.tri_attn_mask_to_kv_lengths.restype = I
         lib.tri_attn_get_status.argtypes = [P]
@@ -390,6 +393,11 @@ def tri_attn_prompt_bwd(q, k, v, dtype, cu_seqlens_q, cu_seqlens_k, num_seqs, to
 def tri_attn_prompt_bwd_workspace_size(dtype, num_seqs, total_q, total_k, max_seqlen_q, max_seqlen_k, Hq, Hk, D) -> int:
     return int(load().tri_attn_prompt_bwd_workspace_size(dtype, num_seqs, total_q, total_k, max_seqlen_q, max_seqlen_k, Hq, Hk,
                                                          D))
+
+
+def tri_attn_zero_rest(x, dtype, cu_seqlens, num_seqs, total, H, D, stream) -> None:
+    st = load().tri_attn_zero_rest(x, dtype, cu_seqlens, num_seqs, total, H, D, stream or None)
+    _check(st, "tri_attn_zero_rest")
 
 
 def tri_attn_mask_to_kv_lengths(mask, B, N, K, kv_lengths, nonprefix_count, stream) -> None:

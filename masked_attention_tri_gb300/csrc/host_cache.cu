@@ -588,3 +588,13 @@ TA_EXPORT ta_status tri_attn_prompt_bwd(const void* q, const void* k, const void
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return launched(prompt_on_tc(dtype, D) ? launch_prompt_tc_bwd(p, s) : launch_prompt_simt_bwd(p, s));
 }
+
+TA_EXPORT ta_status tri_attn_zero_rest(void* x, ta_dtype dtype, const int32_t* cu_seqlens, int num_seqs, int total, int H, int D,
+                                       void* stream) {
+    if (!x || !cu_seqlens || num_seqs < 0 || total < 0 || H <= 0 || D <= 0) return TA_ERR_INVALID_ARG;
+    if (!valid_dtype(dtype) || !aligned(x, 16) || !aligned(cu_seqlens, 4)) return TA_ERR_INVALID_ARG;
+    if (!supported_d(dtype, D)) return TA_ERR_UNSUPPORTED;
+    if (total == 0) return TA_OK;
+    return launched(launch_zero_rest(x, (long long)H * D * dtype_bytes(dtype), cu_seqlens, num_seqs, total,
+                                     static_cast<cudaStream_t>(stream)));
+}

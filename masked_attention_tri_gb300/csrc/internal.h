@@ -258,6 +258,9 @@ cudaError_t launch_prompt_tc_fwd(const PromptParams& p, cudaStream_t stream);
 cudaError_t launch_prompt_tc_bwd(const PromptParams& p, cudaStream_t stream);
 int prompt_bwd_splits(int num_seqs, int total_k, int max_q, int max_k, int Hk, int G);  // CTAs of a key tile there
 
+// Zeros into the rows [0, cu[0]) and [cu[num_seqs], total) of x, row_bytes (a multiple of 16) each.
+cudaError_t launch_zero_rest(void* x, long long row_bytes, const int32_t* cu, int num_seqs, int total, cudaStream_t stream);
+
 // Device address of the status word on the current device (set up once per device).
 int* status_word();
 

@@ -104,10 +104,20 @@ def prompt_attention_backward(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
     return dq, dk, dv
 
 
+def _zero_rest(x, cu):
+    """Zeros into the rows of x that no sequence of cu has (what comes after sums over all rows)."""
+    total, H, D = x.shape
+    if total:
+        with _on(x.device):
+            abi.tri_attn_zero_rest(_ptr(x), _DT[x.dtype], _ptr(cu), cu.numel() - 1, total, H, D, _stream(x.device))
+    return x
+
+
 class _PromptFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, cu_q, cu_k, max_q, max_k, scale):
         out, lse = prompt_attention(q, k, v, cu_q, cu_k, max_q, max_k, scale, return_aux=True)
+        _zero_rest(out, cu_q)
         ctx.save_for_backward(q, k, v, cu_q, cu_k, out, lse)
         ctx.sizes = max_q, max_k, scale
         return out
@@ -118,11 +128,14 @@ class _PromptFn(torch.autograd.Function):
         q, k, v, cu_q, cu_k, out, lse = ctx.saved_tensors
         max_q, max_k, scale = ctx.sizes
         dq, dk, dv = prompt_attention_backward(q, k, v, cu_q, cu_k, max_q, max_k, out, lse, d_out.contiguous(), scale)
-        return dq, dk, dv, None, None, None, None, None
+        return _zero_rest(dq, cu_q), _zero_rest(dk, cu_k), _zero_rest(dv, cu_k), None, None, None, None, None
 
 
 def prompt_attention_autograd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale=None):
     """``prompt_attention`` (O alone) with gradients for q, k and v (of first order).
+
+    Rows that belong to no sequence (before the first entries of cu_seqlens and from the last ones on) get O = 0 and
+    gradients of 0, whatever they hold.
 
     Its backward may be captured into a graph, as any autograd function's, only while no
     graph of the same leaves made outside the capture lives (PyTorch ties the leaves'
