@@ -40,6 +40,13 @@ def _new(t: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """t as the kernels read it: contiguous and on a 16-byte boundary (a gradient may be a slice of another, as torch.cat's
+    are)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _check_out(out, shape, dtype) -> None:
     """A preallocated output must be exactly what the kernels write: they store whole rows of
     `shape` in `dtype`, so a smaller or differently typed buffer would be overrun."""
@@ -254,7 +261,7 @@ class _TriangleAttentionFn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, d_out, _d_lse, _d_mx):
         q, k, v, bias, mask, kv_lengths, lse, o = ctx.saved_tensors
-        dq, dk, dv, dbias = triangle_attention_backward(q, k, v, bias, lse, d_out.contiguous(), mask, ctx.scale,
+        dq, dk, dv, dbias = triangle_attention_backward(q, k, v, bias, lse, _dense(d_out), mask, ctx.scale,
                                                         kv_lengths=kv_lengths, need_dbias=ctx.needs_input_grad[3],
                                                         out=o)
         return dq, dk, dv, dbias, None, None, None

@@ -11,7 +11,7 @@ from typing import Optional
 import torch
 
 from . import abi
-from .api import _DT, _need, _new, _on, _ptr, _row_stride, _stream
+from .api import _DT, _dense, _need, _new, _on, _ptr, _row_stride, _stream
 
 _SCALINGS = (None, "linear", "ntk", "yarn")
 
@@ -218,8 +218,8 @@ class _RotaryFn(torch.autograd.Function):
         # (the turn is linear: its gradient is the opposite turn, itself differentiable, for second derivatives)
         (positions,) = ctx.saved_tensors
         if d_k is None:
-            return _RotaryFn.apply(d_q.contiguous(), None, positions, ctx.rotary, not ctx.inverse), None, None, None, None
-        d_q, d_k = _RotaryFn.apply(d_q.contiguous(), d_k.contiguous(), positions, ctx.rotary, not ctx.inverse)
+            return _RotaryFn.apply(_dense(d_q), None, positions, ctx.rotary, not ctx.inverse), None, None, None, None
+        d_q, d_k = _RotaryFn.apply(_dense(d_q), _dense(d_k), positions, ctx.rotary, not ctx.inverse)
         return d_q, d_k, None, None, None
 
 

@@ -10,7 +10,7 @@ import math
 import torch
 
 from . import abi
-from .api import _DT, _check_out, _need, _new, _on, _ptr, _row_stride, _stream
+from .api import _DT, _check_out, _dense, _need, _new, _on, _ptr, _row_stride, _stream
 
 
 def _prompt_args(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale):
@@ -127,7 +127,7 @@ class _PromptFn(torch.autograd.Function):
     def backward(ctx, d_out):
         q, k, v, cu_q, cu_k, out, lse = ctx.saved_tensors
         max_q, max_k, scale = ctx.sizes
-        dq, dk, dv = prompt_attention_backward(q, k, v, cu_q, cu_k, max_q, max_k, out, lse, d_out.contiguous(), scale)
+        dq, dk, dv = prompt_attention_backward(q, k, v, cu_q, cu_k, max_q, max_k, out, lse, _dense(d_out), scale)
         return _zero_rest(dq, cu_q), _zero_rest(dk, cu_k), _zero_rest(dv, cu_k), None, None, None, None, None
 
 
