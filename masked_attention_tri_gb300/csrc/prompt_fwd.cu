@@ -285,20 +285,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
             for (;;) {
                 int tail = 0, tail_st = 0;
                 if (leader) {
+                    if (j == 0) {  // (nothing is pending)
+                        do there = fetch(k0, k1, lk);
+                        while (there && max(k0, k1) <= 0);
+                        if (there) await(kv_full(kr.idx), kr.ph);
+                        if (there && ok && k0 > 0) qk(0, k0, 0, kr.idx);
+                        if (there && ok && k1 > 0) qk(1, k1, 0, kr.idx);
+                        if (there && ok) mma_commit(kv_empty(kr.idx));
+                        kr.next(S);
+                        n = (max(k0, k1) + 127) / 128;
+                        j = 1;
+                    }
                     while (ok && there) {
-                        if (j == 0) {  // (nothing is pending)
-                            do there = fetch(k0, k1, lk);
-                            while (there && max(k0, k1) <= 0);
-                            if (there) await(kv_full(kr.idx), kr.ph);
-                            if (!there || !ok) break;
-                            if (k0 > 0) qk(0, k0, 0, kr.idx);
-                            if (ok && k1 > 0) qk(1, k1, 0, kr.idx);
-                            if (!ok) break;
-                            mma_commit(kv_empty(kr.idx));
-                            kr.next(S);
-                            n = (max(k0, k1) + 127) / 128;
-                            j = 1;
-                        }
                         // Whole key tiles in the middle of an item, without a question (a few dozen instructions of one
                         // thread are a product's time).
                         for (const int whole = min(k0, k1); 128 * (j + 1) < whole; ++j) {
@@ -377,13 +375,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
                             k1 = n1;
                             lk = nlk;
                             n = (max(k0, k1) + 127) / 128;
-                            j = n > 0 ? 1 : 0;  // (an item without keys: its rows are the epilogue's)
+                            j = 1;
+                            if (there && n == 0) {  // an item without keys: its rows are the epilogue's
+                                j = 0;
+                                tail = -1;
+                                break;
+                            }
                         }
                     }
                 }
                 tail = __shfl_sync(0xffffffffu, tail, lead);
                 if (tail == 0) break;
-                clear_rows<NB>(kv_smem(__shfl_sync(0xffffffffu, tail_st, lead)), tail, (tail + 15) & ~15);
+                if (tail > 0) clear_rows<NB>(kv_smem(__shfl_sync(0xffffffffu, tail_st, lead)), tail, (tail + 15) & ~15);
             }
             if (!ok && leader) *abort_flag = 1;
             if (leader) mma_commit(drain);
