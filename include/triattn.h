@@ -677,7 +677,10 @@ ta_status tri_attn_prompt_fwd(const void* q, const void* k, const void* v, ta_dt
  *   workspace     device scratch of tri_attn_prompt_bwd_workspace_size(...) bytes, 256-byte aligned, owned by the caller;
  *                 two calls in flight must not share it.
  * Arithmetic as in the forward (P and dx rounded to the inputs' type as operands on tensor cores; dx as two such numbers
- * for queries that see up to 512 keys).  Results do not vary from run to run.  Errors as tri_attn_prompt_fwd.
+ * for queries that see up to 512 keys).  In fp16 the operands are held times powers of two, P 2^14 and dx as much as the
+ * bound |dO| max |V| + |dO . O| leaves below 2^15 (of the query for dQ, of the sequence's queries on the key head for dK), so
+ * that small dO, as a mean loss gives, and large ones keep their gradients: dx is off by 2^-39 of that bound beside its
+ * rounding.  (The gradients themselves are fp16 numbers, which end at 2^-24.)  Results do not vary from run to run.  Errors as tri_attn_prompt_fwd.
  */
 ta_status tri_attn_prompt_bwd(const void* q, const void* k, const void* v, ta_dtype dtype, const int32_t* cu_seqlens_q,
                               const int32_t* cu_seqlens_k, int num_seqs, int total_q, int total_k, int max_seqlen_q,

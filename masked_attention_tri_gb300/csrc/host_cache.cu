@@ -389,7 +389,7 @@ ta_status prompt_params(const void* q, const void* k, const void* v, ta_dtype dt
     return TA_OK;
 }
 
-// The backward's workspace: dO . O, and fp32 parts of dK and dV where several CTAs share them (tensor cores); its size, and
+// The backward's workspace: dO . O, in fp16 what scales dS (prompt_tc.cuh), and fp32 parts of dK and dV where several CTAs share them (tensor cores); its size, and
 // with p its parts.
 size_t prompt_workspace(int dtype, int num_seqs, int total_q, int total_k, int max_q, int max_k, int Hq, int Hk, int D,
                         char* ws, PromptParams* p) {
@@ -397,11 +397,15 @@ size_t prompt_workspace(int dtype, int num_seqs, int total_q, int total_k, int m
     if (max_k > total_k) max_k = total_k;
     const size_t rows = ((size_t)total_q * Hq + 63) / 64 * 64 * sizeof(float);
     const int splits = prompt_on_tc(dtype, D) ? prompt_bwd_splits(num_seqs, total_k, max_q, max_k, Hk, Hq / Hk) : 1;
+    const bool scaled = dtype == TA_F16 && prompt_on_tc(dtype, D);
+    const size_t most = scaled ? ((size_t)num_seqs * Hk * 3 + 63) / 64 * 64 * sizeof(float) : 0, sums = rows + (scaled ? rows + most : 0);
     if (p) {
         p->delta = reinterpret_cast<float*>(ws);
-        p->parts = splits > 1 ? reinterpret_cast<float*>(ws + rows) : nullptr;
+        p->norm = scaled ? reinterpret_cast<float*>(ws + rows) : nullptr;
+        p->most = scaled ? reinterpret_cast<float*>(ws + 2 * rows) : nullptr;
+        p->parts = splits > 1 ? reinterpret_cast<float*>(ws + sums) : nullptr;
     }
-    return rows + (splits > 1 ? (size_t)splits * 2 * total_k * Hk * D * sizeof(float) : 0);
+    return sums + (splits > 1 ? (size_t)splits * 2 * total_k * Hk * D * sizeof(float) : 0);
 }
 
 }  // namespace

@@ -248,6 +248,8 @@ struct PromptParams {
     void* dk;
     void* dv;
     float* delta;               // workspace: dO . O (Hq, total_q)
+    float* norm;                // workspace, fp16 on tensor cores (else NULL): |dO| of the rows (Hq, total_q)
+    float* most;                // workspace, with norm: the largest |V|, |dO| and |delta| of each (sequence, key head) (num_seqs, Hk, 3)
     float* parts;               // workspace: fp32 parts of dK and dV (splits, 2, total_k, Hk, D) where several CTAs share them, else NULL
 };
 // 16-bit inputs with D <= 128 run on tensor cores.

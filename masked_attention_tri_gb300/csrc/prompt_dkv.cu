@@ -6,6 +6,7 @@
 //     S^T = K Q^T, dP^T = V dO^T         keys on the tensor-memory lanes, rows of the tile in the columns
 //     dV += P^T dO                       P^T as 16-bit pairs over S^T
 //     dS = P (dP - delta),  dK += dS^T Q dS^T as 16-bit pairs over dP^T (as two in rows that see few keys: prompt_dq.cu)
+// (fp16: P and dS times powers of two, prompt_tc.cuh).
 // Tensor memory: S^T, dP^T, dV, dK: 4 x 128 columns at D = 128.  The sums over the group's heads are sums over rows.
 //
 // 12 warps: 0-7 softmax and dS (key = lane, 64 rows each half), 8 MMA, 9 TMA, 10 the rows' lse and delta.  The tensor core's
@@ -95,6 +96,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
             }
         }
         return;
+    }
+    // fp16: the exponents by which P and dS are held (prompt_tc.cuh).
+    constexpr int kP = BF16 ? 0 : kHalfP;
+    int ds_exp = 0;
+    if constexpr (!BF16) {
+        const float* most = p.most + ((long long)seq * p.Hk + h) * 3;
+        ds_exp = half_exponent(fmaf(most[0], most[1], most[2]));
     }
     // The tiles of the walk whose rows see up to kFineKeys keys.
     const int fine_blocks = min(blocks, max(0, kFineKeys - q.shift) / P.t.tq) * P.t.ng;
@@ -212,8 +220,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
             if (!ok) break;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                row_s[s * 256 + 32 * i + lane] = -a[i] * tc::kLog2e;
-                row_s[s * 256 + 128 + 32 * i + lane] = -b[i];
+                row_s[s * 256 + 32 * i + lane] = fmaf(-a[i], tc::kLog2e, (float)kP);
+                row_s[s * 256 + 128 + 32 * i + lane] = BF16 ? -b[i] : -b[i] * pow2(ds_exp - kP);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(row_full(s));
@@ -322,6 +330,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
         const uint32_t lane_off = (uint32_t)(warp % 4 * 32) << 16;
         const uint32_t sA = tS + lane_off + 64u * half, dpA = tDP + lane_off + 64u * half;
         const float f = P.scale_log2e;
+        [[maybe_unused]] const float2 ds2 = make_float2(pow2(ds_exp - kP), pow2(ds_exp - kP));
+        auto less_delta = [&](uint32_t x, uint32_t y, float2 d) {  // (d: -delta as it is held)
+            const float2 v = make_float2(__uint_as_float(x), __uint_as_float(y));
+            return BF16 ? __fadd2_rn(v, d) : __ffma2_rn(v, ds2, d);
+        };
         for (int j = 0; j < n && ok; ++j) {
             const uint32_t ph = (uint32_t)j & 1u;
             const int s = j & 1;
@@ -390,8 +403,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
                     for (int c = 0; c < 32; c += 4) {
                         const float4 d = nd[8 * i + c / 4];
                         const int pa = 32 * i + c;
-                        float2 u = __fadd2_rn(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), make_float2(d.x, d.y));
-                        float2 v = __fadd2_rn(make_float2(__uint_as_float(dr[c + 2]), __uint_as_float(dr[c + 3])), make_float2(d.z, d.w));
+                        float2 u = less_delta(dr[c], dr[c + 1], make_float2(d.x, d.y));
+                        float2 v = less_delta(dr[c + 2], dr[c + 3], make_float2(d.z, d.w));
                         u = __fmul2_rn(u, make_float2(pr[pa], pr[pa + 1]));
                         v = __fmul2_rn(v, make_float2(pr[pa + 2], pr[pa + 3]));
                         if (edge) {  // (dP and delta of a row that is not there may be anything)
@@ -426,7 +439,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
         if (ok && !*abort_flag) {
             tc_fence_after();
             const uint32_t from = (half ? tDK : tDV) + lane_off;
-            const float by = half ? p.scale : 1.f;
+            const float by = half ? p.scale * pow2(-ds_exp) : pow2(-kP);
             uint16_t* to = (half ? dk : dv) + (long long)kr * p.Hk * p.D;
             float* acc = P.splits > 1 ? part(p, split, half ? 0 : 1, q.k0 + k0 + kr, h) : nullptr;
 #pragma unroll 1

@@ -3,7 +3,7 @@
 //
 // A tile of rows (prompt_tc.cuh) walks the key tiles that it sees, as in the forward, with P = 2^(s - lse) recomputed:
 //     S = Q K^T, dP = dO V^T             rows on the tensor-memory lanes
-//     dS = P (dP - delta)                as 16-bit pairs over dP
+//     dS = P (dP - delta)                as 16-bit pairs over dP (fp16: times a power of two, prompt_tc.cuh)
 //     dQ += dS K                         dS from tensor memory
 // lse and delta = dO . O (one pass of its own before: half a row a thread at the start of an item was 5 us of each) are one
 // number a thread, dQ stays in tensor memory, and is rounded once: no sum in memory, no order that varies.
@@ -358,7 +358,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
             const long long tok = it.q0 + it.tok[0] + tok_r, head = it.head[0] + head_r;
             const long long at = head * p.total_q + tok, row0 = (tok * p.Hq + head) * p.D;
             const int limit = it.tok[0] + tok_r + it.shift, first = it.tok[0] + it.shift;
-            const float nl = row ? -p.lse[at] * tc::kLog2e : 0.f, nd = row ? -p.delta[at] : 0.f;
+            const float nl = row ? -p.lse[at] * tc::kLog2e : 0.f;
+            float nd = row ? -p.delta[at] : 0.f, by = p.scale;
+            [[maybe_unused]] float ds = 1.f;
+            if constexpr (!BF16) {  // dS times a power of two (prompt_tc.cuh)
+                const float most = p.most[((long long)it.seq * p.Hk + it.h) * 3];
+                const int e = row ? half_exponent(fmaf(p.norm[at], most, fabsf(nd))) : 0;
+                ds = pow2(e);
+                nd *= ds;
+                by *= pow2(-e);
+            }
             for (int j = 0; j < n && ok; ++j, ++g) {
                 const uint32_t b = g & 1u;
                 const uint32_t sA = tmem + lane_off + 64u * half, dpA = tDP + lane_off + 128u * b + 64u * half;
@@ -398,7 +407,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                         tmem_ld_x32(dpA + 32 * i, dr);
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
-                            float2 x = __fadd2_rn(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), make_float2(nd, nd));
+                            float2 x = make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1]));
+                            x = BF16 ? __fadd2_rn(x, make_float2(nd, nd)) : __ffma2_rn(x, make_float2(ds, ds), make_float2(nd, nd));
                             x = __fmul2_rn(x, make_float2(pr[32 * i + c], pr[32 * i + c + 1]));
                             if (edge) {
                                 x.x = (see[i] >> c) & 1u ? x.x : 0.f;
@@ -441,7 +451,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                     uint32_t w[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        w[k] = n > 0 ? pack2<BF16>(__uint_as_float(o[e + 2 * k]) * p.scale, __uint_as_float(o[e + 2 * k + 1]) * p.scale) : 0u;
+                        w[k] = n > 0 ? pack2<BF16>(__uint_as_float(o[e + 2 * k]) * by, __uint_as_float(o[e + 2 * k + 1]) * by) : 0u;
                     if (row && c + e + 16 <= p.D) {
                         if (wide) {
                             store32(to + c + e, w);

@@ -7,6 +7,8 @@
 // tile of keys (dK, dV) and one for each tile of rows (dQ): both form P and dP, no sum is left to atomics, and the order of
 // every sum is fixed.
 
+#include <type_traits>
+
 #include "prompt.cuh"
 #include "tc_kernel.cuh"
 
@@ -352,24 +354,81 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_simt(const PromptParams p,
     }
 }
 
-// Sixteen lanes a row of (t, h).
+// Sixteen lanes a row of (t, h): delta, and in fp16 on tensor cores |dO|.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) prompt_delta_kernel(const PromptParams p) {
     constexpr int kV = Vec<T>::n;
     const long long r = ((long long)blockIdx.x * kThreads + threadIdx.x) / 16;
     const int lane = threadIdx.x % 16;
     const bool in = r < (long long)p.total_q * p.Hq;
-    float sum = 0.f;
+    float sum = 0.f, square = 0.f;
     for (int d = lane * kV; in && d < p.D; d += 16 * kV) {
         float a[kV], b[kV];
         Vec<T>::load(static_cast<const T*>(p.out) + r * p.D + d, a);
         Vec<T>::load(static_cast<const T*>(p.d_out) + r * p.D + d, b);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) sum = fmaf(a[i], b[i], sum);
+        for (int i = 0; i < kV; ++i) {
+            sum = fmaf(a[i], b[i], sum);
+            if constexpr (std::is_same<T, __half>::value) square = fmaf(b[i], b[i], square);
+        }
+    }
+    float* to = p.delta;
+    if constexpr (std::is_same<T, __half>::value) {  // (even lanes go on with the sum, odd ones with the square)
+        const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? sum : square, 1);
+        sum = (lane & 1 ? square : sum) + other;
+        if (lane & 1) to = p.norm;
+    } else {
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     }
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (in && lane == 0) p.delta[(r % p.Hq) * p.total_q + r / p.Hq] = sum;
+    for (int o = 2; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (in && lane < (std::is_same<T, __half>::value ? 2 : 1) && to) to[(r % p.Hq) * p.total_q + r / p.Hq] = lane ? sqrtf(sum) : sum;
+    if constexpr (std::is_same<T, __half>::value) {
+        if (!p.norm) return;
+        for (long long e = (long long)blockIdx.x * kThreads + threadIdx.x; e < (long long)p.num_seqs * p.Hk * 3; e += (long long)gridDim.x * kThreads)
+            p.most[e] = 0.f;  // (for prompt_most_kernel)
+    }
+}
+
+// p.most (zeroed before) of the block's (sequence, key head): the largest |V| of its keys (D <= 128), |dO| and |delta| of its
+// rows; blocks along y share them out.  An infinity or NaN does not count (what is multiplied with one is no number anyway).
+__global__ void __launch_bounds__(kThreads) prompt_most_kernel(const PromptParams p) {
+    const Seq q = load_seq(p, (int)(blockIdx.x / (unsigned)p.Hk), false);
+    const int h = (int)(blockIdx.x % (unsigned)p.Hk), lane = threadIdx.x % 16;
+    auto finite = [](float x) { return x <= 3.4e38f ? x : 0.f; };
+    float most[3] = {0.f, 0.f, 0.f};
+    constexpr int kAhead = 4, kPer = kThreads / 16 * kAhead;  // keys a thread has in flight, keys of a block at a time
+    for (int k0 = (int)blockIdx.y * kPer; k0 < q.lk; k0 += (int)gridDim.y * kPer) {
+        float square[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int k = k0 + j * (kThreads / 16) + threadIdx.x / 16;
+            float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (k < q.lk && lane * 8 < p.D) Vec<__half>::load(key_at<__half>(p, q, h, k, p.v, p.v_rs) + lane * 8, a);
+            square[j] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) square[j] = fmaf(a[i], a[i], square[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) square[j] += __shfl_xor_sync(0xffffffffu, square[j], o);
+            most[0] = fmaxf(most[0], finite(sqrtf(square[j])));
+        }
+    }
+    for (int g = 0; g < p.G; ++g) {
+        const long long row = (long long)(h * p.G + g) * p.total_q + q.q0;
+#pragma unroll 4
+        for (int t = (int)blockIdx.y * kThreads + threadIdx.x; t < q.lq; t += (int)gridDim.y * kThreads) {
+            most[1] = fmaxf(most[1], finite(p.norm[row + t]));
+            most[2] = fmaxf(most[2], finite(fabsf(p.delta[row + t])));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const unsigned m = __reduce_max_sync(0xffffffffu, __float_as_uint(most[i]));  // (not negative: ordered as its bits)
+        if (threadIdx.x % 32 == 0 && m) atomicMax(reinterpret_cast<unsigned*>(p.most) + blockIdx.x * 3 + i, m);
+    }
 }
 
 cudaError_t grid_of(const PromptParams& p, long long tiles, unsigned& grid) {
@@ -406,6 +465,12 @@ cudaError_t launch_delta(const PromptParams& p, cudaStream_t stream) {
     case TA_F16: prompt_delta_kernel<__half><<<(unsigned)n, kThreads, 0, stream>>>(p); break;
     default: prompt_delta_kernel<__nv_bfloat16><<<(unsigned)n, kThreads, 0, stream>>>(p); break;
     }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !p.norm) return e;
+    const long long pairs = (long long)p.num_seqs * p.Hk;
+    if (pairs > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const int longest = p.max_q > p.max_k ? p.max_q : p.max_k, shares = (longest + 63) / 64;
+    prompt_most_kernel<<<dim3((unsigned)pairs, (unsigned)(shares < 1 ? 1 : shares < 64 ? shares : 64)), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

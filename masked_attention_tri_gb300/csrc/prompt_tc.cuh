@@ -118,6 +118,17 @@ template <int N>
 struct Count {
     static constexpr int value = N;
 };
+// fp16 operands of the gradients are held times a power of two, which their products' fp32 sums are divided by exactly: the
+// least step of fp16 is 2^-24, and with thousands of keys and the dO of a mean loss (1e-4) dS = P (dP - delta) lies below it.
+// P, at most 1, is held times 2^14.  |dP - delta| <= |dO| |V| + |delta|: dS times 2^e is below 2^15 with e = 14 - floor(log2 of
+// that bound), for the row itself in dQ, for the largest of the sequence's rows of a key head in dK, whose sums run over rows.
+// bf16 has fp32's exponents and needs neither.
+constexpr int kHalfP = 14;
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }  // -126 to 127
+__device__ __forceinline__ int half_exponent(float bound) {
+    const int e = 14 + 127 - (int)(__float_as_uint(bound) >> 23 & 255u);
+    return min(max(e, -100), 100);
+}
 template <bool BF16>
 __device__ __forceinline__ uint32_t rest2(float2 x, uint32_t rounded) {
     const float2 y = unpack2<BF16>(rounded);
@@ -129,7 +140,7 @@ template <int PER>
 struct alignas(16) Item {
     int on;                    // 0: the end
     int q0, k0, lq, shift;     // the sequence: first packed rows, queries, and how many more keys than queries it has
-    int h;                     // key head
+    int seq, h;                // the sequence's number, key head
     int tok[PER], head[PER];     // of each tile: first token (of the sequence), first query head
     int keys[PER];             // keys that some row of the tile sees
     int rows[PER];             // rows that exist (0: no tile)
@@ -235,6 +246,7 @@ __device__ __forceinline__ bool order_item(const PromptParams& p, const Tiles& T
         auto get = [&](int x) { return __shfl_sync(0xffffffffu, x, l); };
         const int t0 = PER * get(first + place - (upto - c));
         it.on = 1;
+        it.seq = s0 + l;
         it.q0 = get(q.q0);
         it.k0 = get(q.k0);
         it.lq = get(q.lq);
