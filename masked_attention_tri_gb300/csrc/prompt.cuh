@@ -9,17 +9,12 @@
 #pragma once
 
 #include "internal.h"
+#include "prompt_order.h"
 #include "rotary.cuh"
 
 namespace triattn {
 namespace prompt {
 
-// What a sequence gives.
-struct Seq {
-    int q0, k0;                // first packed rows
-    int lq, lk;
-    int shift;                 // query j sees the keys up to j + shift
-};
 // A sequence that breaks the contract counts as holding nothing.
 __device__ __forceinline__ Seq load_seq(const PromptParams& p, int s, bool tell) {
     Seq q;

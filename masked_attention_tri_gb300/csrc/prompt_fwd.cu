@@ -586,7 +586,6 @@ Tiles make_tiles(const PromptParams& p) {
     t.tq = 128 / t.hp;
     t.ng = p.G / t.hp;
     t.fd_hp = make_fastdiv((uint32_t)t.hp);
-    t.fd_hk = make_fastdiv((uint32_t)p.Hk);
     return t;
 }
 

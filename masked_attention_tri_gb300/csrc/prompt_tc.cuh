@@ -15,7 +15,7 @@ using namespace tc;
 // Tiles of rows: tq tokens x hp heads of a group, ng tiles of the same tokens (G / hp).
 struct Tiles {
     int hp, tq, ng;
-    FastDiv fd_hp, fd_hk;
+    FastDiv fd_hp;
 };
 Tiles make_tiles(const PromptParams& p);
 
@@ -168,103 +168,68 @@ __device__ __forceinline__ int clc_answer(uint32_t at) {
     return x;
 }
 
-// The order of the items of PER tiles each (one warp): by the key tiles of their last tile, most first; of those with as many
-// by sequence, then place, then head.
-struct Order {
-    int level;                 // key tiles
-    long long base;            // items of the levels before
-    long long here;            // items of this level
-};
-// Items of a sequence that end within n key tiles.
-template <int PER>
-__device__ __forceinline__ int items_upto(const Tiles& T, const Seq& q, int n) {
-    const int tiles = (q.lq + T.tq - 1) / T.tq * T.ng;
-    if (n < 0) return 0;
-    if (q.lk <= 128LL * n) return (tiles + PER - 1) / PER;
-    const int x = 128 * n - q.shift;                   // tokens (of the sequence) whose last key lies there
-    return x <= 0 ? 0 : (int)((long long)(x / T.tq) * T.ng / PER);
-}
-template <int PER>
-__device__ __forceinline__ long long level_items(const PromptParams& p, const Tiles& T, int n) {
-    const int lane = threadIdx.x % 32;
-    long long sum = 0;
-    for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-        int c = 0;
-        if (s0 + lane < p.num_seqs) {
-            const Seq q = load_seq(p, s0 + lane, false);
-            c = items_upto<PER>(T, q, n) - items_upto<PER>(T, q, n - 1);
-        }
-        sum += __reduce_add_sync(0xffffffffu, c);
+// The sequences to a warp (prompt_order.h), a lane each.
+struct WarpSeqs {
+    const PromptParams& p;
+    __device__ __forceinline__ int n() const { return p.num_seqs; }
+    __device__ __forceinline__ Seq at(int s) const { return load_seq(p, s, false); }
+    template <typename F>
+    __device__ __forceinline__ int of_lane(int s0, F f, int none) const {
+        const int s = s0 + threadIdx.x % 32;
+        return s < p.num_seqs ? f(at(s)) : none;
     }
-    return sum * p.Hk;
-}
-template <int PER>
-__device__ __forceinline__ Order order_begin(const PromptParams& p, const Tiles& T) {
-    int most = 0;
-    for (int s = threadIdx.x % 32; s < p.num_seqs; s += 32) {
-        const Seq q = load_seq(p, s, blockIdx.x == 0);
-        if (q.lq > 0) most = max(most, (q.lk + 127) / 128);
+    template <typename F>
+    __device__ __forceinline__ int sum(int s0, F f) const {
+        return __reduce_add_sync(0xffffffffu, of_lane(s0, f, 0));
     }
-    Order o;
-    o.level = __reduce_max_sync(0xffffffffu, most);
-    o.base = 0;
-    o.here = level_items<PER>(p, T, o.level);
-    return o;
-}
-// Item `at` (never an earlier one than before): false past the last.
-template <int PER>
-__device__ __forceinline__ bool order_item(const PromptParams& p, const Tiles& T, Order& o, long long at, Item<PER>& it) {
-    while (at >= o.base + o.here) {
-        o.base += o.here;
-        if (--o.level < 0) return false;
-        o.here = level_items<PER>(p, T, o.level);
+    template <typename F>
+    __device__ __forceinline__ int most(int s0, F f) const {
+        return __reduce_max_sync(0xffffffffu, of_lane(s0, f, -1));
     }
-    const int lane = threadIdx.x % 32;
-    const int rank = (int)(at - o.base);
-    int place = (int)T.fd_hk.div((uint32_t)rank);
-    it.h = rank - place * p.Hk;
-    for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-        Seq q{};
-        int c = 0, first = 0;
-        if (s0 + lane < p.num_seqs) {
-            q = load_seq(p, s0 + lane, false);
-            first = items_upto<PER>(T, q, o.level - 1);
-            c = items_upto<PER>(T, q, o.level) - first;
-        }
+    template <typename F>
+    __device__ __forceinline__ bool find(int s0, F f, int& place, int& s) const {
+        const int c = of_lane(s0, f, 0);
         int upto = c;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += x;
+            if (threadIdx.x % 32 >= d) upto += x;
         }
         const uint32_t has = __ballot_sync(0xffffffffu, place < upto);
         if (!has) {
             place -= __shfl_sync(0xffffffffu, upto, 31);
-            continue;
+            return false;
         }
         const int l = __ffs((int)has) - 1;
-        auto get = [&](int x) { return __shfl_sync(0xffffffffu, x, l); };
-        const int t0 = PER * get(first + place - (upto - c));
-        it.on = 1;
-        it.seq = s0 + l;
-        it.q0 = get(q.q0);
-        it.k0 = get(q.k0);
-        it.lq = get(q.lq);
-        it.shift = get(q.shift);
-        const int blocks = (it.lq + T.tq - 1) / T.tq;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int t = t0 + i, b = t / T.ng;
-            const bool there = b < blocks;
-            it.tok[i] = b * T.tq;
-            it.head[i] = it.h * p.G + (t - b * T.ng) * T.hp;
-            const int tokens = there ? min(T.tq, it.lq - it.tok[i]) : 0;
-            it.rows[i] = tokens * T.hp;
-            it.keys[i] = there ? max(0, it.tok[i] + tokens + it.shift) : 0;
-        }
+        place -= __shfl_sync(0xffffffffu, upto - c, l);
+        s = s0 + l;
         return true;
     }
-    return false;
+};
+// Item `at` of the order: false past the last.
+template <int PER>
+__device__ __forceinline__ bool order_item(const PromptParams& p, const Tiles& T, Order<PER>& o, long long at, Item<PER>& it) {
+    const WarpSeqs seqs{p};
+    int n = 0;
+    if (!o.locate(seqs, at, it.seq, n, it.h)) return false;
+    const Seq q = seqs.at(it.seq);
+    it.on = 1;
+    it.q0 = q.q0;
+    it.k0 = q.k0;
+    it.lq = q.lq;
+    it.shift = q.shift;
+    const int blocks = (it.lq + T.tq - 1) / T.tq;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int t = PER * n + i, b = t / T.ng;
+        const bool there = b < blocks;
+        it.tok[i] = b * T.tq;
+        it.head[i] = it.h * p.G + (t - b * T.ng) * T.hp;
+        const int tokens = there ? min(T.tq, it.lq - it.tok[i]) : 0;
+        it.rows[i] = tokens * T.hp;
+        it.keys[i] = there ? max(0, it.tok[i] + tokens + it.shift) : 0;
+    }
+    return true;
 }
 // The warp that hands the items to `consumers` warps through a ring of R: items in shared memory, barriers full(r) (1) and
 // empty(r) (consumers), the answer's place and barrier.  False after a wait that ran out.
@@ -272,7 +237,10 @@ template <int PER, int R, typename Full, typename Empty>
 __device__ __forceinline__ bool hand_out(const PromptParams& p, const Tiles& T, Item<PER>* items, Full full, Empty empty,
                                          uint32_t clc_at, uint32_t clc_bar, volatile int* abort_flag) {
     const int lane = threadIdx.x % 32;
-    Order o = order_begin<PER>(p, T);
+    if (blockIdx.x == 0)
+        for (int s = lane; s < p.num_seqs; s += 32) load_seq(p, s, true);  // (records a broken sequence)
+    Order<PER> o;
+    o.begin(WarpSeqs{p}, __ffs(T.tq) - 1, T.ng, p.Hk);
     int at = (int)blockIdx.x;
     for (int n = 0;; ++n) {
         Item<PER> it{};

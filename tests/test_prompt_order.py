@@ -1,0 +1,135 @@
+"""The order of prompt attention's work items: every item once, by falling cost, whatever the order in which indexes are asked for.
+
+The host program below runs the kernels' own arithmetic (csrc/prompt_order.h) with 32 lanes as a loop; the reference counts
+the items of a problem one by one.
+"""
+import os
+import random
+import shutil
+import subprocess
+
+import pytest
+
+from masked_attention_tri_gb300 import build
+
+PROGRAM = r"""
+#include <cstdio>
+#include <vector>
+#include "prompt_order.h"
+using namespace triattn::prompt;
+struct HostSeqs {
+    std::vector<Seq> v;
+    mutable long long passes = 0;
+    int n() const { return (int)v.size(); }
+    Seq at(int s) const { return v[s]; }
+    int end(int s0) const { return s0 + 32 < n() ? s0 + 32 : n(); }
+    template <typename F> int sum(int s0, F f) const {
+        ++passes;
+        int x = 0;
+        for (int s = s0; s < end(s0); ++s) x += f(v[s]);
+        return x;
+    }
+    template <typename F> int most(int s0, F f) const {
+        ++passes;
+        int x = -1;
+        for (int s = s0; s < end(s0); ++s) x = f(v[s]) > x ? f(v[s]) : x;
+        return x;
+    }
+    template <typename F> bool find(int s0, F f, int& place, int& s) const {
+        ++passes;
+        for (s = s0; s < end(s0); ++s) {
+            const int c = f(v[s]);
+            if (place < c) return true;
+            place -= c;
+        }
+        return false;
+    }
+};
+template <int PER> void run(const HostSeqs& seqs, int tq, int ng, int heads, int asks) {
+    Order<PER> o;
+    int bits = 0;
+    while (1 << bits < tq) ++bits;
+    o.begin(seqs, bits, ng, heads);
+    for (int i = 0; i < asks; ++i) {
+        long long at;
+        if (std::scanf("%lld", &at) != 1) return;
+        int s = -1, item = -1, h = -1;
+        if (!o.locate(seqs, at, s, item, h)) s = item = h = -1;
+        std::printf("%d %d %d %lld\n", s, item, h, seqs.passes);
+    }
+}
+int main() {
+    int per, tq, ng, heads, n, asks;
+    while (std::scanf("%d %d %d %d %d %d", &per, &tq, &ng, &heads, &n, &asks) == 6) {
+        HostSeqs seqs;
+        for (int i = 0; i < n; ++i) {
+            Seq q{};
+            if (std::scanf("%d %d", &q.lq, &q.lk) != 2) return 1;
+            q.shift = q.lk - q.lq;
+            seqs.v.push_back(q);
+        }
+        if (per == 1) run<1>(seqs, tq, ng, heads, asks);
+        else run<2>(seqs, tq, ng, heads, asks);
+    }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def locate(tmp_path_factory):
+    d = tmp_path_factory.mktemp("order")
+    src, exe = d / "order.cpp", d / "order"
+    src.write_text(PROGRAM)
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    subprocess.run([cxx, "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover", "-I", build.CSRC, str(src), "-o",
+                    str(exe)], check=True)
+
+    def run(per, tq, ng, heads, seqs, asks):
+        text = " ".join(str(x) for x in [per, tq, ng, heads, len(seqs), len(asks)] + [y for s in seqs for y in s] + list(asks))
+        out = subprocess.run([str(exe)], input=text, capture_output=True, text=True, check=True).stdout.split("\n")
+        return [tuple(int(x) for x in line.split()) for line in out if line]
+    return run
+
+
+def _items(per, tq, ng, heads, seqs):
+    """{(sequence, item, head): key tiles that the item's last tile sees}."""
+    all_items = {}
+    for s, (lq, lk) in enumerate(seqs):
+        tiles = [(b, g) for b in range(-(-lq // tq)) for g in range(ng)]
+        for i in range(-(-len(tiles) // per)):
+            b = tiles[i * per:(i + 1) * per][-1][0]
+            keys = max(0, min((b + 1) * tq, lq) + lk - lq)
+            for h in range(heads):
+                all_items[s, i, h] = -(-keys // 128)
+    return all_items
+
+
+def _problem(r):
+    tq = r.choice([1, 2, 8, 32, 64, 128])
+    n = r.choice([1, 2, 5, 31, 32, 33, 70])
+    lens = [r.choice([0, 1, r.randint(0, 40), r.randint(0, 600)]) * (4 if tq >= 32 else 1) for _ in range(n)]
+    seqs = [(lq, r.choice([lq, lq, 0, r.randint(0, 3000), lq + r.randint(0, 20000)])) for lq in lens]
+    return r.choice([1, 2]), tq, r.choice([1, 1, 2, 3, 5]), r.choice([1, 2, 3, 8]), seqs
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_every_item_once_by_falling_cost(locate, seed):
+    r = random.Random(seed)
+    for _ in range(4):
+        per, tq, ng, heads, seqs = _problem(r)
+        want = _items(per, tq, ng, heads, seqs)
+        got = [x[:3] for x in locate(per, tq, ng, heads, seqs, range(len(want) + 5))]
+        assert got[len(want):] == [(-1, -1, -1)] * 5
+        assert len(set(got[:len(want)])) == len(want) and set(got[:len(want)]) == set(want)
+        cost = [want[x] for x in got[:len(want)]]
+        assert cost == sorted(cost, reverse=True)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_any_order_of_asking(locate, seed):
+    r = random.Random(100 + seed)
+    per, tq, ng, heads, seqs = _problem(r)
+    n = len(_items(per, tq, ng, heads, seqs))
+    got = [x[:3] for x in locate(per, tq, ng, heads, seqs, range(n + 3))]
+    asks = [r.randrange(n + 3) for _ in range(200)] + [n + 2, 0, n, max(0, n - 1), 0]
+    assert [x[:3] for x in locate(per, tq, ng, heads, seqs, asks)] == [got[a] for a in asks]
