@@ -237,8 +237,6 @@ template <int PER, int R, typename Full, typename Empty>
 __device__ __forceinline__ bool hand_out(const PromptParams& p, const Tiles& T, Item<PER>* items, Full full, Empty empty,
                                          uint32_t clc_at, uint32_t clc_bar, volatile int* abort_flag) {
     const int lane = threadIdx.x % 32;
-    if (blockIdx.x == 0)
-        for (int s = lane; s < p.num_seqs; s += 32) load_seq(p, s, true);  // (records a broken sequence)
     Order<PER> o;
     o.begin(WarpSeqs{p}, __ffs(T.tq) - 1, T.ng, p.Hk);
     int at = (int)blockIdx.x;
@@ -251,13 +249,16 @@ __device__ __forceinline__ bool hand_out(const PromptParams& p, const Tiles& T, 
             items[r] = it;
             mbar_arrive(full(r));
         }
-        if (!it.on) return true;
+        if (!it.on) break;
         if (lane == 0) clc_ask(clc_at, clc_bar);
         // (awaited whatever happens: the answer is written into this block's memory)
         if (!__all_sync(0xffffffffu, wait_bar_drain(clc_bar, (uint32_t)n & 1u))) return false;
         at = clc_answer(clc_at);
         __syncwarp();
     }
+    if (blockIdx.x == 0)
+        for (int s = lane; s < p.num_seqs; s += 32) load_seq(p, s, true);  // (records a broken sequence)
+    return true;
 }
 // Blocks of the grid: one for each item that there can be.  A sequence has ceil(ceil(lq / tq) ng / PER) items, at most
 // lq ng / (PER tq) + (ng + PER - 1) / PER, and no more than the longest has.

@@ -133,3 +133,80 @@ def test_any_order_of_asking(locate, seed):
     got = [x[:3] for x in locate(per, tq, ng, heads, seqs, range(n + 3))]
     asks = [r.randrange(n + 3) for _ in range(200)] + [n + 2, 0, n, max(0, n - 1), 0]
     assert [x[:3] for x in locate(per, tq, ng, heads, seqs, asks)] == [got[a] for a in asks]
+
+
+def _chunks(seqs):
+    return -(-len(seqs) // 32)
+
+
+def test_a_long_prefix_beside_many_short_prompts(locate):
+    """Levels without items cost nothing, and the items of a level one pass: 128k keys and 2000 prompts."""
+    r = random.Random(7)
+    seqs = [(r.randint(1, 64), 0) for _ in range(2000)]
+    seqs = [(a, a) for a, _ in seqs]
+    seqs.insert(900, (64, 131072))
+    per, tq, ng, heads = 2, 32, 1, 8
+    want = _items(per, tq, ng, heads, seqs)
+    got = locate(per, tq, ng, heads, seqs, range(len(want)))
+    assert set(x[:3] for x in got) == set(want) and got[0][0] == 900
+    # begin (two passes), two levels with items, one between them; then one look an item
+    assert got[-1][3] <= 8 * _chunks(seqs) + len(want)
+    # a block that takes a short one alone
+    one = locate(per, tq, ng, heads, seqs, [len(want) - 1])
+    assert one[0][:3] == got[-1][:3] and one[0][3] <= 8 * _chunks(seqs)
+
+
+def test_past_the_last_item(locate):
+    seqs = [(64 * i, 64 * i) for i in range(1, 129)] * 2
+    n = len(_items(2, 32, 1, 8, seqs))
+    for x in locate(2, 32, 1, 8, seqs, [n, n + 1, n + 1000]):
+        assert x[:3] == (-1, -1, -1) and x[3] == 2 * _chunks(seqs)
+
+
+def test_many_sequences_and_levels(locate):
+    """The most sequences that a call may have, and keys up to 2^30: as many passes as 256 levels take."""
+    r = random.Random(9)
+    seqs = [(r.choice([0, 1, 1, 2]), r.choice([1, 5, r.randint(1, 1 << 20)])) for _ in range(65535)]
+    seqs[30000] = (3, (1 << 30) - 1)
+    items = sum(a > 0 for a, _ in seqs)
+    asks = [0, 1, 2, items // 2, items - 1, items, 5]
+    got = locate(2, 128, 1, 1, seqs, asks)
+    assert got[0][:2] == (30000, 0) and got[5][0] == -1
+    assert got[-1][3] <= 2 * (3 * 256 + 8) * _chunks(seqs)
+    seqs = [(1 << 15, 1 << 15)] + [(1, r.randint(1, 1 << 15)) for _ in range(5000)]  # items at every level
+    want = _items(1, 128, 1, 1, seqs)
+    got = locate(1, 128, 1, 1, seqs, range(len(want)))
+    assert set(x[:3] for x in got) == set(want)
+    cost = [want[x[:3]] for x in got]
+    assert cost == sorted(cost, reverse=True) and got[-1][3] <= (3 * 257 + 4) * _chunks(seqs) + len(want)
+
+
+@pytest.mark.parametrize("per,tq,ng", [(2, 32, 1), (1, 128, 3), (2, 1, 2)])
+def test_levels_of_several_key_tiles(locate, per, tq, ng):
+    """Past 32768 keys a level is several key tiles: every item once, and no item more than a level's key tiles after a cheaper one."""
+    seqs = [(300, 100000), (70, 70), (129, 33000), (5, 2), (64, 99000), (1, 0)]
+    want = _items(per, tq, ng, 2, seqs)
+    got = [x[:3] for x in locate(per, tq, ng, 2, seqs, range(len(want)))]
+    assert len(set(got)) == len(want) and set(got) == set(want)
+    least, step = None, -(-(-(-100000 // 128)) // 256)
+    for x in got:
+        least = want[x] if least is None else min(least, want[x])
+        assert want[x] < least + step
+
+
+@pytest.mark.gpu
+def test_values_of_a_long_prefix_beside_many_short_prompts():
+    from test_prompt_attention import BF, _run
+    r = random.Random(11)
+    lq = [r.randint(0, 40) for _ in range(500)]
+    lk = [n + r.choice([0, 0, 0, r.randint(0, 200)]) for n in lq]
+    lq[123], lk[123] = 64, 40000
+    _run(lq, lk, 8, 2, 64, BF)
+
+
+@pytest.mark.gpu
+def test_values_of_prompts_of_many_lengths():
+    from test_prompt_attention import F16, _run
+    r = random.Random(12)
+    lq = [r.randint(1, 700) for _ in range(100)]
+    _run(lq, lq, 4, 2, 128, F16)
