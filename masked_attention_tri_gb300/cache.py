@@ -67,7 +67,40 @@ class PagedKVCache:
         return cls(k, v, ks, vs)
 
 
-class PagedKVCache4:
+class _Parts:
+    """The tensors of a cache as public attributes, and what the calls read of them (`_describe`), made again where another tensor,
+    or other memory of one, stands there: a call must not use memory that the cache no longer holds."""
+
+    _PARTS = ("k", "v", "k_scale", "v_scale", "k_factor", "v_factor")
+    _OWN = ("_c", "_at")  # addresses: not for a copy
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name in self._PARTS:
+            object.__setattr__(self, "_at", None)
+
+    def _addresses(self):
+        return (self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(), _ptr(self.k_factor),
+                _ptr(self.v_factor))
+
+    def _now(self):
+        """Describes the tensors as they are now."""
+        if self._at is None or self._at != self._addresses():
+            self._describe()
+            self._at = self._addresses()
+
+    # (8-bit floating point as bytes: plain pickle cannot read such tensors back)
+    def __getstate__(self):
+        state = {n: x for n, x in self.__dict__.items() if n not in self._OWN}
+        eight = [n for n in self._PARTS if isinstance(state.get(n), torch.Tensor) and state[n].dtype == torch.float8_e4m3fn]
+        return {**state, **{n: state[n].view(torch.uint8) for n in eight}}, eight
+
+    def __setstate__(self, state):
+        state, eight = state
+        self.__dict__.update({**state, **{n: state[n].view(torch.float8_e4m3fn) for n in eight}, "_at": None})
+
+
+class PagedKVCache4(_Parts):
     """The pages of a 4-bit cache: an element of head h stands for n * scale * factor[h], n a whole number from -7 to 7.
 
     k, v: uint8 (num_pages, Hk, page_size, D / 2), two codes n + 8 a byte (the even element in the low half);
@@ -75,12 +108,18 @@ class PagedKVCache4:
     k_factor, v_factor: float32 (Hk,) or None (1), positive, fixed for the cache's life (powers of two cost no
     precision; a factor around the 100th part of a head's usual magnitudes keeps its scales in e4m3's middle).
 
-    The tensors are used in place.  Pages and heads may be strided (a head's page is contiguous), such as the halves
-    of one (num_pages, 2, Hk, page_size, D / 2) buffer.  page_size is a power of two from 16 to 1024, D a multiple
-    of 32.
+    The tensors are used in place, as they are at each call (another may be put in one's place).  Pages and heads may be
+    strided (a head's page is contiguous), such as the halves of one (num_pages, 2, Hk, page_size, D / 2) buffer.  page_size is
+    a power of two from 16 to 1024, D a multiple of 32.
     """
 
     def __init__(self, k, v, k_scale, v_scale, k_factor=None, v_factor=None):
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.k_factor, self.v_factor = k_factor, v_factor
+        self._now()
+
+    def _describe(self):
+        k, v, k_scale, v_scale, k_factor, v_factor = (getattr(self, n) for n in self._PARTS)
         for t, nm in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{nm} must be a torch.Tensor")
@@ -108,8 +147,6 @@ class PagedKVCache4:
             _need(t, nm, k.device)
             if t.dtype != torch.float32 or tuple(t.shape) != (self.heads,):
                 raise ValueError(f"{nm} must be float32 {(self.heads,)}")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.k_factor, self.v_factor = k_factor, v_factor
         strides = (ctypes.c_longlong * 8)()
         parts = (k, v, k_scale, v_scale)
         if not all(t.is_contiguous() for t in parts):
@@ -181,6 +218,8 @@ def kv_cache_append(cache: Union[PagedKVCache, PagedKVCache4], k, v, page_table,
     """
     if not isinstance(cache, _CACHES):
         raise TypeError("cache must be a PagedKVCache or a PagedKVCache4")
+    if isinstance(cache, PagedKVCache4):
+        cache._now()
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("expected k (total, Hk, D)")
     dev = k.device
@@ -254,6 +293,8 @@ def kv_cache_read(cache: Union[PagedKVCache, PagedKVCache4], page_table, kv_leng
     """
     if not isinstance(cache, _CACHES):
         raise TypeError("cache must be a PagedKVCache or a PagedKVCache4")
+    if isinstance(cache, PagedKVCache4):
+        cache._now()
     dev, Hk, D = cache.device, cache.heads, cache.head_dim
     if not cache.k.is_cuda:
         raise ValueError("kv_cache_read runs on CUDA tensors only")
@@ -318,6 +359,8 @@ def paged_attention(q, cache: Union[PagedKVCache, PagedKVCache4], page_table, kv
     """
     if not isinstance(cache, _CACHES):
         raise TypeError("cache must be a PagedKVCache or a PagedKVCache4")
+    if isinstance(cache, PagedKVCache4):
+        cache._now()
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     if q.dim() != 3:
