@@ -151,8 +151,11 @@ class PagedKVCache4(_Parts):
         parts = (k, v, k_scale, v_scale)
         if not all(t.is_contiguous() for t in parts):
             for i, t in enumerate(parts):
-                head = t.stride(1) if t.shape[1] > 1 else t.shape[2] * t.shape[3]
-                strides[2 * i] = t.stride(0) if t.shape[0] > 1 else max(head * t.shape[1], t.shape[2] * t.shape[3])
+                least = t.shape[2] * t.shape[3]
+                head = t.stride(1) if t.shape[1] > 1 else least
+                strides[2 * i] = t.stride(0) if t.shape[0] > 1 else max(head * t.shape[1], least)
+                if head < least or strides[2 * i] < least:  # (an expanded tensor; strides that are all 0 mean a contiguous one)
+                    raise ValueError("pages or heads of the cache's tensors overlap")
                 strides[2 * i + 1] = head
         self._c = abi.Cache4(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(k_factor) or None,
                              _ptr(v_factor) or None, self.num_pages, self.page_size, strides)

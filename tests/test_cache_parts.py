@@ -67,6 +67,23 @@ def test_another_tensor_that_does_not_fit(name, other, exc):
             c._now()
 
 
+def test_expanded_tensors_are_refused():
+    """One page that stands for all of them: its strides of 0 must not be taken for those of a contiguous cache."""
+    one = _parts4(pages=1, heads=1)
+    whole = {n: t.expand(3, 2, *t.shape[2:]) if t.dim() == 4 else None for n, t in one.items()}
+    with pytest.raises(ValueError):
+        PagedKVCache4(**whole)
+    for n in ("k", "v", "k_scale", "v_scale"):
+        for shape in ((3, 1), (1, 2)):  # pages, then heads
+            parts = _parts4(pages=shape[0], heads=shape[1])
+            t = parts[n][:1, :1].expand(*shape, *parts[n].shape[2:])
+            with pytest.raises(ValueError):
+                PagedKVCache4(**{**parts, "k_factor": None, "v_factor": None, n: t})
+    whole = _parts4(pages=6)
+    every_second = {n: t[::2] if t.dim() == 4 else t for n, t in whole.items()}
+    assert list(PagedKVCache4(**every_second)._c.strides)[:2] == [2 * 2 * 16 * 16, 16 * 16]
+
+
 def _pickled(c):
     f = io.BytesIO()
     pickle.dump(c, f)
