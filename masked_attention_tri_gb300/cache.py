@@ -19,18 +19,54 @@ from .positions import Rotary, _check_positions, _check_rotary
 _CACHE_DT = {**_DT, torch.float8_e4m3fn: abi.TA_E4M3}
 
 
-class PagedKVCache:
+class _Parts:
+    """The tensors of a cache as public attributes, and what the calls read of them (`_describe`), made again by `_now` where another
+    tensor, or other memory of one, stands there: a call must not use memory that the cache no longer holds."""
+
+    _PARTS = ("k", "v", "k_scale", "v_scale")
+    _OWN = ("_c", "_strides", "_at")  # what a copy describes anew
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name in self._PARTS:
+            object.__setattr__(self, "_at", None)
+
+    def _renew(self):
+        self._describe()
+        self._at = tuple([_ptr(getattr(self, n)) for n in self._PARTS])
+
+    # (8-bit floating point as bytes: plain pickle cannot read such tensors back)
+    def __getstate__(self):
+        state = {n: x for n, x in self.__dict__.items() if n not in self._OWN}
+        eight = [n for n in self._PARTS if isinstance(state.get(n), torch.Tensor) and state[n].dtype == torch.float8_e4m3fn]
+        return {**state, **{n: state[n].view(torch.uint8) for n in eight}}, eight
+
+    def __setstate__(self, state):
+        state, eight = state
+        self.__dict__.update({**state, **{n: state[n].view(torch.float8_e4m3fn) for n in eight}, "_at": None})
+
+
+class PagedKVCache(_Parts):
     """The pages of a cache: k and v (num_pages, Hk, page_size, D), with k_scale and v_scale
     (num_pages, Hk) float32 where they hold float8_e4m3fn codes (an element stands for code * scale;
     v_scale from 2^-56 to 2^56).
 
-    The tensors are used in place.  k and v may be strided views whose last
-    dimension is contiguous, such as the halves of one (num_pages, 2, Hk,
-    page_size, D) buffer or a (num_pages, page_size, Hk, D) buffer with its middle
-    dimensions exchanged.  page_size is a power of two from 16 to 1024.
+    The tensors are used in place, as they are at each call (another may be put in
+    one's place).  k and v may be strided views whose last dimension is contiguous,
+    such as the halves of one (num_pages, 2, Hk, page_size, D) buffer or a (num_pages,
+    page_size, Hk, D) buffer with its middle dimensions exchanged.  page_size is a power of two from 16 to 1024.
     """
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._now()
+
+    def _now(self):
+        if self._at is None or self._at != (self.k.data_ptr(), self.v.data_ptr(), _ptr(self.k_scale), _ptr(self.v_scale)):
+            self._renew()
+
+    def _describe(self):
+        k, v, k_scale, v_scale = self.k, self.v, self.k_scale, self.v_scale
         for t, nm in ((k, "k"), (v, "v")):
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{nm} must be a torch.Tensor")
@@ -51,7 +87,6 @@ class PagedKVCache:
                     raise ValueError(f"{nm} must be float32 {(self.num_pages, self.heads)}")
         elif k_scale is not None or v_scale is not None:
             raise ValueError("scales belong to a float8_e4m3fn cache")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self._code = _CACHE_DT[k.dtype]
         self._strides = tuple(None if t.is_contiguous() else
                               abi.strides3([t.stride(i) if t.shape[i] > 1 else t.shape[2] * t.shape[3] * t.shape[1]
@@ -67,39 +102,6 @@ class PagedKVCache:
         return cls(k, v, ks, vs)
 
 
-class _Parts:
-    """The tensors of a cache as public attributes, and what the calls read of them (`_describe`), made again where another tensor,
-    or other memory of one, stands there: a call must not use memory that the cache no longer holds."""
-
-    _PARTS = ("k", "v", "k_scale", "v_scale", "k_factor", "v_factor")
-    _OWN = ("_c", "_at")  # addresses: not for a copy
-
-    def __setattr__(self, name, value):
-        object.__setattr__(self, name, value)
-        if name in self._PARTS:
-            object.__setattr__(self, "_at", None)
-
-    def _addresses(self):
-        return (self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(), _ptr(self.k_factor),
-                _ptr(self.v_factor))
-
-    def _now(self):
-        """Describes the tensors as they are now."""
-        if self._at is None or self._at != self._addresses():
-            self._describe()
-            self._at = self._addresses()
-
-    # (8-bit floating point as bytes: plain pickle cannot read such tensors back)
-    def __getstate__(self):
-        state = {n: x for n, x in self.__dict__.items() if n not in self._OWN}
-        eight = [n for n in self._PARTS if isinstance(state.get(n), torch.Tensor) and state[n].dtype == torch.float8_e4m3fn]
-        return {**state, **{n: state[n].view(torch.uint8) for n in eight}}, eight
-
-    def __setstate__(self, state):
-        state, eight = state
-        self.__dict__.update({**state, **{n: state[n].view(torch.float8_e4m3fn) for n in eight}, "_at": None})
-
-
 class PagedKVCache4(_Parts):
     """The pages of a 4-bit cache: an element of head h stands for n * scale * factor[h], n a whole number from -7 to 7.
 
@@ -113,10 +115,17 @@ class PagedKVCache4(_Parts):
     a power of two from 16 to 1024, D a multiple of 32.
     """
 
+    _PARTS = _Parts._PARTS + ("k_factor", "v_factor")
+
     def __init__(self, k, v, k_scale, v_scale, k_factor=None, v_factor=None):
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.k_factor, self.v_factor = k_factor, v_factor
         self._now()
+
+    def _now(self):
+        if self._at is None or self._at != (self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                                            _ptr(self.k_factor), _ptr(self.v_factor)):
+            self._renew()
 
     def _describe(self):
         k, v, k_scale, v_scale, k_factor, v_factor = (getattr(self, n) for n in self._PARTS)
@@ -221,8 +230,7 @@ def kv_cache_append(cache: Union[PagedKVCache, PagedKVCache4], k, v, page_table,
     """
     if not isinstance(cache, _CACHES):
         raise TypeError("cache must be a PagedKVCache or a PagedKVCache4")
-    if isinstance(cache, PagedKVCache4):
-        cache._now()
+    cache._now()
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("expected k (total, Hk, D)")
     dev = k.device
@@ -296,8 +304,7 @@ def kv_cache_read(cache: Union[PagedKVCache, PagedKVCache4], page_table, kv_leng
     """
     if not isinstance(cache, _CACHES):
         raise TypeError("cache must be a PagedKVCache or a PagedKVCache4")
-    if isinstance(cache, PagedKVCache4):
-        cache._now()
+    cache._now()
     dev, Hk, D = cache.device, cache.heads, cache.head_dim
     if not cache.k.is_cuda:
         raise ValueError("kv_cache_read runs on CUDA tensors only")
@@ -362,8 +369,7 @@ def paged_attention(q, cache: Union[PagedKVCache, PagedKVCache4], page_table, kv
     """
     if not isinstance(cache, _CACHES):
         raise TypeError("cache must be a PagedKVCache or a PagedKVCache4")
-    if isinstance(cache, PagedKVCache4):
-        cache._now()
+    cache._now()
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     if q.dim() != 3:

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from masked_attention_tri_gb300 import build
-from masked_attention_tri_gb300.cache import PagedKVCache4
+from masked_attention_tri_gb300.cache import PagedKVCache, PagedKVCache4
 
 U8, F8 = torch.uint8, torch.float8_e4m3fn
 
@@ -101,6 +101,45 @@ def test_copies(how):
         x = getattr(d, n)
         assert torch.equal(x.view(U8) if t.dtype == F8 else x, t.view(U8) if t.dtype == F8 else t)
         assert (x.data_ptr() == t.data_ptr()) == (how is copy.copy)
+
+
+def _parts(dtype, pages=3, heads=2, page=16, D=32, device="cpu"):
+    if dtype == F8:
+        k, v = (torch.randn(pages, heads, page, D, device=device).to(F8) for _ in range(2))
+        return dict(k=k, v=v, k_scale=torch.ones(pages, heads, device=device), v_scale=torch.ones(pages, heads, device=device))
+    return dict(zip("kv", (torch.randn(pages, heads, page, D, device=device).to(dtype) for _ in range(2))))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F8, torch.float32])
+def test_a_wider_cache_of_other_sizes(dtype):
+    """Fewer pages, another page size, strided pages and another type: the next call counts them anew."""
+    c = PagedKVCache(**_parts(F8))
+    for n in ("k", "v", "k_scale", "v_scale"):
+        setattr(c, n, _parts(dtype, 2, 4, 32, 64).get(n))
+    c._now()
+    assert (c.num_pages, c.heads, c.page_size, c.head_dim, c.dtype) == (2, 4, 32, 64, dtype) and c._strides == (None, None)
+    both = torch.stack([_parts(dtype, 5, 4, 32, 64)["k"] for _ in range(2)], 1)  # the halves of one buffer
+    c.k, c.v = both[:, 0], both[:, 1]
+    if dtype == F8:
+        c.k_scale, c.v_scale = torch.ones(5, 4), torch.ones(5, 4)
+    c._now()
+    assert c.num_pages == 5 and list(c._strides[0]) == [2 * 4 * 32 * 64, 32 * 64, 64]
+    c.k = c.k[:4]
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            c._now()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F8, torch.float32])
+@pytest.mark.parametrize("how", [copy.deepcopy, copy.copy, _pickled])
+def test_copies_of_a_wider_cache(dtype, how):
+    both = torch.stack([_parts(dtype)["k"] for _ in range(2)], 1)
+    c = PagedKVCache(**{**_parts(dtype), "k": both[:, 0], "v": both[:, 1]})
+    d = how(c)
+    d._now()
+    assert torch.equal(d.k.float(), c.k.float()) and torch.equal(d.v.float(), c.v.float()) and d.num_pages == c.num_pages
+    assert (d.k.data_ptr() == c.k.data_ptr()) == (how is copy.copy)
+    assert all(tuple(a) == tuple(b) for a, b in zip(c._strides, d._strides))
 
 
 @pytest.mark.gpu
