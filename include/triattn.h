@@ -83,7 +83,7 @@ typedef enum {
  * neighbouring elements of a row to an e4m3 scale.  An element of head h stands for n * scale * factor[h].
  *   k, v              (num_pages, Hk, page_size, D / 2) bytes
  *   k_scale, v_scale  (num_pages, Hk, page_size, D / 16) e4m3 numbers
- *   k_factor, v_factor  (Hk) fp32, positive and finite, fixed for the cache's life; powers of two cost no precision.
+ *   k_factor, v_factor  (Hk) fp32, from 2^-100 to 2^100, fixed for the cache's life; powers of two cost no precision.
  *                     NULL: 1.  The scale covers magnitudes up to 3136 factors, and 7 * 2^-9 factors is the least
  *                     largest magnitude of 16 elements that uses all of the codes.
  *   strides           bytes between pages and between heads: {k, v, k_scale, v_scale} x {page, head}; a head's slots

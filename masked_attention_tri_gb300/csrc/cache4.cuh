@@ -18,6 +18,9 @@
 namespace triattn {
 namespace cache4 {
 
+// Factors: within these 1 / f, and times 1 / s, are fp32 numbers of full precision.
+constexpr float kLeastFactor = 0x1p-100f, kMostFactor = 0x1p100f;
+
 // Tag of a 4-bit cache's elements.
 struct Code {
     uint8_t two;

@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(THREADS) kv_append4_kernel(const Append4Args a
     const int nh = a.heads[kind], h0 = job * nh;
     uint8_t *codes0 = nullptr, *scale0 = nullptr;              // of the page's first head of the job
     long long codes_h = 0, scale_h = 0;
+    bool bad = false;
     if (kind != 2) {
         const long long page = p.table[(long long)seq * p.max_pages + lp];
         if (page < 0 || page >= p.num_pages) {
@@ -126,7 +127,11 @@ __global__ void __launch_bounds__(THREADS) kv_append4_kernel(const Append4Args a
         scale_h = p.c4.ss[kind][1];
         codes0 = p.c4.codes[kind] + page * p.c4.cs[kind][0] + h0 * codes_h;
         scale0 = p.c4.scale[kind] + page * p.c4.ss[kind][0] + h0 * scale_h;
-        if (threadIdx.x < nh) inv_s[threadIdx.x] = p.c4.factor[kind] ? 1.f / p.c4.factor[kind][h0 + threadIdx.x] : 1.f;
+        if (threadIdx.x < nh) {
+            const float f = p.c4.factor[kind] ? p.c4.factor[kind][h0 + threadIdx.x] : 1.f;
+            bad = !(f >= cache4::kLeastFactor && f <= cache4::kMostFactor);
+            inv_s[threadIdx.x] = 1.f / f;
+        }
     }
     const bool turn = kind != 1 && p.dim > 0;
     const int np = p.dim / 2;
@@ -138,7 +143,10 @@ __global__ void __launch_bounds__(THREADS) kv_append4_kernel(const Append4Args a
             table[e] = make_float2(cs.x * p.mscale, cs.y * p.mscale);
         }
     }
-    __syncthreads();
+    if (__syncthreads_or(bad)) {  // a factor out of range: its heads' rows are not written
+        if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusDevice);
+        return;
+    }
     const T* src = static_cast<const T*>(kind == 0 ? p.k : kind == 1 ? p.v : p.q) + (long long)h0 * p.D;
     const long long rs = kind == 0 ? p.k_rs : kind == 1 ? p.v_rs : p.q_rs;
     const int items = cnt * nh * a.units;
