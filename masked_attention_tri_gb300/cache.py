@@ -243,7 +243,7 @@ def kv_cache_append(cache: Union[PagedKVCache, PagedKVCache4], k, v, page_table,
     total, Hk, D = k.shape
     if Hk != cache.heads or D != cache.head_dim:
         raise ValueError(f"k must have the cache's {cache.heads} heads of {cache.head_dim}")
-    k_rs, v_rs = _rows(k, "k", dev, k.dtype, total, D), _rows(v, "v", dev, k.dtype, total, D)
+    k_rs, v_rs = _row_stride(k, "k", dev), _rows(v, "v", dev, k.dtype, total, D)
     if v.shape[1] != Hk:
         raise ValueError("v must have k's heads")
     S, MP = _table(page_table, kv_lengths, cu_seqlens, dev)
@@ -275,8 +275,8 @@ def kv_cache_append(cache: Union[PagedKVCache, PagedKVCache4], k, v, page_table,
         axes, pair_axes = rotary.num_axes, rotary.pair_axes
     if total == 0 or S == 0:
         return out_q
-    rows = (_ptr(q), _ptr(k), _ptr(v), _DT[k.dtype], _ptr(cu_seqlens), _ptr(kv_lengths), _ptr(page_table), S, total,
-            max_seqlen, Hq, Hk, D, q_rs, k_rs, v_rs, qo_rs, _ptr(positions))
+    rows = (_ptr(q), k.data_ptr(), v.data_ptr(), _DT[k.dtype], _ptr(cu_seqlens), kv_lengths.data_ptr(), page_table.data_ptr(), S,
+            total, max_seqlen, Hq, Hk, D, q_rs, k_rs, v_rs, qo_rs, _ptr(positions))
     with _on(dev):
         if isinstance(cache, PagedKVCache4):
             abi.tri_attn_kv_append4(*rows, axes, _ptr(pair_axes), turns, dim, inter, ms, cache._c, MP, _ptr(out_q),
