@@ -551,8 +551,9 @@ ta_status tri_attn_kv_append_axes(const void* q, const void* k, const void* v, t
  * With a the largest |x| / factor of 16 elements, scale = e4m3(a / 7), not below 2^-9 and not above 448, and
  * n = x / (factor scale) rounded to the nearest whole number (ties to even) and to 7 at most; fp32 arithmetic.  (16-bit rows
  * that are turned, or a factor that is no power of two: a quotient within 2^-16 of a border may fall on either side.)  Rows
- * that are there keep their codes and scales.  An infinity or NaN makes its 16 elements NaN.  Every other argument and error as
- * in tri_attn_kv_append.
+ * that are there keep their codes and scales.  An infinity or NaN makes its 16 elements NaN.  The rows of heads beside a factor
+ * out of range (a CTA's, up to eight) are not written, and TA_ERR_DEVICE is recorded.  Every other argument and error as in
+ * tri_attn_kv_append.
  */
 ta_status tri_attn_kv_append4(const void* q, const void* k, const void* v, ta_dtype dtype, const int32_t* cu_seqlens,
                               const int32_t* kv_lengths, const int32_t* page_table, int num_seqs, int total,

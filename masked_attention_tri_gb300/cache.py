@@ -107,7 +107,7 @@ class PagedKVCache4(_Parts):
 
     k, v: uint8 (num_pages, Hk, page_size, D / 2), two codes n + 8 a byte (the even element in the low half);
     k_scale, v_scale: float8_e4m3fn (num_pages, Hk, page_size, D / 16), one for 16 neighbouring elements of a row;
-    k_factor, v_factor: float32 (Hk,) or None (1), positive, fixed for the cache's life (powers of two cost no
+    k_factor, v_factor: float32 (Hk,) or None (1), from 2^-100 to 2^100, fixed for the cache's life (powers of two cost no
     precision; a factor around the 100th part of a head's usual magnitudes keeps its scales in e4m3's middle).
 
     The tensors are used in place, as they are at each call (another may be put in one's place).  Pages and heads may be
