@@ -153,13 +153,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
         mbar_init(fin, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    // Rows of Q and dO that no box fills (tq hp < 128) stay zeros.
-    const int full_rows = P.t.tq * P.t.hp;
-    for (int e = threadIdx.x; e < (kQStages + 2) * NB * (128 - full_rows) * 8; e += kWarps * 32) {
-        const int c = e % 8, r = e / 8 % (128 - full_rows) + full_rows, b = e / 8 / (128 - full_rows);
-        st_shared_v4(base + M::kQ + (uint32_t)b * kBox + (uint32_t)r * 128u + c * 16u, 0u, 0u, 0u, 0u);
-    }
-    fence_async_shared();
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
                      : "memory");
@@ -181,7 +174,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
                 tma_load_3d(base + M::kV + b * kBox, &P.tm_v, 64 * b, h, q.k0 + k0, kv_full);
             }
         }
-        const uint32_t bytes = (uint32_t)full_rows * 128u * NB;
         StageRing qr = {0, 0u, false};
         for (int j = 0; j < n && ok; ++j) {
             int tok, head, rows;
@@ -190,14 +182,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
             const uint32_t before = (uint32_t)(j / 2 - 1) & 1u;
             if (qr.wrapped) ok = __all_sync(0xffffffffu, wait(q_empty(qr.idx), qr.ph ^ 1u, abort_flag, p.status));
             if (ok && lane == 0) {
-                mbar_expect_tx(q_full(qr.idx), bytes);
+                mbar_expect_tx(q_full(qr.idx), kTile);
                 for (int b = 0; b < NB; ++b)
                     tma_load_3d(q_smem(qr.idx) + b * kBox, &P.tm_q, 64 * b, head, q.q0 + tok, q_full(qr.idx));
             }
             qr.next(kQStages);
             if (j >= 2 && ok) ok = __all_sync(0xffffffffu, wait(do_empty(s), before, abort_flag, p.status));
             if (ok && lane == 0) {
-                mbar_expect_tx(do_full(s), bytes);
+                mbar_expect_tx(do_full(s), kTile);
                 for (int b = 0; b < NB; ++b) tma_load_3d(do_smem(s) + b * kBox, &P.tm_do, 64 * b, head, q.q0 + tok, do_full(s));
             }
         }
@@ -234,13 +226,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
         const bool leader = elect_one();
         const int lead = __ffs((int)__ballot_sync(0xffffffffu, leader)) - 1;
         const int last_from = (blocks - 1) * P.t.ng, last_rows = min(P.t.tq, q.lq - (blocks - 1) * P.t.tq) * P.t.hp;
-        auto rows_of = [&](int j) { return first + j * P.splits < last_from ? full_rows : last_rows; };
+        auto rows_of = [&](int j) { return first + j * P.splits < last_from ? 128 : last_rows; };
         auto await = [&](uint32_t b, uint32_t parity) {
             if (ok) ok = wait(b, parity, abort_flag, p.status);
             tc_fence_after();
         };
-        const int steps = (full_rows + 15) / 16;
-        const int whole = steps == 8 ? max(0, (last_from - first + P.splits - 1) / P.splits) : 0;  // tiles before the last block's
+        const int whole = max(0, (last_from - first + P.splits - 1) / P.splits);  // tiles before the last block's
         StageRing qs = {0, 0u, false}, qk = {0, 0u, false};  // Q for S, Q for dK
         // Whole tiles, without a question (a few dozen instructions of one thread are a product's time; by all sixteens of
         // columns, or by as many as there are).
@@ -288,7 +279,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dkv_kernel(const __grid
                             if (!clean) {
                                 await(second ? do_full(s) : q_full(qs.idx), second ? (uint32_t)(j / 2) & 1u : qs.ph);
                                 const int rows = rows_of(j);
-                                if (ok && rows < full_rows && rows % 16) {
+                                if (ok && rows < 128 && rows % 16) {
                                     tail = rows;
                                     tail_at = at;
                                     clean = true;

@@ -114,13 +114,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    // Rows of Q and dO that no box fills (tq hp < 128) stay zeros.
-    const int full_rows = P.t.tq * P.t.hp;
-    for (int e = threadIdx.x; e < 2 * NB * (128 - full_rows) * 8; e += kWarps * 32) {
-        const int c = e % 8, r = e / 8 % (128 - full_rows) + full_rows, b = e / 8 / (128 - full_rows);
-        st_shared_v4(base + M::kQ + (uint32_t)b * kBox + (uint32_t)r * 128u + c * 16u, 0u, 0u, 0u, 0u);
-    }
-    fence_async_shared();
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
                      : "memory");
@@ -152,7 +145,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
         StageRing kr = {0, 0u, false}, vr = {0, 0u, false};
         Item<1> it;
         uint32_t q_use = 0;
-        const uint32_t q_bytes = (uint32_t)full_rows * 128u * NB;
         while (ok && next_item(it)) {
             const int n = (it.keys[0] + 127) / 128;
             if (n == 0) continue;
@@ -161,7 +153,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_dq_kernel(const __grid_
                 const uint32_t full = d_o ? do_full : q_full;
                 if (ok && q_use > 0) ok = __all_sync(0xffffffffu, wait(d_o ? do_empty : q_empty, (q_use - 1u) & 1u, abort_flag, p.status));
                 if (ok && lane == 0) {
-                    mbar_expect_tx(full, q_bytes);
+                    mbar_expect_tx(full, kTile);
                     for (int b = 0; b < NB; ++b)
                         tma_load_3d(base + (d_o ? M::kDO : M::kQ) + b * kBox, d_o ? &P.tm_do : &P.tm_q, 64 * b, it.head[0],
                                     it.q0 + it.tok[0], full);

@@ -1,7 +1,7 @@
 // prompt_fwd.cu -- causal attention of packed prompts with grouped heads on tcgen05 tensor cores: 16-bit inputs, D <= 128.
 //
-// The mathematics is prompt.cuh's: the heads of a group are rows.  A tile is up to 128 rows, tq tokens x hp heads of a group
-// (hp a divisor of the group, the whole group where it fits), loaded by one TMA box of a (D, head, token) map, so that
+// The mathematics is prompt.cuh's: the heads of a group are rows.  A tile is 128 rows, tq tokens x hp heads of a group (hp the
+// largest power of two in the group's heads: all of 4, one of 7), loaded by one TMA box of a (D, head, token) map, so that
 // short sequences fill tiles by their heads and the keys past the causal border are few.  A work item is two neighbouring
 // tiles of one (sequence, key head), which share every K and V tile (128 keys) that is loaded.
 //
@@ -145,12 +145,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    // Rows of Q that no box fills (tq hp < 128) stay zeros.
-    for (int e = threadIdx.x; e < 2 * NB * (128 - P.t.tq * P.t.hp) * 8; e += kWarps * 32) {
-        const int c = e % 8, r = e / 8 % (128 - P.t.tq * P.t.hp) + P.t.tq * P.t.hp, b = e / 8 / (128 - P.t.tq * P.t.hp);
-        st_shared_v4(base + M::kQ + (uint32_t)b * kBox + (uint32_t)r * 128u + c * 16u, 0u, 0u, 0u, 0u);
-    }
-    fence_async_shared();
     if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
                      : "memory");
@@ -186,6 +180,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) prompt_fwd_kernel(const __grid
             StageRing kr = {0, 0u, false};
             Item<2> it;
             uint32_t q_use[2] = {0u, 0u};
+            // (kTile, as a number of the launch: with the constant the compiler's loop of the issuing thread is 2% slower)
             const uint32_t q_bytes = (uint32_t)(P.t.tq * P.t.hp) * 128u * NB;
             while (ok && next_item(it)) {
                 const int n = (max(it.keys[0], it.keys[1]) + 127) / 128;
@@ -576,13 +571,11 @@ cudaError_t start(const FwdParams& P, unsigned grid, cudaStream_t stream) {
 
 }  // namespace
 
-// Heads of a tile: the divisor of the group that fills most of 128 rows, the largest of those (fewer keys past the
-// causal border).
+// Heads of a tile: the largest power of two that divides the group (up to 128), so that tokens fill the rest of the 128 rows.
 Tiles make_tiles(const PromptParams& p) {
     Tiles t;
-    t.hp = 1;
-    for (int d = 1; d <= p.G && d <= 128; ++d)
-        if (p.G % d == 0 && 128 / d * d >= 128 / t.hp * t.hp) t.hp = d;
+    t.hp = p.G & -p.G;
+    if (t.hp > 128) t.hp = 128;
     t.tq = 128 / t.hp;
     t.ng = p.G / t.hp;
     t.fd_hp = make_fastdiv((uint32_t)t.hp);

@@ -12,7 +12,7 @@ namespace prompt {
 
 using namespace tc;
 
-// Tiles of rows: tq tokens x hp heads of a group, ng tiles of the same tokens (G / hp).
+// Tiles of 128 rows: tq tokens x hp heads of a group (both powers of two), ng tiles of the same tokens (G / hp).
 struct Tiles {
     int hp, tq, ng;
     FastDiv fd_hp;
