@@ -469,8 +469,11 @@ cudaError_t launch_delta(const PromptParams& p, cudaStream_t stream) {
     if (e != cudaSuccess || !p.norm) return e;
     const long long pairs = (long long)p.num_seqs * p.Hk;
     if (pairs > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const int longest = p.max_q > p.max_k ? p.max_q : p.max_k, shares = (longest + 63) / 64;
-    prompt_most_kernel<<<dim3((unsigned)pairs, (unsigned)(shares < 1 ? 1 : shares < 64 ? shares : 64)), kThreads, 0, stream>>>(p);
+    // Blocks of a pair: one for 64 keys or rows of the longest, up to 64, but not many more in all than the GPU has places.
+    const long long longest = p.max_q > p.max_k ? p.max_q : p.max_k, room = 16384 / pairs;
+    long long shares = (longest + 63) / 64 < 64 ? (longest + 63) / 64 : 64;
+    if (shares > room) shares = room;
+    prompt_most_kernel<<<dim3((unsigned)pairs, (unsigned)(shares > 1 ? shares : 1)), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
