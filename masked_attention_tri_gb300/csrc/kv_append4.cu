@@ -143,10 +143,8 @@ __global__ void __launch_bounds__(THREADS) kv_append4_kernel(const Append4Args a
             table[e] = make_float2(cs.x * p.mscale, cs.y * p.mscale);
         }
     }
-    if (__syncthreads_or(bad)) {  // a factor out of range: its heads' rows are not written
-        if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusDevice);
-        return;
-    }
+    if (bad) atomicCAS(p.status, 0, kStatusDevice);
+    if (__syncthreads_or(bad)) return;  // a factor out of range: its heads' rows are not written
     const T* src = static_cast<const T*>(kind == 0 ? p.k : kind == 1 ? p.v : p.q) + (long long)h0 * p.D;
     const long long rs = kind == 0 ? p.k_rs : kind == 1 ? p.v_rs : p.q_rs;
     const int items = cnt * nh * a.units;
