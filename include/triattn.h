@@ -651,7 +651,7 @@ ta_status tri_attn_paged4_fwd(const void* q, ta_dtype dtype, const int32_t* cu_s
  *   cu_seqlens_q  (num_seqs + 1) int32: sequence i's queries are rows [cu_q[i], cu_q[i + 1]), at most max_seqlen_q of them;
  *   cu_seqlens_k  (num_seqs + 1) int32: its keys, at most max_seqlen_k.  The queries are its newest tokens: of Lq queries
  *                 and Lk keys, query j sees the keys k <= Lk - Lq + j (the last one all of them).  Either may have none.
- *                 Rows of out and lse past cu_q[num_seqs] are left alone.
+ *                 Rows of out and lse past cu_q[num_seqs] are left alone (tri_attn_zero_rest makes them 0).
  *   lse           optional (Hq, total_q) fp32.
  * A query that sees no key (Lk < Lq) gets O = 0 and lse = -inf.  A key row that no query of its sequence sees takes no
  * part (finite values of v are wanted all the same in rows that share a tile with seen ones: a NaN there may spread).

@@ -566,4 +566,4 @@ TA_EXPORT const char* tri_attn_error_string(ta_status s) {
     }
 }
 
-TA_EXPORT int tri_attn_version(void) { return (1 << 16) | 5; }
+TA_EXPORT int tri_attn_version(void) { return (1 << 16) | 6; }

@@ -1,8 +1,8 @@
 // kv_append4.cu -- new keys and values of packed sequences into the pages of a 4-bit cache (cache4.cuh), with the rotation of k
 // and of q on the way.
 //
-// Bound: memory, with the arithmetic of the codes close behind: eight prompts of 256 to 2048 tokens, 8 heads of 128, 16.6 us (2.9
-// TB/s; 27 by kv_append.cu's threads of half groups with two divisions an element).  One CTA takes some rows of one page of one
+// Bound: memory, with the arithmetic of the codes close behind: eight prompts of 256 to 2048 tokens, 8 heads of 128, 16.4 us (2.9
+// TB/s; 18.6 called from Python; 27 by kv_append.cu's threads of half groups with two divisions an element).  One CTA takes some rows of one page of one
 // sequence and one job: some heads of k, of v or of q.  A thread takes a group of 16 elements, or, where the halves of a head
 // turn together, a group and its partner half a turn away; so no lane waits for another, a row is read and written once, and
 // no two threads write the same byte. cos and sin of the rows' pairs lie in a table in shared memory, computed once for the

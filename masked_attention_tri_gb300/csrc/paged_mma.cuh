@@ -41,8 +41,11 @@
 // conversion instructions run at a quarter of that rate).  k index 2t, 2t + 1, 2t + 8, 2t + 9 of K's products stands for
 // elements e, e + 4, e + 1, e + 5 of lane t's word (it has whole groups of 16); of V a lane reads 8 NDC columns of four
 // slots, whose 16-bit halves side by side hold four columns' pairs.  The scales come into the stage by untiled copies beside
-// the tiles. The 64 sequences above in four bits: 163 us (644 MB, 3.9 TB/s; the copies alone 117, the arithmetic alone 155: 320
-// instructions a block of 16 slots, 128 of them the conversions).  Pages of 16, whose scales are copies of 128 bytes, 330 us.
+// the tiles. (A number put into the low bits of a power of two is a known way from whole numbers to floating point: Kim et al.,
+// "Who Says Elephants Can't Run", 2022, for weights.)  The 64 sequences above in four bits: 163 us (644 MB, 3.9 TB/s; the copies
+// alone 117, all but the copies 155: 320 instructions a block of 16 slots, 128 of them the conversions, at half of the issue
+// slots: a warp's block is a chain, and there are three warps a scheduler).  Pages of 32 206 us, of 16, whose scales are
+// copies of 128 bytes, 333 us.
 //
 // Roundings: P to the products' 16-bit type (fp16 for 8-bit and 4-bit caches: 2^-12 of a weight),
 // as everywhere in this library; S, the maxima, sums and O are fp32.  O is rescaled only

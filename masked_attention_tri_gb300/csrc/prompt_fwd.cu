@@ -25,9 +25,10 @@
 //
 // Bound: the tensor core, 2048 clocks a pair of tiles and 128 keys at D = 128, as long as its products are asked for in time.
 // So one thread issues them, without votes or other lanes to wait for, straight on over whole key tiles and from one item into the
-// next (bf16, 32 heads over 8 of 128; a warp whose waits were votes, before: one chunk of 1216 tokens on a prefix of 30000 425
-// us, 1434 TFLOP/s; so 333 us, 1830; eight prompts of 512 to 4096 tokens 360 and 295, 1480 TFLOP/s, where an item is 9 steps
-// and its first and last are slower).  Heads of 64 are bound by the softmax (two sequences of 16384, 16 heads over 4: 1.01 ms,
+// next (bf16, 32 heads over 8 of 128, in short runs; a warp whose waits were votes, before: one chunk of 1216 tokens on a prefix
+// of 30000, 152 equal items, 425 us, 1434 TFLOP/s; so 333 us, 1830; eight prompts of 512 to 4096 tokens 360 and 290, 1510
+// TFLOP/s, where an item is 9 steps and its first and last are slower; back to back for seconds 315, 1390, as the clock gives
+// way).  Heads of 64 are bound by the softmax (two sequences of 16384, 16 heads over 4: 1.01 ms,
 // 1090 TFLOP/s). Code is time as well: a second form of the softmax for the causal border, with fewer columns, cost 3%.
 #include "prompt_tc.cuh"
 
