@@ -157,7 +157,7 @@ def test_a_long_prefix_beside_many_short_prompts(locate):
 
 
 def test_past_the_last_item(locate):
-    seqs = [(64 * i, 64 * i) for i in range(1, 129)] * 2
+    seqs = [(65 * i, 65 * i) for i in range(1, 129)] * 2
     n = len(_items(2, 32, 1, 8, seqs))
     for x in locate(2, 32, 1, 8, seqs, [n, n + 1, n + 1000]):
         assert x[:3] == (-1, -1, -1) and x[3] == 2 * _chunks(seqs)
