@@ -240,9 +240,23 @@ __device__ __forceinline__ bool hand_out(const PromptParams& p, const Tiles& T, 
     Order<PER> o;
     o.begin(WarpSeqs{p}, __ffs(T.tq) - 1, T.ng, p.Hk);
     int at = (int)blockIdx.x;
+    uint32_t asked = 0;
+    // (awaited whatever happens: the answer is written into this block's memory)
+    auto next = [&]() -> bool {
+        if (lane == 0) clc_ask(clc_at, clc_bar);
+        if (!__all_sync(0xffffffffu, wait_bar_drain(clc_bar, asked++ & 1u))) return false;
+        at = clc_answer(clc_at);
+        __syncwarp();
+        return true;
+    };
     for (int n = 0;; ++n) {
         Item<PER> it{};
-        if (at < 0 || !order_item<PER>(p, T, o, at, it)) it.on = 0;
+        // A place without an item is passed over and the next one asked for, so that the rest of the grid need not start to
+        // learn that (up to 4096 of them, some milliseconds: the others wait for this item with a limit).
+        for (int over = 0; at >= 0 && !order_item<PER>(p, T, o, at, it); ++over) {
+            if (over == 4096) at = -1;
+            else if (!next()) return false;
+        }
         const int r = n % R;
         if (n >= R && !__all_sync(0xffffffffu, wait(empty(r), (uint32_t)(n / R - 1) & 1u, abort_flag, p.status))) return false;
         if (lane == 0) {
@@ -250,11 +264,7 @@ __device__ __forceinline__ bool hand_out(const PromptParams& p, const Tiles& T, 
             mbar_arrive(full(r));
         }
         if (!it.on) break;
-        if (lane == 0) clc_ask(clc_at, clc_bar);
-        // (awaited whatever happens: the answer is written into this block's memory)
-        if (!__all_sync(0xffffffffu, wait_bar_drain(clc_bar, (uint32_t)n & 1u))) return false;
-        at = clc_answer(clc_at);
-        __syncwarp();
+        if (!next()) return false;
     }
     if (blockIdx.x == 0)
         for (int s = lane; s < p.num_seqs; s += 32) load_seq(p, s, true);  // (records a broken sequence)

@@ -9,6 +9,7 @@ import shutil
 import subprocess
 
 import pytest
+import torch
 
 from masked_attention_tri_gb300 import build
 
@@ -210,3 +211,30 @@ def test_values_of_prompts_of_many_lengths():
     r = random.Random(12)
     lq = [r.randint(1, 700) for _ in range(100)]
     _run(lq, lq, 4, 2, 128, F16)
+
+
+@pytest.mark.gpu
+def test_values_where_most_sequences_are_empty():
+    """The grid has a block for each item that there could be: most of them none."""
+    from test_prompt_attention import BF, _run
+    lq = [(5 + i % 60) if i % 150 == 7 else 0 for i in range(3000)]
+    lk = [n + (100 if i % 300 == 7 else 0) for i, n in enumerate(lq)]
+    _run(lq, lk, 16, 8, 64, BF)
+
+
+@pytest.mark.gpu
+def test_values_of_more_places_without_an_item_than_a_block_passes_over():
+    from test_prompt_attention import BF, _inputs, _within, reference
+    import masked_attention_tri_gb300 as ta
+    n = [0] * 30000 + [3] + [0] * 30000 + [40]
+    q, k, v, g = _inputs([43], [43], 32, 32, 64, BF)
+    cu = torch.zeros(len(n) + 1, dtype=torch.int32)
+    cu[1:] = torch.tensor(n).cumsum(0)
+    a = q, k, v, cu.cuda(), cu.cuda(), 40, 40
+    o, lse = ta.prompt_attention(*a, return_aux=True)
+    s = float(torch.tensor(0.125, dtype=torch.float32))
+    R, T = reference(q, k, v, [3, 40], [3, 40], s, g, out=o)
+    _within(o, *reference(q, k, v, [3, 40], [3, 40], s), "o")
+    for x, name in zip(ta.prompt_attention_backward(*a, o, lse, g), ("dq", "dk", "dv")):
+        _within(x, R, T, name)
+    assert ta.get_status() == 0
